@@ -6,12 +6,17 @@ The Python surface is a thin ctypes binding (``sa2.py``); the library is built i
 """
 from .sa2 import (  # noqa: F401
     BlockMask,
+    KvCache8,
     Sa2Error,
     attn_bwd,
     attn_fwd,
     blocks,
     build_mask,
+    cache8_append,
+    cache8_attn,
+    cache8_read,
     check_device,
+    cross_attn_fwd,
     debug_set_wait_limit,
     device_status,
     load_library,

@@ -5,7 +5,7 @@
 #include <cstring>
 #include <cudaTypedefs.h>
 
-#include "sa2_internal.h"
+#include "cross_internal.h"
 
 namespace sa2 {
 
@@ -38,6 +38,21 @@ bool make_token_map(CUtensorMap* map, const void* base, const ShapeArgs& s, int6
                    const_cast<void*>(base), dims, strides, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_group_map(CUtensorMap* map, const TokenRef& t, int B, int heads, int G, int tokens, int d, int box_g,
+                    int box_n, bool f16) {
+  auto enc = encode_tiled();
+  if (!enc) return false;
+  std::memset(map, 0, sizeof(*map));
+  cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)tokens, (cuuint64_t)(heads / G), (cuuint64_t)B};
+  cuuint64_t strides[4] = {(cuuint64_t)t.sh * 2, (cuuint64_t)t.sn * 2, (cuuint64_t)t.sh * G * 2, (cuuint64_t)t.sb * 2};
+  cuuint32_t box[5] = {64, (cuuint32_t)box_g, (cuuint32_t)box_n, 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t.p, dims,
+                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -1,0 +1,775 @@
+// Attention of queries to keys of another length, forward, on sm_103a (tcgen05 + TMEM): over
+// 16-bit keys and values (cross attention) and over the 8-bit cache.
+//
+//   s = scale * q k^T,  O = softmax(s) V,  LSE = log sum exp(s)
+//
+// One CTA per SM works on a pair of query tiles (2 x 128 rows) at a time, so that each key block
+// that reaches shared memory feeds twice the matrix work and one tile's softmax runs beside the
+// other's products.  A tile's rows are the tokens of all G query heads that share the key head
+// (row = token * G + head), which lets few tokens of many heads fill a tile.
+//
+// Roles (512 threads): warp 0 TMA producer (Q tiles, a ring of K and V blocks of 128 keys);
+// warp 1 owner of TMEM and issuer of every MMA; warps 4..7 epilogue (16-bit keys) or converters
+// (8-bit keys: global memory -> registers -> fp16 in the ring, and Q to fp16); warps 8..11 and
+// 12..15 the softmax of tile 0 and 1, one row per thread.
+// Per key block j the issuer runs S_0 S_1 | P_0 V, P_1 V.  S_t(j) overwrites the TMEM columns that
+// hold P_t(j-1), so it waits for the completion of P_t V(j-1); in this order that wait passes while
+// the other tile's product still runs, and P_t(j) is made while S_1 and the other P V run.
+//   S_t  = Q_t K_j^T   M = 128, N = 128, K = d   (shared memory, K-major)
+//   O_t += P_t V_j     M = 128, N = d, K = 128   (A = P from TMEM, V MN-major)
+// The softmax thread reads keys 64..127 of its row first and keeps them, takes the maximum over
+// both halves, writes P for 64..127, then reads 0..63 again: P V of the first written half starts
+// while the other is computed, and a thread never holds more than 64 scores.
+// TMEM columns: S_0 0, S_1 128 (P as 16-bit pairs over the first 32 columns of each half of the
+// scores), O_0 256, O_1 384.
+//
+// The last block of a sequence may be partial.  Its products run over the valid keys rounded up
+// to 16; scores behind the last key are replaced by -inf (whatever they are: NaN too), and up to
+// 15 rows of V behind it are zeroed in shared memory, since 0 * NaN is NaN.
+#include <cuda_fp8.h>
+
+#include "cross_sched.cuh"
+
+namespace sa2 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: O and l are rescaled only past 2^8
+
+template <int D>
+struct XSmem {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = 128 * 128 * kPanels;  // 128 rows x 128 B per panel
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kOffBar = kOffKV + kStages * kTile;
+  // [2][128], for each row 1 / l (16-bit keys) or the scale of its converted query (8-bit keys)
+  static constexpr int kOffRow = kOffBar + 512;
+  static constexpr int kBytes = kOffRow + 1024 + 1024;
+  static_assert(kBytes <= (int)kMaxDynSmem, "shared memory");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void load64(uint32_t taddr, float (&x)[64]) {
+  uint32_t u0[32], u1[32];
+  tmem_ld32(taddr, u0);
+  tmem_ld32(taddr + 32, u1);
+  tmem_ld_wait(u0);
+  tmem_ld_wait(u1);
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    x[c] = __uint_as_float(u0[c]);
+    x[c + 32] = __uint_as_float(u1[c]);
+  }
+}
+
+__device__ __forceinline__ void mask64(float (&x)[64], int valid) {
+  if (valid < 64) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) x[c] = c < valid ? x[c] : -INFINITY;
+  }
+}
+
+__device__ __forceinline__ float max64(const float (&x)[64]) {
+  float m[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) m[c] = x[c];
+#pragma unroll
+  for (int c = 8; c < 64; ++c) m[c & 7] = fmaxf(m[c & 7], x[c]);
+  return fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])));
+}
+
+// p = exp2(x * mul + add) as 16-bit pairs into TMEM; returns their sum (before rounding).
+template <bool F16>
+__device__ __forceinline__ float exp64(const float (&x)[64], float mul, float add, uint32_t taddr) {
+  uint32_t pk[32];
+  float l[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    const float p0 = ex2(fmaf(x[2 * c], mul, add)), p1 = ex2(fmaf(x[2 * c + 1], mul, add));
+    l[c & 3] += p0 + p1;
+    pk[c] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+  }
+  tmem_st32(taddr, pk);
+  tmem_st_wait();
+  return (l[0] + l[1]) + (l[2] + l[3]);
+}
+
+// 32 channels of a row, rounded to the call's type.
+__device__ __forceinline__ void store32(uint16_t* dst, const float (&v)[32], bool f16) {
+  uint4* p = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = f16 ? pack_f16x2(v[8 * i + 2 * q], v[8 * i + 2 * q + 1])
+                 : pack_bf16x2(v[8 * i + 2 * q], v[8 * i + 2 * q + 1]);
+    p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// k-steps [k0, k1) of O (+)= P V: A = P in TMEM (16 keys in 8 columns; keys 64..127 from column 64
+// on), B = V, 16 rows per k-step.
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, int k0, int k1,
+                                         bool fresh) {
+  for (int kk = k0; kk < k1; ++kk)
+    umma_ts(o, p + kk * 8 + (kk >= 4 ? 32 : 0), v + (uint64_t)(kk * 128), idesc, (fresh && kk == k0) ? 0u : 1u);
+}
+
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w) {
+  const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
+  const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// F16: the type of Q and O (and of K, V when they are 16-bit).
+template <int D, bool KV8, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, CrossShape s, FwdPlan plan, CacheRef cache,
+                     CrossFwdArgs a) {
+  using L = XSmem<D>;
+  constexpr int kStages = L::kStages;
+  constexpr bool kMmaF16 = KV8 || F16;  // the cache's products run in fp16
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  auto bar_full = [&](int st) { return smem_u32(&bars[st]); };        // ring stage filled
+  auto bar_empty = [&](int st) { return smem_u32(&bars[8 + st]); };   // ... and read by its MMAs
+  auto bar_qfull = [&](int t) { return smem_u32(&bars[16 + t]); };    // Q of tile t in shared memory
+  auto bar_qempty = [&](int t) { return smem_u32(&bars[18 + t]); };   // ... and read (by its last S; cache: and its row scales)
+  auto bar_s = [&](int t) { return smem_u32(&bars[20 + t]); };        // S_t in TMEM
+  auto bar_pb = [&](int t) { return smem_u32(&bars[22 + t]); };       // P of keys 64..127 written
+  auto bar_pa = [&](int t) { return smem_u32(&bars[24 + t]); };       // P of keys 0..63 written
+  auto bar_pv = [&](int t) { return smem_u32(&bars[26 + t]); };       // P_t V completed
+  auto bar_o = [&](int t) { return smem_u32(&bars[28 + t]); };        // O_t of the piece complete
+  auto bar_ofree = [&](int t) { return smem_u32(&bars[30 + t]); };    // ... and read out
+  auto bar_l = [&](int t) { return smem_u32(&bars[32 + t]); };        // 1 / l of the piece written
+  const uint32_t bar_drain = smem_u32(&bars[34]);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
+  float* row_s = reinterpret_cast<float*>(smem + L::kOffRow);
+  const WaitCtl wc{abort_flag, s.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(bar_full(st), KV8 ? 128 : 1);
+      mbar_init(bar_empty(st), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_qfull(t), KV8 ? 128 : 1);
+      mbar_init(bar_qempty(t), KV8 ? 129 : 1);
+      mbar_init(bar_s(t), 1);
+      mbar_init(bar_pb(t), 128);
+      mbar_init(bar_pa(t), 128);
+      mbar_init(bar_pv(t), 1);
+      mbar_init(bar_o(t), 1);
+      mbar_init(bar_ofree(t), 128);
+      mbar_init(bar_l(t), 128);
+    }
+    mbar_init(bar_drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tp = plan.tp;  // tiles per segment
+  auto active = [&](const Piece& x, int t) { return t < tp && x.pair * tp + t < plan.tiles; };
+  if (a.kv_len && blockIdx.x == 0 && warp == 2) {
+    for (int b = lane; b < s.B; b += 32)
+      if (a.kv_len[b] < 0 || a.kv_len[b] > s.M) report_error(a.status, kDevErrBounds);
+  }
+
+  if (warp == 0 && !KV8) {
+    // ------------------------------------------------------------------ TMA producer
+    PieceIter it(s, plan, a.kv_len);  // (whole warps)
+    if (lane == 0) {
+      tma_prefetch_map(&mq);
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+      const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * plan.nb * s.G);
+      uint32_t r = 0, qn[2] = {0, 0};  // ring loads and Q tiles issued
+      bool ok = true;
+      Piece x;
+      while (ok && it.next(x)) {
+        auto load = [&](const CUtensorMap* map, int kb) {
+          const int st = r % kStages;
+          if (r >= (uint32_t)kStages && !mbar_wait(bar_empty(st), ((r / kStages) - 1) & 1, wc)) return false;
+          mbar_arrive_expect_tx(bar_full(st), L::kTile);
+          for (int pn = 0; pn < L::kPanels; ++pn)
+            tma_load_5d(sbase + L::kOffKV + st * L::kTile + pn * 16384, map, bar_full(st), pn * 64, 0, kb * kKeyBlock,
+                        x.hk, x.b);
+          ++r;
+          return true;
+        };
+        for (int j = 0; ok && j < x.nb; ++j) {
+          ok = load(&mk, x.k0 + j);
+          if (j == 0) {
+            for (int t = 0; ok && t < 2; ++t) {
+              if (!active(x, t)) continue;
+              if (qn[t] >= 1 && !mbar_wait(bar_qempty(t), (qn[t] - 1) & 1, wc)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(bar_qfull(t), q_bytes);
+              for (int pn = 0; pn < L::kPanels; ++pn)
+                tma_load_5d(sbase + t * L::kTile + pn * 16384, &mq, bar_qfull(t), pn * 64, 0,
+                            (x.pair * tp + t) * plan.nb, x.hk, x.b);
+              ++qn[t];
+            }
+          }
+          if (ok) ok = load(&mv, x.k0 + j);
+        }
+      }
+      // No copy may still be in flight when the CTA exits: each stage's last load, each tile's Q.
+      for (uint32_t v = r > (uint32_t)kStages ? r - kStages : 0; v < r; ++v)
+        mbar_drain(bar_full(v % kStages), (v / kStages) & 1, abort_flag);
+      for (int t = 0; t < 2; ++t)
+        if (qn[t]) mbar_drain(bar_qfull(t), (qn[t] - 1) & 1, abort_flag);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    PieceIter it(s, plan, a.kv_len);
+    constexpr uint32_t idO = idesc_f32acc(128, D, false, true, !kMmaF16);
+    bool ok = true;
+    uint32_t r = 0, c[2] = {0, 0}, pc[2] = {0, 0};  // ring loads; blocks and pieces done per tile
+    Piece x;
+    while (ok && it.next(x)) {
+      for (int j = 0; ok && j < x.nb; ++j) {
+        const int valid = min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock);
+        const int steps = (valid + 15) >> 4;
+        const uint32_t idS = idesc_f32acc(128, steps * 16, false, false, !kMmaF16);
+        const int ks = r % kStages, vs = (r + 1) % kStages;
+        const uint32_t kph = (r / kStages) & 1, vph = ((r + 1) / kStages) & 1;
+        r += 2;
+        const bool last = j + 1 == x.nb;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(ks), kph, wc));
+        const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile, 16, 1024);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || !active(x, t)) continue;
+          ok = __all_sync(0xffffffffu, (j > 0 || mbar_wait(bar_qfull(t), pc[t] & 1, wc)) &&
+                                           (c[t] == 0 || mbar_wait(bar_pv(t), (c[t] - 1) & 1, wc)));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = smem_desc(sbase + t * L::kTile, 16, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_ss(tmem + t * 128, qd + kmajor_kstep(kk, 128), kd + kmajor_kstep(kk, 128), idS, kk > 0 ? 1u : 0u);
+            umma_commit(bar_s(t));
+            if (last) umma_commit(bar_qempty(t));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit(bar_empty(ks));
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), vph, wc));
+        if (!ok) break;
+        uint8_t* vt = smem + L::kOffKV + vs * L::kTile;
+        if (!KV8 && (valid & 15)) {
+          // rows valid .. 16 * steps - 1 of V: a row is 128 bytes in each panel
+          const int n = (16 * steps - valid) * 8 * L::kPanels;
+          for (int i = lane; i < n; i += 32) {
+            const int row = valid + (i >> 3) % (16 * steps - valid), pn = (i >> 3) / (16 * steps - valid);
+            *reinterpret_cast<uint4*>(vt + pn * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        const uint64_t vd = smem_desc(sbase + L::kOffKV + vs * L::kTile, 16384, 1024);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || !active(x, t)) continue;
+          ok = __all_sync(0xffffffffu, (j > 0 || pc[t] == 0 || mbar_wait(bar_ofree(t), (pc[t] - 1) & 1, wc)) &&
+                                           mbar_wait(bar_pb(t), c[t] & 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t o = tmem + kColO + t * 128, p = tmem + t * 128;
+          if (steps > 4 && elect_one()) issue_pv(o, p, vd, idO, 4, steps, j == 0);
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_pa(t), c[t] & 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(o, p, vd, idO, 0, min(4, steps), j == 0 && steps <= 4);
+            umma_commit(bar_pv(t));
+            if (last) umma_commit(bar_o(t));
+          }
+          __syncwarp();
+          ++c[t];
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit(bar_empty(vs));
+        __syncwarp();
+      }
+      if (x.nb > 0)
+        for (int t = 0; t < 2; ++t) pc[t] += active(x, t) ? 1 : 0;
+    }
+    // no MMA may still run when TMEM is released, on the abort path too
+    if (elect_one()) umma_commit(bar_drain);
+    __syncwarp();
+    mbar_drain(bar_drain, 0, abort_flag);
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ softmax rows
+    if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
+    PieceIter it(s, plan, a.kv_len);
+    const int t = (warp - 8) >> 2;
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t ts = trow + t * 128, to = trow + kColO + t * 128;
+    const int tok_r = r / s.G, g = r - tok_r * s.G;
+    bool ok = true;
+    uint32_t c = 0, pc = 0;
+    Piece x;
+    while (ok && it.next(x)) {
+      if (!active(x, t)) continue;
+      const int n = (x.pair * tp + t) * plan.nb + tok_r;
+      const bool row_valid = tok_r < plan.nb && n < s.N;
+      const int h = x.hk * s.G + g;
+      const int64_t row = ((int64_t)x.b * s.H + h) * s.N + n;
+      if (x.nb == 0) {  // (direct mode) no keys
+        if (row_valid) {
+          a.lse[row] = -INFINITY;
+          if constexpr (KV8) {
+            uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o.p) + x.b * a.o.sb + h * a.o.sh + n * a.o.sn);
+            for (int i = 0; i < D / 8; ++i) op[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        continue;
+      }
+      // cache: scores are q8 scale * k8 scale * (q . k) and V's scale enters as an exponent
+      float qscale = a.scale_log2;
+      const float *ksp = nullptr, *vsp = nullptr;
+      float nks[2], nvs[2];  // of the next block's halves, loaded one block ahead
+      auto load_scales = [&](int kb) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bool in = kb * kKeyBlock + 64 * i < x.keys;
+          nks[i] = in ? ksp[2 * kb + i] : 1.f;
+          nvs[i] = in ? vsp[2 * kb + i] : 1.f;
+        }
+      };
+      if constexpr (KV8) {
+        const int64_t off = ((int64_t)x.b * s.Hkv + x.hk) * cache.nsb;
+        ksp = cache.ks + off;
+        vsp = cache.vs + off;
+        load_scales(x.k0);
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_qfull(t), pc & 1, wc))) {
+          ok = false;
+          break;
+        }
+        qscale *= row_s[t * 128 + r];
+        mbar_arrive(bar_qempty(t));
+      }
+      float m_used = -INFINITY, l = 0.f;
+      for (int j = 0; j < x.nb; ++j, ++c) {
+        const int valid = min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock);
+        float mul_a = qscale, mul_b = qscale, ev_a = 0.f, ev_b = 0.f;
+        if constexpr (KV8) {
+          mul_a *= nks[0];
+          mul_b *= nks[1];
+          ev_a = (float)((int)(__float_as_uint(nvs[0]) >> 23) - 127);
+          ev_b = (float)((int)(__float_as_uint(nvs[1]) >> 23) - 127);
+          if (j + 1 < x.nb) load_scales(x.k0 + j + 1);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_s(t), c & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float y[64];
+        load64(ts, y);
+        mask64(y, valid);
+        float mx = fmaf(max64(y), mul_a, ev_a);
+        if (valid > 64) {
+          load64(ts + 64, y);
+          mask64(y, valid - 64);
+          mx = fmaxf(mx, fmaf(max64(y), mul_b, ev_b));
+        }
+        if (j == 0) {
+          m_used = mx;
+        } else {
+          const bool need = mx > m_used + kRescaleThreshold;
+          if (__any_sync(0xffffffffu, need)) {
+            // S_t(j) was issued after P_t V(j-1) completed: O holds blocks 0 .. j-1
+            const float alpha = need ? ex2(m_used - mx) : 1.f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(to + c0, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(to + c0, o);
+            }
+            tmem_st_wait();
+            if (need) {
+              l *= alpha;
+              m_used = mx;
+            }
+          }
+        }
+        if (valid > 64) {
+          const float sum = exp64<kMmaF16>(y, mul_b, ev_b - m_used, ts + 64);
+          l += KV8 ? sum * ex2(-ev_b) : sum;
+        }
+        tc_fence_before();
+        mbar_arrive(bar_pb(t));
+        load64(ts, y);
+        mask64(y, valid);
+        const float sum = exp64<kMmaF16>(y, mul_a, ev_a - m_used, ts);
+        l += KV8 ? sum * ex2(-ev_a) : sum;
+        tc_fence_before();
+        mbar_arrive(bar_pa(t));
+      }
+      if (!ok) break;
+      const int64_t slot_row = ((int64_t)blockIdx.x + x.seg) * 256 + t * 128 + r;
+      const float lse2 = m_used + __log2f(l);
+      if (row_valid) {
+        if (plan.split)
+          a.part_l[slot_row] = lse2;
+        else
+          a.lse[row] = lse2 * 0.69314718055994531f;
+      }
+      if constexpr (!KV8) {
+        // the epilogue warps read the previous piece's 1 / l before they released its O
+        if (pc > 0 && !__all_sync(0xffffffffu, mbar_wait(bar_ofree(t), (pc - 1) & 1, wc))) {
+          ok = false;
+          break;
+        }
+        row_s[t * 128 + r] = 1.f / l;
+        mbar_arrive(bar_l(t));
+      } else {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_o(t), pc & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float inv_l = 1.f / l;
+        uint16_t* op = static_cast<uint16_t*>(a.o.p) + x.b * a.o.sb + h * a.o.sh + n * a.o.sn;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t u[32];
+          tmem_ld32(to + c0, u);
+          tmem_ld_wait(u);
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]) * inv_l;
+          if (row_valid && plan.split) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(a.part_o + slot_row * D + c0)[i] =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else if (row_valid) {
+            store32(op + c0, v, F16);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar_ofree(t));
+      }
+      ++pc;
+    }
+  } else if (warp >= 4 && !KV8) {
+    // ------------------------------------------------------------------ epilogue: O / l
+    PieceIter it(s, plan, a.kv_len);
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int tok_r = r / s.G, g = r - tok_r * s.G;
+    bool ok = true;
+    uint32_t pc[2] = {0, 0};
+    Piece x;
+    while (ok && it.next(x)) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || !active(x, t)) continue;
+        const int n = (x.pair * tp + t) * plan.nb + tok_r;
+        const bool row_valid = tok_r < plan.nb && n < s.N;
+        const int h = x.hk * s.G + g;
+        uint16_t* op = static_cast<uint16_t*>(a.o.p) + x.b * a.o.sb + h * a.o.sh + n * a.o.sn;
+        if (x.nb == 0) {
+          if (row_valid)
+            for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(op)[i] = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_l(t), pc[t] & 1, wc) && mbar_wait(bar_o(t), pc[t] & 1, wc));
+        if (!ok) break;
+        ++pc[t];
+        tc_fence_after();
+        const float inv_l = row_s[t * 128 + r];
+        const int64_t slot_row = ((int64_t)blockIdx.x + x.seg) * 256 + t * 128 + r;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t u[32];
+          tmem_ld32(trow + kColO + t * 128 + c0, u);
+          tmem_ld_wait(u);
+          if (c0 + 32 >= D) {
+            tc_fence_before();
+            mbar_arrive(bar_ofree(t));
+          }
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]) * inv_l;
+          if (row_valid && plan.split) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<float4*>(a.part_o + slot_row * D + c0)[i] =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else if (row_valid) {
+            store32(op + c0, v, F16);
+          }
+        }
+      }
+    }
+  } else if (warp >= 4 && KV8) {
+    // --------------------------------------------------- converters: Q, K, V to fp16
+    PieceIter it(s, plan, a.kv_len);
+    constexpr int kChunks = D / 16;         // 16-byte chunks of an 8-bit row
+    constexpr int kRows = 128 / kChunks;    // rows per pass of the 128 threads
+    constexpr int kPasses = 128 / kRows;    // = kChunks
+    const int ct = tid - 128;
+    const int ch = ct % kChunks, r0 = ct / kChunks;
+    bool ok = true;
+    uint32_t r = 0, qn[2] = {0, 0};
+    Piece x;
+    while (ok && it.next(x)) {
+      if (x.nb == 0) continue;
+      const int64_t head = (int64_t)x.b * cache.sb + (int64_t)x.hk * cache.sh + ch * 16;
+      auto fetch = [&](const uint8_t* base, int kb, uint4 (&u)[kPasses]) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int t = kb * kKeyBlock + r0 + i * kRows;
+          u[i] = make_uint4(0, 0, 0, 0);  // behind the last key: zeros
+          if (t < x.keys) u[i] = __ldg(reinterpret_cast<const uint4*>(base + head + (int64_t)t * cache.sn));
+        }
+      };
+      // into the next ring stage, swizzled; a row's 16 values are 32 bytes of panel ch / 4
+      auto put = [&](const uint4 (&u)[kPasses]) {
+        const int st = r % kStages;
+        if (r >= (uint32_t)kStages && !__all_sync(0xffffffffu, mbar_wait(bar_empty(st), ((r / kStages) - 1) & 1, wc)))
+          return false;
+        uint8_t* dst = smem + L::kOffKV + st * L::kTile + (ch >> 2) * 16384;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int row = r0 + i * kRows;
+          const uint2 w0 = e4m3x4_to_f16x4(u[i].x), w1 = e4m3x4_to_f16x4(u[i].y), w2 = e4m3x4_to_f16x4(u[i].z),
+                      w3 = e4m3x4_to_f16x4(u[i].w);
+          const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+          // the two panels' lanes store opposite halves first, so that a quarter warp's 16-byte
+          // stores fall into different banks
+          const int odd = (ch >> 2) & 1, k16 = (ch & 3) * 2;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((k16 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((k16 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+        }
+        fence_proxy_async();
+        mbar_arrive(bar_full(st));
+        ++r;
+        return true;
+      };
+      uint4 uk[kPasses], uv[kPasses];
+      fetch(cache.k, x.k0, uk);
+      // Q: thread = row, scaled by a power of two so that its largest magnitude is in [2^14, 2^15)
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if (!active(x, t)) continue;
+        if (qn[t] >= 1 && !__all_sync(0xffffffffu, mbar_wait(bar_qempty(t), (qn[t] - 1) & 1, wc))) {
+          ok = false;
+          break;
+        }
+        ++qn[t];
+        const int tok_r = ct / s.G, g = ct - tok_r * s.G;
+        const int n = (x.pair * tp + t) * plan.nb + tok_r;
+        const bool row_valid = tok_r < plan.nb && n < s.N;
+        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) + x.b * a.q.sb +
+                                                         (int64_t)(x.hk * s.G + g) * a.q.sh + (int64_t)n * a.q.sn);
+        uint4 u[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) u[i] = row_valid ? __ldg(qp + i) : make_uint4(0, 0, 0, 0);
+        int e = 0;
+        if constexpr (!F16) {
+          // the largest magnitude: bf16 magnitudes compare as integers
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mx = max(mx, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
+          }
+          // a row of zeros, or with an infinity or NaN, keeps its scale
+          if (mx >= 0x0080u && mx < 0x7F80u) e = min(max((int)(mx >> 7) - 127 - 14, -112), 112);
+          const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = pack_f16x2(__uint_as_float(w[q] << 16) * f, __uint_as_float(w[q] & 0xFFFF0000u) * f);
+            u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        row_s[t * 128 + ct] = __uint_as_float((uint32_t)(127 + e) << 23);
+        uint8_t* dst = smem + t * L::kTile + ct * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (ct & 7)) << 4)) = u[i];
+        fence_proxy_async();
+        mbar_arrive(bar_qfull(t));
+      }
+      for (int j = 0; ok && j < x.nb; ++j) {
+        fetch(cache.v, x.k0 + j, uv);
+        ok = put(uk);
+        if (!ok) break;
+        if (j + 1 < x.nb) fetch(cache.k, x.k0 + j + 1, uk);
+        ok = put(uv);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) report_error(a.status, kDevErrTimeout);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of split segments: O = sum_i 2^(l_i - m) O_i / sum_i 2^(l_i - m) over a segment's
+// parts in key order, l_i their log2 sums and m the largest; LSE = ln 2 (m + log2 sum).  Rows of
+// sequences without keys get 0 and -inf.  One warp per row; grid (segments, 8), 32 rows each.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan plan, CrossFwdArgs a) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int seg = blockIdx.x;
+  const int per_b = s.Hkv * plan.pairs;
+  const int b = seg / per_b, hk = (seg - b * per_b) / plan.pairs, pair = seg - b * per_b - hk * plan.pairs;
+  const int64_t run = run_length(total_key_blocks(s, a.kv_len, plan.pairs), plan.grid);
+  int64_t base = 0;
+  for (int i = lane; i < b; i += 32) base += key_blocks(key_count(a.kv_len, i, s.M));
+  for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+  const int nk = key_blocks(key_count(a.kv_len, b, s.M));
+  const int64_t g0 = base * per_b + (int64_t)(seg - b * per_b) * nk;
+  const int c0 = (int)(g0 / run), c1 = nk > 0 ? (int)((g0 + nk - 1) / run) : c0 - 1;
+  for (int i = warp; i < 32; i += 8) {
+    const int rr = blockIdx.y * 32 + i, t = rr >> 7, r = rr & 127;
+    const int tile = pair * plan.tp + t;
+    if (t >= plan.tp || tile >= plan.tiles) return;
+    const int tok_r = r / s.G, g = r - tok_r * s.G, n = tile * plan.nb + tok_r, h = hk * s.G + g;
+    if (tok_r >= plan.nb || n >= s.N) continue;
+    float m = -INFINITY;
+    bool nan = false;
+    for (int cta = c0 + lane; cta <= c1; cta += 32) {
+      const float v = a.part_l[((int64_t)cta + seg) * 256 + rr];
+      nan |= v != v;
+      m = fmaxf(m, v);
+    }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (__any_sync(0xffffffffu, nan)) m = NAN;
+    float acc[kPer] = {}, l = 0.f;
+    for (int cta = c0; cta <= c1; ++cta) {
+      const int64_t row = ((int64_t)cta + seg) * 256 + rr;
+      const float w = ex2(a.part_l[row] - m);
+      l += w;
+      float v[kPer];
+      if constexpr (kPer == 4)
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + row * D + lane * 4);
+      else
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + row * D + lane * 2);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    }
+    const float inv = nk > 0 ? 1.f / l : 0.f;
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int q = 0; q < kPer / 2; ++q)
+      w[q] = F16 ? pack_f16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv) : pack_bf16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv);
+    uint16_t* op = static_cast<uint16_t*>(a.o.p) + b * a.o.sb + h * a.o.sh + (int64_t)n * a.o.sn + lane * kPer;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(op) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(op) = w[0];
+    if (lane == 0)
+      a.lse[((int64_t)b * s.H + h) * s.N + n] = nk > 0 ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int D, bool KV8, bool F16>
+cudaError_t launch_t(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st) {
+  auto kern = cross_fwd_kernel<D, KV8, F16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XSmem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  prof_start(st, kAttnFwd);
+  kern<<<(unsigned)p.grid, kThreads, XSmem<D>::kBytes, st>>>(mq, mk, mv, s, p, c, a);
+  if (p.split) cross_join_kernel<D, F16><<<dim3((unsigned)p.segs, 8), 256, 0, st>>>(s, p, a);
+  prof_stop(st, kAttnFwd);
+  return cudaGetLastError();
+}
+
+template <bool KV8>
+cudaError_t launch_any(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                       const CUtensorMap& mv, const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st) {
+  const bool f16 = s.dtype == SA2_FP16;
+  if (s.d == 128)
+    return f16 ? launch_t<128, KV8, true>(s, p, mq, mk, mv, c, a, st)
+               : launch_t<128, KV8, false>(s, p, mq, mk, mv, c, a, st);
+  return f16 ? launch_t<64, KV8, true>(s, p, mq, mk, mv, c, a, st)
+             : launch_t<64, KV8, false>(s, p, mq, mk, mv, c, a, st);
+}
+
+}  // namespace
+
+// Segments are whole where they fill the SMs at least four times over (their sizes then even
+// out) or where a sequence has fewer than eight key blocks (the second kernel would cost what
+// the split gains).
+FwdPlan cross_fwd_plan(const CrossShape& s, int sms) {
+  FwdPlan p;
+  p.nb = 128 / s.G;
+  p.tiles = (s.N + p.nb - 1) / p.nb;
+  const int64_t heads = (int64_t)s.B * s.Hkv;
+  const int blocks = (s.M + kKeyBlock - 1) / kKeyBlock;
+  const int64_t paired = heads * ((p.tiles + 1) / 2);
+  p.split = blocks >= 8 && paired < 4 * (int64_t)sms;
+  // one tile per CTA while that still finds a free SM
+  p.tp = !p.split && paired < sms ? 1 : 2;
+  p.pairs = (p.tiles + p.tp - 1) / p.tp;
+  const int64_t segs = heads * p.pairs;
+  p.segs = segs > INT32_MAX ? -1 : (int)segs;
+  const int64_t items = p.split ? segs * blocks : segs;
+  p.grid = (int)(items < sms ? items : sms);
+  return p;
+}
+
+size_t cross_fwd_partials(const CrossShape& s, const FwdPlan& p) {
+  return p.split ? (size_t)(p.grid + p.segs) * 256 * (s.d + 1) : 0;
+}
+
+cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                             const CUtensorMap& mv, const CrossFwdArgs& a, cudaStream_t st) {
+  return launch_any<false>(s, p, mq, mk, mv, CacheRef{}, a, st);
+}
+
+cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CacheRef& c, const CrossFwdArgs& a,
+                             cudaStream_t st) {
+  const CUtensorMap none{};
+  return launch_any<true>(s, p, none, none, none, c, a, st);
+}
+
+}  // namespace sa2

@@ -1,0 +1,84 @@
+// Declarations shared by the cross- and cache-attention sources (cross_*.cu, cache8.cu).
+#pragma once
+
+#include "sa2_internal.h"
+
+namespace sa2 {
+
+// Shape of a cross- or cache-attention call.  M is the key capacity: sequence b attends to its
+// first kv_len[b] keys.  Query heads h = hk * G + g share key head hk.
+struct CrossShape {
+  int B, H, Hkv, G, N, M, d;
+  int dtype;  // SA2_BF16 or SA2_FP16
+  unsigned long long wait_ns, stall_ns;
+};
+
+// A token tensor [B, heads, tokens, d], strides in elements.
+struct TokenRef {
+  void* p;
+  int64_t sb, sh, sn;
+};
+
+// The 8-bit cache: e4m3 keys and values and one power-of-two scale per head and 64 tokens.
+struct CacheRef {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int64_t sb, sh, sn;  // of k and v
+  int C, nsb;          // capacity in tokens, scales per head
+};
+
+constexpr int kKeyBlock = 128;  // keys per step of the cross- and cache-attention kernels
+
+// How the work of a forward call is split over CTAs.  A segment is one pair of query tiles of
+// one key head; a tile holds nb tokens of all G heads of the group, row = token * G + g.
+//   direct (split = 0): a work item is a whole segment, items go round robin over the CTAs;
+//   split:              the 128-key blocks of all segments are cut into `grid` equal runs, one
+//                       per CTA.  A run may begin or end inside a segment; each part of a
+//                       segment leaves its own O and log2 sum exp in slot CTA + segment, and a
+//                       second kernel joins a segment's parts in the order of its keys.
+struct FwdPlan {
+  int nb, tiles;
+  int tp, pairs;  // tiles per segment (1 or 2), segments per key head
+  int segs;
+  int grid;
+  int split;
+};
+
+struct CrossFwdArgs {
+  const int32_t* kv_len;  // [B] or null
+  TokenRef q;             // read by the cache kernel only (the other one has a tensor map)
+  TokenRef o;
+  float* lse;     // [B, H, N]
+  float* part_o;  // split: [grid + segs][256][d]
+  float* part_l;  // split: [grid + segs][256], log2 units
+  float scale_log2;
+  unsigned* status;
+};
+
+FwdPlan cross_fwd_plan(const CrossShape& s, int sms);
+size_t cross_fwd_partials(const CrossShape& s, const FwdPlan& p);  // floats of part_o + part_l
+
+// The device's status word, and the wait settings of the calling thread's next launches
+// (sa2_api.cu).
+unsigned* status_word();
+void wait_settings(unsigned long long* wait_ns, unsigned long long* stall_ns);
+
+// Tensor map of a 16-bit token tensor [B, heads, tokens, d] seen as (d, G, tokens, heads / G,
+// B), boxes of 64 channels x box_g heads x box_n tokens with the 128-byte swizzle; tokens past
+// the end read as zero (attn_common.cu).
+bool make_group_map(CUtensorMap* map, const TokenRef& t, int B, int heads, int G, int tokens, int d, int box_g,
+                    int box_n, bool f16);
+
+cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                             const CUtensorMap& mv, const CrossFwdArgs& a, cudaStream_t st);
+cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CacheRef& c, const CrossFwdArgs& a,
+                             cudaStream_t st);
+cudaError_t launch_cache_append(const CacheRef& c, int B, int Hkv, int d, int n, bool f16, const TokenRef& k,
+                                const TokenRef& v, const int32_t* pos, const int32_t* n_new, unsigned* status,
+                                cudaStream_t st);
+cudaError_t launch_cache_read(const CacheRef& c, int B, int Hkv, int d, int n, bool f16, const TokenRef& k,
+                              const TokenRef& v, const int32_t* pos, unsigned* status, cudaStream_t st);
+
+}  // namespace sa2

@@ -1,0 +1,90 @@
+// The order of work of the cross- and cache-attention forward kernels (FwdPlan): every role of a
+// CTA, and the kernel that joins split segments, walks the same sequence of pieces.
+#pragma once
+
+#include "cross_internal.h"
+
+namespace sa2 {
+
+// Keys of sequence b, clamped to [0, M].
+__device__ __forceinline__ int key_count(const int32_t* kv_len, int b, int M) {
+  const int n = kv_len ? kv_len[b] : M;
+  return n < 0 ? 0 : (n > M ? M : n);
+}
+__device__ __forceinline__ int key_blocks(int keys) { return (keys + kKeyBlock - 1) / kKeyBlock; }
+
+// Key blocks of all segments together; called by whole warps.
+__device__ __forceinline__ int64_t total_key_blocks(const CrossShape& s, const int32_t* kv_len, int pairs) {
+  int64_t n = 0;
+  for (int b = (int)(threadIdx.x & 31); b < s.B; b += 32) n += key_blocks(key_count(kv_len, b, s.M));
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n * s.Hkv * pairs;
+}
+// Key blocks of one CTA's run in split mode.
+__device__ __forceinline__ int64_t run_length(int64_t total, int grid) {
+  const int64_t n = (total + grid - 1) / grid;
+  return n > 0 ? n : 1;
+}
+
+// A part of a segment: blocks [k0, k0 + nb) of the keys of key head hk of sequence b, for the
+// tile pair `pair`.
+struct Piece {
+  int b, hk, pair, seg;
+  int k0, nb;
+  int keys;  // of the sequence
+};
+
+struct PieceIter {
+  const CrossShape& s;
+  const FwdPlan& p;
+  const int32_t* kv_len;
+  int64_t g, g_end;  // split: the CTA's run of blocks; direct: the next segment in g
+  int b;             // split: sequence of block g, and the blocks before it
+  int64_t base;
+
+  __device__ __forceinline__ PieceIter(const CrossShape& s_, const FwdPlan& p_, const int32_t* kv_len_)
+      : s(s_), p(p_), kv_len(kv_len_), b(0), base(0) {
+    if (p.split) {
+      const int64_t total = total_key_blocks(s, kv_len, p.pairs);
+      const int64_t run = run_length(total, p.grid);
+      g = run * blockIdx.x;
+      g_end = g + run < total ? g + run : total;
+    } else {
+      g = blockIdx.x;
+      g_end = p.segs;
+    }
+  }
+  __device__ __forceinline__ bool next(Piece& x) {
+    if (g >= g_end) return false;
+    const int per_b = s.Hkv * p.pairs;
+    if (!p.split) {
+      x.seg = (int)g;
+      x.b = x.seg / per_b;
+      x.keys = key_count(kv_len, x.b, s.M);
+      x.k0 = 0;
+      x.nb = key_blocks(x.keys);
+      g += p.grid;
+    } else {
+      int nk = key_blocks(key_count(kv_len, b, s.M));
+      while (g >= base + (int64_t)nk * per_b) {  // g < total: ends at a sequence with keys
+        base += (int64_t)nk * per_b;
+        ++b;
+        nk = key_blocks(key_count(kv_len, b, s.M));
+      }
+      x.b = b;
+      x.keys = key_count(kv_len, b, s.M);
+      const int64_t off = g - base;
+      x.seg = b * per_b + (int)(off / nk);
+      x.k0 = (int)(off % nk);
+      const int64_t left = g_end - g;
+      x.nb = nk - x.k0 < left ? nk - x.k0 : (int)left;
+      g += x.nb;
+    }
+    const int in_b = x.seg - x.b * per_b;
+    x.hk = in_b / p.pairs;
+    x.pair = in_b - x.hk * p.pairs;
+    return true;
+  }
+};
+
+}  // namespace sa2

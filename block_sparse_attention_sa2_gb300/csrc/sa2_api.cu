@@ -6,7 +6,7 @@
 #include <mutex>
 
 #include "../../include/sa2.h"
-#include "sa2_internal.h"
+#include "cross_internal.h"
 
 using namespace sa2;
 
@@ -40,6 +40,14 @@ std::atomic<unsigned long long> g_wait_limit_ns{0}, g_stall_ns{0};
 
 namespace sa2 {
 
+unsigned* status_word() { return status_ptr(); }
+
+void wait_settings(unsigned long long* wait_ns, unsigned long long* stall_ns) {
+  const unsigned long long w = g_wait_limit_ns.load(std::memory_order_relaxed);
+  *wait_ns = w ? w : kWaitLimitNs;
+  *stall_ns = g_stall_ns.load(std::memory_order_relaxed);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 sa2_status check_shape(const sa2_shape* shape, ShapeArgs* s) {
@@ -64,9 +72,7 @@ sa2_status check_shape(const sa2_shape* shape, ShapeArgs* s) {
   s->sb = x.stride_b;
   s->sh = x.stride_h;
   s->sn = x.stride_n;
-  const unsigned long long w = g_wait_limit_ns.load(std::memory_order_relaxed);
-  s->wait_ns = w ? w : kWaitLimitNs;
-  s->stall_ns = g_stall_ns.load(std::memory_order_relaxed);
+  wait_settings(&s->wait_ns, &s->stall_ns);
   if (s->Tk > 7680 || score_rows_per_cta(s->Tk, s->d) == 0) return SA2_ERR_UNSUPPORTED;
   if ((int64_t)s->B * s->H * s->Tq >= (int64_t)1 << 31) return SA2_ERR_UNSUPPORTED;
   return SA2_OK;

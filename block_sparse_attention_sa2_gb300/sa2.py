@@ -18,7 +18,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsa2.so")
 
-SA2_BF16, SA2_FP32 = 0, 1
+SA2_BF16, SA2_FP32, SA2_FP16 = 0, 1, 2  # SA2_FP16: cross- and cache-attention calls only
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "alignment", 4: "workspace", 5: "cuda",
           6: "device timeout", 7: "device bounds", 8: "input beyond fp16 range"}
 
@@ -38,6 +38,23 @@ class Shape(ctypes.Structure):
 
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double)]
+
+
+class CrossShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("M", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class TensorStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+class Cache8Struct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("d", ctypes.c_int32)]
 
 
 class BlockMaskStruct(ctypes.Structure):
@@ -76,6 +93,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa2_vd_loss_workspace_size.argtypes = [S]
     lib.sa2_vd_loss.restype = ctypes.c_int
     lib.sa2_vd_loss.argtypes = [S, P, P, P, P, P, P, P, Z, P]
+    X, T, C, I = ctypes.POINTER(CrossShape), ctypes.POINTER(TensorStruct), ctypes.POINTER(Cache8Struct), ctypes.c_int32
+    lib.sa2_cross_fwd_workspace_size.restype = Z
+    lib.sa2_cross_fwd_workspace_size.argtypes = [X]
+    lib.sa2_cross_attn_fwd.restype = ctypes.c_int
+    lib.sa2_cross_attn_fwd.argtypes = [X, T, T, T, P, F, T, P, P, Z, P]
+    lib.sa2_cache8_append.restype = ctypes.c_int
+    lib.sa2_cache8_append.argtypes = [C, I, I, T, T, P, P, P]
+    lib.sa2_cache8_read.restype = ctypes.c_int
+    lib.sa2_cache8_read.argtypes = [C, I, I, T, T, P, P]
+    lib.sa2_cache8_attn.restype = ctypes.c_int
+    lib.sa2_cache8_attn.argtypes = [X, T, C, P, F, T, P, P, Z, P]
     lib.sa2_get_device_status.restype = ctypes.c_int
     lib.sa2_get_device_status.argtypes = [P]
     lib.sa2_debug_set_wait_limit.restype = None
@@ -236,6 +264,212 @@ def vd_loss(o_s: torch.Tensor, o_t: torch.Tensor, o_s_lo: Optional[torch.Tensor]
                                           _ptr(o_t_lo), d_o.data_ptr(), loss.data_ptr(), ws.data_ptr(),
                                           ws.numel(), _stream(stream)))
     return loss, d_o
+
+
+# --------------------------------------------------- attention to keys of another length
+
+_DTYPE = {torch.bfloat16: SA2_BF16, torch.float16: SA2_FP16}
+
+
+def _token_struct(x: torch.Tensor, name: str, shape, dtype, device) -> TensorStruct:
+    if tuple(x.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(x.shape)}")
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.device != device:
+        raise ValueError(f"{name} must be on {device}, got {x.device}")
+    if x.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return TensorStruct(x.data_ptr(), x.stride(0), x.stride(1), x.stride(2))
+
+
+def _int32(x: Optional[torch.Tensor], name: str, B: int, device) -> Optional[int]:
+    if x is None:
+        return None
+    if x.dtype != torch.int32 or tuple(x.shape) != (B,) or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{B}] on {device}")
+    return x.data_ptr()
+
+
+def _contiguous_f32(x: torch.Tensor, name: str, shape, device) -> int:
+    if x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)} on {device}")
+    return x.data_ptr()
+
+
+def _workspace_of(ws: Optional[torch.Tensor], nbytes: int, device, stream):
+    """The caller's workspace, or a new one that outlives the work on ``stream``."""
+    if ws is None and nbytes:
+        ws = workspace(nbytes, device)
+        if stream is not None:
+            ws.record_stream(stream)
+    if ws is not None and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+
+
+def _new_like(x: torch.Tensor, stream) -> torch.Tensor:
+    y = torch.empty_like(x)
+    if stream is not None:
+        y.record_stream(stream)
+    return y
+
+
+def _on(device):
+    """The device that a call's tensors are on, as the current one."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
+    return torch.cuda.device(device)
+
+
+def _cross_shape(q: torch.Tensor, Hkv: int, M: int) -> CrossShape:
+    if q.dim() != 4:
+        raise ValueError("token tensors are [B, H, N, d]")
+    if q.dtype not in _DTYPE:
+        raise ValueError(f"unsupported dtype {q.dtype}: torch.bfloat16 or torch.float16")
+    B, H, N, d = q.shape
+    return CrossShape(B, H, Hkv, N, M, d, _DTYPE[q.dtype], 0)
+
+
+def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """sa2_cross_attn_fwd: attention of q [B, H, N, d] to k, v [B, Hkv, M, d]; returns (O, LSE).
+
+    H is a multiple of Hkv (query head h reads key head h // (H // Hkv)); bfloat16 or float16; each
+    tensor with strides of its own.  ``kv_len`` ([B] int32 on the device): sequence b attends to its
+    first kv_len[b] keys; without keys O = 0 and LSE = -inf.  LSE is float32 [B, H, N]."""
+    lib = load_library()
+    if k.dim() != 4:
+        raise ValueError("token tensors are [B, H, N, d]")
+    shp = _cross_shape(q, k.shape[1], k.shape[2])
+    B, H, N, d = q.shape
+    kv = (B, k.shape[1], k.shape[2], d)
+    dev = q.device
+    with _on(dev):
+        o = _new_like(q, stream) if o is None else o
+        if lse is None:
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+            if stream is not None:
+                lse.record_stream(stream)
+        args = [_token_struct(x, n, s, q.dtype, dev) for x, n, s in ((q, "q", q.shape), (k, "k", kv), (v, "v", kv),
+                                                                      (o, "o", q.shape))]
+        w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(ctypes.byref(shp)), dev, stream)
+        _check("sa2_cross_attn_fwd", lib.sa2_cross_attn_fwd(
+            ctypes.byref(shp), args[0], args[1], args[2], _int32(kv_len, "kv_len", B, dev), float(scale or 0.0),
+            args[3], _contiguous_f32(lse, "lse", (B, H, N), dev), w, wn, _stream(stream)))
+    return o, lse
+
+
+@dataclass
+class KvCache8:
+    """Keys and values held in 8 bits: e4m3 [B, Hkv, C, d] (k and v with the same strides) and one
+    power-of-two scale for each head and block of 64 tokens.  The caller keeps the lengths."""
+    k: torch.Tensor  # [B, Hkv, C, d] float8_e4m3fn (or uint8)
+    v: torch.Tensor
+    k_scale: torch.Tensor  # [B, Hkv, ceil(C / 64)] float32
+    v_scale: torch.Tensor
+
+    BLOCK = 64
+
+    @staticmethod
+    def empty(B: int, Hkv: int, capacity: int, d: int, device) -> "KvCache8":
+        k, v = (torch.empty((B, Hkv, capacity, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+        ks, vs = (torch.empty((B, Hkv, blocks(capacity, KvCache8.BLOCK)), dtype=torch.float32, device=device)
+                  for _ in range(2))
+        return KvCache8(k, v, ks, vs)
+
+    def struct(self) -> Cache8Struct:
+        k, v = self.k, self.v
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
+            raise ValueError("the cache's k and v are [B, Hkv, C, d] with the same strides, d contiguous")
+        for x in (k, v):
+            if x.dtype not in (torch.float8_e4m3fn, torch.uint8) or x.device != k.device:
+                raise ValueError("the cache's k and v are float8_e4m3fn (or uint8) on one device")
+        B, Hkv, C, d = k.shape
+        scales = (B, Hkv, blocks(C, self.BLOCK))
+        return Cache8Struct(k.data_ptr(), v.data_ptr(), _contiguous_f32(self.k_scale, "k_scale", scales, k.device),
+                            _contiguous_f32(self.v_scale, "v_scale", scales, k.device), k.stride(0), k.stride(1),
+                            k.stride(2), B, Hkv, C, d)
+
+
+def cache8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                  n_new: Optional[torch.Tensor] = None, stream=None) -> None:
+    """sa2_cache8_append: writes k, v [B, Hkv, n, d] (bfloat16 or float16) at positions pos[b] ..
+    pos[b] + n - 1 (n_new[b] tokens of each sequence where given).  ``pos``, ``n_new``: [B] int32."""
+    lib = load_library()
+    c = cache.struct()
+    if k.dim() != 4:
+        raise ValueError("token tensors are [B, H, N, d]")
+    if k.dtype not in _DTYPE:
+        raise ValueError(f"unsupported dtype {k.dtype}: torch.bfloat16 or torch.float16")
+    dev, n = cache.k.device, k.shape[2]
+    if n == 0:
+        return
+    with _on(dev):
+        shape = (c.B, c.Hkv, n, c.d)
+        if pos is None:
+            raise ValueError("pos is required")
+        _check("sa2_cache8_append", lib.sa2_cache8_append(
+            ctypes.byref(c), n, _DTYPE[k.dtype], _token_struct(k, "k", shape, k.dtype, dev),
+            _token_struct(v, "v", shape, k.dtype, dev), _int32(pos, "pos", c.B, dev),
+            _int32(n_new, "n_new", c.B, dev), _stream(stream)))
+
+
+def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
+                v: Optional[torch.Tensor] = None, stream=None):
+    """sa2_cache8_read: the values of tokens pos[b] .. pos[b] + n - 1 as (K, V) [B, Hkv, n, d]."""
+    lib = load_library()
+    c = cache.struct()
+    dev = cache.k.device
+    if dtype not in _DTYPE:
+        raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
+    with _on(dev):
+        shape = (c.B, c.Hkv, n, c.d)
+        if pos is None:
+            raise ValueError("pos is required")
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=dev)
+            if stream is not None:
+                k.record_stream(stream)
+        if v is None:
+            v = _new_like(k, stream)
+        if n == 0:
+            return k, v
+        _check("sa2_cache8_read", lib.sa2_cache8_read(
+            ctypes.byref(c), n, _DTYPE[dtype], _token_struct(k, "k", shape, dtype, dev),
+            _token_struct(v, "v", shape, dtype, dev), _int32(pos, "pos", c.B, dev), _stream(stream)))
+    return k, v
+
+
+def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: Optional[float] = None,
+                o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None, stream=None):
+    """sa2_cache8_attn: attention of q [B, H, N, d] to the first kv_len[b] tokens of the cache;
+    returns (O, LSE) as cross_attn_fwd does."""
+    lib = load_library()
+    c = cache.struct()
+    shp = _cross_shape(q, c.Hkv, c.C)
+    B, H, N, d = q.shape
+    if (B, d) != (c.B, c.d):
+        raise ValueError(f"the cache holds B = {c.B}, d = {c.d}; q has B = {B}, d = {d}")
+    if kv_len is None:
+        raise ValueError("kv_len is required")
+    dev = q.device
+    if cache.k.device != dev:
+        raise ValueError(f"the cache must be on {dev}, got {cache.k.device}")
+    with _on(dev):
+        o = _new_like(q, stream) if o is None else o
+        if lse is None:
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+            if stream is not None:
+                lse.record_stream(stream)
+        w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(ctypes.byref(shp)), dev, stream)
+        _check("sa2_cache8_attn", lib.sa2_cache8_attn(
+            ctypes.byref(shp), _token_struct(q, "q", q.shape, q.dtype, dev), ctypes.byref(c),
+            _int32(kv_len, "kv_len", B, dev), float(scale or 0.0), _token_struct(o, "o", q.shape, q.dtype, dev),
+            _contiguous_f32(lse, "lse", (B, H, N), dev), w, wn, _stream(stream)))
+    return o, lse
 
 
 def device_status(stream=None) -> int:

@@ -50,7 +50,11 @@ typedef enum sa2_status {
   SA2_ERR_RANGE = 8          /* device: an attention input exceeded the fp16 range (saturated) */
 } sa2_status;
 
-typedef enum sa2_dtype { SA2_BF16 = 0, SA2_FP32 = 1 } sa2_dtype;
+typedef enum sa2_dtype {
+  SA2_BF16 = 0,
+  SA2_FP32 = 1,
+  SA2_FP16 = 2 /* cross- and cache-attention calls only */
+} sa2_dtype;
 
 typedef struct sa2_shape {
   int32_t B, H, N, d;
@@ -261,6 +265,113 @@ sa2_status sa2_attn_bwd_with_fwd_ws(const sa2_shape* shape, const void* q, const
 size_t sa2_vd_loss_workspace_size(const sa2_shape* shape);
 sa2_status sa2_vd_loss(const sa2_shape* shape, const void* o_s, const void* o_s_lo, const void* o_t,
                        const void* o_t_lo, void* d_o, double* loss, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Attention to keys of another length: cross attention (queries of N tokens to M keys, e.g.
+ * video tokens to text or image states) and attention to keys and values held in an 8-bit
+ * cache.  The pages have no counterpart; the definitions are those of sa2_attn_fwd and
+ * sa2_attn_bwd with every key kept, and are spelled out at each entry point.
+ *
+ * Conventions of these entry points, beside those above
+ * - Each token tensor carries its own strides (sa2_tensor): q, o, dO, dq are [B, H, N, d],
+ *   k, v, dk, dv are [B, Hkv, M, d], d contiguous.  The stride of a dimension of size 1 is
+ *   ignored; every other one must be positive and a multiple of 16 bytes, stride_n >= d.
+ *   Inputs may overlap one another; outputs overlap nothing.
+ * - Query head h reads key head h / (H / Hkv): H is a multiple of Hkv, H / Hkv <= 64.
+ * - d in {64, 128}; dtype SA2_BF16 or SA2_FP16 (the backward: SA2_BF16); 1 <= N, M < 2^28;
+ *   B, Hkv <= 32767.
+ * - kv_len [B] int32 (device): sequence b attends to its keys 0 .. kv_len[b] - 1.  NULL: all
+ *   M.  What k and v hold behind that, infinities and NaN too, is not used.  A length outside
+ *   [0, M] is clamped and reported as SA2_ERR_DEVICE_BOUNDS.  A sequence of length 0 gets
+ *   O = 0, LSE = -inf and zero gradients.
+ */
+typedef struct sa2_tensor {
+  void* data;
+  int64_t stride_b, stride_h, stride_n; /* in elements */
+} sa2_tensor;
+
+typedef struct sa2_cross_shape {
+  int32_t B, H, Hkv, N, M, d;
+  int32_t dtype;    /* sa2_dtype */
+  int32_t reserved; /* must be 0 */
+} sa2_cross_shape;
+
+/*
+ * Bytes of device workspace sa2_cross_attn_fwd (and sa2_cache8_attn with M = the cache's
+ * capacity) needs: the partial results of calls whose keys are split over the SMs because
+ * they have few queries, else 0.  Also 0 for an invalid shape.  Depends on the current
+ * device's SM count.
+ */
+size_t sa2_cross_fwd_workspace_size(const sa2_cross_shape* shape);
+
+/*
+ * sa2_cross_attn_fwd -- for every query a of sequence b, over its keys c < kv_len[b]:
+ *   s_ac = scale * q_a . k_c,  LSE_a = log sum_c exp(s_ac)  (natural log),
+ *   O_a = sum_c exp(s_ac - LSE_a) v_c.
+ * Scores, the softmax statistics and the sums are held in fp32; P is rounded to the call's
+ * 16-bit type for P V.
+ *   scale   <= 0 means 1/sqrt(d)
+ *   lse     [B, H, N] fp32 output, contiguous
+ *   ws      device workspace of at least sa2_cross_fwd_workspace_size(shape) bytes (may be
+ *           NULL when that is 0); two calls that may run at the same time need one each
+ */
+sa2_status sa2_cross_attn_fwd(const sa2_cross_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
+                              const sa2_tensor* v, const int32_t* kv_len, float scale, const sa2_tensor* o,
+                              float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The 8-bit key/value cache: [B, Hkv, C, d] e4m3 keys and values (k and v share strides, in
+ * elements = bytes) and, for each head and block of 64 tokens, one scale; a token's value is
+ * e4m3 * scale.  k_scale, v_scale: [B, Hkv, ceil(C / 64)] fp32, contiguous.  A scale is a
+ * power of two, 2^e with e in [-100, 119].  The caller keeps the sequences' lengths; bytes
+ * and scales behind them are not used.
+ */
+typedef struct sa2_cache8 {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t stride_b, stride_h, stride_n;
+  int32_t B, Hkv, C, d;
+} sa2_cache8;
+
+/*
+ * sa2_cache8_append -- writes new tokens of k and v ([B, Hkv, n, d], dtype SA2_BF16 or
+ * SA2_FP16) at positions pos[b] .. pos[b] + n_b - 1 of each sequence, n_b = n_new[b] (NULL:
+ * n).  For each touched block and head, K and V apart: e = least integer with
+ * amax(new tokens) <= 448 * 2^e, within [-100, 119]; a block that keeps earlier tokens
+ * (positions before pos[b]) takes the larger of that and its present scale, and where that
+ * raises its scale the kept values are rounded again under it; x8 = e4m3(x / 2^e), to
+ * nearest, ties to even.  Tokens behind the new ones are given up.
+ * A position or count out of range is clamped, tokens beyond C are dropped, both reported as
+ * SA2_ERR_DEVICE_BOUNDS; magnitudes above 448 * 2^119 are saturated and NaN kept, both
+ * reported as SA2_ERR_RANGE.
+ *   pos, n_new  [B] int32, device
+ */
+sa2_status sa2_cache8_append(const sa2_cache8* cache, int32_t n, int32_t dtype, const sa2_tensor* k,
+                             const sa2_tensor* v, const int32_t* pos, const int32_t* n_new, void* stream);
+
+/*
+ * sa2_cache8_read -- the values of tokens pos[b] .. pos[b] + n - 1 of each sequence into k
+ * and v ([B, Hkv, n, d], dtype SA2_BF16, exact, or SA2_FP16, rounded; infinite beyond fp16).
+ * Tokens outside [0, C) read as zero and are reported as SA2_ERR_DEVICE_BOUNDS.
+ */
+sa2_status sa2_cache8_read(const sa2_cache8* cache, int32_t n, int32_t dtype, const sa2_tensor* k,
+                           const sa2_tensor* v, const int32_t* pos, void* stream);
+
+/*
+ * sa2_cache8_attn -- sa2_cross_attn_fwd with the keys and values that the cache stands for
+ * (M = C, kv_len required).  Nothing is written back at 16 bits: K's scale multiplies the
+ * scores, and V's enters the exponent, P V = sum_c exp2(log2(e) s_c + log2(v_scale) - m) v8_c
+ * with m the running maximum of that exponent, so neither loses range.  The products run in
+ * fp16 with fp32 sums (e4m3 is exact in fp16; bf16 queries are converted under a power-of-two
+ * scale for each row, exact unless 2^-29 below the row's largest).
+ *   shape  B, Hkv, d and M as in the cache
+ */
+sa2_status sa2_cache8_attn(const sa2_cross_shape* shape, const sa2_tensor* q, const sa2_cache8* cache,
+                           const int32_t* kv_len, float scale, const sa2_tensor* o, float* lse, void* ws,
+                           size_t ws_bytes, void* stream);
 
 /*
  * Launch profiler (instrumentation of this library; the pages have no counterpart).
