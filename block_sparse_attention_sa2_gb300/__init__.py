@@ -16,6 +16,7 @@ from .sa2 import (  # noqa: F401
     cache8_attn,
     cache8_read,
     check_device,
+    cross_attn_bwd,
     cross_attn_fwd,
     debug_set_wait_limit,
     device_status,

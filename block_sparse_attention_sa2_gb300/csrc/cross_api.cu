@@ -142,6 +142,55 @@ sa2_status sa2_cross_attn_fwd(const sa2_cross_shape* shape, const sa2_tensor* q,
   return cuda_status(launch_cross_fwd(s, plan, mq, mk, mv, a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t sa2_cross_bwd_workspace_size(const sa2_cross_shape* shape) {
+  CrossShape s;
+  if (check_cross(shape, &s) != SA2_OK || s.dtype != SA2_BF16) return 0;
+  size_t stats;
+  return cross_bwd_floats(s, cross_bwd_plan(s, sm_count()), &stats) * sizeof(float);
+}
+
+sa2_status sa2_cross_attn_bwd(const sa2_cross_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
+                              const sa2_tensor* v, const sa2_tensor* o, const float* lse, const sa2_tensor* dO,
+                              const int32_t* kv_len, float scale, const sa2_tensor* dq, const sa2_tensor* dk,
+                              const sa2_tensor* dv, void* ws, size_t ws_bytes, void* stream) {
+  CrossShape s;
+  sa2_status st = check_cross(shape, &s);
+  if (st != SA2_OK) return st;
+  if (s.dtype != SA2_BF16) return SA2_ERR_UNSUPPORTED;
+  if (!lse || !std::isfinite(scale)) return SA2_ERR_INVALID_ARG;
+  CrossBwdArgs a;
+  TokenRef qr, kr, vr;
+  st = check_tensor(q, s.B, s.H, s.N, s.d, 2, &qr);
+  if (st == SA2_OK) st = check_tensor(k, s.B, s.Hkv, s.M, s.d, 2, &kr);
+  if (st == SA2_OK) st = check_tensor(v, s.B, s.Hkv, s.M, s.d, 2, &vr);
+  if (st == SA2_OK) st = check_tensor(o, s.B, s.H, s.N, s.d, 2, &a.o);
+  if (st == SA2_OK) st = check_tensor(dO, s.B, s.H, s.N, s.d, 2, &a.dO);
+  if (st == SA2_OK) st = check_tensor(dq, s.B, s.H, s.N, s.d, 2, &a.dq);
+  if (st == SA2_OK) st = check_tensor(dk, s.B, s.Hkv, s.M, s.d, 2, &a.dk);
+  if (st == SA2_OK) st = check_tensor(dv, s.B, s.Hkv, s.M, s.d, 2, &a.dv);
+  if (st != SA2_OK) return st;
+  if (misaligned4(lse) || misaligned4(kv_len) || !aligned16(ws)) return SA2_ERR_ALIGNMENT;
+  const BwdPlan plan = cross_bwd_plan(s, sm_count());
+  if ((int64_t)s.B * s.Hkv * plan.tiles > INT32_MAX || (int64_t)s.B * s.Hkv > 65535) return SA2_ERR_UNSUPPORTED;
+  size_t stats;
+  const size_t floats = cross_bwd_floats(s, plan, &stats);
+  if (!ws || ws_bytes < floats * sizeof(float)) return SA2_ERR_WORKSPACE;
+  CUtensorMap mq, mk, mv, mdo;
+  if (!make_group_map(&mq, qr, s.B, s.H, s.G, s.N, s.d, s.G, plan.nb, false) ||
+      !make_group_map(&mdo, a.dO, s.B, s.H, s.G, s.N, s.d, s.G, plan.nb, false) ||
+      !make_group_map(&mk, kr, s.B, s.Hkv, 1, s.M, s.d, 1, kKeyBlock, false) ||
+      !make_group_map(&mv, vr, s.B, s.Hkv, 1, s.M, s.d, 1, kKeyBlock, false))
+    return SA2_ERR_CUDA;
+  a.kv_len = kv_len;
+  a.lse = lse;
+  a.stats = static_cast<float*>(ws);
+  a.part = a.stats + stats;
+  a.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)s.d));
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.status = status_word();
+  return cuda_status(launch_cross_bwd(s, plan, mq, mk, mv, mdo, a, static_cast<cudaStream_t>(stream)));
+}
+
 sa2_status sa2_cache8_append(const sa2_cache8* cache, int32_t n, int32_t dtype, const sa2_tensor* k,
                              const sa2_tensor* v, const int32_t* pos, const int32_t* n_new, void* stream) {
   CacheRef c;

@@ -1,0 +1,844 @@
+// Backward of cross attention on sm_103a (tcgen05 + TMEM + TMA):
+//   P = exp(s - LSE), dP = dO V^T, D = rowsum(dO * O), dS = P (dP - D),
+//   dV = P^T dO, dK = scale dS^T Q, dQ = scale dS K.
+// Two kernels, one that walks the keys of a query tile (dQ) and one that walks the queries of a key
+// block (dK, dV): every sum is made in one order, in TMEM or in a fixed order of parts, so the
+// result does not depend on scheduling.  S and dP are computed in both: 7 products where one
+// kernel would do 5, but that one would have to add dQ up across CTAs, in fp32 in memory: for
+// 512 keys four times the size of dQ, written and read again, which costs more than 2 products.
+// P and dS are rounded to bf16 for their products.  A query tile's rows are tokens x the G heads
+// that share the key head, so that dK and dV of shared heads need no other sum.
+#include "cross_sched.cuh"
+
+namespace sa2 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void store32_bf16(uint16_t* dst, const float (&v)[32]) {
+  uint4* p = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                      pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+}
+
+// One product with A and B K-major in shared memory (128 rows per panel each).
+template <int D>
+__device__ __forceinline__ void issue_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    umma_ss(d, a + kmajor_kstep(kk, 128), b + kmajor_kstep(kk, 128), idesc, kk > 0 ? 1u : 0u);
+}
+// D (+)= A B with A in TMEM, 16 rows of B per k-step; A's k-steps 0..3 lie at column 0, 4..7 at 64
+// (each over the half of the scores that it was made from).
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps, bool fresh) {
+  for (int kk = 0; kk < steps; ++kk)
+    umma_ts(d, a + kk * 8 + (kk >= 4 ? 32 : 0), b + (uint64_t)(kk * 128), idesc, (fresh && kk == 0) ? 0u : 1u);
+}
+
+// ------------------------------------------------------------------------- statistics
+//
+// D and log2(e) * LSE of every query row.  D / 8 threads per row, one CTA per query tile.
+template <int D>
+__global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
+  constexpr int kLanes = D / 8;
+  const int64_t item = blockIdx.x;
+  const int tile = (int)(item % plan.tiles);
+  const int64_t head = item / plan.tiles;
+  const int b = (int)(head / s.Hkv), hk = (int)(head - (int64_t)b * s.Hkv);
+  const int ch = (threadIdx.x % kLanes) * 8;
+  float* rec = a.stats + item * 256;
+  for (int r = threadIdx.x / kLanes; r < 128; r += 256 / kLanes) {
+    const int tok_r = r / s.G, h = hk * s.G + r - tok_r * s.G;
+    const int n = tile * plan.nb + tok_r;
+    const bool live = tok_r < plan.nb && n < s.N;
+    float acc = 0.f;
+    if (live) {
+      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dO.p) + b * a.dO.sb +
+                                                      h * a.dO.sh + n * a.dO.sn + ch);
+      const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.p) + b * a.o.sb + h * a.o.sh +
+                                                      n * a.o.sn + ch);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), acc);
+        acc = fmaf(__uint_as_float(xs[i] & 0xFFFF0000u), __uint_as_float(ys[i] & 0xFFFF0000u), acc);
+      }
+    }
+    for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (ch == 0) {
+      rec[r] = live ? a.lse[((int64_t)b * s.H + h) * s.N + n] * 1.4426950408889634f : INFINITY;
+      rec[128 + r] = acc;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------- dQ
+//
+// A work item is a query tile; its CTA walks the key blocks.  Per block j:
+//   S_j = Q K_j^T, dP_j = dO V_j^T  (M = 128 rows, N = 128 keys), dS_j = P (dP - D) in bf16 over
+//   dP_j's columns in TMEM, dQ += dS_j K_j.
+// The issuer runs S_{j+1}, dP_{j+1}, dQ_j: S_{j+1} needs only that the row threads have read S_j
+// (dQ_{j-1} runs meanwhile), dP_{j+1} that dQ_{j-1} has completed (S_{j+1} runs meanwhile; dP has
+// two buffers), and dQ_j has a whole period of three products for dS_j to be made in.
+// Roles: warp 0 TMA, warp 1 MMA issuer, warps 4..11 row threads (two per row: keys 0..63 and
+// 64..127 of each block), warps 12..15 epilogue.
+// TMEM columns: S 0, dP 128 and 256, dQ 384.
+template <int D>
+struct DqSmem {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = 128 * 128 * kPanels;
+  static constexpr int kKStages = 3, kVStages = 2;
+  static constexpr int kOffQ = 0, kOffDO = kTile;
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + kKStages * kTile;
+  static constexpr int kOffBar = kOffV + kVStages * kTile;
+  // at least 120 KB, so that one CTA (512 TMEM columns) has an SM to itself
+  static constexpr int kBytes = (kOffBar + 512 + 1024) > 120 * 1024 ? (kOffBar + 512 + 1024) : 120 * 1024;
+  static_assert(kBytes <= (int)kMaxDynSmem, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, CrossShape s,
+                    BwdPlan plan, CrossBwdArgs a) {
+  using L = DqSmem<D>;
+  constexpr int kKSt = L::kKStages, kVSt = L::kVStages;
+  constexpr uint32_t kS = 0, kDP = 128, kDQ = 384;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  auto bar_kfull = [&](int st) { return smem_u32(&bars[st]); };
+  auto bar_kempty = [&](int st) { return smem_u32(&bars[3 + st]); };
+  auto bar_vfull = [&](int st) { return smem_u32(&bars[6 + st]); };
+  auto bar_vempty = [&](int st) { return smem_u32(&bars[8 + st]); };
+  const uint32_t bar_q = smem_u32(&bars[10]), bar_qfree = smem_u32(&bars[11]);    // Q landed / read
+  const uint32_t bar_do = smem_u32(&bars[12]), bar_dofree = smem_u32(&bars[13]);  // dO
+  const uint32_t bar_s = smem_u32(&bars[14]), bar_sfree = smem_u32(&bars[15]);    // S in TMEM / read out
+  auto bar_dp = [&](int i) { return smem_u32(&bars[16 + i]); };    // dP buffer i in TMEM
+  auto bar_ds = [&](int i) { return smem_u32(&bars[18 + i]); };    // dS written over it
+  auto bar_dqm = [&](int i) { return smem_u32(&bars[20 + i]); };   // dQ += dS K from it completed
+  const uint32_t bar_dq = smem_u32(&bars[22]), bar_dqfree = smem_u32(&bars[23]);  // dQ of the item complete / read
+  const uint32_t bar_drain = smem_u32(&bars[24]);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
+  const WaitCtl wc{abort_flag, s.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kKSt; ++i) {
+      mbar_init(bar_kfull(i), 1);
+      mbar_init(bar_kempty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_vfull(i), 1);
+      mbar_init(bar_vempty(i), 1);
+      mbar_init(bar_dp(i), 1);
+      mbar_init(bar_ds(i), 256);
+      mbar_init(bar_dqm(i), 1);
+    }
+    mbar_init(bar_q, 1);
+    mbar_init(bar_qfree, 1);
+    mbar_init(bar_do, 1);
+    mbar_init(bar_dofree, 1);
+    mbar_init(bar_s, 1);
+    mbar_init(bar_sfree, 256);
+    mbar_init(bar_dq, 1);
+    mbar_init(bar_dqfree, 128);
+    mbar_init(bar_drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t items = (int64_t)s.B * s.Hkv * plan.tiles;
+  struct Item {
+    int b, hk, tile, keys, nk;
+  };
+  auto item_at = [&](int64_t i) {
+    Item x;
+    const int64_t head = i / plan.tiles;
+    x.tile = (int)(i - head * plan.tiles);
+    x.b = (int)(head / s.Hkv);
+    x.hk = (int)(head - (int64_t)x.b * s.Hkv);
+    x.keys = key_count(a.kv_len, x.b, s.M);
+    x.nk = key_blocks(x.keys);
+    return x;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * plan.nb * s.G);
+      uint32_t J = 0, nv = 0, qn = 0, don = 0;  // K, V, Q and dO tiles loaded
+      bool ok = true;
+      for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        const Item x = item_at(i);
+        for (int j = 0; j < x.nk; ++j) {
+          const int ks = J % kKSt, vs = nv % kVSt;
+          if (J >= (uint32_t)kKSt && !mbar_wait(bar_kempty(ks), ((J / kKSt) - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_kfull(ks), L::kTile);
+          for (int p = 0; p < L::kPanels; ++p)
+            tma_load_5d(sbase + L::kOffK + ks * L::kTile + p * 16384, &mk, bar_kfull(ks), p * 64, 0, j * kKeyBlock,
+                        x.hk, x.b);
+          ++J;
+          if (j == 0) {
+            if (qn >= 1 && !mbar_wait(bar_qfree, (qn - 1) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar_q, q_bytes);
+            for (int p = 0; p < L::kPanels; ++p)
+              tma_load_5d(sbase + L::kOffQ + p * 16384, &mq, bar_q, p * 64, 0, x.tile * plan.nb, x.hk, x.b);
+            ++qn;
+            if (don >= 1 && !mbar_wait(bar_dofree, (don - 1) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar_do, q_bytes);
+            for (int p = 0; p < L::kPanels; ++p)
+              tma_load_5d(sbase + L::kOffDO + p * 16384, &mdo, bar_do, p * 64, 0, x.tile * plan.nb, x.hk, x.b);
+            ++don;
+          }
+          if (nv >= (uint32_t)kVSt && !mbar_wait(bar_vempty(vs), ((nv / kVSt) - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_vfull(vs), L::kTile);
+          for (int p = 0; p < L::kPanels; ++p)
+            tma_load_5d(sbase + L::kOffV + vs * L::kTile + p * 16384, &mv, bar_vfull(vs), p * 64, 0, j * kKeyBlock,
+                        x.hk, x.b);
+          ++nv;
+        }
+      }
+      for (uint32_t v = J > (uint32_t)kKSt ? J - kKSt : 0; v < J; ++v)
+        mbar_drain(bar_kfull(v % kKSt), (v / kKSt) & 1, abort_flag);
+      for (uint32_t v = nv > (uint32_t)kVSt ? nv - kVSt : 0; v < nv; ++v)
+        mbar_drain(bar_vfull(v % kVSt), (v / kVSt) & 1, abort_flag);
+      if (qn) mbar_drain(bar_q, (qn - 1) & 1, abort_flag);
+      if (don) mbar_drain(bar_do, (don - 1) & 1, abort_flag);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idQ = idesc_bf16_f32(128, D, false, true);
+    const uint64_t qd = smem_desc(sbase + L::kOffQ, 16, 1024), dod = smem_desc(sbase + L::kOffDO, 16, 1024);
+    bool ok = true;
+    uint32_t J = 0, n = 0;  // blocks whose S, dP were issued; items
+    // dQ += dS K of block jj (count c over the CTA), the previous one issued
+    auto issue_dq = [&](const Item& x, int jj, uint32_t c) {
+      const int ks = c % kKSt, bb = c & 1;
+      const int valid = min(kKeyBlock, x.keys - jj * kKeyBlock), steps = (valid + 15) >> 4;
+      if (!__all_sync(0xffffffffu, (jj > 0 || n == 0 || mbar_wait(bar_dqfree, (n - 1) & 1, wc)) &&
+                                       mbar_wait(bar_ds(bb), (c >> 1) & 1, wc)))
+        return false;
+      if (valid & 15) {
+        // rows of K behind the last key, up to the next multiple of 16, as zeros: dS is 0 there, but
+        // 0 * NaN is NaN.  S_j, which read them before, has completed (dS_j was made from it).
+        const int rows = 16 * steps - valid, nz = rows * 8 * L::kPanels;
+        uint8_t* kt = smem + L::kOffK + ks * L::kTile;
+        for (int i = lane; i < nz; i += 32) {
+          const int row = valid + (i >> 3) % rows, p = (i >> 3) / rows;
+          *reinterpret_cast<uint4*>(kt + p * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+      }
+      tc_fence_after();
+      const uint64_t kmn = smem_desc(sbase + L::kOffK + ks * L::kTile, 16384, 1024);
+      if (elect_one()) {
+        issue_ts(tmem + kDQ, tmem + kDP + bb * 128, kmn, idQ, steps, jj == 0);
+        umma_commit(bar_dqm(bb));
+        umma_commit(bar_kempty(ks));
+        if (jj + 1 == x.nk) umma_commit(bar_dq);
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item x = item_at(i);
+      for (int j = 0; ok && j < x.nk; ++j, ++J) {
+        const int ks = J % kKSt, vs = J % kVSt, bb = J & 1;
+        const int steps = (min(kKeyBlock, x.keys - j * kKeyBlock) + 15) >> 4;
+        const uint32_t idS = idesc_bf16_f32(128, steps * 16, false, false);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_kfull(ks), (J / kKSt) & 1, wc) &&
+                                         (j > 0 || mbar_wait(bar_q, n & 1, wc)) &&
+                                         (J == 0 || mbar_wait(bar_sfree, (J - 1) & 1, wc)));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ss<D>(tmem + kS, qd, smem_desc(sbase + L::kOffK + ks * L::kTile, 16, 1024), idS);
+          umma_commit(bar_s);
+          if (j + 1 == x.nk) umma_commit(bar_qfree);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_vfull(vs), (J / kVSt) & 1, wc) &&
+                                         (j > 0 || mbar_wait(bar_do, n & 1, wc)) &&
+                                         (J < 2 || mbar_wait(bar_dqm(bb), ((J >> 1) - 1) & 1, wc)));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ss<D>(tmem + kDP + bb * 128, dod, smem_desc(sbase + L::kOffV + vs * L::kTile, 16, 1024), idS);
+          umma_commit(bar_dp(bb));
+          umma_commit(bar_vempty(vs));
+          if (j + 1 == x.nk) umma_commit(bar_dofree);
+        }
+        __syncwarp();
+        if (j > 0) ok = issue_dq(x, j - 1, J - 1);
+      }
+      if (ok && x.nk > 0) {
+        ok = issue_dq(x, x.nk - 1, J - 1);
+        ++n;
+      }
+    }
+    if (elect_one()) umma_commit(bar_drain);
+    __syncwarp();
+    mbar_drain(bar_drain, 0, abort_flag);
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------------ row threads
+    if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
+    const int g = (warp - 4) >> 2;  // keys 64 g .. 64 g + 63 of each block
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    bool ok = true;
+    uint32_t J = 0;
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item x = item_at(i);
+      if (x.nk == 0) continue;
+      const float lse2 = a.stats[i * 256 + r], Dr = a.stats[i * 256 + 128 + r];
+      for (int j = 0; j < x.nk; ++j, ++J) {
+        const int bb = J & 1;
+        const int valid = x.keys - j * kKeyBlock - 64 * g;  // of this thread's 64 keys
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_s, J & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t u0[32], u1[32];
+        tmem_ld32(trow + kS + 64 * g, u0);
+        tmem_ld32(trow + kS + 64 * g + 32, u1);
+        tmem_ld_wait(u0);
+        tmem_ld_wait(u1);
+        tc_fence_before();
+        mbar_arrive(bar_sfree);
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          p[c] = ex2(fmaf(__uint_as_float(u0[c]), a.scale_log2, -lse2));
+          p[c + 32] = ex2(fmaf(__uint_as_float(u1[c]), a.scale_log2, -lse2));
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_dp(bb), (J >> 1) & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tdp = trow + kDP + bb * 128 + 64 * g;
+        uint32_t pk[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld32(tdp + 32 * h, u0);
+          tmem_ld_wait(u0);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            // behind the last key dP may be anything
+            const float d0 = 32 * h + c < valid ? p[32 * h + c] * (__uint_as_float(u0[c]) - Dr) : 0.f;
+            const float d1 = 32 * h + c + 1 < valid ? p[32 * h + c + 1] * (__uint_as_float(u0[c + 1]) - Dr) : 0.f;
+            pk[16 * h + c / 2] = pack_bf16x2(d0, d1);
+          }
+        }
+        tmem_st32(tdp, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_ds(bb));
+      }
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------------ epilogue
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int tok_r = r / s.G, gq = r - tok_r * s.G;
+    bool ok = true;
+    uint32_t n = 0;
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item x = item_at(i);
+      const int tok = x.tile * plan.nb + tok_r;
+      const bool row_valid = tok_r < plan.nb && tok < s.N;
+      uint16_t* row = static_cast<uint16_t*>(a.dq.p) + x.b * a.dq.sb + (int64_t)(x.hk * s.G + gq) * a.dq.sh +
+                      (int64_t)tok * a.dq.sn;
+      if (x.nk == 0) {
+        if (row_valid)
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_dq, n & 1, wc))) {
+        ok = false;
+        break;
+      }
+      ++n;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t u[32];
+        tmem_ld32(trow + kDQ + c0, u);
+        tmem_ld_wait(u);
+        if (c0 + 32 >= D) {
+          tc_fence_before();
+          mbar_arrive(bar_dqfree);
+        }
+        float v[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(u[c]) * a.scale;
+        if (row_valid) store32_bf16(row + c0, v);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) report_error(a.status, kDevErrTimeout);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// --------------------------------------------------------------------------- dK, dV
+//
+// A CTA holds a block of 128 keys and walks query tiles.  The products are formed transposed, keys
+// along the TMEM lanes, so that P^T and dS^T go from the element-wise threads to the next product
+// through TMEM.  Per tile u:
+//   S^T = K Q^T, dP^T = V dO^T  (M = 128 keys, N = 128 rows),  dV += P^T dO, dK += dS^T Q.
+// TMEM is full (S^T, dP^T, dV, dK: 128 columns each); P^T is written over S^T and dS^T over dP^T.
+// The issuer runs S, dP, dV, dK in this order: S_{u+1} waits for dV_u while dK_u runs, dP_{u+1} for
+// dK_u while S_{u+1} runs; P is made while dP runs and dS while dV runs.
+// Roles: warp 0 TMA, warp 1 MMA issuer, warps 4..11 element-wise (thread = key, two per key: rows
+// 0..63 and 64..127 of the tile).
+template <int D>
+struct DkvSmem {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = 128 * 128 * kPanels;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kOffK = 0, kOffV = kTile;
+  static constexpr int kOffStage = 2 * kTile;  // Q, dO, statistics
+  static constexpr int kStageQ = 0, kStageDO = kTile, kStageStats = 2 * kTile;
+  static constexpr int kStage = 2 * kTile + 1024;
+  static constexpr int kOffBar = kOffStage + kStages * kStage;
+  static constexpr int kBytes = kOffBar + 512 + 1024;
+  static_assert(kBytes <= (int)kMaxDynSmem && kBytes > 114 * 1024, "shared memory: one CTA per SM");
+};
+constexpr int kDkvThreads = 384;
+
+// The pieces of a CTA's run: key block kb of head (b, hk), query tiles [t0, t0 + nt).
+struct DkvPiece {
+  int b, hk, kb, keys, t0, nt;
+  bool whole;
+  int slot;
+};
+struct DkvIter {
+  const CrossShape& s;
+  const BwdPlan& p;
+  const int32_t* kv_len;
+  int64_t g, g_begin, g_end, base;
+  int b;
+  __device__ __forceinline__ DkvIter(const CrossShape& s_, const BwdPlan& p_, const int32_t* l) : s(s_), p(p_), kv_len(l), base(0), b(0) {
+    const int64_t total = total_key_blocks(s, kv_len, 1) * p.tiles;
+    const int64_t run = run_length(total, p.grid);
+    g = g_begin = run * blockIdx.x;
+    g_end = g + run < total ? g + run : total;
+  }
+  __device__ __forceinline__ bool next(DkvPiece& x) {
+    if (g >= g_end) return false;
+    int64_t nk = key_blocks(key_count(kv_len, b, s.M));
+    while (g >= base + nk * s.Hkv * p.tiles) {
+      base += nk * s.Hkv * p.tiles;
+      ++b;
+      nk = key_blocks(key_count(kv_len, b, s.M));
+    }
+    const int64_t off = g - base, seg = off / p.tiles;
+    x.b = b;
+    x.keys = key_count(kv_len, b, s.M);
+    x.hk = (int)(seg / nk);
+    x.kb = (int)(seg - x.hk * nk);
+    x.t0 = (int)(off - seg * p.tiles);
+    const int64_t left = g_end - g;
+    x.nt = p.tiles - x.t0 < left ? p.tiles - x.t0 : (int)left;
+    x.whole = x.nt == p.tiles;
+    x.slot = 2 * blockIdx.x + (g == g_begin ? 0 : 1);
+    g += x.nt;
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kDkvThreads, 1)
+    cross_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, CrossShape s,
+                      BwdPlan plan, CrossBwdArgs a) {
+  using L = DkvSmem<D>;
+  constexpr int kStages = L::kStages;
+  constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  auto bar_full = [&](int st) { return smem_u32(&bars[st]); };
+  auto bar_empty = [&](int st) { return smem_u32(&bars[4 + st]); };
+  const uint32_t bar_kv = smem_u32(&bars[8]), bar_kvfree = smem_u32(&bars[9]);
+  const uint32_t bar_s = smem_u32(&bars[10]), bar_dp = smem_u32(&bars[11]);    // S^T, dP^T in TMEM
+  const uint32_t bar_p = smem_u32(&bars[12]), bar_ds = smem_u32(&bars[13]);    // P^T, dS^T written
+  const uint32_t bar_dvm = smem_u32(&bars[14]), bar_dkm = smem_u32(&bars[15]); // dV, dK products completed
+  const uint32_t bar_accfree = smem_u32(&bars[16]);                            // the piece's sums read out
+  const uint32_t bar_drain = smem_u32(&bars[17]);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
+  const WaitCtl wc{abort_flag, s.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // Tile rows that hold no query (128 is not a multiple of G) are never loaded: zeros, since their
+  // P and dS are 0 but 0 * NaN is NaN.
+  const int used = plan.nb * s.G;
+  if (used < 128) {
+    const int n = (128 - used) * 8 * L::kPanels * 2 * kStages;
+    for (int i = tid; i < n; i += kDkvThreads) {
+      const int row = used + (i >> 3) % (128 - used);
+      int x = (i >> 3) / (128 - used);
+      const int p = x % L::kPanels;
+      x /= L::kPanels;
+      uint8_t* t = smem + L::kOffStage + (x >> 1) * L::kStage + ((x & 1) ? L::kStageDO : L::kStageQ);
+      *reinterpret_cast<uint4*>(t + p * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async();
+  }
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar_full(i), 1);
+      mbar_init(bar_empty(i), 1);
+    }
+    mbar_init(bar_kv, 1);
+    mbar_init(bar_kvfree, 1);
+    mbar_init(bar_s, 1);
+    mbar_init(bar_dp, 1);
+    mbar_init(bar_p, 256);
+    mbar_init(bar_ds, 256);
+    mbar_init(bar_dvm, 1);
+    mbar_init(bar_dkm, 1);
+    mbar_init(bar_accfree, 256);
+    mbar_init(bar_drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    DkvIter it(s, plan, a.kv_len);
+    if (lane == 0) {
+      const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * used);
+      uint32_t U = 0, n = 0;
+      bool ok = true;
+      DkvPiece x;
+      while (ok && it.next(x)) {
+        if (n >= 1 && !mbar_wait(bar_kvfree, (n - 1) & 1, wc)) break;
+        mbar_arrive_expect_tx(bar_kv, 2 * L::kTile);
+        for (int p = 0; p < L::kPanels; ++p) {
+          tma_load_5d(sbase + L::kOffK + p * 16384, &mk, bar_kv, p * 64, 0, x.kb * kKeyBlock, x.hk, x.b);
+          tma_load_5d(sbase + L::kOffV + p * 16384, &mv, bar_kv, p * 64, 0, x.kb * kKeyBlock, x.hk, x.b);
+        }
+        ++n;
+        for (int t = x.t0; t < x.t0 + x.nt; ++t, ++U) {
+          const int st = U % kStages;
+          if (U >= (uint32_t)kStages && !mbar_wait(bar_empty(st), ((U / kStages) - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
+          mbar_arrive_expect_tx(bar_full(st), 2 * q_bytes + 1024);
+          for (int p = 0; p < L::kPanels; ++p) {
+            tma_load_5d(stg + L::kStageQ + p * 16384, &mq, bar_full(st), p * 64, 0, t * plan.nb, x.hk, x.b);
+            tma_load_5d(stg + L::kStageDO + p * 16384, &mdo, bar_full(st), p * 64, 0, t * plan.nb, x.hk, x.b);
+          }
+          bulk_load(stg + L::kStageStats, a.stats + (((int64_t)x.b * s.Hkv + x.hk) * plan.tiles + t) * 256, 1024,
+                    bar_full(st));
+        }
+      }
+      for (uint32_t v = U > (uint32_t)kStages ? U - kStages : 0; v < U; ++v)
+        mbar_drain(bar_full(v % kStages), (v / kStages) & 1, abort_flag);
+      if (n) mbar_drain(bar_kv, (n - 1) & 1, abort_flag);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    DkvIter it(s, plan, a.kv_len);
+    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false), idG = idesc_bf16_f32(128, D, false, true);
+    const uint64_t kd = smem_desc(sbase + L::kOffK, 16, 1024), vd = smem_desc(sbase + L::kOffV, 16, 1024);
+    bool ok = true;
+    uint32_t U = 0, n = 0;
+    DkvPiece x;
+    while (ok && it.next(x)) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_kv, n & 1, wc));
+      for (int t = 0; ok && t < x.nt; ++t, ++U) {
+        const int st = U % kStages;
+        const bool last = t + 1 == x.nt;
+        const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc) &&
+                                         (U == 0 || mbar_wait(bar_dvm, (U - 1) & 1, wc)));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ss<D>(tmem + kS, kd, smem_desc(stg + L::kStageQ, 16, 1024), idS);
+          umma_commit(bar_s);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, U == 0 || mbar_wait(bar_dkm, (U - 1) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ss<D>(tmem + kDP, vd, smem_desc(stg + L::kStageDO, 16, 1024), idS);
+          umma_commit(bar_dp);
+          if (last) umma_commit(bar_kvfree);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, (t > 0 || n == 0 || mbar_wait(bar_accfree, (n - 1) & 1, wc)) &&
+                                         mbar_wait(bar_p, U & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ts(tmem + kDV, tmem + kS, smem_desc(stg + L::kStageDO, 16384, 1024), idG, 8, t == 0);
+          umma_commit(bar_dvm);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_ds, U & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ts(tmem + kDK, tmem + kDP, smem_desc(stg + L::kStageQ, 16384, 1024), idG, 8, t == 0);
+          umma_commit(bar_dkm);
+          umma_commit(bar_empty(st));
+        }
+        __syncwarp();
+      }
+      ++n;
+    }
+    if (elect_one()) umma_commit(bar_drain);
+    __syncwarp();
+    mbar_drain(bar_drain, 0, abort_flag);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- element-wise threads
+    if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
+    DkvIter it(s, plan, a.kv_len);
+    const int g = (warp - 4) >> 2;  // rows 64 g .. 64 g + 63 of each tile
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    bool ok = true;
+    uint32_t U = 0;
+    DkvPiece x;
+    while (ok && it.next(x)) {
+      const int key = x.kb * kKeyBlock + r;
+      for (int t = 0; t < x.nt; ++t, ++U) {
+        const int st = U % kStages;
+        const float4* l4 = reinterpret_cast<const float4*>(smem + L::kOffStage + st * L::kStage + L::kStageStats) + 16 * g;
+        const float4* d4 = l4 + 32;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc) && mbar_wait(bar_s, U & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float p[64];
+        uint32_t pk[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t u[32];
+          tmem_ld32(trow + kS + 64 * g + 32 * h, u);
+          tmem_ld_wait(u);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 l = l4[8 * h + q];
+            float* pp = p + 32 * h + 4 * q;
+            pp[0] = ex2(fmaf(__uint_as_float(u[4 * q]), a.scale_log2, -l.x));
+            pp[1] = ex2(fmaf(__uint_as_float(u[4 * q + 1]), a.scale_log2, -l.y));
+            pp[2] = ex2(fmaf(__uint_as_float(u[4 * q + 2]), a.scale_log2, -l.z));
+            pp[3] = ex2(fmaf(__uint_as_float(u[4 * q + 3]), a.scale_log2, -l.w));
+            pk[16 * h + 2 * q] = pack_bf16x2(pp[0], pp[1]);
+            pk[16 * h + 2 * q + 1] = pack_bf16x2(pp[2], pp[3]);
+          }
+        }
+        tmem_st32(trow + kS + 64 * g, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_p);
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_dp, U & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t u[32];
+          tmem_ld32(trow + kDP + 64 * g + 32 * h, u);
+          tmem_ld_wait(u);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 d = d4[8 * h + q];
+            const float* pp = p + 32 * h + 4 * q;
+            pk[16 * h + 2 * q] = pack_bf16x2(pp[0] * (__uint_as_float(u[4 * q]) - d.x),
+                                             pp[1] * (__uint_as_float(u[4 * q + 1]) - d.y));
+            pk[16 * h + 2 * q + 1] = pack_bf16x2(pp[2] * (__uint_as_float(u[4 * q + 2]) - d.z),
+                                                 pp[3] * (__uint_as_float(u[4 * q + 3]) - d.w));
+          }
+        }
+        tmem_st32(trow + kDP + 64 * g, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_ds);
+      }
+      if (!ok) break;
+      // ---- the piece's sums: thread = key, group g half of the channels
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_dkm, (U - 1) & 1, wc))) {  // the last product of all
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool live = key < x.keys, store = key < s.M;
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {  // dK, dV
+        const TokenRef& out = w ? a.dv : a.dk;
+        const float mul = w ? 1.f : a.scale;
+        uint16_t* row = static_cast<uint16_t*>(out.p) + x.b * out.sb + (int64_t)x.hk * out.sh + (int64_t)key * out.sn;
+        float* part = a.part + (((int64_t)x.slot * 2 + w) * 128 + r) * D;
+#pragma unroll 1
+        for (int c0 = g * (D / 2); c0 < (g + 1) * (D / 2); c0 += 32) {
+          uint32_t u[32];
+          tmem_ld32(trow + (w ? kDV : kDK) + c0, u);
+          tmem_ld_wait(u);
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = live ? __uint_as_float(u[c]) * mul : 0.f;
+          if (!x.whole) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              reinterpret_cast<float4*>(part + c0)[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          } else if (store) {
+            store32_bf16(row + c0, v);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar_accfree);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) report_error(a.status, kDevErrTimeout);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Adds the parts of key blocks whose tiles several runs shared, in run order, and writes zeros
+// behind the last key block of each sequence.  Grid (key blocks of M, B * Hkv).
+template <int D>
+__global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
+  const int kb = blockIdx.x, lane = threadIdx.x & 31;
+  const int b = blockIdx.y / s.Hkv, hk = blockIdx.y - b * s.Hkv;
+  const int keys = key_count(a.kv_len, b, s.M), nk = key_blocks(keys);
+  int64_t g0 = 0, g1 = 0, run = 1;
+  if (kb < nk) {
+    run = run_length(total_key_blocks(s, a.kv_len, 1) * plan.tiles, plan.grid);
+    int64_t before = 0;
+    for (int i = lane; i < b; i += 32) before += key_blocks(key_count(a.kv_len, i, s.M));
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    g0 = (before * s.Hkv + (int64_t)hk * nk + kb) * plan.tiles;
+    g1 = g0 + plan.tiles;
+    if (g0 / run == (g1 - 1) / run) return;  // one CTA had them all
+  }
+  const int c0 = (int)(g0 / run), c1 = kb < nk ? (int)((g1 - 1) / run) : c0 - 1;
+  for (int i = threadIdx.x; i < 2 * 128 * (D / 8); i += 256) {
+    const int w = i / (128 * (D / 8)), r = i / (D / 8) % 128, ch = i % (D / 8) * 8;
+    const int key = kb * kKeyBlock + r;
+    if (key >= s.M) continue;
+    float v[8] = {};
+    if (key < keys) {
+      for (int c = c0; c <= c1; ++c) {
+        const int slot = 2 * c + (run * c >= g0 ? 0 : 1);  // the part starts with the run, or inside it
+        const float4* p = reinterpret_cast<const float4*>(a.part + (((int64_t)slot * 2 + w) * 128 + r) * D + ch);
+        const float4 x = p[0], y = p[1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+    }
+    const TokenRef& out = w ? a.dv : a.dk;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out.p) + b * out.sb + hk * out.sh + key * out.sn + ch) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, const CUtensorMap& mdo, const CrossBwdArgs& a, cudaStream_t st) {
+  auto dq = cross_dq_kernel<D>;
+  auto dkv = cross_dkdv_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqSmem<D>::kBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvSmem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  prof_start(st, kBwdPre);
+  cross_stats_kernel<D><<<(unsigned)((int64_t)s.B * s.Hkv * p.tiles), 256, 0, st>>>(s, p, a);
+  prof_stop(st, kBwdPre);
+  prof_start(st, kAttnBwd);
+  dkv<<<(unsigned)p.grid, kDkvThreads, DkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
+  cross_dkdv_join_kernel<D><<<dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv)), 256, 0, st>>>(s, p, a);
+  prof_stop(st, kAttnBwd);
+  prof_start(st, kAttnBwdDq);
+  dq<<<(unsigned)p.dq_grid, kThreads, DqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
+  prof_stop(st, kAttnBwdDq);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+BwdPlan cross_bwd_plan(const CrossShape& s, int sms) {
+  BwdPlan p;
+  p.nb = 128 / s.G;
+  p.tiles = (s.N + p.nb - 1) / p.nb;
+  p.kblocks = (s.M + kKeyBlock - 1) / kKeyBlock;
+  const int64_t heads = (int64_t)s.B * s.Hkv;
+  p.dq_grid = (int)(heads * p.tiles < sms ? heads * p.tiles : sms);
+  const int64_t work = heads * p.kblocks * p.tiles;
+  p.grid = (int)(work < sms ? work : sms);
+  return p;
+}
+
+size_t cross_bwd_floats(const CrossShape& s, const BwdPlan& p, size_t* stats) {
+  *stats = (size_t)s.B * s.Hkv * p.tiles * 256;
+  return *stats + (size_t)2 * p.grid * 2 * 128 * s.d;
+}
+
+cudaError_t launch_cross_bwd(const CrossShape& s, const BwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                             const CUtensorMap& mv, const CUtensorMap& mdo, const CrossBwdArgs& a, cudaStream_t st) {
+  return s.d == 128 ? launch_t<128>(s, p, mq, mk, mv, mdo, a, st) : launch_t<64>(s, p, mq, mk, mv, mdo, a, st);
+}
+
+}  // namespace sa2

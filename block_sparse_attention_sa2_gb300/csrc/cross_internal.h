@@ -60,6 +60,34 @@ struct CrossFwdArgs {
 FwdPlan cross_fwd_plan(const CrossShape& s, int sms);
 size_t cross_fwd_partials(const CrossShape& s, const FwdPlan& p);  // floats of part_o + part_l
 
+// The backward's query tiles are those of the forward (nb tokens of all G heads, row = token * G +
+// g); its statistics are kept per tile: stats[(head * tiles + tile) * 256 + r] = log2(e) * LSE of
+// row r (+inf for rows that hold no query: their P is 0) and [... + 128 + r] = D, head = b * Hkv + hk.
+// The dK / dV kernel's work, (key block, query tile) pairs ordered by key head, key block and tile,
+// is cut into `grid` equal runs, one per CTA.  A run that holds a key block's tiles whole writes
+// its dK, dV; of the others each run leaves fp32 sums, slot 2 * CTA for the part that the run
+// begins with and 2 * CTA + 1 for one that begins inside it, which a second kernel adds in order.
+struct BwdPlan {
+  int nb, tiles;
+  int kblocks;  // 128-key blocks of M
+  int dq_grid, grid;
+};
+
+struct CrossBwdArgs {
+  const int32_t* kv_len;
+  TokenRef o, dO, dq, dk, dv;
+  const float* lse;
+  float* stats;
+  float* part;  // [2 * grid][2][128][d]: dK, dV
+  float scale, scale_log2;
+  unsigned* status;
+};
+
+BwdPlan cross_bwd_plan(const CrossShape& s, int sms);
+size_t cross_bwd_floats(const CrossShape& s, const BwdPlan& p, size_t* stats);
+cudaError_t launch_cross_bwd(const CrossShape& s, const BwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                             const CUtensorMap& mv, const CUtensorMap& mdo, const CrossBwdArgs& a, cudaStream_t st);
+
 // The device's status word, and the wait settings of the calling thread's next launches
 // (sa2_api.cu).
 unsigned* status_word();

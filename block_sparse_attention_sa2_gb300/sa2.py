@@ -98,6 +98,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa2_cross_fwd_workspace_size.argtypes = [X]
     lib.sa2_cross_attn_fwd.restype = ctypes.c_int
     lib.sa2_cross_attn_fwd.argtypes = [X, T, T, T, P, F, T, P, P, Z, P]
+    lib.sa2_cross_bwd_workspace_size.restype = Z
+    lib.sa2_cross_bwd_workspace_size.argtypes = [X]
+    lib.sa2_cross_attn_bwd.restype = ctypes.c_int
+    lib.sa2_cross_attn_bwd.argtypes = [X, T, T, T, T, P, T, P, F, T, T, T, P, Z, P]
     lib.sa2_cache8_append.restype = ctypes.c_int
     lib.sa2_cache8_append.argtypes = [C, I, I, T, T, P, P, P]
     lib.sa2_cache8_read.restype = ctypes.c_int
@@ -359,6 +363,31 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Op
             ctypes.byref(shp), args[0], args[1], args[2], _int32(kv_len, "kv_len", B, dev), float(scale or 0.0),
             args[3], _contiguous_f32(lse, "lse", (B, H, N), dev), w, wn, _stream(stream)))
     return o, lse
+
+
+def cross_attn_bwd(q, k, v, o, lse, do, kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   dq=None, dk=None, dv=None, ws: Optional[torch.Tensor] = None, stream=None):
+    """sa2_cross_attn_bwd: gradients (dQ, dK, dV) of cross_attn_fwd (bfloat16), whose o and lse on the
+    same q, k, v, kv_len and scale it takes; zero behind kv_len."""
+    lib = load_library()
+    if k.dim() != 4:
+        raise ValueError("token tensors are [B, H, N, d]")
+    shp = _cross_shape(q, k.shape[1], k.shape[2])
+    B, H, N, d = q.shape
+    kv = (B, k.shape[1], k.shape[2], d)
+    dev = q.device
+    with _on(dev):
+        dq = _new_like(q, stream) if dq is None else dq
+        dk = _new_like(k, stream) if dk is None else dk
+        dv = _new_like(v, stream) if dv is None else dv
+        t = {n: _token_struct(x, n, s, q.dtype, dev) for x, n, s in (
+            (q, "q", q.shape), (k, "k", kv), (v, "v", kv), (o, "o", q.shape), (do, "do", q.shape),
+            (dq, "dq", q.shape), (dk, "dk", kv), (dv, "dv", kv))}
+        w, wn = _workspace_of(ws, lib.sa2_cross_bwd_workspace_size(ctypes.byref(shp)), dev, stream)
+        _check("sa2_cross_attn_bwd", lib.sa2_cross_attn_bwd(
+            ctypes.byref(shp), t["q"], t["k"], t["v"], t["o"], _contiguous_f32(lse, "lse", (B, H, N), dev), t["do"],
+            _int32(kv_len, "kv_len", B, dev), float(scale or 0.0), t["dq"], t["dk"], t["dv"], w, wn, _stream(stream)))
+    return dq, dk, dv
 
 
 @dataclass

@@ -321,6 +321,29 @@ sa2_status sa2_cross_attn_fwd(const sa2_cross_shape* shape, const sa2_tensor* q,
                               float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Bytes of device workspace sa2_cross_attn_bwd needs: per-row statistics, and fp32 partial
+ * sums of dK and dV.  0 for an invalid shape.  Depends on the current device's SM count.
+ */
+size_t sa2_cross_bwd_workspace_size(const sa2_cross_shape* shape);
+
+/*
+ * sa2_cross_attn_bwd -- backward of sa2_cross_attn_fwd (SA2_BF16):
+ *   P = exp(s - LSE),  dV = P^T dO,  dP = dO V^T,  D_a = dO_a . O_a,
+ *   dS = P * (dP - D),  dQ = scale dS K,  dK = scale dS^T Q,
+ * dK and dV summed over the query heads that share a key head.  Sums are held in fp32, P and
+ * dS rounded to bf16 for their products; no sum depends on scheduling.  Keys behind
+ * kv_len[b], and sequences of length 0, get zero gradients.
+ *   o, lse       from sa2_cross_attn_fwd on the same q, k, v, kv_len and scale
+ *   dq, dk, dv   outputs: [B, H, N, d] and [B, Hkv, M, d], every element is written
+ *   ws           device workspace of at least sa2_cross_bwd_workspace_size(shape) bytes;
+ *                two calls that may run at the same time need one each
+ */
+sa2_status sa2_cross_attn_bwd(const sa2_cross_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
+                              const sa2_tensor* v, const sa2_tensor* o, const float* lse, const sa2_tensor* dO,
+                              const int32_t* kv_len, float scale, const sa2_tensor* dq, const sa2_tensor* dk,
+                              const sa2_tensor* dv, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * The 8-bit key/value cache: [B, Hkv, C, d] e4m3 keys and values (k and v share strides, in
  * elements = bytes) and, for each head and block of 64 tokens, one scale; a token's value is
  * e4m3 * scale.  k_scale, v_scale: [B, Hkv, ceil(C / 64)] fp32, contiguous.  A scale is a

@@ -10,6 +10,14 @@ O     the output's rounding, u |O|; P's rounding, u A with A = sum p |v|; the sc
       keys adds M 2^-25 max|v| (the row's largest p is at least 1 in that scale; with a cache the
       reference includes V's scale, so that max|v| is 448 times the largest scale).
 LSE   ds + 2^-19 (|LSE| + 1).
+
+dV    the output's rounding, u |dV|, and (u + 4 ds + 2^-16) sum p |dO|: P's rounding, what the scores
+      and the LSE (each by ds) change p by, and fp32 sums.
+dQ,   u |dQ| and (2 u + 4 ds + 2^-16) sum |dS||k| with |dS| taken by its terms, p (|dO||v| + sum p
+dK    |dO||v|): dS is rounded (u) and D = dO . O is made from the rounded O (u).
+In the 2-norm the roundings are independent and each is u / sqrt(3) of its term on average, so that
+with random inputs, where no sum cancels, the whole gradient is within sqrt(3) u / sqrt(3) = u of
+its norm; the tests ask for 2 u.
 """
 import math
 
@@ -68,8 +76,9 @@ def gradients(q, k, v, do, lens, scale=None):
             dq[b, h] = ds @ kk * scale
             dk[b, g, :n] += ds.T @ qq * scale
             dv[b, g, :n] += p.T @ dd
-            # magnitudes: dS is off by its own rounding and by what P and D are off
-            da = p * ((dd.abs() @ vv.abs().T) + (p * dp.abs()).sum(1, keepdim=True))
+            # magnitudes: |dP| and |D| by their terms
+            ap = dd.abs() @ vv.abs().T
+            da = p * (ap + (p * ap).sum(1, keepdim=True))
             aq[b, h] = da @ kk.abs() * scale
             ak[b, g, :n] += da.T @ qq.abs() * scale
             av[b, g, :n] += p.T @ dd.abs()
@@ -97,6 +106,21 @@ def check_forward(o, lse, q, k, v, lens, scale=None, p_type=None, v_max=None):
     bl = ds + 2.0**-19 * (torch.where(empty, 0.0, rl).abs() + 1)
     assert float((el / bl).max()) <= 1.0, f"LSE: {float((el / bl).max()):.3f} of the bound"
     return worst
+
+
+def check_gradients(got, q, k, v, do, lens, scale=None, norm=True):
+    want, mags = gradients(q, k, v, do, lens, scale)
+    ds = float(attention(q, k, v, lens, scale)[3].max())
+    u = U[q.dtype]
+    for name, g, w, a, roundings in zip(("dq", "dk", "dv"), got, want, mags, (2, 2, 1)):
+        assert g.shape == w.shape and g.dtype == q.dtype
+        bound = u * w.abs() * (1 + 2.0**-6) + (roundings * u + 4 * ds + 2.0**-16) * a
+        err = (g.double() - w).abs()
+        over = torch.where(err > 0, err / bound.clamp(min=1e-300), 0.0)
+        assert float(over.max()) <= 1.0, f"{name}: {float(over.max()):.3f} of the bound, max error {float(err.max()):.3e}"
+        if norm and float(w.norm()):
+            rel = float((g.double() - w).norm() / w.norm())
+            assert rel <= 2 * u, f"{name}: relative error {rel:.2e}"
 
 
 # ------------------------------------------------------------------------------ 8-bit cache
