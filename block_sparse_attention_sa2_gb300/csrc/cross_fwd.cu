@@ -9,12 +9,12 @@
 // (row = token * G + head), which lets few tokens of many heads fill a tile.
 //
 // Roles (512 threads): warp 0 TMA producer (Q tiles, a ring of K and V blocks of 128 keys);
-// warp 1 owner of TMEM and issuer of every MMA; warps 4..7 epilogue (16-bit keys) or converters
-// (8-bit keys: global memory -> registers -> fp16 in the ring, and Q to fp16); warps 8..11 and
-// 12..15 the softmax of tile 0 and 1, one row per thread.
-// Per key block j the issuer runs S_0 S_1 | P_0 V, P_1 V.  S_t(j) overwrites the TMEM columns that
-// hold P_t(j-1), so it waits for the completion of P_t V(j-1); in this order that wait passes while
-// the other tile's product still runs, and P_t(j) is made while S_1 and the other P V run.
+// warps 1 and 2 issuers of the MMAs of tile 0 and 1; warps 4..7 epilogue (16-bit keys) or
+// converters (8-bit keys: global memory -> registers -> fp16 in the ring, and Q to fp16); warps
+// 8..11 and 12..15 the softmax of tile 0 and 1, one row per thread.
+// The two tiles are chains of their own, S_t(j), softmax, P_t V(j), S_t(j+1), that share the ring
+// of keys: while one is in its softmax the other has the tensor cores.  S_t(j) overwrites the TMEM
+// columns that hold P_t(j-1), so its issuer waits for the completion of P_t V(j-1).
 //   S_t  = Q_t K_j^T   M = 128, N = 128, K = d   (shared memory, K-major)
 //   O_t += P_t V_j     M = 128, N = d, K = 128   (A = P from TMEM, V MN-major)
 // The softmax thread reads keys 64..127 of its row first and keeps them, takes the maximum over
@@ -77,29 +77,59 @@ __device__ __forceinline__ void mask64(float (&x)[64], int valid) {
   }
 }
 
+// Maximum of three in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 __device__ __forceinline__ float max64(const float (&x)[64]) {
-  float m[8];
+  float m[4];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) m[c] = x[c];
+  for (int c = 0; c < 4; ++c) m[c] = x[c];
 #pragma unroll
-  for (int c = 8; c < 64; ++c) m[c & 7] = fmaxf(m[c & 7], x[c]);
-  return fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])));
+  for (int c = 4; c < 60; c += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], x[c + i], x[c + 4 + i]);
+  return max3(max3(m[0], x[60], x[61]), max3(m[1], x[62], x[63]), fmaxf(m[2], m[3]));
+}
+
+// Two fp32 operations in one instruction (the results are those of two single ones).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 y;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(y.x), "=f"(y.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return y;
 }
 
 // p = exp2(x * mul + add) as 16-bit pairs into TMEM; returns their sum (before rounding).
 template <bool F16>
 __device__ __forceinline__ float exp64(const float (&x)[64], float mul, float add, uint32_t taddr) {
   uint32_t pk[32];
-  float l[4] = {0.f, 0.f, 0.f, 0.f};
+  float2 l[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+  const float2 mul2{mul, mul}, addv{add, add};
 #pragma unroll
   for (int c = 0; c < 32; ++c) {
-    const float p0 = ex2(fmaf(x[2 * c], mul, add)), p1 = ex2(fmaf(x[2 * c + 1], mul, add));
-    l[c & 3] += p0 + p1;
-    pk[c] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+    const float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), mul2, addv);
+    const float2 p{ex2(y.x), ex2(y.y)};
+    l[c & 3] = add2(l[c & 3], p);
+    pk[c] = F16 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
   }
   tmem_st32(taddr, pk);
   tmem_st_wait();
-  return (l[0] + l[1]) + (l[2] + l[3]);
+  const float2 s = add2(add2(l[0], l[1]), add2(l[2], l[3]));
+  return s.x + s.y;
 }
 
 // 32 channels of a row, rounded to the call's type.
@@ -154,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_o = [&](int t) { return smem_u32(&bars[28 + t]); };        // O_t of the piece complete
   auto bar_ofree = [&](int t) { return smem_u32(&bars[30 + t]); };    // ... and read out
   auto bar_l = [&](int t) { return smem_u32(&bars[32 + t]); };        // 1 / l of the piece written
-  const uint32_t bar_drain = smem_u32(&bars[34]);
+  auto bar_drain = [&](int t) { return smem_u32(&bars[34 + t]); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   float* row_s = reinterpret_cast<float*>(smem + L::kOffRow);
@@ -165,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     for (int st = 0; st < kStages; ++st) {
       mbar_init(bar_full(st), KV8 ? 128 : 1);
-      mbar_init(bar_empty(st), 1);
+      mbar_init(bar_empty(st), 2);  // both issuers
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_qfull(t), KV8 ? 128 : 1);
@@ -177,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_o(t), 1);
       mbar_init(bar_ofree(t), 128);
       mbar_init(bar_l(t), 128);
+      mbar_init(bar_drain(t), 1);
     }
-    mbar_init(bar_drain, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -191,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int tp = plan.tp;  // tiles per segment
   auto active = [&](const Piece& x, int t) { return t < tp && x.pair * tp + t < plan.tiles; };
-  if (a.kv_len && blockIdx.x == 0 && warp == 2) {
+  if (a.kv_len && blockIdx.x == 0 && warp == 3) {
     for (int b = lane; b < s.B; b += 32)
       if (a.kv_len[b] < 0 || a.kv_len[b] > s.M) report_error(a.status, kDevErrBounds);
   }
@@ -243,90 +273,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < 2; ++t)
         if (qn[t]) mbar_drain(bar_qfull(t), (qn[t] - 1) & 1, abort_flag);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------------ MMA issuer of tile t
     PieceIter it(s, plan, a.kv_len);
     constexpr uint32_t idO = idesc_f32acc(128, D, false, true, !kMmaF16);
+    const int t = warp - 1;
+    const uint32_t ts = tmem + t * 128, to = tmem + kColO + t * 128;
+    const uint64_t qd = smem_desc(sbase + t * L::kTile, 16, 1024);
     bool ok = true;
-    uint32_t r = 0, c[2] = {0, 0}, pc[2] = {0, 0};  // ring loads; blocks and pieces done per tile
+    uint32_t r = 0, c = 0, pc = 0;  // ring loads; blocks and pieces done
     Piece x;
     while (ok && it.next(x)) {
-      for (int j = 0; ok && j < x.nb; ++j) {
+      const bool mine = active(x, t);
+      for (int j = 0; j < x.nb; ++j) {
         const int valid = min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock);
         const int steps = (valid + 15) >> 4;
         const uint32_t idS = idesc_f32acc(128, steps * 16, false, false, !kMmaF16);
         const int ks = r % kStages, vs = (r + 1) % kStages;
         const uint32_t kph = (r / kStages) & 1, vph = ((r + 1) / kStages) & 1;
         r += 2;
-        const bool last = j + 1 == x.nb;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(ks), kph, wc));
-        const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile, 16, 1024);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || !active(x, t)) continue;
-          ok = __all_sync(0xffffffffu, (j > 0 || mbar_wait(bar_qfull(t), pc[t] & 1, wc)) &&
-                                           (c[t] == 0 || mbar_wait(bar_pv(t), (c[t] - 1) & 1, wc)));
+        if (!mine) {  // the stages are free as far as this tile goes
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_full(ks), kph, wc));
           if (!ok) break;
-          tc_fence_after();
-          const uint64_t qd = smem_desc(sbase + t * L::kTile, 16, 1024);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(tmem + t * 128, qd + kmajor_kstep(kk, 128), kd + kmajor_kstep(kk, 128), idS, kk > 0 ? 1u : 0u);
-            umma_commit(bar_s(t));
-            if (last) umma_commit(bar_qempty(t));
-          }
-          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_empty(ks));
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), vph, wc));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(bar_empty(vs));
+          continue;
         }
+        const bool last = j + 1 == x.nb;
+        // S_t(j) overwrites the columns of P_t(j-1)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(ks), kph, wc) &&
+                                         (j > 0 || mbar_wait(bar_qfull(t), pc & 1, wc)) &&
+                                         (c == 0 || mbar_wait(bar_pv(t), (c - 1) & 1, wc)));
         if (!ok) break;
-        if (elect_one()) umma_commit(bar_empty(ks));
+        tc_fence_after();
+        const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile, 16, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(ts, qd + kmajor_kstep(kk, 128), kd + kmajor_kstep(kk, 128), idS, kk > 0 ? 1u : 0u);
+          umma_commit(bar_s(t));
+          umma_commit(bar_empty(ks));
+          if (last) umma_commit(bar_qempty(t));
+        }
         __syncwarp();
         ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), vph, wc));
         if (!ok) break;
         uint8_t* vt = smem + L::kOffKV + vs * L::kTile;
         if (!KV8 && (valid & 15)) {
-          // rows valid .. 16 * steps - 1 of V: a row is 128 bytes in each panel
-          const int n = (16 * steps - valid) * 8 * L::kPanels;
-          for (int i = lane; i < n; i += 32) {
-            const int row = valid + (i >> 3) % (16 * steps - valid), pn = (i >> 3) / (16 * steps - valid);
+          // rows valid .. 16 * steps - 1 of V (both issuers write the same zeros): a row is 128 bytes
+          // in each panel
+          const int rows = 16 * steps - valid, nz = rows * 8 * L::kPanels;
+          for (int i = lane; i < nz; i += 32) {
+            const int row = valid + (i >> 3) % rows, pn = (i >> 3) / rows;
             *reinterpret_cast<uint4*>(vt + pn * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
           __syncwarp();
         }
         const uint64_t vd = smem_desc(sbase + L::kOffKV + vs * L::kTile, 16384, 1024);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || !active(x, t)) continue;
-          ok = __all_sync(0xffffffffu, (j > 0 || pc[t] == 0 || mbar_wait(bar_ofree(t), (pc[t] - 1) & 1, wc)) &&
-                                           mbar_wait(bar_pb(t), c[t] & 1, wc));
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t o = tmem + kColO + t * 128, p = tmem + t * 128;
-          if (steps > 4 && elect_one()) issue_pv(o, p, vd, idO, 4, steps, j == 0);
-          __syncwarp();
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_pa(t), c[t] & 1, wc));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_pv(o, p, vd, idO, 0, min(4, steps), j == 0 && steps <= 4);
-            umma_commit(bar_pv(t));
-            if (last) umma_commit(bar_o(t));
-          }
-          __syncwarp();
-          ++c[t];
-        }
+        ok = __all_sync(0xffffffffu, (j > 0 || pc == 0 || mbar_wait(bar_ofree(t), (pc - 1) & 1, wc)) &&
+                                         mbar_wait(bar_pb(t), c & 1, wc));
         if (!ok) break;
-        if (elect_one()) umma_commit(bar_empty(vs));
+        tc_fence_after();
+        if (steps > 4 && elect_one()) issue_pv(to, ts, vd, idO, 4, steps, j == 0);
         __syncwarp();
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_pa(t), c & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_pv(to, ts, vd, idO, 0, min(4, steps), j == 0 && steps <= 4);
+          umma_commit(bar_pv(t));
+          umma_commit(bar_empty(vs));
+          if (last) umma_commit(bar_o(t));
+        }
+        __syncwarp();
+        ++c;
       }
-      if (x.nb > 0)
-        for (int t = 0; t < 2; ++t) pc[t] += active(x, t) ? 1 : 0;
+      if (mine && x.nb > 0) ++pc;
     }
     // no MMA may still run when TMEM is released, on the abort path too
-    if (elect_one()) umma_commit(bar_drain);
+    if (elect_one()) umma_commit(bar_drain(t));
     __syncwarp();
-    mbar_drain(bar_drain, 0, abort_flag);
+    mbar_drain(bar_drain(t), 0, abort_flag);
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ softmax rows
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
