@@ -133,13 +133,14 @@ sa2_status sa2_cross_attn_fwd(const sa2_cross_shape* shape, const sa2_tensor* q,
   CrossFwdArgs a;
   st = fwd_args(s, q, kv_len, scale, o, lse, ws, ws_bytes, &plan, &a);
   if (st != SA2_OK) return st;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   const bool f16 = s.dtype == SA2_FP16;
   if (!make_group_map(&mq, a.q, s.B, s.H, s.G, s.N, s.d, s.G, plan.nb, f16) ||
+      !make_group_map(&mo, a.o, s.B, s.H, s.G, s.N, s.d, s.G, plan.nb, f16) ||
       !make_group_map(&mk, kr, s.B, s.Hkv, 1, s.M, s.d, 1, kKeyBlock, f16) ||
       !make_group_map(&mv, vr, s.B, s.Hkv, 1, s.M, s.d, 1, kKeyBlock, f16))
     return SA2_ERR_CUDA;
-  return cuda_status(launch_cross_fwd(s, plan, mq, mk, mv, a, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_cross_fwd(s, plan, mq, mk, mv, mo, a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t sa2_cross_bwd_workspace_size(const sa2_cross_shape* shape) {

@@ -17,11 +17,9 @@
 // columns that hold P_t(j-1), so its issuer waits for the completion of P_t V(j-1).
 //   S_t  = Q_t K_j^T   M = 128, N = 128, K = d   (shared memory, K-major)
 //   O_t += P_t V_j     M = 128, N = d, K = 128   (A = P from TMEM, V MN-major)
-// The softmax thread reads keys 64..127 of its row first and keeps them, takes the maximum over
-// both halves, writes P for 64..127, then reads 0..63 again: P V of the first written half starts
-// while the other is computed, and a thread never holds more than 64 scores.
-// TMEM columns: S_0 0, S_1 128 (P as 16-bit pairs over the first 32 columns of each half of the
-// scores), O_0 256, O_1 384.
+// The softmax thread keeps its row's 128 scores in registers; P V of keys 0..95 starts while it takes
+// the exponentials of 96..127.  At d = 64 the accumulators leave TMEM room for P in columns of its own:
+// S_t(j+1) then follows as soon as S_t(j) has been read, and the chain is the softmax alone.
 //
 // The last block of a sequence may be partial.  Its products run over the valid keys rounded up
 // to 16; scores behind the last key are replaced by -inf (whatever they are: NaN too), and up to
@@ -34,17 +32,34 @@ namespace sa2 {
 namespace {
 
 constexpr int kThreads = 512;
+// Registers: 512 threads are launched with 128 each and share them out anew by role, warpgroup by
+// warpgroup: issuers, epilogue or converters, 2 x softmax.
+template <bool KV8>
+struct Regs {
+  static constexpr int kIssue = KV8 ? 48 : 56, kEpilogue = KV8 ? 112 : 72, kSoftmax = KV8 ? 176 : 192;
+  static_assert(kIssue + kEpilogue + 2 * kSoftmax == 4 * 128, "more would wait for ever");
+};
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;
+constexpr long long kStaggerCycles = 2500;  // a little more than S and one softmax
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O and l are rescaled only past 2^8
-
+// TMEM columns: S of tile t at 128 t.  d = 128: O at 256 + 128 t, and P over the S it was made from
+// (64 columns of 16-bit pairs).  d = 64: O at 256 + 64 t, and P in columns of its own at 384 + 64 t.
 template <int D>
+struct Cols {
+  static constexpr bool kOwnP = D == 64;
+  static __device__ __forceinline__ uint32_t S(int t) { return 128u * t; }
+  static __device__ __forceinline__ uint32_t P(int t) { return kOwnP ? 384u + 64u * t : 128u * t; }
+  static __device__ __forceinline__ uint32_t O(int t) { return 256u + (uint32_t)D * t; }
+};
+
+template <int D, bool KV8>
 struct XSmem {
   static constexpr int kPanels = D / 64;
   static constexpr int kTile = 128 * 128 * kPanels;  // 128 rows x 128 B per panel
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 64 ? 8 : (KV8 ? 5 : 4);
   static constexpr int kOffKV = 2 * kTile;
-  static constexpr int kOffBar = kOffKV + kStages * kTile;
+  static constexpr int kOffO = kOffKV + kStages * kTile;  // 16-bit keys: a tile of O on its way out
+  static constexpr int kOffBar = kOffO + (KV8 ? 0 : kTile);
   // [2][128], for each row 1 / l (16-bit keys) or the scale of its converted query (8-bit keys)
   static constexpr int kOffRow = kOffBar + 512;
   static constexpr int kBytes = kOffRow + 1024 + 1024;
@@ -57,23 +72,29 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void load64(uint32_t taddr, float (&x)[64]) {
-  uint32_t u0[32], u1[32];
-  tmem_ld32(taddr, u0);
-  tmem_ld32(taddr + 32, u1);
-  tmem_ld_wait(u0);
-  tmem_ld_wait(u1);
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    x[c] = __uint_as_float(u0[c]);
-    x[c + 32] = __uint_as_float(u1[c]);
-  }
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void mask64(float (&x)[64], int valid) {
-  if (valid < 64) {
+// A row's 128 scores; those behind the last key (whatever they are) as -inf.
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&x)[128], int valid) {
+  uint32_t u[4][32];
 #pragma unroll
-    for (int c = 0; c < 64; ++c) x[c] = c < valid ? x[c] : -INFINITY;
+  for (int q = 0; q < 4; ++q) tmem_ld32(taddr + 32 * q, u[q]);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    tmem_ld_wait(u[q]);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) x[32 * q + c] = __uint_as_float(u[q][c]);
+  }
+  if (valid < 128) {
+#pragma unroll
+    for (int c = 0; c < 128; ++c) x[c] = c < valid ? x[c] : -INFINITY;
   }
 }
 
@@ -84,15 +105,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-__device__ __forceinline__ float max64(const float (&x)[64]) {
+template <int FROM>
+__device__ __forceinline__ float max64(const float (&x)[128]) {
   float m[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) m[c] = x[c];
+  for (int c = 0; c < 4; ++c) m[c] = x[FROM + c];
 #pragma unroll
   for (int c = 4; c < 60; c += 8)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], x[c + i], x[c + 4 + i]);
-  return max3(max3(m[0], x[60], x[61]), max3(m[1], x[62], x[63]), fmaxf(m[2], m[3]));
+    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], x[FROM + c + i], x[FROM + c + 4 + i]);
+  return max3(max3(m[0], x[FROM + 60], x[FROM + 61]), max3(m[1], x[FROM + 62], x[FROM + 63]), fmaxf(m[2], m[3]));
 }
 
 // Two fp32 operations in one instruction (the results are those of two single ones).
@@ -113,23 +135,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return y;
 }
 
-// p = exp2(x * mul + add) as 16-bit pairs into TMEM; returns their sum (before rounding).
-template <bool F16>
-__device__ __forceinline__ float exp64(const float (&x)[64], float mul, float add, uint32_t taddr) {
-  uint32_t pk[32];
-  float2 l[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+// p = exp2(x * mul + add) of 32 scores as 16-bit pairs, their sum (before rounding) onto l.
+template <bool F16, int FROM>
+__device__ __forceinline__ void exp32(const float (&x)[128], float mul, float add, uint32_t* pk, float2 (&l)[2]) {
   const float2 mul2{mul, mul}, addv{add, add};
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), mul2, addv);
+  for (int c = 0; c < 16; ++c) {
+    const float2 y = fma2(make_float2(x[FROM + 2 * c], x[FROM + 2 * c + 1]), mul2, addv);
     const float2 p{ex2(y.x), ex2(y.y)};
-    l[c & 3] = add2(l[c & 3], p);
+    l[c & 1] = add2(l[c & 1], p);
     pk[c] = F16 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
   }
-  tmem_st32(taddr, pk);
-  tmem_st_wait();
-  const float2 s = add2(add2(l[0], l[1]), add2(l[2], l[3]));
-  return s.x + s.y;
 }
 
 // 32 channels of a row, rounded to the call's type.
@@ -146,12 +162,30 @@ __device__ __forceinline__ void store32(uint16_t* dst, const float (&v)[32], boo
   }
 }
 
-// k-steps [k0, k1) of O (+)= P V: A = P in TMEM (16 keys in 8 columns; keys 64..127 from column 64
-// on), B = V, 16 rows per k-step.
-__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, int k0, int k1,
-                                         bool fresh) {
-  for (int kk = k0; kk < k1; ++kk)
-    umma_ts(o, p + kk * 8 + (kk >= 4 ? 32 : 0), v + (uint64_t)(kk * 128), idesc, (fresh && kk == k0) ? 0u : 1u);
+// 32 lanes x 16 columns of TMEM.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15}, [%16];"
+      : SA2_R8(0), SA2_R8(8)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : SA2_P8(0), SA2_P8(8)::"memory");
+}
+
+// N k-steps from K0 on, as far as they are below `steps`, of O (+)= P V: A = P in TMEM (16 keys in 8
+// columns), B = V, 16 rows per k-step.
+template <int K0, int N>
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, int steps, bool fresh) {
+  if (steps >= K0 + N) {
+    umma_ts(o, p + K0 * 8, v + (uint64_t)(K0 * 128), idesc, fresh ? 0u : 1u);
+#pragma unroll
+    for (int kk = 1; kk < N; ++kk) umma_ts(o, p + (K0 + kk) * 8, v + (uint64_t)((K0 + kk) * 128), idesc, 1u);
+  } else {
+    for (int kk = K0; kk < steps; ++kk)
+      umma_ts(o, p + kk * 8, v + (uint64_t)(kk * 128), idesc, (fresh && kk == 0) ? 0u : 1u);
+  }
 }
 
 __device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w) {
@@ -164,11 +198,15 @@ __device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w) {
 template <int D, bool KV8, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, CrossShape s, FwdPlan plan, CacheRef cache,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, CrossShape s,
+                     FwdPlan plan, CacheRef cache,
                      CrossFwdArgs a) {
-  using L = XSmem<D>;
+  using L = XSmem<D, KV8>;
+  using C = Cols<D>;
   constexpr int kStages = L::kStages;
   constexpr bool kMmaF16 = KV8 || F16;  // the cache's products run in fp16
+  // how far (log2) a block's maximum may lead the reference before P leaves its type's range
+  constexpr float kMaxLead = kMmaF16 ? 14.f : 100.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -178,13 +216,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_qfull = [&](int t) { return smem_u32(&bars[16 + t]); };    // Q of tile t in shared memory
   auto bar_qempty = [&](int t) { return smem_u32(&bars[18 + t]); };   // ... and read (by its last S; cache: and its row scales)
   auto bar_s = [&](int t) { return smem_u32(&bars[20 + t]); };        // S_t in TMEM
-  auto bar_pb = [&](int t) { return smem_u32(&bars[22 + t]); };       // P of keys 64..127 written
-  auto bar_pa = [&](int t) { return smem_u32(&bars[24 + t]); };       // P of keys 0..63 written
+  auto bar_pb = [&](int t) { return smem_u32(&bars[22 + t]); };       // P of keys 96..127 written
+  auto bar_pa = [&](int t) { return smem_u32(&bars[24 + t]); };       // P of keys 0..95 written
   auto bar_pv = [&](int t) { return smem_u32(&bars[26 + t]); };       // P_t V completed
   auto bar_o = [&](int t) { return smem_u32(&bars[28 + t]); };        // O_t of the piece complete
   auto bar_ofree = [&](int t) { return smem_u32(&bars[30 + t]); };    // ... and read out
   auto bar_l = [&](int t) { return smem_u32(&bars[32 + t]); };        // 1 / l of the piece written
   auto bar_drain = [&](int t) { return smem_u32(&bars[34 + t]); };
+  const uint32_t bar_st = smem_u32(&bars[38]), bar_stfree = smem_u32(&bars[39]);  // O tile staged / copied out
+  auto bar_sfree = [&](int t) { return smem_u32(&bars[36 + t]); };    // S_t read out (d = 64)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   float* row_s = reinterpret_cast<float*>(smem + L::kOffRow);
@@ -208,7 +248,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_ofree(t), 128);
       mbar_init(bar_l(t), 128);
       mbar_init(bar_drain(t), 1);
+      mbar_init(bar_sfree(t), 128);
     }
+    mbar_init(bar_st, 128);
+    mbar_init(bar_stfree, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -228,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 && !KV8) {
     // ------------------------------------------------------------------ TMA producer
+    give_registers<Regs<KV8>::kIssue>();
     PieceIter it(s, plan, a.kv_len);  // (whole warps)
     if (lane == 0) {
       tma_prefetch_map(&mq);
@@ -275,39 +319,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------------ MMA issuer of tile t
+    give_registers<Regs<KV8>::kIssue>();
     PieceIter it(s, plan, a.kv_len);
     constexpr uint32_t idO = idesc_f32acc(128, D, false, true, !kMmaF16);
     const int t = warp - 1;
-    const uint32_t ts = tmem + t * 128, to = tmem + kColO + t * 128;
+    const uint32_t ts = tmem + C::S(t), tpp = tmem + C::P(t), to = tmem + C::O(t);
     const uint64_t qd = smem_desc(sbase + t * L::kTile, 16, 1024);
     bool ok = true;
-    uint32_t r = 0, c = 0, pc = 0;  // ring loads; blocks and pieces done
+    uint32_t r = 0, c = 0, pc = 0;  // ring loads of earlier pieces; blocks and pieces done
     Piece x;
     while (ok && it.next(x)) {
-      const bool mine = active(x, t);
-      for (int j = 0; j < x.nb; ++j) {
-        const int valid = min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock);
-        const int steps = (valid + 15) >> 4;
-        const uint32_t idS = idesc_f32acc(128, steps * 16, false, false, !kMmaF16);
-        const int ks = r % kStages, vs = (r + 1) % kStages;
-        const uint32_t kph = (r / kStages) & 1, vph = ((r + 1) / kStages) & 1;
-        r += 2;
-        if (!mine) {  // the stages are free as far as this tile goes
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_full(ks), kph, wc));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(bar_empty(ks));
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), vph, wc));
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(bar_empty(vs));
-          continue;
+      if (!active(x, t)) {  // the stages are free as far as this tile goes
+        for (int i = 0; ok && i < 2 * x.nb; ++i, ++r) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_full(r % kStages), (r / kStages) & 1, wc));
+          if (ok && lane == 0) mbar_arrive(bar_empty(r % kStages));
         }
-        const bool last = j + 1 == x.nb;
-        // S_t(j) overwrites the columns of P_t(j-1)
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(ks), kph, wc) &&
-                                         (j > 0 || mbar_wait(bar_qfull(t), pc & 1, wc)) &&
-                                         (c == 0 || mbar_wait(bar_pv(t), (c - 1) & 1, wc)));
-        if (!ok) break;
+        continue;
+      }
+      auto steps_of = [&](int j) { return (min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock) + 15) >> 4; };
+      // S_t(j).  It overwrites the columns of P_t(j-1) (d = 128) or those of S_t(j-1) (d = 64).
+      auto issue_s = [&](int j) {
+        const uint32_t rk = r + 2 * j, cj = c + j;
+        const int ks = rk % kStages;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(bar_full(ks), (rk / kStages) & 1, wc) &&
+                            (j > 0 || mbar_wait(bar_qfull(t), pc & 1, wc)) &&
+                            (cj == 0 || mbar_wait(C::kOwnP ? bar_sfree(t) : bar_pv(t), (cj - 1) & 1, wc))))
+          return false;
         tc_fence_after();
+        const uint32_t idS = idesc_f32acc(128, steps_of(j) * 16, false, false, !kMmaF16);
         const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile, 16, 1024);
         if (elect_one()) {
 #pragma unroll
@@ -315,18 +355,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_ss(ts, qd + kmajor_kstep(kk, 128), kd + kmajor_kstep(kk, 128), idS, kk > 0 ? 1u : 0u);
           umma_commit(bar_s(t));
           umma_commit(bar_empty(ks));
-          if (last) umma_commit(bar_qempty(t));
+          if (j + 1 == x.nb) umma_commit(bar_qempty(t));
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), vph, wc));
+        return true;
+      };
+      // d = 128: keep the tiles half a period apart, so that one's products run beside the other's
+      // softmax.  Left alone they settle anywhere, also in step, where the tensor cores wait for
+      // both (5000 cycles per block against 3300).  So tile 1 begins a piece when tile 0 has its
+      // first P, or after kStaggerCycles: it is a hint, and nothing depends on it.
+      if (!C::kOwnP && t == 1 && x.nb > 0) {
+        const long long z = clock64();
+        while (clock64() - z < kStaggerCycles && !mbar_test(bar_pa(0), c & 1)) {
+        }
+      }
+      if (x.nb > 0) ok = issue_s(0);
+      for (int j = 0; ok && j < x.nb; ++j) {
+        if (C::kOwnP && j + 1 < x.nb) {
+          ok = issue_s(j + 1);
+          if (!ok) break;
+        }
+        const uint32_t rv = r + 2 * j + 1, cj = c + j;
+        const int vs = rv % kStages, steps = steps_of(j);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), (rv / kStages) & 1, wc));
         if (!ok) break;
         uint8_t* vt = smem + L::kOffKV + vs * L::kTile;
-        if (!KV8 && (valid & 15)) {
-          // rows valid .. 16 * steps - 1 of V (both issuers write the same zeros): a row is 128 bytes
-          // in each panel
-          const int rows = 16 * steps - valid, nz = rows * 8 * L::kPanels;
+        const int rows = 16 * steps - (x.keys - (x.k0 + j) * kKeyBlock);
+        if (!KV8 && rows > 0) {
+          // the last `rows` rows of V (both issuers write the same zeros): a row is 128 bytes in each
+          // panel
+          const int nz = rows * 8 * L::kPanels;
           for (int i = lane; i < nz; i += 32) {
-            const int row = valid + (i >> 3) % rows, pn = (i >> 3) / rows;
+            const int row = 16 * steps - rows + (i >> 3) % rows, pn = (i >> 3) / rows;
             *reinterpret_cast<uint4*>(vt + pn * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
@@ -334,24 +394,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint64_t vd = smem_desc(sbase + L::kOffKV + vs * L::kTile, 16384, 1024);
         ok = __all_sync(0xffffffffu, (j > 0 || pc == 0 || mbar_wait(bar_ofree(t), (pc - 1) & 1, wc)) &&
-                                         mbar_wait(bar_pb(t), c & 1, wc));
+                                         mbar_wait(bar_pa(t), cj & 1, wc));
         if (!ok) break;
         tc_fence_after();
-        if (steps > 4 && elect_one()) issue_pv(to, ts, vd, idO, 4, steps, j == 0);
+        if (elect_one()) issue_pv<0, 6>(to, tpp, vd, idO, steps, j == 0);
         __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_pa(t), c & 1, wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_pb(t), cj & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_pv(to, ts, vd, idO, 0, min(4, steps), j == 0 && steps <= 4);
+          issue_pv<6, 2>(to, tpp, vd, idO, steps, false);
           umma_commit(bar_pv(t));
           umma_commit(bar_empty(vs));
-          if (last) umma_commit(bar_o(t));
+          if (j + 1 == x.nb) umma_commit(bar_o(t));
         }
         __syncwarp();
-        ++c;
+        if (!C::kOwnP && j + 1 < x.nb) ok = issue_s(j + 1);
       }
-      if (mine && x.nb > 0) ++pc;
+      if (x.nb > 0) ++pc;
+      r += 2 * x.nb;
+      c += x.nb;
     }
     // no MMA may still run when TMEM is released, on the abort path too
     if (elect_one()) umma_commit(bar_drain(t));
@@ -359,12 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_drain(bar_drain(t), 0, abort_flag);
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ softmax rows
+    take_registers<Regs<KV8>::kSoftmax>();
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
     PieceIter it(s, plan, a.kv_len);
     const int t = (warp - 8) >> 2;
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t ts = trow + t * 128, to = trow + kColO + t * 128;
+    const uint32_t ts = trow + C::S(t), tpp = trow + C::P(t), to = trow + C::O(t);
     const int tok_r = r / s.G, g = r - tok_r * s.G;
     bool ok = true;
     uint32_t c = 0, pc = 0;
@@ -409,7 +472,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         qscale *= row_s[t * 128 + r];
         mbar_arrive(bar_qempty(t));
       }
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = 0.f, m_run = 0.f, l = 0.f;  // reference of the exponentials, largest so far, sum
+      auto rescale = [&](float m_new) {
+        const float alpha = ex2(m_used - m_new);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t o[16];
+          tmem_ld16(to + c0, o);
+          tmem_ld_wait16(o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(to + c0, o);
+        }
+        tmem_st_wait();
+        l *= alpha;
+        m_used = m_new;
+      };
       for (int j = 0; j < x.nb; ++j, ++c) {
         const int valid = min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock);
         float mul_a = qscale, mul_b = qscale, ev_a = 0.f, ev_b = 0.f;
@@ -425,50 +503,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        float y[64];
-        load64(ts, y);
-        mask64(y, valid);
-        float mx = fmaf(max64(y), mul_a, ev_a);
-        if (valid > 64) {
-          load64(ts + 64, y);
-          mask64(y, valid - 64);
-          mx = fmaxf(mx, fmaf(max64(y), mul_b, ev_b));
-        }
-        if (j == 0) {
-          m_used = mx;
-        } else {
-          const bool need = mx > m_used + kRescaleThreshold;
-          if (__any_sync(0xffffffffu, need)) {
-            // S_t(j) was issued after P_t V(j-1) completed: O holds blocks 0 .. j-1
-            const float alpha = need ? ex2(m_used - mx) : 1.f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              tmem_ld32(to + c0, o);
-              tmem_ld_wait(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(to + c0, o);
-            }
-            tmem_st_wait();
-            if (need) {
-              l *= alpha;
-              m_used = mx;
-            }
+        float y[128];
+        load_scores(ts, y, valid);
+        const float mx = fmaxf(fmaf(max64<0>(y), mul_a, ev_a), fmaf(max64<64>(y), mul_b, ev_b));
+        // S_t(j) was issued after P_t V(j-1) completed (d = 64: that is waited for here), so O holds
+        // blocks 0 .. j-1 and P's columns are free
+        if (C::kOwnP && c > 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_pv(t), (c - 1) & 1, wc))) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
         }
-        if (valid > 64) {
-          const float sum = exp64<kMmaF16>(y, mul_b, ev_b - m_used, ts + 64);
-          l += KV8 ? sum * ex2(-ev_b) : sum;
+        // The exponentials are taken against a maximum of the blocks before this one, so that they need
+        // not wait for this one's: the first block uses its own, then O and l follow when the maximum
+        // has grown past 2^8.  Only where P would leave its type's range does a block's own maximum
+        // come first (the loop below runs twice).
+        if (j == 0)
+          m_used = mx;
+        else if (__any_sync(0xffffffffu, m_run > m_used + kRescaleThreshold))
+          rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
+        m_run = j == 0 ? mx : fmaxf(m_run, mx);
+        uint32_t pk[32], pk2[16];
+        float2 la[2], lb[2];
+        for (;;) {
+          la[0] = la[1] = lb[0] = lb[1] = make_float2(0.f, 0.f);
+          exp32<kMmaF16, 0>(y, mul_a, ev_a - m_used, pk, la);
+          exp32<kMmaF16, 32>(y, mul_a, ev_a - m_used, pk + 16, la);
+          exp32<kMmaF16, 64>(y, mul_b, ev_b - m_used, pk2, lb);
+          if (!__any_sync(0xffffffffu, mx > m_used + kMaxLead)) break;
+          rescale(fmaxf(mx, m_used));
+          load_scores(ts, y, valid);  // (again, so that the usual path need not keep them)
         }
-        tc_fence_before();
-        mbar_arrive(bar_pb(t));
-        load64(ts, y);
-        mask64(y, valid);
-        const float sum = exp64<kMmaF16>(y, mul_a, ev_a - m_used, ts);
-        l += KV8 ? sum * ex2(-ev_a) : sum;
+        if constexpr (C::kOwnP) {
+          tc_fence_before();
+          mbar_arrive(bar_sfree(t));
+        }
+        tmem_st32(tpp, pk);
+        tmem_st16(tpp + 32, pk2);
+        tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar_pa(t));
+        exp32<kMmaF16, 96>(y, mul_b, ev_b - m_used, pk2, lb);
+        tmem_st16(tpp + 48, pk2);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_pb(t));
+        const float2 sa = add2(la[0], la[1]), sb = add2(lb[0], lb[1]);
+        l += KV8 ? (sa.x + sa.y) * ex2(-ev_a) + (sb.x + sb.y) * ex2(-ev_b) : (sa.x + sa.y) + (sb.x + sb.y);
       }
       if (!ok) break;
       const int64_t slot_row = ((int64_t)blockIdx.x + x.seg) * 256 + t * 128 + r;
@@ -519,12 +601,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4 && !KV8) {
     // ------------------------------------------------------------------ epilogue: O / l
+    // A tile goes out through shared memory with one TMA store: stored row by row, 16 bytes per
+    // thread, it kept the load/store unit busy for 3000 cycles, which the softmax threads' tcgen05.ld
+    // waited for (M = 512: a fifth of the time).
+    give_registers<Regs<KV8>::kEpilogue>();
     PieceIter it(s, plan, a.kv_len);
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const int tok_r = r / s.G, g = r - tok_r * s.G;
     bool ok = true;
-    uint32_t pc[2] = {0, 0};
+    uint32_t pc[2] = {0, 0}, staged = 0;
     Piece x;
     while (ok && it.next(x)) {
 #pragma unroll
@@ -533,47 +619,78 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = (x.pair * tp + t) * plan.nb + tok_r;
         const bool row_valid = tok_r < plan.nb && n < s.N;
         const int h = x.hk * s.G + g;
-        uint16_t* op = static_cast<uint16_t*>(a.o.p) + x.b * a.o.sb + h * a.o.sh + n * a.o.sn;
         if (x.nb == 0) {
+          uint16_t* op = static_cast<uint16_t*>(a.o.p) + x.b * a.o.sb + h * a.o.sh + n * a.o.sn;
           if (row_valid)
             for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(op)[i] = make_uint4(0, 0, 0, 0);
           continue;
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_l(t), pc[t] & 1, wc) && mbar_wait(bar_o(t), pc[t] & 1, wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_l(t), pc[t] & 1, wc) && mbar_wait(bar_o(t), pc[t] & 1, wc) &&
+                                         (plan.split || staged == 0 || mbar_wait(bar_stfree, (staged - 1) & 1, wc)));
         if (!ok) break;
         ++pc[t];
         tc_fence_after();
         const float inv_l = row_s[t * 128 + r];
         const int64_t slot_row = ((int64_t)blockIdx.x + x.seg) * 256 + t * 128 + r;
+        uint8_t* st_row = smem + L::kOffO + r * 128;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t u[32];
-          tmem_ld32(trow + kColO + t * 128 + c0, u);
+          tmem_ld32(trow + C::O(t) + c0, u);
           tmem_ld_wait(u);
           if (c0 + 32 >= D) {
             tc_fence_before();
             mbar_arrive(bar_ofree(t));
           }
-          float v[32];
+          if (plan.split) {
+            if (row_valid) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]) * inv_l;
-          if (row_valid && plan.split) {
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(a.part_o + slot_row * D + c0)[i] =
+                    make_float4(__uint_as_float(u[4 * i]) * inv_l, __uint_as_float(u[4 * i + 1]) * inv_l,
+                                __uint_as_float(u[4 * i + 2]) * inv_l, __uint_as_float(u[4 * i + 3]) * inv_l);
+            }
+          } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(a.part_o + slot_row * D + c0)[i] =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else if (row_valid) {
-            store32(op + c0, v, F16);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float v0 = __uint_as_float(u[8 * i + 2 * q]) * inv_l, v1 = __uint_as_float(u[8 * i + 2 * q + 1]) * inv_l;
+                w[q] = F16 ? pack_f16x2(v0, v1) : pack_bf16x2(v0, v1);
+              }
+              // 16-byte chunk k of the row's 128 bytes in panel c0 / 64, swizzled
+              const int k = (c0 & 32) / 8 + i;
+              *reinterpret_cast<uint4*>(st_row + (c0 >> 6) * 16384 + ((k ^ (r & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
+        }
+        if (!plan.split) {
+          fence_proxy_async();
+          mbar_arrive(bar_st);
+          if (warp == 4) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_st, staged & 1, wc));
+            if (!ok) break;
+            if (lane == 0) {
+              for (int pn = 0; pn < L::kPanels; ++pn)  // tokens past the end are not written
+                tma_store_5d(&mo, sbase + L::kOffO + pn * 16384, pn * 64, 0, (x.pair * tp + t) * plan.nb, x.hk, x.b);
+              bulk_commit();
+              bulk_wait_read();
+              mbar_arrive(bar_stfree);
+            }
+            __syncwarp();
+          }
+          ++staged;
         }
       }
     }
   } else if (warp >= 4 && KV8) {
     // --------------------------------------------------- converters: Q, K, V to fp16
+    give_registers<Regs<KV8>::kEpilogue>();
     PieceIter it(s, plan, a.kv_len);
-    constexpr int kChunks = D / 16;         // 16-byte chunks of an 8-bit row
-    constexpr int kRows = 128 / kChunks;    // rows per pass of the 128 threads
-    constexpr int kPasses = 128 / kRows;    // = kChunks
+    constexpr int kChunks = D / 16;       // 16-byte chunks of an 8-bit row
+    constexpr int kRows = 128 / kChunks;  // rows per pass of the 128 threads
     const int ct = tid - 128;
     const int ch = ct % kChunks, r0 = ct / kChunks;
     bool ok = true;
@@ -582,25 +699,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && it.next(x)) {
       if (x.nb == 0) continue;
       const int64_t head = (int64_t)x.b * cache.sb + (int64_t)x.hk * cache.sh + ch * 16;
-      auto fetch = [&](const uint8_t* base, int kb, uint4 (&u)[kPasses]) {
+      // a tile into registers; behind the last key zeros
+      auto fetch = [&](const uint8_t* base, int kb, uint4 (&u)[kChunks]) {
+        const int t0 = kb * kKeyBlock + r0;
+        const uint8_t* p = base + head + (int64_t)t0 * cache.sn;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int t = kb * kKeyBlock + r0 + i * kRows;
-          u[i] = make_uint4(0, 0, 0, 0);  // behind the last key: zeros
-          if (t < x.keys) u[i] = __ldg(reinterpret_cast<const uint4*>(base + head + (int64_t)t * cache.sn));
+        for (int q = 0; q < kChunks; ++q) {
+          u[q] = make_uint4(0, 0, 0, 0);
+          if (t0 + q * kRows < x.keys) u[q] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)(q * kRows) * cache.sn));
         }
       };
-      // into the next ring stage, swizzled; a row's 16 values are 32 bytes of panel ch / 4
-      auto put = [&](const uint4 (&u)[kPasses]) {
+      // ... and into the next ring stage, swizzled; a row's 16 values are 32 bytes of panel ch / 4
+      auto put = [&](const uint4 (&u)[kChunks]) {
         const int st = r % kStages;
         if (r >= (uint32_t)kStages && !__all_sync(0xffffffffu, mbar_wait(bar_empty(st), ((r / kStages) - 1) & 1, wc)))
           return false;
         uint8_t* dst = smem + L::kOffKV + st * L::kTile + (ch >> 2) * 16384;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int row = r0 + i * kRows;
-          const uint2 w0 = e4m3x4_to_f16x4(u[i].x), w1 = e4m3x4_to_f16x4(u[i].y), w2 = e4m3x4_to_f16x4(u[i].z),
-                      w3 = e4m3x4_to_f16x4(u[i].w);
+        for (int q = 0; q < kChunks; ++q) {
+          const int row = r0 + q * kRows;
+          const uint2 w0 = e4m3x4_to_f16x4(u[q].x), w1 = e4m3x4_to_f16x4(u[q].y), w2 = e4m3x4_to_f16x4(u[q].z),
+                      w3 = e4m3x4_to_f16x4(u[q].w);
           const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
           // the two panels' lanes store opposite halves first, so that a quarter warp's 16-byte
           // stores fall into different banks
@@ -613,8 +732,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++r;
         return true;
       };
-      uint4 uk[kPasses], uv[kPasses];
-      fetch(cache.k, x.k0, uk);
       // Q: thread = row, scaled by a power of two so that its largest magnitude is in [2^14, 2^15)
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
@@ -629,39 +746,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_valid = tok_r < plan.nb && n < s.N;
         const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q.p) + x.b * a.q.sb +
                                                          (int64_t)(x.hk * s.G + g) * a.q.sh + (int64_t)n * a.q.sn);
-        uint4 u[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) u[i] = row_valid ? __ldg(qp + i) : make_uint4(0, 0, 0, 0);
         int e = 0;
         if constexpr (!F16) {
           // the largest magnitude: bf16 magnitudes compare as integers
           uint32_t mx = 0;
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < D / 8; ++i) {
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) mx = max(mx, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
+            const uint4 u = row_valid ? __ldg(qp + i) : make_uint4(0, 0, 0, 0);
+            mx = max(max(mx, max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu)), max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu));
+            mx = max(max(mx, max(u.z & 0x7FFFu, (u.z >> 16) & 0x7FFFu)), max(u.w & 0x7FFFu, (u.w >> 16) & 0x7FFFu));
           }
           // a row of zeros, or with an infinity or NaN, keeps its scale
           if (mx >= 0x0080u && mx < 0x7F80u) e = min(max((int)(mx >> 7) - 127 - 14, -112), 112);
-          const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] = pack_f16x2(__uint_as_float(w[q] << 16) * f, __uint_as_float(w[q] & 0xFFFF0000u) * f);
-            u[i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
         }
         row_s[t * 128 + ct] = __uint_as_float((uint32_t)(127 + e) << 23);
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
         uint8_t* dst = smem + t * L::kTile + ct * 128;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (ct & 7)) << 4)) = u[i];
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 u = row_valid ? __ldg(qp + i) : make_uint4(0, 0, 0, 0);
+          if constexpr (!F16) {
+            u.x = pack_f16x2(__uint_as_float(u.x << 16) * f, __uint_as_float(u.x & 0xFFFF0000u) * f);
+            u.y = pack_f16x2(__uint_as_float(u.y << 16) * f, __uint_as_float(u.y & 0xFFFF0000u) * f);
+            u.z = pack_f16x2(__uint_as_float(u.z << 16) * f, __uint_as_float(u.z & 0xFFFF0000u) * f);
+            u.w = pack_f16x2(__uint_as_float(u.w << 16) * f, __uint_as_float(u.w & 0xFFFF0000u) * f);
+          }
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (ct & 7)) << 4)) = u;
+        }
         fence_proxy_async();
         mbar_arrive(bar_qfull(t));
       }
+      if (!ok) break;
+      // K_0, V_0, K_1, ...: the next tile's loads are in flight while one is converted
+      uint4 uk[kChunks], uv[kChunks];
+      fetch(cache.k, x.k0, uk);
       for (int j = 0; ok && j < x.nb; ++j) {
         fetch(cache.v, x.k0 + j, uv);
         ok = put(uk);
@@ -670,6 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = put(uv);
       }
     }
+  } else {
+    give_registers<Regs<KV8>::kIssue>();  // the rest of the issuers' warpgroup
   }
   tc_fence_before();
   __syncthreads();
@@ -742,12 +862,18 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
 
 template <int D, bool KV8, bool F16>
 cudaError_t launch_t(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
-                     const CUtensorMap& mv, const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st) {
+                     const CUtensorMap& mv, const CUtensorMap& mo, const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st) {
   auto kern = cross_fwd_kernel<D, KV8, F16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XSmem<D>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XSmem<D, KV8>::kBytes);
   if (e != cudaSuccess) return e;
+  // the roles' registers add up to 128 a thread: with fewer at launch they would wait for ever
+  static const int regs = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs != 128) return cudaErrorInvalidConfiguration;
   prof_start(st, kAttnFwd);
-  kern<<<(unsigned)p.grid, kThreads, XSmem<D>::kBytes, st>>>(mq, mk, mv, s, p, c, a);
+  kern<<<(unsigned)p.grid, kThreads, XSmem<D, KV8>::kBytes, st>>>(mq, mk, mv, mo, s, p, c, a);
   if (p.split) cross_join_kernel<D, F16><<<dim3((unsigned)p.segs, 8), 256, 0, st>>>(s, p, a);
   prof_stop(st, kAttnFwd);
   return cudaGetLastError();
@@ -755,13 +881,14 @@ cudaError_t launch_t(const CrossShape& s, const FwdPlan& p, const CUtensorMap& m
 
 template <bool KV8>
 cudaError_t launch_any(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
-                       const CUtensorMap& mv, const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st) {
+                       const CUtensorMap& mv, const CUtensorMap& mo, const CacheRef& c, const CrossFwdArgs& a,
+                       cudaStream_t st) {
   const bool f16 = s.dtype == SA2_FP16;
   if (s.d == 128)
-    return f16 ? launch_t<128, KV8, true>(s, p, mq, mk, mv, c, a, st)
-               : launch_t<128, KV8, false>(s, p, mq, mk, mv, c, a, st);
-  return f16 ? launch_t<64, KV8, true>(s, p, mq, mk, mv, c, a, st)
-             : launch_t<64, KV8, false>(s, p, mq, mk, mv, c, a, st);
+    return f16 ? launch_t<128, KV8, true>(s, p, mq, mk, mv, mo, c, a, st)
+               : launch_t<128, KV8, false>(s, p, mq, mk, mv, mo, c, a, st);
+  return f16 ? launch_t<64, KV8, true>(s, p, mq, mk, mv, mo, c, a, st)
+             : launch_t<64, KV8, false>(s, p, mq, mk, mv, mo, c, a, st);
 }
 
 }  // namespace
@@ -792,14 +919,14 @@ size_t cross_fwd_partials(const CrossShape& s, const FwdPlan& p) {
 }
 
 cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
-                             const CUtensorMap& mv, const CrossFwdArgs& a, cudaStream_t st) {
-  return launch_any<false>(s, p, mq, mk, mv, CacheRef{}, a, st);
+                             const CUtensorMap& mv, const CUtensorMap& mo, const CrossFwdArgs& a, cudaStream_t st) {
+  return launch_any<false>(s, p, mq, mk, mv, mo, CacheRef{}, a, st);
 }
 
 cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CacheRef& c, const CrossFwdArgs& a,
                              cudaStream_t st) {
   const CUtensorMap none{};
-  return launch_any<true>(s, p, none, none, none, c, a, st);
+  return launch_any<true>(s, p, none, none, none, none, c, a, st);
 }
 
 }  // namespace sa2

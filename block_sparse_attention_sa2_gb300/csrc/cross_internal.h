@@ -100,7 +100,7 @@ bool make_group_map(CUtensorMap* map, const TokenRef& t, int B, int heads, int G
                     int box_n, bool f16);
 
 cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
-                             const CUtensorMap& mv, const CrossFwdArgs& a, cudaStream_t st);
+                             const CUtensorMap& mv, const CUtensorMap& mo, const CrossFwdArgs& a, cudaStream_t st);
 cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CacheRef& c, const CrossFwdArgs& a,
                              cudaStream_t st);
 cudaError_t launch_cache_append(const CacheRef& c, int B, int Hkv, int d, int n, bool f16, const TokenRef& k,
