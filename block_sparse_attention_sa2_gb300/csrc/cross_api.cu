@@ -101,7 +101,7 @@ sa2_status fwd_args(const CrossShape& s, const sa2_tensor* q, const int32_t* kv_
   a->kv_len = kv_len;
   a->lse = lse;
   a->part_o = static_cast<float*>(ws);
-  a->part_l = floats ? a->part_o + (size_t)(plan->grid + plan->segs) * 256 * s.d : nullptr;
+  a->part_l = floats ? a->part_o + (size_t)(plan->grid + plan->segs) * plan->rows * s.d : nullptr;
   const float sc = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)s.d));
   a->scale_log2 = sc * 1.4426950408889634f;
   a->status = status_word();
@@ -133,6 +133,8 @@ sa2_status sa2_cross_attn_fwd(const sa2_cross_shape* shape, const sa2_tensor* q,
   CrossFwdArgs a;
   st = fwd_args(s, q, kv_len, scale, o, lse, ws, ws_bytes, &plan, &a);
   if (st != SA2_OK) return st;
+  if (plan.few)
+    return cuda_status(launch_few_rows(s, plan, kr, vr, CacheRef{}, false, a, static_cast<cudaStream_t>(stream)));
   CUtensorMap mq, mk, mv, mo;
   const bool f16 = s.dtype == SA2_FP16;
   if (!make_group_map(&mq, a.q, s.B, s.H, s.G, s.N, s.d, s.G, plan.nb, f16) ||
@@ -239,6 +241,8 @@ sa2_status sa2_cache8_attn(const sa2_cross_shape* shape, const sa2_tensor* q, co
   CrossFwdArgs a;
   st = fwd_args(s, q, kv_len, scale, o, lse, ws, ws_bytes, &plan, &a);
   if (st != SA2_OK) return st;
+  if (plan.few)
+    return cuda_status(launch_few_rows(s, plan, TokenRef{}, TokenRef{}, c, true, a, static_cast<cudaStream_t>(stream)));
   return cuda_status(launch_cache_fwd(s, plan, c, a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -24,6 +24,7 @@
 // The last block of a sequence may be partial.  Its products run over the valid keys rounded up
 // to 16; scores behind the last key are replaced by -inf (whatever they are: NaN too), and up to
 // 15 rows of V behind it are zeroed in shared memory, since 0 * NaN is NaN.
+#include <algorithm>
 #include <cuda_fp8.h>
 
 #include "cross_sched.cuh"
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of split segments: O = sum_i 2^(l_i - m) O_i / sum_i 2^(l_i - m) over a segment's
 // parts in key order, l_i their log2 sums and m the largest; LSE = ln 2 (m + log2 sum).  Rows of
-// sequences without keys get 0 and -inf.  One warp per row; grid (segments, 8), 32 rows each.
+// sequences without keys get 0 and -inf.  One warp per row; grid (segments, rows / 16), 16 rows each.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan plan, CrossFwdArgs a) {
   constexpr int kPer = D / 32;
@@ -810,15 +811,15 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
   const int seg = blockIdx.x;
   const int per_b = s.Hkv * plan.pairs;
   const int b = seg / per_b, hk = (seg - b * per_b) / plan.pairs, pair = seg - b * per_b - hk * plan.pairs;
-  const int64_t run = run_length(total_key_blocks(s, a.kv_len, plan.pairs), plan.grid);
+  const int64_t run = run_length(total_key_blocks(s, a.kv_len, plan.pairs, plan.shift), plan.grid);
   int64_t base = 0;
-  for (int i = lane; i < b; i += 32) base += key_blocks(key_count(a.kv_len, i, s.M));
+  for (int i = lane; i < b; i += 32) base += key_blocks(key_count(a.kv_len, i, s.M), plan.shift);
   for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
-  const int nk = key_blocks(key_count(a.kv_len, b, s.M));
+  const int nk = key_blocks(key_count(a.kv_len, b, s.M), plan.shift);
   const int64_t g0 = base * per_b + (int64_t)(seg - b * per_b) * nk;
   const int c0 = (int)(g0 / run), c1 = nk > 0 ? (int)((g0 + nk - 1) / run) : c0 - 1;
-  for (int i = warp; i < 32; i += 8) {
-    const int rr = blockIdx.y * 32 + i, t = rr >> 7, r = rr & 127;
+  for (int i = warp; i < 16; i += 8) {
+    const int rr = blockIdx.y * 16 + i, t = rr >> 7, r = rr & 127;
     const int tile = pair * plan.tp + t;
     if (t >= plan.tp || tile >= plan.tiles) return;
     const int tok_r = r / s.G, g = r - tok_r * s.G, n = tile * plan.nb + tok_r, h = hk * s.G + g;
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
     float m = -INFINITY;
     bool nan = false;
     for (int cta = c0 + lane; cta <= c1; cta += 32) {
-      const float v = a.part_l[((int64_t)cta + seg) * 256 + rr];
+      const float v = a.part_l[((int64_t)cta + seg) * plan.rows + rr];
       nan |= v != v;
       m = fmaxf(m, v);
     }
@@ -834,7 +835,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
     if (__any_sync(0xffffffffu, nan)) m = NAN;
     float acc[kPer] = {}, l = 0.f;
     for (int cta = c0; cta <= c1; ++cta) {
-      const int64_t row = ((int64_t)cta + seg) * 256 + rr;
+      const int64_t row = ((int64_t)cta + seg) * plan.rows + rr;
       const float w = ex2(a.part_l[row] - m);
       l += w;
       float v[kPer];
@@ -874,9 +875,9 @@ cudaError_t launch_t(const CrossShape& s, const FwdPlan& p, const CUtensorMap& m
   if (regs != 128) return cudaErrorInvalidConfiguration;
   prof_start(st, kAttnFwd);
   kern<<<(unsigned)p.grid, kThreads, XSmem<D, KV8>::kBytes, st>>>(mq, mk, mv, mo, s, p, c, a);
-  if (p.split) cross_join_kernel<D, F16><<<dim3((unsigned)p.segs, 8), 256, 0, st>>>(s, p, a);
   prof_stop(st, kAttnFwd);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e == cudaSuccess && p.split ? launch_cross_join(s, p, a, st) : e;
 }
 
 template <bool KV8>
@@ -898,6 +899,23 @@ cudaError_t launch_any(const CrossShape& s, const FwdPlan& p, const CUtensorMap&
 // the split gains).
 FwdPlan cross_fwd_plan(const CrossShape& s, int sms) {
   FwdPlan p;
+  if (s.N * (int64_t)s.G <= kFewRows) {
+    // One tile of all rows.  Whole segments where a CTA's warps have at most four steps each, or
+    // where there are CTAs enough to even out the lengths.
+    p.few = true;
+    p.nb = s.N;
+    p.tiles = p.tp = p.pairs = 1;
+    p.shift = 6;
+    p.rows = kFewRows;
+    const int64_t segs = (int64_t)s.B * s.Hkv;
+    p.segs = segs > INT32_MAX ? -1 : (int)segs;
+    p.split = s.M > 1024 && segs < 8 * (int64_t)sms;
+    p.grid = p.split ? (int)std::min<int64_t>(sms, segs * ((s.M + 63) / 64)) : p.segs;
+    return p;
+  }
+  p.few = false;
+  p.shift = kKeyBlockShift;
+  p.rows = 256;
   p.nb = 128 / s.G;
   p.tiles = (s.N + p.nb - 1) / p.nb;
   const int64_t heads = (int64_t)s.B * s.Hkv;
@@ -914,8 +932,22 @@ FwdPlan cross_fwd_plan(const CrossShape& s, int sms) {
   return p;
 }
 
+cudaError_t launch_cross_join(const CrossShape& s, const FwdPlan& p, const CrossFwdArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)p.segs, (unsigned)((p.tp * 128 < p.rows ? p.tp * 128 : p.rows) / 16));
+  const bool f16 = s.dtype == SA2_FP16;
+  prof_start(st, kAttnFwd);
+  if (s.d == 128)
+    f16 ? cross_join_kernel<128, true><<<grid, 256, 0, st>>>(s, p, a)
+        : cross_join_kernel<128, false><<<grid, 256, 0, st>>>(s, p, a);
+  else
+    f16 ? cross_join_kernel<64, true><<<grid, 256, 0, st>>>(s, p, a)
+        : cross_join_kernel<64, false><<<grid, 256, 0, st>>>(s, p, a);
+  prof_stop(st, kAttnFwd);
+  return cudaGetLastError();
+}
+
 size_t cross_fwd_partials(const CrossShape& s, const FwdPlan& p) {
-  return p.split ? (size_t)(p.grid + p.segs) * 256 * (s.d + 1) : 0;
+  return p.split ? (size_t)(p.grid + p.segs) * p.rows * (s.d + 1) : 0;
 }
 
 cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,

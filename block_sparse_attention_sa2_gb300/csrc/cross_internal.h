@@ -29,7 +29,7 @@ struct CacheRef {
   int C, nsb;          // capacity in tokens, scales per head
 };
 
-constexpr int kKeyBlock = 128;  // keys per step of the cross- and cache-attention kernels
+constexpr int kKeyBlock = 128, kKeyBlockShift = 7;  // keys per step of the kernels on query tiles
 
 // How the work of a forward call is split over CTAs.  A segment is one pair of query tiles of
 // one key head; a tile holds nb tokens of all G heads of the group, row = token * G + g.
@@ -44,15 +44,19 @@ struct FwdPlan {
   int segs;
   int grid;
   int split;
+  int shift;  // log2 of the keys per block
+  int rows;   // of a slot of the split's partial results
+  bool few;   // at most kFewRows query rows per key head: the kernel of cross_decode.cu
 };
+constexpr int kFewRows = 16;
 
 struct CrossFwdArgs {
   const int32_t* kv_len;  // [B] or null
   TokenRef q;             // read by the cache kernel only (the other one has a tensor map)
   TokenRef o;
   float* lse;     // [B, H, N]
-  float* part_o;  // split: [grid + segs][256][d]
-  float* part_l;  // split: [grid + segs][256], log2 units
+  float* part_o;  // split: [grid + segs][rows][d]
+  float* part_l;  // split: [grid + segs][rows], log2 units
   float scale_log2;
   unsigned* status;
 };
@@ -103,6 +107,10 @@ cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtens
                              const CUtensorMap& mv, const CUtensorMap& mo, const CrossFwdArgs& a, cudaStream_t st);
 cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CacheRef& c, const CrossFwdArgs& a,
                              cudaStream_t st);
+cudaError_t launch_cross_join(const CrossShape& s, const FwdPlan& p, const CrossFwdArgs& a, cudaStream_t st);
+// Few query rows: over 16-bit keys and values (cache = false) or the cache.
+cudaError_t launch_few_rows(const CrossShape& s, const FwdPlan& p, const TokenRef& k, const TokenRef& v,
+                            const CacheRef& c, bool cache, const CrossFwdArgs& a, cudaStream_t st);
 cudaError_t launch_cache_append(const CacheRef& c, int B, int Hkv, int d, int n, bool f16, const TokenRef& k,
                                 const TokenRef& v, const int32_t* pos, const int32_t* n_new, unsigned* status,
                                 cudaStream_t st);

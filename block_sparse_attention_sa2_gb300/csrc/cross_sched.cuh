@@ -11,12 +11,16 @@ __device__ __forceinline__ int key_count(const int32_t* kv_len, int b, int M) {
   const int n = kv_len ? kv_len[b] : M;
   return n < 0 ? 0 : (n > M ? M : n);
 }
-__device__ __forceinline__ int key_blocks(int keys) { return (keys + kKeyBlock - 1) / kKeyBlock; }
+// Blocks of 2^shift keys.
+__device__ __forceinline__ int key_blocks(int keys, int shift = kKeyBlockShift) {
+  return (keys + (1 << shift) - 1) >> shift;
+}
 
 // Key blocks of all segments together; called by whole warps.
-__device__ __forceinline__ int64_t total_key_blocks(const CrossShape& s, const int32_t* kv_len, int pairs) {
+__device__ __forceinline__ int64_t total_key_blocks(const CrossShape& s, const int32_t* kv_len, int pairs,
+                                                    int shift = kKeyBlockShift) {
   int64_t n = 0;
-  for (int b = (int)(threadIdx.x & 31); b < s.B; b += 32) n += key_blocks(key_count(kv_len, b, s.M));
+  for (int b = (int)(threadIdx.x & 31); b < s.B; b += 32) n += key_blocks(key_count(kv_len, b, s.M), shift);
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n * s.Hkv * pairs;
 }
@@ -45,7 +49,7 @@ struct PieceIter {
   __device__ __forceinline__ PieceIter(const CrossShape& s_, const FwdPlan& p_, const int32_t* kv_len_)
       : s(s_), p(p_), kv_len(kv_len_), b(0), base(0) {
     if (p.split) {
-      const int64_t total = total_key_blocks(s, kv_len, p.pairs);
+      const int64_t total = total_key_blocks(s, kv_len, p.pairs, p.shift);
       const int64_t run = run_length(total, p.grid);
       g = run * blockIdx.x;
       g_end = g + run < total ? g + run : total;
@@ -62,14 +66,14 @@ struct PieceIter {
       x.b = x.seg / per_b;
       x.keys = key_count(kv_len, x.b, s.M);
       x.k0 = 0;
-      x.nb = key_blocks(x.keys);
+      x.nb = key_blocks(x.keys, p.shift);
       g += p.grid;
     } else {
-      int nk = key_blocks(key_count(kv_len, b, s.M));
+      int nk = key_blocks(key_count(kv_len, b, s.M), p.shift);
       while (g >= base + (int64_t)nk * per_b) {  // g < total: ends at a sequence with keys
         base += (int64_t)nk * per_b;
         ++b;
-        nk = key_blocks(key_count(kv_len, b, s.M));
+        nk = key_blocks(key_count(kv_len, b, s.M), p.shift);
       }
       x.b = b;
       x.keys = key_count(kv_len, b, s.M);
