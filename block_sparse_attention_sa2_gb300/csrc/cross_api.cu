@@ -12,11 +12,16 @@ constexpr int kMaxTokens = 1 << 28;
 constexpr int kMaxGroup = 64;
 constexpr int kMaxGridYZ = 32767;  // B and Hkv are grid dimensions (B twice over)
 
+// SMs of the current device (152 where there is none, so that sizes can be asked for on any host).
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  sms = known[dev].load(std::memory_order_relaxed);
+  if (sms == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 152;
+    known[dev].store(sms, std::memory_order_relaxed);
+  }
   return sms;
 }
 

@@ -801,8 +801,9 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
                      const CUtensorMap& mv, const CUtensorMap& mdo, const CrossBwdArgs& a, cudaStream_t st) {
   auto dq = cross_dq_kernel<D>;
   auto dkv = cross_dkdv_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqSmem<D>::kBytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvSmem<D>::kBytes);
+  static std::atomic<unsigned long long> dq_allowed{0}, dkv_allowed{0};
+  cudaError_t e = allow_smem(dq, DqSmem<D>::kBytes, dq_allowed);
+  if (e == cudaSuccess) e = allow_smem(dkv, DkvSmem<D>::kBytes, dkv_allowed);
   if (e != cudaSuccess) return e;
   prof_start(st, kBwdPre);
   cross_stats_kernel<D><<<(unsigned)((int64_t)s.B * s.Hkv * p.tiles), 256, 0, st>>>(s, p, a);

@@ -376,7 +376,8 @@ cudaError_t launch_t(const CrossShape& s, const FwdPlan& p, const KvRef& kv, con
   constexpr int kBytes = kWarps * kStages * kStageBytes;
   static_assert(kWarps * kFewRows * (D + 4) * 4 <= kBytes && kBytes + 1024 <= (int)kMaxDynSmem, "shared memory");
   auto kern = cross_few_kernel<D, KV8, F16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem(kern, kBytes, allowed);
   if (e != cudaSuccess) return e;
   prof_start(st, kAttnFwd);
   kern<<<(unsigned)p.grid, kThreads, kBytes, st>>>(s, p, kv, a);

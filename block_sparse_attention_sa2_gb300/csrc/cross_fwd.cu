@@ -865,7 +865,8 @@ template <int D, bool KV8, bool F16>
 cudaError_t launch_t(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
                      const CUtensorMap& mv, const CUtensorMap& mo, const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st) {
   auto kern = cross_fwd_kernel<D, KV8, F16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XSmem<D, KV8>::kBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem(kern, XSmem<D, KV8>::kBytes, allowed);
   if (e != cudaSuccess) return e;
   // the roles' registers add up to 128 a thread: with fewer at launch they would wait for ever
   static const int regs = [&] {

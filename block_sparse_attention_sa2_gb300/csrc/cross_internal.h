@@ -1,6 +1,8 @@
 // Declarations shared by the cross- and cache-attention sources (cross_*.cu, cache8.cu).
 #pragma once
 
+#include <atomic>
+
 #include "sa2_internal.h"
 
 namespace sa2 {
@@ -91,6 +93,19 @@ BwdPlan cross_bwd_plan(const CrossShape& s, int sms);
 size_t cross_bwd_floats(const CrossShape& s, const BwdPlan& p, size_t* stats);
 cudaError_t launch_cross_bwd(const CrossShape& s, const BwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
                              const CUtensorMap& mv, const CUtensorMap& mdo, const CrossBwdArgs& a, cudaStream_t st);
+
+// Allows a kernel its dynamic shared memory, once per device (`done` has a bit for each).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // The device's status word, and the wait settings of the calling thread's next launches
 // (sa2_api.cu).

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -38,23 +39,6 @@ class Shape(ctypes.Structure):
 
 class KernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", ctypes.c_int), ("total_ms", ctypes.c_double)]
-
-
-class CrossShape(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("N", ctypes.c_int32),
-                ("M", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
-
-
-class TensorStruct(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
-                ("stride_n", ctypes.c_int64)]
-
-
-class Cache8Struct(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
-                ("stride_n", ctypes.c_int64), ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("C", ctypes.c_int32),
-                ("d", ctypes.c_int32)]
 
 
 class BlockMaskStruct(ctypes.Structure):
@@ -93,7 +77,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa2_vd_loss_workspace_size.argtypes = [S]
     lib.sa2_vd_loss.restype = ctypes.c_int
     lib.sa2_vd_loss.argtypes = [S, P, P, P, P, P, P, P, Z, P]
-    X, T, C, I = ctypes.POINTER(CrossShape), ctypes.POINTER(TensorStruct), ctypes.POINTER(Cache8Struct), ctypes.c_int32
+    X = T = C = P  # sa2_cross_shape, sa2_tensor, sa2_cache8 as packed bytes
+    I = ctypes.c_int32
     lib.sa2_cross_fwd_workspace_size.restype = Z
     lib.sa2_cross_fwd_workspace_size.argtypes = [X]
     lib.sa2_cross_attn_fwd.restype = ctypes.c_int
@@ -271,68 +256,91 @@ def vd_loss(o_s: torch.Tensor, o_t: torch.Tensor, o_s_lo: Optional[torch.Tensor]
 
 
 # --------------------------------------------------- attention to keys of another length
+#
+# The structs of these calls are packed with ``struct`` (a few tenths of a microsecond each): a call
+# over a few keys takes the GPU less time than ctypes structures take the host.
 
 _DTYPE = {torch.bfloat16: SA2_BF16, torch.float16: SA2_FP16}
+_pack_tensor = struct.Struct("Pqqq").pack  # sa2_tensor
+_pack_cross = struct.Struct("8i").pack  # sa2_cross_shape
+_pack_cache = struct.Struct("PPPPqqqiiii").pack  # sa2_cache8
 
 
-def _token_struct(x: torch.Tensor, name: str, shape, dtype, device) -> TensorStruct:
-    if tuple(x.shape) != shape:
+def _tensor(x: torch.Tensor, name: str, shape, dtype, device) -> bytes:
+    """sa2_tensor of a token tensor of this shape, type and device."""
+    if x.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(x.shape)}")
     if x.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
     if x.device != device:
         raise ValueError(f"{name} must be on {device}, got {x.device}")
-    if x.stride(3) != 1:
+    sb, sh, sn, sd = x.stride()
+    if sd != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return TensorStruct(x.data_ptr(), x.stride(0), x.stride(1), x.stride(2))
+    return _pack_tensor(x.data_ptr(), sb, sh, sn)
 
 
 def _int32(x: Optional[torch.Tensor], name: str, B: int, device) -> Optional[int]:
     if x is None:
         return None
-    if x.dtype != torch.int32 or tuple(x.shape) != (B,) or not x.is_contiguous() or x.device != device:
+    if x.dtype != torch.int32 or x.shape != (B,) or not x.is_contiguous() or x.device != device:
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{B}] on {device}")
     return x.data_ptr()
 
 
-def _contiguous_f32(x: torch.Tensor, name: str, shape, device) -> int:
-    if x.dtype != torch.float32 or tuple(x.shape) != shape or not x.is_contiguous() or x.device != device:
+def _float32(x: torch.Tensor, name: str, shape, device) -> int:
+    if x.dtype != torch.float32 or x.shape != shape or not x.is_contiguous() or x.device != device:
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)} on {device}")
     return x.data_ptr()
 
 
-def _workspace_of(ws: Optional[torch.Tensor], nbytes: int, device, stream):
-    """The caller's workspace, or a new one that outlives the work on ``stream``."""
-    if ws is None and nbytes:
-        ws = workspace(nbytes, device)
-        if stream is not None:
-            ws.record_stream(stream)
-    if ws is not None and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous()):
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
-
-
-def _new_like(x: torch.Tensor, stream) -> torch.Tensor:
-    y = torch.empty_like(x)
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that stays allocated until the work on ``stream`` is done with it."""
+    x = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None:
-        y.record_stream(stream)
-    return y
+        x.record_stream(stream)
+    return x
 
 
-def _on(device):
-    """The device that a call's tensors are on, as the current one."""
+def _empty_like(y: torch.Tensor, stream) -> torch.Tensor:
+    x = torch.empty_like(y)
+    if stream is not None:
+        x.record_stream(stream)
+    return x
+
+
+def _workspace_of(ws: Optional[torch.Tensor], nbytes: int, device, stream):
+    if ws is None:
+        if not nbytes:
+            return None, 0
+        ws = _empty(nbytes, torch.uint8, device, stream)
+    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws.data_ptr(), ws.numel()
+
+
+def _on_other_device(device) -> bool:
+    """Whether the device that a call's tensors are on is not the current one."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, got {device}")
-    return torch.cuda.device(device)
+    return device.index != torch.cuda.current_device()
 
 
-def _cross_shape(q: torch.Tensor, Hkv: int, M: int) -> CrossShape:
-    if q.dim() != 4:
-        raise ValueError("token tensors are [B, H, N, d]")
-    if q.dtype not in _DTYPE:
-        raise ValueError(f"unsupported dtype {q.dtype}: torch.bfloat16 or torch.float16")
-    B, H, N, d = q.shape
-    return CrossShape(B, H, Hkv, N, M, d, _DTYPE[q.dtype], 0)
+def _raw_stream(stream, device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _dtype_code(dtype) -> int:
+    code = _DTYPE.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
+    return code
+
+
+def _dims(x: torch.Tensor, name: str):
+    if x.dim() != 4:
+        raise ValueError(f"{name}: token tensors are [B, H, N, d]")
+    return x.shape
 
 
 def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Optional[torch.Tensor] = None,
@@ -344,24 +352,21 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Op
     tensor with strides of its own.  ``kv_len`` ([B] int32 on the device): sequence b attends to its
     first kv_len[b] keys; without keys O = 0 and LSE = -inf.  LSE is float32 [B, H, N]."""
     lib = load_library()
-    if k.dim() != 4:
-        raise ValueError("token tensors are [B, H, N, d]")
-    shp = _cross_shape(q, k.shape[1], k.shape[2])
-    B, H, N, d = q.shape
-    kv = (B, k.shape[1], k.shape[2], d)
-    dev = q.device
-    with _on(dev):
-        o = _new_like(q, stream) if o is None else o
-        if lse is None:
-            lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
-            if stream is not None:
-                lse.record_stream(stream)
-        args = [_token_struct(x, n, s, q.dtype, dev) for x, n, s in ((q, "q", q.shape), (k, "k", kv), (v, "v", kv),
-                                                                      (o, "o", q.shape))]
-        w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(ctypes.byref(shp)), dev, stream)
-        _check("sa2_cross_attn_fwd", lib.sa2_cross_attn_fwd(
-            ctypes.byref(shp), args[0], args[1], args[2], _int32(kv_len, "kv_len", B, dev), float(scale or 0.0),
-            args[3], _contiguous_f32(lse, "lse", (B, H, N), dev), w, wn, _stream(stream)))
+    B, H, N, d = qs = _dims(q, "q")
+    _, Hkv, M, _ = _dims(k, "k")
+    dt, dev, kvs = q.dtype, q.device, (B, Hkv, M, d)
+    shp = _pack_cross(B, H, Hkv, N, M, d, _dtype_code(dt), 0)
+    if _on_other_device(dev):
+        with torch.cuda.device(dev):
+            return cross_attn_fwd(q, k, v, kv_len, scale, o, lse, ws, stream)
+    o = _empty_like(q, stream) if o is None else o
+    if lse is None:
+        lse = _empty((B, H, N), torch.float32, dev, stream)
+    w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(shp), dev, stream)
+    _check("sa2_cross_attn_fwd", lib.sa2_cross_attn_fwd(
+        shp, _tensor(q, "q", qs, dt, dev), _tensor(k, "k", kvs, dt, dev), _tensor(v, "v", kvs, dt, dev),
+        _int32(kv_len, "kv_len", B, dev), scale or 0.0, _tensor(o, "o", qs, dt, dev),
+        _float32(lse, "lse", (B, H, N), dev), w, wn, _raw_stream(stream, dev)))
     return o, lse
 
 
@@ -370,36 +375,55 @@ def cross_attn_bwd(q, k, v, o, lse, do, kv_len: Optional[torch.Tensor] = None, s
     """sa2_cross_attn_bwd: gradients (dQ, dK, dV) of cross_attn_fwd (bfloat16), whose o and lse on the
     same q, k, v, kv_len and scale it takes; zero behind kv_len."""
     lib = load_library()
-    if k.dim() != 4:
-        raise ValueError("token tensors are [B, H, N, d]")
-    shp = _cross_shape(q, k.shape[1], k.shape[2])
-    B, H, N, d = q.shape
-    kv = (B, k.shape[1], k.shape[2], d)
-    dev = q.device
-    with _on(dev):
-        dq = _new_like(q, stream) if dq is None else dq
-        dk = _new_like(k, stream) if dk is None else dk
-        dv = _new_like(v, stream) if dv is None else dv
-        t = {n: _token_struct(x, n, s, q.dtype, dev) for x, n, s in (
-            (q, "q", q.shape), (k, "k", kv), (v, "v", kv), (o, "o", q.shape), (do, "do", q.shape),
-            (dq, "dq", q.shape), (dk, "dk", kv), (dv, "dv", kv))}
-        w, wn = _workspace_of(ws, lib.sa2_cross_bwd_workspace_size(ctypes.byref(shp)), dev, stream)
-        _check("sa2_cross_attn_bwd", lib.sa2_cross_attn_bwd(
-            ctypes.byref(shp), t["q"], t["k"], t["v"], t["o"], _contiguous_f32(lse, "lse", (B, H, N), dev), t["do"],
-            _int32(kv_len, "kv_len", B, dev), float(scale or 0.0), t["dq"], t["dk"], t["dv"], w, wn, _stream(stream)))
+    B, H, N, d = qs = _dims(q, "q")
+    _, Hkv, M, _ = _dims(k, "k")
+    dt, dev, kvs = q.dtype, q.device, (B, Hkv, M, d)
+    shp = _pack_cross(B, H, Hkv, N, M, d, _dtype_code(dt), 0)
+    if _on_other_device(dev):
+        with torch.cuda.device(dev):
+            return cross_attn_bwd(q, k, v, o, lse, do, kv_len, scale, dq, dk, dv, ws, stream)
+    dq = _empty_like(q, stream) if dq is None else dq
+    dk = _empty_like(k, stream) if dk is None else dk
+    dv = _empty_like(v, stream) if dv is None else dv
+    w, wn = _workspace_of(ws, lib.sa2_cross_bwd_workspace_size(shp), dev, stream)
+    _check("sa2_cross_attn_bwd", lib.sa2_cross_attn_bwd(
+        shp, _tensor(q, "q", qs, dt, dev), _tensor(k, "k", kvs, dt, dev), _tensor(v, "v", kvs, dt, dev),
+        _tensor(o, "o", qs, dt, dev), _float32(lse, "lse", (B, H, N), dev), _tensor(do, "do", qs, dt, dev),
+        _int32(kv_len, "kv_len", B, dev), scale or 0.0, _tensor(dq, "dq", qs, dt, dev),
+        _tensor(dk, "dk", kvs, dt, dev), _tensor(dv, "dv", kvs, dt, dev), w, wn, _raw_stream(stream, dev)))
     return dq, dk, dv
 
 
-@dataclass
+_CACHE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
 class KvCache8:
-    """Keys and values held in 8 bits: e4m3 [B, Hkv, C, d] (k and v with the same strides) and one
-    power-of-two scale for each head and block of 64 tokens.  The caller keeps the lengths."""
-    k: torch.Tensor  # [B, Hkv, C, d] float8_e4m3fn (or uint8)
-    v: torch.Tensor
-    k_scale: torch.Tensor  # [B, Hkv, ceil(C / 64)] float32
-    v_scale: torch.Tensor
+    """Keys and values held in 8 bits: k, v e4m3 [B, Hkv, C, d] (float8_e4m3fn or uint8, with the same
+    strides) and k_scale, v_scale float32 [B, Hkv, ceil(C / 64)], one power-of-two scale for each head
+    and block of 64 tokens.  The tensors are the cache's for good; the caller keeps the lengths."""
 
     BLOCK = 64
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_shape", "_struct")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        B, Hkv, C, d = self._shape = _dims(k, "the cache's k")
+        sb, sh, sn, sd = st = k.stride()
+        dev = k.device
+        if v.shape != k.shape or v.stride() != st or sd != 1:
+            raise ValueError("the cache's k and v are [B, Hkv, C, d] with the same strides, d contiguous")
+        if k.dtype not in _CACHE_DTYPES or v.dtype not in _CACHE_DTYPES or v.device != dev:
+            raise ValueError("the cache's k and v are float8_e4m3fn (or uint8) on one device")
+        scales = (B, Hkv, -(-C // 64))
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        self._struct = _pack_cache(k.data_ptr(), v.data_ptr(), _float32(k_scale, "k_scale", scales, dev),
+                                   _float32(v_scale, "v_scale", scales, dev), sb, sh, sn, B, Hkv, C, d)
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
+    shape = property(lambda self: self._shape, doc="(B, Hkv, capacity, d)")
+    device = property(lambda self: self._k.device)
 
     @staticmethod
     def empty(B: int, Hkv: int, capacity: int, d: int, device) -> "KvCache8":
@@ -408,66 +432,46 @@ class KvCache8:
                   for _ in range(2))
         return KvCache8(k, v, ks, vs)
 
-    def struct(self) -> Cache8Struct:
-        k, v = self.k, self.v
-        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or k.stride(3) != 1:
-            raise ValueError("the cache's k and v are [B, Hkv, C, d] with the same strides, d contiguous")
-        for x in (k, v):
-            if x.dtype not in (torch.float8_e4m3fn, torch.uint8) or x.device != k.device:
-                raise ValueError("the cache's k and v are float8_e4m3fn (or uint8) on one device")
-        B, Hkv, C, d = k.shape
-        scales = (B, Hkv, blocks(C, self.BLOCK))
-        return Cache8Struct(k.data_ptr(), v.data_ptr(), _contiguous_f32(self.k_scale, "k_scale", scales, k.device),
-                            _contiguous_f32(self.v_scale, "v_scale", scales, k.device), k.stride(0), k.stride(1),
-                            k.stride(2), B, Hkv, C, d)
-
 
 def cache8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
                   n_new: Optional[torch.Tensor] = None, stream=None) -> None:
     """sa2_cache8_append: writes k, v [B, Hkv, n, d] (bfloat16 or float16) at positions pos[b] ..
     pos[b] + n - 1 (n_new[b] tokens of each sequence where given).  ``pos``, ``n_new``: [B] int32."""
     lib = load_library()
-    c = cache.struct()
-    if k.dim() != 4:
-        raise ValueError("token tensors are [B, H, N, d]")
-    if k.dtype not in _DTYPE:
-        raise ValueError(f"unsupported dtype {k.dtype}: torch.bfloat16 or torch.float16")
-    dev, n = cache.k.device, k.shape[2]
+    c = cache._struct
+    B, Hkv, _, d = cache._shape
+    n, dt, dev = _dims(k, "k")[2], k.dtype, cache._k.device
+    code, shape = _dtype_code(dt), (B, Hkv, n, d)
+    if pos is None:
+        raise ValueError("pos is required")
     if n == 0:
         return
-    with _on(dev):
-        shape = (c.B, c.Hkv, n, c.d)
-        if pos is None:
-            raise ValueError("pos is required")
-        _check("sa2_cache8_append", lib.sa2_cache8_append(
-            ctypes.byref(c), n, _DTYPE[k.dtype], _token_struct(k, "k", shape, k.dtype, dev),
-            _token_struct(v, "v", shape, k.dtype, dev), _int32(pos, "pos", c.B, dev),
-            _int32(n_new, "n_new", c.B, dev), _stream(stream)))
+    if _on_other_device(dev):
+        with torch.cuda.device(dev):
+            return cache8_append(cache, k, v, pos, n_new, stream)
+    _check("sa2_cache8_append", lib.sa2_cache8_append(
+        c, n, code, _tensor(k, "k", shape, dt, dev), _tensor(v, "v", shape, dt, dev), _int32(pos, "pos", B, dev),
+        _int32(n_new, "n_new", B, dev), _raw_stream(stream, dev)))
 
 
 def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
                 v: Optional[torch.Tensor] = None, stream=None):
     """sa2_cache8_read: the values of tokens pos[b] .. pos[b] + n - 1 as (K, V) [B, Hkv, n, d]."""
     lib = load_library()
-    c = cache.struct()
-    dev = cache.k.device
-    if dtype not in _DTYPE:
-        raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
-    with _on(dev):
-        shape = (c.B, c.Hkv, n, c.d)
-        if pos is None:
-            raise ValueError("pos is required")
-        if k is None:
-            k = torch.empty(shape, dtype=dtype, device=dev)
-            if stream is not None:
-                k.record_stream(stream)
-        if v is None:
-            v = _new_like(k, stream)
-        if n == 0:
-            return k, v
+    c = cache._struct
+    B, Hkv, _, d = cache._shape
+    code, dev, shape = _dtype_code(dtype), cache._k.device, (B, Hkv, n, d)
+    if pos is None:
+        raise ValueError("pos is required")
+    if _on_other_device(dev):
+        with torch.cuda.device(dev):
+            return cache8_read(cache, pos, n, dtype, k, v, stream)
+    k = _empty(shape, dtype, dev, stream) if k is None else k
+    v = _empty(shape, dtype, dev, stream) if v is None else v
+    if n:
         _check("sa2_cache8_read", lib.sa2_cache8_read(
-            ctypes.byref(c), n, _DTYPE[dtype], _token_struct(k, "k", shape, dtype, dev),
-            _token_struct(v, "v", shape, dtype, dev), _int32(pos, "pos", c.B, dev), _stream(stream)))
+            c, n, code, _tensor(k, "k", shape, dtype, dev), _tensor(v, "v", shape, dtype, dev),
+            _int32(pos, "pos", B, dev), _raw_stream(stream, dev)))
     return k, v
 
 
@@ -477,27 +481,27 @@ def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: O
     """sa2_cache8_attn: attention of q [B, H, N, d] to the first kv_len[b] tokens of the cache;
     returns (O, LSE) as cross_attn_fwd does."""
     lib = load_library()
-    c = cache.struct()
-    shp = _cross_shape(q, c.Hkv, c.C)
-    B, H, N, d = q.shape
-    if (B, d) != (c.B, c.d):
-        raise ValueError(f"the cache holds B = {c.B}, d = {c.d}; q has B = {B}, d = {d}")
+    c = cache._struct
+    B, H, N, d = qs = _dims(q, "q")
+    cb, Hkv, C, cd = cache._shape
+    dt, dev = q.dtype, q.device
+    if (B, d) != (cb, cd):
+        raise ValueError(f"the cache holds B = {cb}, d = {cd}; q has B = {B}, d = {d}")
     if kv_len is None:
         raise ValueError("kv_len is required")
-    dev = q.device
-    if cache.k.device != dev:
-        raise ValueError(f"the cache must be on {dev}, got {cache.k.device}")
-    with _on(dev):
-        o = _new_like(q, stream) if o is None else o
-        if lse is None:
-            lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
-            if stream is not None:
-                lse.record_stream(stream)
-        w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(ctypes.byref(shp)), dev, stream)
-        _check("sa2_cache8_attn", lib.sa2_cache8_attn(
-            ctypes.byref(shp), _token_struct(q, "q", q.shape, q.dtype, dev), ctypes.byref(c),
-            _int32(kv_len, "kv_len", B, dev), float(scale or 0.0), _token_struct(o, "o", q.shape, q.dtype, dev),
-            _contiguous_f32(lse, "lse", (B, H, N), dev), w, wn, _stream(stream)))
+    if cache._k.device != dev:
+        raise ValueError(f"the cache must be on {dev}, got {cache._k.device}")
+    shp = _pack_cross(B, H, Hkv, N, C, d, _dtype_code(dt), 0)
+    if _on_other_device(dev):
+        with torch.cuda.device(dev):
+            return cache8_attn(q, cache, kv_len, scale, o, lse, ws, stream)
+    o = _empty_like(q, stream) if o is None else o
+    if lse is None:
+        lse = _empty((B, H, N), torch.float32, dev, stream)
+    w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(shp), dev, stream)
+    _check("sa2_cache8_attn", lib.sa2_cache8_attn(
+        shp, _tensor(q, "q", qs, dt, dev), c, _int32(kv_len, "kv_len", B, dev), scale or 0.0,
+        _tensor(o, "o", qs, dt, dev), _float32(lse, "lse", (B, H, N), dev), w, wn, _raw_stream(stream, dev)))
     return o, lse
 
 

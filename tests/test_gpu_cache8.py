@@ -218,9 +218,9 @@ def test_refusals(sa2):
               lambda: sa2.cache8_append(c, x, x.half(), kl), lambda: sa2.cache8_append(c, x[:, :1], x[:, :1], kl),
               lambda: sa2.cache8_append(c, x, x, kl[:1]), lambda: sa2.cache8_append(c, x, x, None),
               lambda: sa2.cache8_read(c, kl, 4, dtype=torch.float32), lambda: sa2.cache8_read(c, None, 4),
-              lambda: sa2.KvCache8(c.k, c.v[:, :, :64], c.k_scale, c.v_scale).struct(),
-              lambda: sa2.KvCache8(c.k, c.v, c.k_scale[:, :, :1], c.v_scale).struct(),
-              lambda: sa2.KvCache8(c.k.float(), c.v.float(), c.k_scale, c.v_scale).struct()):
+              lambda: sa2.KvCache8(c.k, c.v[:, :, :64], c.k_scale, c.v_scale),
+              lambda: sa2.KvCache8(c.k, c.v, c.k_scale[:, :, :1], c.v_scale),
+              lambda: sa2.KvCache8(c.k.float(), c.v.float(), c.k_scale, c.v_scale)):
         with pytest.raises(ValueError):
             f()
     with pytest.raises(sa2.Sa2Error):  # three query heads, two key heads
