@@ -40,8 +40,14 @@ __device__ __forceinline__ void issue_ss(uint32_t d, uint64_t a, uint64_t b, uin
 // D (+)= A B with A in TMEM, 16 rows of B per k-step; A's k-steps 0..3 lie at column 0, 4..7 at 64
 // (each over the half of the scores that it was made from).
 __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps, bool fresh) {
-  for (int kk = 0; kk < steps; ++kk)
-    umma_ts(d, a + kk * 8 + (kk >= 4 ? 32 : 0), b + (uint64_t)(kk * 128), idesc, (fresh && kk == 0) ? 0u : 1u);
+  if (steps == 8) {
+    umma_ts(d, a, b, idesc, fresh ? 0u : 1u);
+#pragma unroll
+    for (int kk = 1; kk < 8; ++kk) umma_ts(d, a + kk * 8 + (kk >= 4 ? 32 : 0), b + (uint64_t)(kk * 128), idesc, 1u);
+  } else {
+    for (int kk = 0; kk < steps; ++kk)
+      umma_ts(d, a + kk * 8 + (kk >= 4 ? 32 : 0), b + (uint64_t)(kk * 128), idesc, (fresh && kk == 0) ? 0u : 1u);
+  }
 }
 
 // ------------------------------------------------------------------------- statistics
@@ -56,27 +62,41 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan 
   const int b = (int)(head / s.Hkv), hk = (int)(head - (int64_t)b * s.Hkv);
   const int ch = (threadIdx.x % kLanes) * 8;
   float* rec = a.stats + item * 256;
-  for (int r = threadIdx.x / kLanes; r < 128; r += 256 / kLanes) {
-    const int tok_r = r / s.G, h = hk * s.G + r - tok_r * s.G;
-    const int n = tile * plan.nb + tok_r;
-    const bool live = tok_r < plan.nb && n < s.N;
-    float acc = 0.f;
-    if (live) {
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dO.p) + b * a.dO.sb +
-                                                      h * a.dO.sh + n * a.dO.sn + ch);
-      const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.p) + b * a.o.sb + h * a.o.sh +
-                                                      n * a.o.sn + ch);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  constexpr int kRows = 256 / kLanes;  // rows per pass
+  constexpr int kFly = 4;              // passes whose loads are in flight together
+#pragma unroll 1
+  for (int r0 = threadIdx.x / kLanes; r0 < 128; r0 += kFly * kRows) {
+    uint4 x[kFly], y[kFly];
+    bool live[kFly];
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) {
+      const int r = r0 + u * kRows, tok_r = r / s.G, h = hk * s.G + r - tok_r * s.G;
+      const int n = tile * plan.nb + tok_r;
+      live[u] = tok_r < plan.nb && n < s.N;
+      x[u] = y[u] = make_uint4(0, 0, 0, 0);
+      if (live[u]) {
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dO.p) + b * a.dO.sb + h * a.dO.sh +
+                                               n * a.dO.sn + ch);
+        y[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.p) + b * a.o.sb + h * a.o.sh +
+                                               n * a.o.sn + ch);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFly; ++u) {
+      const int r = r0 + u * kRows, tok_r = r / s.G, h = hk * s.G + r - tok_r * s.G;
+      const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+      float acc = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), acc);
         acc = fmaf(__uint_as_float(xs[i] & 0xFFFF0000u), __uint_as_float(ys[i] & 0xFFFF0000u), acc);
       }
-    }
-    for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (ch == 0) {
-      rec[r] = live ? a.lse[((int64_t)b * s.H + h) * s.N + n] * 1.4426950408889634f : INFINITY;
-      rec[128 + r] = acc;
+      for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (ch == 0) {
+        const int n = tile * plan.nb + tok_r;
+        rec[r] = live[u] ? a.lse[((int64_t)b * s.H + h) * s.N + n] * 1.4426950408889634f : INFINITY;
+        rec[128 + r] = acc;
+      }
     }
   }
 }
@@ -426,9 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // through TMEM.  Per tile u:
 //   S^T = K Q^T, dP^T = V dO^T  (M = 128 keys, N = 128 rows),  dV += P^T dO, dK += dS^T Q.
 // TMEM is full (S^T, dP^T, dV, dK: 128 columns each); P^T is written over S^T and dS^T over dP^T.
-// The issuer runs S, dP, dV, dK in this order: S_{u+1} waits for dV_u while dK_u runs, dP_{u+1} for
-// dK_u while S_{u+1} runs; P is made while dP runs and dS while dV runs.
-// Roles: warp 0 TMA, warp 1 MMA issuer, warps 4..11 element-wise (thread = key, two per key: rows
+// The products run S, dP, dV, dK in this order: S_{u+1} waits for dV_u while dK_u runs, dP_{u+1} for
+// dK_u while S_{u+1} runs; P is made while dP runs and dS while dV runs.  Two issuers, so that one waits
+// on its barriers while the other's products run.
+// Roles: warp 0 TMA, warp 1 issuer of S, dP, warp 2 of dV, dK, warps 4..11 element-wise (thread = key, two per key: rows
 // 0..63 and 64..127 of the tile).
 template <int D>
 struct DkvSmem {
@@ -505,7 +526,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const uint32_t bar_p = smem_u32(&bars[12]), bar_ds = smem_u32(&bars[13]);    // P^T, dS^T written
   const uint32_t bar_dvm = smem_u32(&bars[14]), bar_dkm = smem_u32(&bars[15]); // dV, dK products completed
   const uint32_t bar_accfree = smem_u32(&bars[16]);                            // the piece's sums read out
-  const uint32_t bar_drain = smem_u32(&bars[17]);
+  const uint32_t bar_drain = smem_u32(&bars[17]), bar_gdrain = smem_u32(&bars[18]);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   const WaitCtl wc{abort_flag, s.wait_ns};
@@ -542,6 +563,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     mbar_init(bar_dkm, 1);
     mbar_init(bar_accfree, 256);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_gdrain, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -590,9 +612,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       if (n) mbar_drain(bar_kv, (n - 1) & 1, abort_flag);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------------ issuer of S^T and dP^T
     DkvIter it(s, plan, a.kv_len);
-    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false), idG = idesc_bf16_f32(128, D, false, true);
+    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
     const uint64_t kd = smem_desc(sbase + L::kOffK, 16, 1024), vd = smem_desc(sbase + L::kOffV, 16, 1024);
     bool ok = true;
     uint32_t U = 0, n = 0;
@@ -601,7 +623,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(bar_kv, n & 1, wc));
       for (int t = 0; ok && t < x.nt; ++t, ++U) {
         const int st = U % kStages;
-        const bool last = t + 1 == x.nt;
         const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
         ok = __all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc) &&
                                          (U == 0 || mbar_wait(bar_dvm, (U - 1) & 1, wc)));
@@ -618,11 +639,28 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         if (elect_one()) {
           issue_ss<D>(tmem + kDP, vd, smem_desc(stg + L::kStageDO, 16, 1024), idS);
           umma_commit(bar_dp);
-          if (last) umma_commit(bar_kvfree);
+          if (t + 1 == x.nt) umma_commit(bar_kvfree);
         }
         __syncwarp();
+      }
+      ++n;
+    }
+    if (elect_one()) umma_commit(bar_drain);
+    __syncwarp();
+    mbar_drain(bar_drain, 0, abort_flag);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ issuer of dV and dK
+    DkvIter it(s, plan, a.kv_len);
+    constexpr uint32_t idG = idesc_bf16_f32(128, D, false, true);
+    bool ok = true;
+    uint32_t U = 0, n = 0;
+    DkvPiece x;
+    while (ok && it.next(x)) {
+      for (int t = 0; ok && t < x.nt; ++t, ++U) {
+        const int st = U % kStages;
+        const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
         ok = __all_sync(0xffffffffu, (t > 0 || n == 0 || mbar_wait(bar_accfree, (n - 1) & 1, wc)) &&
-                                         mbar_wait(bar_p, U & 1, wc));
+                                         mbar_wait(bar_full(st), (U / kStages) & 1, wc) && mbar_wait(bar_p, U & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -642,9 +680,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       }
       ++n;
     }
-    if (elect_one()) umma_commit(bar_drain);
+    if (elect_one()) umma_commit(bar_gdrain);
     __syncwarp();
-    mbar_drain(bar_drain, 0, abort_flag);
+    mbar_drain(bar_gdrain, 0, abort_flag);
   } else if (warp >= 4) {
     // ------------------------------------------------------------- element-wise threads
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
