@@ -52,51 +52,57 @@ __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uin
 
 // ------------------------------------------------------------------------- statistics
 //
-// D and log2(e) * LSE of every query row.  D / 8 threads per row, one CTA per query tile.
+// D and log2(e) * LSE of every query row.  One CTA per query tile, D / 16 threads per row, every load
+// of a thread (16 times 16 bytes at d = 128) in flight at once: bound by the bytes of dO and O.
 template <int D>
 __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
-  constexpr int kLanes = D / 8;
-  const int64_t item = blockIdx.x;
-  const int tile = (int)(item % plan.tiles);
-  const int64_t head = item / plan.tiles;
-  const int b = (int)(head / s.Hkv), hk = (int)(head - (int64_t)b * s.Hkv);
-  const int ch = (threadIdx.x % kLanes) * 8;
-  float* rec = a.stats + item * 256;
-  constexpr int kRows = 256 / kLanes;  // rows per pass
-  constexpr int kFly = 4;              // passes whose loads are in flight together
-#pragma unroll 1
-  for (int r0 = threadIdx.x / kLanes; r0 < 128; r0 += kFly * kRows) {
-    uint4 x[kFly], y[kFly];
-    bool live[kFly];
+  constexpr int kLanes = D / 16;
+  constexpr int kRows = 256 / kLanes;    // rows per pass
+  constexpr int kPasses = 128 / kRows;
+  const int head = blockIdx.x / plan.tiles, tile = blockIdx.x - head * plan.tiles;
+  const int b = head / s.Hkv, hk = head - b * s.Hkv;
+  const int ch = (threadIdx.x % kLanes) * 16;
+  const int r0 = threadIdx.x / kLanes;
+  const uint16_t* dop = static_cast<const uint16_t*>(a.dO.p) + b * a.dO.sb + (int64_t)hk * s.G * a.dO.sh + ch;
+  const uint16_t* op = static_cast<const uint16_t*>(a.o.p) + b * a.o.sb + (int64_t)hk * s.G * a.o.sh + ch;
+  float* rec = a.stats + (int64_t)blockIdx.x * 256;
+  uint4 x[kPasses][2], y[kPasses][2];
+  float lse[kPasses];
 #pragma unroll
-    for (int u = 0; u < kFly; ++u) {
-      const int r = r0 + u * kRows, tok_r = r / s.G, h = hk * s.G + r - tok_r * s.G;
-      const int n = tile * plan.nb + tok_r;
-      live[u] = tok_r < plan.nb && n < s.N;
-      x[u] = y[u] = make_uint4(0, 0, 0, 0);
-      if (live[u]) {
-        x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dO.p) + b * a.dO.sb + h * a.dO.sh +
-                                               n * a.dO.sn + ch);
-        y[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.p) + b * a.o.sb + h * a.o.sh +
-                                               n * a.o.sn + ch);
+  for (int u = 0; u < kPasses; ++u) {
+    const int r = r0 + u * kRows, tok_r = r / s.G, g = r - tok_r * s.G;
+    const int n = tile * plan.nb + tok_r;
+    x[u][0] = x[u][1] = y[u][0] = y[u][1] = make_uint4(0, 0, 0, 0);
+    lse[u] = INFINITY;
+    if (tok_r < plan.nb && n < s.N) {
+      const uint4* px = reinterpret_cast<const uint4*>(dop + g * a.dO.sh + n * a.dO.sn);
+      const uint4* py = reinterpret_cast<const uint4*>(op + g * a.o.sh + n * a.o.sn);
+      x[u][0] = __ldg(px);
+      x[u][1] = __ldg(px + 1);
+      y[u][0] = __ldg(py);
+      y[u][1] = __ldg(py + 1);
+      if (ch == 0) lse[u] = a.lse[((int64_t)b * s.H + hk * s.G + g) * s.N + n];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kPasses; ++u) {
+    float acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t xs[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+      const uint32_t ys[4] = {y[u][i].x, y[u][i].y, y[u][i].z, y[u][i].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(ys[q] << 16), acc);
+        acc = fmaf(__uint_as_float(xs[q] & 0xFFFF0000u), __uint_as_float(ys[q] & 0xFFFF0000u), acc);
       }
     }
 #pragma unroll
-    for (int u = 0; u < kFly; ++u) {
-      const int r = r0 + u * kRows, tok_r = r / s.G, h = hk * s.G + r - tok_r * s.G;
-      const uint32_t xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
-      float acc = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), acc);
-        acc = fmaf(__uint_as_float(xs[i] & 0xFFFF0000u), __uint_as_float(ys[i] & 0xFFFF0000u), acc);
-      }
-      for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-      if (ch == 0) {
-        const int n = tile * plan.nb + tok_r;
-        rec[r] = live[u] ? a.lse[((int64_t)b * s.H + h) * s.N + n] * 1.4426950408889634f : INFINITY;
-        rec[128 + r] = acc;
-      }
+    for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (ch == 0) {
+      const int r = r0 + u * kRows;
+      rec[r] = lse[u] * 1.4426950408889634f;
+      rec[128 + r] = acc;
     }
   }
 }
@@ -106,10 +112,10 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan 
 // A work item is a query tile; its CTA walks the key blocks.  Per block j:
 //   S_j = Q K_j^T, dP_j = dO V_j^T  (M = 128 rows, N = 128 keys), dS_j = P (dP - D) in bf16 over
 //   dP_j's columns in TMEM, dQ += dS_j K_j.
-// The issuer runs S_{j+1}, dP_{j+1}, dQ_j: S_{j+1} needs only that the row threads have read S_j
-// (dQ_{j-1} runs meanwhile), dP_{j+1} that dQ_{j-1} has completed (S_{j+1} runs meanwhile; dP has
-// two buffers), and dQ_j has a whole period of three products for dS_j to be made in.
-// Roles: warp 0 TMA, warp 1 MMA issuer, warps 4..11 row threads (two per row: keys 0..63 and
+// S_{j+1} needs only that the row threads have read S_j (dQ_{j-1} runs meanwhile), dP_{j+1} that
+// dQ_{j-1} has completed (S_{j+1} runs meanwhile; dP has two buffers), and dQ_j has a whole period of
+// three products for dS_j to be made in.
+// Roles: warp 0 TMA, warp 1 issuer of S and dP, warp 2 of dQ, warps 4..11 row threads (two per row: keys 0..63 and
 // 64..127 of each block), warps 12..15 epilogue.
 // TMEM columns: S 0, dP 128 and 256, dQ 384.
 template <int D>
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_ds = [&](int i) { return smem_u32(&bars[18 + i]); };    // dS written over it
   auto bar_dqm = [&](int i) { return smem_u32(&bars[20 + i]); };   // dQ += dS K from it completed
   const uint32_t bar_dq = smem_u32(&bars[22]), bar_dqfree = smem_u32(&bars[23]);  // dQ of the item complete / read
-  const uint32_t bar_drain = smem_u32(&bars[24]);
+  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   const WaitCtl wc{abort_flag, s.wait_ns};
@@ -177,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar_dq, 1);
     mbar_init(bar_dqfree, 128);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_gdrain, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -258,41 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (don) mbar_drain(bar_do, (don - 1) & 1, abort_flag);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    constexpr uint32_t idQ = idesc_bf16_f32(128, D, false, true);
+    // ------------------------------------------------------------------ issuer of S and dP
     const uint64_t qd = smem_desc(sbase + L::kOffQ, 16, 1024), dod = smem_desc(sbase + L::kOffDO, 16, 1024);
     bool ok = true;
-    uint32_t J = 0, n = 0;  // blocks whose S, dP were issued; items
-    // dQ += dS K of block jj (count c over the CTA), the previous one issued
-    auto issue_dq = [&](const Item& x, int jj, uint32_t c) {
-      const int ks = c % kKSt, bb = c & 1;
-      const int valid = min(kKeyBlock, x.keys - jj * kKeyBlock), steps = (valid + 15) >> 4;
-      if (!__all_sync(0xffffffffu, (jj > 0 || n == 0 || mbar_wait(bar_dqfree, (n - 1) & 1, wc)) &&
-                                       mbar_wait(bar_ds(bb), (c >> 1) & 1, wc)))
-        return false;
-      if (valid & 15) {
-        // rows of K behind the last key, up to the next multiple of 16, as zeros: dS is 0 there, but
-        // 0 * NaN is NaN.  S_j, which read them before, has completed (dS_j was made from it).
-        const int rows = 16 * steps - valid, nz = rows * 8 * L::kPanels;
-        uint8_t* kt = smem + L::kOffK + ks * L::kTile;
-        for (int i = lane; i < nz; i += 32) {
-          const int row = valid + (i >> 3) % rows, p = (i >> 3) / rows;
-          *reinterpret_cast<uint4*>(kt + p * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-        __syncwarp();
-      }
-      tc_fence_after();
-      const uint64_t kmn = smem_desc(sbase + L::kOffK + ks * L::kTile, 16384, 1024);
-      if (elect_one()) {
-        issue_ts(tmem + kDQ, tmem + kDP + bb * 128, kmn, idQ, steps, jj == 0);
-        umma_commit(bar_dqm(bb));
-        umma_commit(bar_kempty(ks));
-        if (jj + 1 == x.nk) umma_commit(bar_dq);
-      }
-      __syncwarp();
-      return true;
-    };
+    uint32_t J = 0, n = 0;  // blocks, items
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item x = item_at(i);
       for (int j = 0; ok && j < x.nk; ++j, ++J) {
@@ -322,16 +298,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j + 1 == x.nk) umma_commit(bar_dofree);
         }
         __syncwarp();
-        if (j > 0) ok = issue_dq(x, j - 1, J - 1);
       }
-      if (ok && x.nk > 0) {
-        ok = issue_dq(x, x.nk - 1, J - 1);
-        ++n;
-      }
+      if (x.nk > 0) ++n;
     }
     if (elect_one()) umma_commit(bar_drain);
     __syncwarp();
     mbar_drain(bar_drain, 0, abort_flag);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ issuer of dQ
+    constexpr uint32_t idQ = idesc_bf16_f32(128, D, false, true);
+    bool ok = true;
+    uint32_t J = 0, n = 0;
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item x = item_at(i);
+      for (int j = 0; j < x.nk; ++j, ++J) {
+        const int ks = J % kKSt, bb = J & 1;
+        const int valid = min(kKeyBlock, x.keys - j * kKeyBlock), steps = (valid + 15) >> 4;
+        ok = __all_sync(0xffffffffu, (j > 0 || n == 0 || mbar_wait(bar_dqfree, (n - 1) & 1, wc)) &&
+                                         mbar_wait(bar_kfull(ks), (J / kKSt) & 1, wc) &&
+                                         mbar_wait(bar_ds(bb), (J >> 1) & 1, wc));
+        if (!ok) break;
+        if (valid & 15) {
+          // rows of K behind the last key, up to the next multiple of 16, as zeros: dS is 0 there, but
+          // 0 * NaN is NaN.  S_j, which read them before, has completed (dS_j was made from it).
+          const int rows = 16 * steps - valid, nz = rows * 8 * L::kPanels;
+          uint8_t* kt = smem + L::kOffK + ks * L::kTile;
+          for (int q = lane; q < nz; q += 32) {
+            const int row = valid + (q >> 3) % rows, p = (q >> 3) / rows;
+            *reinterpret_cast<uint4*>(kt + p * 16384 + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        tc_fence_after();
+        const uint64_t kmn = smem_desc(sbase + L::kOffK + ks * L::kTile, 16384, 1024);
+        if (elect_one()) {
+          issue_ts(tmem + kDQ, tmem + kDP + bb * 128, kmn, idQ, steps, j == 0);
+          umma_commit(bar_dqm(bb));
+          umma_commit(bar_kempty(ks));
+          if (j + 1 == x.nk) umma_commit(bar_dq);
+        }
+        __syncwarp();
+      }
+      if (x.nk > 0) ++n;
+    }
+    if (elect_one()) umma_commit(bar_gdrain);
+    __syncwarp();
+    mbar_drain(bar_gdrain, 0, abort_flag);
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------------ row threads
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
@@ -472,17 +485,39 @@ struct DkvPiece {
   bool whole;
   int slot;
 };
+// Parts that every key block's tiles are cut into, one per CTA, where that leaves less than a tenth of
+// the CTAs without work; 0: equal runs.  With parts, the key blocks of a head read the same tiles at
+// the same time, and all but the first find them in L2 (512 keys, 12 heads of 32760 queries: DRAM
+// traffic 805 -> 201 MB).
+__device__ __forceinline__ int dkv_parts(int64_t segs, int tiles, int grid) {
+  if (segs == 0 || segs > grid) return 0;
+  const int64_t parts = min((int64_t)tiles, grid / segs);
+  return parts * segs * 10 >= (int64_t)grid * 9 ? (int)parts : 0;
+}
+
 struct DkvIter {
   const CrossShape& s;
   const BwdPlan& p;
   const int32_t* kv_len;
   int64_t g, g_begin, g_end, base;
   int b;
-  __device__ __forceinline__ DkvIter(const CrossShape& s_, const BwdPlan& p_, const int32_t* l) : s(s_), p(p_), kv_len(l), base(0), b(0) {
-    const int64_t total = total_key_blocks(s, kv_len, 1) * p.tiles;
-    const int64_t run = run_length(total, p.grid);
-    g = g_begin = run * blockIdx.x;
-    g_end = g + run < total ? g + run : total;
+  // (whole warps)
+  __device__ __forceinline__ DkvIter(const CrossShape& s_, const BwdPlan& p_, const int32_t* l)
+      : s(s_), p(p_), kv_len(l), base(0), b(0) {
+    const int64_t segs = total_key_blocks(s, kv_len, 1), total = segs * p.tiles;
+    const int parts = dkv_parts(segs, p.tiles, p.grid);
+    if (parts) {
+      // part i of segment blockIdx.x % segs, so that a head's key blocks are neighbours
+      const int64_t seg = blockIdx.x % segs;
+      const int i = (int)(blockIdx.x / segs);
+      g = seg * p.tiles + (int64_t)i * p.tiles / parts;
+      g_end = i < parts ? seg * p.tiles + (int64_t)(i + 1) * p.tiles / parts : g;
+    } else {
+      const int64_t run = run_length(total, p.grid);
+      g = run * blockIdx.x;
+      g_end = g + run < total ? g + run : total;
+    }
+    g_begin = g;
   }
   __device__ __forceinline__ bool next(DkvPiece& x) {
     if (g >= g_end) return false;
@@ -803,25 +838,37 @@ __global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdP
   const int kb = blockIdx.x, lane = threadIdx.x & 31;
   const int b = blockIdx.y / s.Hkv, hk = blockIdx.y - b * s.Hkv;
   const int keys = key_count(a.kv_len, b, s.M), nk = key_blocks(keys);
-  int64_t g0 = 0, g1 = 0, run = 1;
+  // the parts: slots first, first + step, ... of CTAs; the part that a run begins with is in 2 * CTA
+  int c0 = 0, count = 0, step = 1;
+  int64_t g0 = 0, run = 0;
   if (kb < nk) {
-    run = run_length(total_key_blocks(s, a.kv_len, 1) * plan.tiles, plan.grid);
+    const int64_t segs = total_key_blocks(s, a.kv_len, 1);
     int64_t before = 0;
     for (int i = lane; i < b; i += 32) before += key_blocks(key_count(a.kv_len, i, s.M));
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    g0 = (before * s.Hkv + (int64_t)hk * nk + kb) * plan.tiles;
-    g1 = g0 + plan.tiles;
-    if (g0 / run == (g1 - 1) / run) return;  // one CTA had them all
+    const int64_t seg = before * s.Hkv + (int64_t)hk * nk + kb;
+    const int parts = dkv_parts(segs, plan.tiles, plan.grid);
+    if (parts) {
+      c0 = (int)seg;
+      count = parts;
+      step = (int)segs;
+    } else {
+      run = run_length(segs * plan.tiles, plan.grid);
+      g0 = seg * plan.tiles;
+      c0 = (int)(g0 / run);
+      count = (int)((g0 + plan.tiles - 1) / run) - c0 + 1;
+    }
+    if (count == 1) return;  // one CTA had all of its tiles
   }
-  const int c0 = (int)(g0 / run), c1 = kb < nk ? (int)((g1 - 1) / run) : c0 - 1;
   for (int i = threadIdx.x; i < 2 * 128 * (D / 8); i += 256) {
     const int w = i / (128 * (D / 8)), r = i / (D / 8) % 128, ch = i % (D / 8) * 8;
     const int key = kb * kKeyBlock + r;
     if (key >= s.M) continue;
     float v[8] = {};
     if (key < keys) {
-      for (int c = c0; c <= c1; ++c) {
-        const int slot = 2 * c + (run * c >= g0 ? 0 : 1);  // the part starts with the run, or inside it
+      for (int k = 0; k < count; ++k) {
+        const int c = c0 + k * step;
+        const int slot = 2 * c + (run * c >= g0 ? 0 : 1);  // the part begins with the run, or inside it
         const float4* p = reinterpret_cast<const float4*>(a.part + (((int64_t)slot * 2 + w) * 128 + r) * D + ch);
         const float4 x = p[0], y = p[1];
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;

@@ -70,7 +70,7 @@ size_t cross_fwd_partials(const CrossShape& s, const FwdPlan& p);  // floats of 
 // g); its statistics are kept per tile: stats[(head * tiles + tile) * 256 + r] = log2(e) * LSE of
 // row r (+inf for rows that hold no query: their P is 0) and [... + 128 + r] = D, head = b * Hkv + hk.
 // The dK / dV kernel's work, (key block, query tile) pairs ordered by key head, key block and tile,
-// is cut into `grid` equal runs, one per CTA.  A run that holds a key block's tiles whole writes
+// is cut into equal runs, one per CTA (dkv_parts in cross_bwd.cu).  A run that holds a key block's tiles whole writes
 // its dK, dV; of the others each run leaves fp32 sums, slot 2 * CTA for the part that the run
 // begins with and 2 * CTA + 1 for one that begins inside it, which a second kernel adds in order.
 struct BwdPlan {
