@@ -56,6 +56,20 @@ bool make_group_map(CUtensorMap* map, const TokenRef& t, int B, int heads, int G
   return r == CUDA_SUCCESS;
 }
 
+bool make_cache_map(CUtensorMap* map, const uint8_t* base, const CacheRef& c, int B, int Hkv, int d, int box_n) {
+  auto enc = encode_tiled();
+  if (!enc) return false;
+  std::memset(map, 0, sizeof(*map));
+  cuuint64_t dims[5] = {(cuuint64_t)d, 1, (cuuint64_t)c.C, (cuuint64_t)Hkv, (cuuint64_t)B};
+  cuuint64_t strides[4] = {(cuuint64_t)c.sn, (cuuint64_t)c.sn, (cuuint64_t)c.sh, (cuuint64_t)c.sb};
+  cuuint32_t box[5] = {(cuuint32_t)d, 1, (cuuint32_t)box_n, 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<uint8_t*>(base), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 template <typename T>
 __device__ __forceinline__ float4 ld4(const T* p);
 template <>

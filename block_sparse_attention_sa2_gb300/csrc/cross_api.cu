@@ -248,7 +248,10 @@ sa2_status sa2_cache8_attn(const sa2_cross_shape* shape, const sa2_tensor* q, co
   if (st != SA2_OK) return st;
   if (plan.few)
     return cuda_status(launch_few_rows(s, plan, TokenRef{}, TokenRef{}, c, true, a, static_cast<cudaStream_t>(stream)));
-  return cuda_status(launch_cache_fwd(s, plan, c, a, static_cast<cudaStream_t>(stream)));
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, c.k, c, s.B, s.Hkv, s.d, kKeyBlock) || !make_cache_map(&mv, c.v, c, s.B, s.Hkv, s.d, kKeyBlock))
+    return SA2_ERR_CUDA;
+  return cuda_status(launch_cache_fwd(s, plan, mk, mv, c, a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

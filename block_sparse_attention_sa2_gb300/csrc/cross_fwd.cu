@@ -10,7 +10,7 @@
 //
 // Roles (512 threads): warp 0 TMA producer (Q tiles, a ring of K and V blocks of 128 keys);
 // warps 1 and 2 issuers of the MMAs of tile 0 and 1; warps 4..7 epilogue (16-bit keys) or
-// converters (8-bit keys: global memory -> registers -> fp16 in the ring, and Q to fp16); warps
+// converters (8-bit keys: from blocks as they lie in the cache to fp16 in the ring, and Q to fp16); warps
 // 8..11 and 12..15 the softmax of tile 0 and 1, one row per thread.
 // The two tiles are chains of their own, S_t(j), softmax, P_t V(j), S_t(j+1), that share the ring
 // of keys: while one is in its softmax the other has the tensor cores.  S_t(j) overwrites the TMEM
@@ -37,7 +37,7 @@ constexpr int kThreads = 512;
 // warpgroup: issuers, epilogue or converters, 2 x softmax.
 template <bool KV8>
 struct Regs {
-  static constexpr int kIssue = KV8 ? 48 : 56, kEpilogue = KV8 ? 112 : 72, kSoftmax = KV8 ? 176 : 192;
+  static constexpr int kIssue = 56, kEpilogue = 72, kSoftmax = 192;
   static_assert(kIssue + kEpilogue + 2 * kSoftmax == 4 * 128, "more would wait for ever");
 };
 constexpr uint32_t kTmemCols = 512;
@@ -57,10 +57,13 @@ template <int D, bool KV8>
 struct XSmem {
   static constexpr int kPanels = D / 64;
   static constexpr int kTile = 128 * 128 * kPanels;  // 128 rows x 128 B per panel
-  static constexpr int kStages = D == 64 ? 8 : (KV8 ? 5 : 4);
+  static constexpr int kStages = D == 64 ? 8 : 4;
   static constexpr int kOffKV = 2 * kTile;
-  static constexpr int kOffO = kOffKV + kStages * kTile;  // 16-bit keys: a tile of O on its way out
-  static constexpr int kOffBar = kOffO + (KV8 ? 0 : kTile);
+  static constexpr int kRaw = kTile / 2;                  // 8-bit keys: a block as it lies in the cache
+  static constexpr int kRawStages = D == 64 ? 4 : 2;
+  static constexpr int kOffRaw = kOffKV + kStages * kTile;
+  static constexpr int kOffO = kOffRaw;                   // 16-bit keys: a tile of O on its way out
+  static constexpr int kOffBar = kOffRaw + (KV8 ? kRawStages * kRaw : kTile);
   // [2][128], for each row 1 / l (16-bit keys) or the scale of its converted query (8-bit keys)
   static constexpr int kOffRow = kOffBar + 512;
   static constexpr int kBytes = kOffRow + 1024 + 1024;
@@ -225,6 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_l = [&](int t) { return smem_u32(&bars[32 + t]); };        // 1 / l of the piece written
   auto bar_drain = [&](int t) { return smem_u32(&bars[34 + t]); };
   const uint32_t bar_st = smem_u32(&bars[38]), bar_stfree = smem_u32(&bars[39]);  // O tile staged / copied out
+  auto bar_rfull = [&](int i) { return smem_u32(&bars[40 + i]); };    // 8-bit block landed
+  auto bar_rempty = [&](int i) { return smem_u32(&bars[44 + i]); };   // ... and converted
   auto bar_sfree = [&](int t) { return smem_u32(&bars[36 + t]); };    // S_t read out (d = 64)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
@@ -250,6 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_l(t), 128);
       mbar_init(bar_drain(t), 1);
       mbar_init(bar_sfree(t), 128);
+    }
+    for (int i = 0; i < L::kRawStages; ++i) {
+      mbar_init(bar_rfull(i), 1);
+      mbar_init(bar_rempty(i), 128);
     }
     mbar_init(bar_st, 128);
     mbar_init(bar_stfree, 1);
@@ -317,6 +326,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(bar_full(v % kStages), (v / kStages) & 1, abort_flag);
       for (int t = 0; t < 2; ++t)
         if (qn[t]) mbar_drain(bar_qfull(t), (qn[t] - 1) & 1, abort_flag);
+    }
+  } else if (warp == 0) {
+    // ---------------------------------------------------- TMA producer of the 8-bit blocks
+    give_registers<Regs<KV8>::kIssue>();
+    PieceIter it(s, plan, a.kv_len);  // (whole warps)
+    if (lane == 0) {
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+      uint32_t r = 0;
+      bool ok = true;
+      Piece x;
+      while (ok && it.next(x)) {
+        for (int i = 0; i < 2 * x.nb; ++i, ++r) {
+          const int st = r % L::kRawStages;
+          if (r >= (uint32_t)L::kRawStages && !mbar_wait(bar_rempty(st), ((r / L::kRawStages) - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_rfull(st), L::kRaw);
+          tma_load_5d(sbase + L::kOffRaw + st * L::kRaw, (i & 1) ? &mv : &mk, bar_rfull(st), 0, 0,
+                      (x.k0 + (i >> 1)) * kKeyBlock, x.hk, x.b);
+        }
+      }
+      for (uint32_t v = r > (uint32_t)L::kRawStages ? r - L::kRawStages : 0; v < r; ++v)
+        mbar_drain(bar_rfull(v % L::kRawStages), (v / L::kRawStages) & 1, abort_flag);
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------------ MMA issuer of tile t
@@ -699,40 +733,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Piece x;
     while (ok && it.next(x)) {
       if (x.nb == 0) continue;
-      const int64_t head = (int64_t)x.b * cache.sb + (int64_t)x.hk * cache.sh + ch * 16;
-      // a tile into registers; behind the last key zeros
-      auto fetch = [&](const uint8_t* base, int kb, uint4 (&u)[kChunks]) {
-        const int t0 = kb * kKeyBlock + r0;
-        const uint8_t* p = base + head + (int64_t)t0 * cache.sn;
-#pragma unroll
-        for (int q = 0; q < kChunks; ++q) {
-          u[q] = make_uint4(0, 0, 0, 0);
-          if (t0 + q * kRows < x.keys) u[q] = __ldg(reinterpret_cast<const uint4*>(p + (int64_t)(q * kRows) * cache.sn));
-        }
-      };
-      // ... and into the next ring stage, swizzled; a row's 16 values are 32 bytes of panel ch / 4
-      auto put = [&](const uint4 (&u)[kChunks]) {
-        const int st = r % kStages;
-        if (r >= (uint32_t)kStages && !__all_sync(0xffffffffu, mbar_wait(bar_empty(st), ((r / kStages) - 1) & 1, wc)))
-          return false;
-        uint8_t* dst = smem + L::kOffKV + st * L::kTile + (ch >> 2) * 16384;
-#pragma unroll
-        for (int q = 0; q < kChunks; ++q) {
-          const int row = r0 + q * kRows;
-          const uint2 w0 = e4m3x4_to_f16x4(u[q].x), w1 = e4m3x4_to_f16x4(u[q].y), w2 = e4m3x4_to_f16x4(u[q].z),
-                      w3 = e4m3x4_to_f16x4(u[q].w);
-          const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
-          // the two panels' lanes store opposite halves first, so that a quarter warp's 16-byte
-          // stores fall into different banks
-          const int odd = (ch >> 2) & 1, k16 = (ch & 3) * 2;
-          *reinterpret_cast<uint4*>(dst + row * 128 + (((k16 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + row * 128 + (((k16 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
-        }
-        fence_proxy_async();
-        mbar_arrive(bar_full(st));
-        ++r;
-        return true;
-      };
       // Q: thread = row, scaled by a power of two so that its largest magnitude is in [2^14, 2^15)
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
@@ -778,15 +778,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar_qfull(t));
       }
       if (!ok) break;
-      // K_0, V_0, K_1, ...: the next tile's loads are in flight while one is converted
-      uint4 uk[kChunks], uv[kChunks];
-      fetch(cache.k, x.k0, uk);
-      for (int j = 0; ok && j < x.nb; ++j) {
-        fetch(cache.v, x.k0 + j, uv);
-        ok = put(uk);
-        if (!ok) break;
-        if (j + 1 < x.nb) fetch(cache.k, x.k0 + j + 1, uk);
-        ok = put(uv);
+      // K_0, V_0, K_1, ... as they land, into the ring, swizzled: a key's 16 values of chunk ch are 32
+      // bytes of panel ch / 4; behind the last key zeros
+      for (int i = 0; i < 2 * x.nb; ++i, ++r) {
+        const int st = r % kStages, rs = r % L::kRawStages;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(bar_rfull(rs), (r / L::kRawStages) & 1, wc) &&
+                            (r < (uint32_t)kStages || mbar_wait(bar_empty(st), ((r / kStages) - 1) & 1, wc)))) {
+          ok = false;
+          break;
+        }
+        const int valid = x.keys - (x.k0 + (i >> 1)) * kKeyBlock;
+        const uint8_t* src = smem + L::kOffRaw + rs * L::kRaw + r0 * D + ch * 16;
+        uint8_t* dst = smem + L::kOffKV + st * L::kTile + (ch >> 2) * 16384;
+#pragma unroll
+        for (int q = 0; q < kChunks; ++q) {
+          const int row = r0 + q * kRows;
+          const uint4 u = row < valid ? *reinterpret_cast<const uint4*>(src + q * kRows * D) : make_uint4(0, 0, 0, 0);
+          const uint2 w0 = e4m3x4_to_f16x4(u.x), w1 = e4m3x4_to_f16x4(u.y), w2 = e4m3x4_to_f16x4(u.z),
+                      w3 = e4m3x4_to_f16x4(u.w);
+          const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+          // the two panels' lanes store opposite halves first, so that a quarter warp's 16-byte
+          // stores fall into different banks
+          const int odd = (ch >> 2) & 1, k16 = (ch & 3) * 2;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((k16 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((k16 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+        }
+        fence_proxy_async();
+        mbar_arrive(bar_full(st));
+        mbar_arrive(bar_rempty(rs));
       }
     }
   } else {
@@ -956,10 +976,10 @@ cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtens
   return launch_any<false>(s, p, mq, mk, mv, mo, CacheRef{}, a, st);
 }
 
-cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CacheRef& c, const CrossFwdArgs& a,
-                             cudaStream_t st) {
+cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                             const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st) {
   const CUtensorMap none{};
-  return launch_any<true>(s, p, none, none, none, none, c, a, st);
+  return launch_any<true>(s, p, none, mk, mv, none, c, a, st);
 }
 
 }  // namespace sa2

@@ -118,10 +118,13 @@ void wait_settings(unsigned long long* wait_ns, unsigned long long* stall_ns);
 bool make_group_map(CUtensorMap* map, const TokenRef& t, int B, int heads, int G, int tokens, int d, int box_g,
                     int box_n, bool f16);
 
+// Tensor map of the cache's keys or values, boxes of d channels x box_n tokens as they lie.
+bool make_cache_map(CUtensorMap* map, const uint8_t* base, const CacheRef& c, int B, int Hkv, int d, int box_n);
+
 cudaError_t launch_cross_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
                              const CUtensorMap& mv, const CUtensorMap& mo, const CrossFwdArgs& a, cudaStream_t st);
-cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CacheRef& c, const CrossFwdArgs& a,
-                             cudaStream_t st);
+cudaError_t launch_cache_fwd(const CrossShape& s, const FwdPlan& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                             const CacheRef& c, const CrossFwdArgs& a, cudaStream_t st);
 cudaError_t launch_cross_join(const CrossShape& s, const FwdPlan& p, const CrossFwdArgs& a, cudaStream_t st);
 // Few query rows: over 16-bit keys and values (cache = false) or the cache.
 cudaError_t launch_few_rows(const CrossShape& s, const FwdPlan& p, const TokenRef& k, const TokenRef& v,
