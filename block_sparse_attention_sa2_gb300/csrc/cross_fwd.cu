@@ -8,18 +8,17 @@
 // other's products.  A tile's rows are the tokens of all G query heads that share the key head
 // (row = token * G + head), which lets few tokens of many heads fill a tile.
 //
-// Roles (512 threads): warp 0 TMA producer (Q tiles, a ring of K and V blocks of 128 keys);
-// warps 1 and 2 issuers of the MMAs of tile 0 and 1; warps 4..7 epilogue (16-bit keys) or
-// converters (8-bit keys: from blocks as they lie in the cache to fp16 in the ring, and Q to fp16); warps
-// 8..11 and 12..15 the softmax of tile 0 and 1, one row per thread.
-// The two tiles are chains of their own, S_t(j), softmax, P_t V(j), S_t(j+1), that share the ring
-// of keys: while one is in its softmax the other has the tensor cores.  S_t(j) overwrites the TMEM
-// columns that hold P_t(j-1), so its issuer waits for the completion of P_t V(j-1).
-//   S_t  = Q_t K_j^T   M = 128, N = 128, K = d   (shared memory, K-major)
-//   O_t += P_t V_j     M = 128, N = d, K = 128   (A = P from TMEM, V MN-major)
-// The softmax thread keeps its row's 128 scores in registers; P V of keys 0..95 starts while it takes
-// the exponentials of 96..127.  At d = 64 the accumulators leave TMEM room for P in columns of its own:
-// S_t(j+1) then follows as soon as S_t(j) has been read, and the chain is the softmax alone.
+// Roles (512 threads): warp 0 TMA producer (Q tiles, a ring of K and V blocks of 128 keys); warps 1
+// and 2 issuers of the MMAs of tile 0 and 1; warps 4..7 epilogue (16-bit keys) or converters (8-bit
+// keys: from blocks as they lie in the cache to fp16 in the ring, and Q to fp16); warps 8..11 and
+// 12..15 the softmax of tile 0 and 1, one row per thread.
+// A tile goes through its keys in half blocks of 64, with two S buffers:
+//   S_t(i) = Q_t K_i^T   M = 128, N = 64, K = d   (shared memory, K-major)
+//   O_t   += P_t(i) V_i  M = 128, N = d, K = 64   (A = P from TMEM, written over S_t(i); V MN-major)
+// S_t(i+1) is made while the softmax of S_t(i) runs, once P_t(i-1) V, which read its columns, has
+// completed.  With blocks of 128 keys TMEM has room for one S per tile only, and S, softmax and P V
+// are one chain: 3300 to 5000 cycles per 128 keys and tile pair, by how the two tiles happened to fall
+// in step, against 2560 of shared-memory reads for the products here.
 //
 // The last block of a sequence may be partial.  Its products run over the valid keys rounded up
 // to 16; scores behind the last key are replaced by -inf (whatever they are: NaN too), and up to
@@ -33,25 +32,12 @@ namespace sa2 {
 namespace {
 
 constexpr int kThreads = 512;
-// Registers: 512 threads are launched with 128 each and share them out anew by role, warpgroup by
-// warpgroup: issuers, epilogue or converters, 2 x softmax.
-template <bool KV8>
-struct Regs {
-  static constexpr int kIssue = 56, kEpilogue = 72, kSoftmax = 192;
-  static_assert(kIssue + kEpilogue + 2 * kSoftmax == 4 * 128, "more would wait for ever");
-};
 constexpr uint32_t kTmemCols = 512;
-constexpr long long kStaggerCycles = 2500;  // a little more than S and one softmax
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O and l are rescaled only past 2^8
-// TMEM columns: S of tile t at 128 t.  d = 128: O at 256 + 128 t, and P over the S it was made from
-// (64 columns of 16-bit pairs).  d = 64: O at 256 + 64 t, and P in columns of its own at 384 + 64 t.
-template <int D>
-struct Cols {
-  static constexpr bool kOwnP = D == 64;
-  static __device__ __forceinline__ uint32_t S(int t) { return 128u * t; }
-  static __device__ __forceinline__ uint32_t P(int t) { return kOwnP ? 384u + 64u * t : 128u * t; }
-  static __device__ __forceinline__ uint32_t O(int t) { return 256u + (uint32_t)D * t; }
-};
+// TMEM columns: the two S buffers of tile t at 128 t and 128 t + 64 (P as 16-bit pairs over the first
+// 32 columns of its S), O at 256 + 128 t.
+__device__ __forceinline__ uint32_t col_s(int t, uint32_t buf) { return 128u * t + 64u * buf; }
+__device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
 
 template <int D, bool KV8>
 struct XSmem {
@@ -76,29 +62,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-template <int N>
-__device__ __forceinline__ void give_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void take_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// A row's 128 scores; those behind the last key (whatever they are) as -inf.
-__device__ __forceinline__ void load_scores(uint32_t taddr, float (&x)[128], int valid) {
-  uint32_t u[4][32];
+// A row's 64 scores; those behind the last key (whatever they are) as -inf.
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&x)[64], int valid) {
+  uint32_t u0[32], u1[32];
+  tmem_ld32(taddr, u0);
+  tmem_ld32(taddr + 32, u1);
+  tmem_ld_wait(u0);
+  tmem_ld_wait(u1);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) tmem_ld32(taddr + 32 * q, u[q]);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    tmem_ld_wait(u[q]);
-#pragma unroll
-    for (int c = 0; c < 32; ++c) x[32 * q + c] = __uint_as_float(u[q][c]);
+  for (int c = 0; c < 32; ++c) {
+    x[c] = __uint_as_float(u0[c]);
+    x[c + 32] = __uint_as_float(u1[c]);
   }
-  if (valid < 128) {
+  if (valid < 64) {
 #pragma unroll
-    for (int c = 0; c < 128; ++c) x[c] = c < valid ? x[c] : -INFINITY;
+    for (int c = 0; c < 64; ++c) x[c] = c < valid ? x[c] : -INFINITY;
   }
 }
 
@@ -109,16 +87,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-template <int FROM>
-__device__ __forceinline__ float max64(const float (&x)[128]) {
+__device__ __forceinline__ float max64(const float (&x)[64]) {
   float m[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) m[c] = x[FROM + c];
+  for (int c = 0; c < 4; ++c) m[c] = x[c];
 #pragma unroll
   for (int c = 4; c < 60; c += 8)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], x[FROM + c + i], x[FROM + c + 4 + i]);
-  return max3(max3(m[0], x[FROM + 60], x[FROM + 61]), max3(m[1], x[FROM + 62], x[FROM + 63]), fmaxf(m[2], m[3]));
+    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], x[c + i], x[c + 4 + i]);
+  return max3(max3(m[0], x[60], x[61]), max3(m[1], x[62], x[63]), fmaxf(m[2], m[3]));
 }
 
 // Two fp32 operations in one instruction (the results are those of two single ones).
@@ -139,17 +116,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return y;
 }
 
-// p = exp2(x * mul + add) of 32 scores as 16-bit pairs, their sum (before rounding) onto l.
-template <bool F16, int FROM>
-__device__ __forceinline__ void exp32(const float (&x)[128], float mul, float add, uint32_t* pk, float2 (&l)[2]) {
+// p = exp2(x * mul + add) as 16-bit pairs; returns their sum (before rounding).
+template <bool F16>
+__device__ __forceinline__ float exp64(const float (&x)[64], float mul, float add, uint32_t (&pk)[32]) {
   const float2 mul2{mul, mul}, addv{add, add};
+  float2 l[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const float2 y = fma2(make_float2(x[FROM + 2 * c], x[FROM + 2 * c + 1]), mul2, addv);
+  for (int c = 0; c < 32; ++c) {
+    const float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), mul2, addv);
     const float2 p{ex2(y.x), ex2(y.y)};
     l[c & 1] = add2(l[c & 1], p);
     pk[c] = F16 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
   }
+  const float2 s = add2(l[0], l[1]);
+  return s.x + s.y;
 }
 
 // 32 channels of a row, rounded to the call's type.
@@ -178,17 +158,14 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SA2_P8(0), SA2_P8(8)::"memory");
 }
 
-// N k-steps from K0 on, as far as they are below `steps`, of O (+)= P V: A = P in TMEM (16 keys in 8
-// columns), B = V, 16 rows per k-step.
-template <int K0, int N>
+// O (+)= P V over up to 64 keys: A = P in TMEM (16 keys in 8 columns), B = V, 16 rows per k-step.
 __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, int steps, bool fresh) {
-  if (steps >= K0 + N) {
-    umma_ts(o, p + K0 * 8, v + (uint64_t)(K0 * 128), idesc, fresh ? 0u : 1u);
+  umma_ts(o, p, v, idesc, fresh ? 0u : 1u);
+  if (steps == 4) {
 #pragma unroll
-    for (int kk = 1; kk < N; ++kk) umma_ts(o, p + (K0 + kk) * 8, v + (uint64_t)((K0 + kk) * 128), idesc, 1u);
+    for (int kk = 1; kk < 4; ++kk) umma_ts(o, p + kk * 8, v + (uint64_t)(kk * 128), idesc, 1u);
   } else {
-    for (int kk = K0; kk < steps; ++kk)
-      umma_ts(o, p + kk * 8, v + (uint64_t)(kk * 128), idesc, (fresh && kk == 0) ? 0u : 1u);
+    for (int kk = 1; kk < steps; ++kk) umma_ts(o, p + kk * 8, v + (uint64_t)(kk * 128), idesc, 1u);
   }
 }
 
@@ -206,7 +183,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                      FwdPlan plan, CacheRef cache,
                      CrossFwdArgs a) {
   using L = XSmem<D, KV8>;
-  using C = Cols<D>;
   constexpr int kStages = L::kStages;
   constexpr bool kMmaF16 = KV8 || F16;  // the cache's products run in fp16
   // how far (log2) a block's maximum may lead the reference before P leaves its type's range
@@ -219,10 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_empty = [&](int st) { return smem_u32(&bars[8 + st]); };   // ... and read by its MMAs
   auto bar_qfull = [&](int t) { return smem_u32(&bars[16 + t]); };    // Q of tile t in shared memory
   auto bar_qempty = [&](int t) { return smem_u32(&bars[18 + t]); };   // ... and read (by its last S; cache: and its row scales)
-  auto bar_s = [&](int t) { return smem_u32(&bars[20 + t]); };        // S_t in TMEM
-  auto bar_pb = [&](int t) { return smem_u32(&bars[22 + t]); };       // P of keys 96..127 written
-  auto bar_pa = [&](int t) { return smem_u32(&bars[24 + t]); };       // P of keys 0..95 written
-  auto bar_pv = [&](int t) { return smem_u32(&bars[26 + t]); };       // P_t V completed
+  auto bar_s = [&](int t, uint32_t u) { return smem_u32(&bars[20 + 2 * t + u]); };   // S buffer u of tile t in TMEM
+  auto bar_p = [&](int t, uint32_t u) { return smem_u32(&bars[24 + 2 * t + u]); };   // P written over it
+  auto bar_pv = [&](int t, uint32_t u) { return smem_u32(&bars[48 + 2 * t + u]); };  // P V from it completed
   auto bar_o = [&](int t) { return smem_u32(&bars[28 + t]); };        // O_t of the piece complete
   auto bar_ofree = [&](int t) { return smem_u32(&bars[30 + t]); };    // ... and read out
   auto bar_l = [&](int t) { return smem_u32(&bars[32 + t]); };        // 1 / l of the piece written
@@ -230,9 +205,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_st = smem_u32(&bars[38]), bar_stfree = smem_u32(&bars[39]);  // O tile staged / copied out
   auto bar_rfull = [&](int i) { return smem_u32(&bars[40 + i]); };    // 8-bit block landed
   auto bar_rempty = [&](int i) { return smem_u32(&bars[44 + i]); };   // ... and converted
-  auto bar_sfree = [&](int t) { return smem_u32(&bars[36 + t]); };    // S_t read out (d = 64)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 448);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 456);
   float* row_s = reinterpret_cast<float*>(smem + L::kOffRow);
   const WaitCtl wc{abort_flag, s.wait_ns};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -246,15 +220,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_qfull(t), KV8 ? 128 : 1);
       mbar_init(bar_qempty(t), KV8 ? 129 : 1);
-      mbar_init(bar_s(t), 1);
-      mbar_init(bar_pb(t), 128);
-      mbar_init(bar_pa(t), 128);
-      mbar_init(bar_pv(t), 1);
+      for (uint32_t u = 0; u < 2; ++u) {
+        mbar_init(bar_s(t, u), 1);
+        mbar_init(bar_p(t, u), 128);
+        mbar_init(bar_pv(t, u), 1);
+      }
       mbar_init(bar_o(t), 1);
       mbar_init(bar_ofree(t), 128);
       mbar_init(bar_l(t), 128);
       mbar_init(bar_drain(t), 1);
-      mbar_init(bar_sfree(t), 128);
     }
     for (int i = 0; i < L::kRawStages; ++i) {
       mbar_init(bar_rfull(i), 1);
@@ -281,7 +255,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0 && !KV8) {
     // ------------------------------------------------------------------ TMA producer
-    give_registers<Regs<KV8>::kIssue>();
     PieceIter it(s, plan, a.kv_len);  // (whole warps)
     if (lane == 0) {
       tma_prefetch_map(&mq);
@@ -329,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 0) {
     // ---------------------------------------------------- TMA producer of the 8-bit blocks
-    give_registers<Regs<KV8>::kIssue>();
     PieceIter it(s, plan, a.kv_len);  // (whole warps)
     if (lane == 0) {
       tma_prefetch_map(&mk);
@@ -354,14 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------------ MMA issuer of tile t
-    give_registers<Regs<KV8>::kIssue>();
     PieceIter it(s, plan, a.kv_len);
     constexpr uint32_t idO = idesc_f32acc(128, D, false, true, !kMmaF16);
     const int t = warp - 1;
-    const uint32_t ts = tmem + C::S(t), tpp = tmem + C::P(t), to = tmem + C::O(t);
     const uint64_t qd = smem_desc(sbase + t * L::kTile, 16, 1024);
     bool ok = true;
-    uint32_t r = 0, c = 0, pc = 0;  // ring loads of earlier pieces; blocks and pieces done
+    uint32_t r = 0, c = 0, pc = 0;  // ring loads of earlier pieces; half blocks and pieces done
     Piece x;
     while (ok && it.next(x)) {
       if (!active(x, t)) {  // the stages are free as far as this tile goes
@@ -371,84 +341,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      auto steps_of = [&](int j) { return (min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock) + 15) >> 4; };
-      // S_t(j).  It overwrites the columns of P_t(j-1) (d = 128) or those of S_t(j-1) (d = 64).
-      auto issue_s = [&](int j) {
-        const uint32_t rk = r + 2 * j, cj = c + j;
+      const int keys = min(x.nb * kKeyBlock, x.keys - x.k0 * kKeyBlock);
+      const int halves = (keys + 63) >> 6;
+      // S of half block i, into buffer (c + i) & 1, whose P V two half blocks ago has completed
+      auto issue_s = [&](int i) {
+        const uint32_t rk = r + (i & ~1), ci = c + i, u = ci & 1;
         const int ks = rk % kStages;
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(bar_full(ks), (rk / kStages) & 1, wc) &&
-                            (j > 0 || mbar_wait(bar_qfull(t), pc & 1, wc)) &&
-                            (cj == 0 || mbar_wait(C::kOwnP ? bar_sfree(t) : bar_pv(t), (cj - 1) & 1, wc))))
+        const bool last = i + 1 == halves;
+        if (!__all_sync(0xffffffffu, ((i & 1) || mbar_wait(bar_full(ks), (rk / kStages) & 1, wc)) &&
+                                         (i > 0 || mbar_wait(bar_qfull(t), pc & 1, wc)) &&
+                                         (ci < 2 || mbar_wait(bar_pv(t, u), ((ci >> 1) - 1) & 1, wc))))
           return false;
         tc_fence_after();
-        const uint32_t idS = idesc_f32acc(128, steps_of(j) * 16, false, false, !kMmaF16);
-        const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile, 16, 1024);
+        const uint32_t idS = idesc_f32acc(128, min(64, (keys - 64 * i + 15) & ~15), false, false, !kMmaF16);
+        const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile + (i & 1) * 8192, 16, 1024);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(ts, qd + kmajor_kstep(kk, 128), kd + kmajor_kstep(kk, 128), idS, kk > 0 ? 1u : 0u);
-          umma_commit(bar_s(t));
-          umma_commit(bar_empty(ks));
-          if (j + 1 == x.nb) umma_commit(bar_qempty(t));
+            umma_ss(tmem + col_s(t, u), qd + kmajor_kstep(kk, 128), kd + kmajor_kstep(kk, 128), idS, kk > 0 ? 1u : 0u);
+          umma_commit(bar_s(t, u));
+          if ((i & 1) || last) umma_commit(bar_empty(ks));
+          if (last) umma_commit(bar_qempty(t));
         }
         __syncwarp();
         return true;
       };
-      // d = 128: keep the tiles half a period apart, so that one's products run beside the other's
-      // softmax.  Left alone they settle anywhere, also in step, where the tensor cores wait for
-      // both (5000 cycles per block against 3300).  So tile 1 begins a piece when tile 0 has its
-      // first P, or after kStaggerCycles: it is a hint, and nothing depends on it.
-      if (!C::kOwnP && t == 1 && x.nb > 0) {
-        const long long z = clock64();
-        while (clock64() - z < kStaggerCycles && !mbar_test(bar_pa(0), c & 1)) {
-        }
-      }
-      if (x.nb > 0) ok = issue_s(0);
-      for (int j = 0; ok && j < x.nb; ++j) {
-        if (C::kOwnP && j + 1 < x.nb) {
-          ok = issue_s(j + 1);
+      if (halves > 0) ok = issue_s(0);
+      for (int i = 0; ok && i < halves; ++i) {
+        if (i + 1 < halves) {
+          ok = issue_s(i + 1);
           if (!ok) break;
         }
-        const uint32_t rv = r + 2 * j + 1, cj = c + j;
-        const int vs = rv % kStages, steps = steps_of(j);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(vs), (rv / kStages) & 1, wc));
+        const uint32_t rv = r + (i & ~1) + 1, ci = c + i, u = ci & 1;
+        const int vs = rv % kStages, valid = min(64, keys - 64 * i), steps = (valid + 15) >> 4;
+        const bool last = i + 1 == halves;
+        ok = __all_sync(0xffffffffu, (i & 1) || mbar_wait(bar_full(vs), (rv / kStages) & 1, wc));
         if (!ok) break;
-        uint8_t* vt = smem + L::kOffKV + vs * L::kTile;
-        const int rows = 16 * steps - (x.keys - (x.k0 + j) * kKeyBlock);
+        const int rows = 16 * steps - valid;
         if (!KV8 && rows > 0) {
-          // the last `rows` rows of V (both issuers write the same zeros): a row is 128 bytes in each
-          // panel
+          // `rows` rows of V behind the last key (both issuers write the same zeros): a row is 128 bytes
+          // in each panel
+          uint8_t* vt = smem + L::kOffKV + vs * L::kTile + (i & 1) * 8192;
           const int nz = rows * 8 * L::kPanels;
-          for (int i = lane; i < nz; i += 32) {
-            const int row = 16 * steps - rows + (i >> 3) % rows, pn = (i >> 3) / rows;
-            *reinterpret_cast<uint4*>(vt + pn * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          for (int q = lane; q < nz; q += 32) {
+            const int row = valid + (q >> 3) % rows, pn = (q >> 3) / rows;
+            *reinterpret_cast<uint4*>(vt + pn * 16384 + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
           __syncwarp();
         }
-        const uint64_t vd = smem_desc(sbase + L::kOffKV + vs * L::kTile, 16384, 1024);
-        ok = __all_sync(0xffffffffu, (j > 0 || pc == 0 || mbar_wait(bar_ofree(t), (pc - 1) & 1, wc)) &&
-                                         mbar_wait(bar_pa(t), cj & 1, wc));
+        ok = __all_sync(0xffffffffu, (i > 0 || pc == 0 || mbar_wait(bar_ofree(t), (pc - 1) & 1, wc)) &&
+                                         mbar_wait(bar_p(t, u), (ci >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) issue_pv<0, 6>(to, tpp, vd, idO, steps, j == 0);
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_pb(t), cj & 1, wc));
-        if (!ok) break;
-        tc_fence_after();
+        const uint64_t vd = smem_desc(sbase + L::kOffKV + vs * L::kTile + (i & 1) * 8192, 16384, 1024);
         if (elect_one()) {
-          issue_pv<6, 2>(to, tpp, vd, idO, steps, false);
-          umma_commit(bar_pv(t));
-          umma_commit(bar_empty(vs));
-          if (j + 1 == x.nb) umma_commit(bar_o(t));
+          issue_pv(tmem + col_o(t), tmem + col_s(t, u), vd, idO, steps, i == 0);
+          umma_commit(bar_pv(t, u));
+          if ((i & 1) || last) umma_commit(bar_empty(vs));
+          if (last) umma_commit(bar_o(t));
         }
         __syncwarp();
-        if (!C::kOwnP && j + 1 < x.nb) ok = issue_s(j + 1);
       }
       if (x.nb > 0) ++pc;
       r += 2 * x.nb;
-      c += x.nb;
+      c += halves;
     }
     // no MMA may still run when TMEM is released, on the abort path too
     if (elect_one()) umma_commit(bar_drain(t));
@@ -456,13 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_drain(bar_drain(t), 0, abort_flag);
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ softmax rows
-    take_registers<Regs<KV8>::kSoftmax>();
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
     PieceIter it(s, plan, a.kv_len);
     const int t = (warp - 8) >> 2;
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t ts = trow + C::S(t), tpp = trow + C::P(t), to = trow + C::O(t);
+    const uint32_t to = trow + col_o(t);
     const int tok_r = r / s.G, g = r - tok_r * s.G;
     bool ok = true;
     uint32_t c = 0, pc = 0;
@@ -486,20 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // cache: scores are q8 scale * k8 scale * (q . k) and V's scale enters as an exponent
       float qscale = a.scale_log2;
       const float *ksp = nullptr, *vsp = nullptr;
-      float nks[2], nvs[2];  // of the next block's halves, loaded one block ahead
-      auto load_scales = [&](int kb) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool in = kb * kKeyBlock + 64 * i < x.keys;
-          nks[i] = in ? ksp[2 * kb + i] : 1.f;
-          nvs[i] = in ? vsp[2 * kb + i] : 1.f;
-        }
-      };
+      float nks = 1.f, nvs = 1.f;  // of the next half block, loaded one ahead
       if constexpr (KV8) {
         const int64_t off = ((int64_t)x.b * s.Hkv + x.hk) * cache.nsb;
         ksp = cache.ks + off;
         vsp = cache.vs + off;
-        load_scales(x.k0);
+        nks = ksp[2 * x.k0];
+        nvs = vsp[2 * x.k0];
         if (!__all_sync(0xffffffffu, mbar_wait(bar_qfull(t), pc & 1, wc))) {
           ok = false;
           break;
@@ -508,7 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar_qempty(t));
       }
       float m_used = 0.f, m_run = 0.f, l = 0.f;  // reference of the exponentials, largest so far, sum
+      // O and l to another reference.  O holds the half blocks before this one once their P V has
+      // completed: the last one's, from the other buffer, is waited for.
       auto rescale = [&](float m_new) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_pv(t, (c & 1) ^ 1), ((c - 1) >> 1) & 1, wc))) return false;
+        tc_fence_after();
         const float alpha = ex2(m_used - m_new);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 16) {
@@ -522,70 +475,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         l *= alpha;
         m_used = m_new;
+        return true;
       };
-      for (int j = 0; j < x.nb; ++j, ++c) {
-        const int valid = min(kKeyBlock, x.keys - (x.k0 + j) * kKeyBlock);
-        float mul_a = qscale, mul_b = qscale, ev_a = 0.f, ev_b = 0.f;
+      const int keys = min(x.nb * kKeyBlock, x.keys - x.k0 * kKeyBlock);
+      for (int i = 0; 64 * i < keys; ++i, ++c) {
+        const uint32_t u = c & 1, ts = trow + col_s(t, u);
+        const int valid = keys - 64 * i;
+        float mul = qscale, ev = 0.f;
         if constexpr (KV8) {
-          mul_a *= nks[0];
-          mul_b *= nks[1];
-          ev_a = (float)((int)(__float_as_uint(nvs[0]) >> 23) - 127);
-          ev_b = (float)((int)(__float_as_uint(nvs[1]) >> 23) - 127);
-          if (j + 1 < x.nb) load_scales(x.k0 + j + 1);
+          mul *= nks;
+          ev = (float)((int)(__float_as_uint(nvs) >> 23) - 127);
+          if (valid > 64) {
+            nks = ksp[2 * x.k0 + i + 1];
+            nvs = vsp[2 * x.k0 + i + 1];
+          }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_s(t), c & 1, wc))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_s(t, u), (c >> 1) & 1, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float y[128];
+        float y[64];
         load_scores(ts, y, valid);
-        const float mx = fmaxf(fmaf(max64<0>(y), mul_a, ev_a), fmaf(max64<64>(y), mul_b, ev_b));
-        // S_t(j) was issued after P_t V(j-1) completed (d = 64: that is waited for here), so O holds
-        // blocks 0 .. j-1 and P's columns are free
-        if (C::kOwnP && c > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(bar_pv(t), (c - 1) & 1, wc))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-        }
-        // The exponentials are taken against a maximum of the blocks before this one, so that they need
-        // not wait for this one's: the first block uses its own, then O and l follow when the maximum
-        // has grown past 2^8.  Only where P would leave its type's range does a block's own maximum
-        // come first (the loop below runs twice).
-        if (j == 0)
+        const float mx = fmaf(max64(y), mul, ev);
+        // The exponentials are taken against a maximum of the half blocks before this one, so that they
+        // need not wait for this one's: the first uses its own, then O and l follow when the maximum
+        // has grown past 2^8.  Only where P would leave its type's range does a half block's own
+        // maximum come first (the loop below runs twice).
+        if (i == 0)
           m_used = mx;
         else if (__any_sync(0xffffffffu, m_run > m_used + kRescaleThreshold))
-          rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
-        m_run = j == 0 ? mx : fmaxf(m_run, mx);
-        uint32_t pk[32], pk2[16];
-        float2 la[2], lb[2];
+          ok = rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
+        m_run = i == 0 ? mx : fmaxf(m_run, mx);
+        uint32_t pk[32];
+        float sum;
         for (;;) {
-          la[0] = la[1] = lb[0] = lb[1] = make_float2(0.f, 0.f);
-          exp32<kMmaF16, 0>(y, mul_a, ev_a - m_used, pk, la);
-          exp32<kMmaF16, 32>(y, mul_a, ev_a - m_used, pk + 16, la);
-          exp32<kMmaF16, 64>(y, mul_b, ev_b - m_used, pk2, lb);
-          if (!__any_sync(0xffffffffu, mx > m_used + kMaxLead)) break;
-          rescale(fmaxf(mx, m_used));
+          sum = exp64<kMmaF16>(y, mul, ev - m_used, pk);
+          if (!ok || !__any_sync(0xffffffffu, mx > m_used + kMaxLead)) break;
+          ok = rescale(fmaxf(mx, m_used));
           load_scores(ts, y, valid);  // (again, so that the usual path need not keep them)
         }
-        if constexpr (C::kOwnP) {
-          tc_fence_before();
-          mbar_arrive(bar_sfree(t));
-        }
-        tmem_st32(tpp, pk);
-        tmem_st16(tpp + 32, pk2);
+        if (!ok) break;
+        tmem_st32(ts, pk);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_pa(t));
-        exp32<kMmaF16, 96>(y, mul_b, ev_b - m_used, pk2, lb);
-        tmem_st16(tpp + 48, pk2);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar_pb(t));
-        const float2 sa = add2(la[0], la[1]), sb = add2(lb[0], lb[1]);
-        l += KV8 ? (sa.x + sa.y) * ex2(-ev_a) + (sb.x + sb.y) * ex2(-ev_b) : (sa.x + sa.y) + (sb.x + sb.y);
+        mbar_arrive(bar_p(t, u));
+        l += KV8 ? sum * ex2(-ev) : sum;
       }
       if (!ok) break;
       const int64_t slot_row = ((int64_t)blockIdx.x + x.seg) * 256 + t * 128 + r;
@@ -639,7 +574,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A tile goes out through shared memory with one TMA store: stored row by row, 16 bytes per
     // thread, it kept the load/store unit busy for 3000 cycles, which the softmax threads' tcgen05.ld
     // waited for (M = 512: a fifth of the time).
-    give_registers<Regs<KV8>::kEpilogue>();
     PieceIter it(s, plan, a.kv_len);
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -671,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t u[32];
-          tmem_ld32(trow + C::O(t) + c0, u);
+          tmem_ld32(trow + col_o(t) + c0, u);
           tmem_ld_wait(u);
           if (c0 + 32 >= D) {
             tc_fence_before();
@@ -722,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4 && KV8) {
     // --------------------------------------------------- converters: Q, K, V to fp16
-    give_registers<Regs<KV8>::kEpilogue>();
     PieceIter it(s, plan, a.kv_len);
     constexpr int kChunks = D / 16;       // 16-byte chunks of an 8-bit row
     constexpr int kRows = 128 / kChunks;  // rows per pass of the 128 threads
@@ -809,8 +742,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar_rempty(rs));
       }
     }
-  } else {
-    give_registers<Regs<KV8>::kIssue>();  // the rest of the issuers' warpgroup
   }
   tc_fence_before();
   __syncthreads();
@@ -888,12 +819,6 @@ cudaError_t launch_t(const CrossShape& s, const FwdPlan& p, const CUtensorMap& m
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_smem(kern, XSmem<D, KV8>::kBytes, allowed);
   if (e != cudaSuccess) return e;
-  // the roles' registers add up to 128 a thread: with fewer at launch they would wait for ever
-  static const int regs = [&] {
-    cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
-  }();
-  if (regs != 128) return cudaErrorInvalidConfiguration;
   prof_start(st, kAttnFwd);
   kern<<<(unsigned)p.grid, kThreads, XSmem<D, KV8>::kBytes, st>>>(mq, mk, mv, mo, s, p, c, a);
   prof_stop(st, kAttnFwd);
