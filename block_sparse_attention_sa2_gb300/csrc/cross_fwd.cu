@@ -775,27 +775,41 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
     if (t >= plan.tp || tile >= plan.tiles) return;
     const int tok_r = r / s.G, g = r - tok_r * s.G, n = tile * plan.nb + tok_r, h = hk * s.G + g;
     if (tok_r >= plan.nb || n >= s.N) continue;
-    float m = -INFINITY;
-    bool nan = false;
-    for (int cta = c0 + lane; cta <= c1; cta += 32) {
-      const float v = a.part_l[((int64_t)cta + seg) * plan.rows + rr];
-      nan |= v != v;
-      m = fmaxf(m, v);
-    }
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (__any_sync(0xffffffffu, nan)) m = NAN;
-    float acc[kPer] = {}, l = 0.f;
-    for (int cta = c0; cta <= c1; ++cta) {
-      const int64_t row = ((int64_t)cta + seg) * plan.rows + rr;
-      const float w = ex2(a.part_l[row] - m);
-      l += w;
-      float v[kPer];
-      if constexpr (kPer == 4)
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + row * D + lane * 4);
-      else
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + row * D + lane * 2);
+    // lane i has part c0 + i's sum; 32 parts at a time (more are rare), eight of their rows in flight
+    float m = -INFINITY, acc[kPer] = {}, l = 0.f;
+    for (int base = c0; base <= c1; base += 32) {
+      const int n32 = min(32, c1 + 1 - base);
+      const float mine = lane < n32 ? a.part_l[((int64_t)base + lane + seg) * plan.rows + rr] : -INFINITY;
+      float mx = mine;
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (__any_sync(0xffffffffu, mine != mine)) mx = NAN;
+      const float m_new = m != m ? m : (mx > m || mx != mx ? mx : m);
+      const float keep = base == c0 ? 0.f : ex2(m - m_new);
+      m = m_new;
+      l *= keep;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+      for (int q = 0; q < kPer; ++q) acc[q] *= keep;
+      const float wl = lane < n32 ? ex2(mine - m) : 0.f;
+      for (int k = 0; k < n32; k += 8) {
+        float v[8][kPer];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float* src = a.part_o + (((int64_t)base + min(k + u, n32 - 1) + seg) * plan.rows + rr) * D;
+          if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src + lane * 4);
+          else
+            *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src + lane * 2);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float w = __shfl_sync(0xffffffffu, wl, (k + u) & 31);
+          if (k + u < n32) {
+            l += w;
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) acc[q] = fmaf(w, v[u][q], acc[q]);
+          }
+        }
+      }
     }
     const float inv = nk > 0 ? 1.f / l : 0.f;
     uint32_t w[kPer / 2];
