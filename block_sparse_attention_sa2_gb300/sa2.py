@@ -1,4 +1,5 @@
-"""Thin Python binding of libsa2 (include/sa2.h): argument marshalling only.
+"""Thin Python binding of libsa2 (include/sa2.h): argument marshalling only, through ctypes and, for the
+cross- and cache-attention calls, the extension module ``_cross``.
 
 Every step of the hot path runs in the library's CUDA kernels; this module allocates the
 output tensors and workspaces with PyTorch, passes raw device pointers and the current CUDA
@@ -77,22 +78,6 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa2_vd_loss_workspace_size.argtypes = [S]
     lib.sa2_vd_loss.restype = ctypes.c_int
     lib.sa2_vd_loss.argtypes = [S, P, P, P, P, P, P, P, Z, P]
-    X = T = C = P  # sa2_cross_shape, sa2_tensor, sa2_cache8 as packed bytes
-    I = ctypes.c_int32
-    lib.sa2_cross_fwd_workspace_size.restype = Z
-    lib.sa2_cross_fwd_workspace_size.argtypes = [X]
-    lib.sa2_cross_attn_fwd.restype = ctypes.c_int
-    lib.sa2_cross_attn_fwd.argtypes = [X, T, T, T, P, F, T, P, P, Z, P]
-    lib.sa2_cross_bwd_workspace_size.restype = Z
-    lib.sa2_cross_bwd_workspace_size.argtypes = [X]
-    lib.sa2_cross_attn_bwd.restype = ctypes.c_int
-    lib.sa2_cross_attn_bwd.argtypes = [X, T, T, T, T, P, T, P, F, T, T, T, P, Z, P]
-    lib.sa2_cache8_append.restype = ctypes.c_int
-    lib.sa2_cache8_append.argtypes = [C, I, I, T, T, P, P, P]
-    lib.sa2_cache8_read.restype = ctypes.c_int
-    lib.sa2_cache8_read.argtypes = [C, I, I, T, T, P, P]
-    lib.sa2_cache8_attn.restype = ctypes.c_int
-    lib.sa2_cache8_attn.argtypes = [X, T, C, P, F, T, P, P, Z, P]
     lib.sa2_get_device_status.restype = ctypes.c_int
     lib.sa2_get_device_status.argtypes = [P]
     lib.sa2_debug_set_wait_limit.restype = None
@@ -257,90 +242,24 @@ def vd_loss(o_s: torch.Tensor, o_t: torch.Tensor, o_s_lo: Optional[torch.Tensor]
 
 # --------------------------------------------------- attention to keys of another length
 #
-# The structs of these calls are packed with ``struct`` (a few tenths of a microsecond each): a call
-# over a few keys takes the GPU less time than ctypes structures take the host.
+# Argument checks, allocation and the C calls are in the extension module (csrc/cross_binding.cpp).
 
-_DTYPE = {torch.bfloat16: SA2_BF16, torch.float16: SA2_FP16}
-_pack_tensor = struct.Struct("Pqqq").pack  # sa2_tensor
-_pack_cross = struct.Struct("8i").pack  # sa2_cross_shape
-_pack_cache = struct.Struct("PPPPqqqiiii").pack  # sa2_cache8
+_binding = None
 
 
-def _tensor(x: torch.Tensor, name: str, shape, dtype, device) -> bytes:
-    """sa2_tensor of a token tensor of this shape, type and device."""
-    if x.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(x.shape)}")
-    if x.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.device != device:
-        raise ValueError(f"{name} must be on {device}, got {x.device}")
-    sb, sh, sn, sd = x.stride()
-    if sd != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _pack_tensor(x.data_ptr(), sb, sh, sn)
+def load_binding():
+    """The extension module of the cross- and cache-attention calls; raises if it is not built."""
+    global _binding
+    if _binding is None:
+        load_library()  # the module is linked to it
+        from . import _cross
+        _cross.set_error(Sa2Error)
+        _binding = _cross
+    return _binding
 
 
-def _int32(x: Optional[torch.Tensor], name: str, B: int, device) -> Optional[int]:
-    if x is None:
-        return None
-    if x.dtype != torch.int32 or x.shape != (B,) or not x.is_contiguous() or x.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape [{B}] on {device}")
-    return x.data_ptr()
-
-
-def _float32(x: torch.Tensor, name: str, shape, device) -> int:
-    if x.dtype != torch.float32 or x.shape != shape or not x.is_contiguous() or x.device != device:
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {list(shape)} on {device}")
-    return x.data_ptr()
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor that stays allocated until the work on ``stream`` is done with it."""
-    x = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        x.record_stream(stream)
-    return x
-
-
-def _empty_like(y: torch.Tensor, stream) -> torch.Tensor:
-    x = torch.empty_like(y)
-    if stream is not None:
-        x.record_stream(stream)
-    return x
-
-
-def _workspace_of(ws: Optional[torch.Tensor], nbytes: int, device, stream):
-    if ws is None:
-        if not nbytes:
-            return None, 0
-        ws = _empty(nbytes, torch.uint8, device, stream)
-    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
-    return ws.data_ptr(), ws.numel()
-
-
-def _on_other_device(device) -> bool:
-    """Whether the device that a call's tensors are on is not the current one."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors must be on a CUDA device, got {device}")
-    return device.index != torch.cuda.current_device()
-
-
-def _raw_stream(stream, device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-
-
-def _dtype_code(dtype) -> int:
-    code = _DTYPE.get(dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
-    return code
-
-
-def _dims(x: torch.Tensor, name: str):
-    if x.dim() != 4:
-        raise ValueError(f"{name}: token tensors are [B, H, N, d]")
-    return x.shape
+def _handle(stream) -> Optional[int]:
+    return None if stream is None else stream.cuda_stream
 
 
 def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Optional[torch.Tensor] = None,
@@ -351,49 +270,18 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Op
     H is a multiple of Hkv (query head h reads key head h // (H // Hkv)); bfloat16 or float16; each
     tensor with strides of its own.  ``kv_len`` ([B] int32 on the device): sequence b attends to its
     first kv_len[b] keys; without keys O = 0 and LSE = -inf.  LSE is float32 [B, H, N]."""
-    lib = load_library()
-    B, H, N, d = qs = _dims(q, "q")
-    _, Hkv, M, _ = _dims(k, "k")
-    dt, dev, kvs = q.dtype, q.device, (B, Hkv, M, d)
-    shp = _pack_cross(B, H, Hkv, N, M, d, _dtype_code(dt), 0)
-    if _on_other_device(dev):
-        with torch.cuda.device(dev):
-            return cross_attn_fwd(q, k, v, kv_len, scale, o, lse, ws, stream)
-    o = _empty_like(q, stream) if o is None else o
-    if lse is None:
-        lse = _empty((B, H, N), torch.float32, dev, stream)
-    w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(shp), dev, stream)
-    _check("sa2_cross_attn_fwd", lib.sa2_cross_attn_fwd(
-        shp, _tensor(q, "q", qs, dt, dev), _tensor(k, "k", kvs, dt, dev), _tensor(v, "v", kvs, dt, dev),
-        _int32(kv_len, "kv_len", B, dev), scale or 0.0, _tensor(o, "o", qs, dt, dev),
-        _float32(lse, "lse", (B, H, N), dev), w, wn, _raw_stream(stream, dev)))
-    return o, lse
+    return (_binding or load_binding()).cross_attn_fwd(q, k, v, kv_len, scale, o, lse, ws, _handle(stream))
 
 
 def cross_attn_bwd(q, k, v, o, lse, do, kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                    dq=None, dk=None, dv=None, ws: Optional[torch.Tensor] = None, stream=None):
     """sa2_cross_attn_bwd: gradients (dQ, dK, dV) of cross_attn_fwd (bfloat16), whose o and lse on the
     same q, k, v, kv_len and scale it takes; zero behind kv_len."""
-    lib = load_library()
-    B, H, N, d = qs = _dims(q, "q")
-    _, Hkv, M, _ = _dims(k, "k")
-    dt, dev, kvs = q.dtype, q.device, (B, Hkv, M, d)
-    shp = _pack_cross(B, H, Hkv, N, M, d, _dtype_code(dt), 0)
-    if _on_other_device(dev):
-        with torch.cuda.device(dev):
-            return cross_attn_bwd(q, k, v, o, lse, do, kv_len, scale, dq, dk, dv, ws, stream)
-    dq = _empty_like(q, stream) if dq is None else dq
-    dk = _empty_like(k, stream) if dk is None else dk
-    dv = _empty_like(v, stream) if dv is None else dv
-    w, wn = _workspace_of(ws, lib.sa2_cross_bwd_workspace_size(shp), dev, stream)
-    _check("sa2_cross_attn_bwd", lib.sa2_cross_attn_bwd(
-        shp, _tensor(q, "q", qs, dt, dev), _tensor(k, "k", kvs, dt, dev), _tensor(v, "v", kvs, dt, dev),
-        _tensor(o, "o", qs, dt, dev), _float32(lse, "lse", (B, H, N), dev), _tensor(do, "do", qs, dt, dev),
-        _int32(kv_len, "kv_len", B, dev), scale or 0.0, _tensor(dq, "dq", qs, dt, dev),
-        _tensor(dk, "dk", kvs, dt, dev), _tensor(dv, "dv", kvs, dt, dev), w, wn, _raw_stream(stream, dev)))
-    return dq, dk, dv
+    return (_binding or load_binding()).cross_attn_bwd(q, k, v, o, lse, do, kv_len, scale, dq, dk, dv, ws,
+                                                       _handle(stream))
 
 
+_pack_cache = struct.Struct("PPPPqqqiiii").pack  # sa2_cache8
 _CACHE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -403,20 +291,26 @@ class KvCache8:
     and block of 64 tokens.  The tensors are the cache's for good; the caller keeps the lengths."""
 
     BLOCK = 64
-    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_shape", "_struct")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_shape", "_device", "_struct")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
-        B, Hkv, C, d = self._shape = _dims(k, "the cache's k")
+        if k.dim() != 4:
+            raise ValueError("the cache's k and v are [B, Hkv, C, d] with the same strides, d contiguous")
+        B, Hkv, C, d = self._shape = tuple(k.shape)
         sb, sh, sn, sd = st = k.stride()
         dev = k.device
         if v.shape != k.shape or v.stride() != st or sd != 1:
             raise ValueError("the cache's k and v are [B, Hkv, C, d] with the same strides, d contiguous")
         if k.dtype not in _CACHE_DTYPES or v.dtype not in _CACHE_DTYPES or v.device != dev:
             raise ValueError("the cache's k and v are float8_e4m3fn (or uint8) on one device")
-        scales = (B, Hkv, -(-C // 64))
+        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (x.dtype != torch.float32 or x.shape != (B, Hkv, blocks(C, self.BLOCK)) or not x.is_contiguous()
+                    or x.device != dev):
+                raise ValueError(f"{name} must be a contiguous float32 tensor [B, Hkv, ceil(C / 64)] on {dev}")
+        self._device = -1 if dev.index is None else dev.index
         self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
-        self._struct = _pack_cache(k.data_ptr(), v.data_ptr(), _float32(k_scale, "k_scale", scales, dev),
-                                   _float32(v_scale, "v_scale", scales, dev), sb, sh, sn, B, Hkv, C, d)
+        self._struct = _pack_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), sb, sh, sn,
+                                   B, Hkv, C, d)
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
@@ -437,42 +331,16 @@ def cache8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, pos: torch.
                   n_new: Optional[torch.Tensor] = None, stream=None) -> None:
     """sa2_cache8_append: writes k, v [B, Hkv, n, d] (bfloat16 or float16) at positions pos[b] ..
     pos[b] + n - 1 (n_new[b] tokens of each sequence where given).  ``pos``, ``n_new``: [B] int32."""
-    lib = load_library()
-    c = cache._struct
-    B, Hkv, _, d = cache._shape
-    n, dt, dev = _dims(k, "k")[2], k.dtype, cache._k.device
-    code, shape = _dtype_code(dt), (B, Hkv, n, d)
-    if pos is None:
-        raise ValueError("pos is required")
-    if n == 0:
-        return
-    if _on_other_device(dev):
-        with torch.cuda.device(dev):
-            return cache8_append(cache, k, v, pos, n_new, stream)
-    _check("sa2_cache8_append", lib.sa2_cache8_append(
-        c, n, code, _tensor(k, "k", shape, dt, dev), _tensor(v, "v", shape, dt, dev), _int32(pos, "pos", B, dev),
-        _int32(n_new, "n_new", B, dev), _raw_stream(stream, dev)))
+    (_binding or load_binding()).cache8_append(cache._struct, cache._device, k, v, pos, n_new, _handle(stream))
 
 
 def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
                 v: Optional[torch.Tensor] = None, stream=None):
     """sa2_cache8_read: the values of tokens pos[b] .. pos[b] + n - 1 as (K, V) [B, Hkv, n, d]."""
-    lib = load_library()
-    c = cache._struct
-    B, Hkv, _, d = cache._shape
-    code, dev, shape = _dtype_code(dtype), cache._k.device, (B, Hkv, n, d)
-    if pos is None:
-        raise ValueError("pos is required")
-    if _on_other_device(dev):
-        with torch.cuda.device(dev):
-            return cache8_read(cache, pos, n, dtype, k, v, stream)
-    k = _empty(shape, dtype, dev, stream) if k is None else k
-    v = _empty(shape, dtype, dev, stream) if v is None else v
-    if n:
-        _check("sa2_cache8_read", lib.sa2_cache8_read(
-            c, n, code, _tensor(k, "k", shape, dtype, dev), _tensor(v, "v", shape, dtype, dev),
-            _int32(pos, "pos", B, dev), _raw_stream(stream, dev)))
-    return k, v
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
+    return (_binding or load_binding()).cache8_read(cache._struct, cache._device, pos, n, dtype is torch.float16, k, v,
+                                                    _handle(stream))
 
 
 def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: Optional[float] = None,
@@ -480,29 +348,8 @@ def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: O
                 ws: Optional[torch.Tensor] = None, stream=None):
     """sa2_cache8_attn: attention of q [B, H, N, d] to the first kv_len[b] tokens of the cache;
     returns (O, LSE) as cross_attn_fwd does."""
-    lib = load_library()
-    c = cache._struct
-    B, H, N, d = qs = _dims(q, "q")
-    cb, Hkv, C, cd = cache._shape
-    dt, dev = q.dtype, q.device
-    if (B, d) != (cb, cd):
-        raise ValueError(f"the cache holds B = {cb}, d = {cd}; q has B = {B}, d = {d}")
-    if kv_len is None:
-        raise ValueError("kv_len is required")
-    if cache._k.device != dev:
-        raise ValueError(f"the cache must be on {dev}, got {cache._k.device}")
-    shp = _pack_cross(B, H, Hkv, N, C, d, _dtype_code(dt), 0)
-    if _on_other_device(dev):
-        with torch.cuda.device(dev):
-            return cache8_attn(q, cache, kv_len, scale, o, lse, ws, stream)
-    o = _empty_like(q, stream) if o is None else o
-    if lse is None:
-        lse = _empty((B, H, N), torch.float32, dev, stream)
-    w, wn = _workspace_of(ws, lib.sa2_cross_fwd_workspace_size(shp), dev, stream)
-    _check("sa2_cache8_attn", lib.sa2_cache8_attn(
-        shp, _tensor(q, "q", qs, dt, dev), c, _int32(kv_len, "kv_len", B, dev), scale or 0.0,
-        _tensor(o, "o", qs, dt, dev), _float32(lse, "lse", (B, H, N), dev), w, wn, _raw_stream(stream, dev)))
-    return o, lse
+    return (_binding or load_binding()).cache8_attn(q, cache._struct, cache._device, kv_len, scale, o, lse, ws,
+                                                    _handle(stream))
 
 
 def device_status(stream=None) -> int:
