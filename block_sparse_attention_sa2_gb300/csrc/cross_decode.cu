@@ -132,6 +132,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
     };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) copy_step(i);
+    float nks = 1.f, nvs = 1.f;  // the next step's scales
+    auto load_scales = [&](int i) {
+      if (KV8 && i < steps) {  // (a step lies within one block of 64 tokens)
+        const int block = (key0 + (i * kWarps + warp) * T::kKeys) >> 6;
+        nks = __ldg(ksp + block);
+        nvs = __ldg(vsp + block);
+      }
+    };
+    load_scales(0);
 
     // Q's fragments: rows g and g + 8; of each, this thread's channels in the order of its K chunks
     uint32_t qf[kKS][4];
@@ -181,13 +190,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
       const uint8_t* vt = kt + kTileBytes;
       const int base = key0 + (i * kWarps + warp) * T::kKeys;
       float mul[2] = {row_scale[0], row_scale[1]}, ev = 0.f, unscale = 1.f;
-      if constexpr (KV8) {  // a step lies within one block of 64 tokens
-        const float ksc = ksp[base >> 6], vsc = vsp[base >> 6];
-        mul[0] *= ksc;
-        mul[1] *= ksc;
-        const int e = (int)(__float_as_uint(vsc) >> 23) - 127;
+      if constexpr (KV8) {
+        mul[0] *= nks;
+        mul[1] *= nks;
+        const int e = (int)(__float_as_uint(nvs) >> 23) - 127;
         ev = (float)e;
         unscale = __uint_as_float((uint32_t)(127 - e) << 23);
+        load_scales(i + 1);
       }
       // S: tile j has keys 8 j .. 8 j + 7; thread: rows g, g + 8, keys 8 j + 2 t, + 1
       float sc[kNT][4];
