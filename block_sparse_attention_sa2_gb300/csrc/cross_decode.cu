@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
   constexpr int kKS = D / 16;         // k-steps of S
   constexpr int kKC = T::kChunks / 4 > 0 ? T::kChunks / 4 : 1;  // K chunks per thread and key
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float warp_m[kWarps][kFewRows], warp_l[kWarps][kFewRows];
+  __shared__ float warp_m[kWarps][kFewRows], warp_l[kWarps][kFewRows], warp_r[kWarps][kFewRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
     }
 
     float o[kCT][4] = {};
-    float m_used[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
+    // reference of the exponentials; sum of exp2(s), relative to m_used, cache: to l_ref (see cross_fwd.cu)
+    float m_used[2] = {0.f, 0.f}, l[2] = {0.f, 0.f}, l_ref[2] = {-INFINITY, -INFINITY};
     for (int i = 0; i < steps; ++i) {
       copy_step(i + kStages - 1);
       copy_wait<kStages - 1>();
@@ -189,13 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
       const uint8_t* kt = ring + (i % kStages) * kStageBytes;
       const uint8_t* vt = kt + kTileBytes;
       const int base = key0 + (i * kWarps + warp) * T::kKeys;
-      float mul[2] = {row_scale[0], row_scale[1]}, ev = 0.f, unscale = 1.f;
+      float mul[2] = {row_scale[0], row_scale[1]}, ev = 0.f;
       if constexpr (KV8) {
         mul[0] *= nks;
         mul[1] *= nks;
-        const int e = (int)(__float_as_uint(nvs) >> 23) - 127;
-        ev = (float)e;
-        unscale = __uint_as_float((uint32_t)(127 - e) << 23);
+        ev = (float)((int)(__float_as_uint(nvs) >> 23) - 127);
         load_scales(i + 1);
       }
       // S: tile j has keys 8 j .. 8 j + 7; thread: rows g, g + 8, keys 8 j + 2 t, + 1
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
         for (int hf = 0; hf < 2; ++hf) {
           const float m = fmaxf(m_used[hf], mx[hf]);
           al[hf] = ex2(m_used[hf] - m);
-          l[hf] *= al[hf];
+          if constexpr (!KV8) l[hf] *= al[hf];
           m_used[hf] = m;
         }
 #pragma unroll
@@ -258,7 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
       // P in the layout of an A operand: 16 keys (tiles 2 k, 2 k + 1) per k-step
       uint32_t pf[kNT / 2][4];
       float ls[2] = {0.f, 0.f};
-      const float add[2] = {ev - m_used[0], ev - m_used[1]};
+      // cache: scores whose exponent is 2^-64 or less of the reference's are 0 in P, but count in the sum
+      const bool low[2] = {KV8 && mx[0] < m_used[0] - 64.f, KV8 && mx[1] < m_used[1] - 64.f};
+      const float ref[2] = {low[0] ? mx[0] : m_used[0], low[1] ? mx[1] : m_used[1]};
+      const float add[2] = {ev - ref[0], ev - ref[1]};
 #pragma unroll
       for (int j = 0; j < kNT; ++j) {
         float p[4];
@@ -270,8 +272,28 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
         pf[j >> 1][2 * (j & 1)] = kMmaF16 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]);
         pf[j >> 1][2 * (j & 1) + 1] = kMmaF16 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]);
       }
-      l[0] = fmaf(ls[0], unscale, l[0]);
-      l[1] = fmaf(ls[1], unscale, l[1]);
+      if constexpr (KV8) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const float y = ref[hf] - ev;
+          if (y > l_ref[hf] + 60.f) {  // (the first step too)
+            l[hf] *= ex2(l_ref[hf] - y);
+            l_ref[hf] = y;
+          }
+          l[hf] = fmaf(ls[hf], ex2(y - l_ref[hf]), l[hf]);
+        }
+        if (__any_sync(0xffffffffu, low[0] || low[1])) {
+#pragma unroll
+          for (int k = 0; k < kNT / 2; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) pf[k][q] = low[q & 1] ? 0u : pf[k][q];
+        }
+      } else {
+        l[0] += ls[0];
+        l[1] += ls[1];
+        l_ref[0] = m_used[0];
+        l_ref[1] = m_used[1];
+      }
       // O += P V: keys 16 k + 2 t, + 1 and 16 k + 8 + 2 t, + 1; channels of chunk g (+ 8 i)
 #pragma unroll
       for (int k = 0; k < kNT / 2; ++k) {
@@ -325,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
       if (t == 0) {
         warp_m[warp][g + 8 * hf] = steps > 0 ? m_used[hf] : -INFINITY;
         warp_l[warp][g + 8 * hf] = steps > 0 ? l[hf] : 0.f;
+        warp_r[warp][g + 8 * hf] = steps > 0 ? l_ref[hf] : -INFINITY;
       }
     }
     copy_wait<0>();
@@ -345,12 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
     __syncthreads();
     for (int i = tid; i < rows * (D / 2); i += kThreads) {
       const int r = i / (D / 2), ch = i % (D / 2) * 2;
-      float m = -INFINITY;
+      float m = -INFINITY, lr = -INFINITY;
       bool nan = false;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         nan |= warp_m[w][r] != warp_m[w][r];
         m = fmaxf(m, warp_m[w][r]);
+        lr = fmaxf(lr, warp_r[w][r]);
       }
       if (nan) m = NAN;
       float v0 = 0.f, v1 = 0.f, sum = 0.f;
@@ -361,10 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
         const float2 u = *reinterpret_cast<const float2*>(os + (w * kFewRows + r) * kPitch + ch);
         v0 = fmaf(f, u.x, v0);
         v1 = fmaf(f, u.y, v1);
-        sum = fmaf(f, warp_l[w][r], sum);
+        sum = fmaf(ex2(warp_r[w][r] - lr), warp_l[w][r], sum);
       }
-      const float inv = x.nb > 0 ? 1.f / sum : 0.f;
-      const float lse2 = x.nb > 0 ? m + __log2f(sum) : -INFINITY;
+      const float root = ex2(0.5f * (m - lr));  // 2^(m - lr) alone may leave fp32's range
+      const float inv = x.nb > 0 ? root / sum * root : 0.f;
+      const float lse2 = x.nb > 0 ? (nan ? m : lr) + __log2f(sum) : -INFINITY;
       const int n = r / s.G, h = x.hk * s.G + r - n * s.G;
       if (plan.split) {
         const int64_t row = ((int64_t)blockIdx.x + x.seg) * kFewRows + r;

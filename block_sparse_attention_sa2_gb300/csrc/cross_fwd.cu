@@ -456,7 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         qscale *= row_s[t * 128 + r];
         mbar_arrive(bar_qempty(t));
       }
-      float m_used = 0.f, m_run = 0.f, l = 0.f;  // reference of the exponentials, largest so far, sum
+      float m_used = 0.f, m_run = 0.f;  // reference of the exponentials, largest so far
+      // sum of exp2(s) relative to m_used; cache: to l_ref, since s + log2(V's scale), which m_used follows,
+      // can be any distance from s
+      float l = 0.f, l_ref = -INFINITY;
       // O and l to another reference.  O holds the half blocks before this one once their P V has
       // completed: the last one's, from the other buffer, is waited for.
       auto rescale = [&](float m_new) {
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(to + c0, o);
         }
         tmem_st_wait();
-        l *= alpha;
+        if constexpr (!KV8) l *= alpha;
         m_used = m_new;
         return true;
       };
@@ -508,10 +511,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
         m_run = i == 0 ? mx : fmaxf(m_run, mx);
         uint32_t pk[32];
-        float sum;
+        float sum, ref;
+        bool low;
         for (;;) {
-          sum = exp64<kMmaF16>(y, mul, ev - m_used, pk);
-          if (!ok || !__any_sync(0xffffffffu, mx > m_used + kMaxLead)) break;
+          // cache: scores whose exponent is 2^-64 or less of the reference's (small values beside large
+          // ones) are 0 in P, but count in the sum: relative to their own maximum
+          low = KV8 && mx < m_used - 64.f;
+          ref = low ? mx : m_used;
+          sum = exp64<kMmaF16>(y, mul, ev - ref, pk);
+          if (!ok || !__any_sync(0xffffffffu, low || mx > m_used + kMaxLead)) break;
+          if (!__any_sync(0xffffffffu, mx > m_used + kMaxLead)) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) pk[q] = low ? 0u : pk[q];
+            break;
+          }
           ok = rescale(fmaxf(mx, m_used));
           load_scores(ts, y, valid);  // (again, so that the usual path need not keep them)
         }
@@ -520,11 +533,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar_p(t, u));
-        l += KV8 ? sum * ex2(-ev) : sum;
+        if constexpr (KV8) {
+          const float x = ref - ev;
+          if (x > l_ref + 60.f) {  // (the first half block too)
+            l *= ex2(l_ref - x);
+            l_ref = x;
+          }
+          l = fmaf(sum, ex2(x - l_ref), l);
+        } else {
+          l += sum;
+        }
       }
       if (!ok) break;
       const int64_t slot_row = ((int64_t)blockIdx.x + x.seg) * 256 + t * 128 + r;
-      const float lse2 = m_used + __log2f(l);
+      const float lse2 = (KV8 ? l_ref : m_used) + __log2f(l);
       if (row_valid) {
         if (plan.split)
           a.part_l[slot_row] = lse2;
@@ -545,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const float inv_l = 1.f / l;
+        // 2^(m_used - l_ref) / l; the power alone may leave fp32's range, where l makes up for it
+        const float root = ex2(0.5f * (m_used - l_ref)), inv_l = root / l * root;
         uint16_t* op = static_cast<uint16_t*>(a.o.p) + x.b * a.o.sb + h * a.o.sh + n * a.o.sn;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
