@@ -13,7 +13,6 @@
 namespace sa2 {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -37,17 +36,14 @@ __device__ __forceinline__ void issue_ss(uint32_t d, uint64_t a, uint64_t b, uin
   for (int kk = 0; kk < D / 16; ++kk)
     umma_ss(d, a + kmajor_kstep(kk, 128), b + kmajor_kstep(kk, 128), idesc, kk > 0 ? 1u : 0u);
 }
-// D (+)= A B with A in TMEM, 16 rows of B per k-step; A's k-steps 0..3 lie at column 0, 4..7 at 64
-// (each over the half of the scores that it was made from).
+// D (+)= A B with A in TMEM, 16 rows of B per k-step; A's k-steps 2 i and 2 i + 1 lie in the first 16 of
+// the columns 32 i .. 32 i + 31 (over the scores that they were made from).
+__device__ __forceinline__ constexpr uint32_t a_kstep(int kk) { return 32u * (kk >> 1) + 8u * (kk & 1); }
 __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int steps, bool fresh) {
-  if (steps == 8) {
-    umma_ts(d, a, b, idesc, fresh ? 0u : 1u);
+  umma_ts(d, a, b, idesc, fresh ? 0u : 1u);
 #pragma unroll
-    for (int kk = 1; kk < 8; ++kk) umma_ts(d, a + kk * 8 + (kk >= 4 ? 32 : 0), b + (uint64_t)(kk * 128), idesc, 1u);
-  } else {
-    for (int kk = 0; kk < steps; ++kk)
-      umma_ts(d, a + kk * 8 + (kk >= 4 ? 32 : 0), b + (uint64_t)(kk * 128), idesc, (fresh && kk == 0) ? 0u : 1u);
-  }
+  for (int kk = 1; kk < 8; ++kk)
+    if (kk < steps) umma_ts(d, a + a_kstep(kk), b + (uint64_t)(kk * 128), idesc, 1u);
 }
 
 // ------------------------------------------------------------------------- statistics
@@ -115,9 +111,10 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan 
 // S_{j+1} needs only that the row threads have read S_j (dQ_{j-1} runs meanwhile), dP_{j+1} that
 // dQ_{j-1} has completed (S_{j+1} runs meanwhile; dP has two buffers), and dQ_j has a whole period of
 // three products for dS_j to be made in.
-// Roles: warp 0 TMA, warp 1 issuer of S and dP, warp 2 of dQ, warps 4..11 row threads (two per row: keys 0..63 and
-// 64..127 of each block), warps 12..15 epilogue.
+// Roles: warp 0 TMA, warp 1 issuer of S and dP, warp 2 of dQ, warps 4..11 row threads (two per
+// row: keys 0..63 and 64..127 of each block), warps 12..15 epilogue.
 // TMEM columns: S 0, dP 128 and 256, dQ 384.
+constexpr int kDqThreads = 512;
 template <int D>
 struct DqSmem {
   static constexpr int kPanels = D / 64;
@@ -133,7 +130,7 @@ struct DqSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDqThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, CrossShape s,
                     BwdPlan plan, CrossBwdArgs a) {
@@ -384,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t tdp = trow + kDP + bb * 128 + 64 * g;
-        uint32_t pk[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
           tmem_ld32(tdp + 32 * h, u0);
           tmem_ld_wait(u0);
 #pragma unroll
@@ -394,10 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // behind the last key dP may be anything
             const float d0 = 32 * h + c < valid ? p[32 * h + c] * (__uint_as_float(u0[c]) - Dr) : 0.f;
             const float d1 = 32 * h + c + 1 < valid ? p[32 * h + c + 1] * (__uint_as_float(u0[c + 1]) - Dr) : 0.f;
-            pk[16 * h + c / 2] = pack_bf16x2(d0, d1);
+            pk[c / 2] = pack_bf16x2(d0, d1);
           }
+          tmem_st16(tdp + 32 * h, pk);
         }
-        tmem_st32(tdp, pk);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar_ds(bb));
@@ -454,16 +451,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // --------------------------------------------------------------------------- dK, dV
 //
-// A CTA holds a block of 128 keys and walks query tiles.  The products are formed transposed, keys
-// along the TMEM lanes, so that P^T and dS^T go from the element-wise threads to the next product
-// through TMEM.  Per tile u:
-//   S^T = K Q^T, dP^T = V dO^T  (M = 128 keys, N = 128 rows),  dV += P^T dO, dK += dS^T Q.
-// TMEM is full (S^T, dP^T, dV, dK: 128 columns each); P^T is written over S^T and dS^T over dP^T.
-// The products run S, dP, dV, dK in this order: S_{u+1} waits for dV_u while dK_u runs, dP_{u+1} for
-// dK_u while S_{u+1} runs; P is made while dP runs and dS while dV runs.  Two issuers, so that one waits
-// on its barriers while the other's products run.
-// Roles: warp 0 TMA, warp 1 issuer of S, dP, warp 2 of dV, dK, warps 4..11 element-wise (thread = key, two per key: rows
-// 0..63 and 64..127 of the tile).
+// A CTA holds a block of 128 keys and walks query tiles, a half tile of 64 rows at a time.  The products
+// are formed transposed, keys along the TMEM lanes, so that P^T and dS^T go from the element-wise threads
+// to the next product through TMEM.  Per half tile u, in buffer u % 2:
+//   S^T = K Q^T, dP^T = V dO^T  (M = 128 keys, N = 64 rows),  dV += P^T dO, dK += dS^T Q  (K = 64).
+// P^T is written over S^T and dS^T over dP^T; S^T and dP^T of half tile u + 2 wait for dV and dK of u, those
+// of u + 1 are made meanwhile.  (With whole tiles TMEM has room for one S^T and dP^T, and S, P, dV, S are
+// one chain: 3000 cycles at d = 64, 3600 at d = 128 per tile, half of it the element-wise threads', against
+// 1280 and 2560 of shared-memory reads for the products here.)
+// Roles: warp 0 TMA, warp 1 issuer of S and dP, warp 2 of dV and dK (one waits on its barriers while the
+// other's products run), warps 4..19 element-wise: two sets of 8 warps take half tiles in turn, so that
+// one's latencies fall into the other's work; thread = key, two per key: rows 0..31 and 32..63.
+constexpr int kDkvThreads = 640;
 template <int D>
 struct DkvSmem {
   static constexpr int kPanels = D / 64;
@@ -477,7 +476,6 @@ struct DkvSmem {
   static constexpr int kBytes = kOffBar + 512 + 1024;
   static_assert(kBytes <= (int)kMaxDynSmem && kBytes > 114 * 1024, "shared memory: one CTA per SM");
 };
-constexpr int kDkvThreads = 384;
 
 // The pieces of a CTA's run: key block kb of head (b, hk), query tiles [t0, t0 + nt).
 struct DkvPiece {
@@ -549,7 +547,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                       BwdPlan plan, CrossBwdArgs a) {
   using L = DkvSmem<D>;
   constexpr int kStages = L::kStages;
-  constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
+  constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;  // (buffers 64 columns apart)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -557,11 +555,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   auto bar_full = [&](int st) { return smem_u32(&bars[st]); };
   auto bar_empty = [&](int st) { return smem_u32(&bars[4 + st]); };
   const uint32_t bar_kv = smem_u32(&bars[8]), bar_kvfree = smem_u32(&bars[9]);
-  const uint32_t bar_s = smem_u32(&bars[10]), bar_dp = smem_u32(&bars[11]);    // S^T, dP^T in TMEM
-  const uint32_t bar_p = smem_u32(&bars[12]), bar_ds = smem_u32(&bars[13]);    // P^T, dS^T written
-  const uint32_t bar_dvm = smem_u32(&bars[14]), bar_dkm = smem_u32(&bars[15]); // dV, dK products completed
-  const uint32_t bar_accfree = smem_u32(&bars[16]);                            // the piece's sums read out
-  const uint32_t bar_drain = smem_u32(&bars[17]), bar_gdrain = smem_u32(&bars[18]);
+  auto bar_s = [&](uint32_t b) { return smem_u32(&bars[10 + b]); };    // S^T, dP^T in TMEM buffer b
+  auto bar_dp = [&](uint32_t b) { return smem_u32(&bars[12 + b]); };
+  auto bar_p = [&](uint32_t b) { return smem_u32(&bars[14 + b]); };    // P^T, dS^T written over them
+  auto bar_ds = [&](uint32_t b) { return smem_u32(&bars[16 + b]); };
+  auto bar_dvm = [&](uint32_t b) { return smem_u32(&bars[18 + b]); };  // dV, dK products from them completed
+  auto bar_dkm = [&](uint32_t b) { return smem_u32(&bars[20 + b]); };
+  const uint32_t bar_acc = smem_u32(&bars[22]), bar_accfree = smem_u32(&bars[23]);  // the piece's sums complete / read
+  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   const WaitCtl wc{abort_flag, s.wait_ns};
@@ -590,13 +591,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     mbar_init(bar_kv, 1);
     mbar_init(bar_kvfree, 1);
-    mbar_init(bar_s, 1);
-    mbar_init(bar_dp, 1);
-    mbar_init(bar_p, 256);
-    mbar_init(bar_ds, 256);
-    mbar_init(bar_dvm, 1);
-    mbar_init(bar_dkm, 1);
-    mbar_init(bar_accfree, 256);
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(bar_s(b), 1);
+      mbar_init(bar_dp(b), 1);
+      mbar_init(bar_p(b), 256);
+      mbar_init(bar_ds(b), 256);
+      mbar_init(bar_dvm(b), 1);
+      mbar_init(bar_dkm(b), 1);
+    }
+    mbar_init(bar_acc, 1);
+    mbar_init(bar_accfree, 512);
     mbar_init(bar_drain, 1);
     mbar_init(bar_gdrain, 1);
     fence_barrier_init();
@@ -649,32 +653,32 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ issuer of S^T and dP^T
     DkvIter it(s, plan, a.kv_len);
-    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t idS = idesc_bf16_f32(128, 64, false, false);
     const uint64_t kd = smem_desc(sbase + L::kOffK, 16, 1024), vd = smem_desc(sbase + L::kOffV, 16, 1024);
     bool ok = true;
-    uint32_t U = 0, n = 0;
+    uint32_t u = 0, n = 0;  // half tiles, pieces
     DkvPiece x;
     while (ok && it.next(x)) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar_kv, n & 1, wc));
-      for (int t = 0; ok && t < x.nt; ++t, ++U) {
-        const int st = U % kStages;
-        const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc) &&
-                                         (U == 0 || mbar_wait(bar_dvm, (U - 1) & 1, wc)));
+      for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
+        const uint32_t U = u >> 1, st = U % kStages, b = u & 1;
+        const uint32_t stg = sbase + L::kOffStage + st * L::kStage + b * 8192;  // rows 64 b .. of each panel
+        ok = __all_sync(0xffffffffu, (b || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) &&
+                                         (u < 2 || mbar_wait(bar_dvm(b), (U - 1) & 1, wc)));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_ss<D>(tmem + kS, kd, smem_desc(stg + L::kStageQ, 16, 1024), idS);
-          umma_commit(bar_s);
+          issue_ss<D>(tmem + kS + 64 * b, kd, smem_desc(stg + L::kStageQ, 16, 1024), idS);
+          umma_commit(bar_s(b));
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, U == 0 || mbar_wait(bar_dkm, (U - 1) & 1, wc));
+        ok = __all_sync(0xffffffffu, u < 2 || mbar_wait(bar_dkm(b), (U - 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_ss<D>(tmem + kDP, vd, smem_desc(stg + L::kStageDO, 16, 1024), idS);
-          umma_commit(bar_dp);
-          if (t + 1 == x.nt) umma_commit(bar_kvfree);
+          issue_ss<D>(tmem + kDP + 64 * b, vd, smem_desc(stg + L::kStageDO, 16, 1024), idS);
+          umma_commit(bar_dp(b));
+          if (i + 1 == 2 * x.nt) umma_commit(bar_kvfree);
         }
         __syncwarp();
       }
@@ -688,28 +692,30 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     DkvIter it(s, plan, a.kv_len);
     constexpr uint32_t idG = idesc_bf16_f32(128, D, false, true);
     bool ok = true;
-    uint32_t U = 0, n = 0;
+    uint32_t u = 0, n = 0;
     DkvPiece x;
     while (ok && it.next(x)) {
-      for (int t = 0; ok && t < x.nt; ++t, ++U) {
-        const int st = U % kStages;
-        const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
-        ok = __all_sync(0xffffffffu, (t > 0 || n == 0 || mbar_wait(bar_accfree, (n - 1) & 1, wc)) &&
-                                         mbar_wait(bar_full(st), (U / kStages) & 1, wc) && mbar_wait(bar_p, U & 1, wc));
+      for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
+        const uint32_t U = u >> 1, st = U % kStages, b = u & 1;
+        const uint32_t stg = sbase + L::kOffStage + st * L::kStage + b * 8192;
+        ok = __all_sync(0xffffffffu, (i > 0 || n == 0 || mbar_wait(bar_accfree, (n - 1) & 1, wc)) &&
+                                         (b || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) &&
+                                         mbar_wait(bar_p(b), U & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_ts(tmem + kDV, tmem + kS, smem_desc(stg + L::kStageDO, 16384, 1024), idG, 8, t == 0);
-          umma_commit(bar_dvm);
+          issue_ts(tmem + kDV, tmem + kS + 64 * b, smem_desc(stg + L::kStageDO, 16384, 1024), idG, 4, i == 0);
+          umma_commit(bar_dvm(b));
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_ds, U & 1, wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_ds(b), U & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_ts(tmem + kDK, tmem + kDP, smem_desc(stg + L::kStageQ, 16384, 1024), idG, 8, t == 0);
-          umma_commit(bar_dkm);
-          umma_commit(bar_empty(st));
+          issue_ts(tmem + kDK, tmem + kDP + 64 * b, smem_desc(stg + L::kStageQ, 16384, 1024), idG, 4, i == 0);
+          umma_commit(bar_dkm(b));
+          if (b) umma_commit(bar_empty(st));
+          if (i + 1 == 2 * x.nt) umma_commit(bar_acc);
         }
         __syncwarp();
       }
@@ -722,78 +728,73 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     // ------------------------------------------------------------- element-wise threads
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
     DkvIter it(s, plan, a.kv_len);
-    const int g = (warp - 4) >> 2;  // rows 64 g .. 64 g + 63 of each tile
+    const uint32_t b = (uint32_t)(warp - 4) >> 3;  // half tiles of this parity (pieces have an even number)
+    const int g = ((warp - 4) >> 2) & 1;           // rows 32 g .. 32 g + 31 of the half tile
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t ts = trow + kS + 64 * b + 32 * g, tdp = trow + kDP + 64 * b + 32 * g;
     bool ok = true;
-    uint32_t U = 0;
+    uint32_t U = 0, n = 0;  // tiles, pieces
     DkvPiece x;
     while (ok && it.next(x)) {
-      const int key = x.kb * kKeyBlock + r;
       for (int t = 0; t < x.nt; ++t, ++U) {
         const int st = U % kStages;
-        const float4* l4 = reinterpret_cast<const float4*>(smem + L::kOffStage + st * L::kStage + L::kStageStats) + 16 * g;
+        const float4* l4 = reinterpret_cast<const float4*>(smem + L::kOffStage + st * L::kStage + L::kStageStats) +
+                           16 * b + 8 * g;
         const float4* d4 = l4 + 32;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc) && mbar_wait(bar_s, U & 1, wc))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc) && mbar_wait(bar_s(b), U & 1, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float p[64];
-        uint32_t pk[32];
+        float p[32];
+        uint32_t v[32], pk[16];
+        tmem_ld32(ts, v);
+        tmem_ld_wait(v);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t u[32];
-          tmem_ld32(trow + kS + 64 * g + 32 * h, u);
-          tmem_ld_wait(u);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 l = l4[8 * h + q];
-            float* pp = p + 32 * h + 4 * q;
-            pp[0] = ex2(fmaf(__uint_as_float(u[4 * q]), a.scale_log2, -l.x));
-            pp[1] = ex2(fmaf(__uint_as_float(u[4 * q + 1]), a.scale_log2, -l.y));
-            pp[2] = ex2(fmaf(__uint_as_float(u[4 * q + 2]), a.scale_log2, -l.z));
-            pp[3] = ex2(fmaf(__uint_as_float(u[4 * q + 3]), a.scale_log2, -l.w));
-            pk[16 * h + 2 * q] = pack_bf16x2(pp[0], pp[1]);
-            pk[16 * h + 2 * q + 1] = pack_bf16x2(pp[2], pp[3]);
-          }
+        for (int q = 0; q < 8; ++q) {
+          const float4 l = l4[q];
+          float* pp = p + 4 * q;
+          pp[0] = ex2(fmaf(__uint_as_float(v[4 * q]), a.scale_log2, -l.x));
+          pp[1] = ex2(fmaf(__uint_as_float(v[4 * q + 1]), a.scale_log2, -l.y));
+          pp[2] = ex2(fmaf(__uint_as_float(v[4 * q + 2]), a.scale_log2, -l.z));
+          pp[3] = ex2(fmaf(__uint_as_float(v[4 * q + 3]), a.scale_log2, -l.w));
+          pk[2 * q] = pack_bf16x2(pp[0], pp[1]);
+          pk[2 * q + 1] = pack_bf16x2(pp[2], pp[3]);
         }
-        tmem_st32(trow + kS + 64 * g, pk);
+        tmem_st16(ts, pk);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_p);
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_dp, U & 1, wc))) {
+        mbar_arrive(bar_p(b));
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_dp(b), U & 1, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
+        tmem_ld32(tdp, v);
+        tmem_ld_wait(v);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t u[32];
-          tmem_ld32(trow + kDP + 64 * g + 32 * h, u);
-          tmem_ld_wait(u);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 d = d4[8 * h + q];
-            const float* pp = p + 32 * h + 4 * q;
-            pk[16 * h + 2 * q] = pack_bf16x2(pp[0] * (__uint_as_float(u[4 * q]) - d.x),
-                                             pp[1] * (__uint_as_float(u[4 * q + 1]) - d.y));
-            pk[16 * h + 2 * q + 1] = pack_bf16x2(pp[2] * (__uint_as_float(u[4 * q + 2]) - d.z),
-                                                 pp[3] * (__uint_as_float(u[4 * q + 3]) - d.w));
-          }
+        for (int q = 0; q < 8; ++q) {
+          const float4 d = d4[q];
+          const float* pp = p + 4 * q;
+          pk[2 * q] = pack_bf16x2(pp[0] * (__uint_as_float(v[4 * q]) - d.x), pp[1] * (__uint_as_float(v[4 * q + 1]) - d.y));
+          pk[2 * q + 1] =
+              pack_bf16x2(pp[2] * (__uint_as_float(v[4 * q + 2]) - d.z), pp[3] * (__uint_as_float(v[4 * q + 3]) - d.w));
         }
-        tmem_st32(trow + kDP + 64 * g, pk);
+        tmem_st16(tdp, pk);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_ds);
+        mbar_arrive(bar_ds(b));
       }
       if (!ok) break;
-      // ---- the piece's sums: thread = key, group g half of the channels
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_dkm, (U - 1) & 1, wc))) {  // the last product of all
+      // ---- the piece's sums: thread = key, a quarter of the channels
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_acc, n & 1, wc))) {
         ok = false;
         break;
       }
+      ++n;
       tc_fence_after();
+      const int key = x.kb * kKeyBlock + r, quarter = 2 * (int)b + g;
       const bool live = key < x.keys, store = key < s.M;
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {  // dK, dV
@@ -801,20 +802,25 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         const float mul = w ? 1.f : a.scale;
         uint16_t* row = static_cast<uint16_t*>(out.p) + x.b * out.sb + (int64_t)x.hk * out.sh + (int64_t)key * out.sn;
         float* part = a.part + (((int64_t)x.slot * 2 + w) * 128 + r) * D;
-#pragma unroll 1
-        for (int c0 = g * (D / 2); c0 < (g + 1) * (D / 2); c0 += 32) {
-          uint32_t u[32];
-          tmem_ld32(trow + (w ? kDV : kDK) + c0, u);
-          tmem_ld_wait(u);
-          float v[32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = live ? __uint_as_float(u[c]) * mul : 0.f;
+        for (int c0 = 0; c0 < D / 4; c0 += 16) {
+          const int ch = quarter * (D / 4) + c0;
+          uint32_t z[16];
+          tmem_ld16(trow + (w ? kDV : kDK) + ch, z);
+          tmem_ld_wait16(z);
+          float f[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] = live ? __uint_as_float(z[c]) * mul : 0.f;
           if (!x.whole) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              reinterpret_cast<float4*>(part + c0)[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            for (int c = 0; c < 4; ++c)
+              reinterpret_cast<float4*>(part + ch)[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
           } else if (store) {
-            store32_bf16(row + c0, v);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              reinterpret_cast<uint4*>(row + ch)[c] =
+                  make_uint4(pack_bf16x2(f[8 * c], f[8 * c + 1]), pack_bf16x2(f[8 * c + 2], f[8 * c + 3]),
+                             pack_bf16x2(f[8 * c + 4], f[8 * c + 5]), pack_bf16x2(f[8 * c + 6], f[8 * c + 7]));
           }
         }
       }
@@ -898,7 +904,7 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
   cross_dkdv_join_kernel<D><<<dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv)), 256, 0, st>>>(s, p, a);
   prof_stop(st, kAttnBwd);
   prof_start(st, kAttnBwdDq);
-  dq<<<(unsigned)p.dq_grid, kThreads, DqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
+  dq<<<(unsigned)p.dq_grid, kDqThreads, DqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
   prof_stop(st, kAttnBwdDq);
   return cudaGetLastError();
 }

@@ -146,18 +146,6 @@ __device__ __forceinline__ void store32(uint16_t* dst, const float (&v)[32], boo
   }
 }
 
-// 32 lanes x 16 columns of TMEM.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-      "%13, %14, %15}, [%16];"
-      : SA2_R8(0), SA2_R8(8)
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : SA2_P8(0), SA2_P8(8)::"memory");
-}
-
 // O (+)= P V over up to 64 keys: A = P in TMEM (16 keys in 8 columns), B = V, 16 rows per k-step.
 __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, uint32_t idesc, int steps, bool fresh) {
   umma_ts(o, p, v, idesc, fresh ? 0u : 1u);
