@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 // of u + 1 are made meanwhile.  (With whole tiles TMEM has room for one S^T and dP^T, and S, P, dV, S are
 // one chain: 3000 cycles at d = 64, 3600 at d = 128 per tile, half of it the element-wise threads', against
 // 1280 and 2560 of shared-memory reads for the products here.)
-// Roles: warp 0 TMA, warp 1 issuer of S and dP, warp 2 of dV and dK (one waits on its barriers while the
-// other's products run), warps 4..19 element-wise: two sets of 8 warps take half tiles in turn, so that
+// Roles: warp 0 TMA, warps 1, 3 and 2 issuers of S, of dP, and of dV and dK (a wait and its bookkeeping take an
+// issuer 200 to 400 cycles beside the element-wise warps: one for S and dP was the bound of d = 64), warps 4..19 element-wise: two sets of 8 warps take half tiles in turn, so that
 // one's latencies fall into the other's work; thread = key, two per key: rows 0..31 and 32..63.
 constexpr int kDkvThreads = 640;
 template <int D>
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   auto bar_dvm = [&](uint32_t b) { return smem_u32(&bars[18 + b]); };  // dV, dK products from them completed
   auto bar_dkm = [&](uint32_t b) { return smem_u32(&bars[20 + b]); };
   const uint32_t bar_acc = smem_u32(&bars[22]), bar_accfree = smem_u32(&bars[23]);  // the piece's sums complete / read
-  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]);
+  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]), bar_pdrain = smem_u32(&bars[26]);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   const WaitCtl wc{abort_flag, s.wait_ns};
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       mbar_init(bar_empty(i), 1);
     }
     mbar_init(bar_kv, 1);
-    mbar_init(bar_kvfree, 1);
+    mbar_init(bar_kvfree, 2);
     for (uint32_t b = 0; b < 2; ++b) {
       mbar_init(bar_s(b), 1);
       mbar_init(bar_dp(b), 1);
@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     mbar_init(bar_accfree, 512);
     mbar_init(bar_drain, 1);
     mbar_init(bar_gdrain, 1);
+    mbar_init(bar_pdrain, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -650,11 +651,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         mbar_drain(bar_full(v % kStages), (v / kStages) & 1, abort_flag);
       if (n) mbar_drain(bar_kv, (n - 1) & 1, abort_flag);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ issuer of S^T and dP^T
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------------ issuers of S^T and of dP^T
     DkvIter it(s, plan, a.kv_len);
     constexpr uint32_t idS = idesc_bf16_f32(128, 64, false, false);
-    const uint64_t kd = smem_desc(sbase + L::kOffK, 16, 1024), vd = smem_desc(sbase + L::kOffV, 16, 1024);
+    const bool dp = warp == 3;
+    const uint64_t akd = smem_desc(sbase + (dp ? L::kOffV : L::kOffK), 16, 1024);
+    const uint32_t bst = sbase + L::kOffStage + (dp ? L::kStageDO : L::kStageQ);
+    const uint32_t dst = tmem + (dp ? kDP : kS), done = dp ? bar_dp(0) : bar_s(0), freed = dp ? bar_dkm(0) : bar_dvm(0);
     bool ok = true;
     uint32_t u = 0, n = 0;  // half tiles, pieces
     DkvPiece x;
@@ -662,31 +666,22 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(bar_kv, n & 1, wc));
       for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
         const uint32_t U = u >> 1, st = U % kStages, b = u & 1;
-        const uint32_t stg = sbase + L::kOffStage + st * L::kStage + b * 8192;  // rows 64 b .. of each panel
         ok = __all_sync(0xffffffffu, (b || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) &&
-                                         (u < 2 || mbar_wait(bar_dvm(b), (U - 1) & 1, wc)));
+                                         (u < 2 || mbar_wait(freed + 8 * b, (U - 1) & 1, wc)));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_ss<D>(tmem + kS + 64 * b, kd, smem_desc(stg + L::kStageQ, 16, 1024), idS);
-          umma_commit(bar_s(b));
-        }
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, u < 2 || mbar_wait(bar_dkm(b), (U - 1) & 1, wc));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_ss<D>(tmem + kDP + 64 * b, vd, smem_desc(stg + L::kStageDO, 16, 1024), idS);
-          umma_commit(bar_dp(b));
+          issue_ss<D>(dst + 64 * b, akd, smem_desc(bst + st * L::kStage + b * 8192, 16, 1024), idS);  // rows 64 b ..
+          umma_commit(done + 8 * b);
           if (i + 1 == 2 * x.nt) umma_commit(bar_kvfree);
         }
         __syncwarp();
       }
       ++n;
     }
-    if (elect_one()) umma_commit(bar_drain);
+    if (elect_one()) umma_commit(dp ? bar_pdrain : bar_drain);
     __syncwarp();
-    mbar_drain(bar_drain, 0, abort_flag);
+    mbar_drain(dp ? bar_pdrain : bar_drain, 0, abort_flag);
   } else if (warp == 2) {
     // ------------------------------------------------------------------ issuer of dV and dK
     DkvIter it(s, plan, a.kv_len);
