@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan 
 // S_{j+1} needs only that the row threads have read S_j (dQ_{j-1} runs meanwhile), dP_{j+1} that
 // dQ_{j-1} has completed (S_{j+1} runs meanwhile; dP has two buffers), and dQ_j has a whole period of
 // three products for dS_j to be made in.
-// Roles: warp 0 TMA, warp 1 issuer of S and dP, warp 2 of dQ, warps 4..11 row threads (two per
-// row: keys 0..63 and 64..127 of each block), warps 12..15 epilogue.
+// Roles: warp 0 TMA, warps 1, 3 and 2 issuers of S, dP and dQ, warps 4..11 row threads (two per row: keys
+// 0..63 and 64..127 of each block), warps 12..15 epilogue.
 // TMEM columns: S 0, dP 128 and 256, dQ 384.
 constexpr int kDqThreads = 512;
 template <int D>
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   auto bar_ds = [&](int i) { return smem_u32(&bars[18 + i]); };    // dS written over it
   auto bar_dqm = [&](int i) { return smem_u32(&bars[20 + i]); };   // dQ += dS K from it completed
   const uint32_t bar_dq = smem_u32(&bars[22]), bar_dqfree = smem_u32(&bars[23]);  // dQ of the item complete / read
-  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]);
+  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]), bar_pdrain = smem_u32(&bars[26]);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   const WaitCtl wc{abort_flag, s.wait_ns};
@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(bar_dqfree, 128);
     mbar_init(bar_drain, 1);
     mbar_init(bar_gdrain, 1);
+    mbar_init(bar_pdrain, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -262,14 +263,14 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       if (don) mbar_drain(bar_do, (don - 1) & 1, abort_flag);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ issuer of S and dP
-    const uint64_t qd = smem_desc(sbase + L::kOffQ, 16, 1024), dod = smem_desc(sbase + L::kOffDO, 16, 1024);
+    // ------------------------------------------------------------------ issuer of S
+    const uint64_t qd = smem_desc(sbase + L::kOffQ, 16, 1024);
     bool ok = true;
     uint32_t J = 0, n = 0;  // blocks, items
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item x = item_at(i);
-      for (int j = 0; ok && j < x.nk; ++j, ++J) {
-        const int ks = J % kKSt, vs = J % kVSt, bb = J & 1;
+      for (int j = 0; j < x.nk; ++j, ++J) {
+        const int ks = J % kKSt;
         const int steps = (min(kKeyBlock, x.keys - j * kKeyBlock) + 15) >> 4;
         const uint32_t idS = idesc_bf16_f32(128, steps * 16, false, false);
         ok = __all_sync(0xffffffffu, mbar_wait(bar_kfull(ks), (J / kKSt) & 1, wc) &&
@@ -283,6 +284,23 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           if (j + 1 == x.nk) umma_commit(bar_qfree);
         }
         __syncwarp();
+      }
+      if (x.nk > 0) ++n;
+    }
+    if (elect_one()) umma_commit(bar_drain);
+    __syncwarp();
+    mbar_drain(bar_drain, 0, abort_flag);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ issuer of dP
+    const uint64_t dod = smem_desc(sbase + L::kOffDO, 16, 1024);
+    bool ok = true;
+    uint32_t J = 0, n = 0;
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item x = item_at(i);
+      for (int j = 0; j < x.nk; ++j, ++J) {
+        const int vs = J % kVSt, bb = J & 1;
+        const int steps = (min(kKeyBlock, x.keys - j * kKeyBlock) + 15) >> 4;
+        const uint32_t idS = idesc_bf16_f32(128, steps * 16, false, false);
         ok = __all_sync(0xffffffffu, mbar_wait(bar_vfull(vs), (J / kVSt) & 1, wc) &&
                                          (j > 0 || mbar_wait(bar_do, n & 1, wc)) &&
                                          (J < 2 || mbar_wait(bar_dqm(bb), ((J >> 1) - 1) & 1, wc)));
@@ -298,9 +316,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       }
       if (x.nk > 0) ++n;
     }
-    if (elect_one()) umma_commit(bar_drain);
+    if (elect_one()) umma_commit(bar_pdrain);
     __syncwarp();
-    mbar_drain(bar_drain, 0, abort_flag);
+    mbar_drain(bar_pdrain, 0, abort_flag);
   } else if (warp == 2) {
     // ------------------------------------------------------------------ issuer of dQ
     constexpr uint32_t idQ = idesc_bf16_f32(128, D, false, true);
@@ -453,26 +471,52 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 //
 // A CTA holds a block of 128 keys and walks query tiles, a half tile of 64 rows at a time.  The products
 // are formed transposed, keys along the TMEM lanes, so that P^T and dS^T go from the element-wise threads
-// to the next product through TMEM.  Per half tile u, in buffer u % 2:
+// to the next product through TMEM.  Per half tile, in its buffer (two at d = 128, three at d = 64):
 //   S^T = K Q^T, dP^T = V dO^T  (M = 128 keys, N = 64 rows),  dV += P^T dO, dK += dS^T Q  (K = 64).
-// P^T is written over S^T and dS^T over dP^T; S^T and dP^T of half tile u + 2 wait for dV and dK of u, those
-// of u + 1 are made meanwhile.  (With whole tiles TMEM has room for one S^T and dP^T, and S, P, dV, S are
-// one chain: 3000 cycles at d = 64, 3600 at d = 128 per tile, half of it the element-wise threads', against
-// 1280 and 2560 of shared-memory reads for the products here.)
-// Roles: warp 0 TMA, warps 1, 3 and 2 issuers of S, of dP, and of dV and dK (a wait and its bookkeeping take an
-// issuer 200 to 400 cycles beside the element-wise warps: one for S and dP was the bound of d = 64), warps 4..19 element-wise: two sets of 8 warps take half tiles in turn, so that
-// one's latencies fall into the other's work; thread = key, two per key: rows 0..31 and 32..63.
-constexpr int kDkvThreads = 640;
+// P^T is written over S^T and dS^T over dP^T; S^T and dP^T of a half tile wait for dV and dK of the one that
+// had the buffer, those between are made meanwhile.  (With whole tiles TMEM has room for one S^T and dP^T,
+// and S, P, dV, S are one chain: 19 heads x 8192 x 4096, d = 128: 485 us, half tiles 441.)
+// LSE and D belong to TMEM columns here, and every element-wise thread needs all of them: from shared memory
+// 32 cycles of its 128 bytes per clock for each warp and 32 values, 1000 cycles per tile beside the products'
+// reads.  At d = 64 they come through the products instead: 16 more channels, K and V with ones in three of
+// them, Q with -LSE / scale and dO with -D as three bf16 each, so that S^T is s - LSE (in units of the
+// scale) and dP^T is dP - D, in fp32, for one more step of 48 cycles: the same shape at d = 64 takes 269
+// us, 314 with loads.  At d = 128, where the products take three quarters of the time, 488 against 441.
+// Roles: warp 0 TMA; warps 1, 3 and 2 issuers of S, of dP, and of dV and dK (a wait and its bookkeeping take
+// an issuer 200 to 400 cycles beside the element-wise warps); warps 4..19 element-wise: two sets of 8 warps
+// take half tiles in turn, so that one's latencies fall into the other's work; thread = key, two per key:
+// rows 0..31 and 32..63; warp 20 (d = 64) writes the 16 channels.
+// 16 more channels of 128 rows: 16-byte rows of 8 channels in groups of 8, the groups of channels 0..7
+// and 8..15 next to each other.
+constexpr int kXTile = 4096;
+// LSE is divided by the scale; below this one q . k counts for nothing beside it, and is left to.
+constexpr float kMinScale = 0x1p-100f;
+__device__ __forceinline__ uint32_t x_row(int r) { return (uint32_t)(r >> 3) * 256 + (r & 7) * 16; }
+__device__ __forceinline__ uint64_t x_desc(uint32_t saddr) { return smem_desc(saddr, 128, 256, 0); }
+// x as the sum of three bf16 numbers, exact to 2^-24 of x (an infinity or NaN: the first alone).
+__device__ __forceinline__ uint2 split3(float x) {
+  const uint32_t hi = pack_bf16x2(x, 0.f) & 0xFFFFu;
+  const float r1 = x - __uint_as_float(hi << 16);
+  if (!(fabsf(r1) < INFINITY)) return make_uint2(hi, 0u);
+  const uint32_t mid = pack_bf16x2(r1, 0.f) & 0xFFFFu;
+  const uint32_t lo = pack_bf16x2(r1 - __uint_as_float(mid << 16), 0.f) & 0xFFFFu;
+  return make_uint2(hi | mid << 16, lo);
+}
+
 template <int D>
 struct DkvSmem {
+  static constexpr bool kX = D == 64;  // LSE and D through the products
+  static constexpr int kThreads = kX ? 672 : 640;
   static constexpr int kPanels = D / 64;
   static constexpr int kTile = 128 * 128 * kPanels;
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kOffK = 0, kOffV = kTile;
   static constexpr int kOffStage = 2 * kTile;  // Q, dO, statistics
-  static constexpr int kStageQ = 0, kStageDO = kTile, kStageStats = 2 * kTile;
-  static constexpr int kStage = 2 * kTile + 1024;
-  static constexpr int kOffBar = kOffStage + kStages * kStage;
+  static constexpr int kStageQ = 0, kStageDO = kTile, kStageX = 2 * kTile;
+  static constexpr int kStageStats = kStageX + (kX ? 2 * kXTile : 0);
+  static constexpr int kStage = kStageStats + 1024;
+  static constexpr int kOffOnes = kOffStage + kStages * kStage;
+  static constexpr int kOffBar = kOffOnes + (kX ? kXTile : 0);
   static constexpr int kBytes = kOffBar + 512 + 1024;
   static_assert(kBytes <= (int)kMaxDynSmem && kBytes > 114 * 1024, "shared memory: one CTA per SM");
 };
@@ -541,13 +585,14 @@ struct DkvIter {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kDkvThreads, 1)
+__global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
     cross_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, CrossShape s,
                       BwdPlan plan, CrossBwdArgs a) {
   using L = DkvSmem<D>;
   constexpr int kStages = L::kStages;
-  constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;  // (buffers 64 columns apart)
+  constexpr uint32_t kBufs = D == 128 ? 2 : 3;  // of S^T and dP^T, 64 columns each
+  constexpr uint32_t kS = 0, kDP = 64 * kBufs, kDV = 2 * kDP, kDK = kDV + D;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -556,13 +601,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   auto bar_empty = [&](int st) { return smem_u32(&bars[4 + st]); };
   const uint32_t bar_kv = smem_u32(&bars[8]), bar_kvfree = smem_u32(&bars[9]);
   auto bar_s = [&](uint32_t b) { return smem_u32(&bars[10 + b]); };    // S^T, dP^T in TMEM buffer b
-  auto bar_dp = [&](uint32_t b) { return smem_u32(&bars[12 + b]); };
-  auto bar_p = [&](uint32_t b) { return smem_u32(&bars[14 + b]); };    // P^T, dS^T written over them
-  auto bar_ds = [&](uint32_t b) { return smem_u32(&bars[16 + b]); };
-  auto bar_dvm = [&](uint32_t b) { return smem_u32(&bars[18 + b]); };  // dV, dK products from them completed
-  auto bar_dkm = [&](uint32_t b) { return smem_u32(&bars[20 + b]); };
-  const uint32_t bar_acc = smem_u32(&bars[22]), bar_accfree = smem_u32(&bars[23]);  // the piece's sums complete / read
-  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]), bar_pdrain = smem_u32(&bars[26]);
+  auto bar_dp = [&](uint32_t b) { return smem_u32(&bars[13 + b]); };
+  auto bar_p = [&](uint32_t b) { return smem_u32(&bars[16 + b]); };    // P^T, dS^T written over them
+  auto bar_ds = [&](uint32_t b) { return smem_u32(&bars[19 + b]); };
+  auto bar_dvm = [&](uint32_t b) { return smem_u32(&bars[22 + b]); };  // dV, dK products from them completed
+  auto bar_dkm = [&](uint32_t b) { return smem_u32(&bars[25 + b]); };
+  const uint32_t bar_acc = smem_u32(&bars[28]), bar_accfree = smem_u32(&bars[29]);  // the piece's sums complete / read
+  const uint32_t bar_drain = smem_u32(&bars[30]), bar_gdrain = smem_u32(&bars[31]), bar_pdrain = smem_u32(&bars[32]);
+  auto bar_x = [&](int st) { return smem_u32(&bars[33 + st]); };  // the 16 channels written
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   const WaitCtl wc{abort_flag, s.wait_ns};
@@ -573,7 +619,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int used = plan.nb * s.G;
   if (used < 128) {
     const int n = (128 - used) * 8 * L::kPanels * 2 * kStages;
-    for (int i = tid; i < n; i += kDkvThreads) {
+    for (int i = tid; i < n; i += L::kThreads) {
       const int row = used + (i >> 3) % (128 - used);
       int x = (i >> 3) / (128 - used);
       const int p = x % L::kPanels;
@@ -581,17 +627,25 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       uint8_t* t = smem + L::kOffStage + (x >> 1) * L::kStage + ((x & 1) ? L::kStageDO : L::kStageQ);
       *reinterpret_cast<uint4*>(t + p * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
-    fence_proxy_async();
   }
+  for (int i = tid; L::kX && i < (2 * kStages + 1) * (kXTile / 16); i += L::kThreads) {
+    const int x = i / (kXTile / 16), at = (i % (kXTile / 16)) * 16;
+    const bool ones = x == 2 * kStages && !(at & 128);
+    uint8_t* tile = x == 2 * kStages ? smem + L::kOffOnes
+                                     : smem + L::kOffStage + (x >> 1) * L::kStage + L::kStageX + (x & 1) * kXTile;
+    *reinterpret_cast<uint4*>(tile + at) = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async();
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar_full(i), 1);
       mbar_init(bar_empty(i), 1);
+      mbar_init(bar_x(i), 1);
     }
     mbar_init(bar_kv, 1);
     mbar_init(bar_kvfree, 2);
-    for (uint32_t b = 0; b < 2; ++b) {
+    for (uint32_t b = 0; b < kBufs; ++b) {
       mbar_init(bar_s(b), 1);
       mbar_init(bar_dp(b), 1);
       mbar_init(bar_p(b), 256);
@@ -658,6 +712,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const bool dp = warp == 3;
     const uint64_t akd = smem_desc(sbase + (dp ? L::kOffV : L::kOffK), 16, 1024);
     const uint32_t bst = sbase + L::kOffStage + (dp ? L::kStageDO : L::kStageQ);
+    const uint32_t xst = sbase + L::kOffStage + L::kStageX + (dp ? kXTile : 0);
     const uint32_t dst = tmem + (dp ? kDP : kS), done = dp ? bar_dp(0) : bar_s(0), freed = dp ? bar_dkm(0) : bar_dvm(0);
     bool ok = true;
     uint32_t u = 0, n = 0;  // half tiles, pieces
@@ -665,13 +720,16 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     while (ok && it.next(x)) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar_kv, n & 1, wc));
       for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
-        const uint32_t U = u >> 1, st = U % kStages, b = u & 1;
-        ok = __all_sync(0xffffffffu, (b || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) &&
-                                         (u < 2 || mbar_wait(freed + 8 * b, (U - 1) & 1, wc)));
+        const uint32_t U = u >> 1, st = U % kStages, half = u & 1, b = u % kBufs;
+        ok = __all_sync(0xffffffffu, (half || (mbar_wait(bar_full(st), (U / kStages) & 1, wc) &&
+                                                   (!L::kX || mbar_wait(bar_x(st), (U / kStages) & 1, wc)))) &&
+                                         (u < kBufs || mbar_wait(freed + 8 * b, (u / kBufs - 1) & 1, wc)));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_ss<D>(dst + 64 * b, akd, smem_desc(bst + st * L::kStage + b * 8192, 16, 1024), idS);  // rows 64 b ..
+          issue_ss<D>(dst + 64 * b, akd, smem_desc(bst + st * L::kStage + half * 8192, 16, 1024), idS);
+          if constexpr (L::kX)
+            umma_ss(dst + 64 * b, x_desc(sbase + L::kOffOnes), x_desc(xst + st * L::kStage + half * (kXTile / 2)), idS, 1u);
           umma_commit(done + 8 * b);
           if (i + 1 == 2 * x.nt) umma_commit(bar_kvfree);
         }
@@ -691,11 +749,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     DkvPiece x;
     while (ok && it.next(x)) {
       for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
-        const uint32_t U = u >> 1, st = U % kStages, b = u & 1;
-        const uint32_t stg = sbase + L::kOffStage + st * L::kStage + b * 8192;
+        const uint32_t U = u >> 1, st = U % kStages, half = u & 1, b = u % kBufs, use = (u / kBufs) & 1;
+        const uint32_t stg = sbase + L::kOffStage + st * L::kStage + half * 8192;  // rows 64 .. of each panel
         ok = __all_sync(0xffffffffu, (i > 0 || n == 0 || mbar_wait(bar_accfree, (n - 1) & 1, wc)) &&
-                                         (b || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) &&
-                                         mbar_wait(bar_p(b), U & 1, wc));
+                                         (half || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) &&
+                                         mbar_wait(bar_p(b), use, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -703,13 +761,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           umma_commit(bar_dvm(b));
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_ds(b), U & 1, wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_ds(b), use, wc));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           issue_ts(tmem + kDK, tmem + kDP + 64 * b, smem_desc(stg + L::kStageQ, 16384, 1024), idG, 4, i == 0);
           umma_commit(bar_dkm(b));
-          if (b) umma_commit(bar_empty(st));
+          if (half) umma_commit(bar_empty(st));
           if (i + 1 == 2 * x.nt) umma_commit(bar_acc);
         }
         __syncwarp();
@@ -719,25 +777,53 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (elect_one()) umma_commit(bar_gdrain);
     __syncwarp();
     mbar_drain(bar_gdrain, 0, abort_flag);
+  } else if (L::kX && warp == 20) {
+    // ------------------------------------------------------------- the 16 channels of LSE and D
+    DkvIter it(s, plan, a.kv_len);
+    const float inv = -1.f / fmaxf(a.scale_log2, kMinScale);
+    uint32_t U = 0;
+    bool ok = true;
+    DkvPiece x;
+    while (ok && it.next(x)) {
+      for (int t = 0; t < x.nt; ++t, ++U) {
+        const int st = U % kStages;
+        uint8_t* stg = smem + L::kOffStage + st * L::kStage;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc));
+        if (!ok) break;
+        const float* rec = reinterpret_cast<const float*>(stg + L::kStageStats);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * i + lane;
+          *reinterpret_cast<uint2*>(stg + L::kStageX + x_row(r)) = split3(rec[r] * inv);
+          *reinterpret_cast<uint2*>(stg + L::kStageX + kXTile + x_row(r)) = split3(-rec[128 + r]);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_x(st));
+      }
+    }
   } else if (warp >= 4) {
     // ------------------------------------------------------------- element-wise threads
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
     DkvIter it(s, plan, a.kv_len);
-    const uint32_t b = (uint32_t)(warp - 4) >> 3;  // half tiles of this parity (pieces have an even number)
+    const uint32_t half = (uint32_t)(warp - 4) >> 3;  // of every tile
     const int g = ((warp - 4) >> 2) & 1;           // rows 32 g .. 32 g + 31 of the half tile
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t ts = trow + kS + 64 * b + 32 * g, tdp = trow + kDP + 64 * b + 32 * g;
+    const float mul = L::kX ? fmaxf(a.scale_log2, kMinScale) : a.scale_log2;
+    const uint32_t ts0 = trow + kS + 32 * g + (kBufs == 2 ? 64 * half : 0);
     bool ok = true;
     uint32_t U = 0, n = 0;  // tiles, pieces
     DkvPiece x;
     while (ok && it.next(x)) {
       for (int t = 0; t < x.nt; ++t, ++U) {
+        const uint32_t u = 2 * U + half, b = kBufs == 2 ? half : u % kBufs, use = (kBufs == 2 ? U : u / kBufs) & 1;
+        const uint32_t ts = kBufs == 2 ? ts0 : ts0 + 64 * b, tdp = ts + kDP - kS;
         const int st = U % kStages;
         const float4* l4 = reinterpret_cast<const float4*>(smem + L::kOffStage + st * L::kStage + L::kStageStats) +
-                           16 * b + 8 * g;
+                           16 * half + 8 * g;
         const float4* d4 = l4 + 32;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_full(st), (U / kStages) & 1, wc) && mbar_wait(bar_s(b), U & 1, wc))) {
+        if (!__all_sync(0xffffffffu, (L::kX || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) && mbar_wait(bar_s(b), use, wc))) {
           ok = false;
           break;
         }
@@ -746,35 +832,48 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         uint32_t v[32], pk[16];
         tmem_ld32(ts, v);
         tmem_ld_wait(v);
+        if constexpr (L::kX) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 l = l4[q];
-          float* pp = p + 4 * q;
-          pp[0] = ex2(fmaf(__uint_as_float(v[4 * q]), a.scale_log2, -l.x));
-          pp[1] = ex2(fmaf(__uint_as_float(v[4 * q + 1]), a.scale_log2, -l.y));
-          pp[2] = ex2(fmaf(__uint_as_float(v[4 * q + 2]), a.scale_log2, -l.z));
-          pp[3] = ex2(fmaf(__uint_as_float(v[4 * q + 3]), a.scale_log2, -l.w));
-          pk[2 * q] = pack_bf16x2(pp[0], pp[1]);
-          pk[2 * q + 1] = pack_bf16x2(pp[2], pp[3]);
+          for (int c = 0; c < 32; ++c) p[c] = ex2(__uint_as_float(v[c]) * mul);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 l = l4[q];
+            float* pp = p + 4 * q;
+            pp[0] = ex2(fmaf(__uint_as_float(v[4 * q]), mul, -l.x));
+            pp[1] = ex2(fmaf(__uint_as_float(v[4 * q + 1]), mul, -l.y));
+            pp[2] = ex2(fmaf(__uint_as_float(v[4 * q + 2]), mul, -l.z));
+            pp[3] = ex2(fmaf(__uint_as_float(v[4 * q + 3]), mul, -l.w));
+            pk[2 * q] = pack_bf16x2(pp[0], pp[1]);
+            pk[2 * q + 1] = pack_bf16x2(pp[2], pp[3]);
+          }
         }
         tmem_st16(ts, pk);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar_p(b));
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_dp(b), U & 1, wc))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_dp(b), use, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
         tmem_ld32(tdp, v);
         tmem_ld_wait(v);
+        if constexpr (L::kX) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 d = d4[q];
-          const float* pp = p + 4 * q;
-          pk[2 * q] = pack_bf16x2(pp[0] * (__uint_as_float(v[4 * q]) - d.x), pp[1] * (__uint_as_float(v[4 * q + 1]) - d.y));
-          pk[2 * q + 1] =
-              pack_bf16x2(pp[2] * (__uint_as_float(v[4 * q + 2]) - d.z), pp[3] * (__uint_as_float(v[4 * q + 3]) - d.w));
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16x2(p[2 * c] * __uint_as_float(v[2 * c]), p[2 * c + 1] * __uint_as_float(v[2 * c + 1]));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 d = d4[q];
+            const float* pp = p + 4 * q;
+            pk[2 * q] = pack_bf16x2(pp[0] * (__uint_as_float(v[4 * q]) - d.x), pp[1] * (__uint_as_float(v[4 * q + 1]) - d.y));
+            pk[2 * q + 1] =
+                pack_bf16x2(pp[2] * (__uint_as_float(v[4 * q + 2]) - d.z), pp[3] * (__uint_as_float(v[4 * q + 3]) - d.w));
+          }
         }
         tmem_st16(tdp, pk);
         tmem_st_wait();
@@ -789,7 +888,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       }
       ++n;
       tc_fence_after();
-      const int key = x.kb * kKeyBlock + r, quarter = 2 * (int)b + g;
+      const int key = x.kb * kKeyBlock + r, quarter = 2 * (int)half + g;
       const bool live = key < x.keys, store = key < s.M;
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {  // dK, dV
@@ -895,7 +994,7 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
   cross_stats_kernel<D><<<(unsigned)((int64_t)s.B * s.Hkv * p.tiles), 256, 0, st>>>(s, p, a);
   prof_stop(st, kBwdPre);
   prof_start(st, kAttnBwd);
-  dkv<<<(unsigned)p.grid, kDkvThreads, DkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
+  dkv<<<(unsigned)p.grid, DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
   cross_dkdv_join_kernel<D><<<dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv)), 256, 0, st>>>(s, p, a);
   prof_stop(st, kAttnBwd);
   prof_start(st, kAttnBwdDq);
