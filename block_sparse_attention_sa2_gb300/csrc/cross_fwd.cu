@@ -31,7 +31,7 @@
 namespace sa2 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 544;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: O and l are rescaled only past 2^8
 // TMEM columns: the two S buffers of tile t at 128 t and 128 t + 64 (P as 16-bit pairs over the first
@@ -62,21 +62,16 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A row's 64 scores; those behind the last key (whatever they are) as -inf.
-__device__ __forceinline__ void load_scores(uint32_t taddr, float (&x)[64], int valid) {
-  uint32_t u0[32], u1[32];
-  tmem_ld32(taddr, u0);
-  tmem_ld32(taddr + 32, u1);
-  tmem_ld_wait(u0);
-  tmem_ld_wait(u1);
+// 32 scores of a row; those behind the last key (whatever they are) as -inf.
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&x)[32], int valid) {
+  uint32_t u[32];
+  tmem_ld32(taddr, u);
+  tmem_ld_wait(u);
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    x[c] = __uint_as_float(u0[c]);
-    x[c + 32] = __uint_as_float(u1[c]);
-  }
-  if (valid < 64) {
+  for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(u[c]);
+  if (valid < 32) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) x[c] = c < valid ? x[c] : -INFINITY;
+    for (int c = 0; c < 32; ++c) x[c] = c < valid ? x[c] : -INFINITY;
   }
 }
 
@@ -87,15 +82,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-__device__ __forceinline__ float max64(const float (&x)[64]) {
+__device__ __forceinline__ float max32(const float (&x)[32]) {
   float m[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) m[c] = x[c];
+  for (int c = 0; c < 4; ++c) m[c] = max3(x[c], x[c + 4], x[c + 8]);
 #pragma unroll
-  for (int c = 4; c < 60; c += 8)
+  for (int c = 12; c < 28; c += 8)
 #pragma unroll
     for (int i = 0; i < 4; ++i) m[i] = max3(m[i], x[c + i], x[c + 4 + i]);
-  return max3(max3(m[0], x[60], x[61]), max3(m[1], x[62], x[63]), fmaxf(m[2], m[3]));
+  return max3(max3(m[0], x[28], x[29]), max3(m[1], x[30], x[31]), fmaxf(m[2], m[3]));
 }
 
 // Two fp32 operations in one instruction (the results are those of two single ones).
@@ -116,20 +111,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return y;
 }
 
-// p = exp2(x * mul + add) as 16-bit pairs; returns their sum (before rounding).
+// p = exp2(x * mul + add) as 16-bit pairs, and their sum (before rounding) added to l.
 template <bool F16>
-__device__ __forceinline__ float exp64(const float (&x)[64], float mul, float add, uint32_t (&pk)[32]) {
+__device__ __forceinline__ void exp32(const float (&x)[32], float mul, float add, uint32_t* pk, float2 (&l)[2]) {
   const float2 mul2{mul, mul}, addv{add, add};
-  float2 l[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
+  for (int c = 0; c < 16; ++c) {
     const float2 y = fma2(make_float2(x[2 * c], x[2 * c + 1]), mul2, addv);
     const float2 p{ex2(y.x), ex2(y.y)};
     l[c & 1] = add2(l[c & 1], p);
     pk[c] = F16 ? pack_f16x2(p.x, p.y) : pack_bf16x2(p.x, p.y);
   }
-  const float2 s = add2(l[0], l[1]);
-  return s.x + s.y;
 }
 
 // 32 channels of a row, rounded to the call's type.
@@ -190,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_ofree = [&](int t) { return smem_u32(&bars[30 + t]); };    // ... and read out
   auto bar_l = [&](int t) { return smem_u32(&bars[32 + t]); };        // 1 / l of the piece written
   auto bar_drain = [&](int t) { return smem_u32(&bars[34 + t]); };
+  auto bar_pdrain = [&](int t) { return smem_u32(&bars[36 + t]); };
   const uint32_t bar_st = smem_u32(&bars[38]), bar_stfree = smem_u32(&bars[39]);  // O tile staged / copied out
   auto bar_rfull = [&](int i) { return smem_u32(&bars[40 + i]); };    // 8-bit block landed
   auto bar_rempty = [&](int i) { return smem_u32(&bars[44 + i]); };   // ... and converted
@@ -217,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_ofree(t), 128);
       mbar_init(bar_l(t), 128);
       mbar_init(bar_drain(t), 1);
+      mbar_init(bar_pdrain(t), 1);
     }
     for (int i = 0; i < L::kRawStages; ++i) {
       mbar_init(bar_rfull(i), 1);
@@ -236,6 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   const int tp = plan.tp;  // tiles per segment
   auto active = [&](const Piece& x, int t) { return t < tp && x.pair * tp + t < plan.tiles; };
+  // K's or V's stages of a piece, free as far as a tile without rows goes.  Every phase of bar_full is
+  // waited for: a warp that skipped one would take the phase before it for its own.
+  auto pass_stages = [&](uint32_t r, int nb) {
+    for (int i = 0; i < nb; ++i, r += 2) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_full(r % kStages), (r / kStages) & 1, wc))) return false;
+      if (lane == 0) mbar_arrive(bar_empty(r % kStages));
+    }
+    return true;
+  };
   if (a.kv_len && blockIdx.x == 0 && warp == 3) {
     for (int b = lane; b < s.B; b += 32)
       if (a.kv_len[b] < 0 || a.kv_len[b] > s.M) report_error(a.status, kDevErrBounds);
@@ -313,33 +316,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(bar_rfull(v % L::kRawStages), (v / L::kRawStages) & 1, abort_flag);
     }
   } else if (warp == 1 || warp == 2) {
-    // ------------------------------------------------------------------ MMA issuer of tile t
+    // ------------------------------------------------------------------ issuer of S of tile t
     PieceIter it(s, plan, a.kv_len);
-    constexpr uint32_t idO = idesc_f32acc(128, D, false, true, !kMmaF16);
     const int t = warp - 1;
     const uint64_t qd = smem_desc(sbase + t * L::kTile, 16, 1024);
     bool ok = true;
     uint32_t r = 0, c = 0, pc = 0;  // ring loads of earlier pieces; half blocks and pieces done
     Piece x;
     while (ok && it.next(x)) {
-      if (!active(x, t)) {  // the stages are free as far as this tile goes
-        for (int i = 0; ok && i < 2 * x.nb; ++i, ++r) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_full(r % kStages), (r / kStages) & 1, wc));
-          if (ok && lane == 0) mbar_arrive(bar_empty(r % kStages));
-        }
+      if (!active(x, t)) {
+        ok = pass_stages(r, x.nb);
+        r += 2 * x.nb;
         continue;
       }
       const int keys = min(x.nb * kKeyBlock, x.keys - x.k0 * kKeyBlock);
       const int halves = (keys + 63) >> 6;
-      // S of half block i, into buffer (c + i) & 1, whose P V two half blocks ago has completed
-      auto issue_s = [&](int i) {
-        const uint32_t rk = r + (i & ~1), ci = c + i, u = ci & 1;
+      // into buffer c & 1, whose P V two half blocks ago has completed
+      for (int i = 0; i < halves; ++i, ++c) {
+        const uint32_t rk = r + (i & ~1), u = c & 1;
         const int ks = rk % kStages;
         const bool last = i + 1 == halves;
-        if (!__all_sync(0xffffffffu, ((i & 1) || mbar_wait(bar_full(ks), (rk / kStages) & 1, wc)) &&
+        ok = __all_sync(0xffffffffu, ((i & 1) || mbar_wait(bar_full(ks), (rk / kStages) & 1, wc)) &&
                                          (i > 0 || mbar_wait(bar_qfull(t), pc & 1, wc)) &&
-                                         (ci < 2 || mbar_wait(bar_pv(t, u), ((ci >> 1) - 1) & 1, wc))))
-          return false;
+                                         (c < 2 || mbar_wait(bar_pv(t, u), ((c >> 1) - 1) & 1, wc)));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t idS = idesc_f32acc(128, min(64, (keys - 64 * i + 15) & ~15), false, false, !kMmaF16);
         const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile + (i & 1) * 8192, 16, 1024);
@@ -352,15 +352,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (last) umma_commit(bar_qempty(t));
         }
         __syncwarp();
-        return true;
-      };
-      if (halves > 0) ok = issue_s(0);
-      for (int i = 0; ok && i < halves; ++i) {
-        if (i + 1 < halves) {
-          ok = issue_s(i + 1);
-          if (!ok) break;
-        }
-        const uint32_t rv = r + (i & ~1) + 1, ci = c + i, u = ci & 1;
+      }
+      if (x.nb > 0) ++pc;
+      r += 2 * x.nb;
+    }
+    // no MMA may still run when TMEM is released, on the abort path too
+    if (elect_one()) umma_commit(bar_drain(t));
+    __syncwarp();
+    mbar_drain(bar_drain(t), 0, abort_flag);
+  } else if (warp == 3 || warp == 16) {
+    // ------------------------------------------------------------------ issuer of P V of tile t
+    PieceIter it(s, plan, a.kv_len);
+    constexpr uint32_t idO = idesc_f32acc(128, D, false, true, !kMmaF16);
+    const int t = warp >> 4;
+    bool ok = true;
+    uint32_t r = 0, c = 0, pc = 0;
+    Piece x;
+    while (ok && it.next(x)) {
+      if (!active(x, t)) {
+        ok = pass_stages(r + 1, x.nb);
+        r += 2 * x.nb;
+        continue;
+      }
+      const int keys = min(x.nb * kKeyBlock, x.keys - x.k0 * kKeyBlock);
+      const int halves = (keys + 63) >> 6;
+      for (int i = 0; i < halves; ++i, ++c) {
+        const uint32_t rv = r + (i & ~1) + 1, u = c & 1;
         const int vs = rv % kStages, valid = min(64, keys - 64 * i), steps = (valid + 15) >> 4;
         const bool last = i + 1 == halves;
         ok = __all_sync(0xffffffffu, (i & 1) || mbar_wait(bar_full(vs), (rv / kStages) & 1, wc));
@@ -379,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         ok = __all_sync(0xffffffffu, (i > 0 || pc == 0 || mbar_wait(bar_ofree(t), (pc - 1) & 1, wc)) &&
-                                         mbar_wait(bar_p(t, u), (ci >> 1) & 1, wc));
+                                         mbar_wait(bar_p(t, u), (c >> 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
         const uint64_t vd = smem_desc(sbase + L::kOffKV + vs * L::kTile + (i & 1) * 8192, 16384, 1024);
@@ -393,12 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (x.nb > 0) ++pc;
       r += 2 * x.nb;
-      c += halves;
     }
-    // no MMA may still run when TMEM is released, on the abort path too
-    if (elect_one()) umma_commit(bar_drain(t));
+    if (elect_one()) umma_commit(bar_pdrain(t));
     __syncwarp();
-    mbar_drain(bar_drain(t), 0, abort_flag);
+    mbar_drain(bar_pdrain(t), 0, abort_flag);
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ softmax rows
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
@@ -486,37 +501,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        float y[64];
-        load_scores(ts, y, valid);
-        const float mx = fmaf(max64(y), mul, ev);
         // The exponentials are taken against a maximum of the half blocks before this one, so that they
         // need not wait for this one's: the first uses its own, then O and l follow when the maximum
         // has grown past 2^8.  Only where P would leave its type's range does a half block's own
         // maximum come first (the loop below runs twice).
-        if (i == 0)
-          m_used = mx;
-        else if (__any_sync(0xffffffffu, m_run > m_used + kRescaleThreshold))
+        if (i == 0) {
+          float y[32];
+          load_scores(ts, y, valid);
+          const float m0 = max32(y);
+          load_scores(ts + 32, y, valid - 32);
+          m_used = m_run = fmaf(fmaxf(m0, max32(y)), mul, ev);
+        } else if (__any_sync(0xffffffffu, m_run > m_used + kRescaleThreshold)) {
           ok = rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
-        m_run = i == 0 ? mx : fmaxf(m_run, mx);
+        }
         uint32_t pk[32];
-        float sum, ref;
-        bool low;
-        for (;;) {
-          // cache: scores whose exponent is 2^-64 or less of the reference's (small values beside large
-          // ones) are 0 in P, but count in the sum: relative to their own maximum
+        float sum, ref = m_used;
+        // cache: scores whose exponent is 2^-64 or less of the reference's (small values beside large
+        // ones) are 0 in P, but count in the sum: relative to their own maximum
+        bool low = false;
+        for (bool again = false;;) {
+          float2 part[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          float mx;
+          {
+            float y[32];
+            load_scores(ts, y, valid);
+            mx = max32(y);
+            exp32<kMmaF16>(y, mul, ev - ref, pk, part);
+            load_scores(ts + 32, y, valid - 32);
+            mx = fmaxf(mx, max32(y));
+            exp32<kMmaF16>(y, mul, ev - ref, pk + 16, part);
+          }
+          const float2 both = add2(part[0], part[1]);
+          sum = both.x + both.y;
+          mx = fmaf(mx, mul, ev);
+          m_run = fmaxf(m_run, mx);
+          if (again || !ok) break;
+          low = KV8 && mx < m_used - 64.f;
+          if (!__any_sync(0xffffffffu, low || mx > m_used + kMaxLead)) break;
+          if (__any_sync(0xffffffffu, mx > m_used + kMaxLead)) ok = rescale(fmaxf(mx, m_used));
           low = KV8 && mx < m_used - 64.f;
           ref = low ? mx : m_used;
-          sum = exp64<kMmaF16>(y, mul, ev - ref, pk);
-          if (!ok || !__any_sync(0xffffffffu, low || mx > m_used + kMaxLead)) break;
-          if (!__any_sync(0xffffffffu, mx > m_used + kMaxLead)) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) pk[q] = low ? 0u : pk[q];
-            break;
-          }
-          ok = rescale(fmaxf(mx, m_used));
-          load_scores(ts, y, valid);  // (again, so that the usual path need not keep them)
+          again = true;
         }
         if (!ok) break;
+        if (KV8 && low) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) pk[q] = 0u;
+        }
         tmem_st32(ts, pk);
         tmem_st_wait();
         tc_fence_before();
