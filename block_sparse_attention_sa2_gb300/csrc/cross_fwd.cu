@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int tp = plan.tp;  // tiles per segment
-  auto active = [&](const Piece& x, int t) { return t < tp && x.pair * tp + t < plan.tiles; };
+  auto active = [&](const Piece& x, int t) { return (x.mask >> t) & 1; };
   // K's or V's stages of a piece, free as far as a tile without rows goes.  Every phase of bar_full is
   // waited for: a warp that skipped one would take the phase before it for its own.
   auto pass_stages = [&](uint32_t r, int nb) {
@@ -422,17 +422,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t to = trow + col_o(t);
-    const int tok_r = r / s.G, g = r - tok_r * s.G;
     bool ok = true;
     uint32_t c = 0, pc = 0;
     Piece x;
     while (ok && it.next(x)) {
       if (!active(x, t)) continue;
-      const int n = (x.pair * tp + t) * plan.nb + tok_r;
-      const bool row_valid = tok_r < plan.nb && n < s.N;
-      const int h = x.hk * s.G + g;
-      const int64_t row = ((int64_t)x.b * s.H + h) * s.N + n;
+      // (found again behind the keys, for the registers of the loop between)
+      auto row_of = [&](int& h, int& n) {
+        const int tok_r = r / s.G;
+        n = (x.pair * tp + t) * plan.nb + tok_r;
+        h = x.hk * s.G + r - tok_r * s.G;
+        return tok_r < plan.nb && n < s.N;
+      };
       if (x.nb == 0) {  // (direct mode) no keys
+        int h, n;
+        const bool row_valid = row_of(h, n);
+        const int64_t row = ((int64_t)x.b * s.H + h) * s.N + n;
         if (row_valid) {
           a.lse[row] = -INFINITY;
           if constexpr (KV8) {
@@ -564,6 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      int h, n;
+      const bool row_valid = row_of(h, n);
+      const int64_t row = ((int64_t)x.b * s.H + h) * s.N + n;
       const int64_t slot_row = ((int64_t)blockIdx.x + x.seg) * 256 + t * 128 + r;
       const float lse2 = (KV8 ? l_ref : m_used) + __log2f(l);
       if (row_valid) {
@@ -924,8 +932,8 @@ FwdPlan cross_fwd_plan(const CrossShape& s, int sms) {
   const int blocks = (s.M + kKeyBlock - 1) / kKeyBlock;
   const int64_t paired = heads * ((p.tiles + 1) / 2);
   p.split = blocks >= 8 && paired < 4 * (int64_t)sms;
-  // one tile per CTA while that still finds a free SM
-  p.tp = !p.split && paired < sms ? 1 : 2;
+  // one tile per CTA while each finds an SM of its own
+  p.tp = !p.split && heads * p.tiles <= sms ? 1 : 2;
   p.pairs = (p.tiles + p.tp - 1) / p.tp;
   const int64_t segs = heads * p.pairs;
   p.segs = segs > INT32_MAX ? -1 : (int)segs;

@@ -36,18 +36,27 @@ struct Piece {
   int b, hk, pair, seg;
   int k0, nb;
   int keys;  // of the sequence
+  int mask;  // tiles of the pair that the piece is for: 1, 2 or 3 (0: none left of its pair)
 };
+
+// Direct mode: segments that do not fill a last round of the grid, and whose tiles can go one by one
+// without another round, are taken so: a single tile takes two thirds of a pair's time.
+__device__ __forceinline__ int single_segs(const FwdPlan& p) {
+  const int rest = p.segs % p.grid;
+  return !p.split && p.tp == 2 && 2 * rest <= p.grid ? rest : 0;
+}
 
 struct PieceIter {
   const CrossShape& s;
   const FwdPlan& p;
   const int32_t* kv_len;
   int64_t g, g_end;  // split: the CTA's run of blocks; direct: the next segment in g
+  int paired;        // direct: segments taken whole
   int b;             // split: sequence of block g, and the blocks before it
   int64_t base;
 
   __device__ __forceinline__ PieceIter(const CrossShape& s_, const FwdPlan& p_, const int32_t* kv_len_)
-      : s(s_), p(p_), kv_len(kv_len_), b(0), base(0) {
+      : s(s_), p(p_), kv_len(kv_len_), paired(0), b(0), base(0) {
     if (p.split) {
       const int64_t total = total_key_blocks(s, kv_len, p.pairs, p.shift);
       const int64_t run = run_length(total, p.grid);
@@ -55,14 +64,18 @@ struct PieceIter {
       g_end = g + run < total ? g + run : total;
     } else {
       g = blockIdx.x;
-      g_end = p.segs;
+      const int single = single_segs(p);
+      paired = p.segs - single;
+      g_end = p.segs + single;
     }
   }
   __device__ __forceinline__ bool next(Piece& x) {
     if (g >= g_end) return false;
     const int per_b = s.Hkv * p.pairs;
     if (!p.split) {
-      x.seg = (int)g;
+      const int k = (int)g - paired;
+      x.seg = k < 0 ? (int)g : paired + (k >> 1);
+      x.mask = k < 0 ? 3 : 1 << (k & 1);
       x.b = x.seg / per_b;
       x.keys = key_count(kv_len, x.b, s.M);
       x.k0 = 0;
@@ -83,10 +96,12 @@ struct PieceIter {
       const int64_t left = g_end - g;
       x.nb = nk - x.k0 < left ? nk - x.k0 : (int)left;
       g += x.nb;
+      x.mask = 3;
     }
     const int in_b = x.seg - x.b * per_b;
     x.hk = in_b / p.pairs;
     x.pair = in_b - x.hk * p.pairs;
+    if (p.tp == 1 || 2 * x.pair + 1 == p.tiles) x.mask &= 1;
     return true;
   }
 };

@@ -83,6 +83,15 @@ def test_many_segments_per_cta(sa2):
     run(sa2, *tensors(3, 24, 8, 1000, 300, 128, torch.bfloat16, seed=10), kv_len=[300, 13, 256])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv_len", [None, [300, 0], [1, 129]])
+def test_last_round_of_single_tiles(sa2, kv_len, d):
+    """A few tile pairs more than SMs: those go tile by tile, the last pair of each head has one tile only."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    pairs = (sms + 12) // 4  # times 2 x 2 heads: 8 to 12 segments behind the first round
+    run(sa2, *tensors(2, 2, 2, (2 * pairs - 1) * 128 - 5, 300, d, torch.bfloat16, seed=21), kv_len=kv_len)
+
+
 def test_token_major_tensors(sa2):
     run(sa2, *tensors(2, 8, 4, 333, 190, 128, torch.bfloat16, seed=4, token_major=True), kv_len=[190, 100])
 
