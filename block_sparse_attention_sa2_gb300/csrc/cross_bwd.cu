@@ -111,12 +111,13 @@ __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan 
 // S_{j+1} needs only that the row threads have read S_j (dQ_{j-1} runs meanwhile), dP_{j+1} that
 // dQ_{j-1} has completed (S_{j+1} runs meanwhile; dP has two buffers), and dQ_j has a whole period of
 // three products for dS_j to be made in.
-// Roles: warp 0 TMA, warps 1, 3 and 2 issuers of S, dP and dQ, warps 4..11 row threads (two per row: keys
-// 0..63 and 64..127 of each block), warps 12..15 epilogue.
+// Roles: warp 0 TMA; warps 1, 3 and 2 issuers of S, dP and dQ; 8 (d = 128) or 16 (d = 64) warps of row threads,
+// two or four per row (d = 64, 19 heads x 8192 x 4096: two 254 us, four 188); 4 warps epilogue.
 // TMEM columns: S 0, dP 128 and 256, dQ 384.
-constexpr int kDqThreads = 512;
 template <int D>
 struct DqSmem {
+  static constexpr int kRowWarps = D == 128 ? 8 : 16;
+  static constexpr int kThreads = 32 * (4 + kRowWarps + 4);
   static constexpr int kPanels = D / 64;
   static constexpr int kTile = 128 * 128 * kPanels;
   static constexpr int kKStages = 3, kVStages = 2;
@@ -130,7 +131,7 @@ struct DqSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kDqThreads, 1)
+__global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, CrossShape s,
                     BwdPlan plan, CrossBwdArgs a) {
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       mbar_init(bar_vfull(i), 1);
       mbar_init(bar_vempty(i), 1);
       mbar_init(bar_dp(i), 1);
-      mbar_init(bar_ds(i), 256);
+      mbar_init(bar_ds(i), 32 * L::kRowWarps);
       mbar_init(bar_dqm(i), 1);
     }
     mbar_init(bar_q, 1);
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     mbar_init(bar_do, 1);
     mbar_init(bar_dofree, 1);
     mbar_init(bar_s, 1);
-    mbar_init(bar_sfree, 256);
+    mbar_init(bar_sfree, 32 * L::kRowWarps);
     mbar_init(bar_dq, 1);
     mbar_init(bar_dqfree, 128);
     mbar_init(bar_drain, 1);
@@ -360,10 +361,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if (elect_one()) umma_commit(bar_gdrain);
     __syncwarp();
     mbar_drain(bar_gdrain, 0, abort_flag);
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < 4 + L::kRowWarps) {
     // ------------------------------------------------------------------ row threads
     if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
-    const int g = (warp - 4) >> 2;  // keys 64 g .. 64 g + 63 of each block
+    constexpr int kKeys = 512 / L::kRowWarps;  // of each block, for this thread
+    const int k0 = kKeys * ((warp - 4) >> 2);
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     bool ok = true;
@@ -374,42 +376,49 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const float lse2 = a.stats[i * 256 + r], Dr = a.stats[i * 256 + 128 + r];
       for (int j = 0; j < x.nk; ++j, ++J) {
         const int bb = J & 1;
-        const int valid = x.keys - j * kKeyBlock - 64 * g;  // of this thread's 64 keys
+        const int valid = x.keys - j * kKeyBlock - k0;  // of this thread's keys
         if (!__all_sync(0xffffffffu, mbar_wait(bar_s, J & 1, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t u0[32], u1[32];
-        tmem_ld32(trow + kS + 64 * g, u0);
-        tmem_ld32(trow + kS + 64 * g + 32, u1);
-        tmem_ld_wait(u0);
-        tmem_ld_wait(u1);
+        uint32_t u[kKeys / 32][32];
+        float p[kKeys];
+#pragma unroll
+        for (int h = 0; h < kKeys / 32; ++h) tmem_ld32(trow + kS + k0 + 32 * h, u[h]);
+#pragma unroll
+        for (int h = 0; h < kKeys / 32; ++h) tmem_ld_wait(u[h]);
         tc_fence_before();
         mbar_arrive(bar_sfree);
-        float p[64];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          p[c] = ex2(fmaf(__uint_as_float(u0[c]), a.scale_log2, -lse2));
-          p[c + 32] = ex2(fmaf(__uint_as_float(u1[c]), a.scale_log2, -lse2));
-        }
+        for (int c = 0; c < kKeys; ++c) p[c] = ex2(fmaf(__uint_as_float(u[c >> 5][c & 31]), a.scale_log2, -lse2));
         if (!__all_sync(0xffffffffu, mbar_wait(bar_dp(bb), (J >> 1) & 1, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t tdp = trow + kDP + bb * 128 + 64 * g;
+        const uint32_t tdp = trow + kDP + bb * 128 + k0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kKeys / 32; ++h) {
           uint32_t pk[16];
-          tmem_ld32(tdp + 32 * h, u0);
-          tmem_ld_wait(u0);
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            // behind the last key dP may be anything
-            const float d0 = 32 * h + c < valid ? p[32 * h + c] * (__uint_as_float(u0[c]) - Dr) : 0.f;
-            const float d1 = 32 * h + c + 1 < valid ? p[32 * h + c + 1] * (__uint_as_float(u0[c + 1]) - Dr) : 0.f;
-            pk[c / 2] = pack_bf16x2(d0, d1);
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[16];
+            tmem_ld16(tdp + 32 * h + 16 * q, v);
+            tmem_ld_wait16(v);
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const int k = 32 * h + 16 * q + c;
+              const float d0 = p[k] * (__uint_as_float(v[c]) - Dr), d1 = p[k + 1] * (__uint_as_float(v[c + 1]) - Dr);
+              pk[(16 * q + c) / 2] = pack_bf16x2(d0, d1);
+            }
+          }
+          if (valid < 32 * (h + 1)) {  // behind the last key dP may be anything
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const int left = valid - 32 * h - 2 * c;
+              pk[c] = left > 1 ? pk[c] : (left > 0 ? pk[c] & 0xFFFFu : 0u);
+            }
           }
           tmem_st16(tdp + 32 * h, pk);
         }
@@ -418,7 +427,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         mbar_arrive(bar_ds(bb));
       }
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + L::kRowWarps) {
     // ------------------------------------------------------------------ epilogue
     const int r = 32 * (warp & 3) + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
@@ -998,7 +1007,7 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
   cross_dkdv_join_kernel<D><<<dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv)), 256, 0, st>>>(s, p, a);
   prof_stop(st, kAttnBwd);
   prof_start(st, kAttnBwdDq);
-  dq<<<(unsigned)p.dq_grid, kDqThreads, DqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
+  dq<<<(unsigned)p.dq_grid, DqSmem<D>::kThreads, DqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
   prof_stop(st, kAttnBwdDq);
   return cudaGetLastError();
 }
