@@ -449,14 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // cache: scores are q8 scale * k8 scale * (q . k) and V's scale enters as an exponent
       float qscale = a.scale_log2;
-      const float *ksp = nullptr, *vsp = nullptr;
+      int64_t sc = 0;  // of the piece's first half block
       float nks = 1.f, nvs = 1.f;  // of the next half block, loaded one ahead
       if constexpr (KV8) {
-        const int64_t off = ((int64_t)x.b * s.Hkv + x.hk) * cache.nsb;
-        ksp = cache.ks + off;
-        vsp = cache.vs + off;
-        nks = ksp[2 * x.k0];
-        nvs = vsp[2 * x.k0];
+        sc = ((int64_t)x.b * s.Hkv + x.hk) * cache.nsb + 2 * x.k0;
+        nks = cache.ks[sc];
+        nvs = cache.vs[sc];
         if (!__all_sync(0xffffffffu, mbar_wait(bar_qfull(t), pc & 1, wc))) {
           ok = false;
           break;
@@ -497,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mul *= nks;
           ev = (float)((int)(__float_as_uint(nvs) >> 23) - 127);
           if (valid > 64) {
-            nks = ksp[2 * x.k0 + i + 1];
-            nvs = vsp[2 * x.k0 + i + 1];
+            nks = cache.ks[sc + i + 1];
+            nvs = cache.vs[sc + i + 1];
           }
         }
         if (!__all_sync(0xffffffffu, mbar_wait(bar_s(t, u), (c >> 1) & 1, wc))) {
