@@ -48,58 +48,51 @@ __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint64_t b, uin
 
 // ------------------------------------------------------------------------- statistics
 //
-// D and log2(e) * LSE of every query row.  One CTA per query tile, D / 16 threads per row, every load
-// of a thread (16 times 16 bytes at d = 128) in flight at once: bound by the bytes of dO and O.
+// D and log2(e) * LSE of every query row: D / 16 threads per row, one row each, grid (query tiles,
+// 128 / rows of a CTA).  Bound by the bytes of dO and O: 12 heads x 32760, d = 128: 33 us, 6.1 TB/s (with
+// a whole tile per CTA, four rows per thread, 44: too few CTAs on an SM to cover the others' ends).
+template <int D>
+constexpr int kStatsRows = 256 / (D / 16);
 template <int D>
 __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
   constexpr int kLanes = D / 16;
-  constexpr int kRows = 256 / kLanes;    // rows per pass
-  constexpr int kPasses = 128 / kRows;
   const int head = blockIdx.x / plan.tiles, tile = blockIdx.x - head * plan.tiles;
   const int b = head / s.Hkv, hk = head - b * s.Hkv;
   const int ch = (threadIdx.x % kLanes) * 16;
-  const int r0 = threadIdx.x / kLanes;
-  const uint16_t* dop = static_cast<const uint16_t*>(a.dO.p) + b * a.dO.sb + (int64_t)hk * s.G * a.dO.sh + ch;
-  const uint16_t* op = static_cast<const uint16_t*>(a.o.p) + b * a.o.sb + (int64_t)hk * s.G * a.o.sh + ch;
-  float* rec = a.stats + (int64_t)blockIdx.x * 256;
-  uint4 x[kPasses][2], y[kPasses][2];
-  float lse[kPasses];
+  const int r = threadIdx.x / kLanes + blockIdx.y * kStatsRows<D>;
+  const int tok_r = r / s.G, g = r - tok_r * s.G;
+  const int n = tile * plan.nb + tok_r;
+  uint4 x[2], y[2];
+  x[0] = x[1] = y[0] = y[1] = make_uint4(0, 0, 0, 0);
+  float lse = INFINITY;
+  if (tok_r < plan.nb && n < s.N) {
+    const uint4* px = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dO.p) + b * a.dO.sb +
+                                                     (int64_t)(hk * s.G + g) * a.dO.sh + n * a.dO.sn + ch);
+    const uint4* py = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.p) + b * a.o.sb +
+                                                     (int64_t)(hk * s.G + g) * a.o.sh + n * a.o.sn + ch);
+    x[0] = __ldg(px);
+    x[1] = __ldg(px + 1);
+    y[0] = __ldg(py);
+    y[1] = __ldg(py + 1);
+    if (ch == 0) lse = a.lse[((int64_t)b * s.H + hk * s.G + g) * s.N + n];
+  }
+  float acc = 0.f;
 #pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    const int r = r0 + u * kRows, tok_r = r / s.G, g = r - tok_r * s.G;
-    const int n = tile * plan.nb + tok_r;
-    x[u][0] = x[u][1] = y[u][0] = y[u][1] = make_uint4(0, 0, 0, 0);
-    lse[u] = INFINITY;
-    if (tok_r < plan.nb && n < s.N) {
-      const uint4* px = reinterpret_cast<const uint4*>(dop + g * a.dO.sh + n * a.dO.sn);
-      const uint4* py = reinterpret_cast<const uint4*>(op + g * a.o.sh + n * a.o.sn);
-      x[u][0] = __ldg(px);
-      x[u][1] = __ldg(px + 1);
-      y[u][0] = __ldg(py);
-      y[u][1] = __ldg(py + 1);
-      if (ch == 0) lse[u] = a.lse[((int64_t)b * s.H + hk * s.G + g) * s.N + n];
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    const uint32_t ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      acc = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(ys[q] << 16), acc);
+      acc = fmaf(__uint_as_float(xs[q] & 0xFFFF0000u), __uint_as_float(ys[q] & 0xFFFF0000u), acc);
     }
   }
 #pragma unroll
-  for (int u = 0; u < kPasses; ++u) {
-    float acc = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t xs[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
-      const uint32_t ys[4] = {y[u][i].x, y[u][i].y, y[u][i].z, y[u][i].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(ys[q] << 16), acc);
-        acc = fmaf(__uint_as_float(xs[q] & 0xFFFF0000u), __uint_as_float(ys[q] & 0xFFFF0000u), acc);
-      }
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (ch == 0) {
-      const int r = r0 + u * kRows;
-      rec[r] = lse[u] * 1.4426950408889634f;
-      rec[128 + r] = acc;
-    }
+  for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (ch == 0) {
+    float* rec = a.stats + (int64_t)blockIdx.x * 256;
+    rec[r] = lse * 1.4426950408889634f;
+    rec[128 + r] = acc;
   }
 }
 
@@ -1000,7 +993,7 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
   if (e == cudaSuccess) e = allow_smem(dkv, DkvSmem<D>::kBytes, dkv_allowed);
   if (e != cudaSuccess) return e;
   prof_start(st, kBwdPre);
-  cross_stats_kernel<D><<<(unsigned)((int64_t)s.B * s.Hkv * p.tiles), 256, 0, st>>>(s, p, a);
+  cross_stats_kernel<D><<<dim3((unsigned)((int64_t)s.B * s.Hkv * p.tiles), 128 / kStatsRows<D>), 256, 0, st>>>(s, p, a);
   prof_stop(st, kBwdPre);
   prof_start(st, kAttnBwd);
   dkv<<<(unsigned)p.grid, DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
