@@ -934,7 +934,9 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
 }
 
 // Adds the parts of key blocks whose tiles several runs shared, in run order, and writes zeros
-// behind the last key block of each sequence.  Grid (key blocks of M, B * Hkv).
+// behind the last key block of each sequence.  Grid (key blocks of M, B * Hkv, 8): an eighth of a block
+// each, since a head has few (12 heads x 32760 x 512: the whole backward 314 us, with one CTA per block 322).
+constexpr int kJoinParts = 8;
 template <int D>
 __global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
   const int kb = blockIdx.x, lane = threadIdx.x & 31;
@@ -962,7 +964,9 @@ __global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdP
     }
     if (count == 1) return;  // one CTA had all of its tiles
   }
-  for (int i = threadIdx.x; i < 2 * 128 * (D / 8); i += 256) {
+  constexpr int kItems = 2 * 128 * (D / 8) / kJoinParts;
+  for (int j = threadIdx.x; j < kItems; j += 256) {
+    const int i = blockIdx.z * kItems + j;
     const int w = i / (128 * (D / 8)), r = i / (D / 8) % 128, ch = i % (D / 8) * 8;
     const int key = kb * kKeyBlock + r;
     if (key >= s.M) continue;
@@ -997,7 +1001,7 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
   prof_stop(st, kBwdPre);
   prof_start(st, kAttnBwd);
   dkv<<<(unsigned)p.grid, DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
-  cross_dkdv_join_kernel<D><<<dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv)), 256, 0, st>>>(s, p, a);
+  cross_dkdv_join_kernel<D><<<dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv), kJoinParts), 256, 0, st>>>(s, p, a);
   prof_stop(st, kAttnBwd);
   prof_start(st, kAttnBwdDq);
   dq<<<(unsigned)p.dq_grid, DqSmem<D>::kThreads, DqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);

@@ -8,9 +8,11 @@
 // other's products.  A tile's rows are the tokens of all G query heads that share the key head
 // (row = token * G + head), which lets few tokens of many heads fill a tile.
 //
-// Roles (512 threads): warp 0 TMA producer (Q tiles, a ring of K and V blocks of 128 keys); warps 1
-// and 2 issuers of the MMAs of tile 0 and 1; warps 4..7 epilogue (16-bit keys) or converters (8-bit
-// keys: from blocks as they lie in the cache to fp16 in the ring, and Q to fp16); warps 8..11 and
+// Roles (544 threads): warp 0 TMA producer (Q tiles, a ring of K and V blocks of 128 keys); warps 1 and
+// 2 issuers of S of tile 0 and 1, warps 3 and 16 of their P V (an issuer's waits and bookkeeping take 200
+// to 400 cycles beside the softmax warps: with S and P V of a tile in one warp they were the bound, 12
+// heads x 32760 x 512, d = 128: 106 us, apart 98); warps 4..7 epilogue (16-bit keys) or converters
+// (8-bit keys: from blocks as they lie in the cache to fp16 in the ring, and Q to fp16); warps 8..11 and
 // 12..15 the softmax of tile 0 and 1, one row per thread.
 // A tile goes through its keys in half blocks of 64, with two S buffers:
 //   S_t(i) = Q_t K_i^T   M = 128, N = 64, K = d   (shared memory, K-major)
@@ -19,6 +21,9 @@
 // completed.  With blocks of 128 keys TMEM has room for one S per tile only, and S, softmax and P V
 // are one chain: 3300 to 5000 cycles per 128 keys and tile pair, by how the two tiles happened to fall
 // in step, against 2560 of shared-memory reads for the products here.
+// Bound now: d = 128 by the products and, in long runs, the power limit (24 heads x 8192 x 4096: 313 us, 1310
+// TFLOP/s at 1350 W); d = 64 by the softmax threads (1370 cycles per half block, two of them per scheduler,
+// most of it latency; the exponentials are 512 of them: without them it is no faster).
 //
 // The last block of a sequence may be partial.  Its products run over the valid keys rounded up
 // to 16; scores behind the last key are replaced by -inf (whatever they are: NaN too), and up to
@@ -802,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of split segments: O = sum_i 2^(l_i - m) O_i / sum_i 2^(l_i - m) over a segment's
 // parts in key order, l_i their log2 sums and m the largest; LSE = ln 2 (m + log2 sum).  Rows of
-// sequences without keys get 0 and -inf.  One warp per row; grid (segments, rows / 16), 16 rows each.
+// sequences without keys get 0 and -inf.  One warp per row; grid (segments, parts of their rows).
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan plan, CrossFwdArgs a) {
   constexpr int kPer = D / 32;
@@ -817,8 +822,9 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
   const int nk = key_blocks(key_count(a.kv_len, b, s.M), plan.shift);
   const int64_t g0 = base * per_b + (int64_t)(seg - b * per_b) * nk;
   const int c0 = (int)(g0 / run), c1 = nk > 0 ? (int)((g0 + nk - 1) / run) : c0 - 1;
-  for (int i = warp; i < 16; i += 8) {
-    const int rr = blockIdx.y * 16 + i, t = rr >> 7, r = rr & 127;
+  const int rows = min(plan.tp * 128, plan.rows) / gridDim.y;
+  for (int i = warp; i < rows; i += 8) {
+    const int rr = blockIdx.y * rows + i, t = rr >> 7, r = rr & 127;
     const int tile = pair * plan.tp + t;
     if (t >= plan.tp || tile >= plan.tiles) return;
     const int tok_r = r / s.G, g = r - tok_r * s.G, n = tile * plan.nb + tok_r, h = hk * s.G + g;
@@ -842,7 +848,8 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
         float v[8][kPer];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const float* src = a.part_o + (((int64_t)base + min(k + u, n32 - 1) + seg) * plan.rows + rr) * D;
+          if (k + u >= n32) break;
+          const float* src = a.part_o + (((int64_t)base + k + u + seg) * plan.rows + rr) * D;
           if constexpr (kPer == 4)
             *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src + lane * 4);
           else
@@ -941,7 +948,10 @@ FwdPlan cross_fwd_plan(const CrossShape& s, int sms) {
 }
 
 cudaError_t launch_cross_join(const CrossShape& s, const FwdPlan& p, const CrossFwdArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)p.segs, (unsigned)((p.tp * 128 < p.rows ? p.tp * 128 : p.rows) / 16));
+  // 16 rows per CTA while that is needed to fill the SMs, then 64 (finding a segment's parts takes a
+  // warp as long as two rows)
+  const int rows = std::min(p.tp * 128, p.rows), per = p.segs * (rows / 16) > 8 * 152 && rows >= 64 ? 64 : 16;
+  const dim3 grid((unsigned)p.segs, (unsigned)(rows / per));
   const bool f16 = s.dtype == SA2_FP16;
   prof_start(st, kAttnFwd);
   if (s.d == 128)
