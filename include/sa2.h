@@ -403,8 +403,11 @@ sa2_status sa2_cache8_attn(const sa2_cross_shape* shape, const sa2_tensor* q, co
  * sa2_profiler_collect waits for the recorded events, writes up to max_entries records
  * (one per kernel of the library: name, launches, summed device milliseconds) and clears
  * them; it returns the number of records written, or -1 when an event could not be read.
- * With out == NULL it returns the number of kernels and leaves the records in place.  Not thread-safe against concurrent
- * launches from several host threads on different streams of the same kernel.
+ * With out == NULL it returns the number of kernels and leaves the records in place.  Not
+ * thread-safe against concurrent launches from several host threads on different streams of
+ * the same kernel.  The cross and cache calls are counted under the names of their kind:
+ * attn_fwd (with the join of parts), to_f16 (append and read), bwd_preprocess, attn_bwd_dkdv
+ * (with its join) and attn_bwd_dq.
  */
 typedef struct sa2_kernel_time {
   const char* name; /* static string */
