@@ -56,6 +56,7 @@ constexpr int kStatsRows = 256 / (D / 16);
 template <int D>
 __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
   constexpr int kLanes = D / 16;
+  kernel_trigger();
   const int head = blockIdx.x / plan.tiles, tile = blockIdx.x - head * plan.tiles;
   const int b = head / s.Hkv, hk = head - b * s.Hkv;
   const int ch = (threadIdx.x % kLanes) * 16;
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  kernel_wait();
   const int64_t items = (int64_t)s.B * s.Hkv * plan.tiles;
   struct Item {
     int b, hk, tile, keys, nk;
@@ -670,6 +672,8 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  kernel_trigger();
+  kernel_wait();
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
@@ -939,6 +943,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
 constexpr int kJoinParts = 8;
 template <int D>
 __global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
+  kernel_trigger();
   const int kb = blockIdx.x, lane = threadIdx.x & 31;
   const int b = blockIdx.y / s.Hkv, hk = blockIdx.y - b * s.Hkv;
   const int keys = key_count(a.kv_len, b, s.M), nk = key_blocks(keys);
@@ -962,8 +967,9 @@ __global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdP
       c0 = (int)(g0 / run);
       count = (int)((g0 + plan.tiles - 1) / run) - c0 + 1;
     }
-    if (count == 1) return;  // one CTA had all of its tiles
   }
+  kernel_wait();  // (by every CTA: the dQ kernel waits for this one alone)
+  if (count == 1) return;  // one CTA had all of its tiles
   constexpr int kItems = 2 * 128 * (D / 8) / kJoinParts;
   for (int j = threadIdx.x; j < kItems; j += 256) {
     const int i = blockIdx.z * kItems + j;
@@ -999,14 +1005,19 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
   prof_start(st, kBwdPre);
   cross_stats_kernel<D><<<dim3((unsigned)((int64_t)s.B * s.Hkv * p.tiles), 128 / kStatsRows<D>), 256, 0, st>>>(s, p, a);
   prof_stop(st, kBwdPre);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   prof_start(st, kAttnBwd);
-  dkv<<<(unsigned)p.grid, DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
-  cross_dkdv_join_kernel<D><<<dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv), kJoinParts), 256, 0, st>>>(s, p, a);
+  e = launch_early(dkv, dim3((unsigned)p.grid), DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
+  if (e == cudaSuccess)
+    e = launch_early(cross_dkdv_join_kernel<D>, dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv), kJoinParts), 256, 0,
+                     st, s, p, a);
   prof_stop(st, kAttnBwd);
+  if (e != cudaSuccess) return e;
   prof_start(st, kAttnBwdDq);
-  dq<<<(unsigned)p.dq_grid, DqSmem<D>::kThreads, DqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, s, p, a);
+  e = launch_early(dq, dim3((unsigned)p.dq_grid), DqSmem<D>::kThreads, DqSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
   prof_stop(st, kAttnBwdDq);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace

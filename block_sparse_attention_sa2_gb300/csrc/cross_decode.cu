@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
     for (int b = tid; b < s.B; b += kThreads)
       if (a.kv_len[b] < 0 || a.kv_len[b] > s.M) report_error(a.status, kDevErrBounds);
 
+  if (plan.split) kernel_trigger();
   PieceIter it(s, plan, a.kv_len);
   Piece x;
   while (it.next(x)) {

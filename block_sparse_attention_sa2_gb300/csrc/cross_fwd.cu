@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (plan.split) kernel_trigger();
   const int tp = plan.tp;  // tiles per segment
   auto active = [&](const Piece& x, int t) { return (x.mask >> t) & 1; };
   // K's or V's stages of a piece, free as far as a tile without rows goes.  Every phase of bar_full is
@@ -823,6 +824,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
   const int64_t g0 = base * per_b + (int64_t)(seg - b * per_b) * nk;
   const int c0 = (int)(g0 / run), c1 = nk > 0 ? (int)((g0 + nk - 1) / run) : c0 - 1;
   const int rows = min(plan.tp * 128, plan.rows) / gridDim.y;
+  kernel_wait();
   for (int i = warp; i < rows; i += 8) {
     const int rr = blockIdx.y * rows + i, t = rr >> 7, r = rr & 127;
     const int tile = pair * plan.tp + t;
@@ -954,14 +956,11 @@ cudaError_t launch_cross_join(const CrossShape& s, const FwdPlan& p, const Cross
   const dim3 grid((unsigned)p.segs, (unsigned)(rows / per));
   const bool f16 = s.dtype == SA2_FP16;
   prof_start(st, kAttnFwd);
-  if (s.d == 128)
-    f16 ? cross_join_kernel<128, true><<<grid, 256, 0, st>>>(s, p, a)
-        : cross_join_kernel<128, false><<<grid, 256, 0, st>>>(s, p, a);
-  else
-    f16 ? cross_join_kernel<64, true><<<grid, 256, 0, st>>>(s, p, a)
-        : cross_join_kernel<64, false><<<grid, 256, 0, st>>>(s, p, a);
+  const auto kern = s.d == 128 ? (f16 ? cross_join_kernel<128, true> : cross_join_kernel<128, false>)
+                               : (f16 ? cross_join_kernel<64, true> : cross_join_kernel<64, false>);
+  const cudaError_t e = launch_early(kern, grid, 256, 0, st, s, p, a);
   prof_stop(st, kAttnFwd);
-  return cudaGetLastError();
+  return e;
 }
 
 size_t cross_fwd_partials(const CrossShape& s, const FwdPlan& p) {

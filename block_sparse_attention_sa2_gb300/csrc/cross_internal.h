@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <utility>
 
 #include "sa2_internal.h"
 
@@ -105,6 +106,24 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& don
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
+}
+
+// A launch that may begin while the kernel before it on the stream, once all of that one's CTAs have
+// called kernel_trigger(), still runs: it calls kernel_wait() before it touches what that kernel (or
+// one before it) writes.  Between the kernels of one call only: the last one of a call never triggers.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = st;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, std::forward<A>(args)...);
 }
 
 // The device's status word, and the wait settings of the calling thread's next launches

@@ -6,6 +6,10 @@
 
 namespace sa2 {
 
+// See launch_early.
+__device__ __forceinline__ void kernel_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void kernel_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Keys of sequence b, clamped to [0, M].
 __device__ __forceinline__ int key_count(const int32_t* kv_len, int b, int M) {
   const int n = kv_len ? kv_len[b] : M;
