@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
         float al[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const float m = fmaxf(m_used[hf], mx[hf]);
-          al[hf] = ex2(m_used[hf] - m);
+          // (a row's reference follows from its own scores only)
+          const float m = mx[hf] > m_used[hf] + kRescaleThreshold ? mx[hf] : m_used[hf];
+          al[hf] = m == m_used[hf] ? 1.f : ex2(m_used[hf] - m);
           if constexpr (!KV8) l[hf] *= al[hf];
           m_used[hf] = m;
         }

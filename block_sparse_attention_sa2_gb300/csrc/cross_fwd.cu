@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto rescale = [&](float m_new) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar_pv(t, (c & 1) ^ 1), ((c - 1) >> 1) & 1, wc))) return false;
         tc_fence_after();
-        const float alpha = ex2(m_used - m_new);
+        const float alpha = m_new == m_used ? 1.f : ex2(m_used - m_new);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 16) {
           uint32_t o[16];
@@ -547,7 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (again || !ok) break;
           low = KV8 && mx < m_used - 64.f;
           if (!__any_sync(0xffffffffu, low || mx > m_used + kMaxLead)) break;
-          if (__any_sync(0xffffffffu, mx > m_used + kMaxLead)) ok = rescale(fmaxf(mx, m_used));
+          // (a row's reference follows from its own scores only: neighbours, and rows of the tile that are no
+          // query's, must not change its roundings)
+          if (__any_sync(0xffffffffu, mx > m_used + kMaxLead)) ok = rescale(mx > m_used + kMaxLead ? mx : m_used);
           low = KV8 && mx < m_used - 64.f;
           ref = low ? mx : m_used;
           again = true;

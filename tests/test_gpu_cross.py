@@ -125,6 +125,45 @@ def test_scale_and_large_scores(sa2):
     run(sa2, torch.ones_like(q), (ramp * torch.ones_like(k)).contiguous(), v, scale=1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_level_of_the_first_scores(sa2, d, dtype):
+    """Rows whose first 64 scores lie far from 0, all at one side of it, beside rows that lie around it:
+    the reference of their exponentials is their own maximum."""
+    g = torch.Generator(device="cuda").manual_seed(31)
+    q, k, v = tensors(1, 2, 2, 300, 200, d, dtype, seed=31, amp=0.25)
+    level = torch.tensor([0.0, -4.0, 5.0, -9.0, 9.0, -30.0, 40.0, -200.0, 150.0], device="cuda")
+    rows = level[torch.randint(0, len(level), (300,), generator=g, device="cuda")]
+    q[..., 0], k[..., 0] = rows.to(dtype)[None, None], 1.0
+    run(sa2, q, k, v, scale=1.0)
+    k[:, :, 64:, 0] = -1.0  # and those behind them at the other side
+    run(sa2, q, k, v, scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,Hkv,N", [(2, 2, 300), (6, 2, 300), (14, 2, 40), (6, 2, 5), (2, 2, 3)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_do_not_depend_on_each_other(sa2, d, H, Hkv, N, dtype):
+    """The same bits for a row beside rows whose scores leap past every range, and whatever the call before
+    left in the parts of a tile that hold no query."""
+    q, k, v = tensors(1, H, Hkv, N, 700, d, dtype, seed=33)
+    k[:, :, 200:] *= 3
+    wild, odd = q.clone(), torch.arange(N, device="cuda") % 7 == 2
+    wild[:, :, odd] *= 100
+    c = sa2.KvCache8.empty(1, Hkv, 700, d, "cuda")
+    kl = torch.tensor([700], dtype=torch.int32, device="cuda")
+    sa2.cache8_append(c, k, v, torch.zeros_like(kl))
+    for f in (lambda x: sa2.cross_attn_fwd(x, k, v), lambda x: sa2.cache8_attn(x, c, kl)):
+        o, lse = f(q)
+        for other in (wild, torch.full_like(q, math.nan)):
+            o2, lse2 = f(other)
+            if other is wild:
+                assert torch.equal(o2[:, :, ~odd], o[:, :, ~odd]) and torch.equal(lse2[:, :, ~odd], lse[:, :, ~odd])
+            o2, lse2 = f(q)
+            assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    sa2.check_device()
+
+
 def test_repeated_calls_are_identical(sa2):
     q, k, v = tensors(2, 8, 2, 70, 3000, 128, torch.bfloat16, seed=7)
     o, lse = sa2.cross_attn_fwd(q, k, v)
