@@ -44,7 +44,8 @@ struct Piece {
 };
 
 // Direct mode: segments that do not fill a last round of the grid, and whose tiles can go one by one
-// without another round, are taken so: a single tile takes two thirds of a pair's time.
+// without another round, are taken so, since a single tile takes less time than a pair (24 heads x 8192 x
+// 4096, d = 128: 324 us with pairs alone, 313).
 __device__ __forceinline__ int single_segs(const FwdPlan& p) {
   const int rest = p.segs % p.grid;
   return !p.split && p.tp == 2 && 2 * rest <= p.grid ? rest : 0;

@@ -11,7 +11,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -281,10 +280,6 @@ def cross_attn_bwd(q, k, v, o, lse, do, kv_len: Optional[torch.Tensor] = None, s
                                                        _handle(stream))
 
 
-_pack_cache = struct.Struct("PPPPqqqiiii").pack  # sa2_cache8
-_CACHE_DTYPES = (torch.float8_e4m3fn, torch.uint8)
-
-
 class KvCache8:
     """Keys and values held in 8 bits: k, v e4m3 [B, Hkv, C, d] (float8_e4m3fn or uint8, with the same
     strides) and k_scale, v_scale float32 [B, Hkv, ceil(C / 64)], one power-of-two scale for each head
@@ -294,23 +289,8 @@ class KvCache8:
     __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_shape", "_device", "_struct")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
-        if k.dim() != 4:
-            raise ValueError("the cache's k and v are [B, Hkv, C, d] with the same strides, d contiguous")
-        B, Hkv, C, d = self._shape = tuple(k.shape)
-        sb, sh, sn, sd = st = k.stride()
-        dev = k.device
-        if v.shape != k.shape or v.stride() != st or sd != 1:
-            raise ValueError("the cache's k and v are [B, Hkv, C, d] with the same strides, d contiguous")
-        if k.dtype not in _CACHE_DTYPES or v.dtype not in _CACHE_DTYPES or v.device != dev:
-            raise ValueError("the cache's k and v are float8_e4m3fn (or uint8) on one device")
-        for name, x in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if (x.dtype != torch.float32 or x.shape != (B, Hkv, blocks(C, self.BLOCK)) or not x.is_contiguous()
-                    or x.device != dev):
-                raise ValueError(f"{name} must be a contiguous float32 tensor [B, Hkv, ceil(C / 64)] on {dev}")
-        self._device = -1 if dev.index is None else dev.index
+        self._shape, self._device, self._struct = (_binding or load_binding()).cache8_pack(k, v, k_scale, v_scale)
         self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
-        self._struct = _pack_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), sb, sh, sn,
-                                   B, Hkv, C, d)
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
