@@ -53,30 +53,6 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 
 using Sizes = c10::IntArrayRef;
 
-// sa2_tensor of a token tensor of this shape, type and device.
-sa2_tensor token(const at::Tensor& x, const char* name, Sizes shape, at::ScalarType dtype, c10::Device device) {
-  if (x.sizes() != shape) refuse(name, " must be ", shape, ", got ", x.sizes());
-  if (x.scalar_type() != dtype) refuse(name, " must be ", dtype, ", got ", x.scalar_type());
-  if (x.device() != device) refuse(name, " must be on ", device, ", got ", x.device());
-  const Sizes st = x.strides();
-  if (st[3] != 1) refuse(name, ": the last dimension must be contiguous");
-  return {x.data_ptr(), st[0], st[1], st[2]};
-}
-
-const int32_t* int32s(PyObject* o, const char* name, int64_t B, c10::Device device) {
-  if (none(o)) return nullptr;
-  const at::Tensor& x = tensor(o, name);
-  if (x.scalar_type() != at::kInt || x.dim() != 1 || x.size(0) != B || !x.is_contiguous() || x.device() != device)
-    refuse(name, " must be a contiguous int32 tensor of shape [", B, "] on ", device);
-  return static_cast<const int32_t*>(x.data_ptr());
-}
-
-float* float32s(const at::Tensor& x, const char* name, Sizes shape, c10::Device device) {
-  if (x.scalar_type() != at::kFloat || x.sizes() != shape || !x.is_contiguous() || x.device() != device)
-    refuse(name, " must be a contiguous float32 tensor of shape ", shape, " on ", device);
-  return static_cast<float*>(x.data_ptr());
-}
-
 int dtype_code(at::ScalarType t) {
   if (t == at::kBFloat16) return SA2_BF16;
   if (t == at::kHalf) return SA2_FP16;
@@ -93,12 +69,16 @@ int32_t narrow(int64_t n, const char* what) {
   return (int32_t)n;
 }
 
-// The device of a call's tensors made the current one, and the stream that it is issued on.
+// The device of a call's tensors and the stream that it is issued on, both made the current ones: what is
+// allocated here comes from that stream's memory, where work of the same stream alone can have gone before.
+// (From the caller's current stream's memory a workspace could be one that an earlier call, still running
+// there, has given back.)
 struct Place {
   c10::Device device;
   c10::cuda::OptionalCUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard stream_guard;
+  std::optional<c10::cuda::CUDAStream> named, caller;  // a stream that the caller named; the one current then
   cudaStream_t stream = nullptr;
-  bool own_stream = false;  // the caller named a stream: what is allocated here outlives its work
 
   Place(c10::Device d, PyObject* stream_handle) : device(d) {
     if (!d.is_cuda()) refuse("the tensors must be on a CUDA device, got ", d);
@@ -106,23 +86,64 @@ struct Place {
     if (none(stream_handle)) {
       stream = c10::cuda::getCurrentCUDAStream(d.index()).stream();
     } else {
-      own_stream = true;
       stream = reinterpret_cast<cudaStream_t>(PyLong_AsUnsignedLongLong(stream_handle));
-      if (PyErr_Occurred()) refuse("stream must be a torch.cuda.Stream");
+      if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("stream must be a torch.cuda.Stream");
+      }
+      caller = c10::cuda::getCurrentCUDAStream(d.index());
+      named = c10::cuda::getStreamFromExternal(stream, d.index());
+      stream_guard.reset_stream(*named);
     }
   }
-  at::Tensor keep(at::Tensor x) const {
-    if (own_stream) x.record_stream(c10::cuda::getStreamFromExternal(stream, device.index()));
+  // A tensor of the call, which may have been allocated on another stream: its memory is not given out
+  // again before the named stream has got this far.
+  const at::Tensor& use(const at::Tensor& x) const {
+    if (named) x.record_stream(*named);
+    return x;
+  }
+  // A tensor made here: the caller's stream may be the one that reads it.
+  at::Tensor made(at::Tensor x) const {
+    if (caller) x.record_stream(*caller);
     return x;
   }
   at::Tensor empty(Sizes shape, at::ScalarType t) const {
-    return keep(at::empty(shape, at::TensorOptions().dtype(t).device(device)));
+    return made(at::empty(shape, at::TensorOptions().dtype(t).device(device)));
   }
-  at::Tensor empty_like(const at::Tensor& x) const { return keep(at::empty_like(x)); }
+  at::Tensor empty_like(const at::Tensor& x) const { return made(at::empty_like(x)); }
   at::Tensor given_or_like(PyObject* o, const char* name, const at::Tensor& x) const {
     return none(o) ? empty_like(x) : tensor(o, name);
   }
 };
+
+// sa2_tensor of a token tensor of this shape, type and device.
+sa2_tensor token(const at::Tensor& x, const char* name, Sizes shape, at::ScalarType dtype, const Place& at_) {
+  if (x.sizes() != shape) refuse(name, " must be ", shape, ", got ", x.sizes());
+  if (x.scalar_type() != dtype) refuse(name, " must be ", dtype, ", got ", x.scalar_type());
+  if (x.device() != at_.device) refuse(name, " must be on ", at_.device, ", got ", x.device());
+  const Sizes st = x.strides();
+  if (st[3] != 1) refuse(name, ": the last dimension must be contiguous");
+  return {at_.use(x).data_ptr(), st[0], st[1], st[2]};
+}
+
+const int32_t* int32s(PyObject* o, const char* name, int64_t B, const Place& at_) {
+  if (none(o)) return nullptr;
+  const at::Tensor& x = tensor(o, name);
+  if (x.scalar_type() != at::kInt || x.dim() != 1 || x.size(0) != B || !x.is_contiguous() || x.device() != at_.device)
+    refuse(name, " must be a contiguous int32 tensor of shape [", B, "] on ", at_.device);
+  return static_cast<const int32_t*>(at_.use(x).data_ptr());
+}
+
+float* float32s(const at::Tensor& x, const char* name, Sizes shape, c10::Device device) {
+  if (x.scalar_type() != at::kFloat || x.sizes() != shape || !x.is_contiguous() || x.device() != device)
+    refuse(name, " must be a contiguous float32 tensor of shape ", shape, " on ", device);
+  return static_cast<float*>(x.data_ptr());
+}
+float* float32s(const at::Tensor& x, const char* name, Sizes shape, const Place& at_) {
+  float* p = float32s(x, name, shape, at_.device);
+  at_.use(x);
+  return p;
+}
 
 struct Workspace {
   at::Tensor hold;
@@ -131,11 +152,12 @@ struct Workspace {
   Workspace(PyObject* ws, size_t need, const Place& at_) {
     if (none(ws)) {
       if (need == 0) return;
-      hold = at_.empty({(int64_t)need}, at::kByte);
+      hold = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(at_.device));
     } else {
       hold = tensor(ws, "ws");
       if (hold.device() != at_.device || hold.scalar_type() != at::kByte || !hold.is_contiguous())
         refuse("ws must be a contiguous uint8 tensor on ", at_.device);
+      at_.use(hold);
     }
     p = hold.data_ptr();
     bytes = (size_t)hold.numel();
@@ -188,15 +210,15 @@ PyObject* cross_fwd(PyObject* const* a) {
   const Place at_(q.device(), a[8]);
   const int64_t kvs[4] = {q.size(0), k.size(1), k.size(2), q.size(3)}, ls[3] = {q.size(0), q.size(1), q.size(2)};
   const at::ScalarType t = q.scalar_type();
-  const sa2_tensor qt = token(q, "q", q.sizes(), t, at_.device), kt = token(k, "k", kvs, t, at_.device),
-                   vt = token(v, "v", kvs, t, at_.device);
-  const int32_t* len = int32s(a[3], "kv_len", s.B, at_.device);
+  const sa2_tensor qt = token(q, "q", q.sizes(), t, at_), kt = token(k, "k", kvs, t, at_),
+                   vt = token(v, "v", kvs, t, at_);
+  const int32_t* len = int32s(a[3], "kv_len", s.B, at_);
   const at::Tensor o = at_.given_or_like(a[5], "o", q);
   const at::Tensor lse = none(a[6]) ? at_.empty(ls, at::kFloat) : tensor(a[6], "lse");
-  const sa2_tensor ot = token(o, "o", q.sizes(), t, at_.device);
+  const sa2_tensor ot = token(o, "o", q.sizes(), t, at_);
   const Workspace ws(a[7], sa2_cross_fwd_workspace_size(&s), at_);
   check("sa2_cross_attn_fwd", sa2_cross_attn_fwd(&s, &qt, &kt, &vt, len, scale_of(a[4]), &ot,
-                                                 float32s(lse, "lse", ls, at_.device), ws.p, ws.bytes, at_.stream));
+                                                 float32s(lse, "lse", ls, at_), ws.p, ws.bytes, at_.stream));
   return tuple_of(o, lse);
 }
 
@@ -209,16 +231,15 @@ PyObject* cross_bwd(PyObject* const* a) {
   const Place at_(q.device(), a[12]);
   const int64_t kvs[4] = {q.size(0), k.size(1), k.size(2), q.size(3)}, ls[3] = {q.size(0), q.size(1), q.size(2)};
   const at::ScalarType t = q.scalar_type();
-  const c10::Device d = at_.device;
-  const sa2_tensor qt = token(q, "q", q.sizes(), t, d), kt = token(k, "k", kvs, t, d), vt = token(v, "v", kvs, t, d),
-                   ot = token(tensor(a[3], "o"), "o", q.sizes(), t, d),
-                   dot = token(tensor(a[5], "do"), "do", q.sizes(), t, d);
-  const float* lse = float32s(tensor(a[4], "lse"), "lse", ls, d);
-  const int32_t* len = int32s(a[6], "kv_len", s.B, d);
+  const sa2_tensor qt = token(q, "q", q.sizes(), t, at_), kt = token(k, "k", kvs, t, at_), vt = token(v, "v", kvs, t, at_),
+                   ot = token(tensor(a[3], "o"), "o", q.sizes(), t, at_),
+                   dot = token(tensor(a[5], "do"), "do", q.sizes(), t, at_);
+  const float* lse = float32s(tensor(a[4], "lse"), "lse", ls, at_);
+  const int32_t* len = int32s(a[6], "kv_len", s.B, at_);
   const at::Tensor dq = at_.given_or_like(a[8], "dq", q), dk = at_.given_or_like(a[9], "dk", k),
                    dv = at_.given_or_like(a[10], "dv", v);
-  const sa2_tensor dqt = token(dq, "dq", q.sizes(), t, d), dkt = token(dk, "dk", kvs, t, d),
-                   dvt = token(dv, "dv", kvs, t, d);
+  const sa2_tensor dqt = token(dq, "dq", q.sizes(), t, at_), dkt = token(dk, "dk", kvs, t, at_),
+                   dvt = token(dv, "dv", kvs, t, at_);
   const Workspace ws(a[11], sa2_cross_bwd_workspace_size(&s), at_);
   check("sa2_cross_attn_bwd", sa2_cross_attn_bwd(&s, &qt, &kt, &vt, &ot, lse, &dot, len, scale_of(a[7]), &dqt, &dkt,
                                                  &dvt, ws.p, ws.bytes, at_.stream));
@@ -253,9 +274,8 @@ PyObject* cache_append(PyObject* const* a) {
   const int code = dtype_code(t);
   const int64_t shape[4] = {c->B, c->Hkv, k.size(2), c->d};
   if (none(a[4])) refuse("pos is required");
-  const sa2_tensor kt = token(k, "k", shape, t, at_.device),
-                   vt = token(tensor(a[3], "v"), "v", shape, t, at_.device);
-  const int32_t *pos = int32s(a[4], "pos", c->B, at_.device), *n_new = int32s(a[5], "n_new", c->B, at_.device);
+  const sa2_tensor kt = token(k, "k", shape, t, at_), vt = token(tensor(a[3], "v"), "v", shape, t, at_);
+  const int32_t *pos = int32s(a[4], "pos", c->B, at_), *n_new = int32s(a[5], "n_new", c->B, at_);
   if (shape[2] > 0)
     check("sa2_cache8_append",
           sa2_cache8_append(c, narrow(shape[2], "n"), code, &kt, &vt, pos, n_new, at_.stream));
@@ -274,10 +294,10 @@ PyObject* cache_read(PyObject* const* a) {
   const int64_t shape[4] = {c->B, c->Hkv, n, c->d};
   const at::ScalarType t = PyObject_IsTrue(a[4]) ? at::kHalf : at::kBFloat16;
   if (none(a[2])) refuse("pos is required");
-  const int32_t* pos = int32s(a[2], "pos", c->B, at_.device);
+  const int32_t* pos = int32s(a[2], "pos", c->B, at_);
   const at::Tensor k = none(a[5]) ? at_.empty(shape, t) : tensor(a[5], "k");
   const at::Tensor v = none(a[6]) ? at_.empty(shape, t) : tensor(a[6], "v");
-  const sa2_tensor kt = token(k, "k", shape, t, at_.device), vt = token(v, "v", shape, t, at_.device);
+  const sa2_tensor kt = token(k, "k", shape, t, at_), vt = token(v, "v", shape, t, at_);
   if (n > 0)
     check("sa2_cache8_read", sa2_cache8_read(c, narrow(n, "n"), dtype_code(t), &kt, &vt, pos, at_.stream));
   return tuple_of(k, v);
@@ -295,13 +315,13 @@ PyObject* cache_attn(PyObject* const* a) {
   if (cuda(a[2]) != at_.device) refuse("the cache must be on ", at_.device, ", got ", cuda(a[2]));
   const int64_t ls[3] = {q.size(0), q.size(1), q.size(2)};
   const at::ScalarType t = q.scalar_type();
-  const sa2_tensor qt = token(q, "q", q.sizes(), t, at_.device);
-  const int32_t* len = int32s(a[3], "kv_len", s.B, at_.device);
+  const sa2_tensor qt = token(q, "q", q.sizes(), t, at_);
+  const int32_t* len = int32s(a[3], "kv_len", s.B, at_);
   const at::Tensor o = at_.given_or_like(a[5], "o", q);
   const at::Tensor lse = none(a[6]) ? at_.empty(ls, at::kFloat) : tensor(a[6], "lse");
-  const sa2_tensor ot = token(o, "o", q.sizes(), t, at_.device);
+  const sa2_tensor ot = token(o, "o", q.sizes(), t, at_);
   const Workspace ws(a[7], sa2_cross_fwd_workspace_size(&s), at_);
-  check("sa2_cache8_attn", sa2_cache8_attn(&s, &qt, c, len, scale_of(a[4]), &ot, float32s(lse, "lse", ls, at_.device),
+  check("sa2_cache8_attn", sa2_cache8_attn(&s, &qt, c, len, scale_of(a[4]), &ot, float32s(lse, "lse", ls, at_),
                                            ws.p, ws.bytes, at_.stream));
   return tuple_of(o, lse);
 }

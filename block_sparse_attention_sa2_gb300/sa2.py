@@ -242,6 +242,12 @@ def vd_loss(o_s: torch.Tensor, o_t: torch.Tensor, o_s_lo: Optional[torch.Tensor]
 # --------------------------------------------------- attention to keys of another length
 #
 # Argument checks, allocation and the C calls are in the extension module (csrc/cross_binding.cpp).
+#
+# ``stream``: the torch.cuda.Stream that a call is issued on, the current one where it is not given.  The caller
+# orders it behind the work that makes the inputs, and whatever reads the outputs behind it.  Outputs and the
+# workspace that a call makes come from that stream's memory; the memory of every tensor of the call, given or
+# made, is held back from reuse until the streams concerned are done with it, so that tensors may be dropped
+# as soon as the call returns.
 
 _binding = None
 
@@ -299,6 +305,12 @@ class KvCache8:
     shape = property(lambda self: self._shape, doc="(B, Hkv, capacity, d)")
     device = property(lambda self: self._k.device)
 
+    def _used_on(self, stream) -> None:
+        """Holds the cache's memory back until `stream`, where one was named, is done with it."""
+        if stream is not None:
+            for x in (self._k, self._v, self._k_scale, self._v_scale):
+                x.record_stream(stream)
+
     @staticmethod
     def empty(B: int, Hkv: int, capacity: int, d: int, device) -> "KvCache8":
         k, v = (torch.empty((B, Hkv, capacity, d), dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
@@ -312,6 +324,7 @@ def cache8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, pos: torch.
     """sa2_cache8_append: writes k, v [B, Hkv, n, d] (bfloat16 or float16) at positions pos[b] ..
     pos[b] + n - 1 (n_new[b] tokens of each sequence where given).  ``pos``, ``n_new``: [B] int32."""
     (_binding or load_binding()).cache8_append(cache._struct, cache._device, k, v, pos, n_new, _handle(stream))
+    cache._used_on(stream)
 
 
 def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
@@ -319,8 +332,10 @@ def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16
     """sa2_cache8_read: the values of tokens pos[b] .. pos[b] + n - 1 as (K, V) [B, Hkv, n, d]."""
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
-    return (_binding or load_binding()).cache8_read(cache._struct, cache._device, pos, n, dtype is torch.float16, k, v,
-                                                    _handle(stream))
+    got = (_binding or load_binding()).cache8_read(cache._struct, cache._device, pos, n, dtype is torch.float16, k, v,
+                                                   _handle(stream))
+    cache._used_on(stream)
+    return got
 
 
 def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: Optional[float] = None,
@@ -328,8 +343,10 @@ def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: O
                 ws: Optional[torch.Tensor] = None, stream=None):
     """sa2_cache8_attn: attention of q [B, H, N, d] to the first kv_len[b] tokens of the cache;
     returns (O, LSE) as cross_attn_fwd does."""
-    return (_binding or load_binding()).cache8_attn(q, cache._struct, cache._device, kv_len, scale, o, lse, ws,
-                                                    _handle(stream))
+    got = (_binding or load_binding()).cache8_attn(q, cache._struct, cache._device, kv_len, scale, o, lse, ws,
+                                                   _handle(stream))
+    cache._used_on(stream)
+    return got
 
 
 def device_status(stream=None) -> int:
