@@ -5,9 +5,16 @@ Every step of the hot path runs in the library's CUDA kernels; this module alloc
 output tensors and workspaces with PyTorch, passes raw device pointers and the current CUDA
 stream through ctypes, and turns status codes into exceptions.  It fails loudly when the
 library is missing.  Names follow the C ABI: ``build_mask``, ``attn_fwd``, ``attn_bwd``.
+
+``stream``: the torch.cuda.Stream that a call is issued on, the current one where it is not given.  The caller
+orders it behind the work that makes the inputs, and whatever reads the outputs behind it.  Outputs and the
+workspace that a call makes come from that stream's memory; the memory of every tensor of the call, given or
+made, is held back from reuse until the streams concerned are done with it, so that tensors may be dropped
+as soon as the call returns.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -114,6 +121,25 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _memory_of(stream):
+    """Outputs and workspaces made under it come from the named stream's memory (None: the current one's), where
+    no other stream's work can still use what it gives out."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _hold(stream, used, made) -> None:
+    """For a call on a named stream: holds the memory of the tensors that it used back from reuse until that
+    stream is done with them, and of those that it made until the current one is."""
+    if stream is None:
+        return
+    for x in used:
+        if x is not None:
+            x.record_stream(stream)
+    for x in made:
+        if x is not None:
+            x.record_stream(torch.cuda.current_stream())
+
+
 def _check(fn: str, code: int):
     if code != 0:
         raise Sa2Error(fn, code)
@@ -129,6 +155,9 @@ class BlockMask:
     col_idx: torch.Tensor  # [B, H, Tk, Tq] int32
     mask: Optional[torch.Tensor] = None  # [B, H, Tq, Tk] uint8
     pooled_p: Optional[torch.Tensor] = None  # [B, H, Tq, Tk] float32
+
+    def tensors(self):
+        return self.row_cnt, self.row_idx, self.col_cnt, self.col_idx, self.mask, self.pooled_p
 
     def struct(self) -> BlockMaskStruct:
         return BlockMaskStruct(_ptr(self.row_cnt), _ptr(self.row_idx), _ptr(self.col_cnt), _ptr(self.col_idx),
@@ -161,14 +190,16 @@ def build_mask(q: torch.Tensor, k: torch.Tensor, topk: float, topp: float, bq: i
         raise ValueError("q and k must have the same shape and strides")
     B, H, N, _ = q.shape
     Tq, Tk = blocks(N, bq), blocks(N, bk)
-    if out is None:
-        out = BlockMask.empty(B, H, Tq, Tk, q.device, mask=want_mask, pooled=want_pooled)
-    if ws is None:
-        ws = workspace(lib.sa2_mask_workspace_size(ctypes.byref(shp)), q.device)
+    with _memory_of(stream):
+        if out is None:
+            out = BlockMask.empty(B, H, Tq, Tk, q.device, mask=want_mask, pooled=want_pooled)
+        if ws is None:
+            ws = workspace(lib.sa2_mask_workspace_size(ctypes.byref(shp)), q.device)
     m = out.struct()
     _check("sa2_build_mask", lib.sa2_build_mask(ctypes.byref(shp), q.data_ptr(), k.data_ptr(), float(topk),
                                                 float(topp), ctypes.byref(m), ws.data_ptr(), ws.numel(),
                                                 _stream(stream)))
+    _hold(stream, (q, k, ws, *out.tensors()), out.tensors())
     return out
 
 
@@ -180,16 +211,18 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: BlockMask,
     lib = load_library()
     shp = make_shape(q, bq, bk)
     B, H, N, d = q.shape
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = workspace(lib.sa2_fwd_workspace_size(ctypes.byref(shp)), q.device)
+    with _memory_of(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = workspace(lib.sa2_fwd_workspace_size(ctypes.byref(shp)), q.device)
     m = mask.struct()
     _check("sa2_attn_fwd", lib.sa2_attn_fwd(ctypes.byref(shp), q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                             ctypes.byref(m), float(scale or 0.0), o.data_ptr(), _ptr(o_lo),
                                             lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+    _hold(stream, (q, k, v, o, o_lo, lse, ws, *mask.tensors()), (o, lse))
     return o, lse
 
 
@@ -203,11 +236,12 @@ def attn_bwd(q, k, v, o, lse, do, mask: BlockMask, bq: int = 128, bk: int = 64, 
     (sa2_attn_bwd_with_fwd_ws)."""
     lib = load_library()
     shp = make_shape(q, bq, bk)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    if ws is None:
-        ws = workspace(lib.sa2_bwd_workspace_size(ctypes.byref(shp)), q.device)
+    with _memory_of(stream):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if ws is None:
+            ws = workspace(lib.sa2_bwd_workspace_size(ctypes.byref(shp)), q.device)
     m = mask.struct()
     args = (ctypes.byref(shp), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(o_lo), lse.data_ptr(),
             do.data_ptr(), ctypes.byref(m), float(scale or 0.0), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
@@ -217,6 +251,7 @@ def attn_bwd(q, k, v, o, lse, do, mask: BlockMask, bq: int = 128, bk: int = 64, 
     else:
         _check("sa2_attn_bwd_with_fwd_ws",
                lib.sa2_attn_bwd_with_fwd_ws(*args, fwd_ws.data_ptr(), fwd_ws.numel(), _stream(stream)))
+    _hold(stream, (q, k, v, o, o_lo, lse, do, dq, dk, dv, ws, fwd_ws, *mask.tensors()), (dq, dk, dv))
     return dq, dk, dv
 
 
@@ -229,25 +264,21 @@ def vd_loss(o_s: torch.Tensor, o_t: torch.Tensor, o_s_lo: Optional[torch.Tensor]
     shp = make_shape(o_s, 128, 64)
     if o_t.shape != o_s.shape or o_t.stride() != o_s.stride():
         raise ValueError("o_s and o_t must have the same shape and strides")
-    d_o = torch.empty_like(o_s) if d_o is None else d_o
-    loss = torch.empty((), dtype=torch.float64, device=o_s.device)
-    if ws is None:
-        ws = workspace(lib.sa2_vd_loss_workspace_size(ctypes.byref(shp)), o_s.device)
+    with _memory_of(stream):
+        d_o = torch.empty_like(o_s) if d_o is None else d_o
+        loss = torch.empty((), dtype=torch.float64, device=o_s.device)
+        if ws is None:
+            ws = workspace(lib.sa2_vd_loss_workspace_size(ctypes.byref(shp)), o_s.device)
     _check("sa2_vd_loss", lib.sa2_vd_loss(ctypes.byref(shp), o_s.data_ptr(), _ptr(o_s_lo), o_t.data_ptr(),
                                           _ptr(o_t_lo), d_o.data_ptr(), loss.data_ptr(), ws.data_ptr(),
                                           ws.numel(), _stream(stream)))
+    _hold(stream, (o_s, o_t, o_s_lo, o_t_lo, d_o, ws), (loss, d_o))
     return loss, d_o
 
 
 # --------------------------------------------------- attention to keys of another length
 #
 # Argument checks, allocation and the C calls are in the extension module (csrc/cross_binding.cpp).
-#
-# ``stream``: the torch.cuda.Stream that a call is issued on, the current one where it is not given.  The caller
-# orders it behind the work that makes the inputs, and whatever reads the outputs behind it.  Outputs and the
-# workspace that a call makes come from that stream's memory; the memory of every tensor of the call, given or
-# made, is held back from reuse until the streams concerned are done with it, so that tensors may be dropped
-# as soon as the call returns.
 
 _binding = None
 
