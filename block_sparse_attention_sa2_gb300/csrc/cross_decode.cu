@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
       const int base = key0 + (i * kWarps + warp) * T::kKeys;
       float mul[2] = {row_scale[0], row_scale[1]}, ev = 0.f;
       if constexpr (KV8) {
-        mul[0] *= nks;
-        mul[1] *= nks;
+        mul[0] = score_factor(row_scale[0], nks);
+        mul[1] = score_factor(row_scale[1], nks);
         ev = (float)((int)(__float_as_uint(nvs) >> 23) - 127);
         load_scales(i + 1);
       }

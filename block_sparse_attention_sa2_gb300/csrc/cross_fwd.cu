@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int valid = keys - 64 * i;
         float mul = qscale, ev = 0.f;
         if constexpr (KV8) {
-          mul *= nks;
+          mul = score_factor(qscale, nks);
           ev = (float)((int)(__float_as_uint(nvs) >> 23) - 127);
           if (valid > 64) {
             nks = cache.ks[sc + i + 1];

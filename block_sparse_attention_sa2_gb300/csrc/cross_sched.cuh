@@ -10,6 +10,14 @@ namespace sa2 {
 __device__ __forceinline__ void kernel_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void kernel_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The factor from products to scores of a block of cached keys.  It is a product of three numbers, of which two are
+// powers of two as small as 2^-112 and 2^-100: kept above 0, where every score is 0 all the same (the products are
+// below 2^32), since scores behind the last key are -inf and 0 times that is NaN.
+__device__ __forceinline__ float score_factor(float row, float key_scale) {
+  const float x = row * key_scale;
+  return x < 0x1p-126f ? 0x1p-126f : x;
+}
+
 // Keys of sequence b, clamped to [0, M].
 __device__ __forceinline__ int key_count(const int32_t* kv_len, int b, int M) {
   const int n = kv_len ? kv_len[b] : M;

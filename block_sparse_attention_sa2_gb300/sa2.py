@@ -337,10 +337,9 @@ class KvCache8:
     device = property(lambda self: self._k.device)
 
     def _used_on(self, stream) -> None:
-        """Holds the cache's memory back until `stream`, where one was named, is done with it."""
-        if stream is not None:
-            for x in (self._k, self._v, self._k_scale, self._v_scale):
-                x.record_stream(stream)
+        """Holds the cache's memory back from reuse until the stream is done with it."""
+        for x in (self._k, self._v, self._k_scale, self._v_scale):
+            x.record_stream(stream)
 
     @staticmethod
     def empty(B: int, Hkv: int, capacity: int, d: int, device) -> "KvCache8":
@@ -355,7 +354,8 @@ def cache8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, pos: torch.
     """sa2_cache8_append: writes k, v [B, Hkv, n, d] (bfloat16 or float16) at positions pos[b] ..
     pos[b] + n - 1 (n_new[b] tokens of each sequence where given).  ``pos``, ``n_new``: [B] int32."""
     (_binding or load_binding()).cache8_append(cache._struct, cache._device, k, v, pos, n_new, _handle(stream))
-    cache._used_on(stream)
+    if stream is not None:
+        cache._used_on(stream)
 
 
 def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
@@ -365,7 +365,8 @@ def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16
         raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
     got = (_binding or load_binding()).cache8_read(cache._struct, cache._device, pos, n, dtype is torch.float16, k, v,
                                                    _handle(stream))
-    cache._used_on(stream)
+    if stream is not None:
+        cache._used_on(stream)
     return got
 
 
@@ -376,7 +377,8 @@ def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: O
     returns (O, LSE) as cross_attn_fwd does."""
     got = (_binding or load_binding()).cache8_attn(q, cache._struct, cache._device, kv_len, scale, o, lse, ws,
                                                    _handle(stream))
-    cache._used_on(stream)
+    if stream is not None:
+        cache._used_on(stream)
     return got
 
 
