@@ -170,8 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = XSmem<D, KV8>;
   constexpr int kStages = L::kStages;
   constexpr bool kMmaF16 = KV8 || F16;  // the cache's products run in fp16
-  // how far (log2) a block's maximum may lead the reference before P leaves its type's range
-  constexpr float kMaxLead = kMmaF16 ? 14.f : 100.f;
+  // How far (log2) a block's maximum may lead the reference.  fp16 P holds 2^15; bf16 P could hold far more, but P V
+  // is summed in fp32 before O and l follow: V would be left what the lead does not take of 2^128.
+  constexpr float kMaxLead = 14.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -512,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // The exponentials are taken against a maximum of the half blocks before this one, so that they
         // need not wait for this one's: the first uses its own, then O and l follow when the maximum
-        // has grown past 2^8.  Only where P would leave its type's range does a half block's own
-        // maximum come first (the loop below runs twice).
+        // has grown past 2^8.  Only where P would lead by more than 2^14 does a half block's own maximum
+        // come first (the loop below runs twice).
         if (i == 0) {
           float y[32];
           load_scores(ts, y, valid);

@@ -310,7 +310,8 @@ size_t sa2_cross_fwd_workspace_size(const sa2_cross_shape* shape);
  *   s_ac = scale * q_a . k_c,  LSE_a = log sum_c exp(s_ac)  (natural log),
  *   O_a = sum_c exp(s_ac - LSE_a) v_c.
  * Scores, the softmax statistics and the sums are held in fp32; P is rounded to the call's
- * 16-bit type for P V.
+ * 16-bit type for P V.  The sums of P V run relative to a running maximum that single scores
+ * may exceed by 2^14 until it follows: O is finite for |v| < 2^100 (M < 2^20).
  *   scale   <= 0 means 1/sqrt(d)
  *   lse     [B, H, N] fp32 output, contiguous
  *   ws      device workspace of at least sa2_cross_fwd_workspace_size(shape) bytes (may be
