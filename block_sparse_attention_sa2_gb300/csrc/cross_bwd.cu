@@ -57,6 +57,9 @@ template <int D>
 __global__ void __launch_bounds__(256) cross_stats_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
   constexpr int kLanes = D / 16;
   kernel_trigger();
+  if (a.kv_len && blockIdx.x == 0 && blockIdx.y == 0)
+    for (int b = threadIdx.x; b < s.B; b += 256)
+      if (a.kv_len[b] < 0 || a.kv_len[b] > s.M) report_error(a.status, kDevErrBounds);
   const int head = blockIdx.x / plan.tiles, tile = blockIdx.x - head * plan.tiles;
   const int b = head / s.Hkv, hk = head - b * s.Hkv;
   const int ch = (threadIdx.x % kLanes) * 16;
