@@ -1,5 +1,6 @@
 // The C ABI of cross attention and of the 8-bit cache (include/sa2.h): argument checks, workspace
 // layout, tensor maps and launches.
+#include <algorithm>
 #include <cmath>
 
 #include "cross_internal.h"
@@ -179,7 +180,8 @@ sa2_status sa2_cross_attn_bwd(const sa2_cross_shape* shape, const sa2_tensor* q,
   if (st != SA2_OK) return st;
   if (misaligned4(lse) || misaligned4(kv_len) || !aligned16(ws)) return SA2_ERR_ALIGNMENT;
   const BwdPlan plan = cross_bwd_plan(s, sm_count());
-  if ((int64_t)s.B * s.Hkv * plan.tiles > INT32_MAX || (int64_t)s.B * s.Hkv > 65535) return SA2_ERR_UNSUPPORTED;
+  // (grid dimensions; tensors of so many tiles or key blocks have terabytes)
+  if ((int64_t)s.B * s.Hkv * std::max(plan.tiles, plan.kblocks) > INT32_MAX) return SA2_ERR_UNSUPPORTED;
   size_t stats;
   const size_t floats = cross_bwd_floats(s, plan, &stats);
   if (!ws || ws_bytes < floats * sizeof(float)) return SA2_ERR_WORKSPACE;

@@ -941,14 +941,14 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
 }
 
 // Adds the parts of key blocks whose tiles several runs shared, in run order, and writes zeros
-// behind the last key block of each sequence.  Grid (key blocks of M, B * Hkv, 8): an eighth of a block
+// behind the last key block of each sequence.  Grid (B * Hkv * key blocks of M, 8): an eighth of a block
 // each, since a head has few (12 heads x 32760 x 512: the whole backward 314 us, with one CTA per block 322).
 constexpr int kJoinParts = 8;
 template <int D>
 __global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdPlan plan, CrossBwdArgs a) {
   kernel_trigger();
-  const int kb = blockIdx.x, lane = threadIdx.x & 31;
-  const int b = blockIdx.y / s.Hkv, hk = blockIdx.y - b * s.Hkv;
+  const int head = blockIdx.x / plan.kblocks, kb = blockIdx.x - head * plan.kblocks, lane = threadIdx.x & 31;
+  const int b = head / s.Hkv, hk = head - b * s.Hkv;
   const int keys = key_count(a.kv_len, b, s.M), nk = key_blocks(keys);
   // the parts: slots first, first + step, ... of CTAs; the part that a run begins with is in 2 * CTA
   int c0 = 0, count = 0, step = 1;
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(256) cross_dkdv_join_kernel(CrossShape s, BwdP
   if (count == 1) return;  // one CTA had all of its tiles
   constexpr int kItems = 2 * 128 * (D / 8) / kJoinParts;
   for (int j = threadIdx.x; j < kItems; j += 256) {
-    const int i = blockIdx.z * kItems + j;
+    const int i = blockIdx.y * kItems + j;
     const int w = i / (128 * (D / 8)), r = i / (D / 8) % 128, ch = i % (D / 8) * 8;
     const int key = kb * kKeyBlock + r;
     if (key >= s.M) continue;
@@ -1013,8 +1013,8 @@ cudaError_t launch_t(const CrossShape& s, const BwdPlan& p, const CUtensorMap& m
   prof_start(st, kAttnBwd);
   e = launch_early(dkv, dim3((unsigned)p.grid), DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
   if (e == cudaSuccess)
-    e = launch_early(cross_dkdv_join_kernel<D>, dim3((unsigned)p.kblocks, (unsigned)(s.B * s.Hkv), kJoinParts), 256, 0,
-                     st, s, p, a);
+    e = launch_early(cross_dkdv_join_kernel<D>, dim3((unsigned)((int64_t)s.B * s.Hkv * p.kblocks), kJoinParts), 256,
+                     0, st, s, p, a);
   prof_stop(st, kAttnBwd);
   if (e != cudaSuccess) return e;
   prof_start(st, kAttnBwdDq);
