@@ -47,7 +47,8 @@ bool make_group_map(CUtensorMap* map, const TokenRef& t, int B, int heads, int G
   if (!enc) return false;
   std::memset(map, 0, sizeof(*map));
   cuuint64_t dims[5] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)tokens, (cuuint64_t)(heads / G), (cuuint64_t)B};
-  cuuint64_t strides[4] = {(cuuint64_t)t.sh * 2, (cuuint64_t)t.sn * 2, (cuuint64_t)t.sh * G * 2, (cuuint64_t)t.sb * 2};
+  const int64_t group = heads > G ? t.sh * G : t.sh;  // (one group: not used)
+  cuuint64_t strides[4] = {(cuuint64_t)t.sh * 2, (cuuint64_t)t.sn * 2, (cuuint64_t)group * 2, (cuuint64_t)t.sb * 2};
   cuuint32_t box[5] = {64, (cuuint32_t)box_g, (cuuint32_t)box_n, 1, 1};
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   CUresult r = enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t.p, dims,

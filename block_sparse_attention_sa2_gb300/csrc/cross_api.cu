@@ -49,20 +49,20 @@ sa2_status check_cross(const sa2_cross_shape* x, CrossShape* s) {
   return SA2_OK;
 }
 
-// Checks a token tensor of B x heads x tokens x d 16-bit elements; strides of dimensions of size 1
-// are replaced by those of a dense tensor, so that a tensor map never sees them.
-sa2_status check_tensor(const sa2_tensor* t, int B, int heads, int tokens, int d, int esz, TokenRef* r) {
+// Checks a token tensor of B x heads x tokens x d elements of which G heads share a key head; strides of
+// dimensions of size 1 are replaced by d, so that a tensor map sees legal ones.
+sa2_status check_tensor(const sa2_tensor* t, int B, int heads, int G, int tokens, int d, int esz, TokenRef* r) {
   if (!t || !t->data) return SA2_ERR_INVALID_ARG;
   if (!aligned16(t->data)) return SA2_ERR_ALIGNMENT;
   r->p = t->data;
   r->sn = tokens > 1 ? t->stride_n : d;
-  r->sh = heads > 1 ? t->stride_h : r->sn * tokens;
-  r->sb = B > 1 ? t->stride_b : r->sn * tokens;
+  r->sh = heads > 1 ? t->stride_h : d;
+  r->sb = B > 1 ? t->stride_b : d;
   if (r->sn < d || r->sh < 1 || r->sb < 1) return SA2_ERR_INVALID_ARG;
   if (r->sn * esz % 16 || r->sh * esz % 16 || r->sb * esz % 16) return SA2_ERR_ALIGNMENT;
-  // a tensor map's strides are below 2^40 bytes
-  const int64_t most = ((int64_t)1 << 40) / esz / kMaxGroup;
-  if (r->sn >= most || r->sh >= most || r->sb >= most) return SA2_ERR_UNSUPPORTED;
+  // a tensor map's strides are below 2^40 bytes; that of the key heads' groups is one of them
+  const int64_t most = ((int64_t)1 << 40) / esz;
+  if (r->sn >= most || r->sh >= (heads > G ? most / G : most) || r->sb >= most) return SA2_ERR_UNSUPPORTED;
   return SA2_OK;
 }
 
@@ -73,7 +73,7 @@ sa2_status check_cache(const sa2_cache8* x, CacheRef* c) {
   if (x->C >= kMaxTokens || x->B > kMaxGridYZ || x->Hkv > kMaxGridYZ) return SA2_ERR_UNSUPPORTED;
   const sa2_tensor k{x->k, x->stride_b, x->stride_h, x->stride_n};
   TokenRef r;
-  const sa2_status st = check_tensor(&k, x->B, x->Hkv, x->C, x->d, 1, &r);
+  const sa2_status st = check_tensor(&k, x->B, x->Hkv, 1, x->C, x->d, 1, &r);
   if (st != SA2_OK) return st;
   if (!aligned16(x->v) || (reinterpret_cast<uintptr_t>(x->k_scale) & 3u) ||
       (reinterpret_cast<uintptr_t>(x->v_scale) & 3u))
@@ -96,8 +96,8 @@ bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) !
 sa2_status fwd_args(const CrossShape& s, const sa2_tensor* q, const int32_t* kv_len, float scale, const sa2_tensor* o,
                     float* lse, void* ws, size_t ws_bytes, FwdPlan* plan, CrossFwdArgs* a) {
   if (!lse || !std::isfinite(scale)) return SA2_ERR_INVALID_ARG;
-  sa2_status st = check_tensor(q, s.B, s.H, s.N, s.d, 2, &a->q);
-  if (st == SA2_OK) st = check_tensor(o, s.B, s.H, s.N, s.d, 2, &a->o);
+  sa2_status st = check_tensor(q, s.B, s.H, s.G, s.N, s.d, 2, &a->q);
+  if (st == SA2_OK) st = check_tensor(o, s.B, s.H, s.G, s.N, s.d, 2, &a->o);
   if (st != SA2_OK) return st;
   if (misaligned4(lse) || misaligned4(kv_len) || !aligned16(ws)) return SA2_ERR_ALIGNMENT;
   *plan = cross_fwd_plan(s, sm_count());
@@ -132,8 +132,8 @@ sa2_status sa2_cross_attn_fwd(const sa2_cross_shape* shape, const sa2_tensor* q,
   sa2_status st = check_cross(shape, &s);
   if (st != SA2_OK) return st;
   TokenRef kr, vr;
-  st = check_tensor(k, s.B, s.Hkv, s.M, s.d, 2, &kr);
-  if (st == SA2_OK) st = check_tensor(v, s.B, s.Hkv, s.M, s.d, 2, &vr);
+  st = check_tensor(k, s.B, s.Hkv, 1, s.M, s.d, 2, &kr);
+  if (st == SA2_OK) st = check_tensor(v, s.B, s.Hkv, 1, s.M, s.d, 2, &vr);
   if (st != SA2_OK) return st;
   FwdPlan plan;
   CrossFwdArgs a;
@@ -169,14 +169,14 @@ sa2_status sa2_cross_attn_bwd(const sa2_cross_shape* shape, const sa2_tensor* q,
   if (!lse || !std::isfinite(scale)) return SA2_ERR_INVALID_ARG;
   CrossBwdArgs a;
   TokenRef qr, kr, vr;
-  st = check_tensor(q, s.B, s.H, s.N, s.d, 2, &qr);
-  if (st == SA2_OK) st = check_tensor(k, s.B, s.Hkv, s.M, s.d, 2, &kr);
-  if (st == SA2_OK) st = check_tensor(v, s.B, s.Hkv, s.M, s.d, 2, &vr);
-  if (st == SA2_OK) st = check_tensor(o, s.B, s.H, s.N, s.d, 2, &a.o);
-  if (st == SA2_OK) st = check_tensor(dO, s.B, s.H, s.N, s.d, 2, &a.dO);
-  if (st == SA2_OK) st = check_tensor(dq, s.B, s.H, s.N, s.d, 2, &a.dq);
-  if (st == SA2_OK) st = check_tensor(dk, s.B, s.Hkv, s.M, s.d, 2, &a.dk);
-  if (st == SA2_OK) st = check_tensor(dv, s.B, s.Hkv, s.M, s.d, 2, &a.dv);
+  st = check_tensor(q, s.B, s.H, s.G, s.N, s.d, 2, &qr);
+  if (st == SA2_OK) st = check_tensor(k, s.B, s.Hkv, 1, s.M, s.d, 2, &kr);
+  if (st == SA2_OK) st = check_tensor(v, s.B, s.Hkv, 1, s.M, s.d, 2, &vr);
+  if (st == SA2_OK) st = check_tensor(o, s.B, s.H, s.G, s.N, s.d, 2, &a.o);
+  if (st == SA2_OK) st = check_tensor(dO, s.B, s.H, s.G, s.N, s.d, 2, &a.dO);
+  if (st == SA2_OK) st = check_tensor(dq, s.B, s.H, s.G, s.N, s.d, 2, &a.dq);
+  if (st == SA2_OK) st = check_tensor(dk, s.B, s.Hkv, 1, s.M, s.d, 2, &a.dk);
+  if (st == SA2_OK) st = check_tensor(dv, s.B, s.Hkv, 1, s.M, s.d, 2, &a.dv);
   if (st != SA2_OK) return st;
   if (misaligned4(lse) || misaligned4(kv_len) || !aligned16(ws)) return SA2_ERR_ALIGNMENT;
   const BwdPlan plan = cross_bwd_plan(s, sm_count());
@@ -209,8 +209,8 @@ sa2_status sa2_cache8_append(const sa2_cache8* cache, int32_t n, int32_t dtype, 
   if (n < 1 || !pos) return SA2_ERR_INVALID_ARG;
   if (n >= kMaxTokens || (dtype != SA2_BF16 && dtype != SA2_FP16)) return SA2_ERR_UNSUPPORTED;
   TokenRef kr, vr;
-  st = check_tensor(k, cache->B, cache->Hkv, n, cache->d, 2, &kr);
-  if (st == SA2_OK) st = check_tensor(v, cache->B, cache->Hkv, n, cache->d, 2, &vr);
+  st = check_tensor(k, cache->B, cache->Hkv, 1, n, cache->d, 2, &kr);
+  if (st == SA2_OK) st = check_tensor(v, cache->B, cache->Hkv, 1, n, cache->d, 2, &vr);
   if (st != SA2_OK) return st;
   if (misaligned4(pos) || misaligned4(n_new)) return SA2_ERR_ALIGNMENT;
   return cuda_status(launch_cache_append(c, cache->B, cache->Hkv, cache->d, n, dtype == SA2_FP16, kr, vr, pos, n_new,
@@ -225,8 +225,8 @@ sa2_status sa2_cache8_read(const sa2_cache8* cache, int32_t n, int32_t dtype, co
   if (n < 1 || !pos) return SA2_ERR_INVALID_ARG;
   if (n >= kMaxTokens || (dtype != SA2_BF16 && dtype != SA2_FP16)) return SA2_ERR_UNSUPPORTED;
   TokenRef kr, vr;
-  st = check_tensor(k, cache->B, cache->Hkv, n, cache->d, 2, &kr);
-  if (st == SA2_OK) st = check_tensor(v, cache->B, cache->Hkv, n, cache->d, 2, &vr);
+  st = check_tensor(k, cache->B, cache->Hkv, 1, n, cache->d, 2, &kr);
+  if (st == SA2_OK) st = check_tensor(v, cache->B, cache->Hkv, 1, n, cache->d, 2, &vr);
   if (st != SA2_OK) return st;
   if (misaligned4(pos)) return SA2_ERR_ALIGNMENT;
   return cuda_status(launch_cache_read(c, cache->B, cache->Hkv, cache->d, n, dtype == SA2_FP16, kr, vr, pos,

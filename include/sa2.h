@@ -276,7 +276,8 @@ sa2_status sa2_vd_loss(const sa2_shape* shape, const void* o_s, const void* o_s_
  * Conventions of these entry points, beside those above
  * - Each token tensor carries its own strides (sa2_tensor): q, o, dO, dq are [B, H, N, d],
  *   k, v, dk, dv are [B, Hkv, M, d], d contiguous.  The stride of a dimension of size 1 is
- *   ignored; every other one must be positive and a multiple of 16 bytes, stride_n >= d.
+ *   ignored; every other one must be positive, a multiple of 16 bytes and below 2^40 bytes,
+ *   stride_n >= d, and with several key heads stride_h * (H / Hkv) below 2^40 bytes.
  *   Inputs may overlap one another; outputs overlap nothing.
  * - Query head h reads key head h / (H / Hkv): H is a multiple of Hkv, H / Hkv <= 64.
  * - d in {64, 128}; dtype SA2_BF16 or SA2_FP16 (the backward: SA2_BF16); 1 <= N, M < 2^28;
