@@ -179,10 +179,27 @@ float scale_of(PyObject* o) {
   return (float)x;
 }
 
-const sa2_cache8* cache_struct(PyObject* o) {
-  if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof(sa2_cache8)) refuse("cache must be a KvCache8");
-  return reinterpret_cast<const sa2_cache8*>(PyBytes_AS_STRING(o));
-}
+// A KvCache8's (sa2_cache8 as bytes, k, v, k_scale, v_scale).  The struct was made from the tensors when the cache
+// was; one whose memory has been exchanged since (x.data = .., x.set_, x.resize_) is refused.
+struct Cache {
+  const sa2_cache8* c;
+  const at::Tensor* t[4];
+  const sa2_cache8* operator->() const { return c; }
+  explicit Cache(PyObject* o) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5 || !PyBytes_Check(PyTuple_GET_ITEM(o, 0)) ||
+        PyBytes_GET_SIZE(PyTuple_GET_ITEM(o, 0)) != (Py_ssize_t)sizeof(sa2_cache8))
+      refuse("cache must be a KvCache8");
+    c = reinterpret_cast<const sa2_cache8*>(PyBytes_AS_STRING(PyTuple_GET_ITEM(o, 0)));
+    const void* held[4] = {c->k, c->v, c->k_scale, c->v_scale};
+    for (int i = 0; i < 4; ++i) {
+      t[i] = &tensor(PyTuple_GET_ITEM(o, i + 1), "cache");
+      if (t[i]->data_ptr() != held[i]) refuse("the cache's tensors have moved since the KvCache8 was made");
+    }
+  }
+  void use(const Place& at_) const {
+    for (const at::Tensor* x : t) at_.use(*x);
+  }
+};
 c10::Device cuda(PyObject* index) {
   const long i = PyLong_AsLong(index);
   if (i < 0) {
@@ -267,8 +284,9 @@ PyObject* cache_pack(PyObject* const* a) {
 
 // cache, device, k, v, pos, n_new, stream
 PyObject* cache_append(PyObject* const* a) {
-  const sa2_cache8* c = cache_struct(a[0]);
+  const Cache c(a[0]);
   const Place at_(cuda(a[1]), a[6]);
+  c.use(at_);
   const at::Tensor& k = dims4(tensor(a[2], "k"), "k");
   const at::ScalarType t = k.scalar_type();
   const int code = dtype_code(t);
@@ -278,14 +296,15 @@ PyObject* cache_append(PyObject* const* a) {
   const int32_t *pos = int32s(a[4], "pos", c->B, at_), *n_new = int32s(a[5], "n_new", c->B, at_);
   if (shape[2] > 0)
     check("sa2_cache8_append",
-          sa2_cache8_append(c, narrow(shape[2], "n"), code, &kt, &vt, pos, n_new, at_.stream));
+          sa2_cache8_append(c.c, narrow(shape[2], "n"), code, &kt, &vt, pos, n_new, at_.stream));
   Py_RETURN_NONE;
 }
 
 // cache, device, pos, n, fp16, k, v, stream
 PyObject* cache_read(PyObject* const* a) {
-  const sa2_cache8* c = cache_struct(a[0]);
+  const Cache c(a[0]);
   const Place at_(cuda(a[1]), a[7]);
+  c.use(at_);
   const long long n = PyLong_AsLongLong(a[3]);
   if (PyErr_Occurred() || n < 0) {
     PyErr_Clear();
@@ -299,20 +318,21 @@ PyObject* cache_read(PyObject* const* a) {
   const at::Tensor v = none(a[6]) ? at_.empty(shape, t) : tensor(a[6], "v");
   const sa2_tensor kt = token(k, "k", shape, t, at_), vt = token(v, "v", shape, t, at_);
   if (n > 0)
-    check("sa2_cache8_read", sa2_cache8_read(c, narrow(n, "n"), dtype_code(t), &kt, &vt, pos, at_.stream));
+    check("sa2_cache8_read", sa2_cache8_read(c.c, narrow(n, "n"), dtype_code(t), &kt, &vt, pos, at_.stream));
   return tuple_of(k, v);
 }
 
 // q, cache, device, kv_len, scale, o, lse, ws, stream
 PyObject* cache_attn(PyObject* const* a) {
   const at::Tensor& q = dims4(tensor(a[0], "q"), "q");
-  const sa2_cache8* c = cache_struct(a[1]);
+  const Cache c(a[1]);
   const sa2_cross_shape s = cross_shape(q, c->Hkv, c->C);
   if (s.B != c->B || s.d != c->d)
     refuse("the cache holds B = ", c->B, ", d = ", c->d, "; q has B = ", s.B, ", d = ", s.d);
   if (none(a[3])) refuse("kv_len is required");
   const Place at_(q.device(), a[8]);
   if (cuda(a[2]) != at_.device) refuse("the cache must be on ", at_.device, ", got ", cuda(a[2]));
+  c.use(at_);
   const int64_t ls[3] = {q.size(0), q.size(1), q.size(2)};
   const at::ScalarType t = q.scalar_type();
   const sa2_tensor qt = token(q, "q", q.sizes(), t, at_);
@@ -321,7 +341,7 @@ PyObject* cache_attn(PyObject* const* a) {
   const at::Tensor lse = none(a[6]) ? at_.empty(ls, at::kFloat) : tensor(a[6], "lse");
   const sa2_tensor ot = token(o, "o", q.sizes(), t, at_);
   const Workspace ws(a[7], sa2_cross_fwd_workspace_size(&s), at_);
-  check("sa2_cache8_attn", sa2_cache8_attn(&s, &qt, c, len, scale_of(a[4]), &ot, float32s(lse, "lse", ls, at_),
+  check("sa2_cache8_attn", sa2_cache8_attn(&s, &qt, c.c, len, scale_of(a[4]), &ot, float32s(lse, "lse", ls, at_),
                                            ws.p, ws.bytes, at_.stream));
   return tuple_of(o, lse);
 }

@@ -320,14 +320,16 @@ def cross_attn_bwd(q, k, v, o, lse, do, kv_len: Optional[torch.Tensor] = None, s
 class KvCache8:
     """Keys and values held in 8 bits: k, v e4m3 [B, Hkv, C, d] (float8_e4m3fn or uint8, with the same
     strides) and k_scale, v_scale float32 [B, Hkv, ceil(C / 64)], one power-of-two scale for each head
-    and block of 64 tokens.  The tensors are the cache's for good; the caller keeps the lengths."""
+    and block of 64 tokens.  The tensors are the cache's for good: calls refuse one whose memory has been
+    exchanged (``x.data = ...``).  The caller keeps the lengths."""
 
     BLOCK = 64
-    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_shape", "_device", "_struct")
+    __slots__ = ("_k", "_v", "_k_scale", "_v_scale", "_shape", "_device", "_struct", "_held")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         self._shape, self._device, self._struct = (_binding or load_binding()).cache8_pack(k, v, k_scale, v_scale)
         self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        self._held = (self._struct, k, v, k_scale, v_scale)
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
@@ -336,10 +338,8 @@ class KvCache8:
     shape = property(lambda self: self._shape, doc="(B, Hkv, capacity, d)")
     device = property(lambda self: self._k.device)
 
-    def _used_on(self, stream) -> None:
-        """Holds the cache's memory back from reuse until the stream is done with it."""
-        for x in (self._k, self._v, self._k_scale, self._v_scale):
-            x.record_stream(stream)
+    def __reduce__(self):  # a copy's pointers are those of its own tensors
+        return KvCache8, (self._k, self._v, self._k_scale, self._v_scale)
 
     @staticmethod
     def empty(B: int, Hkv: int, capacity: int, d: int, device) -> "KvCache8":
@@ -353,9 +353,7 @@ def cache8_append(cache: KvCache8, k: torch.Tensor, v: torch.Tensor, pos: torch.
                   n_new: Optional[torch.Tensor] = None, stream=None) -> None:
     """sa2_cache8_append: writes k, v [B, Hkv, n, d] (bfloat16 or float16) at positions pos[b] ..
     pos[b] + n - 1 (n_new[b] tokens of each sequence where given).  ``pos``, ``n_new``: [B] int32."""
-    (_binding or load_binding()).cache8_append(cache._struct, cache._device, k, v, pos, n_new, _handle(stream))
-    if stream is not None:
-        cache._used_on(stream)
+    (_binding or load_binding()).cache8_append(cache._held, cache._device, k, v, pos, n_new, _handle(stream))
 
 
 def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
@@ -363,11 +361,8 @@ def cache8_read(cache: KvCache8, pos: torch.Tensor, n: int, dtype=torch.bfloat16
     """sa2_cache8_read: the values of tokens pos[b] .. pos[b] + n - 1 as (K, V) [B, Hkv, n, d]."""
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"unsupported dtype {dtype}: torch.bfloat16 or torch.float16")
-    got = (_binding or load_binding()).cache8_read(cache._struct, cache._device, pos, n, dtype is torch.float16, k, v,
-                                                   _handle(stream))
-    if stream is not None:
-        cache._used_on(stream)
-    return got
+    return (_binding or load_binding()).cache8_read(cache._held, cache._device, pos, n, dtype is torch.float16, k, v,
+                                                    _handle(stream))
 
 
 def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: Optional[float] = None,
@@ -375,11 +370,8 @@ def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: O
                 ws: Optional[torch.Tensor] = None, stream=None):
     """sa2_cache8_attn: attention of q [B, H, N, d] to the first kv_len[b] tokens of the cache;
     returns (O, LSE) as cross_attn_fwd does."""
-    got = (_binding or load_binding()).cache8_attn(q, cache._struct, cache._device, kv_len, scale, o, lse, ws,
-                                                   _handle(stream))
-    if stream is not None:
-        cache._used_on(stream)
-    return got
+    return (_binding or load_binding()).cache8_attn(q, cache._held, cache._device, kv_len, scale, o, lse, ws,
+                                                    _handle(stream))
 
 
 def device_status(stream=None) -> int:
