@@ -931,6 +931,7 @@ FwdPlan cross_fwd_plan(const CrossShape& s, int sms) {
     p.segs = segs > INT32_MAX ? -1 : (int)segs;
     p.split = s.M > 1024 && segs < 8 * (int64_t)sms;
     p.grid = p.split ? (int)std::min<int64_t>(sms, segs * ((s.M + 63) / 64)) : p.segs;
+    p.join_rows = kFewRows;
     return p;
   }
   p.few = false;
@@ -949,14 +950,14 @@ FwdPlan cross_fwd_plan(const CrossShape& s, int sms) {
   p.segs = segs > INT32_MAX ? -1 : (int)segs;
   const int64_t items = p.split ? segs * blocks : segs;
   p.grid = (int)(items < sms ? items : sms);
+  // 16 rows per CTA while that is needed to fill the SMs, eight CTAs on each, then 64 (finding a segment's
+  // parts takes a warp as long as two rows)
+  p.join_rows = segs * (p.tp * 8) > 8 * (int64_t)sms ? 64 : 16;
   return p;
 }
 
 cudaError_t launch_cross_join(const CrossShape& s, const FwdPlan& p, const CrossFwdArgs& a, cudaStream_t st) {
-  // 16 rows per CTA while that is needed to fill the SMs, then 64 (finding a segment's parts takes a
-  // warp as long as two rows)
-  const int rows = std::min(p.tp * 128, p.rows), per = p.segs * (rows / 16) > 8 * 152 && rows >= 64 ? 64 : 16;
-  const dim3 grid((unsigned)p.segs, (unsigned)(rows / per));
+  const dim3 grid((unsigned)p.segs, (unsigned)(std::min(p.tp * 128, p.rows) / p.join_rows));
   const bool f16 = s.dtype == SA2_FP16;
   prof_start(st, kAttnFwd);
   const auto kern = s.d == 128 ? (f16 ? cross_join_kernel<128, true> : cross_join_kernel<128, false>)

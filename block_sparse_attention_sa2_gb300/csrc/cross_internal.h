@@ -49,6 +49,7 @@ struct FwdPlan {
   int split;
   int shift;  // log2 of the keys per block
   int rows;   // of a slot of the split's partial results
+  int join_rows;  // split: rows of a segment per CTA of the kernel that joins the parts
   bool few;   // at most kFewRows query rows per key head: the kernel of cross_decode.cu
 };
 constexpr int kFewRows = 16;
