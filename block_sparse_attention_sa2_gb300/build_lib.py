@@ -1,9 +1,11 @@
 """Build step of libsa2: compiles every CUDA source under csrc/ for sm_103a with nvcc (one
 process per translation unit, in parallel) and links the in-tree shared library
 ``libsa2.so`` next to this file, then the extension module ``_cross`` (csrc/cross_binding.cpp, with
-the host compiler and torch's headers), which is linked to it.  Objects go to ``_build/``.
+the host compiler and torch's headers), which is linked to it.  Objects go to ``_build/``.  A host without
+torch, which has the C ABI alone, gets ``libsa2.so`` alone.
 
 Usage: python -m block_sparse_attention_sa2_gb300.build_lib [--force] [--verbose]
+(without torch: python block_sparse_attention_sa2_gb300/build_lib.py)
 """
 from __future__ import annotations
 
@@ -38,16 +40,29 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + [BINDING_SRC] + sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+def _headers():
+    return sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + \
         sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _torch():
+    """torch, or None on a host without it."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch
+
+
+def _newer(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    """Whether libsa2.so, and with torch its binding, are newer than their sources."""
+    if not _newer(LIB, _sources() + _headers()):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _torch() is None or _newer(BINDING, [BINDING_SRC] + _headers())
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -64,10 +79,8 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_binding() -> str:
+def _compile_binding(torch) -> str:
     import sysconfig
-
-    import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     obj = os.path.join(BUILD, "cross_binding.o")
@@ -81,8 +94,7 @@ def _compile_binding() -> str:
     return obj
 
 
-def _link_binding(obj: str) -> None:
-    import torch
+def _link_binding(obj: str, torch) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lsa2", "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python",
@@ -93,16 +105,7 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libsa2.so (skipped when it is newer than every source)."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
-    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding_obj = binding.result()
+def _link_library(objs) -> None:
     tmp = LIB + ".tmp"
     # static CUDA runtime; driver entry points are resolved at run time, so no -lcuda
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
@@ -110,7 +113,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link libsa2.so, then with torch its binding (skipped when they are newer than every source).
+    A binding that fails to build raises, after libsa2.so has been linked."""
+    if not force and up_to_date():
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    srcs, torch = _sources(), _torch()
+    with ThreadPoolExecutor(max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = None if torch is None else ex.submit(_compile_binding, torch)
+        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+    _link_library(objs)
+    if binding is None:
+        print("build_lib: no torch on this host: libsa2.so alone, without the Python binding _cross.so", file=sys.stderr)
+    else:
+        _link_binding(binding.result(), torch)
     return LIB
 
 
