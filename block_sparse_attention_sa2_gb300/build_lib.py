@@ -21,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsa2.so")
 BINDING = os.path.join(PKG, "_cross.so")
+BINDING_FOR = os.path.join(BUILD, "_cross.for")  # what _cross.so was built for
 BINDING_SRC = os.path.join(CSRC, "cross_binding.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -54,15 +55,26 @@ def _torch():
     return torch
 
 
+def _binding_for(torch) -> str:
+    """The Python and torch that a binding built now is for."""
+    return f"{sys.implementation.cache_tag} torch {torch.__version__} {torch.__file__}"
+
+
 def _newer(target: str, deps) -> bool:
     return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
 
 
 def up_to_date() -> bool:
-    """Whether libsa2.so, and with torch its binding, are newer than their sources."""
+    """Whether libsa2.so, and with torch its binding for that torch, are newer than their sources."""
     if not _newer(LIB, _sources() + _headers()):
         return False
-    return _torch() is None or _newer(BINDING, [BINDING_SRC] + _headers())
+    torch = _torch()
+    if torch is None:
+        return True
+    if not _newer(BINDING, [BINDING_SRC] + _headers()) or not os.path.exists(BINDING_FOR):
+        return False
+    with open(BINDING_FOR) as f:
+        return f.read() == _binding_for(torch)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -103,6 +115,8 @@ def _link_binding(obj: str, torch) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_binding_for(torch))
 
 
 def _link_library(objs) -> None:

@@ -1,4 +1,5 @@
-"""What the build step does without torch or a host compiler (CPU; compilers are stand-ins)."""
+"""What the build step does without torch or a host compiler, and when the Python binding is stale (CPU;
+compilers are stand-ins)."""
 import os
 import sys
 import types
@@ -16,6 +17,8 @@ def build_lib(tmp_path, monkeypatch):
     spec.loader.exec_module(m)
     for name, file in (("LIB", "libsa2.so"), ("BINDING", "_cross.so"), ("BUILD", "_build")):
         monkeypatch.setattr(m, name, str(tmp_path / file))
+    if hasattr(m, "BINDING_FOR"):
+        monkeypatch.setattr(m, "BINDING_FOR", str(tmp_path / "_build" / "_cross.for"))
     runs = []
 
     def run(cmd, **kw):
@@ -51,6 +54,22 @@ def test_without_a_host_compiler_the_library_is_there(build_lib):
     build_lib.no_host_compiler = False
     build_lib.build()
     assert os.path.exists(build_lib.BINDING) and build_lib.up_to_date()
+
+
+@pytest.mark.parametrize("change", ["torch", "python", "unknown"])
+def test_a_binding_for_another_torch_or_python_is_stale(build_lib, monkeypatch, change):
+    torch = pytest.importorskip("torch")
+    build_lib.build()
+    assert build_lib.up_to_date()
+    if change == "torch":
+        monkeypatch.setattr(torch, "__version__", "0.0.1")
+    elif change == "python":
+        monkeypatch.setattr(sys.implementation, "cache_tag", "cpython-399")
+    else:  # built by an earlier form of the build step
+        os.remove(build_lib.BINDING_FOR)
+    assert not build_lib.up_to_date()
+    build_lib.build()
+    assert build_lib.up_to_date()
 
 
 def test_a_newer_source_is_built(build_lib):
