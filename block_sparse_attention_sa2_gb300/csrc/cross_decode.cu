@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
         mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(0xffffffffu, mx[hf], 2));
       }
       if (i == 0) {
-        m_used[0] = mx[0];
-        m_used[1] = mx[1];
+        m_used[0] = fmaxf(mx[0], kLeastRef);
+        m_used[1] = fmaxf(mx[1], kLeastRef);
       } else if (__any_sync(0xffffffffu, mx[0] > m_used[0] + kRescaleThreshold || mx[1] > m_used[1] + kRescaleThreshold)) {
         float al[2];
 #pragma unroll
@@ -391,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, Fw
         sum = fmaf(ex2(warp_r[w][r] - lr), warp_l[w][r], sum);
       }
       const float root = ex2(0.5f * (m - lr));  // 2^(m - lr) alone may leave fp32's range
-      const float inv = x.nb > 0 ? root / sum * root : 0.f;
-      const float lse2 = x.nb > 0 ? (nan ? m : lr) + __log2f(sum) : -INFINITY;
+      const float inv = sum == 0.f ? 0.f : root / sum * root;  // (no keys, or no score above -inf)
+      const float lse2 = (nan ? m : lr) + __log2f(sum);
       const int n = r / s.G, h = x.hk * s.G + r - n * s.G;
       if (plan.split) {
         const int64_t row = ((int64_t)blockIdx.x + x.seg) * kFewRows + r;

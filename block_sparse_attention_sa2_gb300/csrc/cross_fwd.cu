@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_scores(ts, y, valid);
           const float m0 = max32(y);
           load_scores(ts + 32, y, valid - 32);
-          m_used = m_run = fmaf(fmaxf(m0, max32(y)), mul, ev);
+          m_used = m_run = fmaxf(fmaf(fmaxf(m0, max32(y)), mul, ev), kLeastRef);
         } else if (__any_sync(0xffffffffu, m_run > m_used + kRescaleThreshold)) {
           ok = rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
         }
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        row_s[t * 128 + r] = 1.f / l;
+        row_s[t * 128 + r] = inverse_sum(l);
         mbar_arrive(bar_l(t));
       } else {
         if (!__all_sync(0xffffffffu, mbar_wait(bar_o(t), pc & 1, wc))) {
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
     const int tok_r = r / s.G, g = r - tok_r * s.G, n = tile * plan.nb + tok_r, h = hk * s.G + g;
     if (tok_r >= plan.nb || n >= s.N) continue;
     // lane i has part c0 + i's sum; 32 parts at a time (more are rare), eight of their rows in flight
-    float m = -INFINITY, acc[kPer] = {}, l = 0.f;
+    float m = kLeastRef, acc[kPer] = {}, l = 0.f;
     for (int base = c0; base <= c1; base += 32) {
       const int n32 = min(32, c1 + 1 - base);
       const float mine = lane < n32 ? a.part_l[((int64_t)base + lane + seg) * plan.rows + rr] : -INFINITY;
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
         }
       }
     }
-    const float inv = nk > 0 ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
     uint32_t w[kPer / 2];
 #pragma unroll
     for (int q = 0; q < kPer / 2; ++q)
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(CrossShape s, FwdPlan p
     else
       *reinterpret_cast<uint32_t*>(op) = w[0];
     if (lane == 0)
-      a.lse[((int64_t)b * s.H + h) * s.N + n] = nk > 0 ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+      a.lse[((int64_t)b * s.H + h) * s.N + n] = (m + __log2f(l)) * 0.69314718055994531f;
   }
 }
 

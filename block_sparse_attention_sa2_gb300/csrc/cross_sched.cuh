@@ -10,6 +10,12 @@ namespace sa2 {
 __device__ __forceinline__ void kernel_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void kernel_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The least reference of a row's exponentials: finite, so that scores of -inf (an infinite key) count as 0 against it
+// even where a block, a warp's step or a part has no other.
+constexpr float kLeastRef = -3.4028234663852886e38f;
+// 1 / l; 0 for a row without any score above -inf, whose O is then 0 and whose LSE is -inf.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 // The factor from products to scores of a block of cached keys.  It is a product of three numbers, of which two are
 // powers of two as small as 2^-112 and 2^-100: kept above 0, where every score is 0 all the same (the products are
 // below 2^32), since scores behind the last key are -inf and 0 times that is NaN.

@@ -312,7 +312,8 @@ size_t sa2_cross_fwd_workspace_size(const sa2_cross_shape* shape);
  *   O_a = sum_c exp(s_ac - LSE_a) v_c.
  * Scores, the softmax statistics and the sums are held in fp32; P is rounded to the call's
  * 16-bit type for P V.  The sums of P V run relative to a running maximum that single scores
- * may exceed by 2^14 until it follows: O is finite for |v| < 2^100 (M < 2^20).
+ * may exceed by 2^14 until it follows: O is finite for |v| < 2^100 (M < 2^20).  A score of -inf
+ * (an infinite key) leaves its key out; a row without any other gets O = 0, LSE = -inf.
  *   scale   <= 0 means 1/sqrt(d)
  *   lse     [B, H, N] fp32 output, contiguous
  *   ws      device workspace of at least sa2_cross_fwd_workspace_size(shape) bytes (may be
@@ -334,7 +335,9 @@ size_t sa2_cross_bwd_workspace_size(const sa2_cross_shape* shape);
  *   dS = P * (dP - D),  dQ = scale dS K,  dK = scale dS^T Q,
  * dK and dV summed over the query heads that share a key head.  Sums are held in fp32, P and
  * dS rounded to bf16 for their products; no sum depends on scheduling.  Keys behind
- * kv_len[b], and sequences of length 0, get zero gradients.
+ * kv_len[b], and sequences of length 0, get zero gradients.  An infinite key, which the forward
+ * leaves out, has no gradient here: dQ = scale dS K is NaN by the formula (0 * inf), and so may
+ * that key's dK and dV be.
  *   o, lse       from sa2_cross_attn_fwd on the same q, k, v, kv_len and scale
  *   dq, dk, dv   outputs: [B, H, N, d] and [B, Hkv, M, d], every element is written
  *   ws           device workspace of at least sa2_cross_bwd_workspace_size(shape) bytes;
