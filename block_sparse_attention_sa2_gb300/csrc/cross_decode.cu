@@ -4,8 +4,9 @@
 // Every key and value is used for 16 rows at most, so the bytes bound it: the kernel is built to keep
 // them coming.  One CTA of 8 warps per SM; each warp takes its own steps of keys (4 KB of K and 4 KB
 // of V), copied into a ring of its own in shared memory by cp.async, three steps deep: 192 KB under
-// way per SM, and no barrier between warps until the end of a piece (one query of 8 x 40 heads over 16384
-// cached keys, d = 128: 200 us, 6.7 TB/s).  The products are the warp's own
+// way per SM, and no barrier between warps until the end of a piece (8 x 40 heads, 32760 keys, d = 128: one
+// query 376 us over cached keys, 7.1 TB/s, and 796 over 16-bit ones, 6.7 TB/s; 16 queries 388 and 792; 17, which
+// the kernel of 128-row tiles takes, 895 and 798).  The products are the warp's own
 // mma.sync m16n8k16: tcgen05 works on 128 rows, of which 112 would be empty, and needs its operands in
 // the layouts that TMA writes, while here the bytes go from the ring straight into fragments:
 //   S = Q K^T   A = Q (16 rows), B = K: thread (g, t) = (lane / 4, lane % 4) holds key g's channels

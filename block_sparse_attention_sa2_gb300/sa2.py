@@ -305,7 +305,8 @@ def cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Op
 
     H is a multiple of Hkv (query head h reads key head h // (H // Hkv)); bfloat16 or float16; each
     tensor with strides of its own.  ``kv_len`` ([B] int32 on the device): sequence b attends to its
-    first kv_len[b] keys; without keys O = 0 and LSE = -inf.  LSE is float32 [B, H, N]."""
+    first kv_len[b] keys; without keys O = 0 and LSE = -inf.  LSE is float32 [B, H, N].  ``scale``: 1/sqrt(d)
+    where it is not given or not positive."""
     return (_binding or load_binding()).cross_attn_fwd(q, k, v, kv_len, scale, o, lse, ws, _handle(stream))
 
 
