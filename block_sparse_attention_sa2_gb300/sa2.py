@@ -340,7 +340,7 @@ class KvCache8:
     device = property(lambda self: self._k.device)
 
     def __reduce__(self):  # a copy's pointers are those of its own tensors
-        return KvCache8, (self._k, self._v, self._k_scale, self._v_scale)
+        return type(self), (self._k, self._v, self._k_scale, self._v_scale)
 
     @staticmethod
     def empty(B: int, Hkv: int, capacity: int, d: int, device) -> "KvCache8":

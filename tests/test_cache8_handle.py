@@ -58,6 +58,15 @@ def test_a_shallow_copy_is_the_same_cache(sa2):
     assert d.k is c.k and d.v_scale is c.v_scale and pointers(d) == pointers(c) == tensors(c)
 
 
+def test_a_copy_is_of_the_same_class(sa2):
+    class Named(sa2.KvCache8):
+        pass
+
+    c = filled(sa2)
+    n = Named(c.k, c.v, c.k_scale, c.v_scale)
+    assert type(copy.deepcopy(n)) is Named and type(copy.copy(n)) is Named
+
+
 def test_a_copy_is_made_after_tensors_moved(sa2):
     c = filled(sa2)
     c.k.data = c.k.clone()
