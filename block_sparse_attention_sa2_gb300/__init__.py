@@ -7,6 +7,8 @@ The Python surface is a thin ctypes binding (``sa2.py``); the library is built i
 from .sa2 import (  # noqa: F401
     BlockMask,
     KvCache8,
+    PagedCache,
+    Rotary,
     Sa2Error,
     attn_bwd,
     attn_fwd,
@@ -22,8 +24,13 @@ from .sa2 import (  # noqa: F401
     device_status,
     load_library,
     make_shape,
+    packed_attn_fwd,
+    paged_append,
+    paged_attn,
     profiler_collect,
     profiler_enable,
+    rotary,
+    rotary_frequencies,
     vd_loss,
     workspace,
 )

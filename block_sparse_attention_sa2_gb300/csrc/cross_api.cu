@@ -5,13 +5,7 @@
 
 #include "cross_internal.h"
 
-using namespace sa2;
-
-namespace {
-
-constexpr int kMaxTokens = 1 << 28;
-constexpr int kMaxGroup = 64;
-constexpr int kMaxGridYZ = 32767;  // B and Hkv are grid dimensions (B twice over)
+namespace sa2 {
 
 // SMs of the current device (152 where there is none, so that sizes can be asked for on any host).
 int sm_count() {
@@ -27,6 +21,33 @@ int sm_count() {
 }
 
 sa2_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SA2_OK : SA2_ERR_CUDA; }
+
+// Checks a token tensor of B x heads x tokens x d elements of which G heads share a key head; strides of
+// dimensions of size 1 are replaced by d, so that a tensor map sees legal ones.
+sa2_status check_tensor(const sa2_tensor* t, int B, int heads, int G, int tokens, int d, int esz, TokenRef* r) {
+  if (!t || !t->data) return SA2_ERR_INVALID_ARG;
+  if (!aligned16(t->data)) return SA2_ERR_ALIGNMENT;
+  r->p = t->data;
+  r->sn = tokens > 1 ? t->stride_n : d;
+  r->sh = heads > 1 ? t->stride_h : d;
+  r->sb = B > 1 ? t->stride_b : d;
+  if (r->sn < d || r->sh < 1 || r->sb < 1) return SA2_ERR_INVALID_ARG;
+  if (r->sn * esz % 16 || r->sh * esz % 16 || r->sb * esz % 16) return SA2_ERR_ALIGNMENT;
+  // a tensor map's strides are below 2^40 bytes; that of the key heads' groups is one of them
+  const int64_t most = ((int64_t)1 << 40) / esz;
+  if (r->sn >= most || r->sh >= (heads > G ? most / G : most) || r->sb >= most) return SA2_ERR_UNSUPPORTED;
+  return SA2_OK;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace sa2
+
+using namespace sa2;
+
+namespace {
+
+constexpr int kMaxGridYZ = 32767;  // B and Hkv are grid dimensions (B twice over)
 
 sa2_status check_cross(const sa2_cross_shape* x, CrossShape* s) {
   if (!x) return SA2_ERR_INVALID_ARG;
@@ -46,23 +67,6 @@ sa2_status check_cross(const sa2_cross_shape* x, CrossShape* s) {
   s->d = x->d;
   s->dtype = x->dtype;
   wait_settings(&s->wait_ns, &s->stall_ns);
-  return SA2_OK;
-}
-
-// Checks a token tensor of B x heads x tokens x d elements of which G heads share a key head; strides of
-// dimensions of size 1 are replaced by d, so that a tensor map sees legal ones.
-sa2_status check_tensor(const sa2_tensor* t, int B, int heads, int G, int tokens, int d, int esz, TokenRef* r) {
-  if (!t || !t->data) return SA2_ERR_INVALID_ARG;
-  if (!aligned16(t->data)) return SA2_ERR_ALIGNMENT;
-  r->p = t->data;
-  r->sn = tokens > 1 ? t->stride_n : d;
-  r->sh = heads > 1 ? t->stride_h : d;
-  r->sb = B > 1 ? t->stride_b : d;
-  if (r->sn < d || r->sh < 1 || r->sb < 1) return SA2_ERR_INVALID_ARG;
-  if (r->sn * esz % 16 || r->sh * esz % 16 || r->sb * esz % 16) return SA2_ERR_ALIGNMENT;
-  // a tensor map's strides are below 2^40 bytes; that of the key heads' groups is one of them
-  const int64_t most = ((int64_t)1 << 40) / esz;
-  if (r->sn >= most || r->sh >= (heads > G ? most / G : most) || r->sb >= most) return SA2_ERR_UNSUPPORTED;
   return SA2_OK;
 }
 
@@ -89,8 +93,6 @@ sa2_status check_cache(const sa2_cache8* x, CacheRef* c) {
   c->nsb = (x->C + 63) / 64;
   return SA2_OK;
 }
-
-bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 // What the two forward calls share: q, o, lse, kv_len, the plan and its workspace.
 sa2_status fwd_args(const CrossShape& s, const sa2_tensor* q, const int32_t* kv_len, float scale, const sa2_tensor* o,

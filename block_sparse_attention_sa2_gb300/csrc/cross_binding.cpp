@@ -1,5 +1,6 @@
-// Python binding of the cross- and cache-attention calls (include/sa2.h): checks of the tensors,
-// allocation of outputs and workspaces, and the C call, in one extension module.
+// Python binding of the cross-, cache-, packed- and paged-attention calls and of rotary positions
+// (include/sa2.h): checks of the tensors, allocation of outputs and workspaces, and the C call, in one
+// extension module.
 //
 // The rest of the library is called through ctypes (sa2.py).  These calls are not, because they are
 // made with a few keys or a single token too, where the GPU needs 2 to 7 microseconds: packing the
@@ -346,6 +347,226 @@ PyObject* cache_attn(PyObject* const* a) {
   return tuple_of(o, lse);
 }
 
+// ---------------------------------------------------------------- packed sequences, paged cache, rotary positions
+
+const at::Tensor& dims3(const at::Tensor& x, const char* name) {
+  if (x.dim() != 3) refuse(name, ": token tensors of packed sequences are [H, T, d]");
+  return x;
+}
+
+// sa2_tensor of a token tensor of packed sequences of this shape, type and device.
+sa2_tensor token3(const at::Tensor& x, const char* name, Sizes shape, at::ScalarType dtype, const Place& at_) {
+  if (x.sizes() != shape) refuse(name, " must be ", shape, ", got ", x.sizes());
+  if (x.scalar_type() != dtype) refuse(name, " must be ", dtype, ", got ", x.scalar_type());
+  if (x.device() != at_.device) refuse(name, " must be on ", at_.device, ", got ", x.device());
+  const Sizes st = x.strides();
+  if (st[2] != 1) refuse(name, ": the last dimension must be contiguous");
+  return {at_.use(x).data_ptr(), 0, st[0], st[1]};
+}
+
+// Sequences of an argument `seq` of B + 1 places.
+int64_t sequences(PyObject* o) {
+  const at::Tensor& x = tensor(o, "seq");
+  if (x.dim() != 1 || x.size(0) < 2) refuse("seq must be an int32 tensor of the places of B sequences and the end, [B + 1]");
+  return x.size(0) - 1;
+}
+
+bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+
+sa2_packed_shape packed_shape(const at::Tensor& q, int64_t Hkv, int64_t B, bool causal) {
+  return {narrow(B, "B"), narrow(q.size(0), "H"), narrow(Hkv, "Hkv"), narrow(q.size(1), "T"), narrow(q.size(2), "d"),
+          dtype_code(q.scalar_type()), causal ? 1 : 0, 0};
+}
+
+// q, k, v, seq, causal, scale, o, lse, ws, stream
+PyObject* packed_fwd(PyObject* const* a) {
+  const at::Tensor& q = dims3(tensor(a[0], "q"), "q");
+  const at::Tensor& k = dims3(tensor(a[1], "k"), "k");
+  const at::Tensor& v = tensor(a[2], "v");
+  const sa2_packed_shape s = packed_shape(q, k.size(0), sequences(a[3]), truth(a[4]));
+  const Place at_(q.device(), a[9]);
+  const int64_t kvs[3] = {k.size(0), q.size(1), q.size(2)}, ls[2] = {q.size(0), q.size(1)};
+  const at::ScalarType t = q.scalar_type();
+  const sa2_tensor qt = token3(q, "q", q.sizes(), t, at_), kt = token3(k, "k", kvs, t, at_), vt = token3(v, "v", kvs, t, at_);
+  const int32_t* seq = int32s(a[3], "seq", s.B + 1, at_);
+  const at::Tensor o = at_.given_or_like(a[6], "o", q);
+  const at::Tensor lse = none(a[7]) ? at_.empty(ls, at::kFloat) : tensor(a[7], "lse");
+  const sa2_tensor ot = token3(o, "o", q.sizes(), t, at_);
+  float* lp = float32s(lse, "lse", ls, at_);
+  const float scale = scale_of(a[5]);
+  const Workspace ws(a[8], sa2_packed_fwd_workspace_size(&s), at_);
+  if (s.T > 0)
+    check("sa2_packed_attn_fwd", sa2_packed_attn_fwd(&s, &qt, &kt, &vt, seq, scale, &ot, lp, ws.p, ws.bytes, at_.stream));
+  return tuple_of(o, lse);
+}
+
+// k, v: checks a paged cache's tensors; its (shape, device index or -1, sa2_paged_cache as bytes).
+PyObject* paged_pack(PyObject* const* a) {
+  const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+  if (k.dim() != 4 || v.sizes() != k.sizes() || v.strides() != k.strides() || k.stride(3) != 1)
+    refuse("the cache's k and v are [pages, Hkv, page, d] with the same strides, d contiguous");
+  if (v.scalar_type() != k.scalar_type() || v.device() != k.device())
+    refuse("the cache's k and v have one type and are on one device");
+  const Sizes sz = k.sizes(), st = k.strides();
+  sa2_paged_cache c{k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], narrow(sz[0], "pages"), narrow(sz[1], "Hkv"),
+                    narrow(sz[2], "page"), narrow(sz[3], "d"), dtype_code(k.scalar_type()), 0};
+  if (c.page < 16 || c.page > 65536 || (c.page & (c.page - 1)))
+    refuse("a page holds a power of two of tokens from 16 to 65536, got ", c.page);
+  return Py_BuildValue("((LLLL)iy#)", (long long)sz[0], (long long)sz[1], (long long)sz[2], (long long)sz[3],
+                       k.device().has_index() ? (int)k.device().index() : -1, reinterpret_cast<const char*>(&c),
+                       (Py_ssize_t)sizeof(c));
+}
+
+// A PagedCache's (sa2_paged_cache as bytes, k, v), held to its tensors as Cache is.
+struct Pages {
+  const sa2_paged_cache* c;
+  const at::Tensor* t[2];
+  const sa2_paged_cache* operator->() const { return c; }
+  explicit Pages(PyObject* o) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3 || !PyBytes_Check(PyTuple_GET_ITEM(o, 0)) ||
+        PyBytes_GET_SIZE(PyTuple_GET_ITEM(o, 0)) != (Py_ssize_t)sizeof(sa2_paged_cache))
+      refuse("cache must be a PagedCache");
+    c = reinterpret_cast<const sa2_paged_cache*>(PyBytes_AS_STRING(PyTuple_GET_ITEM(o, 0)));
+    const void* held[2] = {c->k, c->v};
+    for (int i = 0; i < 2; ++i) {
+      t[i] = &tensor(PyTuple_GET_ITEM(o, i + 1), "cache");
+      if (t[i]->data_ptr() != held[i]) refuse("the cache's tensors have moved since the PagedCache was made");
+    }
+  }
+  void use(const Place& at_) const {
+    for (const at::Tensor* x : t) at_.use(*x);
+  }
+};
+
+sa2_page_table page_table(PyObject* o, int64_t B, const Place& at_) {
+  const at::Tensor& x = tensor(o, "table");
+  if (x.scalar_type() != at::kInt || x.dim() != 2 || x.size(0) != B || (x.size(1) > 1 && x.stride(1) != 1) || x.device() != at_.device)
+    refuse("table must be an int32 tensor [", B, ", pages of a sequence] on ", at_.device, " with contiguous rows");
+  return {static_cast<const int32_t*>(at_.use(x).data_ptr()), x.stride(0), narrow(x.size(1), "pages of a sequence"), 0};
+}
+
+// cache, device, k, v, seq, kv_len, table, stream
+PyObject* paged_append(PyObject* const* a) {
+  const Pages c(a[0]);
+  const Place at_(cuda(a[1]), a[7]);
+  c.use(at_);
+  const at::Tensor& k = dims3(tensor(a[2], "k"), "k");
+  const int64_t shape[3] = {c->Hkv, k.size(1), c->d}, B = sequences(a[4]);
+  const at::ScalarType t = c.t[0]->scalar_type();
+  if (none(a[5])) refuse("kv_len is required");
+  const sa2_tensor kt = token3(k, "k", shape, t, at_), vt = token3(tensor(a[3], "v"), "v", shape, t, at_);
+  const int32_t *seq = int32s(a[4], "seq", B + 1, at_), *len = int32s(a[5], "kv_len", B, at_);
+  const sa2_page_table table = page_table(a[6], B, at_);
+  if (shape[1] > 0)
+    check("sa2_paged_append", sa2_paged_append(c.c, narrow(B, "B"), narrow(shape[1], "T"), &kt, &vt, seq, len, &table, at_.stream));
+  Py_RETURN_NONE;
+}
+
+// q, cache, device, seq, kv_len, table, causal, max_new, scale, o, lse, ws, stream
+PyObject* paged_attn(PyObject* const* a) {
+  const at::Tensor& q = dims3(tensor(a[0], "q"), "q");
+  const Pages c(a[1]);
+  const sa2_packed_shape s = packed_shape(q, c->Hkv, sequences(a[3]), truth(a[6]));
+  if (s.d != c->d || s.dtype != c->dtype) refuse("the cache holds ", c.t[0]->scalar_type(), " of d = ", c->d, "; q is ", q.scalar_type(), " of d = ", s.d);
+  if (none(a[4])) refuse("kv_len is required");
+  int32_t max_new = 0;
+  if (!none(a[7])) {
+    const long long n = PyLong_AsLongLong(a[7]);
+    if (PyErr_Occurred() || n < 1) {
+      PyErr_Clear();
+      refuse("max_new must be a count of tokens");
+    }
+    max_new = (int32_t)(n < s.T ? n : s.T);
+  }
+  const Place at_(q.device(), a[12]);
+  if (cuda(a[2]) != at_.device) refuse("the cache must be on ", at_.device, ", got ", cuda(a[2]));
+  c.use(at_);
+  const int64_t ls[2] = {q.size(0), q.size(1)};
+  const at::ScalarType t = q.scalar_type();
+  const sa2_tensor qt = token3(q, "q", q.sizes(), t, at_);
+  const int32_t *seq = int32s(a[3], "seq", s.B + 1, at_), *len = int32s(a[4], "kv_len", s.B, at_);
+  const sa2_page_table table = page_table(a[5], s.B, at_);
+  const at::Tensor o = at_.given_or_like(a[9], "o", q);
+  const at::Tensor lse = none(a[10]) ? at_.empty(ls, at::kFloat) : tensor(a[10], "lse");
+  const sa2_tensor ot = token3(o, "o", q.sizes(), t, at_);
+  float* lp = float32s(lse, "lse", ls, at_);
+  const float scale = scale_of(a[8]);
+  const Workspace ws(a[11], sa2_paged_attn_workspace_size(&s, c.c, table.width, max_new), at_);
+  if (s.T > 0)
+    check("sa2_paged_attn", sa2_paged_attn(&s, &qt, c.c, seq, len, &table, max_new, scale, &ot, lp, ws.p, ws.bytes, at_.stream));
+  return tuple_of(o, lse);
+}
+
+// A tensor of rotary positions' calls as [B, H, N, d]: packed ones have B = 1.
+struct Turned {
+  int64_t B, H, N, d;
+  sa2_tensor t;
+  Turned(const at::Tensor& x, const char* name, const Place& at_) {
+    const int64_t n = x.dim();
+    if (n != 3 && n != 4) refuse(name, " must be [B, H, N, d] or, of packed sequences, [H, T, d]");
+    if (x.device() != at_.device) refuse(name, " must be on ", at_.device, ", got ", x.device());
+    if (x.stride(n - 1) != 1) refuse(name, ": the last dimension must be contiguous");
+    B = n == 4 ? x.size(0) : 1;
+    H = x.size(n - 3);
+    N = x.size(n - 2);
+    d = x.size(n - 1);
+    t = {at_.use(x).data_ptr(), n == 4 ? x.stride(0) : 0, x.stride(n - 3), x.stride(n - 2)};
+  }
+};
+
+// pairs, n, axes, halves, gain, d, pos, q, k, inverse, q_out, k_out, stream
+PyObject* rotary(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[7], "q");
+  const Place at_(q.device(), a[12]);
+  const at::Tensor& pairs = tensor(a[0], "pairs");
+  if (pairs.device() != at_.device) refuse("the Rotary must be on ", at_.device, ", got ", pairs.device());
+  at_.use(pairs);
+  const int64_t n = PyLong_AsLongLong(a[1]), axes = PyLong_AsLongLong(a[2]), d = PyLong_AsLongLong(a[5]);
+  const double gain = PyFloat_AsDouble(a[4]);
+  if (PyErr_Occurred()) throw python_error();
+  if (pairs.scalar_type() != at::kLong || !pairs.is_contiguous() || pairs.numel() != 2 * n) refuse("the Rotary's pairs have been exchanged");
+  const sa2_rotary r{static_cast<const int64_t*>(pairs.data_ptr()), narrow(n, "pairs"), narrow(axes, "axes"),
+                     truth(a[3]) ? SA2_ROTARY_HALVES : SA2_ROTARY_INTERLEAVED, (float)gain};
+  const at::ScalarType t = q.scalar_type();
+  const int code = t == at::kFloat ? SA2_FP32 : t == at::kBFloat16 ? SA2_BF16 : t == at::kHalf ? SA2_FP16 : -1;
+  if (code < 0) refuse("unsupported dtype ", t, ": torch.bfloat16, torch.float16 or torch.float32");
+  const Turned x(q, "q", at_);
+  if (x.d != d) refuse("the Rotary is for d = ", d, "; q has d = ", x.d);
+  // positions: [axes,] [B,] N
+  const at::Tensor& pos = tensor(a[6], "pos");
+  const int64_t lead = axes > 1 ? 1 : 0, pd = pos.dim();
+  const bool each = pd == lead + 2;
+  if (pos.scalar_type() != at::kInt || !pos.is_contiguous() || pos.device() != at_.device || (!each && pd != lead + 1) ||
+      (lead && pos.size(0) != axes) || (each && pos.size(lead) != x.B) || pos.size(pd - 1) != x.N)
+    refuse("pos must be a contiguous int32 tensor of the tokens' positions ", axes > 1 ? "[axes, B, N] or [axes, N]" : "[B, N] or [N]",
+           " on ", at_.device, ", got ", pos.sizes());
+  const int32_t* pp = static_cast<const int32_t*>(at_.use(pos).data_ptr());
+  const at::Tensor qo = at_.given_or_like(a[10], "q_out", q);
+  auto same = [&](const at::Tensor& y, const at::Tensor& like, const char* name) {
+    if (y.sizes() != like.sizes() || y.scalar_type() != t) refuse(name, " must be ", t, " ", like.sizes(), ", got ", y.scalar_type(), " ", y.sizes());
+  };
+  same(qo, q, "q_out");
+  const Turned y(qo, "q_out", at_);
+  const bool two = !none(a[8]);
+  at::Tensor ko;
+  std::optional<Turned> x2, y2;
+  if (two) {
+    const at::Tensor& k = tensor(a[8], "k");
+    if (k.scalar_type() != t || k.dim() != q.dim()) refuse("k must be ", t, " with as many dimensions as q");
+    x2.emplace(k, "k", at_);
+    if (x2->B != x.B || x2->N != x.N || x2->d != d) refuse("k must have q's sequences, tokens and d, got ", k.sizes());
+    ko = at_.given_or_like(a[11], "k_out", k);
+    same(ko, k, "k_out");
+    y2.emplace(ko, "k_out", at_);
+  }
+  if (x.B * x.N * x.H > 0)
+    check("sa2_rotary_apply",
+          sa2_rotary_apply(&r, code, narrow(x.B, "B"), narrow(x.N, "N"), narrow(d, "d"), pp, x.N * (each ? x.B : 1),
+                           each ? x.N : 0, narrow(x.H, "H"), &x.t, &y.t, two ? narrow(x2->H, "heads of k") : 0,
+                           two ? &x2->t : nullptr, two ? &y2->t : nullptr, truth(a[9]) ? 1 : 0, at_.stream));
+  return two ? tuple_of(qo, ko) : tuple_of(qo);
+}
+
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -375,6 +596,9 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 PyMethodDef methods[] = {FAST("cross_attn_fwd", cross_fwd, 9),   FAST("cross_attn_bwd", cross_bwd, 13),
                          FAST("cache8_append", cache_append, 7), FAST("cache8_read", cache_read, 8),
                          FAST("cache8_attn", cache_attn, 9),     FAST("cache8_pack", cache_pack, 4),
+                         FAST("packed_attn_fwd", packed_fwd, 10), FAST("paged_pack", paged_pack, 2),
+                         FAST("paged_append", paged_append, 8),  FAST("paged_attn", paged_attn, 13),
+                         FAST("rotary", rotary, 13),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_cross", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -9,17 +9,12 @@
 // P and dS are rounded to bf16 for their products.  A query tile's rows are tokens x the G heads
 // that share the key head, so that dK and dV of shared heads need no other sum.
 #include "cross_sched.cuh"
+#include "cross_softmax.cuh"
 
 namespace sa2 {
 namespace {
 
 constexpr uint32_t kTmemCols = 512;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void store32_bf16(uint16_t* dst, const float (&v)[32]) {
   uint4* p = reinterpret_cast<uint4*>(dst);

@@ -19,6 +19,7 @@
 #include <cuda_fp8.h>
 
 #include "cross_sched.cuh"
+#include "cross_softmax.cuh"
 
 namespace sa2 {
 namespace {
@@ -27,13 +28,6 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kTileBytes = 4096;  // of K, and of V, per step
 constexpr int kStageBytes = 2 * kTileBytes;
-constexpr float kRescaleThreshold = 8.0f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // 16 bytes from global to shared memory; zeros where !live (nothing is read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {

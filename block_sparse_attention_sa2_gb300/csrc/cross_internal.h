@@ -127,6 +127,15 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&c, kernel, std::forward<A>(args)...);
 }
 
+// Argument checks that the entry points share (cross_api.cu): limits, the SMs of the current device (152 where
+// there is none), a status for a CUDA error, and a token tensor's pointer and strides.
+constexpr int kMaxTokens = 1 << 28;
+constexpr int kMaxGroup = 64;
+int sm_count();
+sa2_status cuda_status(cudaError_t e);
+sa2_status check_tensor(const sa2_tensor* t, int B, int heads, int G, int tokens, int d, int esz, TokenRef* r);
+bool misaligned4(const void* p);
+
 // The device's status word, and the wait settings of the calling thread's next launches
 // (sa2_api.cu).
 unsigned* status_word();

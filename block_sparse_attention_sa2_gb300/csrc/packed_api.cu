@@ -1,0 +1,227 @@
+// The C ABI of attention within packed sequences, of the paged cache and of rotary positions (include/sa2.h):
+// argument checks, workspace layout, tensor maps and launches.
+#include <algorithm>
+#include <cmath>
+
+#include "paged.h"
+#include "rotary.h"
+
+using namespace sa2;
+
+namespace {
+
+constexpr int kMaxSequences = 1 << 20;
+constexpr int kMaxKeyHeads = 32767;
+
+sa2_status check_packed(const sa2_packed_shape* x, PackedShape* s) {
+  if (!x) return SA2_ERR_INVALID_ARG;
+  if (x->B < 1 || x->H < 1 || x->Hkv < 1 || x->T < 1 || x->reserved != 0) return SA2_ERR_INVALID_ARG;
+  if (x->H % x->Hkv || (x->causal != 0 && x->causal != 1)) return SA2_ERR_INVALID_ARG;
+  if (x->dtype != SA2_BF16 && x->dtype != SA2_FP16) return SA2_ERR_UNSUPPORTED;
+  if (x->d != 64 && x->d != 128) return SA2_ERR_UNSUPPORTED;
+  if (x->T >= kMaxTokens || x->B >= kMaxSequences || x->Hkv > kMaxKeyHeads || x->H / x->Hkv > kMaxGroup)
+    return SA2_ERR_UNSUPPORTED;
+  *s = PackedShape{};
+  s->B = x->B;
+  s->H = x->H;
+  s->Hkv = x->Hkv;
+  s->G = x->H / x->Hkv;
+  s->T = s->max_new = x->T;
+  s->d = x->d;
+  s->dtype = x->dtype;
+  s->causal = x->causal;
+  // (work items are counted in 32 bits; tensors of so many have terabytes)
+  if (s->Hkv * segment_bound(*s, 128 / s->G) > INT32_MAX) return SA2_ERR_UNSUPPORTED;
+  wait_settings(&s->wait_ns, &s->stall_ns);
+  return SA2_OK;
+}
+
+sa2_status check_pages(const sa2_paged_cache* c, TokenRef* k, TokenRef* v) {
+  if (!c || c->reserved != 0 || c->pages < 1 || c->Hkv < 1 || c->page < 1) return SA2_ERR_INVALID_ARG;
+  if (c->dtype != SA2_BF16 && c->dtype != SA2_FP16) return SA2_ERR_UNSUPPORTED;
+  if (c->d != 64 && c->d != 128) return SA2_ERR_UNSUPPORTED;
+  if (c->page < 16 || c->page > 65536 || (c->page & (c->page - 1)) || c->Hkv > kMaxKeyHeads) return SA2_ERR_UNSUPPORTED;
+  const sa2_tensor kt{c->k, c->stride_p, c->stride_h, c->stride_n}, vt{c->v, c->stride_p, c->stride_h, c->stride_n};
+  const sa2_status st = check_tensor(&kt, c->pages, c->Hkv, 1, c->page, c->d, 2, k);
+  return st == SA2_OK ? check_tensor(&vt, c->pages, c->Hkv, 1, c->page, c->d, 2, v) : st;
+}
+
+sa2_status check_table(const sa2_page_table* t, int B) {
+  if (!t || !t->table || t->width < 1 || t->reserved != 0 || (B > 1 && t->stride_b < 0)) return SA2_ERR_INVALID_ARG;
+  return misaligned4(t->table) ? SA2_ERR_ALIGNMENT : SA2_OK;
+}
+
+// The cache's part of a shape.
+sa2_status paged_shape(const sa2_paged_cache* c, int width, int max_new, PackedShape* s) {
+  if (width < 1 || max_new < 0) return SA2_ERR_INVALID_ARG;
+  if ((int64_t)width * c->page >= kMaxTokens) return SA2_ERR_UNSUPPORTED;
+  if (c->Hkv != s->Hkv || c->d != s->d || c->dtype != s->dtype) return SA2_ERR_INVALID_ARG;
+  s->page = c->page;
+  s->box = std::min(c->page, 128);
+  s->pages = c->pages;
+  s->width = width;
+  if (max_new > 0) s->max_new = std::min(max_new, s->T);
+  return SA2_OK;
+}
+
+// What the two forward calls share behind their keys: q, o, lse, the plan and its workspace.
+sa2_status run_fwd(const PackedShape& s, const sa2_tensor* q, const TokenRef& k, const TokenRef& v, const PackedSeqs& seqs,
+                   float scale, const sa2_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!lse || !seqs.seq || !std::isfinite(scale)) return SA2_ERR_INVALID_ARG;
+  PackedFwdArgs a{};
+  TokenRef qr;
+  sa2_status st = check_tensor(q, 1, s.H, s.G, s.T, s.d, 2, &qr);
+  if (st == SA2_OK) st = check_tensor(o, 1, s.H, s.G, s.T, s.d, 2, &a.o);
+  if (st != SA2_OK) return st;
+  if (misaligned4(lse) || misaligned4(seqs.seq) || misaligned4(seqs.kv_len) || !aligned16(ws)) return SA2_ERR_ALIGNMENT;
+  const PackedPlan p = packed_fwd_plan(s, sm_count());
+  const size_t need = packed_fwd_bytes(s, p);
+  if (need && (!ws || ws_bytes < need)) return SA2_ERR_WORKSPACE;
+  a.seqs = seqs;
+  a.lse = lse;
+  a.counter = static_cast<unsigned*>(ws);
+  a.rec = static_cast<int*>(ws);
+  if (p.split) {
+    a.part_l = reinterpret_cast<float*>(static_cast<char*>(ws) + (size_t)p.grid * sizeof(CutRecord));
+    a.part_o = a.part_l + (size_t)2 * p.grid * 256;
+  }
+  const float sc = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)s.d));
+  a.scale_log2 = sc * 1.4426950408889634f;
+  a.status = status_word();
+  CUtensorMap mq, mk, mv, mo;
+  const bool f16 = s.dtype == SA2_FP16;
+  const int box = s.page ? s.box : kKeyBlock, tokens = s.page ? s.page : s.T, outer = s.page ? s.pages : 1;
+  if (!make_group_map(&mq, qr, 1, s.H, s.G, s.T, s.d, s.G, p.nb, f16) ||
+      !make_group_map(&mo, a.o, 1, s.H, s.G, s.T, s.d, s.G, p.nb, f16) ||
+      !make_group_map(&mk, k, outer, s.Hkv, 1, tokens, s.d, 1, box, f16) ||
+      !make_group_map(&mv, v, outer, s.Hkv, 1, tokens, s.d, 1, box, f16))
+    return SA2_ERR_CUDA;
+  return cuda_status(launch_packed_fwd(s, p, mq, mk, mv, mo, a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sa2_packed_fwd_workspace_size(const sa2_packed_shape* shape) {
+  PackedShape s;
+  return check_packed(shape, &s) == SA2_OK ? packed_fwd_bytes(s, packed_fwd_plan(s, sm_count())) : 0;
+}
+
+sa2_status sa2_packed_attn_fwd(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
+                               const sa2_tensor* v, const int32_t* seq, float scale, const sa2_tensor* o, float* lse,
+                               void* ws, size_t ws_bytes, void* stream) {
+  PackedShape s;
+  sa2_status st = check_packed(shape, &s);
+  if (st != SA2_OK) return st;
+  TokenRef kr, vr;
+  st = check_tensor(k, 1, s.Hkv, 1, s.T, s.d, 2, &kr);
+  if (st == SA2_OK) st = check_tensor(v, 1, s.Hkv, 1, s.T, s.d, 2, &vr);
+  if (st != SA2_OK) return st;
+  return run_fwd(s, q, kr, vr, {seq, nullptr, nullptr}, scale, o, lse, ws, ws_bytes, stream);
+}
+
+sa2_status sa2_paged_append(const sa2_paged_cache* cache, int32_t B, int32_t T, const sa2_tensor* k,
+                            const sa2_tensor* v, const int32_t* seq, const int32_t* kv_len,
+                            const sa2_page_table* table, void* stream) {
+  PagedAppendArgs a{};
+  sa2_status st = check_pages(cache, &a.k_pages, &a.v_pages);
+  if (st == SA2_OK) st = check_table(table, B);
+  if (st != SA2_OK) return st;
+  if (B < 1 || T < 1 || !seq || !kv_len) return SA2_ERR_INVALID_ARG;
+  if (T >= kMaxTokens || B >= kMaxSequences || (int64_t)table->width * cache->page >= kMaxTokens) return SA2_ERR_UNSUPPORTED;
+  st = check_tensor(k, 1, cache->Hkv, 1, T, cache->d, 2, &a.k);
+  if (st == SA2_OK) st = check_tensor(v, 1, cache->Hkv, 1, T, cache->d, 2, &a.v);
+  if (st != SA2_OK) return st;
+  if (misaligned4(seq) || misaligned4(kv_len)) return SA2_ERR_ALIGNMENT;
+  a.seqs = {seq, kv_len, table->table};
+  a.B = B;
+  a.T = T;
+  a.Hkv = cache->Hkv;
+  a.words = cache->d / 8;
+  a.page = cache->page;
+  a.pages = cache->pages;
+  a.width = table->width;
+  a.table_stride = B > 1 ? table->stride_b : 0;
+  a.status = status_word();
+  return cuda_status(launch_paged_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sa2_paged_attn_workspace_size(const sa2_packed_shape* shape, const sa2_paged_cache* cache, int32_t width,
+                                     int32_t max_new) {
+  PackedShape s;
+  TokenRef k, v;
+  if (check_packed(shape, &s) != SA2_OK || check_pages(cache, &k, &v) != SA2_OK ||
+      paged_shape(cache, width, max_new, &s) != SA2_OK)
+    return 0;
+  return packed_fwd_bytes(s, packed_fwd_plan(s, sm_count()));
+}
+
+sa2_status sa2_paged_attn(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_paged_cache* cache,
+                          const int32_t* seq, const int32_t* kv_len, const sa2_page_table* table, int32_t max_new,
+                          float scale, const sa2_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  PackedShape s;
+  TokenRef k, v;
+  sa2_status st = check_packed(shape, &s);
+  if (st == SA2_OK) st = check_pages(cache, &k, &v);
+  if (st == SA2_OK) st = check_table(table, s.B);
+  if (st == SA2_OK) st = paged_shape(cache, table->width, max_new, &s);
+  if (st != SA2_OK) return st;
+  if (!kv_len) return SA2_ERR_INVALID_ARG;
+  s.table_stride = s.B > 1 ? table->stride_b : 0;
+  return run_fwd(s, q, k, v, {seq, kv_len, table->table}, scale, o, lse, ws, ws_bytes, stream);
+}
+
+int64_t sa2_rotary_turns(double frequency) {
+  const double t = frequency / 6.283185307179586477, part = t - std::floor(t);
+  if (!(part >= 0.0 && part < 1.0)) return 0;  // (not finite, or a negative one that rounds to a whole turn)
+  return (int64_t)(uint64_t)std::ldexp(part, 64);
+}
+
+sa2_status sa2_rotary_apply(const sa2_rotary* rotary, int32_t dtype, int32_t B, int32_t N, int32_t d,
+                            const int32_t* pos, int64_t pos_axis, int64_t pos_b, int32_t H, const sa2_tensor* x,
+                            const sa2_tensor* y, int32_t H2, const sa2_tensor* x2, const sa2_tensor* y2,
+                            int32_t inverse, void* stream) {
+  if (!rotary || !rotary->pairs || !pos || B < 1 || N < 1 || H < 1 || H2 < 0 || rotary->n < 1 || rotary->axes < 1 ||
+      pos_axis < 0 || pos_b < 0 || !std::isfinite(rotary->gain) || (inverse != 0 && inverse != 1))
+    return SA2_ERR_INVALID_ARG;
+  if (rotary->layout != SA2_ROTARY_INTERLEAVED && rotary->layout != SA2_ROTARY_HALVES) return SA2_ERR_INVALID_ARG;
+  const bool halves = rotary->layout == SA2_ROTARY_HALVES;
+  if (dtype != SA2_BF16 && dtype != SA2_FP16 && dtype != SA2_FP32) return SA2_ERR_UNSUPPORTED;
+  if (d < 8 || d > 1024 || d % 8 || rotary->n > d / 2 || (halves && rotary->n % 8)) return SA2_ERR_UNSUPPORTED;
+  if ((int64_t)B * N >= kMaxTokens || H > (1 << 18) || H2 > (1 << 18)) return SA2_ERR_UNSUPPORTED;
+  RotaryArgs a{};
+  const int esz = dtype == SA2_FP32 ? 4 : 2;
+  const sa2_tensor* from[2] = {x, x2};
+  const sa2_tensor* to[2] = {y, y2};
+  const int heads[2] = {H, H2};
+  a.in_place = 1;
+  for (int i = 0; i < 2; ++i) {
+    if (heads[i] == 0) continue;
+    sa2_status st = check_tensor(from[i], B, heads[i], 1, N, d, esz, &a.t[i].x);
+    if (st == SA2_OK) st = check_tensor(to[i], B, heads[i], 1, N, d, esz, &a.t[i].y);
+    if (st != SA2_OK) return st;
+    a.t[i].heads = heads[i];
+    const TokenRef &f = a.t[i].x, &t = a.t[i].y;
+    if (f.p != t.p)
+      a.in_place = 0;
+    else if (f.sb != t.sb || f.sh != t.sh || f.sn != t.sn)
+      return SA2_ERR_INVALID_ARG;
+  }
+  if (!aligned16(rotary->pairs) || misaligned4(pos)) return SA2_ERR_ALIGNMENT;
+  a.heads = H + H2;
+  a.N = N;
+  a.tokens = (int64_t)B * N;
+  a.pairs = rotary->pairs;
+  a.pos = pos;
+  a.pos_axis = pos_axis;
+  a.pos_b = pos_b;
+  a.half = rotary->n;
+  a.axes = rotary->axes;
+  a.gain = rotary->gain;
+  a.inverse = inverse;
+  a.status = status_word();
+  return cuda_status(launch_rotary(a, d, dtype, halves, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,668 @@
+// Attention of packed sequences to their own keys, causal or not, and of new tokens to the keys and values
+// that a paged cache holds of their sequence, forward, on sm_103a (tcgen05 + TMEM + TMA):
+//
+//   s = scale * q k^T over the keys up to the query's position,  O = softmax(s) V,  LSE = log sum exp(s)
+//
+// The products, the softmax and its roundings are those of cross_fwd.cu: a CTA per SM works on a pair of
+// query tiles (2 x 128 rows, row = token * G + head of the group) in half blocks of 64 keys, with two S
+// buffers per tile, so that S of one half block runs beside the softmax of the one before.  What differs:
+// - A tile's keys end at its last token's position: its last half blocks are cut row by row, and the
+//   first tile of a pair passes the blocks that only the second one needs.
+// - Sequences are short and long: warp 0 finds the next piece of work (packed_sched.cuh) while the others
+//   still have theirs, and hands it on through a ring of slots; the work's order needs nothing on the host.
+// - Keys come from pages by one TMA copy per page and panel; their numbers are read 32 at a time, ahead of use.
+// - A tile that is not full is stored row by row: behind it lie the next sequence's rows.
+//
+// Roles (544 threads): warp 0 finds work and issues the TMA copies; 1 and 2 issue S, 3 and 16 P V of tile 0
+// and 1; 4..7 epilogue; 8..11 and 12..15 softmax of tile 0 and 1, one row per thread.
+#include <algorithm>
+
+#include "cross_softmax.cuh"
+#include "packed_sched.cuh"
+
+namespace sa2 {
+namespace {
+
+constexpr int kThreads = 544;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSlots = 4;  // pieces handed out and not yet finished
+// TMEM columns as in cross_fwd.cu: the S buffers of tile t at 128 t and 128 t + 64, O at 256 + 128 t.
+__device__ __forceinline__ uint32_t col_s(int t, uint32_t buf) { return 128u * t + 64u * buf; }
+__device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
+
+template <int D>
+struct Smem {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = 128 * 128 * kPanels;  // 128 rows x 128 B per panel
+  static constexpr int kStages = D == 64 ? 8 : 4;
+  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kOffO = kOffKV + kStages * kTile;  // a tile of O on its way out
+  static constexpr int kOffBar = kOffO + kTile;
+  static constexpr int kOffSlot = kOffBar + 640;
+  static constexpr int kOffRow = kOffBar + 1024;  // [2][128]: 1 / l
+  static constexpr int kBytes = kOffRow + 1024 + 1024;
+  static_assert(kSlots * (int)sizeof(Piece2) <= 384 && kBytes <= (int)kMaxDynSmem, "shared memory");
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                      const __grid_constant__ PackedShape s, const __grid_constant__ PackedPlan plan,
+                      const __grid_constant__ PackedFwdArgs a) {
+  using L = Smem<D>;
+  constexpr int kStages = L::kStages;
+  // How far (log2) a half block's maximum may lead the reference: see cross_fwd.cu.
+  constexpr float kMaxLead = 14.f;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  auto bar_full = [&](int st) { return smem_u32(&bars[st]); };        // ring stage filled
+  auto bar_empty = [&](int st) { return smem_u32(&bars[8 + st]); };   // ... and read by its MMAs
+  auto bar_qfull = [&](int t) { return smem_u32(&bars[16 + t]); };    // Q of tile t in shared memory
+  auto bar_qempty = [&](int t) { return smem_u32(&bars[18 + t]); };   // ... and read by its last S
+  auto bar_s = [&](int t, uint32_t u) { return smem_u32(&bars[20 + 2 * t + u]); };   // S buffer u of tile t in TMEM
+  auto bar_p = [&](int t, uint32_t u) { return smem_u32(&bars[24 + 2 * t + u]); };   // P written over it
+  auto bar_pv = [&](int t, uint32_t u) { return smem_u32(&bars[28 + 2 * t + u]); };  // P V from it completed
+  auto bar_o = [&](int t) { return smem_u32(&bars[32 + t]); };        // O_t of the piece complete
+  auto bar_ofree = [&](int t) { return smem_u32(&bars[34 + t]); };    // ... and read out
+  auto bar_l = [&](int t) { return smem_u32(&bars[36 + t]); };        // 1 / l of the piece written
+  auto bar_drain = [&](int t) { return smem_u32(&bars[38 + t]); };
+  auto bar_pdrain = [&](int t) { return smem_u32(&bars[40 + t]); };
+  const uint32_t bar_st = smem_u32(&bars[42]), bar_stfree = smem_u32(&bars[43]);  // O tile staged / copied out
+  auto bar_slot = [&](uint32_t i) { return smem_u32(&bars[44 + i]); };            // a piece of work handed out
+  auto bar_taken = [&](uint32_t i) { return smem_u32(&bars[44 + kSlots + i]); };  // ... and read by 16 warps
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 448);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 456);
+  Piece2* slots = reinterpret_cast<Piece2*>(smem + L::kOffSlot);
+  float* row_s = reinterpret_cast<float*>(smem + L::kOffRow);
+  const WaitCtl wc{abort_flag, s.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(bar_full(st), 1);
+      mbar_init(bar_empty(st), 2);  // both tiles
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_qfull(t), 1);
+      mbar_init(bar_qempty(t), 1);
+      for (uint32_t u = 0; u < 2; ++u) {
+        mbar_init(bar_s(t, u), 1);
+        mbar_init(bar_p(t, u), 128);
+        mbar_init(bar_pv(t, u), 1);
+      }
+      mbar_init(bar_o(t), 1);
+      mbar_init(bar_ofree(t), 128);
+      mbar_init(bar_l(t), 128);
+      mbar_init(bar_drain(t), 1);
+      mbar_init(bar_pdrain(t), 1);
+    }
+    mbar_init(bar_st, 128);
+    mbar_init(bar_stfree, 1);
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      mbar_init(bar_slot(i), 1);
+      mbar_init(bar_taken(i), 16);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (plan.split) kernel_trigger();
+  const int nb = plan.nb;
+
+  // The n-th piece, for every warp but 0; false where there is none.
+  auto take = [&](uint32_t n, Piece2& x) {
+    const uint32_t i = n % kSlots;
+    if (!__all_sync(kFull, mbar_wait(bar_slot(i), (n / kSlots) & 1, wc))) return false;
+    x = slots[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_taken(i));
+    return x.hk >= 0;
+  };
+  auto active = [&](const Piece2& x, int t) { return t < plan.tp && x.ntok > t * nb; };
+  // Keys of a piece that tile t reads, from the piece's first on (none: 0 or less).
+  auto tile_keys = [&](const Piece2& x, int t) {
+    const int to = s.causal ? min(x.keys, x.pos + min(x.ntok, (t + 1) * nb)) : x.keys;
+    return min(x.nb * kKeyBlock, to - x.k0 * kKeyBlock);
+  };
+  // Blocks [from, nb) of K's or V's stages, free as far as this tile goes.  Every phase of bar_full is waited
+  // for: a warp that skipped one would take the phase before it for its own.
+  auto pass_stages = [&](uint32_t r, int from, int n) {
+    for (int i = from; i < n; ++i) {
+      const uint32_t k = r + 2 * i;
+      if (!__all_sync(kFull, mbar_wait(bar_full(k % kStages), (k / kStages) & 1, wc))) return false;
+      if (lane == 0) mbar_arrive(bar_empty(k % kStages));
+    }
+    return true;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------- work finder and TMA producer
+    if (lane == 0) {
+      tma_prefetch_map(&mq);
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+    }
+    PackedWalk walk(s, plan, a);
+    CutRecord rec{0, 0, 0, 0, 0, 0, 0, 0};
+    const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * nb * s.G);
+    const uint32_t key_bytes = (uint32_t)(L::kPanels * 128);
+    const int boxes = s.page ? kKeyBlock / s.box : 1;  // of a key block
+    uint32_t r = 0, qn[2] = {0, 0}, n = 0;              // ring loads, Q tiles and pieces issued
+    bool ok = true;
+    for (;;) {
+      Piece2 x;
+      const bool more = walk.next(x, rec);
+      if (!more) x.hk = -1;
+      const uint32_t i = n % kSlots;
+      ok = n < (uint32_t)kSlots || __all_sync(kFull, mbar_wait(bar_taken(i), (n / kSlots - 1) & 1, wc));
+      if (!ok) break;
+      if (lane == 0) {
+        slots[i] = x;
+        mbar_arrive(bar_slot(i));
+      }
+      ++n;
+      if (!more) break;
+      // the pages of the next 32 boxes, a lane each
+      const int32_t* row = s.page ? a.seqs.table + walk.b * s.table_stride : nullptr;
+      const int end = min(x.keys, (x.k0 + x.nb) * kKeyBlock);
+      auto page_of = [&](int box) {
+        const int64_t tok = (int64_t)box * s.box;
+        if (tok >= end) return s.pages;
+        const int id = row[tok / s.page];
+        if (id >= 0 && id < s.pages) return id;
+        report_error(a.status, kDevErrBounds);
+        return s.pages;  // reads as zero
+      };
+      int held = 0, box0 = x.k0 * boxes;
+      int ids = 0, next_ids = row ? page_of(box0 + lane) : 0;
+      auto load = [&](const CUtensorMap* map, int kb) {
+        const int st = r % kStages;
+        if (r >= (uint32_t)kStages && !__all_sync(kFull, mbar_wait(bar_empty(st), ((r / kStages) - 1) & 1, wc))) return false;
+        const uint32_t dst = sbase + L::kOffKV + st * L::kTile;
+        const int k = kb * kKeyBlock;
+        if (!row) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar_full(st), L::kTile);
+            for (int pn = 0; pn < L::kPanels; ++pn)
+              tma_load_5d(dst + pn * 16384, map, bar_full(st), pn * 64, 0, walk.lo + k, x.hk, 0);
+          }
+        } else {
+          const int nbox = max(0, min(boxes, (end - k + s.box - 1) / s.box));
+          if (lane == 0) mbar_arrive_expect_tx(bar_full(st), nbox * s.box * key_bytes);
+          for (int j = 0; j < nbox; ++j) {
+            const int id = __shfl_sync(kFull, ids, (kb * boxes + j - box0) & 31);
+            if (lane == 0)
+              for (int pn = 0; pn < L::kPanels; ++pn)
+                tma_load_5d(dst + pn * 16384 + j * s.box * 128, map, bar_full(st), pn * 64, 0,
+                            (k + j * s.box) & (s.page - 1), x.hk, id);
+          }
+        }
+        ++r;
+        return true;
+      };
+      for (int j = 0; ok && j < x.nb; ++j) {
+        if (row && j * boxes == held) {
+          ids = next_ids;
+          held += 32;
+          next_ids = page_of(box0 + held + lane);
+        }
+        ok = load(&mk, x.k0 + j);
+        if (ok && j == 0) {
+          for (int t = 0; ok && t < 2; ++t) {
+            if (!active(x, t) || tile_keys(x, t) <= 0) continue;
+            ok = qn[t] == 0 || __all_sync(kFull, mbar_wait(bar_qempty(t), (qn[t] - 1) & 1, wc));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar_qfull(t), q_bytes);
+              for (int pn = 0; pn < L::kPanels; ++pn)
+                tma_load_5d(sbase + t * L::kTile + pn * 16384, &mq, bar_qfull(t), pn * 64, 0, x.qtok + t * nb, x.hk, 0);
+            }
+            ++qn[t];
+          }
+        }
+        if (ok) ok = load(&mv, x.k0 + j);
+      }
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      if (plan.split) reinterpret_cast<CutRecord*>(a.rec)[blockIdx.x] = rec;
+      // No copy may still be in flight when the CTA exits: each stage's last load, each tile's Q.
+      for (uint32_t v = r > (uint32_t)kStages ? r - kStages : 0; v < r; ++v)
+        mbar_drain(bar_full(v % kStages), (v / kStages) & 1, abort_flag);
+      for (int t = 0; t < 2; ++t)
+        if (qn[t]) mbar_drain(bar_qfull(t), (qn[t] - 1) & 1, abort_flag);
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------------ issuer of S of tile t
+    const int t = warp - 1;
+    const uint64_t qd = smem_desc(sbase + t * L::kTile, 16, 1024);
+    bool ok = true;
+    uint32_t r = 0, c = 0, pc = 0;  // ring loads of earlier pieces; half blocks and pieces done
+    Piece2 x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      const int keys = active(x, t) ? tile_keys(x, t) : 0;
+      const int halves = keys > 0 ? (keys + 63) >> 6 : 0;
+      // into buffer c & 1, whose P V two half blocks ago has completed
+      for (int i = 0; i < halves; ++i, ++c) {
+        const uint32_t rk = r + (i & ~1), u = c & 1;
+        const int ks = rk % kStages;
+        const bool last = i + 1 == halves;
+        ok = __all_sync(kFull, ((i & 1) || mbar_wait(bar_full(ks), (rk / kStages) & 1, wc)) &&
+                                   (i > 0 || mbar_wait(bar_qfull(t), pc & 1, wc)) &&
+                                   (c < 2 || mbar_wait(bar_pv(t, u), ((c >> 1) - 1) & 1, wc)));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t idS = idesc_f32acc(128, min(64, (keys - 64 * i + 15) & ~15), false, false, !F16);
+        const uint64_t kd = smem_desc(sbase + L::kOffKV + ks * L::kTile + (i & 1) * 8192, 16, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(tmem + col_s(t, u), qd + kmajor_kstep(kk, 128), kd + kmajor_kstep(kk, 128), idS, kk > 0 ? 1u : 0u);
+          umma_commit(bar_s(t, u));
+          if ((i & 1) || last) umma_commit(bar_empty(ks));
+          if (last) umma_commit(bar_qempty(t));
+        }
+        __syncwarp();
+      }
+      if (halves) ++pc;
+      if (ok) ok = pass_stages(r, (halves + 1) >> 1, x.nb);
+      r += 2 * x.nb;
+    }
+    // no MMA may still run when TMEM is released, on the abort path too
+    if (elect_one()) umma_commit(bar_drain(t));
+    __syncwarp();
+    mbar_drain(bar_drain(t), 0, abort_flag);
+  } else if (warp == 3 || warp == 16) {
+    // ------------------------------------------------------------------ issuer of P V of tile t
+    constexpr uint32_t idO = idesc_f32acc(128, D, false, true, !F16);
+    const int t = warp >> 4;
+    bool ok = true;
+    uint32_t r = 0, c = 0, pc = 0;
+    Piece2 x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      const int keys = active(x, t) ? tile_keys(x, t) : 0;
+      const int halves = keys > 0 ? (keys + 63) >> 6 : 0;
+      for (int i = 0; i < halves; ++i, ++c) {
+        const uint32_t rv = r + (i & ~1) + 1, u = c & 1;
+        const int vs = rv % kStages, steps = (min(64, keys - 64 * i) + 15) >> 4;
+        const bool last = i + 1 == halves;
+        ok = __all_sync(kFull, (i & 1) || mbar_wait(bar_full(vs), (rv / kStages) & 1, wc));
+        if (!ok) break;
+        // rows of V behind the sequence's last key, which the product reads up to a multiple of 16, as zeros:
+        // their P is 0, but 0 * NaN is NaN (both issuers write the same; a row is 128 bytes in each panel)
+        const int valid = x.keys - x.k0 * kKeyBlock - 64 * i, rows = 16 * steps - valid;
+        if (rows > 0) {
+          uint8_t* vt = smem + L::kOffKV + vs * L::kTile + (i & 1) * 8192;
+          const int nz = rows * 8 * L::kPanels;
+          for (int q = lane; q < nz; q += 32) {
+            const int row = valid + (q >> 3) % rows, pn = (q >> 3) / rows;
+            *reinterpret_cast<uint4*>(vt + pn * 16384 + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        ok = __all_sync(kFull, (i > 0 || pc == 0 || mbar_wait(bar_ofree(t), (pc - 1) & 1, wc)) &&
+                                   mbar_wait(bar_p(t, u), (c >> 1) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = smem_desc(sbase + L::kOffKV + vs * L::kTile + (i & 1) * 8192, 16384, 1024);
+        if (elect_one()) {
+          issue_pv(tmem + col_o(t), tmem + col_s(t, u), vd, idO, steps, i == 0);
+          umma_commit(bar_pv(t, u));
+          if ((i & 1) || last) umma_commit(bar_empty(vs));
+          if (last) umma_commit(bar_o(t));
+        }
+        __syncwarp();
+      }
+      if (halves) ++pc;
+      if (ok) ok = pass_stages(r + 1, (halves + 1) >> 1, x.nb);
+      r += 2 * x.nb;
+    }
+    if (elect_one()) umma_commit(bar_pdrain(t));
+    __syncwarp();
+    mbar_drain(bar_pdrain(t), 0, abort_flag);
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ softmax rows
+    if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
+    const int t = (warp - 8) >> 2;
+    const int r = 32 * (warp & 3) + lane;
+    const int tok_r = r / s.G, g = r - tok_r * s.G;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t to = trow + col_o(t);
+    const float mul = a.scale_log2;
+    bool ok = true;
+    uint32_t c = 0, pc = 0;
+    Piece2 x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      if (!active(x, t)) continue;
+      const int tok = t * nb + tok_r;  // of the segment
+      const bool row_valid = tok_r < nb && tok < x.ntok;
+      const int keys = tile_keys(x, t);
+      float* lse = x.slot < 0 ? a.lse + (int64_t)(x.hk * s.G + g) * s.T + x.qtok + tok
+                              : a.part_l + (int64_t)x.slot * 256 + t * 128 + r;
+      if (keys <= 0) {
+        if (row_valid) *lse = -INFINITY;
+        continue;
+      }
+      // keys that this row reads, from the piece's first on (a row without a query: as the tile does)
+      const int mine = s.causal && row_valid ? min(keys, x.pos + tok + 1 - x.k0 * kKeyBlock) : keys;
+      float m_used = 0.f, m_run = 0.f;  // reference of the exponentials, largest so far
+      float l = 0.f;                    // sum of exp2(s - m_used)
+      // O and l to another reference.  O holds the half blocks before this one once their P V has
+      // completed: the last one's, from the other buffer, is waited for.
+      auto rescale = [&](float m_new) {
+        if (!__all_sync(kFull, mbar_wait(bar_pv(t, (c & 1) ^ 1), ((c - 1) >> 1) & 1, wc))) return false;
+        tc_fence_after();
+        const float alpha = m_new == m_used ? 1.f : ex2(m_used - m_new);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          uint32_t o[16];
+          tmem_ld16(to + c0, o);
+          tmem_ld_wait16(o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(to + c0, o);
+        }
+        tmem_st_wait();
+        l *= alpha;
+        m_used = m_new;
+        return true;
+      };
+      for (int i = 0; 64 * i < keys; ++i, ++c) {
+        const uint32_t u = c & 1, ts = trow + col_s(t, u);
+        const int valid = mine - 64 * i;
+        if (!__all_sync(kFull, mbar_wait(bar_s(t, u), (c >> 1) & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // the references: see cross_fwd.cu
+        if (i == 0) {
+          float y[32];
+          load_scores(ts, y, valid);
+          const float m0 = max32(y);
+          load_scores(ts + 32, y, valid - 32);
+          m_used = m_run = fmaxf(fmaxf(m0, max32(y)) * mul, kLeastRef);
+        } else if (__any_sync(kFull, m_run > m_used + kRescaleThreshold)) {
+          ok = rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
+        }
+        uint32_t pk[32];
+        float sum;
+        for (bool again = false;;) {
+          float2 part[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          float mx;
+          {
+            float y[32];
+            load_scores(ts, y, valid);
+            mx = max32(y);
+            exp32<F16>(y, mul, -m_used, pk, part);
+            load_scores(ts + 32, y, valid - 32);
+            mx = fmaxf(mx, max32(y));
+            exp32<F16>(y, mul, -m_used, pk + 16, part);
+          }
+          const float2 both = add2(part[0], part[1]);
+          sum = both.x + both.y;
+          mx *= mul;
+          m_run = fmaxf(m_run, mx);
+          if (again || !ok || !__any_sync(kFull, mx > m_used + kMaxLead)) break;
+          // (a row's reference follows from its own scores only: neighbours, and rows of the tile that are no
+          // query's, must not change its roundings)
+          ok = rescale(mx > m_used + kMaxLead ? mx : m_used);
+          again = true;
+        }
+        if (!ok) break;
+        tmem_st32(ts, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_p(t, u));
+        l += sum;
+      }
+      if (!ok) break;
+      if (row_valid) *lse = (m_used + __log2f(l)) * (x.slot < 0 ? 0.69314718055994531f : 1.f);
+      // the epilogue warps read the previous piece's 1 / l before they released its O
+      if (pc > 0 && !__all_sync(kFull, mbar_wait(bar_ofree(t), (pc - 1) & 1, wc))) {
+        ok = false;
+        break;
+      }
+      row_s[t * 128 + r] = inverse_sum(l);
+      mbar_arrive(bar_l(t));
+      ++pc;
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue: O / l
+    // A full tile goes out through shared memory with one TMA store, any other row by row.
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int tok_r = r / s.G, g = r - tok_r * s.G;
+    bool ok = true;
+    uint32_t pc[2] = {0, 0}, staged = 0;
+    Piece2 x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || !active(x, t)) continue;
+        const int tok = t * nb + tok_r;
+        const bool row_valid = tok_r < nb && tok < x.ntok;
+        const bool full = x.ntok >= (t + 1) * nb;
+        uint16_t* op = static_cast<uint16_t*>(a.o.p) + (int64_t)(x.hk * s.G + g) * a.o.sh + (int64_t)(x.qtok + tok) * a.o.sn;
+        if (tile_keys(x, t) <= 0) {
+          // (of a cut segment the join leaves out parts without keys)
+          if (row_valid && x.slot < 0)
+            for (int i = 0; i < D / 8; ++i) reinterpret_cast<uint4*>(op)[i] = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const bool stage = x.slot < 0 && full;
+        ok = __all_sync(kFull, mbar_wait(bar_l(t), pc[t] & 1, wc) && mbar_wait(bar_o(t), pc[t] & 1, wc) &&
+                                   (!stage || staged == 0 || mbar_wait(bar_stfree, (staged - 1) & 1, wc)));
+        if (!ok) break;
+        ++pc[t];
+        tc_fence_after();
+        const float inv_l = row_s[t * 128 + r];
+        float* po = a.part_o + ((int64_t)x.slot * 256 + t * 128 + r) * D;
+        uint8_t* st_row = smem + L::kOffO + r * 128;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t u[32];
+          tmem_ld32(trow + col_o(t) + c0, u);
+          tmem_ld_wait(u);
+          if (c0 + 32 >= D) {
+            tc_fence_before();
+            mbar_arrive(bar_ofree(t));
+          }
+          if (x.slot >= 0) {
+            if (row_valid) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(po + c0)[i] =
+                    make_float4(__uint_as_float(u[4 * i]) * inv_l, __uint_as_float(u[4 * i + 1]) * inv_l,
+                                __uint_as_float(u[4 * i + 2]) * inv_l, __uint_as_float(u[4 * i + 3]) * inv_l);
+            }
+            continue;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float v0 = __uint_as_float(u[8 * i + 2 * q]) * inv_l, v1 = __uint_as_float(u[8 * i + 2 * q + 1]) * inv_l;
+              w[q] = F16 ? pack_f16x2(v0, v1) : pack_bf16x2(v0, v1);
+            }
+            const uint4 w4 = make_uint4(w[0], w[1], w[2], w[3]);
+            const int k = (c0 & 32) / 8 + i;
+            if (stage)  // 16-byte chunk k of the row's 128 bytes in panel c0 / 64, swizzled
+              *reinterpret_cast<uint4*>(st_row + (c0 >> 6) * 16384 + ((k ^ (r & 7)) << 4)) = w4;
+            else if (row_valid)
+              reinterpret_cast<uint4*>(op + c0)[i] = w4;
+          }
+        }
+        if (stage) {
+          fence_proxy_async();
+          mbar_arrive(bar_st);
+          if (warp == 4) {
+            ok = __all_sync(kFull, mbar_wait(bar_st, staged & 1, wc));
+            if (!ok) break;
+            if (lane == 0) {
+              for (int pn = 0; pn < L::kPanels; ++pn)
+                tma_store_5d(&mo, sbase + L::kOffO + pn * 16384, pn * 64, 0, x.qtok + t * nb, x.hk, 0);
+              bulk_commit();
+              bulk_wait_read();
+              mbar_arrive(bar_stfree);
+            }
+            __syncwarp();
+          }
+          ++staged;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) report_error(a.status, kDevErrTimeout);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of segments that were cut: O = sum_i 2^(l_i - m) O_i / sum_i 2^(l_i - m) over a segment's
+// parts in key order, l_i their log2 sums and m the largest; LSE = ln 2 (m + log2 sum).  Parts in which a
+// row has no keys (l_i = -inf) are left out.  One warp per row; grid (CTAs of the first kernel, parts of a
+// segment's rows); most CTAs find nothing to do.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant__ PackedShape s,
+                                                         const __grid_constant__ PackedPlan plan,
+                                                         const __grid_constant__ PackedFwdArgs a) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  kernel_wait();
+  const CutRecord x = reinterpret_cast<const CutRecord*>(a.rec)[blockIdx.x];
+  if (x.parts == 0) return;
+  for (int i = warp; i < plan.join_rows; i += 8) {
+    const int rr = blockIdx.y * plan.join_rows + i, t = rr >> 7, r = rr & 127;
+    const int tok_r = r / s.G, g = r - tok_r * s.G, tok = t * plan.nb + tok_r, h = x.hk * s.G + g;
+    if (t >= plan.tp || tok_r >= plan.nb || tok >= x.ntok) continue;
+    auto slot_row = [&](int k) { return (int64_t)(k == 0 ? x.slot : 2 * ((int)blockIdx.x + k)) * 256 + rr; };
+    // lane i has part i's sum; 32 parts at a time, eight of their rows in flight
+    float m = kLeastRef, acc[kPer] = {}, l = 0.f;
+    for (int base = 0; base < x.parts; base += 32) {
+      const int n32 = min(32, x.parts - base);
+      const float mine = lane < n32 ? a.part_l[slot_row(base + lane)] : -INFINITY;
+      float mx = mine;
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      if (__any_sync(kFull, mine != mine)) mx = NAN;
+      const float m_new = m != m ? m : (mx > m || mx != mx ? mx : m);
+      const float keep = base == 0 ? 0.f : ex2(m - m_new);
+      m = m_new;
+      l *= keep;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) acc[q] *= keep;
+      const float wl = lane < n32 && mine != -INFINITY ? ex2(mine - m) : 0.f;
+      const unsigned some = __ballot_sync(kFull, lane < n32 && mine != -INFINITY);
+      for (int k = 0; k < n32; k += 8) {
+        float v[8][kPer];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (!((some >> ((k + u) & 31)) & 1)) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) v[u][q] = 0.f;
+            continue;
+          }
+          const float* src = a.part_o + slot_row(base + k + u) * D;
+          if constexpr (kPer == 4)
+            *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src + lane * 4);
+          else
+            *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src + lane * 2);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float w = __shfl_sync(kFull, wl, (k + u) & 31);
+          l += w;
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) acc[q] = fmaf(w, v[u][q], acc[q]);
+        }
+      }
+    }
+    const float inv = inverse_sum(l);
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int q = 0; q < kPer / 2; ++q)
+      w[q] = F16 ? pack_f16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv) : pack_bf16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv);
+    uint16_t* op = static_cast<uint16_t*>(a.o.p) + h * a.o.sh + (int64_t)(x.qtok + tok) * a.o.sn + lane * kPer;
+    if constexpr (kPer == 4)
+      *reinterpret_cast<uint2*>(op) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(op) = w[0];
+    if (lane == 0) a.lse[(int64_t)h * s.T + x.qtok + tok] = (m + __log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+template <int D, bool F16>
+cudaError_t launch_t(const PackedShape& s, const PackedPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, const CUtensorMap& mo, const PackedFwdArgs& a, cudaStream_t st) {
+  auto kern = packed_fwd_kernel<D, F16>;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem(kern, Smem<D>::kBytes, allowed);
+  if (e == cudaSuccess && p.tickets) e = cudaMemsetAsync(a.counter, 0, sizeof(unsigned), st);
+  if (e != cudaSuccess) return e;
+  prof_start(st, kAttnFwd);
+  kern<<<(unsigned)p.grid, kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv, mo, s, p, a);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && p.split)
+    e = launch_early(packed_join_kernel<D, F16>, dim3((unsigned)p.grid, (unsigned)(p.tp * 128 / p.join_rows)), 256, 0,
+                     st, s, p, a);
+  prof_stop(st, kAttnFwd);
+  return e;
+}
+
+}  // namespace
+
+// Split where the segments that there can be do not fill the SMs four times over (whole ones then even out by
+// the order in which they are taken) and their keys are eight blocks or more (the join would cost what the
+// split gains); of packed sequences, whose lengths the host does not know, by their mean.
+PackedPlan packed_fwd_plan(const PackedShape& s, int sms) {
+  PackedPlan p{};
+  p.nb = 128 / s.G;
+  const int64_t most_keys = s.page ? (int64_t)s.width * s.page : s.T / s.B;
+  const int64_t blocks = (most_keys + kKeyBlock - 1) / kKeyBlock;
+  const int64_t paired = s.Hkv * segment_bound(s, 2 * p.nb);
+  p.split = blocks >= 8 && paired < 4 * (int64_t)sms;
+  // one tile per CTA while each finds an SM of its own, and where sequences have no second one
+  p.tp = s.max_new <= p.nb || (!p.split && s.Hkv * segment_bound(s, p.nb) <= sms) ? 1 : 2;
+  p.w = p.tp * p.nb;
+  const int64_t items = s.Hkv * segment_bound(s, p.w);
+  const int64_t all_blocks = (s.page ? ((int64_t)s.width * s.page + kKeyBlock - 1) / kKeyBlock : (s.T + kKeyBlock - 1) / kKeyBlock);
+  p.grid = (int)std::min<int64_t>(sms, p.split ? items * all_blocks : items);
+  p.tickets = !p.split && items > p.grid;
+  // keys and values of the heads of a section take a third of L2 at most
+  const int64_t tokens = s.page ? std::min<int64_t>((int64_t)s.B * s.width, s.pages) * s.page : s.T;
+  const int64_t head_bytes = tokens * s.d * 4;
+  p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(s.Hkv, (40ll << 20) / head_bytes));
+  p.join_rows = 16;
+  return p;
+}
+
+// The counter (and the records of the cut segments) first, then the parts.
+size_t packed_fwd_bytes(const PackedShape& s, const PackedPlan& p) {
+  if (!p.split) return p.tickets ? 256 : 0;
+  return (size_t)p.grid * sizeof(CutRecord) + (size_t)2 * p.grid * 256 * (s.d + 1) * sizeof(float);
+}
+
+cudaError_t launch_packed_fwd(const PackedShape& s, const PackedPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                              const CUtensorMap& mv, const CUtensorMap& mo, const PackedFwdArgs& a, cudaStream_t st) {
+  const bool f16 = s.dtype == SA2_FP16;
+  if (s.d == 128)
+    return f16 ? launch_t<128, true>(s, p, mq, mk, mv, mo, a, st) : launch_t<128, false>(s, p, mq, mk, mv, mo, a, st);
+  return f16 ? launch_t<64, true>(s, p, mq, mk, mv, mo, a, st) : launch_t<64, false>(s, p, mq, mk, mv, mo, a, st);
+}
+
+}  // namespace sa2

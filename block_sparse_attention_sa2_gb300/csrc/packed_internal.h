@@ -1,0 +1,77 @@
+// Declarations shared by the sources of attention within packed sequences and over a paged cache
+// (packed_*.cu, paged.cu).
+#pragma once
+
+#include "cross_internal.h"
+
+namespace sa2 {
+
+// Shape of a call.  B sequences lie one behind the other along the token axis, T tokens in all; query
+// heads h = hk * G + g share key head hk.  page = 0: keys and values lie packed like the queries.
+// Else they are in pages of `page` tokens, and row b of the table names those of sequence b in order.
+struct PackedShape {
+  int B, H, Hkv, G, T, d;
+  int dtype;   // SA2_BF16 or SA2_FP16
+  int causal;
+  int page, box;     // tokens of a page and of a box of its tensor map (min(page, 128))
+  int pages, width;  // pages in all; columns of the table
+  int max_new;       // no sequence has more new tokens (T where the caller did not say)
+  int64_t table_stride;
+  unsigned long long wait_ns, stall_ns;
+};
+
+// Device arrays: where each sequence begins ([B + 1]), and of a paged cache the tokens that it holds
+// of each sequence ([B], the new ones among them; null: packed keys) and the table.
+struct PackedSeqs {
+  const int32_t* seq;
+  const int32_t* kv_len;
+  const int32_t* table;
+};
+
+// How a forward call's work is cut.  A segment is w = tp * nb tokens of a sequence for one key head (a
+// pair of query tiles, row = token * G + g).
+//   direct: a work item is a segment.  CTAs take items from a counter, in sections of `heads` key heads
+//           whose keys and values fit L2 together, and within a section those with the most keys first:
+//           the longest ones then begin early and the last ones are short.
+//   split:  the 128-key blocks of all segments in order are cut into `grid` equal runs.  A segment
+//           that falls into one run is written at once; of one that is cut each part leaves its O and
+//           log2 sum in a slot, 2 * CTA for one that the run begins with and 2 * CTA + 1 for one that
+//           it ends with, and a second kernel joins them in key order.
+struct PackedPlan {
+  int nb, tp, w;
+  int grid;
+  int split;
+  int tickets;  // direct: more items than CTAs may be
+  int heads;
+  int join_rows;
+};
+
+struct PackedFwdArgs {
+  PackedSeqs seqs;
+  TokenRef o;
+  float* lse;          // [H, T]
+  unsigned* counter;   // direct with tickets
+  int* rec;            // split: [grid][8], see CutRecord
+  float* part_o;       // split: [2 * grid][256][d]
+  float* part_l;       // split: [2 * grid][256], log2 units
+  float scale_log2;
+  unsigned* status;
+};
+
+// The segment that a CTA's run ends in, where the runs behind it have the rest: read by the join.
+struct CutRecord {
+  int parts, slot, qtok, ntok, hk, pad0, pad1, pad2;
+};
+
+// Upper bound of the segments of w tokens of one key head: sum ceil(n_b / w) <= (T + B (w - 1)) / w.
+inline int64_t segment_bound(const PackedShape& s, int w) {
+  const int64_t a = ((int64_t)s.T + (int64_t)s.B * (w - 1)) / w;
+  return a < s.T ? a : s.T;
+}
+
+PackedPlan packed_fwd_plan(const PackedShape& s, int sms);
+size_t packed_fwd_bytes(const PackedShape& s, const PackedPlan& p);
+cudaError_t launch_packed_fwd(const PackedShape& s, const PackedPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                              const CUtensorMap& mv, const CUtensorMap& mo, const PackedFwdArgs& a, cudaStream_t st);
+
+}  // namespace sa2

@@ -1,0 +1,161 @@
+// Rotary positions: channel pairs (a, b) of a token's heads turned by the angle of the token's position,
+//   a' = gain (a cos t - b sin t),  b' = gain (b cos t + a sin t),  t = position * frequency of the pair,
+// or, transposed, t = - position * frequency, which is the gradient's way back.
+//
+// A pair's frequency is held as turns per position in 64 bits behind the point: position * turns, whose
+// whole turns fall off the top, is the angle's place in its turn to 2^-31 for any 32-bit position, where
+// position * frequency in fp32 would be off by 0.06 radians at a position of a million.  Sine and cosine
+// are then taken of an angle in [-pi, pi] in fp32.
+#include "rotary.h"
+
+namespace sa2 {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+struct Vec;  // kPer values of a 16-byte word
+template <>
+struct Vec<float> {
+  static constexpr int kPer = 4;
+  static __device__ __forceinline__ void load(const uint4& u, float* v) {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Vec<__half> {
+  static constexpr int kPer = 8;
+  static __device__ __forceinline__ void load(const uint4& u, float* v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kPer = 8;
+  static __device__ __forceinline__ void load(const uint4& u, float* v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
+
+// cos and sin, times the gain, of pair i of a token.
+__device__ __forceinline__ float2 turn(const RotaryArgs& a, int64_t token, int i) {
+  const longlong2 f = reinterpret_cast<const longlong2*>(a.pairs)[i];  // turns, axis
+  const bool known = f.y >= 0 && f.y < a.axes;
+  if (!known) report_error(a.status, kDevErrBounds);
+  const int pos = a.pos[(known ? f.y : 0) * a.pos_axis + token];
+  // the upper 32 bits of the place in the turn, as a signed part of a half turn in [-1, 1)
+  const int place = (int)(uint32_t)(((uint64_t)(int64_t)pos * (uint64_t)f.x) >> 32);
+  float sn, cs;
+  sincospif((float)place * 0x1p-31f, &sn, &cs);
+  return make_float2(cs * a.gain, (a.inverse ? -sn : sn) * a.gain);
+}
+
+// A thread has one word of kPer channels (both halves layout: that word and its partner half the turned
+// channels further on) of one token, and goes through `per` of its heads; the angles, which belong to the
+// token, are made once.  Bound by the bytes, one read and one write of each.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
+  using V = Vec<T>;
+  constexpr int kPer = V::kPer, kPairs = HALF ? kPer : kPer / 2;
+  const int words = a.words;  // of a token and head that are worked on
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int word = (int)(i % words);
+  const int64_t tok = i / words;  // b * N + n
+  if (tok >= a.tokens) return;
+  const int b = (int)(tok / a.N), n = (int)(tok - (int64_t)b * a.N);
+  const bool turned = word < a.turned;
+  const int ch = (HALF && !turned ? word + a.turned : word) * kPer;  // half layout: `turned` words stand for two each
+  float2 w[kPairs];
+  if (turned) {
+    const int p0 = HALF ? ch : ch / 2;
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      w[p] = p0 + p < a.half ? turn(a, b * a.pos_b + n, p0 + p) : make_float2(0.f, 0.f);
+    }
+  }
+  const int h0 = blockIdx.y * a.per, h1 = min(h0 + a.per, a.heads);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const RotaryTensor& t = h < a.t[0].heads ? a.t[0] : a.t[1];
+    const int hh = h < a.t[0].heads ? h : h - a.t[0].heads;
+    const T* src = static_cast<const T*>(t.x.p) + b * t.x.sb + hh * t.x.sh + n * t.x.sn + ch;
+    T* dst = static_cast<T*>(t.y.p) + b * t.y.sb + hh * t.y.sh + n * t.y.sn + ch;
+    const uint4 u = *reinterpret_cast<const uint4*>(src);
+    if (!turned) {
+      *reinterpret_cast<uint4*>(dst) = u;
+      continue;
+    }
+    float x[kPer];
+    V::load(u, x);
+    if constexpr (HALF) {
+      float y[kPer], z[kPer];
+      V::load(*reinterpret_cast<const uint4*>(src + a.half), y);
+#pragma unroll
+      for (int p = 0; p < kPer; ++p) {
+        z[p] = fmaf(x[p], w[p].x, -y[p] * w[p].y);
+        y[p] = fmaf(y[p], w[p].x, x[p] * w[p].y);
+      }
+      *reinterpret_cast<uint4*>(dst) = V::pack(z);
+      *reinterpret_cast<uint4*>(dst + a.half) = V::pack(y);
+    } else {
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        if (ch / 2 + p >= a.half) break;  // (a word may hold channels behind the turned ones)
+        const float c = x[2 * p], s = x[2 * p + 1];
+        x[2 * p] = fmaf(c, w[p].x, -s * w[p].y);
+        x[2 * p + 1] = fmaf(s, w[p].x, c * w[p].y);
+      }
+      *reinterpret_cast<uint4*>(dst) = V::pack(x);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryArgs& args, int d, int dtype, bool half_layout, int sms, cudaStream_t st) {
+  RotaryArgs a = args;
+  const int per_word = dtype == SA2_FP32 ? 4 : 8;
+  const int all = d / per_word;
+  a.turned = half_layout ? a.half / per_word : (2 * a.half + per_word - 1) / per_word;
+  const int standing = a.in_place ? 0 : all - (half_layout ? 2 : 1) * a.turned;
+  a.words = a.turned + standing;
+  if (a.words == 0) return cudaSuccess;
+  const int64_t blocks = (a.tokens * a.words + kThreads - 1) / kThreads;
+  // heads per thread: as many as leave each SM eight CTAs, eight at most
+  a.per = 1;
+  while (a.per < 8 && a.per < a.heads && blocks * ((a.heads + 2 * a.per - 1) / (2 * a.per)) >= 8 * (int64_t)sms) a.per *= 2;
+  const dim3 grid((unsigned)blocks, (unsigned)((a.heads + a.per - 1) / a.per));
+  prof_start(st, kToF16);
+  switch (dtype * 2 + half_layout) {
+    case SA2_BF16 * 2: rotary_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, st>>>(a); break;
+    case SA2_BF16 * 2 + 1: rotary_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, st>>>(a); break;
+    case SA2_FP16 * 2: rotary_kernel<__half, false><<<grid, kThreads, 0, st>>>(a); break;
+    case SA2_FP16 * 2 + 1: rotary_kernel<__half, true><<<grid, kThreads, 0, st>>>(a); break;
+    case SA2_FP32 * 2: rotary_kernel<float, false><<<grid, kThreads, 0, st>>>(a); break;
+    default: rotary_kernel<float, true><<<grid, kThreads, 0, st>>>(a); break;
+  }
+  prof_stop(st, kToF16);
+  return cudaGetLastError();
+}
+
+}  // namespace sa2

@@ -103,7 +103,6 @@ namespace {
 
 size_t token_elems(const ShapeArgs& s) { return (size_t)s.B * s.H * s.N * s.d; }
 
-sa2_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SA2_OK : SA2_ERR_CUDA; }
 
 // Mask workspace: the builder's scratch (pooled pairs, the chunk buffers).
 struct MaskWs {

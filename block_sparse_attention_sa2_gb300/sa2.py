@@ -1,5 +1,5 @@
 """Thin Python binding of libsa2 (include/sa2.h): argument marshalling only, through ctypes and, for the
-cross- and cache-attention calls, the extension module ``_cross``.
+cross-, cache-, packed- and paged-attention calls and rotary positions, the extension module ``_cross``.
 
 Every step of the hot path runs in the library's CUDA kernels; this module allocates the
 output tensors and workspaces with PyTorch, passes raw device pointers and the current CUDA
@@ -84,6 +84,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sa2_vd_loss_workspace_size.argtypes = [S]
     lib.sa2_vd_loss.restype = ctypes.c_int
     lib.sa2_vd_loss.argtypes = [S, P, P, P, P, P, P, P, Z, P]
+    lib.sa2_rotary_turns.restype = ctypes.c_int64
+    lib.sa2_rotary_turns.argtypes = [ctypes.c_double]
     lib.sa2_get_device_status.restype = ctypes.c_int
     lib.sa2_get_device_status.argtypes = [P]
     lib.sa2_debug_set_wait_limit.restype = None
@@ -373,6 +375,138 @@ def cache8_attn(q: torch.Tensor, cache: KvCache8, kv_len: torch.Tensor, scale: O
     returns (O, LSE) as cross_attn_fwd does."""
     return (_binding or load_binding()).cache8_attn(q, cache._held, cache._device, kv_len, scale, o, lse, ws,
                                                     _handle(stream))
+
+
+# ------------------------------------------- packed sequences, the paged cache and rotary positions
+
+
+def packed_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor, causal: bool = True,
+                    scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """sa2_packed_attn_fwd: attention of each sequence to itself, sequences one behind the other; (O, LSE).
+
+    q [H, T, d], k, v [Hkv, T, d] (H a multiple of Hkv; bfloat16 or float16; strides of their own, so
+    projections' [T, H, d] are passed as ``x.transpose(0, 1)``).  ``seq`` ([B + 1] int32 on the device): sequence
+    b has the tokens seq[b] .. seq[b + 1] - 1.  ``causal``: a token attends to those up to itself.  LSE is
+    float32 [H, T].  Tokens outside the sequences are left as they were."""
+    return (_binding or load_binding()).packed_attn_fwd(q, k, v, seq, causal, scale, o, lse, ws, _handle(stream))
+
+
+class PagedCache:
+    """Keys and values in pages: k, v [pages, Hkv, page, d] (bfloat16 or float16, with the same strides), a
+    power of two of tokens from 16 on in each page.  The caller keeps the lengths and hands out the pages: row b
+    of a ``table`` ([B, pages of a sequence] int32) names those of sequence b.  The tensors are the cache's for
+    good: calls refuse one whose memory has been exchanged (``x.data = ...``)."""
+
+    __slots__ = ("_k", "_v", "_shape", "_device", "_held")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        self._shape, self._device, struct = (_binding or load_binding()).paged_pack(k, v)
+        self._k, self._v = k, v
+        self._held = (struct, k, v)
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    shape = property(lambda self: self._shape, doc="(pages, Hkv, tokens of a page, d)")
+    device = property(lambda self: self._k.device)
+
+    def __reduce__(self):  # a copy's pointers are those of its own tensors
+        return type(self), (self._k, self._v)
+
+    @classmethod
+    def empty(cls, pages: int, Hkv: int, page: int, d: int, device, dtype=torch.bfloat16) -> "PagedCache":
+        return cls(*(torch.empty((pages, Hkv, page, d), dtype=dtype, device=device) for _ in range(2)))
+
+
+def paged_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, seq: torch.Tensor, kv_len: torch.Tensor,
+                 table: torch.Tensor, stream=None) -> None:
+    """sa2_paged_append: k, v [Hkv, T, d] of new tokens, packed by ``seq``, into the pages of their sequences.
+    ``kv_len`` ([B] int32): the tokens of each sequence with the new ones, which are its last."""
+    (_binding or load_binding()).paged_append(cache._held, cache._device, k, v, seq, kv_len, table, _handle(stream))
+
+
+def paged_attn(q: torch.Tensor, cache: PagedCache, seq: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor,
+               causal: bool = True, max_new: Optional[int] = None, scale: Optional[float] = None,
+               o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               ws: Optional[torch.Tensor] = None, stream=None):
+    """sa2_paged_attn: attention of new tokens q [H, T, d], packed by ``seq`` and appended already, to all that the
+    cache holds of their sequences up to each of them; returns (O, LSE) as packed_attn_fwd does.  ``max_new``: no
+    sequence has more new tokens (1 where each makes a single one): the kernels for few rows need to know."""
+    return (_binding or load_binding()).paged_attn(q, cache._held, cache._device, seq, kv_len, table, causal, max_new,
+                                                   scale, o, lse, ws, _handle(stream))
+
+
+def rotary_frequencies(n: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                       trained: int = 4096, fast: float = 32.0, slow: float = 1.0) -> list:
+    """Angular frequencies of n channels' n / 2 pairs, base ** (-2 i / n), for contexts ``factor`` times the
+    trained ones:
+
+    ``"linear"``  every frequency divided by ``factor``;
+    ``"base"``    the base times factor ** (n / (n - 2)): the slowest pair is slowed by ``factor``, the fastest not;
+    ``"ramp"``    pairs that turn ``fast`` times or more over ``trained`` positions as they are, those that turn
+                  ``slow`` times or less divided by ``factor``, those between in proportion."""
+    if n < 2 or n % 2:
+        raise ValueError(f"an even count of channels, got {n}")
+    if scaling not in (None, "linear", "base", "ramp"):
+        raise ValueError(f"unknown scaling {scaling!r}: None, 'linear', 'base' or 'ramp'")
+    if scaling == "ramp" and not fast > slow:
+        raise ValueError(f"fast ({fast}) must be above slow ({slow})")
+    if scaling == "base" and n > 2:
+        base = base * factor ** (n / (n - 2))
+    f = [base ** (-2.0 * i / n) for i in range(n // 2)]
+    if scaling == "linear":
+        return [w / factor for w in f]
+    if scaling == "ramp":
+        keep = [min(max((trained * w / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0) for w in f]
+        return [w * x + w / factor * (1 - x) for w, x in zip(f, keep)]
+    return f
+
+
+class Rotary:
+    """Rotary positions of heads of d channels.  ``frequencies``: radians per position of each channel pair
+    (``rotary_frequencies`` makes them); the channels behind the pairs' are left as they are.  ``axes``: how many
+    of the pairs, in order, each axis of the positions has (one axis where not given; for video e.g. frame, row
+    and column).  ``layout``: pairs are ``"interleaved"`` channels (2 i, 2 i + 1) or ``"half"`` (i, i + n / 2).
+    ``gain``: factor of the turned channels."""
+
+    __slots__ = ("d", "frequencies", "axes", "layout", "gain", "_pairs")
+
+    def __init__(self, d: int, frequencies, axes=None, layout: str = "interleaved", gain: float = 1.0, device="cuda"):
+        f = [float(x) for x in frequencies]
+        axes = [len(f)] if axes is None else [int(n) for n in axes]
+        if layout not in ("interleaved", "half"):
+            raise ValueError(f"unknown layout {layout!r}: 'interleaved' or 'half'")
+        if d < 8 or d > 1024 or d % 8:
+            raise ValueError(f"d must be a multiple of 8 up to 1024, got {d}")
+        if not f or 2 * len(f) > d or not all(math.isfinite(x) for x in f):
+            raise ValueError(f"{len(f)} finite frequencies for d = {d}: 1 to d / 2 of them")
+        if layout == "half" and len(f) % 8:
+            raise ValueError(f"the half layout needs a multiple of 8 pairs, got {len(f)}")
+        if min(axes, default=0) < 1 or sum(axes) != len(f):
+            raise ValueError(f"axes {axes} must be counts of pairs that make {len(f)} together")
+        if not math.isfinite(gain):
+            raise ValueError(f"gain must be finite, got {gain}")
+        lib = load_library()
+        axis = [a for a, n in enumerate(axes) for _ in range(n)]
+        self.d, self.frequencies, self.axes, self.layout, self.gain = d, tuple(f), tuple(axes), layout, float(gain)
+        self._pairs = torch.tensor([[lib.sa2_rotary_turns(w), a] for w, a in zip(f, axis)], dtype=torch.int64, device=device)
+
+    def __reduce__(self):
+        return type(self), (self.d, self.frequencies, self.axes, self.layout, self.gain, self._pairs.device)
+
+
+def rotary(rotary: Rotary, pos: torch.Tensor, q: torch.Tensor, k: Optional[torch.Tensor] = None, inverse: bool = False,
+           q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """sa2_rotary_apply: q, and k where given, turned by the angles of their positions: (q', k') or q'.
+
+    q [B, H, N, d] and k [B, Hkv, N, d], or [H, T, d] and [Hkv, T, d] of packed sequences (bfloat16, float16
+    or float32; strides of their own).  ``pos``: int32 [N] or [B, N], with several axes [axes, N] or
+    [axes, B, N].  ``inverse``: the transposed map, which takes gradients of q', k' to those of q, k.
+    ``q_out`` = q, ``k_out`` = k turn in place."""
+    got = (_binding or load_binding()).rotary(rotary._pairs, len(rotary.frequencies), len(rotary.axes),
+                                              rotary.layout == "half", rotary.gain, rotary.d, pos, q, k, inverse, q_out,
+                                              k_out, _handle(stream))
+    return got if k is not None else got[0]
 
 
 def device_status(stream=None) -> int:

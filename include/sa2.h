@@ -402,6 +402,145 @@ sa2_status sa2_cache8_attn(const sa2_cross_shape* shape, const sa2_tensor* q, co
                            size_t ws_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------------------
+ * Attention within packed sequences, attention of new tokens over a paged cache, and rotary
+ * positions: what prompt encoders and frame-by-frame models beside the layers above need.
+ * The pages have no counterpart; the definitions are spelled out at each entry point.
+ *
+ * Conventions of these entry points, beside those of cross attention
+ * - B sequences lie one behind the other along the token axis: token tensors are [H, T, d]
+ *   (q, o, dO, dq) and [Hkv, T, d] (k, v, dk, dv), sa2_tensor with stride_b ignored.
+ *   seq [B + 1] int32 (device): sequence b has the tokens seq[b] .. seq[b + 1] - 1.  Tokens
+ *   before seq[0] and from seq[B] on belong to none: what inputs hold there, infinities and
+ *   NaN too, is not used, and outputs are left as they were.  A sequence may be empty.
+ *   Places that are not in ascending order within [0, T] are reported as
+ *   SA2_ERR_DEVICE_BOUNDS, and the attention calls then write nothing.
+ * - d in {64, 128}; dtype SA2_BF16 or SA2_FP16 (the backward: SA2_BF16); 1 <= T < 2^28;
+ *   B < 2^20; H a multiple of Hkv, H / Hkv <= 64.
+ * - lse is [H, T] fp32, contiguous.
+ */
+typedef struct sa2_packed_shape {
+  int32_t B, H, Hkv, T, d;
+  int32_t dtype;    /* sa2_dtype */
+  int32_t causal;   /* 1: a token attends to those up to itself; 0: to all of its sequence */
+  int32_t reserved; /* must be 0 */
+} sa2_packed_shape;
+
+/*
+ * Bytes of device workspace sa2_packed_attn_fwd needs (0 for an invalid shape): a counter of
+ * work items, or the parts of rows whose keys are split over the SMs.  Depends on the
+ * current device's SM count.
+ */
+size_t sa2_packed_fwd_workspace_size(const sa2_packed_shape* shape);
+
+/*
+ * sa2_packed_attn_fwd -- for token i of a sequence over its tokens j (j <= i where causal):
+ *   s_ij = scale * q_i . k_j,  LSE_i = log sum_j exp(s_ij),  O_i = sum_j exp(s_ij - LSE_i) v_j.
+ * Arithmetic, ranges and `scale` as in sa2_cross_attn_fwd.  A key that is masked counts for
+ * nothing whatever it holds; a value that is infinite or NaN may reach the tokens up to 127
+ * before it, which share products with it (0 * inf).
+ *   ws   device workspace of at least sa2_packed_fwd_workspace_size(shape) bytes (may be NULL
+ *        when that is 0); two calls that may run at the same time need one each
+ */
+sa2_status sa2_packed_attn_fwd(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
+                               const sa2_tensor* v, const int32_t* seq, float scale, const sa2_tensor* o,
+                               float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * A cache in pages: keys and values [pages, Hkv, page, d] (k and v share type and strides;
+ * stride_p from page to page), `page` tokens each, a power of two in [16, 65536].
+ */
+typedef struct sa2_paged_cache {
+  void* k;
+  void* v;
+  int64_t stride_p, stride_h, stride_n; /* in elements */
+  int32_t pages, Hkv, page, d;
+  int32_t dtype; /* SA2_BF16 or SA2_FP16 */
+  int32_t reserved; /* must be 0 */
+} sa2_paged_cache;
+
+/*
+ * Which pages hold which sequence: token t of sequence b is token t % page of page
+ * table[b * stride_b + t / page] (int32, device).  `width` columns; those behind a sequence's
+ * last token are not read.  A page outside [0, pages) is reported as SA2_ERR_DEVICE_BOUNDS;
+ * it reads as zeros and is not written.
+ */
+typedef struct sa2_page_table {
+  const int32_t* table;
+  int64_t stride_b;
+  int32_t width;
+  int32_t reserved; /* must be 0 */
+} sa2_page_table;
+
+/*
+ * sa2_paged_append -- k and v ([Hkv, T, d], of the cache's type) of new tokens into the pages
+ * of their sequences.  kv_len [B] int32 (device): the tokens that the cache holds of each
+ * sequence with the new ones, which are its last.  A length that leaves out new tokens or
+ * passes width * page is reported as SA2_ERR_DEVICE_BOUNDS, and nothing of that sequence is
+ * written.  No page may be in two rows that both get tokens.
+ */
+sa2_status sa2_paged_append(const sa2_paged_cache* cache, int32_t B, int32_t T, const sa2_tensor* k,
+                            const sa2_tensor* v, const int32_t* seq, const int32_t* kv_len,
+                            const sa2_page_table* table, void* stream);
+
+/*
+ * sa2_paged_attn -- sa2_packed_attn_fwd of the new tokens' q over all that the cache holds of
+ * their sequences: token i of n, in a sequence of m = kv_len[b] tokens, has position
+ * m - n + i and attends to the positions up to its own (causal) or to all m.  The new tokens
+ * are in the cache already (sa2_paged_append).  A length out of range, as above, is reported
+ * as SA2_ERR_DEVICE_BOUNDS and counts as no keys: O = 0, LSE = -inf.
+ *   max_new  no sequence has more new tokens than this (0: not known).  With few of them,
+ *            rows (tokens times H / Hkv) that fit one small tile take kernels made for that;
+ *            a sequence with more is reported as SA2_ERR_DEVICE_BOUNDS, and its O and LSE
+ *            are not defined.
+ *   ws       device workspace of at least sa2_paged_attn_workspace_size bytes, as above
+ */
+size_t sa2_paged_attn_workspace_size(const sa2_packed_shape* shape, const sa2_paged_cache* cache, int32_t width,
+                                     int32_t max_new);
+sa2_status sa2_paged_attn(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_paged_cache* cache,
+                          const int32_t* seq, const int32_t* kv_len, const sa2_page_table* table, int32_t max_new,
+                          float scale, const sa2_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions.  Pair i of a token's channels is (2 i, 2 i + 1) (interleaved) or
+ * (i, i + n) (halves), i < n; channels behind the 2 n turned ones stay as they are.
+ *   pairs   device array of n records of two int64: turns per position in 64 bits behind the
+ *           point (sa2_rotary_turns), and the axis whose position counts for the pair
+ *   axes    axes of the positions: 1, or e.g. 3 for frame, row and column
+ *   gain    factor of the turned channels (1 where positions are not scaled)
+ */
+typedef enum sa2_rotary_layout { SA2_ROTARY_INTERLEAVED = 0, SA2_ROTARY_HALVES = 1 } sa2_rotary_layout;
+
+typedef struct sa2_rotary {
+  const int64_t* pairs; /* 16-byte aligned */
+  int32_t n;
+  int32_t axes;
+  int32_t layout; /* sa2_rotary_layout */
+  float gain;
+} sa2_rotary;
+
+/* Turns per position of an angular frequency (radians per position), modulo whole turns, times 2^64. */
+int64_t sa2_rotary_turns(double frequency);
+
+/*
+ * sa2_rotary_apply -- for each token at position p and each pair (a, b), t = p * frequency:
+ *   a' = gain (a cos t - b sin t),  b' = gain (b cos t + a sin t)
+ * and with `inverse` the transposed map, sin t negated: the gradient's way back.  Angles are
+ * exact to 2^-30 of a turn at any position, sine and cosine are fp32, and the result is
+ * rounded once.
+ *   x, y    [B, H, N, d] from and to, dtype SA2_BF16, SA2_FP16 or SA2_FP32; y may be x itself
+ *           (then only the turned channels are touched) and overlaps nothing otherwise
+ *   x2, y2  a second tensor with H2 heads, e.g. keys beside queries (NULL, H2 = 0: none)
+ *   pos     [axes, B, N] int32 (device), any sign; token n of sequence b has its position
+ *           on axis a at pos[a * pos_axis + b * pos_b + n] (pos_b = 0: the same in each)
+ * d a multiple of 8 up to 1024; 2 n <= d, halves: n a multiple of 8; B N < 2^28 in all.
+ */
+sa2_status sa2_rotary_apply(const sa2_rotary* rotary, int32_t dtype, int32_t B, int32_t N, int32_t d,
+                            const int32_t* pos, int64_t pos_axis, int64_t pos_b, int32_t H, const sa2_tensor* x,
+                            const sa2_tensor* y, int32_t H2, const sa2_tensor* x2, const sa2_tensor* y2,
+                            int32_t inverse, void* stream);
+
+/*
  * Launch profiler (instrumentation of this library; the pages have no counterpart).
  * sa2_profiler_enable(1) makes every later kernel launch of the library record a CUDA
  * event before and after it on its stream; sa2_profiler_enable(0) stops that.
