@@ -24,6 +24,7 @@ from .sa2 import (  # noqa: F401
     device_status,
     load_library,
     make_shape,
+    packed_attn_bwd,
     packed_attn_fwd,
     paged_append,
     paged_attn,

@@ -400,6 +400,32 @@ PyObject* packed_fwd(PyObject* const* a) {
   return tuple_of(o, lse);
 }
 
+// q, k, v, o, lse, do, seq, causal, scale, dq, dk, dv, ws, stream
+PyObject* packed_bwd(PyObject* const* a) {
+  const at::Tensor& q = dims3(tensor(a[0], "q"), "q");
+  const at::Tensor& k = dims3(tensor(a[1], "k"), "k");
+  const at::Tensor& v = tensor(a[2], "v");
+  const sa2_packed_shape s = packed_shape(q, k.size(0), sequences(a[6]), truth(a[7]));
+  const Place at_(q.device(), a[13]);
+  const int64_t kvs[3] = {k.size(0), q.size(1), q.size(2)}, ls[2] = {q.size(0), q.size(1)};
+  const at::ScalarType t = q.scalar_type();
+  const sa2_tensor qt = token3(q, "q", q.sizes(), t, at_), kt = token3(k, "k", kvs, t, at_), vt = token3(v, "v", kvs, t, at_),
+                   ot = token3(tensor(a[3], "o"), "o", q.sizes(), t, at_),
+                   dot = token3(tensor(a[5], "do"), "do", q.sizes(), t, at_);
+  const float* lse = float32s(tensor(a[4], "lse"), "lse", ls, at_);
+  const int32_t* seq = int32s(a[6], "seq", s.B + 1, at_);
+  const at::Tensor dq = at_.given_or_like(a[9], "dq", q), dk = at_.given_or_like(a[10], "dk", k),
+                   dv = at_.given_or_like(a[11], "dv", v);
+  const sa2_tensor dqt = token3(dq, "dq", q.sizes(), t, at_), dkt = token3(dk, "dk", kvs, t, at_),
+                   dvt = token3(dv, "dv", kvs, t, at_);
+  const float scale = scale_of(a[8]);
+  const Workspace ws(a[12], sa2_packed_bwd_workspace_size(&s), at_);
+  if (s.T > 0)
+    check("sa2_packed_attn_bwd", sa2_packed_attn_bwd(&s, &qt, &kt, &vt, &ot, lse, &dot, seq, scale, &dqt, &dkt, &dvt, ws.p,
+                                                     ws.bytes, at_.stream));
+  return tuple_of(dq, dk, dv);
+}
+
 // k, v: checks a paged cache's tensors; its (shape, device index or -1, sa2_paged_cache as bytes).
 PyObject* paged_pack(PyObject* const* a) {
   const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
@@ -596,7 +622,8 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 PyMethodDef methods[] = {FAST("cross_attn_fwd", cross_fwd, 9),   FAST("cross_attn_bwd", cross_bwd, 13),
                          FAST("cache8_append", cache_append, 7), FAST("cache8_read", cache_read, 8),
                          FAST("cache8_attn", cache_attn, 9),     FAST("cache8_pack", cache_pack, 4),
-                         FAST("packed_attn_fwd", packed_fwd, 10), FAST("paged_pack", paged_pack, 2),
+                         FAST("packed_attn_fwd", packed_fwd, 10), FAST("packed_attn_bwd", packed_bwd, 14),
+                         FAST("paged_pack", paged_pack, 2),
                          FAST("paged_append", paged_append, 8),  FAST("paged_attn", paged_attn, 13),
                          FAST("rotary", rotary, 13),
                          {"set_error", set_error, METH_O, nullptr},

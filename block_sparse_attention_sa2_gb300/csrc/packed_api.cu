@@ -121,6 +121,54 @@ sa2_status sa2_packed_attn_fwd(const sa2_packed_shape* shape, const sa2_tensor* 
   return run_fwd(s, q, kr, vr, {seq, nullptr, nullptr}, scale, o, lse, ws, ws_bytes, stream);
 }
 
+size_t sa2_packed_bwd_workspace_size(const sa2_packed_shape* shape) {
+  PackedShape s;
+  if (check_packed(shape, &s) != SA2_OK || s.dtype != SA2_BF16) return 0;
+  size_t stats, part;
+  return packed_bwd_bytes(s, packed_bwd_plan(s, sm_count()), &stats, &part);
+}
+
+sa2_status sa2_packed_attn_bwd(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
+                               const sa2_tensor* v, const sa2_tensor* o, const float* lse, const sa2_tensor* dO,
+                               const int32_t* seq, float scale, const sa2_tensor* dq, const sa2_tensor* dk,
+                               const sa2_tensor* dv, void* ws, size_t ws_bytes, void* stream) {
+  PackedShape s;
+  sa2_status st = check_packed(shape, &s);
+  if (st != SA2_OK) return st;
+  if (s.dtype != SA2_BF16) return SA2_ERR_UNSUPPORTED;
+  if (!lse || !seq || !std::isfinite(scale)) return SA2_ERR_INVALID_ARG;
+  PackedBwdArgs a{};
+  TokenRef qr, kr, vr;
+  st = check_tensor(q, 1, s.H, s.G, s.T, s.d, 2, &qr);
+  if (st == SA2_OK) st = check_tensor(k, 1, s.Hkv, 1, s.T, s.d, 2, &kr);
+  if (st == SA2_OK) st = check_tensor(v, 1, s.Hkv, 1, s.T, s.d, 2, &vr);
+  if (st == SA2_OK) st = check_tensor(o, 1, s.H, s.G, s.T, s.d, 2, &a.o);
+  if (st == SA2_OK) st = check_tensor(dO, 1, s.H, s.G, s.T, s.d, 2, &a.dO);
+  if (st == SA2_OK) st = check_tensor(dq, 1, s.H, s.G, s.T, s.d, 2, &a.dq);
+  if (st == SA2_OK) st = check_tensor(dk, 1, s.Hkv, 1, s.T, s.d, 2, &a.dk);
+  if (st == SA2_OK) st = check_tensor(dv, 1, s.Hkv, 1, s.T, s.d, 2, &a.dv);
+  if (st != SA2_OK) return st;
+  if (misaligned4(lse) || misaligned4(seq) || !aligned16(ws)) return SA2_ERR_ALIGNMENT;
+  const PackedBwdPlan p = packed_bwd_plan(s, sm_count());
+  size_t stats, part;
+  if (!ws || ws_bytes < packed_bwd_bytes(s, p, &stats, &part)) return SA2_ERR_WORKSPACE;
+  CUtensorMap mq, mk, mv, mdo;
+  if (!make_group_map(&mq, qr, 1, s.H, s.G, s.T, s.d, s.G, p.nb, false) ||
+      !make_group_map(&mdo, a.dO, 1, s.H, s.G, s.T, s.d, s.G, p.nb, false) ||
+      !make_group_map(&mk, kr, 1, s.Hkv, 1, s.T, s.d, 1, kKeyBlock, false) ||
+      !make_group_map(&mv, vr, 1, s.Hkv, 1, s.T, s.d, 1, kKeyBlock, false))
+    return SA2_ERR_CUDA;
+  a.seqs = {seq, nullptr, nullptr};
+  a.lse = lse;
+  a.counter = static_cast<unsigned*>(ws);
+  a.stats = reinterpret_cast<float*>(static_cast<char*>(ws) + stats);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + part);
+  a.scale = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)s.d));
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.status = status_word();
+  return cuda_status(launch_packed_bwd(s, p, mq, mk, mv, mdo, a, static_cast<cudaStream_t>(stream)));
+}
+
 sa2_status sa2_paged_append(const sa2_paged_cache* cache, int32_t B, int32_t T, const sa2_tensor* k,
                             const sa2_tensor* v, const int32_t* seq, const int32_t* kv_len,
                             const sa2_page_table* table, void* stream) {

@@ -1,0 +1,1006 @@
+// Backward of attention within packed sequences on sm_103a (tcgen05 + TMEM + TMA):
+//   P = exp(s - LSE), dP = dO V^T, D = rowsum(dO * O), dS = P (dP - D),
+//   dV = P^T dO, dK = scale dS^T Q, dQ = scale dS K,   P = 0 behind the diagonal where causal.
+// The kernels are those of cross_bwd.cu, whose comments explain the products, the order in which they are
+// issued and the layouts: one walks the keys of a query tile (dQ), one the query tiles of a key block (dK, dV), and
+// every sum is made in one order.  What differs:
+// - A tile's keys end at its last token and a key block's tiles begin at its first: of a causal sequence
+//   half the products are left out, and P is cut element by element where a tile crosses the diagonal.
+// - The tiles of a key block, or the keys of a tile, are few for one and many for the next: work items come
+//   from a counter, the longest first (ItemQueue); warp 0 finds them and hands them to the others.
+// - Behind a sequence's last token lie the next one's: rows of Q and dO there are zeroed in shared memory (their P
+//   is 0, but 0 * NaN is NaN), and results are stored row by row.
+#include <algorithm>
+
+#include "cross_grad.cuh"
+#include "cross_softmax.cuh"
+#include "packed_sched.cuh"
+
+namespace sa2 {
+namespace {
+
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSlots = 4;  // items handed out and not yet finished
+
+// ------------------------------------------------------------------------- statistics
+//
+// D and log2(e) * LSE of every query row, D / 16 threads per row; grid (tile records, key heads, 128 / rows of
+// a CTA).  Bound by the bytes of dO and O.  It also clears the work counters.
+template <int D>
+constexpr int kStatsRows = 256 / (D / 16);
+template <int D>
+__global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant__ PackedShape s,
+                                                          const __grid_constant__ PackedBwdPlan plan,
+                                                          const __grid_constant__ PackedBwdArgs a) {
+  constexpr int kLanes = D / 16;
+  kernel_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) a.counter[threadIdx.x] = 0u;
+  const int b = sequence_of_record(s, a.seqs, plan.nb, (int)blockIdx.x);
+  const int lo = a.seqs.seq[b], n = a.seqs.seq[b + 1] - lo;
+  const int tile = (int)blockIdx.x - first_record(lo, plan.nb, b), hk = blockIdx.y;
+  // (places out of order: nothing is read out of range here, and the other kernels do nothing)
+  if (tile < 0 || n < 1 || lo < 0 || (int64_t)lo + n > s.T || tile >= (n + plan.nb - 1) / plan.nb) return;
+  const int ch = (threadIdx.x % kLanes) * 16;
+  const int r = threadIdx.x / kLanes + blockIdx.z * kStatsRows<D>;
+  const int tok_r = r / s.G, h = hk * s.G + r - tok_r * s.G, tok = tile * plan.nb + tok_r;
+  uint4 x[2], y[2];
+  x[0] = x[1] = y[0] = y[1] = make_uint4(0, 0, 0, 0);
+  float lse = INFINITY;
+  if (tok_r < plan.nb && tok < n) {
+    const int64_t t = lo + tok;
+    const uint4* px = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dO.p) + h * a.dO.sh + t * a.dO.sn + ch);
+    const uint4* py = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o.p) + h * a.o.sh + t * a.o.sn + ch);
+    x[0] = __ldg(px);
+    x[1] = __ldg(px + 1);
+    y[0] = __ldg(py);
+    y[1] = __ldg(py + 1);
+    if (ch == 0) lse = a.lse[(int64_t)h * s.T + t];
+  }
+  float acc = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    const uint32_t ys[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      acc = fmaf(__uint_as_float(xs[q] << 16), __uint_as_float(ys[q] << 16), acc);
+      acc = fmaf(__uint_as_float(xs[q] & 0xFFFF0000u), __uint_as_float(ys[q] & 0xFFFF0000u), acc);
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
+  if (ch == 0) {
+    float* rec = a.stats + (hk * plan.tile_recs + blockIdx.x) * 256;
+    rec[r] = lse * 1.4426950408889634f;
+    rec[128 + r] = acc;
+  }
+}
+
+// Rows [from, 128) of a tile of Q or dO as zeros; called by a whole warp.
+template <int PANELS>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
+  const int n = (128 - from) * 8 * PANELS;
+  for (int q = threadIdx.x & 31; q < n; q += 32) {
+    const int row = from + (q >> 3) % (128 - from), p = (q >> 3) / (128 - from);
+    *reinterpret_cast<uint4*>(tile + p * 16384 + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------------------- dQ
+
+// A query tile: tile t of the sequence with first token lo and n tokens, for key head hk (-1: no work left),
+// and its record.
+struct DqItem {
+  int lo, n, hk, tile;
+  int64_t rec;
+  int b, pad;
+};
+
+template <int D>
+struct DqSmem {
+  static constexpr int kRowWarps = D == 128 ? 8 : 16;
+  static constexpr int kThreads = 32 * (4 + kRowWarps + 4);
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = 128 * 128 * kPanels;
+  static constexpr int kKStages = 3, kVStages = 2;
+  static constexpr int kOffQ = 0, kOffDO = kTile;
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + kKStages * kTile;
+  static constexpr int kOffBar = kOffV + kVStages * kTile;
+  static constexpr int kOffSlot = kOffBar + 512;
+  // at least 120 KB, so that one CTA (512 TMEM columns) has an SM to itself
+  static constexpr int kBytes = (kOffSlot + 512 + 1024) > 120 * 1024 ? (kOffSlot + 512 + 1024) : 120 * 1024;
+  static_assert(kSlots * (int)sizeof(DqItem) <= 512 && kBytes <= (int)kMaxDynSmem, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
+    packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                     const __grid_constant__ PackedShape s, const __grid_constant__ PackedBwdPlan plan,
+                     const __grid_constant__ PackedBwdArgs a) {
+  using L = DqSmem<D>;
+  constexpr int kKSt = L::kKStages, kVSt = L::kVStages;
+  constexpr uint32_t kS = 0, kDP = 128, kDQ = 384;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  auto bar_kfull = [&](int st) { return smem_u32(&bars[st]); };
+  auto bar_kempty = [&](int st) { return smem_u32(&bars[3 + st]); };
+  auto bar_vfull = [&](int st) { return smem_u32(&bars[6 + st]); };
+  auto bar_vempty = [&](int st) { return smem_u32(&bars[8 + st]); };
+  const uint32_t bar_q = smem_u32(&bars[10]), bar_qfree = smem_u32(&bars[11]);    // Q landed / read
+  const uint32_t bar_do = smem_u32(&bars[12]), bar_dofree = smem_u32(&bars[13]);  // dO
+  const uint32_t bar_s = smem_u32(&bars[14]), bar_sfree = smem_u32(&bars[15]);    // S in TMEM / read out
+  auto bar_dp = [&](int i) { return smem_u32(&bars[16 + i]); };    // dP buffer i in TMEM
+  auto bar_ds = [&](int i) { return smem_u32(&bars[18 + i]); };    // dS written over it
+  auto bar_dqm = [&](int i) { return smem_u32(&bars[20 + i]); };   // dQ += dS K from it completed
+  const uint32_t bar_dq = smem_u32(&bars[22]), bar_dqfree = smem_u32(&bars[23]);  // dQ of the item complete / read
+  const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]), bar_pdrain = smem_u32(&bars[26]);
+  auto bar_slot = [&](uint32_t i) { return smem_u32(&bars[27 + i]); };            // an item handed out
+  auto bar_taken = [&](uint32_t i) { return smem_u32(&bars[27 + kSlots + i]); };  // ... and read by every other warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
+  DqItem* slots = reinterpret_cast<DqItem*>(smem + L::kOffSlot);
+  const WaitCtl wc{abort_flag, s.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kKSt; ++i) {
+      mbar_init(bar_kfull(i), 1);
+      mbar_init(bar_kempty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_vfull(i), 1);
+      mbar_init(bar_vempty(i), 1);
+      mbar_init(bar_dp(i), 1);
+      mbar_init(bar_ds(i), 32 * L::kRowWarps);
+      mbar_init(bar_dqm(i), 1);
+    }
+    mbar_init(bar_q, 1);
+    mbar_init(bar_qfree, 1);
+    mbar_init(bar_do, 1);
+    mbar_init(bar_dofree, 1);
+    mbar_init(bar_s, 1);
+    mbar_init(bar_sfree, 32 * L::kRowWarps);
+    mbar_init(bar_dq, 1);
+    mbar_init(bar_dqfree, 128);
+    mbar_init(bar_drain, 1);
+    mbar_init(bar_gdrain, 1);
+    mbar_init(bar_pdrain, 1);
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      mbar_init(bar_slot(i), 1);
+      mbar_init(bar_taken(i), L::kThreads / 32 - 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  kernel_wait();
+  const int nb = plan.nb;
+
+  auto take = [&](uint32_t n, DqItem& x) {
+    const uint32_t i = n % kSlots;
+    if (!__all_sync(kFull, mbar_wait(bar_slot(i), (n / kSlots) & 1, wc))) return false;
+    x = slots[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_taken(i));
+    return x.hk >= 0;
+  };
+  // keys that any row of the tile reads
+  auto keys_of = [&](const DqItem& x) { return s.causal ? min(x.n, (x.tile + 1) * nb) : x.n; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------- work finder and TMA producer
+    const bool in_order = seqs_in_order(s, a.seqs, false, a.status);
+    ItemQueue queue(s, a.seqs, nb, 1, plan.heads, plan.dq_grid, false, a.counter + 1, in_order);
+    const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * nb * s.G);
+    uint32_t J = 0, nv = 0, qn = 0, don = 0;  // K, V, Q and dO tiles loaded
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      DqItem x{};
+      int part;
+      const bool more = queue.next(x.b, x.tile, x.hk, part);
+      if (more) {
+        x.lo = a.seqs.seq[x.b];
+        x.n = a.seqs.seq[x.b + 1] - x.lo;
+        x.rec = x.hk * plan.tile_recs + first_record(x.lo, nb, x.b) + x.tile;
+      } else {
+        x.hk = -1;
+      }
+      const uint32_t i = n % kSlots;
+      ok = n < (uint32_t)kSlots || __all_sync(kFull, mbar_wait(bar_taken(i), (n / kSlots - 1) & 1, wc));
+      if (!ok) break;
+      if (lane == 0) {
+        slots[i] = x;
+        mbar_arrive(bar_slot(i));
+      }
+      if (!more) break;
+      if (lane == 0) {
+        const int nk = key_blocks(keys_of(x)), tok = x.lo + x.tile * nb;
+        for (int j = 0; j < nk; ++j) {
+          const int ks = J % kKSt, vs = nv % kVSt;
+          if (J >= (uint32_t)kKSt && !mbar_wait(bar_kempty(ks), ((J / kKSt) - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_kfull(ks), L::kTile);
+          for (int p = 0; p < L::kPanels; ++p)
+            tma_load_5d(sbase + L::kOffK + ks * L::kTile + p * 16384, &mk, bar_kfull(ks), p * 64, 0,
+                        x.lo + j * kKeyBlock, x.hk, 0);
+          ++J;
+          if (j == 0) {
+            if (qn >= 1 && !mbar_wait(bar_qfree, (qn - 1) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar_q, q_bytes);
+            for (int p = 0; p < L::kPanels; ++p)
+              tma_load_5d(sbase + L::kOffQ + p * 16384, &mq, bar_q, p * 64, 0, tok, x.hk, 0);
+            ++qn;
+            if (don >= 1 && !mbar_wait(bar_dofree, (don - 1) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(bar_do, q_bytes);
+            for (int p = 0; p < L::kPanels; ++p)
+              tma_load_5d(sbase + L::kOffDO + p * 16384, &mdo, bar_do, p * 64, 0, tok, x.hk, 0);
+            ++don;
+          }
+          if (nv >= (uint32_t)kVSt && !mbar_wait(bar_vempty(vs), ((nv / kVSt) - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_vfull(vs), L::kTile);
+          for (int p = 0; p < L::kPanels; ++p)
+            tma_load_5d(sbase + L::kOffV + vs * L::kTile + p * 16384, &mv, bar_vfull(vs), p * 64, 0,
+                        x.lo + j * kKeyBlock, x.hk, 0);
+          ++nv;
+        }
+      }
+      ok = __shfl_sync(kFull, ok, 0);
+    }
+    // no copy may still be in flight when the CTA exits
+    if (lane == 0) {
+      for (uint32_t v = J > (uint32_t)kKSt ? J - kKSt : 0; v < J; ++v)
+        mbar_drain(bar_kfull(v % kKSt), (v / kKSt) & 1, abort_flag);
+      for (uint32_t v = nv > (uint32_t)kVSt ? nv - kVSt : 0; v < nv; ++v)
+        mbar_drain(bar_vfull(v % kVSt), (v / kVSt) & 1, abort_flag);
+      if (qn) mbar_drain(bar_q, (qn - 1) & 1, abort_flag);
+      if (don) mbar_drain(bar_do, (don - 1) & 1, abort_flag);
+    }
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------------ issuers of S and of dP
+    const bool dp = warp == 3;
+    const uint64_t ad = smem_desc(sbase + (dp ? L::kOffDO : L::kOffQ), 16, 1024);
+    bool ok = true;
+    uint32_t J = 0;  // blocks
+    DqItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      const int keys = keys_of(x), nk = key_blocks(keys);
+      for (int j = 0; j < nk; ++j, ++J) {
+        const int ks = J % kKSt, vs = J % kVSt, bb = J & 1;
+        const int steps = (min(kKeyBlock, keys - j * kKeyBlock) + 15) >> 4;
+        const uint32_t idS = idesc_bf16_f32(128, steps * 16, false, false);
+        if (dp)
+          ok = __all_sync(kFull, mbar_wait(bar_vfull(vs), (J / kVSt) & 1, wc) && (j > 0 || mbar_wait(bar_do, n & 1, wc)) &&
+                                     (J < 2 || mbar_wait(bar_dqm(bb), ((J >> 1) - 1) & 1, wc)));
+        else
+          ok = __all_sync(kFull, mbar_wait(bar_kfull(ks), (J / kKSt) & 1, wc) && (j > 0 || mbar_wait(bar_q, n & 1, wc)) &&
+                                     (J == 0 || mbar_wait(bar_sfree, (J - 1) & 1, wc)));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (dp) {
+            issue_ss<D>(tmem + kDP + bb * 128, ad, smem_desc(sbase + L::kOffV + vs * L::kTile, 16, 1024), idS);
+            umma_commit(bar_dp(bb));
+            umma_commit(bar_vempty(vs));
+            if (j + 1 == nk) umma_commit(bar_dofree);
+          } else {
+            issue_ss<D>(tmem + kS, ad, smem_desc(sbase + L::kOffK + ks * L::kTile, 16, 1024), idS);
+            umma_commit(bar_s);
+            if (j + 1 == nk) umma_commit(bar_qfree);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) umma_commit(dp ? bar_pdrain : bar_drain);
+    __syncwarp();
+    mbar_drain(dp ? bar_pdrain : bar_drain, 0, abort_flag);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ issuer of dQ
+    constexpr uint32_t idQ = idesc_bf16_f32(128, D, false, true);
+    bool ok = true;
+    uint32_t J = 0;
+    DqItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      const int keys = keys_of(x), nk = key_blocks(keys);
+      for (int j = 0; j < nk; ++j, ++J) {
+        const int ks = J % kKSt, bb = J & 1;
+        const int steps = (min(kKeyBlock, keys - j * kKeyBlock) + 15) >> 4;
+        ok = __all_sync(kFull, (j > 0 || n == 0 || mbar_wait(bar_dqfree, (n - 1) & 1, wc)) &&
+                                   mbar_wait(bar_kfull(ks), (J / kKSt) & 1, wc) && mbar_wait(bar_ds(bb), (J >> 1) & 1, wc));
+        if (!ok) break;
+        const int valid = x.n - j * kKeyBlock, rows = 16 * steps - valid;
+        if (rows > 0) {
+          // rows of K behind the sequence's last key, up to the next multiple of 16, as zeros: dS is 0 there, but
+          // 0 * NaN is NaN.  S_j, which read them before, has completed (dS_j was made from it).
+          const int nz = rows * 8 * L::kPanels;
+          uint8_t* kt = smem + L::kOffK + ks * L::kTile;
+          for (int q = lane; q < nz; q += 32) {
+            const int row = valid + (q >> 3) % rows, p = (q >> 3) / rows;
+            *reinterpret_cast<uint4*>(kt + p * 16384 + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        tc_fence_after();
+        const uint64_t kmn = smem_desc(sbase + L::kOffK + ks * L::kTile, 16384, 1024);
+        if (elect_one()) {
+          issue_ts(tmem + kDQ, tmem + kDP + bb * 128, kmn, idQ, steps, j == 0);
+          umma_commit(bar_dqm(bb));
+          umma_commit(bar_kempty(ks));
+          if (j + 1 == nk) umma_commit(bar_dq);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) umma_commit(bar_gdrain);
+    __syncwarp();
+    mbar_drain(bar_gdrain, 0, abort_flag);
+  } else if (warp < 4 + L::kRowWarps) {
+    // ------------------------------------------------------------------ row threads
+    if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
+    constexpr int kKeys = 512 / L::kRowWarps;  // of each block, for this thread
+    const int k0 = kKeys * ((warp - 4) >> 2);
+    const int r = 32 * (warp & 3) + lane, tok_r = r / s.G;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    bool ok = true;
+    uint32_t J = 0;
+    DqItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      const int keys = keys_of(x), nk = key_blocks(keys);
+      const int mine = s.causal ? min(keys, x.tile * nb + tok_r + 1) : keys;  // keys of this row
+      const float lse2 = a.stats[x.rec * 256 + r], Dr = a.stats[x.rec * 256 + 128 + r];
+      for (int j = 0; j < nk; ++j, ++J) {
+        const int bb = J & 1;
+        const int valid = mine - j * kKeyBlock - k0;  // of this thread's keys
+        if (!__all_sync(kFull, mbar_wait(bar_s, J & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t u[kKeys / 32][32];
+        float p[kKeys];
+#pragma unroll
+        for (int h = 0; h < kKeys / 32; ++h) tmem_ld32(trow + kS + k0 + 32 * h, u[h]);
+#pragma unroll
+        for (int h = 0; h < kKeys / 32; ++h) tmem_ld_wait(u[h]);
+        tc_fence_before();
+        mbar_arrive(bar_sfree);
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) p[c] = ex2(fmaf(__uint_as_float(u[c >> 5][c & 31]), a.scale_log2, -lse2));
+        if (!__all_sync(kFull, mbar_wait(bar_dp(bb), (J >> 1) & 1, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tdp = trow + kDP + bb * 128 + k0;
+#pragma unroll
+        for (int h = 0; h < kKeys / 32; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[16];
+            tmem_ld16(tdp + 32 * h + 16 * q, v);
+            tmem_ld_wait16(v);
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const int k = 32 * h + 16 * q + c;
+              const float d0 = p[k] * (__uint_as_float(v[c]) - Dr), d1 = p[k + 1] * (__uint_as_float(v[c + 1]) - Dr);
+              pk[(16 * q + c) / 2] = pack_bf16x2(d0, d1);
+            }
+          }
+          if (valid < 32 * (h + 1)) {  // behind the row's last key P and dP may be anything
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const int left = valid - 32 * h - 2 * c;
+              pk[c] = left > 1 ? pk[c] : (left > 0 ? pk[c] & 0xFFFFu : 0u);
+            }
+          }
+          tmem_st16(tdp + 32 * h, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_ds(bb));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int tok_r = r / s.G, gq = r - tok_r * s.G;
+    bool ok = true;
+    DqItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      const int tok = x.tile * nb + tok_r;
+      const bool row_valid = tok_r < nb && tok < x.n;
+      uint16_t* row = static_cast<uint16_t*>(a.dq.p) + (int64_t)(x.hk * s.G + gq) * a.dq.sh + (int64_t)(x.lo + tok) * a.dq.sn;
+      ok = __all_sync(kFull, mbar_wait(bar_dq, n & 1, wc));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t u[32];
+        tmem_ld32(trow + kDQ + c0, u);
+        tmem_ld_wait(u);
+        if (c0 + 32 >= D) {
+          tc_fence_before();
+          mbar_arrive(bar_dqfree);
+        }
+        float v[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(u[c]) * a.scale;
+        if (row_valid) store32_bf16(row + c0, v);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) report_error(a.status, kDevErrTimeout);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// --------------------------------------------------------------------------- dK, dV
+
+// A key block (128 keys from token 128 kb of the sequence on) with query tiles [t0, t0 + nt), or a part of
+// them; part: its place in the partial sums, or -1; rec: the record of tile 0.
+struct DkvItem {
+  int lo, n, hk, kb, t0, nt;
+  int64_t rec, part;
+};
+
+template <int D>
+struct DkvSmem {
+  static constexpr bool kX = D == 64;  // LSE and D through the products
+  static constexpr int kThreads = kX ? 672 : 640;
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTile = 128 * 128 * kPanels;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kOffK = 0, kOffV = kTile;
+  static constexpr int kOffStage = 2 * kTile;  // Q, dO, statistics
+  static constexpr int kStageQ = 0, kStageDO = kTile, kStageX = 2 * kTile;
+  static constexpr int kStageStats = kStageX + (kX ? 2 * kXTile : 0);
+  static constexpr int kStage = kStageStats + 1024;
+  static constexpr int kOffOnes = kOffStage + kStages * kStage;
+  static constexpr int kOffBar = kOffOnes + (kX ? kXTile : 0);
+  static constexpr int kOffSlot = kOffBar + 512;
+  static constexpr int kBytes = kOffSlot + 512 + 1024;
+  static_assert(kSlots * (int)sizeof(DkvItem) <= 512 && kBytes <= (int)kMaxDynSmem && kBytes > 114 * 1024,
+                "shared memory: one CTA per SM");
+};
+
+// Query tiles of part i of key block kb of a sequence of n tokens.
+__device__ __forceinline__ void part_tiles(const PackedShape& s, const PackedBwdPlan& p, int n, int kb, int i, int& t0, int& nt) {
+  const int first = s.causal ? kb * kKeyBlock / p.nb : 0, tiles = (n + p.nb - 1) / p.nb - first;
+  t0 = first + (int)((int64_t)tiles * i / p.parts);
+  nt = first + (int)((int64_t)tiles * (i + 1) / p.parts) - t0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
+    packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                       const __grid_constant__ PackedShape s, const __grid_constant__ PackedBwdPlan plan,
+                       const __grid_constant__ PackedBwdArgs a) {
+  using L = DkvSmem<D>;
+  constexpr int kStages = L::kStages;
+  constexpr uint32_t kBufs = D == 128 ? 2 : 3;  // of S^T and dP^T, 64 columns each
+  constexpr uint32_t kS = 0, kDP = 64 * kBufs, kDV = 2 * kDP, kDK = kDV + D;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  auto bar_full = [&](int st) { return smem_u32(&bars[st]); };
+  auto bar_empty = [&](int st) { return smem_u32(&bars[4 + st]); };
+  const uint32_t bar_kv = smem_u32(&bars[8]), bar_kvfree = smem_u32(&bars[9]);
+  auto bar_s = [&](uint32_t b) { return smem_u32(&bars[10 + b]); };    // S^T, dP^T in TMEM buffer b
+  auto bar_dp = [&](uint32_t b) { return smem_u32(&bars[13 + b]); };
+  auto bar_p = [&](uint32_t b) { return smem_u32(&bars[16 + b]); };    // P^T, dS^T written over them
+  auto bar_ds = [&](uint32_t b) { return smem_u32(&bars[19 + b]); };
+  auto bar_dvm = [&](uint32_t b) { return smem_u32(&bars[22 + b]); };  // dV, dK products from them completed
+  auto bar_dkm = [&](uint32_t b) { return smem_u32(&bars[25 + b]); };
+  const uint32_t bar_acc = smem_u32(&bars[28]), bar_accfree = smem_u32(&bars[29]);  // the item's sums complete / read
+  const uint32_t bar_drain = smem_u32(&bars[30]), bar_gdrain = smem_u32(&bars[31]), bar_pdrain = smem_u32(&bars[32]);
+  auto bar_x = [&](int st) { return smem_u32(&bars[33 + st]); };                  // the 16 channels written
+  auto bar_slot = [&](uint32_t i) { return smem_u32(&bars[37 + i]); };            // an item handed out
+  auto bar_taken = [&](uint32_t i) { return smem_u32(&bars[37 + kSlots + i]); };  // ... and read by every other warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
+  DkvItem* slots = reinterpret_cast<DkvItem*>(smem + L::kOffSlot);
+  const WaitCtl wc{abort_flag, s.wait_ns};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nb = plan.nb;
+
+  // Tile rows that hold no query (128 is not a multiple of G) are never loaded: zeros, since their
+  // P and dS are 0 but 0 * NaN is NaN.
+  const int used = nb * s.G;
+  if (used < 128) {
+    const int n = (128 - used) * 8 * L::kPanels * 2 * kStages;
+    for (int i = tid; i < n; i += L::kThreads) {
+      const int row = used + (i >> 3) % (128 - used);
+      int x = (i >> 3) / (128 - used);
+      const int p = x % L::kPanels;
+      x /= L::kPanels;
+      uint8_t* t = smem + L::kOffStage + (x >> 1) * L::kStage + ((x & 1) ? L::kStageDO : L::kStageQ);
+      *reinterpret_cast<uint4*>(t + p * 16384 + row * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  for (int i = tid; L::kX && i < (2 * kStages + 1) * (kXTile / 16); i += L::kThreads) {
+    const int x = i / (kXTile / 16), at = (i % (kXTile / 16)) * 16;
+    const bool ones = x == 2 * kStages && !(at & 128);
+    uint8_t* tile = x == 2 * kStages ? smem + L::kOffOnes
+                                     : smem + L::kOffStage + (x >> 1) * L::kStage + L::kStageX + (x & 1) * kXTile;
+    *reinterpret_cast<uint4*>(tile + at) = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async();
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar_full(i), 1);
+      mbar_init(bar_empty(i), 1);
+      mbar_init(bar_x(i), 1);
+    }
+    mbar_init(bar_kv, 1);
+    mbar_init(bar_kvfree, 2);
+    for (uint32_t b = 0; b < kBufs; ++b) {
+      mbar_init(bar_s(b), 1);
+      mbar_init(bar_dp(b), 1);
+      mbar_init(bar_p(b), 256);
+      mbar_init(bar_ds(b), 256);
+      mbar_init(bar_dvm(b), 1);
+      mbar_init(bar_dkm(b), 1);
+    }
+    mbar_init(bar_acc, 1);
+    mbar_init(bar_accfree, 512);
+    mbar_init(bar_drain, 1);
+    mbar_init(bar_gdrain, 1);
+    mbar_init(bar_pdrain, 1);
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      mbar_init(bar_slot(i), 1);
+      mbar_init(bar_taken(i), L::kThreads / 32 - 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  kernel_trigger();
+  kernel_wait();
+
+  auto take = [&](uint32_t n, DkvItem& x) {
+    const uint32_t i = n % kSlots;
+    if (!__all_sync(kFull, mbar_wait(bar_slot(i), (n / kSlots) & 1, wc))) return false;
+    x = slots[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_taken(i));
+    return x.hk >= 0;
+  };
+  // rows of tile t that hold queries
+  auto rows_of = [&](const DkvItem& x, int t) { return min(nb, x.n - t * nb) * s.G; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------- work finder and TMA producer
+    const bool in_order = seqs_in_order(s, a.seqs, blockIdx.x == 0, a.status);
+    ItemQueue queue(s, a.seqs, kKeyBlock, plan.parts, plan.heads, plan.grid, true, a.counter, in_order);
+    const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * used);
+    uint32_t U = 0, kvn = 0;  // tiles, key blocks loaded
+    bool ok = true;
+    for (uint32_t n = 0; ok;) {
+      DkvItem x{};
+      int b, part;
+      const bool more = queue.next(b, x.kb, x.hk, part);
+      if (more) {
+        x.lo = a.seqs.seq[b];
+        x.n = a.seqs.seq[b + 1] - x.lo;
+        part_tiles(s, plan, x.n, x.kb, part, x.t0, x.nt);
+        if (x.nt == 0) continue;
+        x.rec = x.hk * plan.tile_recs + first_record(x.lo, nb, b);
+        x.part = plan.parts == 1 ? -1
+                                 : (x.hk * plan.block_recs + first_record(x.lo, kKeyBlock, b) + x.kb) * plan.parts + part;
+      } else {
+        x.hk = -1;
+      }
+      const uint32_t i = n % kSlots;
+      ok = n < (uint32_t)kSlots || __all_sync(kFull, mbar_wait(bar_taken(i), (n / kSlots - 1) & 1, wc));
+      if (!ok) break;
+      if (lane == 0) {
+        slots[i] = x;
+        mbar_arrive(bar_slot(i));
+      }
+      ++n;
+      if (!more) break;
+      if (lane == 0 && (kvn == 0 || (ok = mbar_wait(bar_kvfree, (kvn - 1) & 1, wc)))) {
+        mbar_arrive_expect_tx(bar_kv, 2 * L::kTile);
+        for (int p = 0; p < L::kPanels; ++p) {
+          tma_load_5d(sbase + L::kOffK + p * 16384, &mk, bar_kv, p * 64, 0, x.lo + x.kb * kKeyBlock, x.hk, 0);
+          tma_load_5d(sbase + L::kOffV + p * 16384, &mv, bar_kv, p * 64, 0, x.lo + x.kb * kKeyBlock, x.hk, 0);
+        }
+        ++kvn;
+        for (int t = x.t0; t < x.t0 + x.nt; ++t, ++U) {
+          const int st = U % kStages;
+          if (U >= (uint32_t)kStages && !mbar_wait(bar_empty(st), ((U / kStages) - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
+          mbar_arrive_expect_tx(bar_full(st), 2 * q_bytes + 1024);
+          for (int p = 0; p < L::kPanels; ++p) {
+            tma_load_5d(stg + L::kStageQ + p * 16384, &mq, bar_full(st), p * 64, 0, x.lo + t * nb, x.hk, 0);
+            tma_load_5d(stg + L::kStageDO + p * 16384, &mdo, bar_full(st), p * 64, 0, x.lo + t * nb, x.hk, 0);
+          }
+          bulk_load(stg + L::kStageStats, a.stats + (x.rec + t) * 256, 1024, bar_full(st));
+        }
+      }
+      ok = __shfl_sync(kFull, ok, 0);
+    }
+    if (lane == 0) {
+      for (uint32_t v = U > (uint32_t)kStages ? U - kStages : 0; v < U; ++v)
+        mbar_drain(bar_full(v % kStages), (v / kStages) & 1, abort_flag);
+      if (kvn) mbar_drain(bar_kv, (kvn - 1) & 1, abort_flag);
+    }
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------------ issuers of S^T and of dP^T
+    constexpr uint32_t idS = idesc_bf16_f32(128, 64, false, false);
+    const bool dp = warp == 3;
+    const uint64_t akd = smem_desc(sbase + (dp ? L::kOffV : L::kOffK), 16, 1024);
+    const uint32_t in_stage = dp ? L::kStageDO : L::kStageQ;
+    const uint32_t bst = sbase + L::kOffStage + in_stage;
+    const uint32_t xst = sbase + L::kOffStage + L::kStageX + (dp ? kXTile : 0);
+    const uint32_t dst = tmem + (dp ? kDP : kS), done = dp ? bar_dp(0) : bar_s(0), freed = dp ? bar_dkm(0) : bar_dvm(0);
+    bool ok = true;
+    uint32_t u = 0;  // half tiles
+    DkvItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      ok = __all_sync(kFull, mbar_wait(bar_kv, n & 1, wc));
+      for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
+        const uint32_t U = u >> 1, st = U % kStages, half = u & 1, b = u % kBufs;
+        ok = __all_sync(kFull, (half || (mbar_wait(bar_full(st), (U / kStages) & 1, wc) &&
+                                             (!L::kX || mbar_wait(bar_x(st), (U / kStages) & 1, wc)))) &&
+                                   (u < kBufs || mbar_wait(freed + 8 * b, (u / kBufs - 1) & 1, wc)));
+        if (!ok) break;
+        if (!half) {
+          const int rows = rows_of(x, x.t0 + (i >> 1));
+          if (rows < used) zero_rows<L::kPanels>(smem + L::kOffStage + st * L::kStage + in_stage, rows);
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ss<D>(dst + 64 * b, akd, smem_desc(bst + st * L::kStage + half * 8192, 16, 1024), idS);
+          if constexpr (L::kX)
+            umma_ss(dst + 64 * b, x_desc(sbase + L::kOffOnes), x_desc(xst + st * L::kStage + half * (kXTile / 2)), idS, 1u);
+          umma_commit(done + 8 * b);
+          if (i + 1 == 2 * x.nt) umma_commit(bar_kvfree);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) umma_commit(dp ? bar_pdrain : bar_drain);
+    __syncwarp();
+    mbar_drain(dp ? bar_pdrain : bar_drain, 0, abort_flag);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ issuer of dV and dK
+    constexpr uint32_t idG = idesc_bf16_f32(128, D, false, true);
+    bool ok = true;
+    uint32_t u = 0;
+    DkvItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
+        const uint32_t U = u >> 1, st = U % kStages, half = u & 1, b = u % kBufs, use = (u / kBufs) & 1;
+        uint8_t* tiles = smem + L::kOffStage + st * L::kStage;
+        const uint32_t stg = smem_u32(tiles) + half * 8192;  // rows 64 .. of each panel
+        ok = __all_sync(kFull, (i > 0 || n == 0 || mbar_wait(bar_accfree, (n - 1) & 1, wc)) &&
+                                   (half || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) && mbar_wait(bar_p(b), use, wc));
+        if (!ok) break;
+        if (!half) {
+          // (the issuer of dP zeroes the same rows, but has not been waited for; Q's were zeroed before S, which P
+          // was made from)
+          const int rows = rows_of(x, x.t0 + (i >> 1));
+          if (rows < used) zero_rows<L::kPanels>(tiles + L::kStageDO, rows);
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ts(tmem + kDV, tmem + kS + 64 * b, smem_desc(stg + L::kStageDO, 16384, 1024), idG, 4, i == 0);
+          umma_commit(bar_dvm(b));
+        }
+        __syncwarp();
+        ok = __all_sync(kFull, mbar_wait(bar_ds(b), use, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ts(tmem + kDK, tmem + kDP + 64 * b, smem_desc(stg + L::kStageQ, 16384, 1024), idG, 4, i == 0);
+          umma_commit(bar_dkm(b));
+          if (half) umma_commit(bar_empty(st));
+          if (i + 1 == 2 * x.nt) umma_commit(bar_acc);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) umma_commit(bar_gdrain);
+    __syncwarp();
+    mbar_drain(bar_gdrain, 0, abort_flag);
+  } else if (L::kX && warp == 20) {
+    // ------------------------------------------------------------- the 16 channels of LSE and D
+    const float inv = -1.f / fmaxf(a.scale_log2, kMinScale);
+    uint32_t U = 0;
+    bool ok = true;
+    DkvItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      for (int t = 0; t < x.nt; ++t, ++U) {
+        const int st = U % kStages;
+        uint8_t* stg = smem + L::kOffStage + st * L::kStage;
+        ok = __all_sync(kFull, mbar_wait(bar_full(st), (U / kStages) & 1, wc));
+        if (!ok) break;
+        const float* rec = reinterpret_cast<const float*>(stg + L::kStageStats);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * i + lane;
+          *reinterpret_cast<uint2*>(stg + L::kStageX + x_row(r)) = split3(rec[r] * inv);
+          *reinterpret_cast<uint2*>(stg + L::kStageX + kXTile + x_row(r)) = split3(-rec[128 + r]);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_x(st));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- element-wise threads
+    if (s.stall_ns && blockIdx.x == 0) stall_for(s.stall_ns);  // failure-path test hook
+    const uint32_t half = (uint32_t)(warp - 4) >> 3;  // of every tile
+    const int g = ((warp - 4) >> 2) & 1;              // rows 32 g .. 32 g + 31 of the half tile
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const float mul = L::kX ? fmaxf(a.scale_log2, kMinScale) : a.scale_log2;
+    const uint32_t ts0 = trow + kS + 32 * g + (kBufs == 2 ? 64 * half : 0);
+    bool ok = true;
+    uint32_t U = 0;  // tiles
+    DkvItem x;
+    for (uint32_t n = 0; ok && take(n, x); ++n) {
+      for (int t = x.t0; t < x.t0 + x.nt; ++t, ++U) {
+        const uint32_t u = 2 * U + half, b = kBufs == 2 ? half : u % kBufs, use = (kBufs == 2 ? U : u / kBufs) & 1;
+        const uint32_t ts = kBufs == 2 ? ts0 : ts0 + 64 * b, tdp = ts + kDP - kS;
+        const int st = U % kStages;
+        // Row c of this thread's 32 holds token floor(row / G) of the tile; where causal it reads this thread's key
+        // from the row on in which that token stands: rows before `cut` are masked.
+        const int cut = s.causal ? (x.kb * kKeyBlock + r - t * nb) * s.G - 64 * (int)half - 32 * g : 0;
+        const bool diagonal = s.causal && t * nb < x.kb * kKeyBlock + kKeyBlock - 1;
+        const float4* l4 = reinterpret_cast<const float4*>(smem + L::kOffStage + st * L::kStage + L::kStageStats) +
+                           16 * half + 8 * g;
+        const float4* d4 = l4 + 32;
+        if (!__all_sync(kFull, (L::kX || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) && mbar_wait(bar_s(b), use, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float p[32];
+        uint32_t v[32], pk[16];
+        tmem_ld32(ts, v);
+        tmem_ld_wait(v);
+        if constexpr (L::kX) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) p[c] = ex2(__uint_as_float(v[c]) * mul);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 l = l4[q];
+            float* pp = p + 4 * q;
+            pp[0] = ex2(fmaf(__uint_as_float(v[4 * q]), mul, -l.x));
+            pp[1] = ex2(fmaf(__uint_as_float(v[4 * q + 1]), mul, -l.y));
+            pp[2] = ex2(fmaf(__uint_as_float(v[4 * q + 2]), mul, -l.z));
+            pp[3] = ex2(fmaf(__uint_as_float(v[4 * q + 3]), mul, -l.w));
+          }
+        }
+        if (diagonal) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) p[c] = c < cut ? 0.f : p[c];
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        tmem_st16(ts, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_p(b));
+        if (!__all_sync(kFull, mbar_wait(bar_dp(b), use, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_ld32(tdp, v);
+        tmem_ld_wait(v);
+        if constexpr (L::kX) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16x2(p[2 * c] * __uint_as_float(v[2 * c]), p[2 * c + 1] * __uint_as_float(v[2 * c + 1]));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 d = d4[q];
+            const float* pp = p + 4 * q;
+            pk[2 * q] = pack_bf16x2(pp[0] * (__uint_as_float(v[4 * q]) - d.x), pp[1] * (__uint_as_float(v[4 * q + 1]) - d.y));
+            pk[2 * q + 1] =
+                pack_bf16x2(pp[2] * (__uint_as_float(v[4 * q + 2]) - d.z), pp[3] * (__uint_as_float(v[4 * q + 3]) - d.w));
+          }
+        }
+        if (diagonal) {  // (dP of a masked place may be anything)
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] = 2 * c + 1 < cut ? 0u : (2 * c < cut ? pk[c] & 0xFFFF0000u : pk[c]);
+        }
+        tmem_st16(tdp, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar_ds(b));
+      }
+      if (!ok) break;
+      // ---- the item's sums: thread = key, a quarter of the channels
+      if (!__all_sync(kFull, mbar_wait(bar_acc, n & 1, wc))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int key = x.kb * kKeyBlock + r, quarter = 2 * (int)half + g;
+      const bool live = key < x.n;
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {  // dK, dV
+        const TokenRef& out = w ? a.dv : a.dk;
+        const float f0 = w ? 1.f : a.scale;
+        uint16_t* row = static_cast<uint16_t*>(out.p) + (int64_t)x.hk * out.sh + (int64_t)(x.lo + key) * out.sn;
+        float* part = a.part + ((x.part * 2 + w) * 128 + r) * D;
+#pragma unroll
+        for (int c0 = 0; c0 < D / 4; c0 += 16) {
+          const int ch = quarter * (D / 4) + c0;
+          uint32_t z[16];
+          tmem_ld16(trow + (w ? kDV : kDK) + ch, z);
+          tmem_ld_wait16(z);
+          float f[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] = __uint_as_float(z[c]) * f0;
+          if (!live) continue;
+          if (x.part >= 0) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              reinterpret_cast<float4*>(part + ch)[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              reinterpret_cast<uint4*>(row + ch)[c] =
+                  make_uint4(pack_bf16x2(f[8 * c], f[8 * c + 1]), pack_bf16x2(f[8 * c + 2], f[8 * c + 3]),
+                             pack_bf16x2(f[8 * c + 4], f[8 * c + 5]), pack_bf16x2(f[8 * c + 6], f[8 * c + 7]));
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar_accfree);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag) report_error(a.status, kDevErrTimeout);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Adds the parts of each key block in their order.  Grid (key block records, key heads, 8): an eighth of a
+// block each, since a head has few.
+constexpr int kJoinParts = 8;
+template <int D>
+__global__ void __launch_bounds__(256) packed_dkdv_join_kernel(const __grid_constant__ PackedShape s,
+                                                              const __grid_constant__ PackedBwdPlan plan,
+                                                              const __grid_constant__ PackedBwdArgs a) {
+  kernel_trigger();
+  const int b = sequence_of_record(s, a.seqs, kKeyBlock, (int)blockIdx.x);
+  const int lo = a.seqs.seq[b], n = a.seqs.seq[b + 1] - lo;
+  const int kb = (int)blockIdx.x - first_record(lo, kKeyBlock, b), hk = blockIdx.y;
+  const bool in_order = seqs_in_order(s, a.seqs, false, a.status);
+  kernel_wait();  // (by every CTA: the dQ kernel waits for this one alone)
+  if (!in_order || kb < 0 || n < 1 || kb >= key_blocks(n)) return;
+  constexpr int kItems = 2 * 128 * (D / 8) / kJoinParts;
+  for (int j = threadIdx.x; j < kItems; j += 256) {
+    const int i = blockIdx.z * kItems + j;
+    const int w = i / (128 * (D / 8)), r = i / (D / 8) % 128, ch = i % (D / 8) * 8;
+    const int key = kb * kKeyBlock + r;
+    if (key >= n) continue;
+    float v[8] = {};
+    for (int k = 0; k < plan.parts; ++k) {
+      int t0, nt;
+      part_tiles(s, plan, n, kb, k, t0, nt);
+      if (nt == 0) continue;  // (not written)
+      const int64_t at = (hk * plan.block_recs + blockIdx.x) * plan.parts + k;
+      const float4* p = reinterpret_cast<const float4*>(a.part + ((at * 2 + w) * 128 + r) * D + ch);
+      const float4 x = p[0], y = p[1];
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    const TokenRef& out = w ? a.dv : a.dk;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out.p) + hk * out.sh + (int64_t)(lo + key) * out.sn + ch) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const PackedShape& s, const PackedBwdPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, const CUtensorMap& mdo, const PackedBwdArgs& a, cudaStream_t st) {
+  auto dq = packed_dq_kernel<D>;
+  auto dkv = packed_dkdv_kernel<D>;
+  static std::atomic<unsigned long long> dq_allowed{0}, dkv_allowed{0};
+  cudaError_t e = allow_smem(dq, DqSmem<D>::kBytes, dq_allowed);
+  if (e == cudaSuccess) e = allow_smem(dkv, DkvSmem<D>::kBytes, dkv_allowed);
+  if (e != cudaSuccess) return e;
+  prof_start(st, kBwdPre);
+  packed_stats_kernel<D><<<dim3((unsigned)p.tile_recs, (unsigned)s.Hkv, 128 / kStatsRows<D>), 256, 0, st>>>(s, p, a);
+  prof_stop(st, kBwdPre);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  prof_start(st, kAttnBwd);
+  e = launch_early(dkv, dim3((unsigned)p.grid), DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
+  if (e == cudaSuccess && p.parts > 1)
+    e = launch_early(packed_dkdv_join_kernel<D>, dim3((unsigned)p.block_recs, (unsigned)s.Hkv, kJoinParts), 256, 0, st, s, p, a);
+  prof_stop(st, kAttnBwd);
+  if (e != cudaSuccess) return e;
+  prof_start(st, kAttnBwdDq);
+  e = launch_early(dq, dim3((unsigned)p.dq_grid), DqSmem<D>::kThreads, DqSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
+  prof_stop(st, kAttnBwdDq);
+  return e;
+}
+
+}  // namespace
+
+PackedBwdPlan packed_bwd_plan(const PackedShape& s, int sms) {
+  PackedBwdPlan p{};
+  p.nb = 128 / s.G;
+  p.tile_recs = s.T / p.nb + s.B;
+  p.block_recs = s.T / kKeyBlock + s.B;
+  const int64_t blocks = s.Hkv * segment_bound(s, kKeyBlock), tiles = s.Hkv * segment_bound(s, p.nb);
+  // twice as many items as SMs, of two query tiles or more in a sequence of mean length
+  const int64_t mean_tiles = ((int64_t)s.T / s.B + p.nb - 1) / p.nb;
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>((2 * sms + blocks - 1) / blocks, mean_tiles / 2));
+  p.grid = (int)std::min<int64_t>(sms, blocks * p.parts);
+  p.dq_grid = (int)std::min<int64_t>(sms, tiles);
+  // Q, dO, K and V of the heads of a section take a third of L2 at most
+  const int64_t head_bytes = (int64_t)s.T * s.d * 4 * (s.G + 1);
+  p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(s.Hkv, (40ll << 20) / head_bytes));
+  return p;
+}
+
+size_t packed_bwd_bytes(const PackedShape& s, const PackedBwdPlan& p, size_t* stats, size_t* part) {
+  *stats = 256;  // behind the counters
+  *part = *stats + (size_t)s.Hkv * p.tile_recs * 256 * sizeof(float);
+  return *part + (p.parts > 1 ? (size_t)s.Hkv * p.block_recs * p.parts * 2 * 128 * s.d * sizeof(float) : 0);
+}
+
+cudaError_t launch_packed_bwd(const PackedShape& s, const PackedBwdPlan& p, const CUtensorMap& mq,
+                              const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                              const PackedBwdArgs& a, cudaStream_t st) {
+  return s.d == 128 ? launch_t<128>(s, p, mq, mk, mv, mdo, a, st) : launch_t<64>(s, p, mq, mk, mv, mdo, a, st);
+}
+
+}  // namespace sa2

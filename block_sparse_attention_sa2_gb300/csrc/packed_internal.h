@@ -69,6 +69,38 @@ inline int64_t segment_bound(const PackedShape& s, int w) {
   return a < s.T ? a : s.T;
 }
 
+// The backward's query tiles (nb tokens, row = token * G + g) and its key blocks of 128 tokens each have a
+// record for every key head: record seq[b] / nb + b + tile of B + T / nb (see first_record).
+//   stats  [Hkv][tile records][256]: log2(e) * LSE of row r (+inf for rows that hold no query: their P is 0)
+//          at r, D at 128 + r
+//   part   [Hkv][key block records][parts][2][128][d] fp32, dK and dV, where each block's query tiles are cut
+//          into parts, since there are too few blocks for the SMs; a second kernel adds them in order
+// Work items come from counters, as in the forward.
+struct PackedBwdPlan {
+  int nb;
+  int64_t tile_recs, block_recs;  // of a key head
+  int parts;
+  int grid, dq_grid;
+  int heads;  // key heads of a section
+};
+
+struct PackedBwdArgs {
+  PackedSeqs seqs;
+  TokenRef o, dO, dq, dk, dv;
+  const float* lse;
+  unsigned* counter;  // [2]: dK / dV, dQ
+  float* stats;
+  float* part;
+  float scale, scale_log2;
+  unsigned* status;
+};
+
+PackedBwdPlan packed_bwd_plan(const PackedShape& s, int sms);
+size_t packed_bwd_bytes(const PackedShape& s, const PackedBwdPlan& p, size_t* stats, size_t* part);
+cudaError_t launch_packed_bwd(const PackedShape& s, const PackedBwdPlan& p, const CUtensorMap& mq,
+                              const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                              const PackedBwdArgs& a, cudaStream_t st);
+
 PackedPlan packed_fwd_plan(const PackedShape& s, int sms);
 size_t packed_fwd_bytes(const PackedShape& s, const PackedPlan& p);
 cudaError_t launch_packed_fwd(const PackedShape& s, const PackedPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,

@@ -93,6 +93,104 @@ __device__ __forceinline__ int64_t blocks_before(const PackedShape& s, const Seq
   return n;
 }
 
+__device__ __forceinline__ int segments_of(const PackedShape& s, const PackedSeqs& q, int w, int b) {
+  const int n = b < s.B ? q.seq[b + 1] - q.seq[b] : 0;
+  return n > 0 ? (n + w - 1) / w : 0;
+}
+
+// Work items, `parts` of every segment of w tokens of every key head, taken from a counter by the CTAs (the
+// first by their own numbers): in sections of `heads` key heads; in a section by the segment's place in its
+// sequence, the last ones first (rising: the first ones first), then by sequence, head and part.
+struct ItemQueue {
+  const PackedShape& s;
+  const PackedSeqs& q;
+  const int w, parts, heads, grid;
+  const bool rising;
+  unsigned* counter;   // null: no more items than CTAs
+  int64_t segs, item;  // segments of one key head; the next item
+  unsigned drawn;      // of the counter, for the item after it (lane 0)
+  int section, level, most;
+  int64_t before, upto;  // segments that come before this level, and with it
+
+  __device__ __forceinline__ ItemQueue(const PackedShape& s_, const PackedSeqs& q_, int w_, int parts_, int heads_,
+                                       int grid_, bool rising_, unsigned* counter_, bool in_order)
+      : s(s_), q(q_), w(w_), parts(parts_), heads(heads_), grid(grid_), rising(rising_), counter(counter_), segs(0),
+        item(blockIdx.x), drawn(0), section(-1), level(0), most(0), before(0), upto(0) {
+    if (!in_order) return;
+    int64_t n = 0;
+    for (int i = (int)(threadIdx.x & 31); i < s.B; i += 32) {
+      const int k = segments_of(s, q, w, i);
+      n += k;
+      most = max(most, k);
+    }
+    segs = warp_sum(n);
+    most = __reduce_max_sync(kFull, most);
+    draw();
+  }
+  __device__ __forceinline__ void draw() {
+    if (counter && (threadIdx.x & 31) == 0) drawn = atomicAdd(counter, 1u);
+  }
+  // Segments that come in order before those of place l.
+  __device__ __forceinline__ int64_t ahead_of(int l) const {
+    int64_t n = 0;
+    for (int i = (int)(threadIdx.x & 31); i < s.B; i += 32) {
+      const int k = segments_of(s, q, w, i);
+      n += rising ? min(k, l) : max(k - l - 1, 0);
+    }
+    return warp_sum(n);
+  }
+  __device__ __forceinline__ bool next(int& b, int& seg, int& hk, int& part) {
+    const int lane = threadIdx.x & 31;
+    const int64_t per_head = segs * parts;
+    if (item >= per_head * s.Hkv) return false;
+    const int sec = (int)(item / (per_head * heads));
+    const int64_t in = item - sec * per_head * heads;
+    const int width = min(heads, s.Hkv - sec * heads);
+    const int64_t rank = in / (width * parts);
+    const int rest = (int)(in - rank * (width * parts));
+    hk = sec * heads + rest / parts;
+    part = rest % parts;
+    if (counter) {
+      item = (int64_t)grid + __shfl_sync(kFull, drawn, 0);
+      draw();  // (back before it is needed)
+    } else {
+      item = per_head * s.Hkv;
+    }
+    if (sec != section) {
+      section = sec;
+      set_level(rising ? 0 : most - 1);
+    }
+    if (rank >= upto) {
+      // places are looked through in their order, d steps behind this one: the last with no more than `rank` ahead
+      int l = 1, h = rising ? most - 1 - level : level;
+      while (l < h) {
+        const int m = (l + h + 1) >> 1;
+        if (ahead_of(rising ? level + m : level - m) <= rank) l = m; else h = m - 1;
+      }
+      set_level(rising ? level + l : level - l);
+    }
+    seg = level;
+    int r = (int)(rank - before);  // of the sequences that have this place
+    for (int c = 0; c < s.B; c += 32) {
+      const bool mine = segments_of(s, q, w, c + lane) > level;
+      const unsigned in_c = __ballot_sync(kFull, mine);
+      const int n = __popc(in_c);
+      if (r < n) {
+        const bool it = mine && __popc(in_c & ((1u << lane) - 1)) == r;
+        b = c + __ffs(__ballot_sync(kFull, it)) - 1;
+        break;
+      }
+      r -= n;
+    }
+    return true;
+  }
+  __device__ __forceinline__ void set_level(int l) {
+    level = l;
+    before = ahead_of(l);
+    upto = rising ? ahead_of(l + 1) : (l > 0 ? ahead_of(l - 1) : segs);
+  }
+};
+
 // A piece of work of a forward CTA: key blocks [k0, k0 + nb) for the tokens of a segment.
 struct Piece2 {
   int qtok;  // its first token in the packed axis,
@@ -107,49 +205,21 @@ struct Piece2 {
 struct PackedWalk {
   const PackedShape& s;
   const PackedPlan& p;
-  const PackedFwdArgs& a;
-  int b, lo;  // of the piece given out last: its sequence, and that one's first token
-  // direct
-  int64_t segs, ticket;  // segments of one key head; the next item
-  unsigned drawn;        // of the counter, for the item after it (lane 0)
-  int section, level, most;
-  int64_t at_level, above;  // segments of at least `level`, of more
-  // split
+  const PackedSeqs& q;
+  const bool in_order;
+  ItemQueue queue;  // direct
+  int b, lo;        // of the piece given out last: its sequence, and that one's first token
+  // split: the run's blocks, and its next piece: sequence, its segments, key head, segment, block in it
   int64_t g, g_end, run, begin;
   SeqInfo x;
-  int at, nseg, hk, pr, cut;  // the run's next piece: sequence, its segments, key head, segment, block in it
+  int at, nseg, hk, pr, cut;
 
-  __device__ __forceinline__ int segments(int b_) const {
-    const int n = b_ < s.B ? a.seqs.seq[b_ + 1] - a.seqs.seq[b_] : 0;
-    return n > 0 ? (n + p.w - 1) / p.w : 0;
-  }
-  // segments with at least `l` before them in their sequence
-  __device__ __forceinline__ int64_t segments_from(int l) const {
-    int64_t n = 0;
-    for (int i = (int)(threadIdx.x & 31); i < s.B; i += 32) {
-      const int k = segments(i);
-      n += k > l ? k - l : 0;
-    }
-    return warp_sum(n);
-  }
-
-  __device__ __forceinline__ PackedWalk(const PackedShape& s_, const PackedPlan& p_, const PackedFwdArgs& a_)
-      : s(s_), p(p_), a(a_), b(0), lo(0), segs(0), ticket(blockIdx.x), drawn(0), section(-1), level(0), most(0),
-        at_level(0), above(0), g(0), g_end(0), run(1), begin(0), at(0), nseg(0), hk(0), pr(0), cut(0) {
-    if (!seqs_in_order(s, a.seqs, blockIdx.x == 0, a.status)) return;
+  __device__ __forceinline__ PackedWalk(const PackedShape& s_, const PackedPlan& p_, const PackedFwdArgs& a)
+      : s(s_), p(p_), q(a.seqs), in_order(seqs_in_order(s_, a.seqs, blockIdx.x == 0, a.status)),
+        queue(s_, a.seqs, p_.w, 1, p_.heads, p_.grid, false, p_.tickets ? a.counter : nullptr, in_order && !p_.split),
+        b(0), lo(0), g(0), g_end(0), run(1), begin(0), at(0), nseg(0), hk(0), pr(0), cut(0) {
+    if (!in_order || !p.split) return;
     const int lane = threadIdx.x & 31;
-    if (!p.split) {
-      int64_t n = 0;
-      for (int i = lane; i < s.B; i += 32) {
-        const int k = segments(i);
-        n += k;
-        most = max(most, k);
-      }
-      segs = warp_sum(n);
-      most = __reduce_max_sync(kFull, most);
-      if (p.tickets) draw();
-      return;
-    }
     int64_t total = 0;
     for (int i = lane; i < s.B; i += 32) total += blocks_of(i);
     total = warp_sum(total);
@@ -171,8 +241,8 @@ struct PackedWalk {
       }
       off -= __shfl_sync(kFull, to, 31);
     }
-    x = seq_info(s, a.seqs, at);
-    nseg = segments(at);
+    x = seq_info(s, q, at);
+    nseg = segments_of(s, q, p.w, at);
     const int64_t per = blocks_before(s, x, p.w, nseg, nseg);
     hk = (int)(off / per);
     off -= hk * per;
@@ -185,63 +255,20 @@ struct PackedWalk {
     cut = (int)(off - blocks_before(s, x, p.w, nseg, pr));
   }
   __device__ __forceinline__ int64_t blocks_of(int b_) const {
-    const int n = segments(b_);
-    return n == 0 ? 0 : s.Hkv * blocks_before(s, seq_info(s, a.seqs, b_), p.w, n, n);
-  }
-  __device__ __forceinline__ void draw() {
-    if ((threadIdx.x & 31) == 0) drawn = atomicAdd(a.counter, 1u);
+    const int n = segments_of(s, q, p.w, b_);
+    return n == 0 ? 0 : s.Hkv * blocks_before(s, seq_info(s, q, b_), p.w, n, n);
   }
 
   __device__ __forceinline__ bool next(Piece2& y, CutRecord& rec) {
     return p.split ? next_of_run(y, rec) : next_item(y);
   }
-
   __device__ __forceinline__ bool next_item(Piece2& y) {
-    const int lane = threadIdx.x & 31;
-    if (ticket >= segs * s.Hkv) return false;
-    const int sec = (int)(ticket / (segs * p.heads));
-    const int64_t in = ticket - sec * segs * p.heads;
-    const int heads = min(p.heads, s.Hkv - sec * p.heads);
-    const int64_t rank = in / heads;  // segments of a section by falling level, then by sequence
-    y.hk = sec * p.heads + (int)(in - rank * heads);
-    if (p.tickets) {
-      ticket = (int64_t)p.grid + __shfl_sync(kFull, drawn, 0);
-      draw();  // (back before it is needed)
-    } else {
-      ticket = segs * s.Hkv;
-    }
-    if (sec != section) {
-      section = sec;
-      level = most - 1;
-      above = 0;
-      at_level = segments_from(level);
-    }
-    if (rank >= at_level) {
-      int l = 0, h = level - 1;  // the highest level with more than `rank` segments from it on
-      while (l < h) {
-        const int m = (l + h + 1) >> 1;
-        if (segments_from(m) > rank) l = m; else h = m - 1;
-      }
-      level = l;
-      at_level = segments_from(l);
-      above = segments_from(l + 1);
-    }
-    int r = (int)(rank - above);  // of the sequences that reach this level
-    for (int c = 0; c < s.B; c += 32) {
-      const bool mine = segments(c + lane) > level;
-      const unsigned in_c = __ballot_sync(kFull, mine);
-      const int n = __popc(in_c);
-      if (r < n) {
-        const bool it = mine && __popc(in_c & ((1u << lane) - 1)) == r;
-        b = c + __ffs(__ballot_sync(kFull, it)) - 1;
-        break;
-      }
-      r -= n;
-    }
-    const SeqInfo z = seq_info(s, a.seqs, b);
-    fill(y, z, level);
+    int seg, part;
+    if (!queue.next(b, seg, y.hk, part)) return false;
+    const SeqInfo z = seq_info(s, q, b);
+    fill(y, z, seg);
     y.k0 = 0;
-    y.nb = segment_blocks(s, z, p.w, level);
+    y.nb = segment_blocks(s, z, p.w, seg);
     y.slot = -1;
     return true;
   }
@@ -252,7 +279,6 @@ struct PackedWalk {
     y.ntok = z.n - seg * p.w;
     y.keys = z.keys;
   }
-
   __device__ __forceinline__ bool next_of_run(Piece2& y, CutRecord& rec) {
     if (g >= g_end) return false;
     const int n = segment_blocks(s, x, p.w, pr);
@@ -271,13 +297,30 @@ struct PackedWalk {
       pr = 0;
       if (++hk == s.Hkv) {
         hk = 0;
-        do ++at; while (segments(at) == 0);  // g < total: there is one
-        x = seq_info(s, a.seqs, at);
-        nseg = segments(at);
+        do ++at; while (segments_of(s, q, p.w, at) == 0);  // g < total: there is one
+        x = seq_info(s, q, at);
+        nseg = segments_of(s, q, p.w, at);
       }
     }
     return true;
   }
 };
+
+// Where a sequence's query tiles have their records: tile t of sequence b has record first_record + t of its
+// key head.  No two sequences share one, since lo / nb + b grows by at least the tiles of what lies between.
+__device__ __forceinline__ int first_record(int lo, int nb, int b) { return lo / nb + b; }
+// The last sequence whose first record (of runs of nb tokens) is at or before i; 32 of them looked at per step.
+__device__ __forceinline__ int sequence_of_record(const PackedShape& s, const PackedSeqs& q, int nb, int i) {
+  const int lane = threadIdx.x & 31;
+  int l = 0, h = s.B;
+  while (h - l > 1) {
+    const int step = (h - l + 31) >> 5, c = l + lane * step;
+    const unsigned m = __ballot_sync(kFull, c < h && first_record(q.seq[c], nb, c) <= i);
+    const int n = m ? 32 - __clz(m) : 1;  // (places in order: the lowest lanes)
+    l += (n - 1) * step;
+    h = min(h, l + step);
+  }
+  return l;
+}
 
 }  // namespace sa2

@@ -392,6 +392,14 @@ def packed_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq: torc
     return (_binding or load_binding()).packed_attn_fwd(q, k, v, seq, causal, scale, o, lse, ws, _handle(stream))
 
 
+def packed_attn_bwd(q, k, v, o, lse, do, seq: torch.Tensor, causal: bool = True, scale: Optional[float] = None,
+                    dq=None, dk=None, dv=None, ws: Optional[torch.Tensor] = None, stream=None):
+    """sa2_packed_attn_bwd: gradients (dQ, dK, dV) of packed_attn_fwd (bfloat16), whose o and lse on the same q, k,
+    v, seq, causal and scale it takes."""
+    return (_binding or load_binding()).packed_attn_bwd(q, k, v, o, lse, do, seq, causal, scale, dq, dk, dv, ws,
+                                                        _handle(stream))
+
+
 class PagedCache:
     """Keys and values in pages: k, v [pages, Hkv, page, d] (bfloat16 or float16, with the same strides), a
     power of two of tokens from 16 on in each page.  The caller keeps the lengths and hands out the pages: row b

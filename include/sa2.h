@@ -447,6 +447,28 @@ sa2_status sa2_packed_attn_fwd(const sa2_packed_shape* shape, const sa2_tensor* 
                                float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Bytes of device workspace sa2_packed_attn_bwd needs (0 for an invalid shape): counters, per-row
+ * statistics, and parts of dK and dV where there are few key blocks.  Depends on the current
+ * device's SM count.
+ */
+size_t sa2_packed_bwd_workspace_size(const sa2_packed_shape* shape);
+
+/*
+ * sa2_packed_attn_bwd -- backward of sa2_packed_attn_fwd (SA2_BF16), formulas and roundings as in
+ * sa2_cross_attn_bwd with P = 0 for keys that are masked.  No sum depends on scheduling.  As in
+ * the forward, a masked key counts for nothing whatever it holds, but tokens up to 127 apart
+ * share products: an infinity or NaN in one's k, v, q or dO may reach the other's gradients.
+ *   o, lse       from sa2_packed_attn_fwd on the same q, k, v, seq, causal and scale
+ *   dq, dk, dv   outputs: [H, T, d] and [Hkv, T, d]
+ *   ws           device workspace of at least sa2_packed_bwd_workspace_size(shape) bytes;
+ *                two calls that may run at the same time need one each
+ */
+sa2_status sa2_packed_attn_bwd(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
+                               const sa2_tensor* v, const sa2_tensor* o, const float* lse, const sa2_tensor* dO,
+                               const int32_t* seq, float scale, const sa2_tensor* dq, const sa2_tensor* dk,
+                               const sa2_tensor* dv, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * A cache in pages: keys and values [pages, Hkv, page, d] (k and v share type and strides;
  * stride_p from page to page), `page` tokens each, a power of two in [16, 65536].
  */
