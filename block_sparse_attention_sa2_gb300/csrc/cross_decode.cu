@@ -18,6 +18,7 @@
 // A piece's warps are joined in shared memory, pieces of a split segment by cross_join_kernel.
 #include <cuda_fp8.h>
 
+#include "cross_few.cuh"
 #include "cross_sched.cuh"
 #include "cross_softmax.cuh"
 
@@ -26,49 +27,13 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr int kTileBytes = 4096;  // of K, and of V, per step
+constexpr int kTileBytes = kFewTileBytes;
 constexpr int kStageBytes = 2 * kTileBytes;
-
-// 16 bytes from global to shared memory; zeros where !live (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ uint32_t f16x2_of(uint32_t e4m3x2) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(e4m3x2 & 0xFFFFu), __NV_E4M3);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-template <int D, bool KV8>
-struct Tile {
-  static constexpr int kRow = D * (KV8 ? 1 : 2);     // bytes of a key
-  static constexpr int kChunks = kRow / 16;          // 16-byte chunks of a key
-  static constexpr int kPer = KV8 ? 16 : 8;          // values per chunk
-  static constexpr int kKeys = kTileBytes / kRow;    // keys per step: 16, 32 or 64
-  // chunk c of key r, swizzled so that the fragments' reads (see the kernel) use all banks
-  static __device__ __forceinline__ uint32_t at(int r, int c) {
-    if constexpr (kChunks >= 8) return r * kRow + ((c ^ (r & 7)) << 4);
-    const int line = r >> 1;  // 64-byte rows: two to a line
-    return line * 128 + (((((r & 1) << 2) | c) ^ (line & 7)) << 4);
-  }
-};
 
 struct KvRef {
   const uint8_t *k, *v;
@@ -80,7 +45,7 @@ struct KvRef {
 // F16: the type of Q and O (and of K, V when they are 16-bit).
 template <int D, bool KV8, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(CrossShape s, FwdPlan plan, KvRef kv, CrossFwdArgs a) {
-  using T = Tile<D, KV8>;
+  using T = FewTile<D, KV8>;
   constexpr bool kMmaF16 = KV8 || F16;
   constexpr int kNT = T::kKeys / 8;   // 8-key tiles of S per step
   constexpr int kCT = D / 8;          // 8-channel tiles of O

@@ -65,7 +65,7 @@ sa2_status paged_shape(const sa2_paged_cache* c, int width, int max_new, PackedS
 }
 
 // What the two forward calls share behind their keys: q, o, lse, the plan and its workspace.
-sa2_status run_fwd(const PackedShape& s, const sa2_tensor* q, const TokenRef& k, const TokenRef& v, const PackedSeqs& seqs,
+sa2_status run_fwd(PackedShape& s, const sa2_tensor* q, const TokenRef& k, const TokenRef& v, const PackedSeqs& seqs,
                    float scale, const sa2_tensor* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
   if (!lse || !seqs.seq || !std::isfinite(scale)) return SA2_ERR_INVALID_ARG;
   PackedFwdArgs a{};
@@ -74,27 +74,24 @@ sa2_status run_fwd(const PackedShape& s, const sa2_tensor* q, const TokenRef& k,
   if (st == SA2_OK) st = check_tensor(o, 1, s.H, s.G, s.T, s.d, 2, &a.o);
   if (st != SA2_OK) return st;
   if (misaligned4(lse) || misaligned4(seqs.seq) || misaligned4(seqs.kv_len) || !aligned16(ws)) return SA2_ERR_ALIGNMENT;
-  const PackedPlan p = packed_fwd_plan(s, sm_count());
-  const size_t need = packed_fwd_bytes(s, p);
+  const PackedPlan p = packed_fwd_plan(&s, sm_count());
+  const size_t need = packed_fwd_bytes(s, p, ws, &a);
   if (need && (!ws || ws_bytes < need)) return SA2_ERR_WORKSPACE;
   a.seqs = seqs;
+  a.q = qr;
+  a.k = k;
+  a.v = v;
   a.lse = lse;
-  a.counter = static_cast<unsigned*>(ws);
-  a.rec = static_cast<int*>(ws);
-  if (p.split) {
-    a.part_l = reinterpret_cast<float*>(static_cast<char*>(ws) + (size_t)p.grid * sizeof(CutRecord));
-    a.part_o = a.part_l + (size_t)2 * p.grid * 256;
-  }
   const float sc = scale > 0.f ? scale : (float)(1.0 / std::sqrt((double)s.d));
   a.scale_log2 = sc * 1.4426950408889634f;
   a.status = status_word();
-  CUtensorMap mq, mk, mv, mo;
+  CUtensorMap mq{}, mk{}, mv{}, mo{};
   const bool f16 = s.dtype == SA2_FP16;
   const int box = s.page ? s.box : kKeyBlock, tokens = s.page ? s.page : s.T, outer = s.page ? s.pages : 1;
-  if (!make_group_map(&mq, qr, 1, s.H, s.G, s.T, s.d, s.G, p.nb, f16) ||
-      !make_group_map(&mo, a.o, 1, s.H, s.G, s.T, s.d, s.G, p.nb, f16) ||
-      !make_group_map(&mk, k, outer, s.Hkv, 1, tokens, s.d, 1, box, f16) ||
-      !make_group_map(&mv, v, outer, s.Hkv, 1, tokens, s.d, 1, box, f16))
+  if (p.tiles && (!make_group_map(&mq, qr, 1, s.H, s.G, s.T, s.d, s.G, p.nb, f16) ||
+                  !make_group_map(&mo, a.o, 1, s.H, s.G, s.T, s.d, s.G, p.nb, f16) ||
+                  !make_group_map(&mk, k, outer, s.Hkv, 1, tokens, s.d, 1, box, f16) ||
+                  !make_group_map(&mv, v, outer, s.Hkv, 1, tokens, s.d, 1, box, f16)))
     return SA2_ERR_CUDA;
   return cuda_status(launch_packed_fwd(s, p, mq, mk, mv, mo, a, static_cast<cudaStream_t>(stream)));
 }
@@ -105,7 +102,9 @@ extern "C" {
 
 size_t sa2_packed_fwd_workspace_size(const sa2_packed_shape* shape) {
   PackedShape s;
-  return check_packed(shape, &s) == SA2_OK ? packed_fwd_bytes(s, packed_fwd_plan(s, sm_count())) : 0;
+  if (check_packed(shape, &s) != SA2_OK) return 0;
+  const PackedPlan p = packed_fwd_plan(&s, sm_count());
+  return packed_fwd_bytes(s, p);
 }
 
 sa2_status sa2_packed_attn_fwd(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_tensor* k,
@@ -202,7 +201,8 @@ size_t sa2_paged_attn_workspace_size(const sa2_packed_shape* shape, const sa2_pa
   if (check_packed(shape, &s) != SA2_OK || check_pages(cache, &k, &v) != SA2_OK ||
       paged_shape(cache, width, max_new, &s) != SA2_OK)
     return 0;
-  return packed_fwd_bytes(s, packed_fwd_plan(s, sm_count()));
+  const PackedPlan p = packed_fwd_plan(&s, sm_count());
+  return packed_fwd_bytes(s, p);
 }
 
 sa2_status sa2_paged_attn(const sa2_packed_shape* shape, const sa2_tensor* q, const sa2_paged_cache* cache,

@@ -985,9 +985,7 @@ PackedBwdPlan packed_bwd_plan(const PackedShape& s, int sms) {
   p.parts = (int)std::max<int64_t>(1, std::min<int64_t>((2 * sms + blocks - 1) / blocks, mean_tiles / 2));
   p.grid = (int)std::min<int64_t>(sms, blocks * p.parts);
   p.dq_grid = (int)std::min<int64_t>(sms, tiles);
-  // Q, dO, K and V of the heads of a section take a third of L2 at most
-  const int64_t head_bytes = (int64_t)s.T * s.d * 4 * (s.G + 1);
-  p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(s.Hkv, (40ll << 20) / head_bytes));
+  p.heads = section_heads(s, s.G + 1);
   return p;
 }
 

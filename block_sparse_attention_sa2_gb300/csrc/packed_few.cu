@@ -1,0 +1,408 @@
+// Attention of few new tokens' rows (at most 16 per key head of a sequence: a single token of up to 16 heads that share
+// a key head, or several of fewer) to the keys and values that a paged cache holds of their sequence, on sm_103a.
+//
+// Every key and value is used for 16 rows at most, so the bytes bound it.  The products, rings and roundings are those of
+// cross_decode.cu: a CTA of 8 warps per SM, each with its own steps of 4 KB of K and of V, copied three steps deep by
+// cp.async, on mma.sync m16n8k16 (a tcgen05 tile would be an eighth full at most).  Here a step's place comes from the
+// table: each lane holds the page of one of the warp's next 32 steps, read a whole round ahead.  A row sees the keys
+// up to its token's position.
+#include <algorithm>
+
+#include "cross_few.cuh"
+#include "cross_softmax.cuh"
+#include "packed_sched.cuh"
+
+namespace sa2 {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr int kStageBytes = 2 * kFewTileBytes;
+
+struct FewPiece {
+  int b, qtok, pos, n;  // sequence, its first new token, that token's position, new tokens
+  int keys, k0, nb;     // of the sequence; 64-key blocks [k0, k0 + nb)
+  int hk, slot;         // key head (-1: no work left), slot of the partial results (-1: whole)
+};
+
+// The order of work, walked by one warp: segments (sequence, key head) of sequences with few tokens; see PackedPlan.
+struct FewWalk {
+  const PackedShape& s;
+  const PackedSeqs& q;
+  const int lane;
+  bool whole;
+  int64_t g, g_end, run, begin;  // whole: the segment; else blocks
+  int at, nblk, hk, cut;
+
+  __device__ __forceinline__ int blocks(int b) const {  // 0: not a sequence of this kernel
+    const int n = b < s.B ? q.seq[b + 1] - q.seq[b] : 0;
+    if (n < 1 || n > s.few) return 0;
+    const int k = key_blocks(seq_info(s, q, b).keys, 6);
+    return k > 0 ? k : 1;
+  }
+  __device__ __forceinline__ FewWalk(const PackedShape& s_, const PackedSeqs& q_, unsigned* status)
+      : s(s_), q(q_), lane(threadIdx.x & 31), whole(false), g(0), g_end(0), run(1), begin(0), at(0), nblk(0), hk(0), cut(0) {
+    if (!seqs_in_order(s, q, blockIdx.x == 0, status)) return;
+    int64_t total = 0, segs = 0;
+    int most = 0;
+    for (int b = lane; b < s.B; b += 32) {
+      const int k = blocks(b);
+      total += k;
+      segs += k > 0;
+      most = max(most, k);
+    }
+    total = warp_sum(total) * s.Hkv;
+    segs = warp_sum(segs) * s.Hkv;
+    most = __reduce_max_sync(kFull, most);
+    whole = segs <= (int64_t)gridDim.x && most <= kFewWhole;
+    int64_t off;
+    if (whole) {
+      g = begin = blockIdx.x;
+      g_end = g < segs ? g + 1 : g;
+      off = g / s.Hkv;
+      hk = (int)(g - off * s.Hkv);
+    } else {
+      run = run_length(total, gridDim.x);
+      g = begin = run * blockIdx.x;
+      g_end = g + run < total ? g + run : total;
+      off = g;
+    }
+    if (g >= g_end) return;
+    // the sequence: whole, the off-th of this kernel; else that of block off
+    for (int c = 0;; c += 32) {  // (found)
+      const int k = blocks(c + lane);
+      const int64_t mine = whole ? (k > 0) : (int64_t)k * s.Hkv, to = warp_scan(mine);
+      const unsigned in = __ballot_sync(kFull, off < to);
+      if (in) {
+        const int src = __ffs(in) - 1;
+        at = c + src;
+        nblk = __shfl_sync(kFull, k, src);
+        off -= __shfl_sync(kFull, to - mine, src);
+        break;
+      }
+      off -= __shfl_sync(kFull, to, 31);
+    }
+    if (!whole) {
+      hk = (int)(off / nblk);
+      cut = (int)(off - (int64_t)hk * nblk);
+    }
+  }
+  __device__ __forceinline__ bool next(FewPiece& y, CutRecord& rec) {
+    if (g >= g_end) return false;
+    const SeqInfo x = seq_info(s, q, at);
+    y.b = at;
+    y.qtok = x.lo;
+    y.pos = x.pos;
+    y.n = x.n;
+    y.keys = x.keys;
+    y.hk = hk;
+    y.k0 = cut;
+    if (whole) {
+      y.nb = nblk;
+      y.slot = -1;
+      g = g_end;
+      return true;
+    }
+    const int64_t left = g_end - g;
+    y.nb = nblk - cut < left ? nblk - cut : (int)left;
+    y.slot = y.nb == nblk ? -1 : 2 * (int)blockIdx.x + (g == begin ? 0 : 1);
+    if (cut == 0 && y.nb < nblk)
+      rec = {(int)((g + nblk - 1) / run) - (int)blockIdx.x + 1, y.slot, y.qtok, y.n, hk, 0, 0, 0};
+    g += y.nb;
+    cut = 0;
+    if (g < g_end && ++hk == s.Hkv) {
+      hk = 0;
+      do ++at; while (blocks(at) == 0);  // g < total: there is one
+      nblk = blocks(at);
+    }
+    return true;
+  }
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_few_kernel(const __grid_constant__ PackedShape s, const __grid_constant__ PackedPlan plan,
+                      const __grid_constant__ PackedFwdArgs a) {
+  using T = FewTile<D, false>;
+  constexpr int kNT = T::kKeys / 8;   // 8-key tiles of S per step
+  constexpr int kCT = D / 8;          // 8-channel tiles of O
+  constexpr int kKS = D / 16;         // k-steps of S
+  constexpr int kKC = T::kChunks / 4;  // K chunks per thread and key
+  constexpr int kIds = T::kKeys / 16;  // places in the table that a step can touch
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float warp_m[kWarps][kFewRows], warp_l[kWarps][kFewRows];
+  __shared__ FewPiece piece;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * kStages * kStageBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  if (plan.tiles || a.few.grid) kernel_trigger();  // another kernel of the call follows
+  const int page_shift = __ffs(s.page) - 1;
+
+  FewWalk walk(s, a.seqs, a.status);  // (walked on by warp 0)
+  CutRecord rec{0, 0, 0, 0, 0, 0, 0, 0};
+  for (;;) {
+    if (warp == 0) {
+      FewPiece y;
+      if (!walk.next(y, rec)) y.hk = -1;
+      if (lane == 0) piece = y;
+    }
+    __syncthreads();
+    const FewPiece x = piece;
+    if (x.hk < 0) break;
+    const int rows = x.n * s.G;
+    const int key0 = x.k0 << 6, key1 = min(x.keys, (x.k0 + x.nb) << 6);
+    const uint16_t* kp = static_cast<const uint16_t*>(a.k.p) + x.hk * a.k.sh;
+    const uint16_t* vp = static_cast<const uint16_t*>(a.v.p) + x.hk * a.v.sh;
+    const int32_t* row = a.seqs.table + x.b * s.table_stride;
+    // step i of this warp: keys from key0 + (i * kWarps + warp) * kKeys on
+    const int steps_all = (key1 - key0 + T::kKeys - 1) / T::kKeys;
+    const int steps = steps_all > warp ? (steps_all - warp + kWarps - 1) / kWarps : 0;
+    // the pages of steps 32 j + lane: of their first 16 keys, and of their second (d = 64), -1 where there are none
+    int ids[2], next_ids[2];
+    auto look_up = [&](int i, int (&id)[2]) {
+#pragma unroll
+      for (int p = 0; p < kIds; ++p) {
+        const int key = key0 + (i * kWarps + warp) * T::kKeys + 16 * p;
+        id[p] = -1;
+        if (i < steps && key < key1) {
+          id[p] = row[key >> page_shift];
+          if (id[p] < 0 || id[p] >= s.pages) {
+            report_error(a.status, kDevErrBounds);
+            id[p] = -1;  // reads as zeros
+          }
+        }
+      }
+    };
+    look_up(lane, next_ids);
+    auto copy_step = [&](int i) {
+      if ((i & 31) == 0) {  // (every warp comes here for each of its steps in turn)
+#pragma unroll
+        for (int p = 0; p < kIds; ++p) ids[p] = next_ids[p];
+        look_up(i + 32 + lane, next_ids);
+      }
+      int id[kIds];
+#pragma unroll
+      for (int p = 0; p < kIds; ++p) id[p] = __shfl_sync(kFull, ids[p], i & 31);
+      if (i < steps) {
+        const uint32_t dst = ring_u + (i % kStages) * kStageBytes;
+        const int base = key0 + (i * kWarps + warp) * T::kKeys;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int c = (q * 32 + lane) % T::kChunks, r = (q * 32 + lane) / T::kChunks;
+          const int pid = id[q * kIds / 8];  // (rows of 16 keys: q 0..7, or 0..3 and 4..7)
+          const bool live = base + r < key1 && pid >= 0;
+          const int64_t slot = (base + r) & (s.page - 1), pg = live ? pid : 0;
+          copy16(dst + T::at(r, c), kp + pg * a.k.sb + slot * a.k.sn + c * 8, live);
+          copy16(dst + kFewTileBytes + T::at(r, c), vp + pg * a.v.sb + slot * a.v.sn + c * 8, live);
+        }
+      }
+      copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) copy_step(i);
+
+    // Q's fragments: rows g and g + 8; of each, this thread's channels in the order of its K chunks
+    uint32_t qf[kKS][4];
+    int lim[2];  // keys before which a row's keys end
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = g + 8 * hf, n = r / s.G, h = x.hk * s.G + r - n * s.G;
+      const bool live = r < rows;
+      lim[hf] = s.causal && live ? min(key1, x.pos + n + 1) : key1;
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q.p) + h * a.q.sh + (int64_t)(x.qtok + n) * a.q.sn;
+      uint32_t w[2 * kKS];
+#pragma unroll
+      for (int i = 0; i < 2 * kKS; ++i) {  // pair i: values 2 i, 2 i + 1 of the thread's list
+        const int pos = 2 * i, ci = pos / T::kPer;
+        const int c = 2 * t + (ci & 1) + 8 * (ci >> 1);
+        w[i] = live ? *reinterpret_cast<const uint32_t*>(qp + c * T::kPer + pos % T::kPer) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kKS; ++k) {
+        qf[k][hf] = w[2 * k];
+        qf[k][2 + hf] = w[2 * k + 1];
+      }
+    }
+
+    float o[kCT][4] = {};
+    float m_used[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // reference of the exponentials; sum of exp2(s) relative to it
+    const float mul = a.scale_log2;
+    for (int i = 0; i < steps; ++i) {
+      copy_step(i + kStages - 1);
+      copy_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* kt = ring + (i % kStages) * kStageBytes;
+      const uint8_t* vt = kt + kFewTileBytes;
+      const int base = key0 + (i * kWarps + warp) * T::kKeys;
+      // S: tile j has keys 8 j .. 8 j + 7; thread: rows g, g + 8, keys 8 j + 2 t, + 1
+      float sc[kNT][4];
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) {
+        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+        uint32_t w[4 * kKC];
+#pragma unroll
+        for (int c = 0; c < kKC; ++c) {
+          const int ch = 2 * t + (c & 1) + 8 * (c >> 1);
+          const uint4 u = *reinterpret_cast<const uint4*>(kt + T::at(8 * j + g, ch));
+          w[4 * c] = u.x;
+          w[4 * c + 1] = u.y;
+          w[4 * c + 2] = u.z;
+          w[4 * c + 3] = u.w;
+        }
+#pragma unroll
+        for (int k = 0; k < kKS; ++k) mma16816<F16>(sc[j], qf[k], w[2 * k], w[2 * k + 1]);
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (base + 8 * j + 2 * t + (q & 1) >= lim[q >> 1]) sc[j][q] = -INFINITY;
+          mx[q >> 1] = fmaxf(mx[q >> 1], sc[j][q]);
+        }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        mx[hf] *= mul;
+        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(kFull, mx[hf], 1));
+        mx[hf] = fmaxf(mx[hf], __shfl_xor_sync(kFull, mx[hf], 2));
+      }
+      if (i == 0) {
+        m_used[0] = fmaxf(mx[0], kLeastRef);
+        m_used[1] = fmaxf(mx[1], kLeastRef);
+      } else if (__any_sync(kFull, mx[0] > m_used[0] + kRescaleThreshold || mx[1] > m_used[1] + kRescaleThreshold)) {
+        float al[2];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          // (a row's reference follows from its own scores only)
+          const float m = mx[hf] > m_used[hf] + kRescaleThreshold ? mx[hf] : m_used[hf];
+          al[hf] = m == m_used[hf] ? 1.f : ex2(m_used[hf] - m);
+          l[hf] *= al[hf];
+          m_used[hf] = m;
+        }
+#pragma unroll
+        for (int c = 0; c < kCT; ++c) {
+          o[c][0] *= al[0];
+          o[c][1] *= al[0];
+          o[c][2] *= al[1];
+          o[c][3] *= al[1];
+        }
+      }
+      // P in the layout of an A operand: 16 keys (tiles 2 k, 2 k + 1) per k-step
+      uint32_t pf[kNT / 2][4];
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) {
+        float p[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          p[q] = ex2(fmaf(sc[j][q], mul, -m_used[q >> 1]));
+          l[q >> 1] += p[q];
+        }
+        pf[j >> 1][2 * (j & 1)] = F16 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]);
+        pf[j >> 1][2 * (j & 1) + 1] = F16 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]);
+      }
+      // O += P V: keys 16 k + 2 t, + 1 and 16 k + 8 + 2 t, + 1; channels of chunk g (+ 8 i)
+#pragma unroll
+      for (int k = 0; k < kNT / 2; ++k) {
+#pragma unroll
+        for (int i8 = 0; i8 < D / 64; ++i8) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = 16 * k + 2 * t + (q & 1) + 8 * (q >> 1);
+            *reinterpret_cast<uint4*>(v[q]) = *reinterpret_cast<const uint4*>(vt + T::at(r, g + 8 * i8));
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            mma16816<F16>(o[8 * i8 + 2 * w], pf[k], __byte_perm(v[0][w], v[1][w], 0x5410),
+                          __byte_perm(v[2][w], v[3][w], 0x5410));
+            mma16816<F16>(o[8 * i8 + 2 * w + 1], pf[k], __byte_perm(v[0][w], v[1][w], 0x7632),
+                          __byte_perm(v[2][w], v[3][w], 0x7632));
+          }
+        }
+      }
+      __syncwarp();  // the step's stage is read before its next copy
+    }
+    // ---- join the warps: O relative to the largest of their references
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      l[hf] += __shfl_xor_sync(kFull, l[hf], 1);
+      l[hf] += __shfl_xor_sync(kFull, l[hf], 2);
+      if (t == 0) {
+        warp_m[warp][g + 8 * hf] = steps > 0 ? m_used[hf] : -INFINITY;
+        warp_l[warp][g + 8 * hf] = steps > 0 ? l[hf] : 0.f;
+      }
+    }
+    copy_wait<0>();
+    __syncthreads();  // every ring is read: it holds the warps' O now, [warp][row][channel]
+    float* os = reinterpret_cast<float*>(smem);
+    constexpr int kPitch = D + 4;
+    if (steps > 0) {
+#pragma unroll
+      for (int c = 0; c < kCT; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = g + 8 * (q >> 1), n = 2 * t + (q & 1);
+          // channel tile c: value c % 8 of chunk n + 8 (c / 8)
+          os[(warp * kFewRows + r) * kPitch + (n + 8 * (c / 8)) * 8 + c % 8] = o[c][q];
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 2); i += kThreads) {
+      const int r = i / (D / 2), ch = i % (D / 2) * 2;
+      float m = -INFINITY;
+      bool nan = false;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        nan |= warp_m[w][r] != warp_m[w][r];
+        m = fmaxf(m, warp_m[w][r]);
+      }
+      if (nan) m = NAN;
+      float v0 = 0.f, v1 = 0.f, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (warp_m[w][r] == -INFINITY) continue;  // no keys
+        const float f = ex2(warp_m[w][r] - m);
+        const float2 u = *reinterpret_cast<const float2*>(os + (w * kFewRows + r) * kPitch + ch);
+        v0 = fmaf(f, u.x, v0);
+        v1 = fmaf(f, u.y, v1);
+        sum = fmaf(f, warp_l[w][r], sum);
+      }
+      const float inv = inverse_sum(sum);  // (0: no keys, or no score above -inf)
+      const float lse2 = sum == 0.f ? -INFINITY : m + __log2f(sum);
+      const int n = r / s.G, h = x.hk * s.G + r - n * s.G;
+      if (x.slot >= 0) {
+        const int64_t pr = (int64_t)x.slot * kFewRows + r;
+        *reinterpret_cast<float2*>(a.few.o + pr * D + ch) = make_float2(v0 * inv, v1 * inv);
+        if (ch == 0) a.few.l[pr] = lse2;
+      } else {
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o.p) + h * a.o.sh + (int64_t)(x.qtok + n) * a.o.sn + ch) =
+            F16 ? pack_f16x2(v0 * inv, v1 * inv) : pack_bf16x2(v0 * inv, v1 * inv);
+        if (ch == 0) a.lse[(int64_t)h * s.T + x.qtok + n] = lse2 * 0.69314718055994531f;
+      }
+    }
+    __syncthreads();  // before the next piece's copies
+  }
+  if (plan.few_split && tid == 0) a.few.rec[blockIdx.x] = rec;
+}
+
+template <int D, bool F16>
+cudaError_t launch_t(const PackedShape& s, const PackedPlan& p, const PackedFwdArgs& a, cudaStream_t st) {
+  constexpr int kBytes = kWarps * kStages * kStageBytes;
+  static_assert(kWarps * kFewRows * (D + 4) * 4 <= kBytes && kBytes + 2048 <= (int)kMaxDynSmem, "shared memory");
+  auto kern = packed_few_kernel<D, F16>;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem(kern, kBytes, allowed);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)p.few_grid, kThreads, kBytes, st>>>(s, p, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_few(const PackedShape& s, const PackedPlan& p, const PackedFwdArgs& a, cudaStream_t st) {
+  const bool f16 = s.dtype == SA2_FP16;
+  if (s.d == 128) return f16 ? launch_t<128, true>(s, p, a, st) : launch_t<128, false>(s, p, a, st);
+  return f16 ? launch_t<64, true>(s, p, a, st) : launch_t<64, false>(s, p, a, st);
+}
+
+}  // namespace sa2

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (plan.split) kernel_trigger();
+  if (a.tile.grid + a.few.grid) kernel_trigger();  // a join follows
   const int nb = plan.nb;
 
   // The n-th piece, for every warp but 0; false where there is none.
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
     }
     if (lane == 0) {
-      if (plan.split) reinterpret_cast<CutRecord*>(a.rec)[blockIdx.x] = rec;
+      if (plan.split) a.tile.rec[blockIdx.x] = rec;
       // No copy may still be in flight when the CTA exits: each stage's last load, each tile's Q.
       for (uint32_t v = r > (uint32_t)kStages ? r - kStages : 0; v < r; ++v)
         mbar_drain(bar_full(v % kStages), (v / kStages) & 1, abort_flag);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_valid = tok_r < nb && tok < x.ntok;
       const int keys = tile_keys(x, t);
       float* lse = x.slot < 0 ? a.lse + (int64_t)(x.hk * s.G + g) * s.T + x.qtok + tok
-                              : a.part_l + (int64_t)x.slot * 256 + t * 128 + r;
+                              : a.tile.l + (int64_t)x.slot * kTileRows + t * 128 + r;
       if (keys <= 0) {
         if (row_valid) *lse = -INFINITY;
         continue;
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++pc[t];
         tc_fence_after();
         const float inv_l = row_s[t * 128 + r];
-        float* po = a.part_o + ((int64_t)x.slot * 256 + t * 128 + r) * D;
+        float* po = a.tile.o + ((int64_t)x.slot * kTileRows + t * 128 + r) * D;
         uint8_t* st_row = smem + L::kOffO + r * 128;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -532,31 +532,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  kernel_wait();  // for the kernel for few rows, whose parts the join reads too
 }
 
 // Joins the parts of segments that were cut: O = sum_i 2^(l_i - m) O_i / sum_i 2^(l_i - m) over a segment's
 // parts in key order, l_i their log2 sums and m the largest; LSE = ln 2 (m + log2 sum).  Parts in which a
-// row has no keys (l_i = -inf) are left out.  One warp per row; grid (CTAs of the first kernel, parts of a
-// segment's rows); most CTAs find nothing to do.
+// row has no keys (l_i = -inf) are left out.  One warp per row; grid (CTAs of the kernel of tiles and of that for few
+// rows, parts of a segment's rows); most CTAs find nothing to do.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant__ PackedShape s,
                                                          const __grid_constant__ PackedPlan plan,
                                                          const __grid_constant__ PackedFwdArgs a) {
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool few = (int)blockIdx.x >= a.tile.grid;
+  const Parts& parts = few ? a.few : a.tile;
+  const int cta = few ? (int)blockIdx.x - a.tile.grid : (int)blockIdx.x;
+  if ((int)blockIdx.y * plan.join_rows >= parts.rows) return;
   kernel_wait();
-  const CutRecord x = reinterpret_cast<const CutRecord*>(a.rec)[blockIdx.x];
+  const CutRecord x = parts.rec[cta];
   if (x.parts == 0) return;
   for (int i = warp; i < plan.join_rows; i += 8) {
     const int rr = blockIdx.y * plan.join_rows + i, t = rr >> 7, r = rr & 127;
     const int tok_r = r / s.G, g = r - tok_r * s.G, tok = t * plan.nb + tok_r, h = x.hk * s.G + g;
-    if (t >= plan.tp || tok_r >= plan.nb || tok >= x.ntok) continue;
-    auto slot_row = [&](int k) { return (int64_t)(k == 0 ? x.slot : 2 * ((int)blockIdx.x + k)) * 256 + rr; };
+    if (rr >= parts.rows || t >= plan.tp || tok_r >= plan.nb || tok >= x.ntok) continue;
+    auto slot_row = [&](int k) { return (int64_t)(k == 0 ? x.slot : 2 * (cta + k)) * parts.rows + rr; };
     // lane i has part i's sum; 32 parts at a time, eight of their rows in flight
     float m = kLeastRef, acc[kPer] = {}, l = 0.f;
     for (int base = 0; base < x.parts; base += 32) {
       const int n32 = min(32, x.parts - base);
-      const float mine = lane < n32 ? a.part_l[slot_row(base + lane)] : -INFINITY;
+      const float mine = lane < n32 ? parts.l[slot_row(base + lane)] : -INFINITY;
       float mx = mine;
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
       if (__any_sync(kFull, mine != mine)) mx = NAN;
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant_
             for (int q = 0; q < kPer; ++q) v[u][q] = 0.f;
             continue;
           }
-          const float* src = a.part_o + slot_row(base + k + u) * D;
+          const float* src = parts.o + slot_row(base + k + u) * D;
           if constexpr (kPer == 4)
             *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src + lane * 4);
           else
@@ -615,46 +620,84 @@ cudaError_t launch_t(const PackedShape& s, const PackedPlan& p, const CUtensorMa
   if (e == cudaSuccess && p.tickets) e = cudaMemsetAsync(a.counter, 0, sizeof(unsigned), st);
   if (e != cudaSuccess) return e;
   prof_start(st, kAttnFwd);
-  kern<<<(unsigned)p.grid, kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv, mo, s, p, a);
-  e = cudaGetLastError();
-  if (e == cudaSuccess && p.split)
-    e = launch_early(packed_join_kernel<D, F16>, dim3((unsigned)p.grid, (unsigned)(p.tp * 128 / p.join_rows)), 256, 0,
-                     st, s, p, a);
+  if (p.few_grid) e = launch_packed_few(s, p, a, st);
+  // (beside the one for few rows, whose outputs are other rows; it waits for it at its end)
+  if (e == cudaSuccess && p.tiles && p.few_grid)
+    e = launch_early(kern, dim3((unsigned)p.grid), kThreads, Smem<D>::kBytes, st, mq, mk, mv, mo, s, p, a);
+  else if (e == cudaSuccess && p.tiles) {
+    kern<<<(unsigned)p.grid, kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv, mo, s, p, a);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && a.tile.grid + a.few.grid)
+    e = launch_early(packed_join_kernel<D, F16>,
+                     dim3((unsigned)(a.tile.grid + a.few.grid), (unsigned)((a.tile.grid ? p.tp * 128 : kFewRows) / p.join_rows)),
+                     256, 0, st, s, p, a);
   prof_stop(st, kAttnFwd);
   return e;
 }
 
 }  // namespace
 
-// Split where the segments that there can be do not fill the SMs four times over (whole ones then even out by
-// the order in which they are taken) and their keys are eight blocks or more (the join would cost what the
-// split gains); of packed sequences, whose lengths the host does not know, by their mean.
-PackedPlan packed_fwd_plan(const PackedShape& s, int sms) {
+// Split where the segments that there can be would leave more than a tenth of the SMs' time unused as whole ones
+// (fewer than the SMs, or a last round that is not full; from four rounds on they even out by the order in which they are
+// taken) and their keys are eight blocks or more (the join would cost what the split gains); of packed sequences, whose
+// lengths the host does not know, by their mean.  Whole segments of one key head run side by side and read its keys from
+// L2 (40 heads x 3600 over 75600, d = 128, 3.95 rounds: split 4120 us at 5.6 TB/s of keys from memory).
+PackedPlan packed_fwd_plan(PackedShape* shape, int sms) {
+  PackedShape& s = *shape;
   PackedPlan p{};
+  p.join_rows = 16;
+  p.tp = 1;
   p.nb = 128 / s.G;
   const int64_t most_keys = s.page ? (int64_t)s.width * s.page : s.T / s.B;
+  // One sequence alone has a kernel to itself: that of tiles, unless its tokens are known to be few.
+  if (s.page && s.G <= kFewRows && (s.B > 1 || (int64_t)s.max_new * s.G <= kFewRows)) {
+    s.few = kFewRows / s.G;
+    const int64_t segs = (int64_t)s.Hkv * std::min(s.B, s.T), blocks = (most_keys + 63) / 64;
+    p.few_grid = (int)std::min<int64_t>(sms, segs * blocks);
+    p.few_split = segs > p.few_grid || blocks > kFewWhole;
+  }
+  p.tiles = s.max_new > s.few;
+  if (!p.tiles) return p;
   const int64_t blocks = (most_keys + kKeyBlock - 1) / kKeyBlock;
-  const int64_t paired = s.Hkv * segment_bound(s, 2 * p.nb);
-  p.split = blocks >= 8 && paired < 4 * (int64_t)sms;
+  const int64_t paired = s.Hkv * segment_bound(s, 2 * p.nb), rounds = (paired + sms - 1) / sms;
+  p.split = blocks >= 8 && rounds <= 4 && 10 * paired < 9 * rounds * sms;
   // one tile per CTA while each finds an SM of its own, and where sequences have no second one
   p.tp = s.max_new <= p.nb || (!p.split && s.Hkv * segment_bound(s, p.nb) <= sms) ? 1 : 2;
   p.w = p.tp * p.nb;
   const int64_t items = s.Hkv * segment_bound(s, p.w);
-  const int64_t all_blocks = (s.page ? ((int64_t)s.width * s.page + kKeyBlock - 1) / kKeyBlock : (s.T + kKeyBlock - 1) / kKeyBlock);
+  const int64_t all_blocks = ((s.page ? (int64_t)s.width * s.page : s.T) + kKeyBlock - 1) / kKeyBlock;
   p.grid = (int)std::min<int64_t>(sms, p.split ? items * all_blocks : items);
   p.tickets = !p.split && items > p.grid;
-  // keys and values of the heads of a section take a third of L2 at most
-  const int64_t tokens = s.page ? std::min<int64_t>((int64_t)s.B * s.width, s.pages) * s.page : s.T;
-  const int64_t head_bytes = tokens * s.d * 4;
-  p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(s.Hkv, (40ll << 20) / head_bytes));
-  p.join_rows = 16;
+  p.heads = section_heads(s, 1);
   return p;
 }
 
-// The counter (and the records of the cut segments) first, then the parts.
-size_t packed_fwd_bytes(const PackedShape& s, const PackedPlan& p) {
-  if (!p.split) return p.tickets ? 256 : 0;
-  return (size_t)p.grid * sizeof(CutRecord) + (size_t)2 * p.grid * 256 * (s.d + 1) * sizeof(float);
+// The counter first, then the records and parts of both kernels.
+size_t packed_fwd_bytes(const PackedShape& s, const PackedPlan& p, void* ws, PackedFwdArgs* a) {
+  size_t at = 0;
+  char* base = static_cast<char*>(ws);
+  auto take = [&](size_t bytes) {
+    char* x = base + at;
+    at += (bytes + 255) & ~(size_t)255;
+    return x;
+  };
+  auto parts = [&](int grid, int rows, Parts* out) {
+    Parts x{};
+    x.grid = grid;
+    x.rows = rows;
+    x.rec = reinterpret_cast<CutRecord*>(take((size_t)grid * sizeof(CutRecord)));
+    x.l = reinterpret_cast<float*>(take((size_t)2 * grid * rows * sizeof(float)));
+    x.o = reinterpret_cast<float*>(take((size_t)2 * grid * rows * s.d * sizeof(float)));
+    if (out) *out = x;
+  };
+  if (p.tickets) {
+    char* x = take(sizeof(unsigned));
+    if (a) a->counter = reinterpret_cast<unsigned*>(x);
+  }
+  if (p.split) parts(p.grid, kTileRows, a ? &a->tile : nullptr);
+  if (p.few_split) parts(p.few_grid, kFewRows, a ? &a->few : nullptr);
+  return at;
 }
 
 cudaError_t launch_packed_fwd(const PackedShape& s, const PackedPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,

@@ -16,6 +16,7 @@ struct PackedShape {
   int page, box;     // tokens of a page and of a box of its tensor map (min(page, 128))
   int pages, width;  // pages in all; columns of the table
   int max_new;       // no sequence has more new tokens (T where the caller did not say)
+  int few;           // sequences of so many tokens or fewer are left to the kernel for few rows (0: none)
   int64_t table_stride;
   unsigned long long wait_ns, stall_ns;
 };
@@ -37,7 +38,14 @@ struct PackedSeqs {
 //           that falls into one run is written at once; of one that is cut each part leaves its O and
 //           log2 sum in a slot, 2 * CTA for one that the run begins with and 2 * CTA + 1 for one that
 //           it ends with, and a second kernel joins them in key order.
+//
+// Over a paged cache, sequences whose new tokens' rows are at most kFewRows (single tokens) go to a kernel of their
+// own, packed_few.cu: a tile of 128 rows would be nearly empty.  It cuts the 64-key blocks of their segments (one for
+// each key head) into equal runs too, or, where there are no more segments than CTAs and none is long, takes them whole.
 struct PackedPlan {
+  int few_grid;    // CTAs of the kernel for few rows; 0: not launched
+  int few_split;   // its segments may be cut
+  int tiles;       // the kernel of query tiles is launched
   int nb, tp, w;
   int grid;
   int split;
@@ -46,22 +54,31 @@ struct PackedPlan {
   int join_rows;
 };
 
-struct PackedFwdArgs {
-  PackedSeqs seqs;
-  TokenRef o;
-  float* lse;          // [H, T]
-  unsigned* counter;   // direct with tickets
-  int* rec;            // split: [grid][8], see CutRecord
-  float* part_o;       // split: [2 * grid][256][d]
-  float* part_l;       // split: [2 * grid][256], log2 units
-  float scale_log2;
-  unsigned* status;
-};
-
 // The segment that a CTA's run ends in, where the runs behind it have the rest: read by the join.
 struct CutRecord {
   int parts, slot, qtok, ntok, hk, pad0, pad1, pad2;
 };
+
+// What a kernel that cuts segments leaves for the join: a record for each CTA, and two slots for each of `rows` rows.
+struct Parts {
+  CutRecord* rec;  // [grid]
+  float* l;        // [2 * grid][rows], log2 units
+  float* o;        // [2 * grid][rows][d]
+  int grid, rows;  // grid = 0: none
+};
+
+struct PackedFwdArgs {
+  PackedSeqs seqs;
+  TokenRef q, k, v;    // for the kernel for few rows (the other one has tensor maps); k, v: the pages
+  TokenRef o;
+  float* lse;          // [H, T]
+  unsigned* counter;   // direct with tickets
+  Parts tile, few;
+  float scale_log2;
+  unsigned* status;
+};
+constexpr int kTileRows = 256;  // of a segment's two tiles
+constexpr int kFewWhole = 16;   // blocks of 64 keys up to which the few-row kernel leaves segments whole
 
 // Upper bound of the segments of w tokens of one key head: sum ceil(n_b / w) <= (T + B (w - 1)) / w.
 inline int64_t segment_bound(const PackedShape& s, int w) {
@@ -95,14 +112,25 @@ struct PackedBwdArgs {
   unsigned* status;
 };
 
+// Key heads of a section: as many as fit a third of L2 with all that is read of them again (pairs of tensors of
+// `tensors` heads' tokens for each), but at least 16, of which each has nine CTAs or more at work that read the same.
+inline int section_heads(const PackedShape& s, int tensors) {
+  const int64_t tokens = s.page ? (int64_t)s.pages * s.page : s.T, bytes = tokens * s.d * 4 * tensors;
+  const int64_t fit = (40ll << 20) / bytes;
+  return (int)(fit < 16 ? (s.Hkv < 16 ? s.Hkv : 16) : (fit < s.Hkv ? fit : s.Hkv));
+}
+
 PackedBwdPlan packed_bwd_plan(const PackedShape& s, int sms);
 size_t packed_bwd_bytes(const PackedShape& s, const PackedBwdPlan& p, size_t* stats, size_t* part);
 cudaError_t launch_packed_bwd(const PackedShape& s, const PackedBwdPlan& p, const CUtensorMap& mq,
                               const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
                               const PackedBwdArgs& a, cudaStream_t st);
 
-PackedPlan packed_fwd_plan(const PackedShape& s, int sms);
-size_t packed_fwd_bytes(const PackedShape& s, const PackedPlan& p);
+// (The plan also says which sequences the kernel for few rows gets: s->few.)
+PackedPlan packed_fwd_plan(PackedShape* s, int sms);
+// Bytes of workspace; with `ws`, the arguments' pointers into it.
+size_t packed_fwd_bytes(const PackedShape& s, const PackedPlan& p, void* ws = nullptr, PackedFwdArgs* a = nullptr);
+cudaError_t launch_packed_few(const PackedShape& s, const PackedPlan& p, const PackedFwdArgs& a, cudaStream_t st);
 cudaError_t launch_packed_fwd(const PackedShape& s, const PackedPlan& p, const CUtensorMap& mq, const CUtensorMap& mk,
                               const CUtensorMap& mv, const CUtensorMap& mo, const PackedFwdArgs& a, cudaStream_t st);
 

@@ -95,7 +95,7 @@ __device__ __forceinline__ int64_t blocks_before(const PackedShape& s, const Seq
 
 __device__ __forceinline__ int segments_of(const PackedShape& s, const PackedSeqs& q, int w, int b) {
   const int n = b < s.B ? q.seq[b + 1] - q.seq[b] : 0;
-  return n > 0 ? (n + w - 1) / w : 0;
+  return n > s.few ? (n + w - 1) / w : 0;
 }
 
 // Work items, `parts` of every segment of w tokens of every key head, taken from a counter by the CTAs (the
