@@ -111,7 +111,9 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<unsigned long long>& don
 
 // A launch that may begin while the kernel before it on the stream, once all of that one's CTAs have
 // called kernel_trigger(), still runs: it calls kernel_wait() before it touches what that kernel (or
-// one before it) writes.  Between the kernels of one call only: the last one of a call never triggers.
+// one before it) writes.  The cross and cache calls use it between the kernels of one call only (the first is launched
+// as usual); of the packed, paged and rotary calls every kernel is launched so, and all of its threads wait before they
+// touch memory, so that a grid ends after all before it and the next may trust that.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A&&... args) {
   cudaLaunchAttribute early{};

@@ -257,7 +257,6 @@ sa2_status sa2_rotary_apply(const sa2_rotary* rotary, int32_t dtype, int32_t B, 
       return SA2_ERR_INVALID_ARG;
   }
   if (!aligned16(rotary->pairs) || misaligned4(pos)) return SA2_ERR_ALIGNMENT;
-  a.heads = H + H2;
   a.N = N;
   a.tokens = (int64_t)B * N;
   a.pairs = rotary->pairs;

@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
                                                           const __grid_constant__ PackedBwdPlan plan,
                                                           const __grid_constant__ PackedBwdArgs a) {
   constexpr int kLanes = D / 16;
+  kernel_wait();
   kernel_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) a.counter[threadIdx.x] = 0u;
   const int b = sequence_of_record(s, a.seqs, plan.nb, (int)blockIdx.x);
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   kernel_wait();
+  kernel_trigger();
   const int nb = plan.nb;
 
   auto take = [&](uint32_t n, DqItem& x) {
@@ -594,8 +596,8 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  kernel_trigger();
   kernel_wait();
+  kernel_trigger();
 
   auto take = [&](uint32_t n, DkvItem& x) {
     const uint32_t i = n % kSlots;
@@ -916,12 +918,12 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_dkdv_join_kernel(const __grid_constant__ PackedShape s,
                                                               const __grid_constant__ PackedBwdPlan plan,
                                                               const __grid_constant__ PackedBwdArgs a) {
+  kernel_wait();  // (by every CTA: the dQ kernel waits for this one alone)
   kernel_trigger();
   const int b = sequence_of_record(s, a.seqs, kKeyBlock, (int)blockIdx.x);
   const int lo = a.seqs.seq[b], n = a.seqs.seq[b + 1] - lo;
   const int kb = (int)blockIdx.x - first_record(lo, kKeyBlock, b), hk = blockIdx.y;
   const bool in_order = seqs_in_order(s, a.seqs, false, a.status);
-  kernel_wait();  // (by every CTA: the dQ kernel waits for this one alone)
   if (!in_order || kb < 0 || n < 1 || kb >= key_blocks(n)) return;
   constexpr int kItems = 2 * 128 * (D / 8) / kJoinParts;
   for (int j = threadIdx.x; j < kItems; j += 256) {
@@ -956,9 +958,8 @@ cudaError_t launch_t(const PackedShape& s, const PackedBwdPlan& p, const CUtenso
   if (e == cudaSuccess) e = allow_smem(dkv, DkvSmem<D>::kBytes, dkv_allowed);
   if (e != cudaSuccess) return e;
   prof_start(st, kBwdPre);
-  packed_stats_kernel<D><<<dim3((unsigned)p.tile_recs, (unsigned)s.Hkv, 128 / kStatsRows<D>), 256, 0, st>>>(s, p, a);
+  e = launch_early(packed_stats_kernel<D>, dim3((unsigned)p.tile_recs, (unsigned)s.Hkv, 128 / kStatsRows<D>), 256, 0, st, s, p, a);
   prof_stop(st, kBwdPre);
-  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   prof_start(st, kAttnBwd);
   e = launch_early(dkv, dim3((unsigned)p.grid), DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);

@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_u = smem_u32(ring);
-  if (plan.tiles || a.few.grid) kernel_trigger();  // another kernel of the call follows
+  kernel_wait();
+  kernel_trigger();
   const int page_shift = __ffs(s.page) - 1;
 
   FewWalk walk(s, a.seqs, a.status);  // (walked on by warp 0)
@@ -393,8 +394,7 @@ cudaError_t launch_t(const PackedShape& s, const PackedPlan& p, const PackedFwdA
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_smem(kern, kBytes, allowed);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)p.few_grid, kThreads, kBytes, st>>>(s, p, a);
-  return cudaGetLastError();
+  return launch_early(kern, dim3((unsigned)p.few_grid), kThreads, kBytes, st, s, p, a);
 }
 
 }  // namespace

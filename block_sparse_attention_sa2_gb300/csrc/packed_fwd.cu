@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (a.tile.grid + a.few.grid) kernel_trigger();  // a join follows
+  kernel_wait();
+  kernel_trigger();
   const int nb = plan.nb;
 
   // The n-th piece, for every warp but 0; false where there is none.
@@ -532,7 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  kernel_wait();  // for the kernel for few rows, whose parts the join reads too
 }
 
 // Joins the parts of segments that were cut: O = sum_i 2^(l_i - m) O_i / sum_i 2^(l_i - m) over a segment's
@@ -548,8 +548,9 @@ __global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant_
   const bool few = (int)blockIdx.x >= a.tile.grid;
   const Parts& parts = few ? a.few : a.tile;
   const int cta = few ? (int)blockIdx.x - a.tile.grid : (int)blockIdx.x;
-  if ((int)blockIdx.y * plan.join_rows >= parts.rows) return;
   kernel_wait();
+  kernel_trigger();
+  if ((int)blockIdx.y * plan.join_rows >= parts.rows) return;
   const CutRecord x = parts.rec[cta];
   if (x.parts == 0) return;
   for (int i = warp; i < plan.join_rows; i += 8) {
@@ -621,13 +622,8 @@ cudaError_t launch_t(const PackedShape& s, const PackedPlan& p, const CUtensorMa
   if (e != cudaSuccess) return e;
   prof_start(st, kAttnFwd);
   if (p.few_grid) e = launch_packed_few(s, p, a, st);
-  // (beside the one for few rows, whose outputs are other rows; it waits for it at its end)
-  if (e == cudaSuccess && p.tiles && p.few_grid)
+  if (e == cudaSuccess && p.tiles)
     e = launch_early(kern, dim3((unsigned)p.grid), kThreads, Smem<D>::kBytes, st, mq, mk, mv, mo, s, p, a);
-  else if (e == cudaSuccess && p.tiles) {
-    kern<<<(unsigned)p.grid, kThreads, Smem<D>::kBytes, st>>>(mq, mk, mv, mo, s, p, a);
-    e = cudaGetLastError();
-  }
   if (e == cudaSuccess && a.tile.grid + a.few.grid)
     e = launch_early(packed_join_kernel<D, F16>,
                      dim3((unsigned)(a.tile.grid + a.few.grid), (unsigned)((a.tile.grid ? p.tp * 128 : kFewRows) / p.join_rows)),

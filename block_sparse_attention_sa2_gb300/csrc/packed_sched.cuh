@@ -60,19 +60,20 @@ __device__ __forceinline__ bool seqs_in_order(const PackedShape& s, const Packed
   return !__any_sync(kFull, bad);
 }
 
-// sum over i < n of floor((a i + b) / m), a, b >= 0: whole parts out, then the lattice points under the
-// line counted along the other axis.
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum over i < n of floor((a i + b) / m), a, b >= 0: whole parts out, then the lattice points under the line
+// counted along the other axis.  In 32 bits but for the sums: with a <= m or n a < 2^31 and b < 2^31 no
+// number passes 2^31 (a n + b is below m n + m after the first step, and shrinks).
+__device__ __forceinline__ int64_t floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   int64_t sum = 0;
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    sum += (int64_t)n * (n - 1) / 2 * (a / m) + (int64_t)n * (b / m);
     a %= m;
     b %= m;
-    const int64_t top = a * n + b;
+    const unsigned top = a * n + b;
     if (top < m) break;
     n = top / m;
     b = top % m;
-    const int64_t t = m;
+    const unsigned t = m;
     m = a;
     a = t;
   }
@@ -88,7 +89,7 @@ __device__ __forceinline__ int segment_blocks(const PackedShape& s, const SeqInf
 __device__ __forceinline__ int64_t blocks_before(const PackedShape& s, const SeqInfo& x, int w, int segs, int p) {
   if (!s.causal || x.keys == 0) return (int64_t)p * segment_blocks(s, x, w, 0);
   const int whole = p < segs ? p : segs - 1;  // all but the last reach w tokens further than the one before
-  int64_t n = floor_sum(whole, kKeyBlock, w, (int64_t)x.pos + w + kKeyBlock - 1);
+  int64_t n = floor_sum(whole, kKeyBlock, w, (unsigned)x.pos + w + kKeyBlock - 1);
   if (p >= segs && segs > 0) n += segment_blocks(s, x, w, segs - 1);
   return n;
 }
@@ -107,47 +108,50 @@ struct ItemQueue {
   const int w, parts, heads, grid;
   const bool rising;
   unsigned* counter;   // null: no more items than CTAs
-  int64_t segs, item;  // segments of one key head; the next item
-  unsigned drawn;      // of the counter, for the item after it (lane 0)
+  int64_t item;    // the next one
+  unsigned drawn;  // of the counter, for the item after it (lane 0)
+  int mine;        // segments of sequence `lane`
+  int segs;        // of one key head (below 2^29)
   int section, level, most;
-  int64_t before, upto;  // segments that come before this level, and with it
+  int before, upto;  // segments that come before this level, and with it
 
   __device__ __forceinline__ ItemQueue(const PackedShape& s_, const PackedSeqs& q_, int w_, int parts_, int heads_,
                                        int grid_, bool rising_, unsigned* counter_, bool in_order)
-      : s(s_), q(q_), w(w_), parts(parts_), heads(heads_), grid(grid_), rising(rising_), counter(counter_), segs(0),
-        item(blockIdx.x), drawn(0), section(-1), level(0), most(0), before(0), upto(0) {
+      : s(s_), q(q_), w(w_), parts(parts_), heads(heads_), grid(grid_), rising(rising_), counter(counter_),
+        item(blockIdx.x), drawn(0), mine(0), segs(0), section(-1), level(0), most(0), before(0), upto(0) {
     if (!in_order) return;
-    int64_t n = 0;
-    for (int i = (int)(threadIdx.x & 31); i < s.B; i += 32) {
+    draw();
+    const int lane = threadIdx.x & 31;
+    int n = most = mine = segments_of(s, q, w, lane);
+    for (int i = lane + 32; i < s.B; i += 32) {
       const int k = segments_of(s, q, w, i);
       n += k;
       most = max(most, k);
     }
-    segs = warp_sum(n);
+    segs = __reduce_add_sync(kFull, n);
     most = __reduce_max_sync(kFull, most);
-    draw();
   }
+  __device__ __forceinline__ int segments(int b) const { return b < 32 ? mine : segments_of(s, q, w, b); }  // b % 32 = lane
   __device__ __forceinline__ void draw() {
     if (counter && (threadIdx.x & 31) == 0) drawn = atomicAdd(counter, 1u);
   }
   // Segments that come in order before those of place l.
-  __device__ __forceinline__ int64_t ahead_of(int l) const {
-    int64_t n = 0;
+  __device__ __forceinline__ int ahead_of(int l) const {
+    int n = 0;
     for (int i = (int)(threadIdx.x & 31); i < s.B; i += 32) {
-      const int k = segments_of(s, q, w, i);
+      const int k = segments(i);
       n += rising ? min(k, l) : max(k - l - 1, 0);
     }
-    return warp_sum(n);
+    return __reduce_add_sync(kFull, n);
   }
   __device__ __forceinline__ bool next(int& b, int& seg, int& hk, int& part) {
     const int lane = threadIdx.x & 31;
-    const int64_t per_head = segs * parts;
+    const int64_t per_head = (int64_t)segs * parts;
     if (item >= per_head * s.Hkv) return false;
     const int sec = (int)(item / (per_head * heads));
     const int64_t in = item - sec * per_head * heads;
     const int width = min(heads, s.Hkv - sec * heads);
-    const int64_t rank = in / (width * parts);
-    const int rest = (int)(in - rank * (width * parts));
+    const int rank = (int)(in / (width * parts)), rest = (int)(in - (int64_t)rank * (width * parts));
     hk = sec * heads + rest / parts;
     part = rest % parts;
     if (counter) {
@@ -170,13 +174,13 @@ struct ItemQueue {
       set_level(rising ? level + l : level - l);
     }
     seg = level;
-    int r = (int)(rank - before);  // of the sequences that have this place
+    int r = rank - before;  // of the sequences that have this place
     for (int c = 0; c < s.B; c += 32) {
-      const bool mine = segments_of(s, q, w, c + lane) > level;
-      const unsigned in_c = __ballot_sync(kFull, mine);
+      const bool has = segments(c + lane) > level;
+      const unsigned in_c = __ballot_sync(kFull, has);
       const int n = __popc(in_c);
       if (r < n) {
-        const bool it = mine && __popc(in_c & ((1u << lane) - 1)) == r;
+        const bool it = has && __popc(in_c & ((1u << lane) - 1)) == r;
         b = c + __ffs(__ballot_sync(kFull, it)) - 1;
         break;
       }
@@ -246,12 +250,12 @@ struct PackedWalk {
     const int64_t per = blocks_before(s, x, p.w, nseg, nseg);
     hk = (int)(off / per);
     off -= hk * per;
-    int l = 0, h = nseg - 1;  // last segment that begins at or before off
-    while (l < h) {
-      const int m = (l + h + 1) >> 1;
-      if (blocks_before(s, x, p.w, nseg, m) <= off) l = m; else h = m - 1;
+    int h = nseg;  // the last segment that begins at or before off, 32 of them looked at per step
+    while (h - pr > 1) {
+      const int step = (h - pr + 31) >> 5, c = pr + lane * step;
+      pr += (31 - __clz(__ballot_sync(kFull, c < h && blocks_before(s, x, p.w, nseg, c) <= off))) * step;
+      h = min(h, pr + step);
     }
-    pr = l;
     cut = (int)(off - blocks_before(s, x, p.w, nseg, pr));
   }
   __device__ __forceinline__ int64_t blocks_of(int b_) const {

@@ -12,6 +12,8 @@ constexpr int kHeads = 4;  // of a token per thread, all of their loads in fligh
 // begins at or before it, by bisection), page and place in it are found once.  K and V in one launch (grid z).
 // Bound by the bytes, one read and one write of each.
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendArgs a) {
+  kernel_wait();
+  kernel_trigger();
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int tok = (int)(i / a.words), word = (int)(i % a.words);
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
@@ -54,9 +56,9 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
   const int64_t blocks = ((int64_t)a.T * a.words + kThreads - 1) / kThreads;
   const dim3 grid((unsigned)blocks, (unsigned)((a.Hkv + kHeads - 1) / kHeads), 2);
   prof_start(st, kToF16);
-  paged_append_kernel<<<grid, kThreads, 0, st>>>(a);
+  const cudaError_t e = launch_early(paged_append_kernel, grid, kThreads, 0, st, a);
   prof_stop(st, kToF16);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace sa2

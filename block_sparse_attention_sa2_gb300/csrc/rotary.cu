@@ -6,6 +6,7 @@
 // whole turns fall off the top, is the angle's place in its turn to 2^-31 for any 32-bit position, where
 // position * frequency in fp32 would be off by 0.06 radians at a position of a million.  Sine and cosine
 // are then taken of an angle in [-pi, pi] in fp32.
+#include "cross_sched.cuh"
 #include "rotary.h"
 
 namespace sa2 {
@@ -71,61 +72,76 @@ __device__ __forceinline__ float2 turn(const RotaryArgs& a, int64_t token, int i
 }
 
 // A thread has one word of kPer channels (both halves layout: that word and its partner half the turned
-// channels further on) of one token, and goes through `per` of its heads; the angles, which belong to the
-// token, are made once.  Bound by the bytes, one read and one write of each.
+// channels further on) of one token, and goes through `per` of its heads, kBatch of them loaded at a time; the angles,
+// which belong to the token, are made once.  Bound by the bytes, one read and one write of each.
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
   using V = Vec<T>;
   constexpr int kPer = V::kPer, kPairs = HALF ? kPer : kPer / 2;
+  constexpr int kBatch = HALF ? 2 : 4;
+  kernel_wait();
+  kernel_trigger();
   const int words = a.words;  // of a token and head that are worked on
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int word = (int)(i % words);
   const int64_t tok = i / words;  // b * N + n
+  const int word = (int)(i - tok * words);
   if (tok >= a.tokens) return;
   const int b = (int)(tok / a.N), n = (int)(tok - (int64_t)b * a.N);
   const bool turned = word < a.turned;
   const int ch = (HALF && !turned ? word + a.turned : word) * kPer;  // half layout: `turned` words stand for two each
+  const bool second = (int)blockIdx.y >= a.chunks;
+  const RotaryTensor& t = a.t[second];
+  const int h0 = ((int)blockIdx.y - (second ? a.chunks : 0)) * a.per, h1 = min(h0 + a.per, t.heads);
+  const T* src = static_cast<const T*>(t.x.p) + b * t.x.sb + n * t.x.sn + ch;
+  T* dst = static_cast<T*>(t.y.p) + b * t.y.sb + n * t.y.sn + ch;
+  uint4 u[kBatch], v[kBatch];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (h + j < h1) {
+        u[j] = *reinterpret_cast<const uint4*>(src + (h + j) * t.x.sh);
+        if (HALF && turned) v[j] = *reinterpret_cast<const uint4*>(src + (h + j) * t.x.sh + a.half);
+      }
+  };
+  load(h0);
   float2 w[kPairs];
   if (turned) {
     const int p0 = HALF ? ch : ch / 2;
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      w[p] = p0 + p < a.half ? turn(a, b * a.pos_b + n, p0 + p) : make_float2(0.f, 0.f);
-    }
+    for (int p = 0; p < kPairs; ++p) w[p] = p0 + p < a.half ? turn(a, b * a.pos_b + n, p0 + p) : make_float2(0.f, 0.f);
   }
-  const int h0 = blockIdx.y * a.per, h1 = min(h0 + a.per, a.heads);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const RotaryTensor& t = h < a.t[0].heads ? a.t[0] : a.t[1];
-    const int hh = h < a.t[0].heads ? h : h - a.t[0].heads;
-    const T* src = static_cast<const T*>(t.x.p) + b * t.x.sb + hh * t.x.sh + n * t.x.sn + ch;
-    T* dst = static_cast<T*>(t.y.p) + b * t.y.sb + hh * t.y.sh + n * t.y.sn + ch;
-    const uint4 u = *reinterpret_cast<const uint4*>(src);
-    if (!turned) {
-      *reinterpret_cast<uint4*>(dst) = u;
-      continue;
-    }
-    float x[kPer];
-    V::load(u, x);
-    if constexpr (HALF) {
-      float y[kPer], z[kPer];
-      V::load(*reinterpret_cast<const uint4*>(src + a.half), y);
+  for (int h = h0; h < h1; h += kBatch) {
+    if (h > h0) load(h);
 #pragma unroll
-      for (int p = 0; p < kPer; ++p) {
-        z[p] = fmaf(x[p], w[p].x, -y[p] * w[p].y);
-        y[p] = fmaf(y[p], w[p].x, x[p] * w[p].y);
+    for (int j = 0; j < kBatch; ++j) {
+      if (h + j >= h1) break;
+      uint4* out = reinterpret_cast<uint4*>(dst + (h + j) * t.y.sh);
+      if (!turned) {
+        *out = u[j];
+        continue;
       }
-      *reinterpret_cast<uint4*>(dst) = V::pack(z);
-      *reinterpret_cast<uint4*>(dst + a.half) = V::pack(y);
-    } else {
+      float x[kPer];
+      V::load(u[j], x);
+      if constexpr (HALF) {
+        float y[kPer], z[kPer];
+        V::load(v[j], y);
 #pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        if (ch / 2 + p >= a.half) break;  // (a word may hold channels behind the turned ones)
-        const float c = x[2 * p], s = x[2 * p + 1];
-        x[2 * p] = fmaf(c, w[p].x, -s * w[p].y);
-        x[2 * p + 1] = fmaf(s, w[p].x, c * w[p].y);
+        for (int p = 0; p < kPer; ++p) {
+          z[p] = fmaf(x[p], w[p].x, -y[p] * w[p].y);
+          y[p] = fmaf(y[p], w[p].x, x[p] * w[p].y);
+        }
+        *out = V::pack(z);
+        *reinterpret_cast<uint4*>(dst + (h + j) * t.y.sh + a.half) = V::pack(y);
+      } else {
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) {
+          if (ch / 2 + p >= a.half) break;  // (a word may hold channels behind the turned ones)
+          const float c = x[2 * p], s = x[2 * p + 1];
+          x[2 * p] = fmaf(c, w[p].x, -s * w[p].y);
+          x[2 * p + 1] = fmaf(s, w[p].x, c * w[p].y);
+        }
+        *out = V::pack(x);
       }
-      *reinterpret_cast<uint4*>(dst) = V::pack(x);
     }
   }
 }
@@ -141,21 +157,22 @@ cudaError_t launch_rotary(const RotaryArgs& args, int d, int dtype, bool half_la
   a.words = a.turned + standing;
   if (a.words == 0) return cudaSuccess;
   const int64_t blocks = (a.tokens * a.words + kThreads - 1) / kThreads;
-  // heads per thread: as many as leave each SM eight CTAs, eight at most
-  a.per = 1;
-  while (a.per < 8 && a.per < a.heads && blocks * ((a.heads + 2 * a.per - 1) / (2 * a.per)) >= 8 * (int64_t)sms) a.per *= 2;
-  const dim3 grid((unsigned)blocks, (unsigned)((a.heads + a.per - 1) / a.per));
+  // heads per thread: 8, whose angles are then made once, or as few as leave each SM four CTAs
+  auto chunks = [&](int i, int per) { return (a.t[i].heads + per - 1) / per; };
+  a.per = 8;
+  while (a.per > 1 && blocks * (chunks(0, a.per) + chunks(1, a.per)) < 4 * (int64_t)sms) a.per /= 2;
+  a.chunks = chunks(0, a.per);
+  const dim3 grid((unsigned)blocks, (unsigned)(a.chunks + chunks(1, a.per)));
   prof_start(st, kToF16);
-  switch (dtype * 2 + half_layout) {
-    case SA2_BF16 * 2: rotary_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, st>>>(a); break;
-    case SA2_BF16 * 2 + 1: rotary_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, st>>>(a); break;
-    case SA2_FP16 * 2: rotary_kernel<__half, false><<<grid, kThreads, 0, st>>>(a); break;
-    case SA2_FP16 * 2 + 1: rotary_kernel<__half, true><<<grid, kThreads, 0, st>>>(a); break;
-    case SA2_FP32 * 2: rotary_kernel<float, false><<<grid, kThreads, 0, st>>>(a); break;
-    default: rotary_kernel<float, true><<<grid, kThreads, 0, st>>>(a); break;
-  }
+  cudaError_t e;
+  if (dtype == SA2_BF16)
+    e = launch_early(half_layout ? rotary_kernel<__nv_bfloat16, true> : rotary_kernel<__nv_bfloat16, false>, grid, kThreads, 0, st, a);
+  else if (dtype == SA2_FP16)
+    e = launch_early(half_layout ? rotary_kernel<__half, true> : rotary_kernel<__half, false>, grid, kThreads, 0, st, a);
+  else
+    e = launch_early(half_layout ? rotary_kernel<float, true> : rotary_kernel<float, false>, grid, kThreads, 0, st, a);
   prof_stop(st, kToF16);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace sa2

@@ -12,7 +12,6 @@ struct RotaryTensor {
 
 struct RotaryArgs {
   RotaryTensor t[2];    // the second may have no heads
-  int heads;            // of both
   int N;                // tokens of a sequence
   int64_t tokens;       // of all
   const int64_t* pairs;  // [half][2]: turns per position (64 bits behind the point), axis
@@ -22,7 +21,8 @@ struct RotaryArgs {
   float gain;
   unsigned* status;
   int inverse, in_place;
-  int turned, words, per;  // words of 16 bytes that hold turned channels; of both kinds; heads per thread
+  // words of 16 bytes that hold turned channels, of both kinds; heads per thread; runs of heads of the first tensor
+  int turned, words, per, chunks;
 };
 
 cudaError_t launch_rotary(const RotaryArgs& a, int d, int dtype, bool half_layout, int sms, cudaStream_t st);
