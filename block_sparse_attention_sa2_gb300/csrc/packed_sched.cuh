@@ -108,8 +108,7 @@ struct ItemQueue {
   const int w, parts, heads, grid;
   const bool rising;
   unsigned* counter;   // null: no more items than CTAs
-  int64_t item;    // the next one
-  unsigned drawn;  // of the counter, for the item after it (lane 0)
+  bool first;
   int mine;        // segments of sequence `lane`
   int segs;        // of one key head (below 2^29)
   int section, level, most;
@@ -118,9 +117,8 @@ struct ItemQueue {
   __device__ __forceinline__ ItemQueue(const PackedShape& s_, const PackedSeqs& q_, int w_, int parts_, int heads_,
                                        int grid_, bool rising_, unsigned* counter_, bool in_order)
       : s(s_), q(q_), w(w_), parts(parts_), heads(heads_), grid(grid_), rising(rising_), counter(counter_),
-        item(blockIdx.x), drawn(0), mine(0), segs(0), section(-1), level(0), most(0), before(0), upto(0) {
+        first(true), mine(0), segs(0), section(-1), level(0), most(0), before(0), upto(0) {
     if (!in_order) return;
-    draw();
     const int lane = threadIdx.x & 31;
     int n = most = mine = segments_of(s, q, w, lane);
     for (int i = lane + 32; i < s.B; i += 32) {
@@ -132,9 +130,6 @@ struct ItemQueue {
     most = __reduce_max_sync(kFull, most);
   }
   __device__ __forceinline__ int segments(int b) const { return b < 32 ? mine : segments_of(s, q, w, b); }  // b % 32 = lane
-  __device__ __forceinline__ void draw() {
-    if (counter && (threadIdx.x & 31) == 0) drawn = atomicAdd(counter, 1u);
-  }
   // Segments that come in order before those of place l.
   __device__ __forceinline__ int ahead_of(int l) const {
     int n = 0;
@@ -147,6 +142,17 @@ struct ItemQueue {
   __device__ __forceinline__ bool next(int& b, int& seg, int& hk, int& part) {
     const int lane = threadIdx.x & 31;
     const int64_t per_head = (int64_t)segs * parts;
+    // An item is taken only when the CTA is about to need it (its loads for the one before are all issued): taken one
+    // ahead, with three or four items to a CTA, the long ones stayed where they had been given out (5 sequences of
+    // 514 to 3314 tokens, 8 key heads: CTAs of 187 to 376 us in the dK, dV kernel).
+    int64_t item = blockIdx.x;
+    if (!first) {
+      if (!counter) return false;
+      unsigned t = 0;
+      if (lane == 0) t = atomicAdd(counter, 1u);
+      item = (int64_t)grid + __shfl_sync(kFull, t, 0);
+    }
+    first = false;
     if (item >= per_head * s.Hkv) return false;
     const int sec = (int)(item / (per_head * heads));
     const int64_t in = item - sec * per_head * heads;
@@ -154,12 +160,6 @@ struct ItemQueue {
     const int rank = (int)(in / (width * parts)), rest = (int)(in - (int64_t)rank * (width * parts));
     hk = sec * heads + rest / parts;
     part = rest % parts;
-    if (counter) {
-      item = (int64_t)grid + __shfl_sync(kFull, drawn, 0);
-      draw();  // (back before it is needed)
-    } else {
-      item = per_head * s.Hkv;
-    }
     if (sec != section) {
       section = sec;
       set_level(rising ? 0 : most - 1);
