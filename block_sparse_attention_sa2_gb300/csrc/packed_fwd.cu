@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++pc[t];
         tc_fence_after();
         const float inv_l = row_s[t * 128 + r];
-        float* po = a.tile.o + ((int64_t)x.slot * kTileRows + t * 128 + r) * D;
+        float4* po = reinterpret_cast<float4*>(a.tile.o) + ((int64_t)x.slot * 2 + t) * (D / 4) * 128 + r;
         uint8_t* st_row = smem + L::kOffO + r * 128;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (row_valid) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4*>(po + c0)[i] =
+                po[(c0 / 4 + i) * 128] =
                     make_float4(__uint_as_float(u[4 * i]) * inv_l, __uint_as_float(u[4 * i + 1]) * inv_l,
                                 __uint_as_float(u[4 * i + 2]) * inv_l, __uint_as_float(u[4 * i + 3]) * inv_l);
             }
@@ -537,79 +537,138 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of segments that were cut: O = sum_i 2^(l_i - m) O_i / sum_i 2^(l_i - m) over a segment's
 // parts in key order, l_i their log2 sums and m the largest; LSE = ln 2 (m + log2 sum).  Parts in which a
-// row has no keys (l_i = -inf) are left out.  One warp per row; grid (CTAs of the kernel of tiles and of that for few
-// rows, parts of a segment's rows); most CTAs find nothing to do.
+// row has no keys (l_i = -inf, whose O may never have been written) are left out.  Grid (CTAs of the kernel of tiles and
+// of that for few rows, shares of a segment's rows); most CTAs find nothing to do.
+//
+// Tiles have few parts each and many rows: a thread has 16 channels of a row, a warp 32 rows.  Few rows may have a part
+// from every SM: a warp has a row, and eight parts of it on their way at a time (one sequence of 32760 tokens, 8 key
+// heads of 5: 33 us in all, a thread per 16 channels 39).
+constexpr int kJoinThreads = 128;
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant__ PackedShape s,
-                                                         const __grid_constant__ PackedPlan plan,
-                                                         const __grid_constant__ PackedFwdArgs a) {
+__device__ __forceinline__ void join_few(const PackedShape& s, const PackedFwdArgs& a, const CutRecord& x, int cta, int rr) {
   constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool few = (int)blockIdx.x >= a.tile.grid;
-  const Parts& parts = few ? a.few : a.tile;
-  const int cta = few ? (int)blockIdx.x - a.tile.grid : (int)blockIdx.x;
-  kernel_wait();
-  kernel_trigger();
-  if ((int)blockIdx.y * plan.join_rows >= parts.rows) return;
-  const CutRecord x = parts.rec[cta];
-  if (x.parts == 0) return;
-  for (int i = warp; i < plan.join_rows; i += 8) {
-    const int rr = blockIdx.y * plan.join_rows + i, t = rr >> 7, r = rr & 127;
-    const int tok_r = r / s.G, g = r - tok_r * s.G, tok = t * plan.nb + tok_r, h = x.hk * s.G + g;
-    if (rr >= parts.rows || t >= plan.tp || tok_r >= plan.nb || tok >= x.ntok) continue;
-    auto slot_row = [&](int k) { return (int64_t)(k == 0 ? x.slot : 2 * (cta + k)) * parts.rows + rr; };
-    // lane i has part i's sum; 32 parts at a time, eight of their rows in flight
-    float m = kLeastRef, acc[kPer] = {}, l = 0.f;
-    for (int base = 0; base < x.parts; base += 32) {
-      const int n32 = min(32, x.parts - base);
-      const float mine = lane < n32 ? parts.l[slot_row(base + lane)] : -INFINITY;
-      float mx = mine;
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-      if (__any_sync(kFull, mine != mine)) mx = NAN;
-      const float m_new = m != m ? m : (mx > m || mx != mx ? mx : m);
-      const float keep = base == 0 ? 0.f : ex2(m - m_new);
-      m = m_new;
-      l *= keep;
+  const int lane = threadIdx.x & 31;
+  const int tok = rr / s.G, h = x.hk * s.G + rr - tok * s.G;
+  if (tok >= x.ntok) return;
+  auto slot_row = [&](int k) { return (int64_t)(k == 0 ? x.slot : 2 * (cta + k)) * kFewRows + rr; };
+  // lane i has part i's sum, 32 parts at a time
+  float m = kLeastRef, acc[kPer] = {}, l = 0.f;
+  for (int base = 0; base < x.parts; base += 32) {
+    const int n32 = min(32, x.parts - base);
+    const float mine = lane < n32 ? a.few.l[slot_row(base + lane)] : -INFINITY;
+    float mx = mine;
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    if (__any_sync(kFull, mine != mine)) mx = NAN;
+    const float m_new = m != m ? m : (mx > m || mx != mx ? mx : m);
+    const float keep = base == 0 ? 0.f : ex2(m - m_new);
+    m = m_new;
+    l *= keep;
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) acc[q] *= keep;
-      const float wl = lane < n32 && mine != -INFINITY ? ex2(mine - m) : 0.f;
-      const unsigned some = __ballot_sync(kFull, lane < n32 && mine != -INFINITY);
-      for (int k = 0; k < n32; k += 8) {
-        float v[8][kPer];
+    for (int q = 0; q < kPer; ++q) acc[q] *= keep;
+    const float wl = lane < n32 ? ex2(mine - m) : 0.f;
+    for (int k = 0; k < n32; k += 8) {
+      float v[8][kPer];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          if (!((some >> ((k + u) & 31)) & 1)) {
+      for (int u = 0; u < 8; ++u) {
+        if (k + u >= n32) break;
+        const float* src = a.few.o + slot_row(base + k + u) * D + lane * kPer;
+        if constexpr (kPer == 4)
+          *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
+      }
 #pragma unroll
-            for (int q = 0; q < kPer; ++q) v[u][q] = 0.f;
-            continue;
-          }
-          const float* src = parts.o + slot_row(base + k + u) * D;
-          if constexpr (kPer == 4)
-            *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src + lane * 4);
-          else
-            *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src + lane * 2);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float w = __shfl_sync(kFull, wl, (k + u) & 31);
+      for (int u = 0; u < 8; ++u) {
+        const float w = __shfl_sync(kFull, wl, (k + u) & 31);
+        if (k + u < n32) {  // (every row of few has been written)
           l += w;
 #pragma unroll
           for (int q = 0; q < kPer; ++q) acc[q] = fmaf(w, v[u][q], acc[q]);
         }
       }
     }
-    const float inv = inverse_sum(l);
-    uint32_t w[kPer / 2];
-#pragma unroll
-    for (int q = 0; q < kPer / 2; ++q)
-      w[q] = F16 ? pack_f16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv) : pack_bf16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv);
-    uint16_t* op = static_cast<uint16_t*>(a.o.p) + h * a.o.sh + (int64_t)(x.qtok + tok) * a.o.sn + lane * kPer;
-    if constexpr (kPer == 4)
-      *reinterpret_cast<uint2*>(op) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(op) = w[0];
-    if (lane == 0) a.lse[(int64_t)h * s.T + x.qtok + tok] = (m + __log2f(l)) * 0.69314718055994531f;
   }
+  const float inv = inverse_sum(l);
+  uint32_t w[kPer / 2];
+#pragma unroll
+  for (int q = 0; q < kPer / 2; ++q)
+    w[q] = F16 ? pack_f16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv) : pack_bf16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv);
+  uint16_t* op = static_cast<uint16_t*>(a.o.p) + h * a.o.sh + (int64_t)(x.qtok + tok) * a.o.sn + lane * kPer;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(op) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(op) = w[0];
+  if (lane == 0) a.lse[(int64_t)h * s.T + x.qtok + tok] = (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const __grid_constant__ PackedShape s,
+                                                                  const __grid_constant__ PackedPlan plan,
+                                                                  const __grid_constant__ PackedFwdArgs a) {
+  kernel_wait();
+  kernel_trigger();
+  if ((int)blockIdx.x >= a.tile.grid) {
+    const int cta = (int)blockIdx.x - a.tile.grid, rr = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    if (rr >= kFewRows) return;
+    const CutRecord x = a.few.rec[cta];
+    if (x.parts) join_few<D, F16>(s, a, x, cta, rr);
+    return;
+  }
+  const int cta = blockIdx.x, at = blockIdx.y * kJoinThreads + threadIdx.x;
+  const CutRecord x = a.tile.rec[cta];
+  const int t = at / (128 * (D / 16)), ch = at / 128 % (D / 16) * 16, r = at % 128;
+  const int tok_r = r / s.G, g = r - tok_r * s.G, tok = t * plan.nb + tok_r, h = x.hk * s.G + g;
+  if (x.parts == 0 || t >= plan.tp || tok_r >= plan.nb || tok >= x.ntok) return;
+  auto slot = [&](int k) { return (int64_t)(k == 0 ? x.slot : 2 * (cta + k)) * 2 + t; };
+  // four parts at a time, the first four's rows on their way while the largest sum is looked for
+  float4 v[4][4];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k0 + k < x.parts) {
+        const float4* src = reinterpret_cast<const float4*>(a.tile.o) + (slot(k0 + k) * (D / 4) + ch / 4) * 128 + r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k][i] = src[i * 128];
+      }
+  };
+  load(0);
+  float m = kLeastRef;
+  bool nan = false;
+#pragma unroll 4
+  for (int k = 0; k < x.parts; ++k) {
+    const float lk = a.tile.l[slot(k) * 128 + r];
+    nan |= lk != lk;
+    m = fmaxf(m, lk);
+  }
+  if (nan) m = NAN;
+  float acc[16] = {}, l = 0.f;
+  for (int k0 = 0; k0 < x.parts; k0 += 4) {
+    if (k0) load(k0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k0 + k >= x.parts) break;
+      const float lk = a.tile.l[slot(k0 + k) * 128 + r];
+      if (lk == -INFINITY) continue;
+      const float w = ex2(lk - m);
+      l += w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[4 * i] = fmaf(w, v[k][i].x, acc[4 * i]);
+        acc[4 * i + 1] = fmaf(w, v[k][i].y, acc[4 * i + 1]);
+        acc[4 * i + 2] = fmaf(w, v[k][i].z, acc[4 * i + 2]);
+        acc[4 * i + 3] = fmaf(w, v[k][i].w, acc[4 * i + 3]);
+      }
+    }
+  }
+  const float inv = inverse_sum(l);
+  uint32_t w[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    w[q] = F16 ? pack_f16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv) : pack_bf16x2(acc[2 * q] * inv, acc[2 * q + 1] * inv);
+  uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o.p) + h * a.o.sh + (int64_t)(x.qtok + tok) * a.o.sn + ch);
+  op[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  op[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (ch == 0) a.lse[(int64_t)h * s.T + x.qtok + tok] = (m + __log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D, bool F16>
@@ -626,23 +685,25 @@ cudaError_t launch_t(const PackedShape& s, const PackedPlan& p, const CUtensorMa
     e = launch_early(kern, dim3((unsigned)p.grid), kThreads, Smem<D>::kBytes, st, mq, mk, mv, mo, s, p, a);
   if (e == cudaSuccess && a.tile.grid + a.few.grid)
     e = launch_early(packed_join_kernel<D, F16>,
-                     dim3((unsigned)(a.tile.grid + a.few.grid), (unsigned)((a.tile.grid ? p.tp * 128 : kFewRows) / p.join_rows)),
-                     256, 0, st, s, p, a);
+                     dim3((unsigned)(a.tile.grid + a.few.grid),
+                          (unsigned)(a.tile.grid ? std::max(p.tp * (D / 16), 4) : 4)),
+                     kJoinThreads, 0, st, s, p, a);
   prof_stop(st, kAttnFwd);
   return e;
 }
 
 }  // namespace
 
-// Split where the segments that there can be would leave more than a tenth of the SMs' time unused as whole ones
-// (fewer than the SMs, or a last round that is not full; from four rounds on they even out by the order in which they are
-// taken) and their keys are eight blocks or more (the join would cost what the split gains); of packed sequences, whose
-// lengths the host does not know, by their mean.  Whole segments of one key head run side by side and read its keys from
-// L2 (40 heads x 3600 over 75600, d = 128, 3.95 rounds: split 4120 us at 5.6 TB/s of keys from memory).
+// Whole segments or keys split over the SMs: by what either would take, counted in key blocks that one SM works on, of
+// the segments that there can be at the lengths that the host knows of (the table's width, or the mean of packed
+// sequences).  Whole ones take a round of the longest after another, or, where they are as different as those of a causal
+// sequence, as long as the longest or an even share; split ones an even share, a tenth longer because whole segments of
+// one key head run side by side and read its keys from L2 (40 heads x 3600 over 75600, d = 128, 3.95 rounds: split 4600
+// us, whole 4350), and kSplitBlocks for the parts that are written and joined (16 heads x 2048, d = 64: as long either way).
+constexpr double kSplitBlocks = 8;
 PackedPlan packed_fwd_plan(PackedShape* shape, int sms) {
   PackedShape& s = *shape;
   PackedPlan p{};
-  p.join_rows = 16;
   p.tp = 1;
   p.nb = 128 / s.G;
   const int64_t most_keys = s.page ? (int64_t)s.width * s.page : s.T / s.B;
@@ -655,9 +716,12 @@ PackedPlan packed_fwd_plan(PackedShape* shape, int sms) {
   }
   p.tiles = s.max_new > s.few;
   if (!p.tiles) return p;
-  const int64_t blocks = (most_keys + kKeyBlock - 1) / kKeyBlock;
-  const int64_t paired = s.Hkv * segment_bound(s, 2 * p.nb), rounds = (paired + sms - 1) / sms;
-  p.split = blocks >= 8 && rounds <= 4 && 10 * paired < 9 * rounds * sms;
+  const double blocks = (double)((most_keys + kKeyBlock - 1) / kKeyBlock);
+  const int64_t paired = s.Hkv * segment_bound(s, 2 * p.nb);
+  const bool uneven = s.causal && !s.page;
+  const double share = (double)paired * blocks * (uneven ? 0.5 : 1.0) / sms;
+  const double whole = uneven ? std::max(blocks, share) : blocks * (double)((paired + sms - 1) / sms);
+  p.split = whole > 1.1 * share + kSplitBlocks;
   // one tile per CTA while each finds an SM of its own, and where sequences have no second one
   p.tp = s.max_new <= p.nb || (!p.split && s.Hkv * segment_bound(s, p.nb) <= sms) ? 1 : 2;
   p.w = p.tp * p.nb;

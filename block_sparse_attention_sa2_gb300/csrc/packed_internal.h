@@ -51,7 +51,6 @@ struct PackedPlan {
   int split;
   int tickets;  // direct: more items than CTAs may be
   int heads;
-  int join_rows;
 };
 
 // The segment that a CTA's run ends in, where the runs behind it have the rest: read by the join.
@@ -60,10 +59,12 @@ struct CutRecord {
 };
 
 // What a kernel that cuts segments leaves for the join: a record for each CTA, and two slots for each of `rows` rows.
+// Four channels lie together; those of the rows of a tile behind one another (a thread has a row there, so that a
+// warp's store is 512 bytes in one piece), those of few rows row by row.
 struct Parts {
   CutRecord* rec;  // [grid]
   float* l;        // [2 * grid][rows], log2 units
-  float* o;        // [2 * grid][rows][d]
+  float* o;        // [2 * grid][rows * d]: tiles [2][d / 4][128][4], few rows [16][d]
   int grid, rows;  // grid = 0: none
 };
 
