@@ -110,7 +110,7 @@ def _link_binding(obj: str, torch) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lsa2", "-Wl,-rpath,$ORIGIN", "-L", libs, "-ltorch_python",
-           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

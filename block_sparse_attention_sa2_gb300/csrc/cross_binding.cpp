@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -108,10 +108,16 @@ struct Place {
     if (caller) x.record_stream(*caller);
     return x;
   }
-  at::Tensor empty(Sizes shape, at::ScalarType t) const {
-    return made(at::empty(shape, at::TensorOptions().dtype(t).device(device)));
+  // (straight from the CUDA allocator's front end: through the dispatcher a tensor takes 1.5 us on a Grace core)
+  at::Tensor fresh(Sizes shape, at::ScalarType t) const {
+    return at::Tensor(at::detail::empty_cuda(shape, t, device, std::nullopt));
   }
-  at::Tensor empty_like(const at::Tensor& x) const { return made(at::empty_like(x)); }
+  at::Tensor empty(Sizes shape, at::ScalarType t) const { return made(fresh(shape, t)); }
+  at::Tensor empty_like(const at::Tensor& x) const {
+    return made(x.is_non_overlapping_and_dense()
+                    ? at::Tensor(at::detail::empty_strided_cuda(x.sizes(), x.strides(), x.scalar_type(), device))
+                    : at::empty_like(x));
+  }
   at::Tensor given_or_like(PyObject* o, const char* name, const at::Tensor& x) const {
     return none(o) ? empty_like(x) : tensor(o, name);
   }
@@ -153,7 +159,7 @@ struct Workspace {
   Workspace(PyObject* ws, size_t need, const Place& at_) {
     if (none(ws)) {
       if (need == 0) return;
-      hold = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(at_.device));
+      hold = at_.fresh({(int64_t)need}, at::kByte);
     } else {
       hold = tensor(ws, "ws");
       if (hold.device() != at_.device || hold.scalar_type() != at::kByte || !hold.is_contiguous())

@@ -51,10 +51,10 @@ __device__ __forceinline__ SeqInfo seq_info(const PackedShape& s, const PackedSe
 __device__ __forceinline__ bool seqs_in_order(const PackedShape& s, const PackedSeqs& q, bool report, unsigned* status) {
   bool bad = false, odd = false;
   for (int b = (int)(threadIdx.x & 31); b < s.B; b += 32) {
-    const int lo = q.seq[b], hi = q.seq[b + 1];
+    const int lo = q.seq[b], hi = q.seq[b + 1], held = q.kv_len ? q.kv_len[b] : 0;  // (loads that do not wait for each other)
     const bool out = lo < 0 || hi < lo || hi > s.T;
     bad |= out;
-    if (!out) odd |= hi - lo > s.max_new || (q.kv_len && !keys_in_range(s, q.kv_len[b], hi - lo));
+    if (!out) odd |= hi - lo > s.max_new || (q.kv_len && !keys_in_range(s, held, hi - lo));
   }
   if (report && (bad || odd)) report_error(status, kDevErrBounds);
   return !__any_sync(kFull, bad);

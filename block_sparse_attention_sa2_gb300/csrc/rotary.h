@@ -23,6 +23,7 @@ struct RotaryArgs {
   int inverse, in_place;
   // words of 16 bytes that hold turned channels, of both kinds; heads per thread; runs of heads of the first tensor
   int turned, words, per, chunks;
+  int toks;  // tokens of a CTA
 };
 
 cudaError_t launch_rotary(const RotaryArgs& a, int d, int dtype, bool half_layout, int sms, cudaStream_t st);
