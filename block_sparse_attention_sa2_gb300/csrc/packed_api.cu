@@ -30,8 +30,8 @@ sa2_status check_packed(const sa2_packed_shape* x, PackedShape* s) {
   s->d = x->d;
   s->dtype = x->dtype;
   s->causal = x->causal;
-  // (work items are counted in 32 bits; tensors of so many have terabytes)
-  if (s->Hkv * segment_bound(*s, 128 / s->G) > INT32_MAX) return SA2_ERR_UNSUPPORTED;
+  // (work items are counted in 32 bits, beside the CTAs that find none left; tensors of so many have terabytes)
+  if (s->Hkv * segment_bound(*s, 128 / s->G) > (1 << 30)) return SA2_ERR_UNSUPPORTED;
   wait_settings(&s->wait_ns, &s->stall_ns);
   return SA2_OK;
 }

@@ -141,23 +141,24 @@ struct ItemQueue {
   }
   __device__ __forceinline__ bool next(int& b, int& seg, int& hk, int& part) {
     const int lane = threadIdx.x & 31;
-    const int64_t per_head = (int64_t)segs * parts;
+    // (the host has seen to it that all items together are below 2^31)
+    const unsigned per_head = (unsigned)segs * parts;
     // An item is taken only when the CTA is about to need it (its loads for the one before are all issued): taken one
     // ahead, with three or four items to a CTA, the long ones stayed where they had been given out (5 sequences of
     // 514 to 3314 tokens, 8 key heads: CTAs of 187 to 376 us in the dK, dV kernel).
-    int64_t item = blockIdx.x;
+    unsigned item = blockIdx.x;
     if (!first) {
       if (!counter) return false;
       unsigned t = 0;
       if (lane == 0) t = atomicAdd(counter, 1u);
-      item = (int64_t)grid + __shfl_sync(kFull, t, 0);
+      item = (unsigned)grid + __shfl_sync(kFull, t, 0);
     }
     first = false;
-    if (item >= per_head * s.Hkv) return false;
-    const int sec = (int)(item / (per_head * heads));
-    const int64_t in = item - sec * per_head * heads;
-    const int width = min(heads, s.Hkv - sec * heads);
-    const int rank = (int)(in / (width * parts)), rest = (int)(in - (int64_t)rank * (width * parts));
+    if (item >= per_head * (unsigned)s.Hkv) return false;
+    const unsigned per_section = per_head * (unsigned)heads;  // (of a full one)
+    const int sec = (int)(item / per_section);
+    const unsigned in = item - (unsigned)sec * per_section, width = (unsigned)(min(heads, s.Hkv - sec * heads) * parts);
+    const int rank = (int)(in / width), rest = (int)(in - (unsigned)rank * width);
     hk = sec * heads + rest / parts;
     part = rest % parts;
     if (sec != section) {
