@@ -77,14 +77,15 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
   }
 }
 
-// Rows [from, 128) of a tile of Q or dO as zeros; called by a whole warp.
+// Rows [from, 128) of a tile of Q or dO as zeros, four rows per step; called by a whole warp.  (With a division per store
+// instead it took 3000 cycles, and every key block of a sequence ends with such a tile.)
 template <int PANELS>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
-  const int n = (128 - from) * 8 * PANELS;
-  for (int q = threadIdx.x & 31; q < n; q += 32) {
-    const int row = from + (q >> 3) % (128 - from), p = (q >> 3) / (128 - from);
-    *reinterpret_cast<uint4*>(tile + p * 16384 + row * 128 + (q & 7) * 16) = make_uint4(0, 0, 0, 0);
-  }
+  const int lane = threadIdx.x & 31;
+  for (int row = from + (lane >> 3); row < 128; row += 4)
+#pragma unroll
+    for (int p = 0; p < PANELS; ++p)
+      *reinterpret_cast<uint4*>(tile + p * 16384 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
   fence_proxy_async();
   __syncwarp();
 }
@@ -209,17 +210,20 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
     const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * nb * s.G);
     uint32_t J = 0, nv = 0, qn = 0, don = 0;  // K, V, Q and dO tiles loaded
     bool ok = true;
-    for (uint32_t n = 0; ok; ++n) {
-      DqItem x{};
+    auto find = [&](DqItem& x) {
       int part;
-      const bool more = queue.next(x.b, x.tile, x.hk, part);
-      if (more) {
+      if (queue.next(x.b, x.tile, x.hk, part)) {
         x.lo = a.seqs.seq[x.b];
         x.n = a.seqs.seq[x.b + 1] - x.lo;
         x.rec = x.hk * plan.tile_recs + first_record(x.lo, nb, x.b) + x.tile;
       } else {
         x.hk = -1;
       }
+    };
+    DqItem x{}, after{};
+    find(x);
+    for (uint32_t n = 0; ok; ++n, x = after) {
+      const bool more = x.hk >= 0;
       const uint32_t i = n % kSlots;
       ok = n < (uint32_t)kSlots || __all_sync(kFull, mbar_wait(bar_taken(i), (n / kSlots - 1) & 1, wc));
       if (!ok) break;
@@ -228,9 +232,10 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
         mbar_arrive(bar_slot(i));
       }
       if (!more) break;
-      if (lane == 0) {
-        const int nk = key_blocks(keys_of(x)), tok = x.lo + x.tile * nb;
-        for (int j = 0; j < nk; ++j) {
+      const int nk = key_blocks(keys_of(x)), tok = x.lo + x.tile * nb;
+      for (int j = 0; ok && j < nk; ++j) {
+        if (j == max(nk - 2, 0)) find(after);  // while the blocks before are worked on
+        if (lane == 0) do {
           const int ks = J % kKSt, vs = nv % kVSt;
           if (J >= (uint32_t)kKSt && !mbar_wait(bar_kempty(ks), ((J / kKSt) - 1) & 1, wc)) {
             ok = false;
@@ -268,9 +273,9 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
             tma_load_5d(sbase + L::kOffV + vs * L::kTile + p * 16384, &mv, bar_vfull(vs), p * 64, 0,
                         x.lo + j * kKeyBlock, x.hk, 0);
           ++nv;
-        }
+        } while (false);
+        ok = __shfl_sync(kFull, ok, 0);
       }
-      ok = __shfl_sync(kFull, ok, 0);
     }
     // no copy may still be in flight when the CTA exits
     if (lane == 0) {
@@ -617,11 +622,9 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
     const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * used);
     uint32_t U = 0, kvn = 0;  // tiles, key blocks loaded
     bool ok = true;
-    for (uint32_t n = 0; ok;) {
-      DkvItem x{};
+    auto find = [&](DkvItem& x) {
       int b, part;
-      const bool more = queue.next(b, x.kb, x.hk, part);
-      if (more) {
+      while (queue.next(b, x.kb, x.hk, part)) {
         x.lo = a.seqs.seq[b];
         x.n = a.seqs.seq[b + 1] - x.lo;
         part_tiles(s, plan, x.n, x.kb, part, x.t0, x.nt);
@@ -629,9 +632,14 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
         x.rec = x.hk * plan.tile_recs + first_record(x.lo, nb, b);
         x.part = plan.parts == 1 ? -1
                                  : (x.hk * plan.block_recs + first_record(x.lo, kKeyBlock, b) + x.kb) * plan.parts + part;
-      } else {
-        x.hk = -1;
+        return;
       }
+      x.hk = -1;
+    };
+    DkvItem x{}, after{};
+    find(x);
+    for (uint32_t n = 0; ok; ++n, x = after) {
+      const bool more = x.hk >= 0;
       const uint32_t i = n % kSlots;
       ok = n < (uint32_t)kSlots || __all_sync(kFull, mbar_wait(bar_taken(i), (n / kSlots - 1) & 1, wc));
       if (!ok) break;
@@ -639,21 +647,23 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
         slots[i] = x;
         mbar_arrive(bar_slot(i));
       }
-      ++n;
       if (!more) break;
-      if (lane == 0 && (kvn == 0 || (ok = mbar_wait(bar_kvfree, (kvn - 1) & 1, wc)))) {
+      ok = kvn == 0 || __all_sync(kFull, mbar_wait(bar_kvfree, (kvn - 1) & 1, wc));
+      if (!ok) break;
+      if (lane == 0) {
         mbar_arrive_expect_tx(bar_kv, 2 * L::kTile);
         for (int p = 0; p < L::kPanels; ++p) {
           tma_load_5d(sbase + L::kOffK + p * 16384, &mk, bar_kv, p * 64, 0, x.lo + x.kb * kKeyBlock, x.hk, 0);
           tma_load_5d(sbase + L::kOffV + p * 16384, &mv, bar_kv, p * 64, 0, x.lo + x.kb * kKeyBlock, x.hk, 0);
         }
-        ++kvn;
-        for (int t = x.t0; t < x.t0 + x.nt; ++t, ++U) {
-          const int st = U % kStages;
-          if (U >= (uint32_t)kStages && !mbar_wait(bar_empty(st), ((U / kStages) - 1) & 1, wc)) {
-            ok = false;
-            break;
-          }
+      }
+      ++kvn;
+      for (int t = x.t0; ok && t < x.t0 + x.nt; ++t, ++U) {
+        const int st = U % kStages;
+        if (t == max(x.t0 + x.nt - 2, x.t0)) find(after);  // while the tiles before are worked on
+        ok = U < (uint32_t)kStages || __all_sync(kFull, mbar_wait(bar_empty(st), ((U / kStages) - 1) & 1, wc));
+        if (!ok) break;
+        if (lane == 0) {
           const uint32_t stg = sbase + L::kOffStage + st * L::kStage;
           mbar_arrive_expect_tx(bar_full(st), 2 * q_bytes + 1024);
           for (int p = 0; p < L::kPanels; ++p) {
@@ -663,7 +673,6 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
           bulk_load(stg + L::kStageStats, a.stats + (x.rec + t) * 256, 1024, bar_full(st));
         }
       }
-      ok = __shfl_sync(kFull, ok, 0);
     }
     if (lane == 0) {
       for (uint32_t v = U > (uint32_t)kStages ? U - kStages : 0; v < U; ++v)
@@ -675,8 +684,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
     constexpr uint32_t idS = idesc_bf16_f32(128, 64, false, false);
     const bool dp = warp == 3;
     const uint64_t akd = smem_desc(sbase + (dp ? L::kOffV : L::kOffK), 16, 1024);
-    const uint32_t in_stage = dp ? L::kStageDO : L::kStageQ;
-    const uint32_t bst = sbase + L::kOffStage + in_stage;
+    const uint32_t bst = sbase + L::kOffStage + (dp ? L::kStageDO : L::kStageQ);
     const uint32_t xst = sbase + L::kOffStage + L::kStageX + (dp ? kXTile : 0);
     const uint32_t dst = tmem + (dp ? kDP : kS), done = dp ? bar_dp(0) : bar_s(0), freed = dp ? bar_dkm(0) : bar_dvm(0);
     bool ok = true;
@@ -691,8 +699,13 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
                                    (u < kBufs || mbar_wait(freed + 8 * b, (u / kBufs - 1) & 1, wc)));
         if (!ok) break;
         if (!half) {
+          // (the issuer of S zeroes dO's rows too: dV reads them once P, made from S, is there)
           const int rows = rows_of(x, x.t0 + (i >> 1));
-          if (rows < used) zero_rows<L::kPanels>(smem + L::kOffStage + st * L::kStage + in_stage, rows);
+          uint8_t* tiles = smem + L::kOffStage + st * L::kStage;
+          if (rows < used) {
+            if (!dp) zero_rows<L::kPanels>(tiles + L::kStageQ, rows);
+            zero_rows<L::kPanels>(tiles + L::kStageDO, rows);
+          }
         }
         tc_fence_after();
         if (elect_one()) {
@@ -717,17 +730,10 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
     for (uint32_t n = 0; ok && take(n, x); ++n) {
       for (int i = 0; ok && i < 2 * x.nt; ++i, ++u) {
         const uint32_t U = u >> 1, st = U % kStages, half = u & 1, b = u % kBufs, use = (u / kBufs) & 1;
-        uint8_t* tiles = smem + L::kOffStage + st * L::kStage;
-        const uint32_t stg = smem_u32(tiles) + half * 8192;  // rows 64 .. of each panel
+        const uint32_t stg = sbase + L::kOffStage + st * L::kStage + half * 8192;  // rows 64 .. of each panel
         ok = __all_sync(kFull, (i > 0 || n == 0 || mbar_wait(bar_accfree, (n - 1) & 1, wc)) &&
                                    (half || mbar_wait(bar_full(st), (U / kStages) & 1, wc)) && mbar_wait(bar_p(b), use, wc));
         if (!ok) break;
-        if (!half) {
-          // (the issuer of dP zeroes the same rows, but has not been waited for; Q's were zeroed before S, which P
-          // was made from)
-          const int rows = rows_of(x, x.t0 + (i >> 1));
-          if (rows < used) zero_rows<L::kPanels>(tiles + L::kStageDO, rows);
-        }
         tc_fence_after();
         if (elect_one()) {
           issue_ts(tmem + kDV, tmem + kS + 64 * b, smem_desc(stg + L::kStageDO, 16384, 1024), idG, 4, i == 0);
