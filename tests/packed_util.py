@@ -29,11 +29,11 @@ def tokens(H, T, d, dtype, seed, scale=1.0, token_major=True):
     return x.transpose(0, 1) if token_major else x
 
 
-def allowed(n, m, causal):
+def allowed(n, m, causal, device):
     """[n, m]: the keys of each of the last n of m tokens."""
     if not causal:
-        return torch.ones((n, m), dtype=torch.bool, device="cuda")
-    return torch.arange(m, device="cuda") <= torch.arange(m - n, m, device="cuda")[:, None]
+        return torch.ones((n, m), dtype=torch.bool, device=device)
+    return torch.arange(m, device=device) <= torch.arange(m - n, m, device=device)[:, None]
 
 
 def attend(q, k, v, causal=True, scale=None):
@@ -41,7 +41,7 @@ def attend(q, k, v, causal=True, scale=None):
     H, n, d = q.shape
     G, m = H // k.shape[0], k.shape[1]
     scale = scale or 1.0 / math.sqrt(d)
-    keep = allowed(n, m, causal)
+    keep = allowed(n, m, causal, q.device)
     o, lse, a, ds = [], [], [], []
     for h in range(H):
         qq, kk, vv = q[h].double(), k[h // G].double(), v[h // G].double()
@@ -79,7 +79,7 @@ def gradients(q, k, v, do, causal=True, scale=None):
     H, n, d = q.shape
     G = H // k.shape[0]
     scale = scale or 1.0 / math.sqrt(d)
-    keep = allowed(n, n, causal)
+    keep = allowed(n, n, causal, q.device)
     z = lambda x: torch.zeros(x.shape, dtype=torch.float64, device=x.device)  # noqa: E731
     dq, dk, dv, aq, ak, av = z(q), z(k), z(v), z(q), z(k), z(v)
     for h in range(H):
