@@ -8,6 +8,9 @@
 //   half the products are left out, and P is cut element by element where a tile crosses the diagonal.
 // - The tiles of a key block, or the keys of a tile, are few for one and many for the next: work items come
 //   from a counter, the longest first (ItemQueue); warp 0 finds them and hands them to the others.
+// - dQ comes first: where a tile's keys are one block, the rows' D is summed anew from P and dP, D = sum_j P_j dP_j, and
+//   left for dK.  dO . O is off by the rounding of O, which for the first tokens of a sequence, whose O is as large as a
+//   single V, is as much as dS's own rounding; with more keys O is the smaller, and with it what D is off by.
 // - Behind a sequence's last token lie the next one's: rows of Q and dO there are zeroed in shared memory (their P
 //   is 0, but 0 * NaN is NaN), and results are stored row by row.
 #include <algorithm>
@@ -100,6 +103,36 @@ struct DqItem {
   int b, pad;
 };
 
+// One 32-bit TMEM column of a thread's lane, and the sum of N of them, STEP columns apart.
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
+}
+template <int N, int STEP>
+__device__ __forceinline__ float tmem_sum(uint32_t taddr) {
+  static_assert(N == 2 || N == 4, "threads per row");
+  uint32_t r[4] = {0, 0, 0, 0};
+  if constexpr (N == 2)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%2];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%3];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1])
+        : "r"(taddr), "r"(taddr + STEP)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%4];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%5];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%6];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%3}, [%7];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3])
+        : "r"(taddr), "r"(taddr + STEP), "r"(taddr + 2 * STEP), "r"(taddr + 3 * STEP)
+        : "memory");
+  const float x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  return N == 2 ? x : x + (__uint_as_float(r[2]) + __uint_as_float(r[3]));
+}
+
 template <int D>
 struct DqSmem {
   static constexpr int kRowWarps = D == 128 ? 8 : 16;
@@ -144,6 +177,7 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
   const uint32_t bar_drain = smem_u32(&bars[24]), bar_gdrain = smem_u32(&bars[25]), bar_pdrain = smem_u32(&bars[26]);
   auto bar_slot = [&](uint32_t i) { return smem_u32(&bars[27 + i]); };            // an item handed out
   auto bar_taken = [&](uint32_t i) { return smem_u32(&bars[27 + kSlots + i]); };  // ... and read by every other warp
+  const uint32_t bar_sum = smem_u32(&bars[27 + 2 * kSlots]);                      // shares of D in TMEM
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 384);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffBar + 392);
   DqItem* slots = reinterpret_cast<DqItem*>(smem + L::kOffSlot);
@@ -169,6 +203,7 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
     mbar_init(bar_dofree, 1);
     mbar_init(bar_s, 1);
     mbar_init(bar_sfree, 32 * L::kRowWarps);
+    mbar_init(bar_sum, 32 * L::kRowWarps);
     mbar_init(bar_dq, 1);
     mbar_init(bar_dqfree, 128);
     mbar_init(bar_drain, 1);
@@ -205,7 +240,7 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------- work finder and TMA producer
-    const bool in_order = seqs_in_order(s, a.seqs, false, a.status);
+    const bool in_order = seqs_in_order(s, a.seqs, blockIdx.x == 0, a.status);
     ItemQueue queue(s, a.seqs, nb, 1, plan.heads, plan.dq_grid, false, a.counter + 1, in_order);
     const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * nb * s.G);
     uint32_t J = 0, nv = 0, qn = 0, don = 0;  // K, V, Q and dO tiles loaded
@@ -374,12 +409,13 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
     const int r = 32 * (warp & 3) + lane, tok_r = r / s.G;
     const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     bool ok = true;
-    uint32_t J = 0;
+    uint32_t J = 0, sums = 0;
     DqItem x;
     for (uint32_t n = 0; ok && take(n, x); ++n) {
       const int keys = keys_of(x), nk = key_blocks(keys);
       const int mine = s.causal ? min(keys, x.tile * nb + tok_r + 1) : keys;  // keys of this row
-      const float lse2 = a.stats[x.rec * 256 + r], Dr = a.stats[x.rec * 256 + 128 + r];
+      const float lse2 = a.stats[x.rec * 256 + r];
+      float Dr = a.stats[x.rec * 256 + 128 + r];
       for (int j = 0; j < nk; ++j, ++J) {
         const int bb = J & 1;
         const int valid = mine - j * kKeyBlock - k0;  // of this thread's keys
@@ -394,8 +430,10 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
         for (int h = 0; h < kKeys / 32; ++h) tmem_ld32(trow + kS + k0 + 32 * h, u[h]);
 #pragma unroll
         for (int h = 0; h < kKeys / 32; ++h) tmem_ld_wait(u[h]);
-        tc_fence_before();
-        mbar_arrive(bar_sfree);
+        if (nk > 1) {
+          tc_fence_before();
+          mbar_arrive(bar_sfree);
+        }
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) p[c] = ex2(fmaf(__uint_as_float(u[c >> 5][c & 31]), a.scale_log2, -lse2));
         if (!__all_sync(kFull, mbar_wait(bar_dp(bb), (J >> 1) & 1, wc))) {
@@ -404,6 +442,38 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
         }
         tc_fence_after();
         const uint32_t tdp = trow + kDP + bb * 128 + k0;
+        if (nk == 1) {
+          // D anew: this thread's share into the first of its columns of S, which it has read, then all of the row's
+          float share = 0.f;
+#pragma unroll 1
+          for (int q = 0; q < kKeys / 16; ++q) {
+            uint32_t v[16];
+            tmem_ld16(tdp + 16 * q, v);
+            tmem_ld_wait16(v);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              // (p by its place: the loop is not unrolled, and p has to stay in registers)
+              float pc = 0.f;
+#pragma unroll
+              for (int w = 0; w < kKeys / 16; ++w) pc = w == q ? p[16 * w + c] : pc;
+              if (16 * q + c < valid) share = fmaf(pc, __uint_as_float(v[c]), share);
+            }
+          }
+          tmem_st1(trow + kS + k0, share);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar_sum);
+          if (!__all_sync(kFull, mbar_wait(bar_sum, sums & 1, wc))) {
+            ok = false;
+            break;
+          }
+          ++sums;
+          tc_fence_after();
+          Dr = tmem_sum<L::kRowWarps / 4, kKeys>(trow + kS);
+          tc_fence_before();
+          mbar_arrive(bar_sfree);
+          if (k0 == 0) a.stats[x.rec * 256 + 128 + r] = lse2 == INFINITY ? 0.f : Dr;  // (0: a row without a query)
+        }
 #pragma unroll
         for (int h = 0; h < kKeys / 32; ++h) {
           uint32_t pk[16];
@@ -617,7 +687,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------- work finder and TMA producer
-    const bool in_order = seqs_in_order(s, a.seqs, blockIdx.x == 0, a.status);
+    const bool in_order = seqs_in_order(s, a.seqs, false, a.status);
     ItemQueue queue(s, a.seqs, kKeyBlock, plan.parts, plan.heads, plan.grid, true, a.counter, in_order);
     const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * used);
     uint32_t U = 0, kvn = 0;  // tiles, key blocks loaded
@@ -924,7 +994,7 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_dkdv_join_kernel(const __grid_constant__ PackedShape s,
                                                               const __grid_constant__ PackedBwdPlan plan,
                                                               const __grid_constant__ PackedBwdArgs a) {
-  kernel_wait();  // (by every CTA: the dQ kernel waits for this one alone)
+  kernel_wait();
   kernel_trigger();
   const int b = sequence_of_record(s, a.seqs, kKeyBlock, (int)blockIdx.x);
   const int lo = a.seqs.seq[b], n = a.seqs.seq[b + 1] - lo;
@@ -967,15 +1037,15 @@ cudaError_t launch_t(const PackedShape& s, const PackedBwdPlan& p, const CUtenso
   e = launch_early(packed_stats_kernel<D>, dim3((unsigned)p.tile_recs, (unsigned)s.Hkv, 128 / kStatsRows<D>), 256, 0, st, s, p, a);
   prof_stop(st, kBwdPre);
   if (e != cudaSuccess) return e;
+  prof_start(st, kAttnBwdDq);
+  e = launch_early(dq, dim3((unsigned)p.dq_grid), DqSmem<D>::kThreads, DqSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
+  prof_stop(st, kAttnBwdDq);
+  if (e != cudaSuccess) return e;
   prof_start(st, kAttnBwd);
   e = launch_early(dkv, dim3((unsigned)p.grid), DkvSmem<D>::kThreads, DkvSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
   if (e == cudaSuccess && p.parts > 1)
     e = launch_early(packed_dkdv_join_kernel<D>, dim3((unsigned)p.block_recs, (unsigned)s.Hkv, kJoinParts), 256, 0, st, s, p, a);
   prof_stop(st, kAttnBwd);
-  if (e != cudaSuccess) return e;
-  prof_start(st, kAttnBwdDq);
-  e = launch_early(dq, dim3((unsigned)p.dq_grid), DqSmem<D>::kThreads, DqSmem<D>::kBytes, st, mq, mk, mv, mdo, s, p, a);
-  prof_stop(st, kAttnBwdDq);
   return e;
 }
 
