@@ -45,8 +45,9 @@ struct FewWalk {
     if (!seqs_in_order(s, q, blockIdx.x == 0, status)) return;
     int64_t total = 0, segs = 0;
     int most = 0;
+    const int first = blocks(lane);
     for (int b = lane; b < s.B; b += 32) {
-      const int k = blocks(b);
+      const int k = b == lane ? first : blocks(b);
       total += k;
       segs += k > 0;
       most = max(most, k);
@@ -59,8 +60,8 @@ struct FewWalk {
     if (whole) {
       g = begin = blockIdx.x;
       g_end = g < segs ? g + 1 : g;
-      off = g / s.Hkv;
-      hk = (int)(g - off * s.Hkv);
+      hk = (int)blockIdx.x % s.Hkv;
+      off = (int)blockIdx.x / s.Hkv;
     } else {
       run = run_length(total, gridDim.x);
       g = begin = run * blockIdx.x;
@@ -70,20 +71,29 @@ struct FewWalk {
     if (g >= g_end) return;
     // the sequence: whole, the off-th of this kernel; else that of block off
     for (int c = 0;; c += 32) {  // (found)
-      const int k = blocks(c + lane);
-      const int64_t mine = whole ? (k > 0) : (int64_t)k * s.Hkv, to = warp_scan(mine);
-      const unsigned in = __ballot_sync(kFull, off < to);
+      const int k = c == 0 ? first : blocks(c + lane);
+      unsigned in;
+      int64_t mine = 0, to = 0;
+      if (whole) {
+        const unsigned some = __ballot_sync(kFull, k > 0);
+        in = __ballot_sync(kFull, k > 0 && __popc(some & ((1u << lane) - 1)) == (int)off);
+        to = __popc(some);
+      } else {
+        mine = (int64_t)k * s.Hkv;
+        to = warp_scan(mine);
+        in = __ballot_sync(kFull, off < to);
+      }
       if (in) {
         const int src = __ffs(in) - 1;
         at = c + src;
         nblk = __shfl_sync(kFull, k, src);
-        off -= __shfl_sync(kFull, to - mine, src);
+        if (!whole) off -= __shfl_sync(kFull, to - mine, src);
         break;
       }
       off -= __shfl_sync(kFull, to, 31);
     }
     if (!whole) {
-      hk = (int)(off / nblk);
+      hk = off < (1 << 30) ? (int)off / nblk : (int)(off / nblk);
       cut = (int)(off - (int64_t)hk * nblk);
     }
   }
@@ -155,6 +165,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint16_t* kp = static_cast<const uint16_t*>(a.k.p) + x.hk * a.k.sh;
     const uint16_t* vp = static_cast<const uint16_t*>(a.v.p) + x.hk * a.v.sh;
     const int32_t* row = a.seqs.table + x.b * s.table_stride;
+    // Q's fragments: rows g and g + 8; of each, this thread's channels in the order of its K chunks (asked for first:
+    // they are back when the pages' numbers are)
+    uint32_t w[2][2 * kKS];
+    int lim[2];  // keys before which a row's keys end
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = g + 8 * hf, n = r / s.G, h = x.hk * s.G + r - n * s.G;
+      const bool live = r < rows;
+      lim[hf] = s.causal && live ? min(key1, x.pos + n + 1) : key1;
+      const uint16_t* qp = static_cast<const uint16_t*>(a.q.p) + h * a.q.sh + (int64_t)(x.qtok + n) * a.q.sn;
+#pragma unroll
+      for (int i = 0; i < 2 * kKS; i += 4) {  // a chunk: values 2 i .. 2 i + 7 of the thread's list
+        const int ci = 2 * i / T::kPer, c = 2 * t + (ci & 1) + 8 * (ci >> 1);
+        const uint4 u = live ? *reinterpret_cast<const uint4*>(qp + c * T::kPer) : make_uint4(0, 0, 0, 0);
+        w[hf][i] = u.x;
+        w[hf][i + 1] = u.y;
+        w[hf][i + 2] = u.z;
+        w[hf][i + 3] = u.w;
+      }
+    }
     // step i of this warp: keys from key0 + (i * kWarps + warp) * kKeys on
     const int steps_all = (key1 - key0 + T::kKeys - 1) / T::kKeys;
     const int steps = steps_all > warp ? (steps_all - warp + kWarps - 1) / kWarps : 0;
@@ -202,28 +232,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) copy_step(i);
 
-    // Q's fragments: rows g and g + 8; of each, this thread's channels in the order of its K chunks
     uint32_t qf[kKS][4];
-    int lim[2];  // keys before which a row's keys end
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = g + 8 * hf, n = r / s.G, h = x.hk * s.G + r - n * s.G;
-      const bool live = r < rows;
-      lim[hf] = s.causal && live ? min(key1, x.pos + n + 1) : key1;
-      const uint16_t* qp = static_cast<const uint16_t*>(a.q.p) + h * a.q.sh + (int64_t)(x.qtok + n) * a.q.sn;
-      uint32_t w[2 * kKS];
+    for (int k = 0; k < kKS; ++k)
 #pragma unroll
-      for (int i = 0; i < 2 * kKS; ++i) {  // pair i: values 2 i, 2 i + 1 of the thread's list
-        const int pos = 2 * i, ci = pos / T::kPer;
-        const int c = 2 * t + (ci & 1) + 8 * (ci >> 1);
-        w[i] = live ? *reinterpret_cast<const uint32_t*>(qp + c * T::kPer + pos % T::kPer) : 0u;
+      for (int hf = 0; hf < 2; ++hf) {
+        qf[k][hf] = w[hf][2 * k];
+        qf[k][2 + hf] = w[hf][2 * k + 1];
       }
-#pragma unroll
-      for (int k = 0; k < kKS; ++k) {
-        qf[k][hf] = w[2 * k];
-        qf[k][2 + hf] = w[2 * k + 1];
-      }
-    }
 
     float o[kCT][4] = {};
     float m_used[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};  // reference of the exponentials; sum of exp2(s) relative to it
