@@ -52,8 +52,8 @@ struct FewWalk {
       segs += k > 0;
       most = max(most, k);
     }
-    total = warp_sum(total) * s.Hkv;
-    segs = warp_sum(segs) * s.Hkv;
+    total = warp_total(total) * s.Hkv;
+    segs = warp_total(segs) * s.Hkv;
     most = __reduce_max_sync(kFull, most);
     whole = segs <= (int64_t)gridDim.x && most <= kFewWhole;
     int64_t off;

@@ -10,8 +10,12 @@ namespace sa2 {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// Sum over the warp of numbers below 2^52, none negative.
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  return x;
+}
+// The same of numbers below 2^52, none negative, in two instructions (and more registers).
+__device__ __forceinline__ int64_t warp_total(int64_t x) {
   const unsigned lo = __reduce_add_sync(kFull, (unsigned)x & 0x3FFFFFFu), hi = __reduce_add_sync(kFull, (unsigned)(x >> 26));
   return (int64_t)lo + ((int64_t)hi << 26);
 }
