@@ -674,13 +674,20 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
   kernel_wait();
   kernel_trigger();
 
-  auto take = [&](uint32_t n, DkvItem& x) {
+  // The n-th item, for every warp but 0, which may read it until it has left it; false where there is none.
+  auto look = [&](uint32_t n) {
     const uint32_t i = n % kSlots;
-    if (!__all_sync(kFull, mbar_wait(bar_slot(i), (n / kSlots) & 1, wc))) return false;
-    x = slots[i];
+    return __all_sync(kFull, mbar_wait(bar_slot(i), (n / kSlots) & 1, wc)) && slots[i].hk >= 0;
+  };
+  auto leave = [&](uint32_t n) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_taken(i));
-    return x.hk >= 0;
+    if (lane == 0) mbar_arrive(bar_taken(n % kSlots));
+  };
+  auto take = [&](uint32_t n, DkvItem& x) {
+    if (!look(n)) return false;
+    x = slots[n % kSlots];
+    leave(n);
+    return true;
   };
   // rows of tile t that hold queries
   auto rows_of = [&](const DkvItem& x, int t) { return min(nb, x.n - t * nb) * s.G; };
@@ -860,16 +867,16 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
     const uint32_t ts0 = trow + kS + 32 * g + (kBufs == 2 ? 64 * half : 0);
     bool ok = true;
     uint32_t U = 0;  // tiles
-    DkvItem x;
-    for (uint32_t n = 0; ok && take(n, x); ++n) {
-      for (int t = x.t0; t < x.t0 + x.nt; ++t, ++U) {
+    for (uint32_t n = 0; ok && look(n); leave(n), ++n) {
+      const int kb = slots[n % kSlots].kb, t1 = slots[n % kSlots].t0 + slots[n % kSlots].nt;
+      for (int t = slots[n % kSlots].t0; t < t1; ++t, ++U) {
         const uint32_t u = 2 * U + half, b = kBufs == 2 ? half : u % kBufs, use = (kBufs == 2 ? U : u / kBufs) & 1;
         const uint32_t ts = kBufs == 2 ? ts0 : ts0 + 64 * b, tdp = ts + kDP - kS;
         const int st = U % kStages;
         // Row c of this thread's 32 holds token floor(row / G) of the tile; where causal it reads this thread's key
         // from the row on in which that token stands: rows before `cut` are masked.
-        const int cut = s.causal ? (x.kb * kKeyBlock + r - t * nb) * s.G - 64 * (int)half - 32 * g : 0;
-        const bool diagonal = s.causal && t * nb < x.kb * kKeyBlock + kKeyBlock - 1;
+        const int cut = s.causal ? (kb * kKeyBlock + r - t * nb) * s.G - 64 * (int)half - 32 * g : 0;
+        const bool diagonal = s.causal && t * nb < kb * kKeyBlock + kKeyBlock - 1;
         const float4* l4 = reinterpret_cast<const float4*>(smem + L::kOffStage + st * L::kStage + L::kStageStats) +
                            16 * half + 8 * g;
         const float4* d4 = l4 + 32;
@@ -943,6 +950,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
         break;
       }
       tc_fence_after();
+      const DkvItem x = slots[n % kSlots];
       const int key = x.kb * kKeyBlock + r, quarter = 2 * (int)half + g;
       const bool live = key < x.n;
 #pragma unroll 1
