@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
     DqItem x;
     for (uint32_t n = 0; ok && take(n, x); ++n) {
       const int keys = keys_of(x), nk = key_blocks(keys);
-      const int mine = s.causal ? min(keys, x.tile * nb + tok_r + 1) : keys;  // keys of this row
+      // keys that this row has a gradient to: none where there is one, whose P is 1 whatever its score
+      int mine = s.causal ? min(keys, x.tile * nb + tok_r + 1) : keys;
+      if (mine == 1) mine = 0;
       const float lse2 = a.stats[x.rec * 256 + r];
       float Dr = a.stats[x.rec * 256 + 128 + r];
       for (int j = 0; j < nk; ++j, ++J) {
@@ -549,6 +551,7 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
 struct DkvItem {
   int lo, n, hk, kb, t0, nt;
   int64_t rec, part;
+  int masked, pad;  // a token sees those up to itself (causal, or a token alone)
 };
 
 template <int D>
@@ -706,6 +709,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
         x.n = a.seqs.seq[b + 1] - x.lo;
         part_tiles(s, plan, x.n, x.kb, part, x.t0, x.nt);
         if (x.nt == 0) continue;
+        x.masked = s.causal || x.n == 1;
         x.rec = x.hk * plan.tile_recs + first_record(x.lo, nb, b);
         x.part = plan.parts == 1 ? -1
                                  : (x.hk * plan.block_recs + first_record(x.lo, kKeyBlock, b) + x.kb) * plan.parts + part;
@@ -868,15 +872,15 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
     bool ok = true;
     uint32_t U = 0;  // tiles
     for (uint32_t n = 0; ok && look(n); leave(n), ++n) {
-      const int kb = slots[n % kSlots].kb, t1 = slots[n % kSlots].t0 + slots[n % kSlots].nt;
+      const int kb = slots[n % kSlots].masked ? slots[n % kSlots].kb : -1, t1 = slots[n % kSlots].t0 + slots[n % kSlots].nt;
       for (int t = slots[n % kSlots].t0; t < t1; ++t, ++U) {
         const uint32_t u = 2 * U + half, b = kBufs == 2 ? half : u % kBufs, use = (kBufs == 2 ? U : u / kBufs) & 1;
         const uint32_t ts = kBufs == 2 ? ts0 : ts0 + 64 * b, tdp = ts + kDP - kS;
         const int st = U % kStages;
-        // Row c of this thread's 32 holds token floor(row / G) of the tile; where causal it reads this thread's key
-        // from the row on in which that token stands: rows before `cut` are masked.
-        const int cut = s.causal ? (kb * kKeyBlock + r - t * nb) * s.G - 64 * (int)half - 32 * g : 0;
-        const bool diagonal = s.causal && t * nb < kb * kKeyBlock + kKeyBlock - 1;
+        // Row c of this thread's 32 holds token floor(row / G) of the tile; where masked (kb >= 0) it reads this
+        // thread's key from the row on in which that token stands: rows before `cut` are masked.
+        const int cut = (kb * kKeyBlock + r - t * nb) * s.G - 64 * (int)half - 32 * g;
+        const bool diagonal = kb >= 0 && t * nb < kb * kKeyBlock + kKeyBlock - 1;
         const float4* l4 = reinterpret_cast<const float4*>(smem + L::kOffStage + st * L::kStage + L::kStageStats) +
                            16 * half + 8 * g;
         const float4* d4 = l4 + 32;
@@ -934,9 +938,10 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
                 pack_bf16x2(pp[2] * (__uint_as_float(v[4 * q + 2]) - d.z), pp[3] * (__uint_as_float(v[4 * q + 3]) - d.w));
           }
         }
-        if (diagonal) {  // (dP of a masked place may be anything)
+        if (diagonal) {  // (dP of a masked place may be anything; a sequence's first token sees one key: dS = 0)
+          const int cut_ds = kb == 0 && t == 0 ? max(cut, s.G - 64 * (int)half - 32 * g) : cut;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] = 2 * c + 1 < cut ? 0u : (2 * c < cut ? pk[c] & 0xFFFF0000u : pk[c]);
+          for (int c = 0; c < 16; ++c) pk[c] = 2 * c + 1 < cut_ds ? 0u : (2 * c < cut_ds ? pk[c] & 0xFFFF0000u : pk[c]);
         }
         tmem_st16(tdp, pk);
         tmem_st_wait();

@@ -40,6 +40,26 @@ def test_short(sa2, lens, d):
     run(sa2, lens, 4, 2, d, norm=False)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_single_key_has_no_gradient(sa2, causal, d):
+    """The weight of a row's only key is 1 whatever its score: dQ of a token alone (where causal, of a sequence's first
+    one) is 0 to the bit, so is dK of a token alone, and dV is dO, summed over the heads that share it."""
+    lens = [1, 1, 5, 1, 140]
+    at = places(lens)
+    q, k, v, do = (tokens(h, at[-1], d, BF16, i) for i, h in enumerate((4, 2, 2, 4)))
+    seq = torch.tensor(at, **I32)
+    o, lse = sa2.packed_attn_fwd(q, k, v, seq, causal=causal)
+    dq, dk, dv = sa2.packed_attn_bwd(q, k, v, o, lse, do, seq, causal=causal)
+    sa2.check_device()
+    alone = [0, 1, 7]
+    assert not dq[:, alone].any() and not dk[:, alone].any() and bool(dq[:, 3].any()) and bool(dk[:, 2].any())
+    assert bool(dq[:, [2, 8]].any()) != causal
+    both = do[:, alone].float().view(2, 2, 3, d).sum(1)
+    assert float((dv[:, alone].float() - both).abs().max()) <= 2.0**-8 * float(both.abs().max())
+    check_gradients((dq, dk, dv), q, k, v, do, at, causal, norm=False)
+
+
 @pytest.mark.parametrize("lens", [[127], [128], [129], [255, 0, 257], [300, 0, 177, 513], [700]], ids=str)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [True, False])
