@@ -574,11 +574,21 @@ struct DkvSmem {
                 "shared memory: one CTA per SM");
 };
 
-// Query tiles of part i of key block kb of a sequence of n tokens.
+// Query tiles of key block kb of a sequence of n tokens: the first, and how many (one at least).
+__device__ __forceinline__ int first_tile(const PackedShape& s, const PackedBwdPlan& p, int kb) {
+  return s.causal ? kb * kKeyBlock / p.nb : 0;
+}
+__device__ __forceinline__ int tile_count(const PackedShape& s, const PackedBwdPlan& p, int n, int kb) {
+  return (n + p.nb - 1) / p.nb - first_tile(s, p, kb);
+}
+// Part i of them; where the tiles are fewer than plan.parts, the last parts are empty.
 __device__ __forceinline__ void part_tiles(const PackedShape& s, const PackedBwdPlan& p, int n, int kb, int i, int& t0, int& nt) {
-  const int first = s.causal ? kb * kKeyBlock / p.nb : 0, tiles = (n + p.nb - 1) / p.nb - first;
-  t0 = first + (int)((int64_t)tiles * i / p.parts);
-  nt = first + (int)((int64_t)tiles * (i + 1) / p.parts) - t0;
+  t0 = first_tile(s, p, kb);
+  nt = tile_count(s, p, n, kb);
+  if (p.parts == 1) return;
+  const int each = nt / p.parts, more = nt - each * p.parts;  // the first `more` parts have one tile more
+  t0 += each * i + min(i, more);
+  nt = each + (i < more);
 }
 
 template <int D>
@@ -1015,19 +1025,17 @@ __global__ void __launch_bounds__(256) packed_dkdv_join_kernel(const __grid_cons
   const bool in_order = seqs_in_order(s, a.seqs, false, a.status);
   if (!in_order || kb < 0 || n < 1 || kb >= key_blocks(n)) return;
   constexpr int kItems = 2 * 128 * (D / 8) / kJoinParts;
+  const int parts = min(plan.parts, tile_count(s, plan, n, kb));  // (no others have been written)
   for (int j = threadIdx.x; j < kItems; j += 256) {
     const int i = blockIdx.z * kItems + j;
     const int w = i / (128 * (D / 8)), r = i / (D / 8) % 128, ch = i % (D / 8) * 8;
     const int key = kb * kKeyBlock + r;
     if (key >= n) continue;
     float v[8] = {};
-    for (int k = 0; k < plan.parts; ++k) {
-      int t0, nt;
-      part_tiles(s, plan, n, kb, k, t0, nt);
-      if (nt == 0) continue;  // (not written)
-      const int64_t at = (hk * plan.block_recs + blockIdx.x) * plan.parts + k;
-      const float4* p = reinterpret_cast<const float4*>(a.part + ((at * 2 + w) * 128 + r) * D + ch);
-      const float4 x = p[0], y = p[1];
+    const float* p = a.part + (((hk * plan.block_recs + blockIdx.x) * plan.parts * 2 + w) * 128 + r) * D + ch;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k, p += 2 * 128 * D) {
+      const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
       v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
       v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
     }

@@ -31,8 +31,10 @@ struct FewWalk {
   const PackedSeqs& q;
   const int lane;
   bool whole;
-  int64_t g, g_end, run, begin;  // whole: the segment; else blocks
+  int64_t g, g_end, run, begin;  // whole: the next segment and their number; else blocks
   int at, nblk, hk, cut;
+  int chunk, before;  // whole: the 32 sequences looked at last, and how many of this kernel lie before them
+  int mine;           // blocks of sequence `lane`
 
   __device__ __forceinline__ int blocks(int b) const {  // 0: not a sequence of this kernel
     const int n = b < s.B ? q.seq[b + 1] - q.seq[b] : 0;
@@ -40,65 +42,77 @@ struct FewWalk {
     const int k = key_blocks(seq_info(s, q, b).keys, 6);
     return k > 0 ? k : 1;
   }
-  __device__ __forceinline__ FewWalk(const PackedShape& s_, const PackedSeqs& q_, unsigned* status)
-      : s(s_), q(q_), lane(threadIdx.x & 31), whole(false), g(0), g_end(0), run(1), begin(0), at(0), nblk(0), hk(0), cut(0) {
+  __device__ __forceinline__ FewWalk(const PackedShape& s_, const PackedSeqs& q_, bool may_split, unsigned* status)
+      : s(s_), q(q_), lane(threadIdx.x & 31), whole(false), g(0), g_end(0), run(1), begin(0), at(0), nblk(0), hk(0), cut(0),
+        chunk(0), before(0), mine(0) {
     if (!seqs_in_order(s, q, blockIdx.x == 0, status)) return;
-    int64_t total = 0, segs = 0;
-    int most = 0;
-    const int first = blocks(lane);
+    int64_t total = 0;
+    int segs = 0, most = 0;
+    mine = blocks(lane);
     for (int b = lane; b < s.B; b += 32) {
-      const int k = b == lane ? first : blocks(b);
+      const int k = b == lane ? mine : blocks(b);
       total += k;
       segs += k > 0;
       most = max(most, k);
     }
     total = warp_total(total) * s.Hkv;
-    segs = warp_total(segs) * s.Hkv;
+    const int64_t all = (int64_t)__reduce_add_sync(kFull, segs) * s.Hkv;
     most = __reduce_max_sync(kFull, most);
-    whole = segs <= (int64_t)gridDim.x && most <= kFewWhole;
-    int64_t off;
+    // Few short segments are never cut: their CTAs share the bandwidth with no others.  Else, in blocks of keys: a piece
+    // takes as long as kPiece more (its pages are looked up, the first keys come, warps are joined), the kernel that
+    // joins parts kJoin, and segments' own lengths leave CTAs half a longest one's excess apart.  (12 key heads of
+    // d = 128, 32 sequences of up to 300 keys: 15.6 us whole, 19.1 us in runs; 8 key heads, 64 sequences of 700 keys:
+    // 46.6 us whole, 43.7 us in runs; 16 of up to 32760: 178 us in runs, where the longest segment alone is 17 MB,
+    // 420 us at a CTA's share of the bandwidth.)
+    constexpr float kPiece = 1.5f, kJoin = 4.5f;
+    const float share = 1.f / gridDim.x, mean = all > 0 ? (float)total / all : 0.f;
+    const float in_whole = fmaxf(ceilf(all * share) * (mean + kPiece) + .5f * (most - mean), most + kPiece);
+    const float in_runs = total * share + kPiece * (1.f + all * share) + kJoin;
+    whole = !may_split || (all <= gridDim.x && most <= kFewWhole) || in_whole <= in_runs;
     if (whole) {
-      g = begin = blockIdx.x;
-      g_end = g < segs ? g + 1 : g;
-      hk = (int)blockIdx.x % s.Hkv;
-      off = (int)blockIdx.x / s.Hkv;
-    } else {
-      run = run_length(total, gridDim.x);
-      g = begin = run * blockIdx.x;
-      g_end = g + run < total ? g + run : total;
-      off = g;
+      g = blockIdx.x;
+      g_end = all;
+      return;
     }
+    run = run_length(total, gridDim.x);
+    begin = g = run * blockIdx.x;
+    g_end = g + run < total ? g + run : total;
     if (g >= g_end) return;
-    // the sequence: whole, the off-th of this kernel; else that of block off
+    // the sequence of block g
+    int64_t off = g;
     for (int c = 0;; c += 32) {  // (found)
-      const int k = c == 0 ? first : blocks(c + lane);
-      unsigned in;
-      int64_t mine = 0, to = 0;
-      if (whole) {
-        const unsigned some = __ballot_sync(kFull, k > 0);
-        in = __ballot_sync(kFull, k > 0 && __popc(some & ((1u << lane) - 1)) == (int)off);
-        to = __popc(some);
-      } else {
-        mine = (int64_t)k * s.Hkv;
-        to = warp_scan(mine);
-        in = __ballot_sync(kFull, off < to);
-      }
+      const int k = c == 0 ? mine : blocks(c + lane);
+      const int64_t here = (int64_t)k * s.Hkv, to = warp_scan(here);
+      const unsigned in = __ballot_sync(kFull, off < to);
       if (in) {
         const int src = __ffs(in) - 1;
         at = c + src;
         nblk = __shfl_sync(kFull, k, src);
-        if (!whole) off -= __shfl_sync(kFull, to - mine, src);
+        off -= __shfl_sync(kFull, to - here, src);
         break;
       }
       off -= __shfl_sync(kFull, to, 31);
     }
-    if (!whole) {
-      hk = off < (1 << 30) ? (int)off / nblk : (int)(off / nblk);
-      cut = (int)(off - (int64_t)hk * nblk);
-    }
+    hk = off < (1 << 30) ? (int)off / nblk : (int)(off / nblk);
+    cut = (int)(off - (int64_t)hk * nblk);
   }
   __device__ __forceinline__ bool next(FewPiece& y, CutRecord& rec) {
     if (g >= g_end) return false;
+    if (whole) {  // segment g: the key head of a sequence of this kernel, in order
+      const int seg = (int)(g / s.Hkv);
+      hk = (int)(g - (int64_t)seg * s.Hkv);
+      for (;; chunk += 32) {  // (found)
+        const int k = chunk == 0 ? mine : blocks(chunk + lane);
+        const unsigned some = __ballot_sync(kFull, k > 0);
+        const unsigned in = __ballot_sync(kFull, k > 0 && before + __popc(some & ((1u << lane) - 1)) == seg);
+        if (in) {
+          at = chunk + __ffs(in) - 1;
+          nblk = __shfl_sync(kFull, k, __ffs(in) - 1);
+          break;
+        }
+        before += __popc(some);
+      }
+    }
     const SeqInfo x = seq_info(s, q, at);
     y.b = at;
     y.qtok = x.lo;
@@ -110,7 +124,7 @@ struct FewWalk {
     if (whole) {
       y.nb = nblk;
       y.slot = -1;
-      g = g_end;
+      g += gridDim.x;
       return true;
     }
     const int64_t left = g_end - g;
@@ -149,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   kernel_trigger();
   const int page_shift = __ffs(s.page) - 1;
 
-  FewWalk walk(s, a.seqs, a.status);  // (walked on by warp 0)
+  FewWalk walk(s, a.seqs, plan.few_split, a.status);  // (walked on by warp 0)
   CutRecord rec{0, 0, 0, 0, 0, 0, 0, 0};
   for (;;) {
     if (warp == 0) {

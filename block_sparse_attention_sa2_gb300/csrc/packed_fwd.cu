@@ -712,7 +712,7 @@ PackedPlan packed_fwd_plan(PackedShape* shape, int sms) {
     s.few = kFewRows / s.G;
     const int64_t segs = (int64_t)s.Hkv * std::min(s.B, s.T), blocks = (most_keys + 63) / 64;
     p.few_grid = (int)std::min<int64_t>(sms, segs * blocks);
-    p.few_split = segs > p.few_grid || blocks > kFewWhole;
+    p.few_split = blocks > (segs > sms ? 4 : kFewWhole);  // (never cut where the table has no room for longer ones)
   }
   p.tiles = s.max_new > s.few;
   if (!p.tiles) return p;

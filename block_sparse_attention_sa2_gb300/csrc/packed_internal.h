@@ -41,7 +41,7 @@ struct PackedSeqs {
 //
 // Over a paged cache, sequences whose new tokens' rows are at most kFewRows (single tokens) go to a kernel of their
 // own, packed_few.cu: a tile of 128 rows would be nearly empty.  It cuts the 64-key blocks of their segments (one for
-// each key head) into equal runs too, or, where there are no more segments than CTAs and none is long, takes them whole.
+// each key head) into equal runs too, or takes them whole, by which takes less at their lengths.
 struct PackedPlan {
   int few_grid;    // CTAs of the kernel for few rows; 0: not launched
   int few_split;   // its segments may be cut
@@ -79,7 +79,7 @@ struct PackedFwdArgs {
   unsigned* status;
 };
 constexpr int kTileRows = 256;  // of a segment's two tiles
-constexpr int kFewWhole = 16;   // blocks of 64 keys up to which the few-row kernel leaves segments whole
+constexpr int kFewWhole = 16;   // blocks of 64 keys up to which the few-row kernel leaves segments whole, if few
 
 // Upper bound of the segments of w tokens of one key head: sum ceil(n_b / w) <= (T + B (w - 1)) / w.
 inline int64_t segment_bound(const PackedShape& s, int w) {
