@@ -19,6 +19,11 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kFewTileBytes;
 
+// A piece of work takes as long as this many 64-key blocks more than it has: its pages are looked up, the first keys come,
+// warps are joined.  Runs count them as blocks that lie before a segment's own.  (100 sequences of 64 to 1351 keys, 8 key
+// heads: 120 us where they do not, since some CTAs have ten times the others' pieces.)
+constexpr int kPiece = 2;
+
 struct FewPiece {
   int b, qtok, pos, n;  // sequence, its first new token, that token's position, new tokens
   int keys, k0, nb;     // of the sequence; 64-key blocks [k0, k0 + nb)
@@ -31,8 +36,8 @@ struct FewWalk {
   const PackedSeqs& q;
   const int lane;
   bool whole;
-  int64_t g, g_end, run, begin;  // whole: the next segment and their number; else blocks
-  int at, nblk, hk, cut;
+  int64_t g, g_end, run;  // whole: the next segment and their number; else blocks
+  int at, nblk, hk, cut;  // cut: from the segment's begin, its kPiece before its blocks
   int chunk, before;  // whole: the 32 sequences looked at last, and how many of this kernel lie before them
   int mine;           // blocks of sequence `lane`
 
@@ -43,7 +48,7 @@ struct FewWalk {
     return k > 0 ? k : 1;
   }
   __device__ __forceinline__ FewWalk(const PackedShape& s_, const PackedSeqs& q_, bool may_split, unsigned* status)
-      : s(s_), q(q_), lane(threadIdx.x & 31), whole(false), g(0), g_end(0), run(1), begin(0), at(0), nblk(0), hk(0), cut(0),
+      : s(s_), q(q_), lane(threadIdx.x & 31), whole(false), g(0), g_end(0), run(1), at(0), nblk(0), hk(0), cut(0),
         chunk(0), before(0), mine(0) {
     if (!seqs_in_order(s, q, blockIdx.x == 0, status)) return;
     int64_t total = 0;
@@ -58,16 +63,16 @@ struct FewWalk {
     total = warp_total(total) * s.Hkv;
     const int64_t all = (int64_t)__reduce_add_sync(kFull, segs) * s.Hkv;
     most = __reduce_max_sync(kFull, most);
-    // Few short segments are never cut: their CTAs share the bandwidth with no others.  Else, in blocks of keys: a piece
-    // takes as long as kPiece more (its pages are looked up, the first keys come, warps are joined), the kernel that
-    // joins parts kJoin, and segments' own lengths leave CTAs half a longest one's excess apart.  (12 key heads of
-    // d = 128, 32 sequences of up to 300 keys: 15.6 us whole, 19.1 us in runs; 8 key heads, 64 sequences of 700 keys:
-    // 46.6 us whole, 43.7 us in runs; 16 of up to 32760: 178 us in runs, where the longest segment alone is 17 MB,
+    // Few short segments are never cut: their CTAs share the bandwidth with no others.  Else the kernel that joins parts
+    // takes as long as kJoin blocks, and segments' own lengths leave CTAs half a longest one's excess apart.  (12 key
+    // heads of d = 128, 32 sequences of up to 300 keys: 15.6 us whole, 19.1 us in runs; 8 key heads, 64 sequences of 700
+    // keys: 46.6 us whole, 43.7 us in runs; 16 of up to 32760: 178 us in runs, where the longest segment alone is 17 MB,
     // 420 us at a CTA's share of the bandwidth.)
-    constexpr float kPiece = 1.5f, kJoin = 4.5f;
+    constexpr float kJoin = 4.5f;
     const float share = 1.f / gridDim.x, mean = all > 0 ? (float)total / all : 0.f;
     const float in_whole = fmaxf(ceilf(all * share) * (mean + kPiece) + .5f * (most - mean), most + kPiece);
-    const float in_runs = total * share + kPiece * (1.f + all * share) + kJoin;
+    total += kPiece * all;
+    const float in_runs = total * share + kPiece + kJoin;
     whole = !may_split || (all <= gridDim.x && most <= kFewWhole) || in_whole <= in_runs;
     if (whole) {
       g = blockIdx.x;
@@ -75,14 +80,14 @@ struct FewWalk {
       return;
     }
     run = run_length(total, gridDim.x);
-    begin = g = run * blockIdx.x;
+    g = run * blockIdx.x;
     g_end = g + run < total ? g + run : total;
     if (g >= g_end) return;
-    // the sequence of block g
+    // the segment of block g
     int64_t off = g;
     for (int c = 0;; c += 32) {  // (found)
       const int k = c == 0 ? mine : blocks(c + lane);
-      const int64_t here = (int64_t)k * s.Hkv, to = warp_scan(here);
+      const int64_t here = k > 0 ? (int64_t)(k + kPiece) * s.Hkv : 0, to = warp_scan(here);
       const unsigned in = __ballot_sync(kFull, off < to);
       if (in) {
         const int src = __ffs(in) - 1;
@@ -93,8 +98,9 @@ struct FewWalk {
       }
       off -= __shfl_sync(kFull, to, 31);
     }
-    hk = off < (1 << 30) ? (int)off / nblk : (int)(off / nblk);
-    cut = (int)(off - (int64_t)hk * nblk);
+    const int len = nblk + kPiece;
+    hk = off < (1 << 30) ? (int)off / len : (int)(off / len);
+    cut = (int)(off - (int64_t)hk * len);
   }
   __device__ __forceinline__ bool next(FewPiece& y, CutRecord& rec) {
     if (g >= g_end) return false;
@@ -120,19 +126,22 @@ struct FewWalk {
     y.n = x.n;
     y.keys = x.keys;
     y.hk = hk;
-    y.k0 = cut;
     if (whole) {
+      y.k0 = 0;
       y.nb = nblk;
       y.slot = -1;
       g += gridDim.x;
       return true;
     }
     const int64_t left = g_end - g;
-    y.nb = nblk - cut < left ? nblk - cut : (int)left;
-    y.slot = y.nb == nblk ? -1 : 2 * (int)blockIdx.x + (g == begin ? 0 : 1);
-    if (cut == 0 && y.nb < nblk)
-      rec = {(int)((g + nblk - 1) / run) - (int)blockIdx.x + 1, y.slot, y.qtok, y.n, hk, 0, 0, 0};
-    g += y.nb;
+    const int len = nblk + kPiece, end = len - cut < left ? len : cut + (int)left;
+    y.k0 = max(cut - kPiece, 0);
+    y.nb = end - kPiece - y.k0;
+    if (y.nb <= 0) return false;  // the run ends before the segment's first block
+    y.slot = y.nb == nblk ? -1 : 2 * (int)blockIdx.x + (y.k0 == 0);
+    if (y.k0 == 0 && y.nb < nblk)
+      rec = {(int)((g - cut + len - 1) / run) - (int)blockIdx.x + 1, y.slot, y.qtok, y.n, hk, 0, 0, 0};
+    g += end - cut;
     cut = 0;
     if (g < g_end && ++hk == s.Hkv) {
       hk = 0;
