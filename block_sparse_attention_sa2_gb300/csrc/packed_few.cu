@@ -20,9 +20,10 @@ constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kFewTileBytes;
 
 // A piece of work takes as long as this many 64-key blocks more than it has: its pages are looked up, the first keys come,
-// warps are joined.  Runs count them as blocks that lie before a segment's own.  (100 sequences of 64 to 1351 keys, 8 key
-// heads: 120 us where they do not, since some CTAs have ten times the others' pieces.)
-constexpr int kPiece = 2;
+// warps are joined.  Runs count them as blocks that lie before a segment's own; without them some CTAs have ten times the
+// others' pieces.  (100 sequences of 64 to 1351 keys, 8 key heads of d = 128: without 120 us, 2 blocks 74, 3 68, 4 63, 5
+// 58, 6 58, 8 59; 11 of 1 to 16001, 4 key heads of d = 64: 2 blocks 24.2 us, 4 21.0, 8 18.4, 10 18.4, 16 18.7.)
+__host__ __device__ constexpr int piece_blocks(int d) { return 5 * 128 / d; }
 
 struct FewPiece {
   int b, qtok, pos, n;  // sequence, its first new token, that token's position, new tokens
@@ -34,10 +35,10 @@ struct FewPiece {
 struct FewWalk {
   const PackedShape& s;
   const PackedSeqs& q;
-  const int lane;
+  const int lane, piece;
   bool whole;
   int64_t g, g_end, run;  // whole: the next segment and their number; else blocks
-  int at, nblk, hk, cut;  // cut: from the segment's begin, its kPiece before its blocks
+  int at, nblk, hk, cut;  // cut: from the segment's begin, the first `piece` lie before its blocks
   int chunk, before;  // whole: the 32 sequences looked at last, and how many of this kernel lie before them
   int mine;           // blocks of sequence `lane`
 
@@ -48,7 +49,7 @@ struct FewWalk {
     return k > 0 ? k : 1;
   }
   __device__ __forceinline__ FewWalk(const PackedShape& s_, const PackedSeqs& q_, bool may_split, unsigned* status)
-      : s(s_), q(q_), lane(threadIdx.x & 31), whole(false), g(0), g_end(0), run(1), at(0), nblk(0), hk(0), cut(0),
+      : s(s_), q(q_), lane(threadIdx.x & 31), piece(piece_blocks(s_.d)), whole(false), g(0), g_end(0), run(1), at(0), nblk(0), hk(0), cut(0),
         chunk(0), before(0), mine(0) {
     if (!seqs_in_order(s, q, blockIdx.x == 0, status)) return;
     int64_t total = 0;
@@ -70,9 +71,9 @@ struct FewWalk {
     // 420 us at a CTA's share of the bandwidth.)
     constexpr float kJoin = 4.5f;
     const float share = 1.f / gridDim.x, mean = all > 0 ? (float)total / all : 0.f;
-    const float in_whole = fmaxf(ceilf(all * share) * (mean + kPiece) + .5f * (most - mean), most + kPiece);
-    total += kPiece * all;
-    const float in_runs = total * share + kPiece + kJoin;
+    const float in_whole = fmaxf(ceilf(all * share) * (mean + piece) + .5f * (most - mean), most + piece);
+    total += piece * all;
+    const float in_runs = total * share + piece + kJoin;
     whole = !may_split || (all <= gridDim.x && most <= kFewWhole) || in_whole <= in_runs;
     if (whole) {
       g = blockIdx.x;
@@ -87,7 +88,7 @@ struct FewWalk {
     int64_t off = g;
     for (int c = 0;; c += 32) {  // (found)
       const int k = c == 0 ? mine : blocks(c + lane);
-      const int64_t here = k > 0 ? (int64_t)(k + kPiece) * s.Hkv : 0, to = warp_scan(here);
+      const int64_t here = k > 0 ? (int64_t)(k + piece) * s.Hkv : 0, to = warp_scan(here);
       const unsigned in = __ballot_sync(kFull, off < to);
       if (in) {
         const int src = __ffs(in) - 1;
@@ -98,7 +99,7 @@ struct FewWalk {
       }
       off -= __shfl_sync(kFull, to, 31);
     }
-    const int len = nblk + kPiece;
+    const int len = nblk + piece;
     hk = off < (1 << 30) ? (int)off / len : (int)(off / len);
     cut = (int)(off - (int64_t)hk * len);
   }
@@ -134,9 +135,9 @@ struct FewWalk {
       return true;
     }
     const int64_t left = g_end - g;
-    const int len = nblk + kPiece, end = len - cut < left ? len : cut + (int)left;
-    y.k0 = max(cut - kPiece, 0);
-    y.nb = end - kPiece - y.k0;
+    const int len = nblk + piece, end = len - cut < left ? len : cut + (int)left;
+    y.k0 = max(cut - piece, 0);
+    y.nb = end - piece - y.k0;
     if (y.nb <= 0) return false;  // the run ends before the segment's first block
     y.slot = y.nb == nblk ? -1 : 2 * (int)blockIdx.x + (y.k0 == 0);
     if (y.k0 == 0 && y.nb < nblk)
