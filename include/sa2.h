@@ -571,9 +571,9 @@ sa2_status sa2_rotary_apply(const sa2_rotary* rotary, int32_t dtype, int32_t B, 
  * them; it returns the number of records written, or -1 when an event could not be read.
  * With out == NULL it returns the number of kernels and leaves the records in place.  Not
  * thread-safe against concurrent launches from several host threads on different streams of
- * the same kernel.  The cross and cache calls are counted under the names of their kind:
- * attn_fwd (with the join of parts), to_f16 (append and read), bwd_preprocess, attn_bwd_dkdv
- * (with its join) and attn_bwd_dq.
+ * the same kernel.  The cross, cache, packed and paged calls are counted under the names of
+ * their kind: attn_fwd (with the join of parts), to_f16 (append and read, rotary),
+ * bwd_preprocess, attn_bwd_dkdv (with its join) and attn_bwd_dq.
  */
 typedef struct sa2_kernel_time {
   const char* name; /* static string */
