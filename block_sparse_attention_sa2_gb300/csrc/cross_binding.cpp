@@ -591,7 +591,8 @@ PyObject* rotary(PyObject* const* a) {
     same(ko, k, "k_out");
     y2.emplace(ko, "k_out", at_);
   }
-  if (x.B * x.N * x.H > 0)
+  if (x.H < 1 || (two && x2->H < 1)) refuse("q and k have a head at least");
+  if (x.B * x.N > 0)
     check("sa2_rotary_apply",
           sa2_rotary_apply(&r, code, narrow(x.B, "B"), narrow(x.N, "N"), narrow(d, "d"), pp, x.N * (each ? x.B : 1),
                            each ? x.N : 0, narrow(x.H, "H"), &x.t, &y.t, two ? narrow(x2->H, "heads of k") : 0,

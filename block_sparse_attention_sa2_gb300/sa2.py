@@ -388,14 +388,15 @@ def packed_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq: torc
     q [H, T, d], k, v [Hkv, T, d] (H a multiple of Hkv; bfloat16 or float16; strides of their own, so
     projections' [T, H, d] are passed as ``x.transpose(0, 1)``).  ``seq`` ([B + 1] int32 on the device): sequence
     b has the tokens seq[b] .. seq[b + 1] - 1.  ``causal``: a token attends to those up to itself.  LSE is
-    float32 [H, T].  Tokens outside the sequences are left as they were."""
+    float32 [H, T].  Tokens outside the sequences are left as they were (in a new tensor, as its memory was found:
+    where they are read later, pass zeroed ones)."""
     return (_binding or load_binding()).packed_attn_fwd(q, k, v, seq, causal, scale, o, lse, ws, _handle(stream))
 
 
 def packed_attn_bwd(q, k, v, o, lse, do, seq: torch.Tensor, causal: bool = True, scale: Optional[float] = None,
                     dq=None, dk=None, dv=None, ws: Optional[torch.Tensor] = None, stream=None):
     """sa2_packed_attn_bwd: gradients (dQ, dK, dV) of packed_attn_fwd (bfloat16), whose o and lse on the same q, k,
-    v, seq, causal and scale it takes."""
+    v, seq, causal and scale it takes.  Tokens outside the sequences: as in the forward."""
     return (_binding or load_binding()).packed_attn_bwd(q, k, v, o, lse, do, seq, causal, scale, dq, dk, dv, ws,
                                                         _handle(stream))
 
@@ -439,7 +440,8 @@ def paged_attn(q: torch.Tensor, cache: PagedCache, seq: torch.Tensor, kv_len: to
                ws: Optional[torch.Tensor] = None, stream=None):
     """sa2_paged_attn: attention of new tokens q [H, T, d], packed by ``seq`` and appended already, to all that the
     cache holds of their sequences up to each of them; returns (O, LSE) as packed_attn_fwd does.  ``max_new``: no
-    sequence has more new tokens (1 where each makes a single one): the kernels for few rows need to know."""
+    sequence has more new tokens (1 where each makes a single one), so that the kernel of query tiles is not launched
+    where none has enough of them for one; a sequence that has more is an error of the device's status."""
     return (_binding or load_binding()).paged_attn(q, cache._held, cache._device, seq, kv_len, table, causal, max_new,
                                                    scale, o, lse, ws, _handle(stream))
 

@@ -193,3 +193,11 @@ def test_refusals(sa2):
     assert sa2.rotary(r, pos[:0], x[:, :, :0]).shape == (2, 3, 0, 128)
     sa2.check_device()
     assert copy.deepcopy(r).frequencies == r.frequencies
+
+
+def test_no_heads_are_refused(sa2):
+    r, pos = sa2.Rotary(128, sa2.rotary_frequencies(128)), torch.arange(10, **I32)
+    x = rnd((2, 3, 10, 128), torch.bfloat16, 0)
+    for heads in ((x[:, :0], x), (x, x[:, :0])):
+        with pytest.raises(ValueError, match="head"):
+            sa2.rotary(r, pos, *heads)
