@@ -560,13 +560,6 @@ struct DkvItem {
   int masked, pad;  // a token sees those up to itself (causal, or a token alone)
 };
 
-// The thread's index, read again: what is made of it is not kept in registers over the loops before.
-__device__ __forceinline__ int thread_anew() {
-  int x;
-  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
-  return x;
-}
-
 template <int D>
 struct DkvSmem {
   static constexpr bool kX = D == 64;  // LSE and D through the products

@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // keys that this row reads, from the piece's first on (a row without a query: as the tile does)
       const int mine = s.causal && row_valid ? min(keys, x.pos + tok + 1 - x.k0 * kKeyBlock) : keys;
+      const int least = __reduce_min_sync(kFull, mine);  // of the warp's rows
       float m_used = 0.f, m_run = 0.f;  // reference of the exponentials, largest so far
       float l = 0.f;                    // sum of exp2(s - m_used)
       // O and l to another reference.  O holds the half blocks before this one once their P V has
@@ -388,22 +389,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int i = 0; 64 * i < keys; ++i, ++c) {
         const uint32_t u = c & 1, ts = trow + col_s(t, u);
-        const int valid = mine - 64 * i;
         if (!__all_sync(kFull, mbar_wait(bar_s(t, u), (c >> 1) & 1, wc))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // the references: see cross_fwd.cu
-        if (i == 0) {
-          float y[32];
-          load_scores(ts, y, valid);
-          const float m0 = max32(y);
-          load_scores(ts + 32, y, valid - 32);
-          m_used = m_run = fmaxf(fmaxf(m0, max32(y)) * mul, kLeastRef);
-        } else if (__any_sync(kFull, m_run > m_used + kRescaleThreshold)) {
-          ok = rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
+        // Scores that some row does not read become -inf in TMEM, and the first ones give the reference, in a pass of its
+        // own: half a block has neither as a rule, and a launch's first one waits for each of its instructions.
+        const bool cut = 64 * (i + 1) > least;
+        if (i == 0 || cut) {
+          float m0 = -INFINITY;
+#pragma unroll 1
+          for (int k = 0; k < 64; k += 32) {
+            float y[32];
+            load_scores(ts + k, y, mine - 64 * i - k);
+            m0 = fmaxf(m0, max32(y));
+            if (cut) {
+              uint32_t w[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(y[j]);
+              tmem_st32(ts + k, w);
+            }
+          }
+          if (cut) tmem_st_wait();
+          if (i == 0) m_used = m_run = fmaxf(m0 * mul, kLeastRef);
         }
+        // the references: see cross_fwd.cu
+        if (i > 0 && __any_sync(kFull, m_run > m_used + kRescaleThreshold))
+          ok = rescale(m_run > m_used + kRescaleThreshold ? m_run : m_used);
         uint32_t pk[32];
         float sum;
         for (bool again = false;;) {
@@ -411,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx;
           {
             float y[32];
-            load_scores(ts, y, valid);
+            load_scores(ts, y, 32);
             mx = max32(y);
             exp32<F16>(y, mul, -m_used, pk, part);
-            load_scores(ts + 32, y, valid - 32);
+            load_scores(ts + 32, y, 32);
             mx = fmaxf(mx, max32(y));
             exp32<F16>(y, mul, -m_used, pk + 16, part);
           }

@@ -10,6 +10,13 @@ namespace sa2 {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// The thread's index, read again: what is made of it is not kept in registers over other loops.
+__device__ __forceinline__ int thread_anew() {
+  int x;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
+  return x;
+}
+
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
   return x;
