@@ -199,3 +199,16 @@ def test_places_out_of_order_are_reported(sa2):
         with pytest.raises(sa2.Sa2Error, match="bounds"):
             sa2.check_device()
         assert bool((o == 3).all()) and bool((lse == 3).all())
+
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)], ids=["64-fp16", "128-bf16"])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (6, 1), (33, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_every_place_of_the_last_key(sa2, d, dtype, H, Hkv, causal):
+    """Sequences that end at each place within half a block of keys, whose last scores are cut row by row."""
+    lens = [64 + n for n in range(0, 64, 7)] + [1, 31, 32, 33, 63, 191, 255]
+    at = places(lens)
+    q, k, v = (tokens(h, at[-1], d, dtype, i) for i, h in enumerate((H, Hkv, Hkv)))
+    o, lse = sa2.packed_attn_fwd(q, k, v, torch.tensor(at, **I32), causal=causal)
+    sa2.check_device()
+    check_packed(o, lse, q, k, v, at, causal)

@@ -224,3 +224,10 @@ def test_refusals(sa2):
         with pytest.raises((ValueError, sa2.Sa2Error)):
             sa2.packed_attn_bwd(**{**good, **bad})
     sa2.check_device()
+
+
+@pytest.mark.parametrize("lens,H,Hkv", [([152], 32, 2), ([1000], 24, 1), ([129, 40, 900], 16, 1), ([260], 64, 1)], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_parts_than_tiles(sa2, lens, H, Hkv, d):
+    """Key blocks cut into as many parts as the longest sequences have tiles for: the last blocks have fewer tiles."""
+    run(sa2, lens, H, Hkv, d, norm=False)

@@ -304,3 +304,15 @@ def test_refusals(sa2):
     assert type(other) is sa2.PagedCache and other.k.data_ptr() != cache.k.data_ptr()
     sa2.paged_append(other, k, v, seq, kv_len, table)
     sa2.check_device()
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(24, 12, 64), (8, 8, 128), (5, 1, 128)])
+@pytest.mark.parametrize("held", ["short", "uneven", "one long"])
+def test_many_single_tokens(sa2, held, H, Hkv, d):
+    """More segments than SMs: short ones are taken whole, several by each CTA, others cut into runs, where a run may end
+    before a segment's first block; some sequences have no new token, two or three have two."""
+    B = 75
+    lens = {"short": [3 + 41 * b % 250 for b in range(B)], "uneven": [2 + 197 * b % 1400 for b in range(B)],
+            "one long": [20 + b if b != 50 else 20000 for b in range(B)]}[held]
+    new = [0 if b % 9 == 4 else 2 if b % 31 == 7 else 1 for b in range(B)]
+    run(sa2, new, lens, 32, H, Hkv, d, max_new=2, seed=H)
