@@ -33,7 +33,7 @@ constexpr int kSlots = 4;  // items handed out and not yet finished
 
 // ------------------------------------------------------------------------- statistics
 //
-// D and log2(e) * LSE of every query row, D / 16 threads per row; grid (tile records, key heads, 128 / rows of
+// -D and -log2(e) * LSE of every query row, D / 16 threads per row; grid (tile records, key heads, 128 / rows of
 // a CTA).  Bound by the bytes of dO and O.  It also clears the work counters.
 template <int D>
 constexpr int kStatsRows = 256 / (D / 16);
@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
   for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
   if (ch == 0) {
     float* rec = a.stats + (hk * plan.tile_recs + blockIdx.x) * 256;
-    rec[r] = lse * 1.4426950408889634f;
-    rec[128 + r] = acc;
+    rec[r] = -lse * 1.4426950408889634f;
+    rec[128 + r] = -acc;
   }
 }
 
@@ -422,8 +422,8 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
       // keys that this row has a gradient to: none where there is one, whose P is 1 whatever its score
       int mine = s.causal ? min(keys, x.tile * nb + tok_r + 1) : keys;
       if (mine == 1) mine = 0;
-      const float lse2 = a.stats[x.rec * 256 + r];
-      float Dr = a.stats[x.rec * 256 + 128 + r];
+      const float lse2 = a.stats[x.rec * 256 + r];     // - LSE
+      float Dr = a.stats[x.rec * 256 + 128 + r];       // - D
       for (int j = 0; j < nk; ++j, ++J) {
         const int bb = J & 1;
         const int valid = mine - j * kKeyBlock - k0;  // of this thread's keys
@@ -443,7 +443,12 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
           mbar_arrive(bar_sfree);
         }
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) p[c] = ex2(fmaf(__uint_as_float(u[c >> 5][c & 31]), a.scale_log2, -lse2));
+        for (int c = 0; c < kKeys; c += 2) {
+          const float2 y = fma2(make_float2(__uint_as_float(u[c >> 5][c & 31]), __uint_as_float(u[c >> 5][(c & 31) + 1])),
+                                make_float2(a.scale_log2, a.scale_log2), make_float2(lse2, lse2));
+          p[c] = ex2(y.x);
+          p[c + 1] = ex2(y.y);
+        }
         if (!__all_sync(kFull, mbar_wait(bar_dp(bb), (J >> 1) & 1, wc))) {
           ok = false;
           break;
@@ -477,10 +482,10 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
           }
           ++sums;
           tc_fence_after();
-          Dr = tmem_sum<L::kRowWarps / 4, kKeys>(trow + kS);
+          Dr = -tmem_sum<L::kRowWarps / 4, kKeys>(trow + kS);
           tc_fence_before();
           mbar_arrive(bar_sfree);
-          if (k0 == 0) a.stats[x.rec * 256 + 128 + r] = lse2 == INFINITY ? 0.f : Dr;  // (0: a row without a query)
+          if (k0 == 0) a.stats[x.rec * 256 + 128 + r] = lse2 == -INFINITY ? 0.f : Dr;  // (0: a row without a query)
         }
 #pragma unroll
         for (int h = 0; h < kKeys / 32; ++h) {
@@ -493,8 +498,9 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
               const int k = 32 * h + 16 * q + c;
-              const float d0 = p[k] * (__uint_as_float(v[c]) - Dr), d1 = p[k + 1] * (__uint_as_float(v[c + 1]) - Dr);
-              pk[(16 * q + c) / 2] = pack_bf16x2(d0, d1);
+              const float2 d = mul2(make_float2(p[k], p[k + 1]), add2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                                                      make_float2(Dr, Dr)));
+              pk[(16 * q + c) / 2] = pack_bf16x2(d.x, d.y);
             }
           }
           if (valid < 32 * (h + 1)) {  // behind the row's last key P and dP may be anything
@@ -855,7 +861,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
     mbar_drain(bar_gdrain, 0, abort_flag);
   } else if (L::kX && warp == 20) {
     // ------------------------------------------------------------- the 16 channels of LSE and D
-    const float inv = -1.f / fmaxf(a.scale_log2, kMinScale);
+    const float inv = 1.f / fmaxf(a.scale_log2, kMinScale);
     uint32_t U = 0;
     bool ok = true;
     DkvItem x;
@@ -870,7 +876,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
         for (int i = 0; i < 4; ++i) {
           const int r = 32 * i + lane;
           *reinterpret_cast<uint2*>(stg + L::kStageX + x_row(r)) = split3(rec[r] * inv);
-          *reinterpret_cast<uint2*>(stg + L::kStageX + kXTile + x_row(r)) = split3(-rec[128 + r]);
+          *reinterpret_cast<uint2*>(stg + L::kStageX + kXTile + x_row(r)) = split3(rec[128 + r]);
         }
         fence_proxy_async();
         __syncwarp();
@@ -910,19 +916,23 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
         uint32_t v[32], pk[16];
         tmem_ld32(ts, v);
         tmem_ld_wait(v);
-        if constexpr (L::kX) {
+        const float2 mul_2{mul, mul};
 #pragma unroll
-          for (int c = 0; c < 32; ++c) p[c] = ex2(__uint_as_float(v[c]) * mul);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 l = l4[q];
-            float* pp = p + 4 * q;
-            pp[0] = ex2(fmaf(__uint_as_float(v[4 * q]), mul, -l.x));
-            pp[1] = ex2(fmaf(__uint_as_float(v[4 * q + 1]), mul, -l.y));
-            pp[2] = ex2(fmaf(__uint_as_float(v[4 * q + 2]), mul, -l.z));
-            pp[3] = ex2(fmaf(__uint_as_float(v[4 * q + 3]), mul, -l.w));
+        for (int q = 0; q < 8; ++q) {
+          float2 y0{__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])};
+          float2 y1{__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])};
+          if constexpr (L::kX) {
+            y0 = mul2(y0, mul_2);
+            y1 = mul2(y1, mul_2);
+          } else {
+            const float4 l = l4[q];  // - LSE
+            y0 = fma2(y0, mul_2, make_float2(l.x, l.y));
+            y1 = fma2(y1, mul_2, make_float2(l.z, l.w));
           }
+          p[4 * q] = ex2(y0.x);
+          p[4 * q + 1] = ex2(y0.y);
+          p[4 * q + 2] = ex2(y1.x);
+          p[4 * q + 3] = ex2(y1.y);
         }
         if (diagonal) {
 #pragma unroll
@@ -941,19 +951,19 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
         tc_fence_after();
         tmem_ld32(tdp, v);
         tmem_ld_wait(v);
-        if constexpr (L::kX) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            pk[c] = pack_bf16x2(p[2 * c] * __uint_as_float(v[2 * c]), p[2 * c + 1] * __uint_as_float(v[2 * c + 1]));
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 d = d4[q];
-            const float* pp = p + 4 * q;
-            pk[2 * q] = pack_bf16x2(pp[0] * (__uint_as_float(v[4 * q]) - d.x), pp[1] * (__uint_as_float(v[4 * q + 1]) - d.y));
-            pk[2 * q + 1] =
-                pack_bf16x2(pp[2] * (__uint_as_float(v[4 * q + 2]) - d.z), pp[3] * (__uint_as_float(v[4 * q + 3]) - d.w));
+        for (int q = 0; q < 8; ++q) {
+          float2 z0{__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])};
+          float2 z1{__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])};
+          if constexpr (!L::kX) {
+            const float4 d = d4[q];  // - D
+            z0 = add2(z0, make_float2(d.x, d.y));
+            z1 = add2(z1, make_float2(d.z, d.w));
           }
+          z0 = mul2(make_float2(p[4 * q], p[4 * q + 1]), z0);
+          z1 = mul2(make_float2(p[4 * q + 2], p[4 * q + 3]), z1);
+          pk[2 * q] = pack_bf16x2(z0.x, z0.y);
+          pk[2 * q + 1] = pack_bf16x2(z1.x, z1.y);
         }
         if (diagonal) {  // (dP of a masked place may be anything; a sequence's first token sees one key: dS = 0)
           const int cut_ds = kb == 0 && t == 0 ? max(cut, s.G - 64 * (int)half - 32 * g) : cut;
