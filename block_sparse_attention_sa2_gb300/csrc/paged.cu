@@ -10,8 +10,8 @@ constexpr int kHeads = 4;  // of a token per thread, all of their loads in fligh
 
 // A thread moves 16 bytes of one token for up to kHeads key heads; the token's sequence (the last that
 // begins at or before it, by bisection), page and place in it are found once.  K and V in one launch (grid z).
-// Bound by the bytes, one read and one write of each (3600 tokens of 10 key heads, d = 128: 9.5 us from HBM, of which 5
-// are the launch and the chain place - page - token; single tokens 4.5).
+// Bound by the bytes, one read and one write of each (3600 tokens of 40 key heads, d = 128: 23 us, 6.4 TB/s), and few
+// tokens by the chain place - page - token (one token 2.0 us of a stream of calls, 2.15 where its keys are read last).
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendArgs a) {
   kernel_wait();
   kernel_trigger();
@@ -24,6 +24,13 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendArgs 
         report_error(a.status, kDevErrBounds);
     }
   if (i >= (int64_t)a.T * a.words) return;
+  const TokenRef &src = blockIdx.z ? a.v : a.k, &dst = blockIdx.z ? a.v_pages : a.k_pages;
+  const int h0 = blockIdx.y * kHeads;
+  const uint16_t* x = static_cast<const uint16_t*>(src.p) + (int64_t)tok * src.sn + h0 * src.sh + word * 8;
+  uint4 u[kHeads];  // (on their way while the place is looked up)
+#pragma unroll
+  for (int q = 0; q < kHeads; ++q)
+    if (h0 + q < a.Hkv) u[q] = *reinterpret_cast<const uint4*>(x + q * src.sh);
   int l = 0, h = a.B;
   while (l < h) {  // first b with seq[b + 1] > tok
     const int m = (l + h) >> 1;
@@ -38,14 +45,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendArgs 
     report_error(a.status, kDevErrBounds);
     return;
   }
-  const TokenRef &src = blockIdx.z ? a.v : a.k, &dst = blockIdx.z ? a.v_pages : a.k_pages;
-  const int h0 = blockIdx.y * kHeads;
-  const uint16_t* x = static_cast<const uint16_t*>(src.p) + (int64_t)tok * src.sn + h0 * src.sh + word * 8;
   uint16_t* y = static_cast<uint16_t*>(dst.p) + id * dst.sb + (pos % a.page) * dst.sn + h0 * dst.sh + word * 8;
-  uint4 u[kHeads];
-#pragma unroll
-  for (int q = 0; q < kHeads; ++q)
-    if (h0 + q < a.Hkv) u[q] = *reinterpret_cast<const uint4*>(x + q * src.sh);
 #pragma unroll
   for (int q = 0; q < kHeads; ++q)
     if (h0 + q < a.Hkv) *reinterpret_cast<uint4*>(y + q * dst.sh) = u[q];
