@@ -7,9 +7,9 @@
 // table: each lane holds the page of one of the warp's next 32 steps, read a whole round ahead.  A row sees the keys
 // up to its token's position.
 //
-// Measured: 16 single tokens over up to 32760 keys (264450 in all), 40/8 heads of d = 128: 171 us, 6.3 TB/s, 94 % of the
-// copy rate, and 4.5 us for the parts' join.  Short ones are bound by the chain place - page - keys - result of a piece
-// (one token over 512 keys, 12 heads: 5.6 us).
+// Measured: 16 single tokens over up to 32760 keys (264450 in all), 40/8 heads of d = 128: 167 us with the parts' join,
+// 6.5 TB/s, 97 % of the copy rate.  Short ones are bound by the chain place - page - keys - steps - result of a piece (one
+// token over 512 keys, 12 heads: 7.2 us; over 16 keys 4.1).
 #include <algorithm>
 
 #include "cross_few.cuh"
@@ -46,39 +46,47 @@ struct FewWalk {
   int chunk, before;  // whole: the 32 sequences looked at last, and how many of this kernel lie before them
   int mine;           // blocks of sequence `lane`
 
-  __device__ __forceinline__ int blocks(int b) const {  // 0: not a sequence of this kernel
-    const int n = b < s.B ? q.seq[b + 1] - q.seq[b] : 0;
+  // Blocks of a sequence of n new tokens; 0: not one of this kernel.
+  __device__ __forceinline__ int blocks_of(int n, int held) const {
     if (n < 1 || n > s.few) return 0;
-    const int k = key_blocks(seq_info(s, q, b).keys, 6);
-    return k > 0 ? k : 1;
+    return max(keys_in_range(s, held, n) ? key_blocks(held, 6) : 0, 1);
+  }
+  __device__ __forceinline__ int blocks(int b) const {
+    return b < s.B ? blocks_of(q.seq[b + 1] - q.seq[b], q.kv_len[b]) : 0;
   }
   __device__ __forceinline__ FewWalk(const PackedShape& s_, const PackedSeqs& q_, bool may_split, unsigned* status)
       : s(s_), q(q_), lane(threadIdx.x & 31), piece(piece_blocks(s_.d)), whole(false), g(0), g_end(0), run(1), at(0), nblk(0), hk(0), cut(0),
         chunk(0), before(0), mine(0) {
-    if (!seqs_in_order(s, q, blockIdx.x == 0, status)) return;
+    if (threadIdx.x >= 32) return;
     int64_t total = 0;
     int segs = 0, most = 0;
-    mine = blocks(lane);
+    Faults f;
     for (int b = lane; b < s.B; b += 32) {
-      const int k = b == lane ? mine : blocks(b);
+      const int lo = q.seq[b], hi = q.seq[b + 1], held = q.kv_len[b];  // (loads that do not wait for each other)
+      const int k = f.add(s, lo, hi, true, held) ? 0 : blocks_of(hi - lo, held);
+      if (b == lane) mine = k;
       total += k;
       segs += k > 0;
       most = max(most, k);
     }
-    total = warp_total(total) * s.Hkv;
-    const int64_t all = (int64_t)__reduce_add_sync(kFull, segs) * s.Hkv;
-    most = __reduce_max_sync(kFull, most);
-    // Few short segments are never cut: their CTAs share the bandwidth with no others.  Else the kernel that joins parts
-    // takes as long as kJoin blocks, and segments' own lengths leave CTAs half a longest one's excess apart.  (12 key
-    // heads of d = 128, 32 sequences of up to 300 keys: 15.6 us whole, 19.1 us in runs; 8 key heads, 64 sequences of 700
-    // keys: 46.6 us whole, 43.7 us in runs; 16 of up to 32760: 178 us in runs, where the longest segment alone is 17 MB,
-    // 420 us at a CTA's share of the bandwidth.)
-    constexpr float kJoin = 4.5f;
-    const float share = 1.f / gridDim.x, mean = all > 0 ? (float)total / all : 0.f;
-    const float in_whole = fmaxf(ceilf(all * share) * (mean + piece) + .5f * (most - mean), most + piece);
-    total += piece * all;
-    const float in_runs = total * share + piece + kJoin;
-    whole = !may_split || (all <= gridDim.x && most <= kFewWhole) || in_whole <= in_runs;
+    if (!f.none_bad(blockIdx.x == 0, status)) return;
+    const unsigned all = __reduce_add_sync(kFull, (unsigned)segs) * s.Hkv;  // (the host has seen to it: below 2^31)
+    whole = !may_split;
+    if (may_split) {
+      total = warp_total(total) * s.Hkv;
+      most = __reduce_max_sync(kFull, most);
+      // Few short segments are never cut: their CTAs share the bandwidth with no others.  Else the kernel that joins parts
+      // takes as long as kJoin blocks, and segments' own lengths leave CTAs half a longest one's excess apart.  (12 key
+      // heads of d = 128, 32 sequences of up to 300 keys: 15.6 us whole, 19.1 us in runs; 8 key heads, 64 sequences of 700
+      // keys: 46.6 us whole, 43.7 us in runs; 16 of up to 32760: 167 us in runs, where the longest segment alone is 17 MB,
+      // 420 us at a CTA's share of the bandwidth.)
+      constexpr float kJoin = 4.5f;
+      const float share = __fdividef(1.f, gridDim.x), mean = all > 0 ? __fdividef(total, all) : 0.f;
+      const float in_whole = fmaxf(ceilf(all * share) * (mean + piece) + .5f * (most - mean), most + piece);
+      total += (int64_t)piece * all;
+      const float in_runs = total * share + piece + kJoin;
+      whole = (all <= gridDim.x && most <= kFewWhole) || in_whole <= in_runs;
+    }
     if (whole) {
       g = blockIdx.x;
       g_end = all;
@@ -110,8 +118,8 @@ struct FewWalk {
   __device__ __forceinline__ bool next(FewPiece& y, CutRecord& rec) {
     if (g >= g_end) return false;
     if (whole) {  // segment g: the key head of a sequence of this kernel, in order
-      const int seg = (int)(g / s.Hkv);
-      hk = (int)(g - (int64_t)seg * s.Hkv);
+      const int seg = (int)((unsigned)g / (unsigned)s.Hkv);
+      hk = (int)g - seg * s.Hkv;
       for (;; chunk += 32) {  // (found)
         const int k = chunk == 0 ? mine : blocks(chunk + lane);
         const unsigned some = __ballot_sync(kFull, k > 0);
@@ -244,15 +252,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int p = 0; p < kIds; ++p) id[p] = __shfl_sync(kFull, ids[p], i & 31);
       if (i < steps) {
         const uint32_t dst = ring_u + (i % kStages) * kStageBytes;
-        const int base = key0 + (i * kWarps + warp) * T::kKeys;
+        constexpr int kRows = 32 / T::kChunks, kPer = 8 / kIds;  // keys of a warp's copy; copies of 16 keys
+        const int r0 = lane / T::kChunks, c = lane % T::kChunks;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int c = (q * 32 + lane) % T::kChunks, r = (q * 32 + lane) / T::kChunks;
-          const int pid = id[q * kIds / 8];  // (rows of 16 keys: q 0..7, or 0..3 and 4..7)
-          const bool live = base + r < key1 && pid >= 0;
-          const int64_t slot = (base + r) & (s.page - 1), pg = live ? pid : 0;
-          copy16(dst + T::at(r, c), kp + pg * a.k.sb + slot * a.k.sn + c * 8, live);
-          copy16(dst + kFewTileBytes + T::at(r, c), vp + pg * a.v.sb + slot * a.v.sn + c * 8, live);
+        for (int p = 0; p < kIds; ++p) {  // 16 keys from a multiple of 16 on lie in one page
+          const int key = key0 + (i * kWarps + warp) * T::kKeys + 16 * p;
+          const int64_t off = (id[p] >= 0 ? id[p] : 0) * a.k.sb + ((key & (s.page - 1)) + r0) * a.k.sn + c * 8;
+          const int left = id[p] >= 0 ? key1 - key - r0 : 0;
+#pragma unroll
+          for (int q = 0; q < kPer; ++q) {
+            const int64_t at = off + (int64_t)(q * kRows) * a.k.sn;  // (V's pages have K's strides)
+            copy16(dst + T::at(16 * p + q * kRows + r0, c), kp + at, q * kRows < left);
+            copy16(dst + kFewTileBytes + T::at(16 * p + q * kRows + r0, c), vp + at, q * kRows < left);
+          }
         }
       }
       copy_commit();

@@ -58,18 +58,30 @@ __device__ __forceinline__ SeqInfo seq_info(const PackedShape& s, const PackedSe
   return x;
 }
 
+// What is wrong with the sequences that it has been shown: places out of order or outside of [0, T], lengths out of range.
+struct Faults {
+  bool bad = false, odd = false;
+  __device__ __forceinline__ bool add(const PackedShape& s, int lo, int hi, bool paged, int held) {
+    const bool out = lo < 0 || hi < lo || hi > s.T;
+    bad |= out;
+    if (!out) odd |= hi - lo > s.max_new || (paged && !keys_in_range(s, held, hi - lo));
+    return out;
+  }
+  // For a whole warp: whether the places are in order; `report`: it reports what it has found.
+  __device__ __forceinline__ bool none_bad(bool report, unsigned* status) const {
+    if (report && (bad || odd)) report_error(status, kDevErrBounds);
+    return !__any_sync(kFull, bad);
+  }
+};
 // True where the sequences' places are in order and within [0, T]; nothing is done in a call where they are
 // not.  `report`: one CTA's warp reports that, and lengths out of range.
 __device__ __forceinline__ bool seqs_in_order(const PackedShape& s, const PackedSeqs& q, bool report, unsigned* status) {
-  bool bad = false, odd = false;
+  Faults f;
   for (int b = (int)(threadIdx.x & 31); b < s.B; b += 32) {
     const int lo = q.seq[b], hi = q.seq[b + 1], held = q.kv_len ? q.kv_len[b] : 0;  // (loads that do not wait for each other)
-    const bool out = lo < 0 || hi < lo || hi > s.T;
-    bad |= out;
-    if (!out) odd |= hi - lo > s.max_new || (q.kv_len && !keys_in_range(s, held, hi - lo));
+    f.add(s, lo, hi, q.kv_len, held);
   }
-  if (report && (bad || odd)) report_error(status, kDevErrBounds);
-  return !__any_sync(kFull, bad);
+  return f.none_bad(report, status);
 }
 
 // sum over i < n of floor((a i + b) / m), a, b >= 0: whole parts out, then the lattice points under the line
