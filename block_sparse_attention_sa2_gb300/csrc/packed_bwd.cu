@@ -246,8 +246,7 @@ __global__ void __launch_bounds__(DqSmem<D>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------- work finder and TMA producer
-    const bool in_order = seqs_in_order(s, a.seqs, blockIdx.x == 0, a.status);
-    ItemQueue queue(s, a.seqs, nb, 1, plan.heads, plan.dq_grid, false, a.counter + 1, in_order);
+    ItemQueue queue(s, a.seqs, nb, 1, plan.heads, plan.dq_grid, false, a.counter + 1, blockIdx.x == 0, a.status);
     const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * nb * s.G);
     uint32_t J = 0, nv = 0, qn = 0, don = 0;  // K, V, Q and dO tiles loaded
     bool ok = true;
@@ -720,8 +719,7 @@ __global__ void __launch_bounds__(DkvSmem<D>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------- work finder and TMA producer
-    const bool in_order = seqs_in_order(s, a.seqs, false, a.status);
-    ItemQueue queue(s, a.seqs, kKeyBlock, plan.parts, plan.heads, plan.grid, true, a.counter, in_order);
+    ItemQueue queue(s, a.seqs, kKeyBlock, plan.parts, plan.heads, plan.grid, true, a.counter, false, a.status);
     const uint32_t q_bytes = (uint32_t)(L::kPanels * 128 * used);
     uint32_t U = 0, kvn = 0;  // tiles, key blocks loaded
     bool ok = true;

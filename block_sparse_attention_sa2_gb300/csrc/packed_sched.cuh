@@ -133,23 +133,28 @@ struct ItemQueue {
   const bool rising;
   unsigned* counter;   // null: no more items than CTAs
   bool first;
+  bool in_order;   // see seqs_in_order; where not, there are no items
   int mine;        // segments of sequence `lane`
   int segs;        // of one key head (below 2^29)
   int section, level, most;
   int before, upto;  // segments that come before this level, and with it
 
   __device__ __forceinline__ ItemQueue(const PackedShape& s_, const PackedSeqs& q_, int w_, int parts_, int heads_,
-                                       int grid_, bool rising_, unsigned* counter_, bool in_order)
+                                       int grid_, bool rising_, unsigned* counter_, bool report, unsigned* status)
       : s(s_), q(q_), w(w_), parts(parts_), heads(heads_), grid(grid_), rising(rising_), counter(counter_),
-        first(true), mine(0), segs(0), section(-1), level(0), most(0), before(0), upto(0) {
-    if (!in_order) return;
+        first(true), in_order(false), mine(0), segs(0), section(-1), level(0), most(0), before(0), upto(0) {
     const int lane = threadIdx.x & 31;
-    int n = most = mine = segments_of(s, q, w, lane);
-    for (int i = lane + 32; i < s.B; i += 32) {
-      const int k = segments_of(s, q, w, i);
+    Faults f;
+    int n = 0;
+    for (int i = lane; i < s.B; i += 32) {
+      const int lo = q.seq[i], hi = q.seq[i + 1], held = q.kv_len ? q.kv_len[i] : 0;  // (loads that do not wait for each other)
+      const int k = !f.add(s, lo, hi, q.kv_len, held) && hi - lo > s.few ? (hi - lo + w - 1) / w : 0;
+      if (i == lane) mine = k;
       n += k;
       most = max(most, k);
     }
+    in_order = f.none_bad(report, status);
+    if (!in_order) return;
     segs = __reduce_add_sync(kFull, n);
     most = __reduce_max_sync(kFull, most);
   }
@@ -235,7 +240,6 @@ struct PackedWalk {
   const PackedShape& s;
   const PackedPlan& p;
   const PackedSeqs& q;
-  const bool in_order;
   ItemQueue queue;  // direct
   int b, lo;        // of the piece given out last: its sequence, and that one's first token
   // split: the run's blocks, and its next piece: sequence, its segments, key head, segment, block in it
@@ -244,10 +248,10 @@ struct PackedWalk {
   int at, nseg, hk, pr, cut;
 
   __device__ __forceinline__ PackedWalk(const PackedShape& s_, const PackedPlan& p_, const PackedFwdArgs& a)
-      : s(s_), p(p_), q(a.seqs), in_order(seqs_in_order(s_, a.seqs, blockIdx.x == 0, a.status)),
-        queue(s_, a.seqs, p_.w, 1, p_.heads, p_.grid, false, p_.tickets ? a.counter : nullptr, in_order && !p_.split),
+      : s(s_), p(p_), q(a.seqs),
+        queue(s_, a.seqs, p_.w, 1, p_.heads, p_.grid, false, p_.tickets ? a.counter : nullptr, blockIdx.x == 0, a.status),
         b(0), lo(0), g(0), g_end(0), run(1), begin(0), at(0), nseg(0), hk(0), pr(0), cut(0) {
-    if (!in_order || !p.split) return;
+    if (!queue.in_order || !p.split) return;
     const int lane = threadIdx.x & 31;
     int64_t total = 0;
     for (int i = lane; i < s.B; i += 32) total += blocks_of(i);
