@@ -7,9 +7,9 @@
 // table: each lane holds the page of one of the warp's next 32 steps, read a whole round ahead.  A row sees the keys
 // up to its token's position.
 //
-// Measured: 16 single tokens over up to 32760 keys (264450 in all), 40/8 heads of d = 128: 167 us with the parts' join,
-// 6.5 TB/s, 97 % of the copy rate.  Short ones are bound by the chain place - page - keys - steps - result of a piece (one
-// token over 512 keys, 12 heads: 7.2 us; over 16 keys 4.1).
+// Measured: 16 single tokens over up to 32760 keys (264450 in all), 40/8 heads of d = 128: 169 us with the parts' join,
+// 6.4 TB/s, 96 % of the copy rate.  Short ones are bound by the chain place - page - keys - steps - result of a piece (one
+// token over 512 keys, 12 heads: 7.4 us; over 16 keys 4.1).
 #include <algorithm>
 
 #include "cross_few.cuh"
@@ -28,6 +28,17 @@ constexpr int kStageBytes = 2 * kFewTileBytes;
 // others' pieces.  (100 sequences of 64 to 1351 keys, 8 key heads of d = 128: without 120 us, 2 blocks 74, 3 68, 4 63, 5
 // 58, 6 58, 8 59; 11 of 1 to 16001, 4 key heads of d = 64: 2 blocks 24.2 us, 4 21.0, 8 18.4, 10 18.4, 16 18.7.)
 __host__ __device__ constexpr int piece_blocks(int d) { return 5 * 128 / d; }
+
+// Two numbers rounded to the call's type, the first in the lower half, and back.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  return F16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
 
 struct FewPiece {
   int b, qtok, pos, n;  // sequence, its first new token, that token's position, new tokens
@@ -344,8 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           o[c][3] *= al[1];
         }
       }
-      // P in the layout of an A operand: 16 keys (tiles 2 k, 2 k + 1) per k-step
-      uint32_t pf[kNT / 2][4];
+      // P in the layout of an A operand: 16 keys (tiles 2 k, 2 k + 1) per k-step; rounded, and what the rounding left.
+      // (O is then as exact as its own type; with P rounded alone a token's O over 512 keys was 1.4 to 1.55 times as far
+      // off as its own rounding.  The second products take 1 to 3 % at d = 128, up to 9 % at d = 64.)
+      uint32_t pf[kNT / 2][4], pr[kNT / 2][4];
 #pragma unroll
       for (int j = 0; j < kNT; ++j) {
         float p[4];
@@ -354,8 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           p[q] = ex2(fmaf(sc[j][q], mul, -m_used[q >> 1]));
           l[q >> 1] += p[q];
         }
-        pf[j >> 1][2 * (j & 1)] = F16 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]);
-        pf[j >> 1][2 * (j & 1) + 1] = F16 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint32_t u = pack2<F16>(p[2 * hf], p[2 * hf + 1]);
+          const float2 r = unpack2<F16>(u);
+          pf[j >> 1][2 * (j & 1) + hf] = u;
+          pr[j >> 1][2 * (j & 1) + hf] = pack2<F16>(p[2 * hf] - r.x, p[2 * hf + 1] - r.y);
+        }
       }
       // O += P V: keys 16 k + 2 t, + 1 and 16 k + 8 + 2 t, + 1; channels of chunk g (+ 8 i)
 #pragma unroll
@@ -370,10 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            mma16816<F16>(o[8 * i8 + 2 * w], pf[k], __byte_perm(v[0][w], v[1][w], 0x5410),
-                          __byte_perm(v[2][w], v[3][w], 0x5410));
-            mma16816<F16>(o[8 * i8 + 2 * w + 1], pf[k], __byte_perm(v[0][w], v[1][w], 0x7632),
-                          __byte_perm(v[2][w], v[3][w], 0x7632));
+            const uint32_t e0 = __byte_perm(v[0][w], v[1][w], 0x5410), e1 = __byte_perm(v[2][w], v[3][w], 0x5410);
+            const uint32_t f0 = __byte_perm(v[0][w], v[1][w], 0x7632), f1 = __byte_perm(v[2][w], v[3][w], 0x7632);
+            mma16816<F16>(o[8 * i8 + 2 * w], pr[k], e0, e1);
+            mma16816<F16>(o[8 * i8 + 2 * w + 1], pr[k], f0, f1);
+            mma16816<F16>(o[8 * i8 + 2 * w], pf[k], e0, e1);
+            mma16816<F16>(o[8 * i8 + 2 * w + 1], pf[k], f0, f1);
           }
         }
       }
