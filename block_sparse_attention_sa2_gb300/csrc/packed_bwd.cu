@@ -14,11 +14,11 @@
 // - Behind a sequence's last token lie the next one's: rows of Q and dO there are zeroed in shared memory (their P
 //   is 0, but 0 * NaN is NaN), and results are stored row by row.
 //
-// Measured, one causal sequence of 8190 tokens, 24/8 heads of d = 128: statistics 19.6 us (the bytes, 5.3 TB/s), dQ 347
-// us (its three products keep the tensor pipe busy 79 % of the time), dK and dV 594 us (four products, 59 %; the pipe is
-// held 73 %, its operands come from shared memory at N = 64).  Of a half tile's 1700 cycles there the element-wise
-// threads work 1600 for each of two, and wait for the next S^T as long.  d = 64 waits for its threads: 16/16 heads 460
-// us in all.  Short sequences: each item's first scores, and its sums' way out, 2500 to 4000 cycles.
+// Measured, one causal sequence of 8190 tokens, 24/8 heads of d = 128: statistics 20 us (the bytes, 5.2 TB/s), dQ 339
+// us (its three products keep the tensor pipe busy 82 % of the time), dK and dV 588 us (four products, 61 %; the pipe is
+// held 75 %, its operands come from shared memory at N = 64).  Of a half tile's 1700 cycles there the element-wise
+// threads work 1600 for each of two, and wait for the next S^T as long.  d = 64 waits for its threads: 16/16 heads 440
+// us in all.  Short sequences: each item's first scores, and its sums' way out.
 #include <algorithm>
 
 #include "cross_grad.cuh"

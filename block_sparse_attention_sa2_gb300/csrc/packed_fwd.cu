@@ -13,12 +13,12 @@
 // - Keys come from pages by one TMA copy per page and panel; their numbers are read 32 at a time, ahead of use.
 // - A tile that is not full is stored row by row: behind it lie the next sequence's rows.
 //
-// Bounds, measured: d = 128 the products, which take 70 % of the tensor pipe's time (1.5 times their shared memory reads
-// at N = 64 keys), and the power limit in long calls: one causal sequence of 32760 tokens, 32/8 heads, 5.9 ms, 1490
-// TFLOP/s; 3600 tokens over 75600 in pages, 40 heads, 4.4 ms, 1230 TFLOP/s.  d = 64 the softmax threads, about 1180
-// cycles per half block and tile, most of it latency: 7 sequences of up to 5370 tokens, 24/8 heads, 339 us, 730 TFLOP/s.
+// Bounds, measured: d = 128 the products, which hold the tensor pipe 80 % of the time (1.5 times their shared memory
+// reads at N = 64 keys), and the power limit in long calls: one causal sequence of 32760 tokens, 32/8 heads, 5.4 ms, 1620
+// TFLOP/s; 3600 tokens over 75600 in pages, 40 heads, 3.9 ms, 1400 TFLOP/s.  d = 64 the softmax threads, about 1000
+// cycles per half block and tile, most of it latency: 7 sequences of up to 5370 tokens, 24/8 heads, 300 us, 820 TFLOP/s.
 // Short sequences: a piece's first half block (2300 cycles, a pass of its own for the reference), and a launch's first
-// piece, 14000 cycles from the kernel's start to its first scores (instructions and pages are not in the caches yet).
+// piece, up to 14000 cycles from the kernel's start to its first scores (instructions and pages are not in the caches yet).
 //
 // Roles (544 threads): warp 0 finds work and issues the TMA copies; 1 and 2 issue S, 3 and 16 P V of tile 0
 // and 1; 4..7 epilogue; 8..11 and 12..15 softmax of tile 0 and 1, one row per thread.
@@ -395,7 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         // Scores that some row does not read become -inf in TMEM, and the first ones give the reference, in a pass of its
-        // own: half a block has neither as a rule, and a launch's first one waits for each of its instructions.
+        // own: half a block has neither as a rule (7 sequences of up to 5370 tokens, 24/8 heads of d = 64: 339 us with the
+        // scores cut as they are read, 300 so; one of 8192, 16 heads of d = 128: 205 and 187), and a launch's first one
+        // waits for each of its instructions.
         const bool cut = 64 * (i + 1) > least;
         if (i == 0 || cut) {
           float m0 = -INFINITY;
