@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.packed_util import HostPages, I32, check_one, places, shuffled_table, tokens  # noqa: E402
+from tests.packed_util import HostPages, I32, U, attend, check_one, places, shuffled_table, tokens  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 NAN = float("nan")
@@ -316,3 +316,23 @@ def test_many_single_tokens(sa2, held, H, Hkv, d):
             "one long": [20 + b if b != 50 else 20000 for b in range(B)]}[held]
     new = [0 if b % 9 == 4 else 2 if b % 31 == 7 else 1 for b in range(B)]
     run(sa2, new, lens, 32, H, Hkv, d, max_new=2, seed=H)
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype", [(12, 12, 128, torch.bfloat16), (40, 8, 128, torch.float16), (16, 2, 64, torch.bfloat16), (32, 4, 64, torch.float16)])
+def test_single_tokens_are_as_exact_as_their_type(sa2, H, Hkv, d, dtype):
+    """P counts in two parts, so that what is left of its rounding is u^2 of its value (in fp16 2^-25 of the row's largest):
+    beside it O has its own rounding, the scores' error ds, and 2^-19 for the exponentials and sums in 32 bits."""
+    new, held, page = [1, 1, 1], [512, 3, 2500], 32
+    cache, table = make(sa2, held, page, Hkv, d, dtype, seed=H)
+    q = tokens(H, 3, d, dtype, H + 1)
+    o, _ = sa2.paged_attn(q, cache, torch.tensor(places(new), **I32), torch.tensor(held, **I32), table, max_new=1)
+    sa2.check_device()
+    u, host = U[dtype], HostPages(cache, table)
+    for b, m in enumerate(held):
+        k, v = host.tokens(b, m)
+        ro, _, a, ds = attend(q[:, b:b + 1], k, v)
+        bound = u * ro.abs() * (1 + 2.0**-6) + (u * u + 2 * ds[..., None] + 2.0**-19) * a
+        if dtype == torch.float16:
+            bound = bound + m * 2.0**-25 * float(v.abs().max()) + 2.0**-25
+        err = (o[:, b:b + 1].double() - ro).abs()
+        assert bool((err <= bound).all()), f"sequence {b}: {float((err / bound).max()):.3f} of the bound"
